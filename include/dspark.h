@@ -415,6 +415,120 @@ DSPARK_API int dspark_sts_fit(const float* z, const int32_t* ceiling, int N, int
                    const float* grid, int n_grid, int n_bins, float* T_out, double* ece_out,
                    void* ws, size_t ws_bytes, dspark_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The target model's side of a step: what a target forward over the packed rows needs next to its
+ * dense layers.  Per layer dspark_append_kv then dspark_window_attention; on the final logits
+ * dspark_process_logits, then dspark_verify; after it dspark_history_commit.
+ *
+ * Rows are packed as dspark_pack packs them: request r owns rows cu_seqlens[r] ..
+ * cu_seqlens[r+1] - 1 (n_r of them; n_r may be 0, and a prompt's chunk is a window like any other).
+ * ctx_len[r] counts the tokens that request r already has in the cache; its row i sits at position
+ * ctx_len[r] + i.  After the verification the request keeps ctx_len[r] + acc_len[r] + 1 tokens: the
+ * next step simply passes that length, and what lies beyond it is overwritten.
+ *
+ * Paged cache, one tensor for K and one for V per layer: [n_pages, Hkv, page_size, D], bf16.
+ * Position p of request r lives in page page_table[r, p / page_size], slot p % page_size.  Entries
+ * of the page table that no call reaches (unused, or evicted behind a sliding window) may hold
+ * anything.  page_size is a power of two, 8 .. 4096.
+ *
+ * Common limits: 1 <= bs <= 256, rows >= 1, D 64 or 128, Hq a multiple of Hkv, Hq / Hkv <= 128,
+ * bf16 only.  These calls use only the status word of `ws` (>= 256 bytes, 256-byte aligned)
+ * unless a workspace size is given.  Row arguments marked "row stride s" are [rows, H, D] with heads
+ * and lanes dense and s elements from row to row (s >= H * D, a multiple of 8). */
+
+/* Rotate and append: for every packed row at position p (fp32 arithmetic, one rounding),
+ *     q_out = R_p q,   K cache slot of p = R_p k,   V cache slot of p = v
+ * R_p turns the first `rot` lanes of a head in pairs (a, b) by the angle of (p, t), t < rot / 2:
+ *     a' = a cos - b sin,   b' = b cos + a sin;      lanes rot .. D-1 pass unchanged
+ * with (a, b) = lanes (t, t + rot/2), or lanes (2t, 2t + 1) when `interleaved`.
+ *   q, k, v     device, row strides q_stride, k_stride, v_stride (parts of one fused projection)
+ *   cu_seqlens  device [bs + 1] int32;  ctx_len device [bs] int32
+ *   rows        rows of q, k, v and q_out; rows from cu_seqlens[bs] on are left alone
+ *   cos_sin     device [max_pos, rot] fp32: rot/2 cosines, then rot/2 sines, of each position
+ *   page_table  device [bs, max_pages] int32
+ *   q_out       device [rows, Hq, D]; may be q itself when q is dense.  q and q_out may both be NULL
+ *               (keys and values only).
+ * Device errors (status word, EINVAL; the row is skipped): a position below 0 or from max_pos on, a
+ * page beyond the table or a page number outside [0, n_pages); cu_seqlens decreasing or beyond rows.
+ * Limits: the common ones; rot a multiple of 16, 16 <= rot <= D. */
+DSPARK_API int dspark_append_kv(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, int dtype, const int32_t* cu_seqlens, const int32_t* ctx_len,
+                                int bs, int rows, const float* cos_sin, int max_pos, int rot, int interleaved,
+                                const int32_t* page_table, int max_pages, int n_pages, int page_size, int Hq,
+                                int Hkv, int D, void* q_out, void* k_cache, void* v_cache, void* ws,
+                                size_t ws_bytes, dspark_stream_t stream);
+
+/* Attention of the packed rows over the paged cache, which holds the rows' own keys already
+ * (dspark_append_kv).  The row at position p of request r sees the positions
+ *     j <= p  with  j > p - window  or  j < n_sink          (window = 0: every j <= p)
+ * i.e. a sliding window and the sequence's first tokens, which stay visible:
+ *     s_j = scale * q . k_j,   lse = log sum_j exp(s_j),   out = sum_j exp(s_j - lse) v_j
+ * Query head h reads KV head h / (Hq / Hkv).  Scores, maxima and sums are fp32; the weights
+ * exp(s_j - m) enter the second product in bf16 and their sum in fp32.
+ *   q         device, row stride q_stride (rotated: dspark_append_kv's q_out)
+ *   k_cache, v_cache, page_table, cu_seqlens, ctx_len, rows as dspark_append_kv
+ *   max_rows  the longest window that the caller expects (>= 1).  It only picks how rows are tiled:
+ *             any n_r is computed correctly.
+ *   window    >= 0;  n_sink >= 0 (ignored when window = 0)
+ *   out       device [rows, Hq, D];  lse device [rows, Hq] fp32 or NULL (natural logarithm)
+ *   ws        dspark_window_attention_workspace_bytes bytes, zeroed once; calls that can overlap on
+ *             the device must not share it
+ * Rows from cu_seqlens[bs] on are left alone.  Pages that no row of a request sees are not read, and
+ * slots that no row sees (past the last row, before the window) may hold anything, NaN included; a NaN
+ * or infinity in a slot that one row of a window sees can reach that window's other rows.
+ * Device errors (status word, EINVAL): ctx_len below 0, or a window beyond max_pages pages (its rows are
+ * then left alone); a page number outside [0, n_pages) on a page that is read (read as zeros); cu_seqlens
+ * decreasing or beyond rows (no row is written).
+ * Limits: the common ones; scale finite. */
+DSPARK_API size_t dspark_window_attention_workspace_bytes(int Hq, int Hkv, int D);
+DSPARK_API int dspark_window_attention(const void* q, int64_t q_stride, int dtype, const void* k_cache,
+                                       const void* v_cache, const int32_t* page_table, int max_pages, int n_pages,
+                                       int page_size, const int32_t* cu_seqlens, const int32_t* ctx_len, int bs,
+                                       int rows, int max_rows, int Hq, int Hkv, int D, float scale, int window,
+                                       int n_sink, void* out, float* lse, void* ws, size_t ws_bytes,
+                                       dspark_stream_t stream);
+
+/* Logit rules on the packed target rows, before dspark_verify.  Row i of request r scores the token
+ * after ids[cu_seqlens[r] + i]; with
+ *     c[v] = said count of v in hist[r]  +  how many of the ids of rows 1 .. i of the window are v
+ *     seen = v in the prompt (hist) or c[v] > 0
+ * (row 0's id, the anchor, is in the history already):
+ *     l' = seen ? (l > 0 ? l / repetition[r] : l * repetition[r]) : l
+ *     l' = l' - frequency[r] * c[v] - presence[r] * [c[v] > 0] + bias[r, v]
+ *     out = mask bit v of the row is 0 ? -inf : l'          (fp32, rounded once)
+ * A row whose mask leaves nothing is all -inf.
+ *   logits, out  device [rows, V] (dtype, fp32 or bf16); out may be logits itself: then only the
+ *                elements that a rule can change are read and written
+ *   ids          device [rows] int32 (dspark_pack)
+ *   hist         device [bs, V] int16: bits 0-14 the said count, bit 15 "in the prompt"
+ *                (dspark_history_build); NULL with repetition, frequency, presence NULL: no penalties
+ *   repetition, frequency, presence  device [bs] fp32, or NULL each: 1, 0, 0
+ *   bias_start   device [bs + 1] int32, bias_ids / bias_vals device int32 / fp32: request r's biases are
+ *                entries bias_start[r] .. bias_start[r+1] - 1, ids strictly increasing; all NULL: none
+ *   mask         device [rows, ceil(V / 32)] uint32, bit v % 32 of word v / 32 set where v is allowed; or NULL
+ * Device errors (status word, EINVAL): cu_seqlens decreasing or beyond rows (the request is skipped),
+ * a drafted id outside [0, V) (not counted), bias ids not strictly increasing or outside [0, V).
+ * Limits: 1 <= bs <= 256, V % 8 == 0, 8 <= V < 2^24. */
+DSPARK_API int dspark_process_logits(const void* logits, int dtype, int rows, int V, const int32_t* cu_seqlens,
+                                     const int32_t* ids, int bs, const int16_t* hist, const float* repetition,
+                                     const float* frequency, const float* presence, const int32_t* bias_start,
+                                     const int32_t* bias_ids, const float* bias_vals, const uint32_t* mask,
+                                     void* out, void* ws, size_t ws_bytes, dspark_stream_t stream);
+
+/* Token history of dspark_process_logits.
+ * build: rewrites hist[0 .. bs-1] from token lists: request r's tokens are tokens[start[r] ..
+ * start[r+1] - 1], the first n_prompt[r] of them its prompt, the others said (counts saturate at 32767).
+ *   tokens device int32;  start device [bs + 1] int32 in [0, n_tokens];  n_prompt device [bs] int32
+ * commit: adds one step's out_tokens [bs, gamma + 1] (dspark_verify) to the said counts; -1 is skipped.
+ * Device errors (status word, EINVAL): ids outside [0, V) (not counted), start decreasing or beyond
+ * n_tokens (the list counts as empty).
+ * Limits: as dspark_process_logits; 1 <= gamma <= 16. */
+DSPARK_API int dspark_history_build(const int32_t* tokens, int n_tokens, const int32_t* start,
+                                    const int32_t* n_prompt, int bs, int V, int16_t* hist, void* ws, size_t ws_bytes,
+                                    dspark_stream_t stream);
+DSPARK_API int dspark_history_commit(const int32_t* out_tokens, int bs, int gamma, int V, int16_t* hist, void* ws,
+                                     size_t ws_bytes, dspark_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -54,6 +54,19 @@ _SIGS = {
                            _i, _f, _u64, _u64, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
+_i64 = ctypes.c_int64
+_SIGS.update({
+    "dspark_append_kv": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _vp, _vp, _i, _i, _vp, _i, _i, _i, _vp, _i, _i, _i,
+                              _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dspark_window_attention_workspace_bytes": (_sz, [_i, _i, _i]),
+    "dspark_window_attention": (_i, [_vp, _i64, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _f,
+                                     _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "dspark_process_logits": (_i, [_vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   _sz, _vp]),
+    "dspark_history_build": (_i, [_vp, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp]),
+    "dspark_history_commit": (_i, [_vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
+})
+
 _LIB: Optional[ctypes.CDLL] = None
 
 
@@ -354,3 +367,141 @@ def dspark_sts_fit(z, ceiling, grid, n_bins, T_out, ece_out, ws=None, stream=Non
         ws = torch.empty(max(nbytes, 8), dtype=torch.uint8, device=z.device)
     _check(lib().dspark_sts_fit(_p(z), _p(ceiling), N, gamma, _p(grid), n_grid, int(n_bins), _p(T_out), _p(ece_out),
                                 _p(ws), ws.numel() * ws.element_size(), _stream(stream)), "dspark_sts_fit")
+
+
+# ----------------------------------------------------------------- the target model's side
+
+def _same(want, **tensors) -> None:
+    """Every tensor given has the wanted dtype (the library sees bare pointers)."""
+    for name, t in tensors.items():
+        if t is not None and t.dtype != want:
+            raise ValueError(f"{name} must be {want}, not {t.dtype}")
+
+
+def _row_stride(t, name: str) -> int:
+    """Elements from row to row of a [rows, H, D] tensor whose heads and lanes are dense."""
+    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+        raise ValueError(f"{name} must be [rows, heads, lanes] with dense heads and lanes")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _shape(name: str, t, *want) -> None:
+    if tuple(t.shape) != want:
+        raise ValueError(f"{name} must have shape {want}, not {tuple(t.shape)}")
+
+
+def dspark_append_kv(q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k_cache, v_cache, ws,
+                     interleaved=False, stream=None):
+    """Rotate q, k by their positions and append k, v of the packed rows to the paged cache.
+    q, k, v [rows, heads, D] (rows may be strided: parts of one projection); cos_sin [max_pos, rot] fp32;
+    page_table [bs, max_pages] int32; k_cache, v_cache [n_pages, Hkv, page_size, D]; q_out [rows, Hq, D]
+    (q and q_out may both be None)."""
+    import torch
+    n_pages, Hkv, page, D = k_cache.shape
+    rows, bs = k.shape[0], cu_seqlens.numel() - 1
+    _same(torch.int32, cu_seqlens=cu_seqlens, ctx_len=ctx_len, page_table=page_table)
+    _same(torch.float32, cos_sin=cos_sin)
+    _same(k_cache.dtype, q=q, k=k, v=v, q_out=q_out, v_cache=v_cache)
+    _shape("v_cache", v_cache, n_pages, Hkv, page, D)
+    _shape("k", k, rows, Hkv, D)
+    _shape("v", v, rows, Hkv, D)
+    _shape("page_table", page_table, bs, page_table.shape[-1])
+    _shape("ctx_len", ctx_len, bs)
+    Hq = Hkv
+    if q is not None:
+        Hq = q.shape[1]
+        _shape("q", q, rows, Hq, D)
+        _shape("q_out", q_out, rows, Hq, D)
+    _check(lib().dspark_append_kv(
+        None if q is None else q.data_ptr(), 0 if q is None else _row_stride(q, "q"), k.data_ptr(),
+        _row_stride(k, "k"), v.data_ptr(), _row_stride(v, "v"), _dtype(k_cache), _p(cu_seqlens), _p(ctx_len), bs, rows,
+        _p(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(interleaved), _p(page_table), page_table.shape[1],
+        n_pages, page, Hq, Hkv, D, _p(q_out), _p(k_cache), _p(v_cache), _p(ws), ws.numel(), _stream(stream)),
+        "dspark_append_kv")
+
+
+def dspark_window_attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().dspark_window_attention_workspace_bytes(Hq, Hkv, D))
+
+
+def alloc_attention_workspace(Hq: int, Hkv: int, D: int, device="cuda"):
+    """A zero-initialised workspace tensor of dspark_window_attention."""
+    import torch
+    n = dspark_window_attention_workspace_bytes(Hq, Hkv, D)
+    if n == 0:
+        raise ValueError("invalid heads for an attention workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def dspark_window_attention(q, k_cache, v_cache, page_table, cu_seqlens, ctx_len, max_rows, scale, window, n_sink, out,
+                            lse, ws, stream=None):
+    """Attention of the packed rows q [rows, Hq, D] over the paged cache: a sliding window (0: everything)
+    and the first n_sink tokens.  out [rows, Hq, D]; lse [rows, Hq] fp32 or None; max_rows: the longest
+    window expected (it only picks the tiling)."""
+    import torch
+    n_pages, Hkv, page, D = k_cache.shape
+    rows, Hq, bs = q.shape[0], q.shape[1], cu_seqlens.numel() - 1
+    _same(torch.int32, cu_seqlens=cu_seqlens, ctx_len=ctx_len, page_table=page_table)
+    _same(k_cache.dtype, q=q, out=out, v_cache=v_cache)
+    _same(torch.float32, lse=lse)
+    _shape("q", q, rows, Hq, D)
+    _shape("out", out, rows, Hq, D)
+    _shape("v_cache", v_cache, n_pages, Hkv, page, D)
+    _shape("page_table", page_table, bs, page_table.shape[-1])
+    _shape("ctx_len", ctx_len, bs)
+    if lse is not None:
+        _shape("lse", lse, rows, Hq)
+    _check(lib().dspark_window_attention(
+        q.data_ptr(), _row_stride(q, "q"), _dtype(k_cache), _p(k_cache), _p(v_cache), _p(page_table),
+        page_table.shape[1], n_pages, page, _p(cu_seqlens), _p(ctx_len), bs, rows, int(max_rows), Hq, Hkv, D,
+        float(scale), int(window), int(n_sink), _p(out), _p(lse), _p(ws), ws.numel(), _stream(stream)),
+        "dspark_window_attention")
+
+
+def dspark_process_logits(logits, cu_seqlens, ids, hist, repetition, frequency, presence, bias_start, bias_ids,
+                          bias_vals, mask, out, ws, stream=None):
+    """Penalties, biases and grammar masks on the packed target rows logits [rows, V] (out may be logits):
+    hist [bs, V] int16 (dspark_history_build) or None; repetition / frequency / presence [bs] fp32 or None;
+    bias_start [bs + 1], bias_ids, bias_vals or None; mask [rows, ceil(V / 32)] int32 words or None."""
+    import torch
+    rows, V = logits.shape
+    bs = cu_seqlens.numel() - 1
+    _same(torch.int32, cu_seqlens=cu_seqlens, ids=ids, bias_start=bias_start, bias_ids=bias_ids, mask=mask)
+    _same(torch.float32, repetition=repetition, frequency=frequency, presence=presence, bias_vals=bias_vals)
+    _same(torch.int16, hist=hist)
+    _same(logits.dtype, out=out)
+    _shape("out", out, rows, V)
+    if ids.numel() < rows:
+        raise ValueError("ids must hold one entry per row")
+    if hist is not None:
+        _shape("hist", hist, bs, V)
+    if mask is not None:
+        _shape("mask", mask, rows, (V + 31) // 32)
+    _check(lib().dspark_process_logits(
+        _p(logits), _dtype(logits), rows, V, _p(cu_seqlens), _p(ids), bs, _p(hist), _p(repetition), _p(frequency),
+        _p(presence), _p(bias_start), _p(bias_ids), _p(bias_vals), _p(mask), _p(out), _p(ws), ws.numel(),
+        _stream(stream)), "dspark_process_logits")
+
+
+def dspark_history_build(tokens, start, n_prompt, hist, ws, stream=None):
+    """Rewrite hist [bs, V] int16 from token lists: request r's are tokens[start[r] : start[r + 1]], the first
+    n_prompt[r] of them its prompt."""
+    import torch
+    bs, V = hist.shape
+    _same(torch.int32, tokens=tokens, start=start, n_prompt=n_prompt)
+    _same(torch.int16, hist=hist)
+    _shape("start", start, bs + 1)
+    _shape("n_prompt", n_prompt, bs)
+    _check(lib().dspark_history_build(_p(tokens), tokens.numel(), _p(start), _p(n_prompt), bs, V, _p(hist), _p(ws),
+                                      ws.numel(), _stream(stream)), "dspark_history_build")
+
+
+def dspark_history_commit(out_tokens, hist, ws, stream=None):
+    """Add a step's out_tokens [bs, gamma + 1] (dspark_verify; -1 skipped) to the said counts of hist [bs, V]."""
+    import torch
+    bs, V = hist.shape
+    _same(torch.int32, out_tokens=out_tokens)
+    _same(torch.int16, hist=hist)
+    _shape("out_tokens", out_tokens, bs, out_tokens.shape[-1])
+    _check(lib().dspark_history_commit(_p(out_tokens), bs, out_tokens.shape[1] - 1, V, _p(hist), _p(ws), ws.numel(),
+                                       _stream(stream)), "dspark_history_commit")

@@ -103,4 +103,26 @@ cudaError_t launch_verify(int dtype, const void* target, const int32_t* cu, cons
                           int32_t* out_tokens, int32_t* acc_len, int32_t* ceiling, void* ws,
                           cudaStream_t s);
 
+// ---- the target model's side: paged cache, attention, logit rules, token history -----------
+cudaError_t launch_append_kv(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const int32_t* cu, const int32_t* ctx, int bs, int rows,
+                             const float* cos_sin, int max_pos, int rot, int interleaved, const int32_t* page_table,
+                             int max_pages, int n_pages, int page_shift, int Hq, int Hkv, int D, void* q_out,
+                             void* k_cache, void* v_cache, uint32_t* status, cudaStream_t s);
+size_t window_attention_ws_bytes(int Hq, int Hkv, int D);
+cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                    const int32_t* page_table, int max_pages, int n_pages, int page_shift,
+                                    const int32_t* cu, const int32_t* ctx, int bs, int rows, int max_rows, int Hq,
+                                    int Hkv, int D, float scale, int window, int n_sink, void* out, float* lse,
+                                    void* ws, cudaStream_t s);
+cudaError_t launch_process_logits(const void* logits, int dtype, int rows, int V, const int32_t* cu,
+                                  const int32_t* ids, int bs, const int16_t* hist, const float* repetition,
+                                  const float* frequency, const float* presence, const int32_t* bias_start,
+                                  const int32_t* bias_ids, const float* bias_vals, const uint32_t* mask, void* out,
+                                  uint32_t* status, cudaStream_t s);
+cudaError_t launch_history_build(const int32_t* tokens, int n_tokens, const int32_t* start, const int32_t* n_prompt,
+                                 int bs, int V, int16_t* hist, uint32_t* status, cudaStream_t s);
+cudaError_t launch_history_commit(const int32_t* out_tokens, int bs, int gamma, int V, int16_t* hist, uint32_t* status,
+                                  cudaStream_t s);
+
 }  // namespace dspark
