@@ -1,0 +1,407 @@
+// The attention of prompts: windows of more (token, head) rows than one tile of 128 holds.
+//
+// Bound by the two products and the exponentials.  A unit is two Q tiles of 128 rows that read the same KV tiles:
+//     S = Q K^T  (tcgen05, fp32 in TMEM)  ->  P = 2^(c S - m), l += sum P  (registers, one thread per row)
+//     O += P V   (tcgen05; P in bf16 in TMEM over S, O in fp32 in TMEM)
+// While one tile's softmax runs, the tensor cores work for the other.  m is only a reference that keeps the
+// exponentials in range: it moves (and O and l are rescaled) when a row's maximum has outgrown it by 2^8,
+// which is exact in the end because the sum is divided out.
+#include "attention_common.cuh"
+
+namespace dspark {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 384;  // warps 0-3: softmax of the first tile, 4-7: of the second, 8: TMA, 9: MMA
+// Registers: launched with 384 x 168; the softmax warps hold a whole row of S and take what the others
+// give back (256 x 208 + 128 x 80 <= 384 x 168).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+constexpr float kRescaleAt = 8.f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;            // 128-byte swizzled column blocks of a tile
+  static constexpr int kHalfBytes = kTile * 128;
+  static constexpr int kTileBytes = kHalves * kHalfBytes;
+  static constexpr int kSlots = D == 128 ? 5 : 10;  // ring of K and V tiles: 160 KB either way
+};
+
+struct Shared {
+  uint64_t q_full[2], q_empty[2], kv_full[10], kv_empty[10], s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem_base;
+  volatile int abort;
+  int mma_pending;
+  Range range;
+  uint8_t long_req[DSPARK_MAX_BS];
+};
+
+// Bits k = 0 .. 7 with lo <= k <= hi.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  const uint32_t below = hi >= 7 ? 0xFFu : hi < 0 ? 0u : (2u << hi) - 1u;
+  const uint32_t from = lo <= 0 ? 0xFFu : lo > 7 ? 0u : 0xFFu << lo;
+  return below & from;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;                       // two Q tiles
+  uint8_t* sKV = smem + 2 * C::kTileBytes;  // ring
+  Shared* sh = reinterpret_cast<Shared*>(sKV + C::kSlots * C::kTileBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int unit_tokens = 2 * a.tokens, tile_rows = a.tokens * a.g;
+  const int active = (tile_rows + 31) / 32;  // softmax warps of a tile that hold rows
+  const Waiter wait{&sh->abort, a.timeout_ns};
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh->q_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->q_empty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->s_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->p_full[i]), active);
+      tc::mbar_init(tc::smem_u32(&sh->o_full[i]), 1);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh->kv_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->kv_empty[i]), 1);
+    }
+    tc::mbar_init(tc::smem_u32(&sh->drain), 1);
+    tc::fence_mbar_init();
+    sh->abort = 0, sh->mma_pending = 0, sh->range.bad = 0, sh->range.n_long = 0;
+    tc::prefetch_tensormap(&map_q);
+    tc::prefetch_tensormap(&map_k);
+    tc::prefetch_tensormap(&map_v);
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(tc::smem_u32(&sh->tmem_base), 512);
+    tc::tmem_relinquish();
+  }
+  __syncthreads();
+  pdl_enter();
+  plan_range(a, sh->range, sh->long_req, unit_tokens);
+  __syncthreads();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == 8) {
+    // --------------------------------------------------------------------- TMA producer
+    // Ring order in a unit: K 0, then V j, K j + 1.  K and V are read by every unit of the head: kept in L2.
+    const uint64_t keep = tc::policy_evict_last();
+    int slot = 0, seg_i = 0, flags = 0, q_use[2] = {0, 0};
+    uint32_t phase = 0, issued = 0;
+    int4 info = make_int4(0, 0, 0, 0);
+    bool ok = true;
+    Walk walk(sh->range, unit_tokens);
+    Segment s = {};
+    auto put = [&](const CUtensorMap* map, const TileLoad& t) {
+      if (!wait(&sh->kv_empty[slot], phase ^ 1)) return false;
+      issue_tile<C::kHalves>(a, map, t, tc::smem_u32(sKV + slot * C::kTileBytes), tc::smem_u32(&sh->kv_full[slot]), keep, lane);
+      issued |= 1u << slot;
+      if (++slot == C::kSlots) slot = 0, phase ^= 1;
+      return true;
+    };
+    auto put_q = [&](int b, int row) {
+      if (!wait(&sh->q_empty[b], (q_use[b] & 1) ^ 1)) return false;
+      if (lane == 0) {
+        const uint32_t bar = tc::smem_u32(&sh->q_full[b]);
+        tc::mbar_arrive_expect_tx(bar, uint32_t(tile_rows * 128 * C::kHalves));
+#pragma unroll
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tc::tma_load_3d(tc::smem_u32(sQ + b * C::kTileBytes + hf * C::kHalfBytes), &map_q, bar, hf * 64, s.h * a.g, row, keep);
+      }
+      ++q_use[b];
+      return true;
+    };
+    while (ok && walk.next(a, sh->range, s)) {
+      if (s.tile0 > 0) flags |= kTailUsed | (s.tile0 + s.n == s.u.ntiles ? kTailEnds : 0);
+      if (s.tile0 == 0 && s.n < s.u.ntiles) flags |= kHeadUsed, info = make_int4(0, s.row0, s.ntok, s.h);
+      TileLoad t0 = tile_load(a, s, 0, lane), t1 = t0;
+      if (s.n > 1) t1 = tile_load(a, s, 1, lane);
+      ok = put(&map_k, t0) && put_q(0, s.row0) && (s.ntok <= a.tokens || put_q(1, s.row0 + a.tokens));
+      for (int j = 0; ok && j < s.n; ++j) {
+        TileLoad t2 = t1;
+        if (j + 2 < s.n) t2 = tile_load(a, s, j + 2, lane);
+        ok = put(&map_v, t0) && (j + 1 >= s.n || put(&map_k, t1));
+        t0 = t1, t1 = t2;
+      }
+      ++seg_i;
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 1u, uint32_t(seg_i));
+      // wait (bounded) for every copy in flight before the CTA exits
+      const volatile int never = 0;
+      const long long dl = tc::deadline_after_ns(200000000ull);
+      for (int i = 0; i < C::kSlots; ++i)  // slots before `slot` were last used in this round, the others in the last one
+        if (issued >> i & 1u)
+          tc::mbar_wait_bounded(tc::smem_u32(&sh->kv_full[i]), i < slot ? phase : phase ^ 1, dl, &never);
+      for (int b = 0; b < 2; ++b)
+        if (q_use[b] > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[b]), (q_use[b] - 1) & 1, dl, &never);
+    }
+    if (lane == 0) {
+      info.x = ok ? flags : 0;
+      a.info[blockIdx.x] = info;
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kTile, kTile);
+    constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kTile, D) | tc::kIdescBMajorMN;
+    int slot = 0, seg_i = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
+    uint32_t phase = 0;
+    bool ok = true, any = false;
+    Walk walk(sh->range, unit_tokens);
+    Segment s = {};
+    auto take = [&](int& which) {  // the next filled slot of the ring
+      which = slot;
+      if (!wait(&sh->kv_full[slot], phase)) return false;
+      if (++slot == C::kSlots) slot = 0, phase ^= 1;
+      return true;
+    };
+    // S_st = Q_st K^T for the tile in ring slot `ks`
+    auto issue_qk = [&](int st, int ks) {
+      const uint32_t q = tc::smem_u32(sQ + st * C::kTileBytes), k = tc::smem_u32(sKV + ks * C::kTileBytes);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t off = (i / 4) * C::kHalfBytes + (i % 4) * 32;
+        tc::mma_bf16(tmem + st * kTile, tc::sdesc_kmajor_sw128(q + off), tc::sdesc_kmajor_sw128(k + off), idesc_qk, i != 0);
+      }
+      tc::mma_commit(tc::smem_u32(&sh->s_full[st]));
+    };
+    // O_st (+)= P_st V; P_st lies over the first 64 columns of S_st
+    auto issue_pv = [&](int st, int vs, bool add) {
+      const uint32_t v = tc::smem_u32(sKV + vs * C::kTileBytes);
+#pragma unroll
+      for (int i = 0; i < kTile / 16; ++i)
+        tc::mma_bf16_ts(tmem + 2 * kTile + st * D, tmem + st * kTile + 8 * i,
+                        tc::sdesc_mnmajor(v + i * 2048, C::kHalfBytes), idesc_pv, add || i != 0);
+    };
+    while (ok && walk.next(a, sh->range, s)) {
+      const int n_st = s.ntok > a.tokens ? 2 : 1;
+      int ks, vs;
+      ok = take(ks) && wait(&sh->q_full[0], q_use[0]++ & 1) && (n_st == 1 || wait(&sh->q_full[1], q_use[1]++ & 1));
+      if (!ok) break;
+      tc::tc_fence_after();
+      if (lane == 0) {
+        for (int st = 0; st < n_st; ++st) {
+          issue_qk(st, ks);
+          if (s.n == 1) tc::mma_commit(tc::smem_u32(&sh->q_empty[st]));
+        }
+        tc::mma_commit(tc::smem_u32(&sh->kv_empty[ks]));
+      }
+      __syncwarp();
+      any = true;
+      for (int j = 0; ok && j < s.n; ++j) {
+        ok = take(vs);
+        if (!ok) break;
+        clear_unseen<C::kHalves>(a, s, j, sKV + vs * C::kTileBytes, lane);
+        const bool more = j + 1 < s.n;
+        for (int st = 0; ok && st < n_st; ++st) {
+          ok = wait(&sh->p_full[st], p_use[st]++ & 1) && (st != 0 || !more || take(ks));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (lane == 0) {
+            issue_pv(st, vs, j > 0);
+            if (!more) tc::mma_commit(tc::smem_u32(&sh->o_full[st]));
+            if (st == n_st - 1) tc::mma_commit(tc::smem_u32(&sh->kv_empty[vs]));
+            if (more) {
+              issue_qk(st, ks);
+              if (j + 2 == s.n) tc::mma_commit(tc::smem_u32(&sh->q_empty[st]));
+              if (st == n_st - 1) tc::mma_commit(tc::smem_u32(&sh->kv_empty[ks]));
+            }
+          }
+          __syncwarp();
+        }
+      }
+      ++seg_i;
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 2u, uint32_t(seg_i));
+    }
+    if (lane == 0) sh->mma_pending = any;
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if ((warp & 3) < active) {
+      const int st = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+      const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
+      const uint32_t t_s = lane_base + st * kTile, t_o = lane_base + 2 * kTile + st * D;
+      const int tok = row / a.g, hh = row - tok * a.g, tok0 = st * a.tokens;
+      const float c2 = a.c2;
+      int seg_i = 0, s_use = 0, o_use = 0;
+      bool ok = true;
+      Walk walk(sh->range, unit_tokens);
+      Segment s = {};
+      while (ok && walk.next(a, sh->range, s)) {
+        ++seg_i;
+        if (tok0 >= s.ntok) continue;  // the unit has no second tile
+        const int p = s.u.p0 + tok0 + tok;  // this row's position; the tile's: q0 .. q1
+        const int q0 = s.u.p0 + tok0, q1 = min(q0 + a.tokens - 1, s.u.p1);
+        const bool valid = row < tile_rows && tok0 + tok < s.ntok;
+        float m = -INFINITY, l = 0.f;  // the reference (log2 units) and the sum
+        for (int j = 0; j < s.n; ++j) {
+          ok = wait(&sh->s_full[st], s_use++ & 1);
+          if (!ok) break;
+          tc::tc_fence_after();
+          float x[kTile];
+          tc::tmem_ld<kTile>(t_s, x);
+          tc::tmem_ld_wait();
+          const int first = (s.tile0 + j) * (kTile >> a.block_shift);
+          const int begin = block_pos(a, s.u, first);
+          const bool inside = first >= s.u.sb && begin + kTile - 1 <= q0 && (a.window == 0 || begin > q1 - a.window);
+          if (!inside) {
+            const float hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
+#pragma unroll
+            for (int gr = 0; gr < kTile / 8; ++gr) {  // 8 slots of one block
+              const int pos = block_pos(a, s.u, first + ((8 * gr) >> a.block_shift)) + ((8 * gr) & ((1 << a.block_shift) - 1));
+              uint32_t see = bits_between(a.window ? p - a.window + 1 - pos : 0, p - pos);
+              if (a.window) see |= bits_between(0, min(p, a.n_sink - 1) - pos);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (!(see >> k & 1u)) x[8 * gr + k] = hidden;
+            }
+          }
+          float t4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t4[i] = x[i];
+          if (c2 > 0.f) {
+#pragma unroll
+            for (int i = 4; i < kTile; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
+            t4[0] = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+          } else {
+#pragma unroll
+            for (int i = 4; i < kTile; ++i) t4[i & 3] = fminf(t4[i & 3], x[i]);
+            t4[0] = fminf(fminf(t4[0], t4[1]), fminf(t4[2], t4[3]));
+          }
+          const float top = t4[0] * c2;
+          float alpha = 1.f;
+          if (top > m + kRescaleAt) {
+            alpha = tc::ex2_approx(m - top);
+            m = top;
+          }
+          if (__any_sync(~0u, alpha != 1.f)) {
+            l *= alpha;
+            if (j > 0) {  // the product with the last tile was issued before this tile's S: it is complete
+#pragma unroll
+              for (int i = 0; i < D; i += 32) {
+                float o[32];
+                tc::tmem_ld<32>(t_o + i, o);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                tc::tmem_st<32>(t_o + i, o);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          const unsigned long long cc = pack_f32x2(c2, c2), mm = pack_f32x2(-ref, -ref);
+          unsigned long long l2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const int i = 64 * hf + 2 * k;
+              float e0, e1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(x[i], x[i + 1]), cc, mm), e0, e1);
+              e0 = tc::ex2_approx(e0);
+              e1 = tc::ex2_approx(e1);
+              l2[k & 1] = add_f32x2(l2[k & 1], pack_f32x2(e0, e1));
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
+              pk[k] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            tc::tmem_st32(t_s + 32 * hf, pk);
+          }
+          float u0, u1;
+          unpack_f32x2(add_f32x2(l2[0], l2[1]), u0, u1);
+          l += u0 + u1;
+          tc::tmem_st_wait();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->p_full[st]));
+        }
+        if (!ok) break;
+        ok = wait(&sh->o_full[st], o_use++ & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        // -------------------------------------------------------------- the tile's rows
+        const int64_t oat = int64_t(s.row0 + tok0 + tok) * a.Hq + s.h * a.g + hh;
+        const int64_t prow = (int64_t(2) * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * (2 * kTile) + st * kTile + row;
+        const bool partial = s.n < s.u.ntiles;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int i = 0; i < D; i += 32) {
+          float v[32];
+          tc::tmem_ld<32>(t_o + i, v);
+          tc::tmem_ld_wait();
+          if (valid && partial) {
+            float4* dst = reinterpret_cast<float4*>(a.partial + prow * D + i);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + oat * D + i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[8 * k + 2 * z] * inv, v[8 * k + 2 * z + 1] * inv);
+                w[z] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (valid) {
+          const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+          if (partial)
+            a.plse[prow] = lse2;
+          else if (a.lse)
+            a.lse[oat] = lse2 * kLn2;
+        }
+        tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
+      }
+      if (!ok) {
+        sh->abort = 1;
+        if (lane == 0) note_timeout(a.status, a.diag, 3u, uint32_t(seg_i) | uint32_t(warp) << 24);
+      }
+    }
+  }
+
+  __syncthreads();
+  if (warp == 9) {
+    if (lane == 0 && sh->mma_pending && sh->abort) {  // MMAs may be in flight: wait (bounded) before TMEM is freed
+      tc::mma_commit(tc::smem_u32(&sh->drain));
+      const volatile int never = 0;
+      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain), 0, tc::deadline_after_ns(200000000ull), &never);
+    }
+    __syncwarp();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int n_cta,
+                   cudaStream_t s) {
+  using C = Cfg<D>;
+  constexpr int kSmem = (2 + C::kSlots) * C::kTileBytes + int(sizeof(Shared));
+  static_assert(kSmem <= 232448, "dynamic shared memory beyond the 227 KB per-block limit");
+  static bool done[tch::kMaxDevices] = {};
+  static std::mutex mu;
+  const cudaError_t e = tch::set_smem_once(prompt_kernel<D>, kSmem, done, &mu);
+  return e != cudaSuccess ? e : launch_pdl(prompt_kernel<D>, dim3(n_cta), dim3(kThreads), kSmem, s, q, k, v, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_prompts(int D, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                     const attn::AttnArgs& a, int n_cta, cudaStream_t s) {
+  return D == 64 ? launch<64>(q, k, v, a, n_cta, s) : launch<128>(q, k, v, a, n_cta, s);
+}
+
+}  // namespace dspark

@@ -1,0 +1,529 @@
+// The attention of short windows: all (token, head) rows of a unit fit one tile of R = 16, 32, 64 or 128.
+//
+// Bound by reading K and V once, so a KV tile's way through the SM has to be short: the products are taken
+// transposed,
+//     S^T = K Q^T        [128 slots x R]   (tcgen05, M = 128, N = R; fp32 in TMEM)
+//     P^T = 2^(c S^T - m)                   (bf16, shared memory), partial sums of P per slot in registers
+//     O^T += V^T P^T     [D x R]            (tcgen05, fp32 in TMEM)
+// so that a thread holds one KV slot and half of the rows, and all eight softmax warps have work however few
+// the rows are.  (With the rows on TMEM lanes instead, 32 rows sat in one warp per stream: a
+// unit of 10 tiles of 128 x 128 at 32 rows took 24 us per CTA; so it takes 12.)
+//
+// m is a reference that only keeps the exponentials in range, the same for all slots of a row: any value
+// within 2^60 of the maximum gives the same result, since the sum is divided out and neither fp32 nor bf16 loses
+// bits there.  So it is set from a unit's first tile and checked, not recomputed, on the others.
+#include "attention_common.cuh"
+
+namespace dspark {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 320;  // warps 0-3: rows 0 .. R/2 - 1, 4-7: the others, 8: TMA, 9: MMA
+constexpr int kMaxSlots = 12;
+constexpr float kUnset = -1e30f, kRescaleAt = 60.f;  // log2 units
+
+template <int R>
+struct Shared {
+  uint64_t q_full[2], q_empty[2], kv_full[kMaxSlots], kv_empty[kMaxSlots], s_full[2], p_full[2], p_empty[2];
+  uint64_t o_full, group[2], drain;
+  uint32_t tmem_base;
+  volatile int abort;
+  int mma_pending;
+  int need[2][2];            // [half][parity]: the last tile at which a warp asked for a new reference
+  Range range;
+  float warp_max[2][4][R / 2], warp_sum[2][4][R / 2];  // [half][warp]: the rows' maxima of a tile, sums of a unit
+  alignas(16) float ref[R];  // the rows' references, read four at a time
+  float scale[R];            // what a new reference scales the old sums by
+};
+
+template <int D, int R>
+struct Cfg {
+  static constexpr int kHalves = D / 64;                   // 128-byte swizzled column blocks of a tile
+  static constexpr int kSlotBytes = kTile * D * 2;
+  static constexpr int kQBytes = R * D * 2, kQBufs = R == 128 ? 1 : 2;
+  static constexpr int kPPitch = R < 64 ? R * 2 : 128;      // bytes of a slot's row of P, R > 64: in two chunks
+  static constexpr int kPBytes = kTile * R * 2, kPBufs = R >= 64 ? 1 : 2;
+  // O^T has M = 128 also where D = 64: its lanes 64 .. 127 come from the 16 KB behind the V tile, whatever
+  // they hold, and are not read
+  static constexpr int kBehind = kQBytes * kQBufs + kPBytes * kPBufs;
+  static constexpr int kPad = D == 64 && kBehind < 16384 ? 16384 - kBehind : 0;
+  static constexpr int kRoom = (232448 - int(sizeof(Shared<R>)) - kBehind - kPad) / kSlotBytes;
+  static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;
+  static constexpr int kSmem = kSlots * kSlotBytes + kBehind + kPad + int(sizeof(Shared<R>));
+  static constexpr int kTmemCols = 4 * R;  // S^T twice, O^T; a power of two
+  static_assert(kSlots >= 3 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "shared memory layout");
+};
+
+// The tiles of a CTA's range one by one.
+struct Cursor {
+  Walk walk;
+  Segment s = {};
+  int j = 0;
+  __device__ Cursor(const Range& g, int unit_tokens) : walk(g, unit_tokens) {}
+  __device__ __forceinline__ bool next(const AttnArgs& a, const Range& g) {
+    if (++j < s.n) return true;
+    j = 0;
+    return walk.next(a, g, s);
+  }
+  __device__ __forceinline__ bool first() const { return j == 0; }
+  __device__ __forceinline__ bool last() const { return j + 1 == s.n; }
+};
+
+// Sums over the 32 lanes of N values each (N = 8, 16 or a multiple of 32), in a fixed order, halving the values with the
+// lanes: afterwards lane l holds the sum of value l * N / 32 (N < 32: of value l / (32 / N)) in v[0], of value
+// 32 + l in v[1], ..
+template <int N>
+__device__ __forceinline__ void warp_sums(float* v, int lane) {
+  constexpr int kFold = N < 32 ? N : 32;
+#pragma unroll
+  for (int b = 0; b < N; b += kFold) {
+    float* x = v + b;
+    int cnt = kFold;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (cnt > 1) {
+        cnt >>= 1;
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < kFold / 2; ++i)
+          if (i < cnt) {
+            const float send = up ? x[i] : x[i + cnt], keep = up ? x[i + cnt] : x[i];
+            x[i] = keep + __shfl_xor_sync(~0u, send, o);
+          }
+      } else {
+        x[0] += __shfl_xor_sync(~0u, x[0], o);
+      }
+    }
+    v[b / kFold] = x[0];
+  }
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnArgs a) {
+  using C = Cfg<D, R>;
+  constexpr int RW = R / 2;  // rows per thread
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sKV = smem;
+  uint8_t* sQ = sKV + C::kSlots * C::kSlotBytes;
+  uint8_t* sP = sQ + C::kQBytes * C::kQBufs;
+  Shared<R>* sh = reinterpret_cast<Shared<R>*>(sP + C::kPBytes * C::kPBufs + C::kPad);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile_rows = a.tokens * a.g;
+  const Waiter wait{&sh->abort, a.timeout_ns};
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh->q_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->q_empty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->s_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->p_full[i]), 8);
+      tc::mbar_init(tc::smem_u32(&sh->p_empty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->group[i]), 4);
+      sh->need[i][0] = sh->need[i][1] = 0;
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh->kv_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->kv_empty[i]), 1);
+    }
+    tc::mbar_init(tc::smem_u32(&sh->o_full), 1);
+    tc::mbar_init(tc::smem_u32(&sh->drain), 1);
+    tc::fence_mbar_init();
+    sh->abort = 0, sh->mma_pending = 0, sh->range.bad = 0, sh->range.n_long = 0;
+    tc::prefetch_tensormap(&map_q);
+    tc::prefetch_tensormap(&map_k);
+    tc::prefetch_tensormap(&map_v);
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(tc::smem_u32(&sh->tmem_base), C::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  // rows of Q past the unit's last are never loaded: zeros, so that their scores are 0
+  for (int i = tid; i < C::kQBytes * C::kQBufs / 16; i += kThreads)
+    reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+  tc::fence_proxy_async_smem();
+  __syncthreads();
+  pdl_enter();
+  plan_range(a, sh->range, reinterpret_cast<uint8_t*>(sh->warp_max), a.tokens);
+  __syncthreads();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (warp == 8) {
+    // --------------------------------------------------------------------- TMA producer
+    // Ring order: K 0, K 1, then V t, K t + 2, over all tiles of the range; a unit's Q with its first K.
+    const uint64_t keep = tc::policy_evict_last(), stream = tc::policy_evict_first();
+    int slot = 0, n_seg = 0, flags = 0;
+    uint32_t phase = 0, issued = 0;
+    int q_uses[2] = {0, 0};
+    int4 info = make_int4(0, 0, 0, 0);
+    Cursor cur(sh->range, a.tokens);
+    struct Ahead {
+      TileLoad t;
+      int row0;  // >= 0: the unit's first tile here
+      bool there;
+    };
+    auto fetch = [&]() {  // the next tile's pages; used three tiles later
+      Ahead f = {};
+      f.there = cur.next(a, sh->range);
+      if (!f.there) return f;
+      const Segment& s = cur.s;
+      f.t = tile_load(a, s, cur.j, lane);
+      f.row0 = cur.first() ? s.row0 : -1;
+      if (cur.first()) {
+        if (s.tile0 > 0) flags |= kTailUsed | (s.tile0 + s.n == s.u.ntiles ? kTailEnds : 0);
+        if (s.tile0 == 0 && s.n < s.u.ntiles) flags |= kHeadUsed, info = make_int4(0, s.row0, s.ntok, s.h);
+      }
+      return f;
+    };
+    auto put = [&](const CUtensorMap* map, const Ahead& f) {
+      if (!wait(&sh->kv_empty[slot], phase ^ 1)) return false;
+      issue_tile<C::kHalves>(a, map, f.t, tc::smem_u32(sKV + slot * C::kSlotBytes), tc::smem_u32(&sh->kv_full[slot]), stream,
+                             lane);
+      issued |= 1u << slot;
+      if (++slot == C::kSlots) slot = 0, phase ^= 1;
+      return true;
+    };
+    auto put_k = [&](const Ahead& f) {
+      if (!put(&map_k, f)) return false;
+      if (f.row0 < 0) return true;
+      const int b = n_seg++ % C::kQBufs;
+      if (!wait(&sh->q_empty[b], (q_uses[b] & 1) ^ 1)) return false;
+      if (lane == 0) {
+        const uint32_t bar = tc::smem_u32(&sh->q_full[b]);
+        tc::mbar_arrive_expect_tx(bar, uint32_t(tile_rows * 128 * C::kHalves));
+#pragma unroll
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tc::tma_load_3d(tc::smem_u32(sQ + b * C::kQBytes + hf * (R * 128)), &map_q, bar, hf * 64, f.t.head * a.g,
+                          f.row0, keep);
+      }
+      ++q_uses[b];
+      return true;
+    };
+    Ahead f0 = fetch(), f1 = fetch(), f2 = fetch(), f3 = fetch();
+    bool ok = (!f0.there || put_k(f0)) && (!f1.there || put_k(f1));
+    while (ok && f0.there) {
+      ok = put(&map_v, f0) && (!f2.there || put_k(f2));
+      f0 = f1, f1 = f2, f2 = f3, f3 = fetch();
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 1u, uint32_t(n_seg));
+      // wait (bounded) for every copy in flight before the CTA exits
+      const volatile int never = 0;
+      const long long dl = tc::deadline_after_ns(200000000ull);
+      for (int i = 0; i < C::kSlots; ++i)  // slots before `slot` were last used in this round, the others in the last one
+        if (issued >> i & 1u)
+          tc::mbar_wait_bounded(tc::smem_u32(&sh->kv_full[i]), i < slot ? phase : phase ^ 1, dl, &never);
+      for (int b = 0; b < 2; ++b)
+        if (q_uses[b] > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[b]), (q_uses[b] - 1) & 1, dl, &never);
+    }
+    if (lane == 0) {
+      info.x = ok ? flags : 0;
+      a.info[blockIdx.x] = info;
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kTile, R);
+    constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(128, R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
+    int slot = 0, n_seg = 0, n_qk = 0;
+    uint32_t phase = 0;
+    int q_uses[2] = {0, 0};
+    bool any = false;
+    Cursor kc(sh->range, a.tokens), vc(sh->range, a.tokens);
+    auto take = [&](int& which) {  // the next filled slot of the ring
+      which = slot;
+      if (!wait(&sh->kv_full[slot], phase)) return false;
+      if (++slot == C::kSlots) slot = 0, phase ^= 1;
+      return true;
+    };
+    auto qk = [&]() {  // S^T of the tile at kc
+      const int b = n_seg % C::kQBufs;
+      if (kc.first() && !wait(&sh->q_full[b], q_uses[b]++ & 1)) return false;
+      int ks;
+      if (!take(ks)) return false;
+      tc::tc_fence_after();
+      if (lane == 0) {
+        const uint32_t q = tc::smem_u32(sQ + b * C::kQBytes), k = tc::smem_u32(sKV + ks * C::kSlotBytes);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          tc::mma_bf16(tmem + (n_qk & 1) * R, tc::sdesc_kmajor_sw128(k + (i / 4) * (kTile * 128) + (i % 4) * 32),
+                       tc::sdesc_kmajor_sw128(q + (i / 4) * (R * 128) + (i % 4) * 32), idesc_qk, i != 0);
+        tc::mma_commit(tc::smem_u32(&sh->s_full[n_qk & 1]));
+        tc::mma_commit(tc::smem_u32(&sh->kv_empty[ks]));
+        if (kc.last()) tc::mma_commit(tc::smem_u32(&sh->q_empty[b]));
+      }
+      __syncwarp();
+      any = true;
+      ++n_qk;
+      if (kc.last()) ++n_seg;
+      return true;
+    };
+    bool more = kc.next(a, sh->range);
+    bool ok = !more || qk();
+    if (ok && more) {
+      more = kc.next(a, sh->range);
+      ok = !more || qk();
+    }
+    int t = 0;
+    for (; ok && vc.next(a, sh->range); ++t) {
+      int vs;
+      ok = take(vs);
+      if (!ok) break;
+      clear_unseen<C::kHalves>(a, vc.s, vc.j, sKV + vs * C::kSlotBytes, lane);
+      ok = wait(&sh->p_full[t & 1], (t >> 1) & 1);
+      if (!ok) break;
+      tc::tc_fence_after();
+      if (lane == 0) {
+        const uint32_t v = tc::smem_u32(sKV + vs * C::kSlotBytes), p = tc::smem_u32(sP + (t % C::kPBufs) * C::kPBytes);
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          tc::mma_bf16(tmem + 2 * R, tc::sdesc_mnmajor<128>(v + i * 2048, kTile * 128),
+                       tc::sdesc_mnmajor<C::kPPitch>(p + i * 16 * C::kPPitch, kTile * 128), idesc_pv, vc.j > 0 || i != 0);
+        tc::mma_commit(tc::smem_u32(&sh->kv_empty[vs]));
+        tc::mma_commit(tc::smem_u32(&sh->p_empty[t % C::kPBufs]));
+        if (vc.last()) tc::mma_commit(tc::smem_u32(&sh->o_full));
+      }
+      __syncwarp();
+      if (more) {
+        more = kc.next(a, sh->range);
+        ok = !more || qk();
+      }
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 2u, uint32_t(t));
+    }
+    if (lane == 0) sh->mma_pending = any;
+  } else {
+    // ------------------------------------------------------------------------- softmax
+    const int half = warp >> 2, w4 = warp & 3;
+    const int kv = w4 * 32 + lane;  // this thread's slot of each tile = TMEM lane
+    const int row0 = half * RW;     // and its rows
+    const uint32_t lane_base = tmem + (uint32_t(w4 * 32) << 16);
+    const uint32_t t_o = lane_base + 2 * R + row0;
+    const float c2 = a.c2;
+    float* ref = sh->ref + row0;
+    float* scale = sh->scale + row0;
+    int t = 0, sync = 0, n_seg = 0;
+    bool ok = true;
+    Walk walk(sh->range, a.tokens);
+    Segment s = {};
+    // the half's four warps: everything before on all of them is visible after
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->group[half]));
+      return wait(&sh->group[half], sync++ & 1);
+    };
+    while (ok && walk.next(a, sh->range, s)) {
+      float l[RW];  // this slot's share of the rows' sums
+#pragma unroll
+      for (int i = 0; i < RW; ++i) l[i] = 0.f;
+      for (int j = 0; j < s.n; ++j, ++t) {
+        ok = wait(&sh->s_full[t & 1], (t >> 1) & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        float x[RW];
+        tc::tmem_ld<RW>(lane_base + (t & 1) * R + row0, x);
+        tc::tmem_ld_wait();
+        const int first = (s.tile0 + j) * (kTile >> a.block_shift);
+        const int begin = block_pos(a, s.u, first);
+        const bool inside = first >= s.u.sb && begin + kTile - 1 <= s.u.p0 && (a.window == 0 || begin > s.u.p1 - a.window);
+        if (!inside) {
+          // rows of tokens at p0 + tok see the slot from tok = pos - p0 on, for `window` tokens, sinks always
+          const int pos = block_pos(a, s.u, first + (kv >> a.block_shift)) + (kv & ((1 << a.block_shift) - 1));
+          const int d = pos - s.u.p0;
+          const int from = d <= 0 ? 0 : d >= a.tokens ? R : d * a.g;
+          int to = R;
+          if (a.window && pos >= a.n_sink) to = d + a.window <= 0 ? 0 : d + a.window >= a.tokens ? R : (d + a.window) * a.g;
+          const float hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
+#pragma unroll
+          for (int i = 0; i < RW; ++i)
+            if (row0 + i < from || row0 + i >= to) x[i] = hidden;
+        }
+        const unsigned long long cc = pack_f32x2(c2, c2);
+        float y[RW];
+        bool fresh = j == 0;  // a new reference is needed
+        if (!fresh) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < RW; i += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(ref + i);
+            unpack_f32x2(fma_f32x2(pack_f32x2(x[i], x[i + 1]), cc, pack_f32x2(-m.x, -m.y)), y[i], y[i + 1]);
+            unpack_f32x2(fma_f32x2(pack_f32x2(x[i + 2], x[i + 3]), cc, pack_f32x2(-m.z, -m.w)), y[i + 2], y[i + 3]);
+            top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
+          }
+          if (__any_sync(~0u, top > kRescaleAt) && lane == 0) sh->need[half][sync & 1] = t + 1;
+          const int at = sync & 1;
+          ok = meet();
+          if (!ok) break;
+          fresh = sh->need[half][at] == t + 1;
+        }
+        if (fresh) {
+          // each row's maximum over the tile's 128 slots, by warp then over the half's warps
+          float mine[(RW + 31) / 32];
+#pragma unroll
+          for (int i = 0; i < RW; ++i) {
+            const float m = tc::redux_max(x[i] * c2);
+            if (lane == (i & 31)) mine[i >> 5] = m;
+          }
+          float old[(RW + 31) / 32];
+#pragma unroll
+          for (int b = 0; b < RW; b += 32)
+            if (b + lane < RW) {
+              sh->warp_max[half][w4][b + lane] = mine[b >> 5];
+              old[b >> 5] = j == 0 ? kUnset : ref[b + lane];
+            }
+          ok = meet();
+          if (!ok) break;
+#pragma unroll
+          for (int b = 0; b < RW; b += 32)
+            if (b + lane < RW) {  // the four warps write the same values
+              const float (*part)[RW] = sh->warp_max[half];
+              const float m = fmaxf(fmaxf(old[b >> 5], fmaxf(part[0][b + lane], part[1][b + lane])),
+                                    fmaxf(part[2][b + lane], part[3][b + lane]));
+              ref[b + lane] = m;
+              scale[b + lane] = tc::ex2_approx(old[b >> 5] - m);
+            }
+          __syncwarp();
+          if (j > 0) {
+            // the sums so far and this thread's lane of O^T, after the last tile's product
+            ok = wait(&sh->p_empty[(t - 1) % C::kPBufs], ((t - 1) / C::kPBufs) & 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+            float o[RW];
+            tc::tmem_ld<RW>(t_o, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < RW; ++i) l[i] *= scale[i], o[i] *= scale[i];
+            tc::tmem_st<RW>(t_o, o);
+            tc::tmem_st_wait();
+          }
+#pragma unroll
+          for (int i = 0; i < RW; ++i) y[i] = fmaf(x[i], c2, -ref[i]);
+        }
+        uint32_t pk[RW / 2];
+#pragma unroll
+        for (int i = 0; i < RW; i += 2) {
+          const float e0 = tc::ex2_approx(y[i]), e1 = tc::ex2_approx(y[i + 1]);
+          l[i] += e0, l[i + 1] += e1;
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
+          pk[i / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        ok = wait(&sh->p_empty[t % C::kPBufs], ((t / C::kPBufs) & 1) ^ 1);
+        if (!ok) break;
+        uint8_t* p = sP + (t % C::kPBufs) * C::kPBytes + (R == 128 ? half * (kTile * 128) : 0);
+        const int piece0 = R == 128 ? 0 : row0 / 8;
+#pragma unroll
+        for (int i = 0; i < RW / 8; ++i)
+          *reinterpret_cast<uint4*>(p + tc::swizzled<C::kPPitch>(kv, piece0 + i)) =
+              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        tc::fence_proxy_async_smem();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->p_full[t & 1]));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------------- the unit's rows
+      // rows' sums over the 128 slots: lanes, then the half's warps in order
+      warp_sums<RW>(l, lane);
+      if (RW >= 32 || (lane & (32 / RW - 1)) == 0) {
+#pragma unroll
+        for (int b = 0; b < (RW + 31) / 32; ++b)
+          sh->warp_sum[half][w4][b * 32 + (RW >= 32 ? lane : lane / (32 / RW))] = l[b];
+      }
+      ok = meet();
+      if (!ok) break;
+      const bool partial = s.n < s.u.ntiles;
+      const int64_t pbase = (int64_t(2) * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * R;
+      const int n_rows = s.ntok * a.g;
+      float inv[(RW + 31) / 32];
+#pragma unroll
+      for (int b = 0; b < RW; b += 32) {
+        const int i = b + lane;
+        inv[b >> 5] = 0.f;
+        if (i < RW) {
+          const float (*part)[RW] = sh->warp_sum[half];
+          const float sum = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+          inv[b >> 5] = sum > 0.f ? 1.f / sum : 0.f;
+          const int row = row0 + i;
+          if (w4 == 0 && row < n_rows) {
+            const float lse2 = sum > 0.f ? ref[i] + log2f(sum) : -INFINITY;
+            if (partial)
+              a.plse[pbase + row] = lse2;
+            else if (a.lse)
+              a.lse[int64_t(s.row0 + row / a.g) * a.Hq + s.h * a.g + row % a.g] = lse2 * kLn2;
+          }
+        }
+      }
+      ok = wait(&sh->o_full, n_seg & 1);
+      if (!ok) break;
+      tc::tc_fence_after();
+      float o[RW];
+      tc::tmem_ld<RW>(t_o, o);
+      tc::tmem_ld_wait();
+      tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
+      if (kv < D) {           // TMEM lane = lane of the head
+        int tok = row0 / a.g, hh = row0 - tok * a.g;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          const float v = o[i] * __shfl_sync(~0u, inv[i >> 5], i & 31);
+          if (row0 + i < n_rows) {
+            if (partial)
+              a.partial[(pbase + row0 + i) * D + kv] = v;
+            else
+              a.out[(int64_t(s.row0 + tok) * a.Hq + s.h * a.g + hh) * D + kv] = __float2bfloat16(v);
+          }
+          if (++hh == a.g) hh = 0, ++tok;
+        }
+      }
+      ++n_seg;
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 3u, uint32_t(t) | uint32_t(warp) << 24);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 9) {
+    if (lane == 0 && sh->mma_pending && sh->abort) {  // MMAs may be in flight: wait (bounded) before TMEM is freed
+      tc::mma_commit(tc::smem_u32(&sh->drain));
+      const volatile int never = 0;
+      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain), 0, tc::deadline_after_ns(200000000ull), &never);
+    }
+    __syncwarp();
+    tc::tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int D, int R>
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int n_cta,
+                   cudaStream_t s) {
+  static bool done[tch::kMaxDevices] = {};
+  static std::mutex mu;
+  constexpr int kSmem = Cfg<D, R>::kSmem;
+  const cudaError_t e = tch::set_smem_once(window_kernel<D, R>, kSmem, done, &mu);
+  return e != cudaSuccess ? e : launch_pdl(window_kernel<D, R>, dim3(n_cta), dim3(kThreads), kSmem, s, q, k, v, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_windows(int D, int unit_rows, const CUtensorMap& q, const CUtensorMap& k,
+                                     const CUtensorMap& v, const attn::AttnArgs& a, int n_cta, cudaStream_t s) {
+  if (D == 64) switch (unit_rows) {
+      case 16: return launch<64, 16>(q, k, v, a, n_cta, s);
+      case 32: return launch<64, 32>(q, k, v, a, n_cta, s);
+      case 64: return launch<64, 64>(q, k, v, a, n_cta, s);
+      default: return launch<64, 128>(q, k, v, a, n_cta, s);
+    }
+  switch (unit_rows) {
+    case 16: return launch<128, 16>(q, k, v, a, n_cta, s);
+    case 32: return launch<128, 32>(q, k, v, a, n_cta, s);
+    case 64: return launch<128, 64>(q, k, v, a, n_cta, s);
+    default: return launch<128, 128>(q, k, v, a, n_cta, s);
+  }
+}
+
+}  // namespace dspark

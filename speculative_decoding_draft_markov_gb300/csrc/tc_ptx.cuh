@@ -218,6 +218,38 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
         "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr));
 }
+// 32 lanes x 8 consecutive 32-bit columns into registers.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr));
+}
+// N columns: 8, 16 or a multiple of 32 (loads), a multiple of 8 (stores).
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  if constexpr (N == 8) {
+    tmem_ld8(taddr, u);
+  } else if constexpr (N == 16) {
+    tmem_ld16(taddr, u);
+  } else {
+    static_assert(N % 32 == 0, "columns");
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tmem_ld32(taddr + i, u + i);
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float* v) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
+  if constexpr (N % 32 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tmem_st32(taddr + i, u + i);
+  } else {
+    static_assert(N % 8 == 0, "columns");
+#pragma unroll
+    for (int i = 0; i < N; i += 8) tmem_st8(taddr + i, u + i);
+  }
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -242,18 +274,34 @@ __device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t saddr) {
 // The same for an MN-major operand (rows of 64 elements of the M or N dimension, one row per K
 // element): 8-row groups of K are 1024 bytes apart (stride byte offset), further 64-element chunks
 // of M or N `chunk_bytes` apart (leading byte offset).  The start address advances by 2048 bytes per
-// 16-element K step.
-__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t chunk_bytes) {
+// 16-element K step.  Rows of 32 or 16 elements use the 64- or 32-byte swizzle, everything in proportion.
+template <int kRowBytes = 128>
+__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t saddr, uint32_t chunk_bytes) {
+  static_assert(kRowBytes == 128 || kRowBytes == 64 || kRowBytes == 32, "swizzle span");
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
   d |= static_cast<uint64_t>(chunk_bytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>((8 * kRowBytes) >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
+  d |= static_cast<uint64_t>(kRowBytes == 128 ? 2 : kRowBytes == 64 ? 4 : 6) << 61;
   return d;
 }
+// Byte of 16-byte piece `piece` of row `row` under that layout's swizzle.
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t swizzled(int row, int piece) {
+  const int x = kRowBytes == 128 ? row & 7 : kRowBytes == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+  return uint32_t(row * kRowBytes + ((piece ^ x) << 4));
+}
 
-constexpr uint32_t kIdescBMajorMN = 1u << 16;  // instruction descriptor: B is MN-major
+// Instruction descriptor bits: A, B is MN-major.
+constexpr uint32_t kIdescAMajorMN = 1u << 15, kIdescBMajorMN = 1u << 16;
+
+// Maximum over the warp's lanes, in all lanes.
+__device__ __forceinline__ float redux_max(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
 
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, both K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {

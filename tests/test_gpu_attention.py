@@ -119,6 +119,21 @@ CASES = {
     "prompts": ([257, 1, 130], [5, 600, 40], 4, 2, 128, 32, 0, 0),
     "prompt_window": ([400, 190], [100, 0], 6, 2, 64, 16, 90, 5),
     "prompt_group_5": ([150, 77], [300, 12], 5, 1, 128, 128, 64, 4),
+    "rows_16": ([4, 1, 2], [300, 128, 1000], 8, 2, 64, 32, 200, 4),
+    "rows_64": ([16, 5], [700, 77], 8, 2, 128, 32, 300, 4),
+    "rows_64_d64": ([13, 16], [900, 130], 4, 1, 64, 64, 0, 0),
+    "rows_128": ([16, 11], [700, 77], 16, 2, 128, 32, 300, 4),
+    "rows_128_d64": ([16, 9, 3], [900, 130, 0], 8, 1, 64, 16, 500, 2),
+    "rows_128_split": ([16], [5000], 8, 1, 128, 64, 0, 0),
+    # enough work that one block takes many tiles of many units, at each tiling
+    "busy_16": ([1, 3, 2] * 30, [1500, 700, 1111] * 30, 8, 2, 64, 64, 0, 0),
+    "busy_32": ([8, 5, 3] * 25, [1500, 700, 90] * 25, 8, 2, 128, 32, 600, 4),
+    "busy_64": ([16, 5, 9] * 12, [1500, 700, 2000] * 12, 16, 4, 64, 16, 900, 4),
+    "busy_64_d128": ([16, 5, 9] * 12, [1500, 700, 2000] * 12, 8, 2, 128, 64, 0, 0),
+    "busy_128": ([16, 5] * 12, [1500, 300] * 12, 16, 2, 128, 64, 800, 4),
+    "busy_128_d64": ([16, 5] * 12, [1500, 300] * 12, 16, 2, 64, 64, 0, 0),
+    "busy_prompts": ([90, 40] * 10, [1500, 300] * 10, 8, 2, 128, 64, 500, 4),
+    "busy_prompts_d64": ([90, 40] * 10, [1500, 300] * 10, 8, 2, 64, 64, 0, 0),
     "many_requests": ([1 + r % 4 for r in range(150)], [(r * 37) % 300 for r in range(150)], 2, 1, 64, 16, 64, 2),
 }
 
@@ -172,6 +187,35 @@ def test_attention_far_scores(q_scale, scale):
             first += n
         return
     _check_attention(c, 4, 0, 0, seed=10, scale=scale)
+
+
+@pytest.mark.parametrize("n,hq", [(1, 4), (8, 4), (16, 4), (16, 8), (40, 8)])
+def test_attention_scores_that_grow(n, hq):
+    """Scores that jump by hundreds from tile to tile, up and down, at each tiling: the reference of the
+    exponentials has to follow.  q = 1, key j = c_j in every lane and scale 1 / D: the scores are c_j exactly."""
+    d, page, ctx = 64, 32, 900
+    c = Cache([n], [ctx], 1, d, page, seed=18)
+    step = np.array([0.0, 110.0, -40.0, 300.0, 290.0, 301.0, 1000.0, 990.0])
+    level = step[np.minimum(np.arange(ctx + n) // 128, 7)] + (np.arange(ctx + n) % 4) * 0.5
+    level = _f64(torch.from_numpy(level).to(torch.bfloat16))
+    c.keys[0] = np.repeat(level[:, None, None], d, 2)
+    table = c.table.cpu().numpy()
+    for j in range(ctx + n):
+        c.k[table[0, j // page], :, j % page] = float(level[j])
+    # 160 requests over the same pages: enough work that a block takes whole units
+    bs = 160
+    q = torch.ones(bs * n, hq, d, dtype=torch.bfloat16, device="cuda")
+    cu = torch.arange(0, bs * n + 1, n, dtype=torch.int32, device="cuda")
+    many = c.ctx.repeat(bs), c.table.repeat(bs, 1)
+    ws = B.alloc_attention_workspace(hq, 1, d)
+    for window, sinks in ((0, 0), (200, 4), (600, 0)):
+        out = torch.zeros_like(q)
+        lse = torch.zeros(bs * n, hq, device="cuda")
+        B.dspark_window_attention(q, c.k, c.v, many[1], cu, many[0], n, 1.0 / d, window, sinks, out, lse, ws)
+        assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+        ref, rl, mag = R.attention(_f64(q)[:n], c.keys[0], c.vals[0], ctx, 1.0 / d, window, sinks)
+        assert (np.abs(_f64(out).reshape(bs, n, hq, d) - ref) <= R.attention_bound(mag)).all()
+        assert np.abs(_f64(lse).reshape(bs, n, hq) - rl).max() <= 1e-4 * (1 + np.abs(rl).max())
 
 
 def test_attention_offsets_beyond_32_bits():
