@@ -19,17 +19,17 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 320;  // warps 0-3: rows 0 .. R/2 - 1, 4-7: the others, 8: TMA, 9: MMA
-constexpr int kMaxSlots = 12;
+constexpr int kThreads = 352;  // warps 0-3: softmax of rows 0 .. R/2 - 1, 4-7: of the others, 8: TMA, 9: S, 10: O
+constexpr int kMaxSlots = 6;
 constexpr float kUnset = -1e30f, kRescaleAt = 60.f;  // log2 units
 
 template <int R>
 struct Shared {
-  uint64_t q_full[2], q_empty[2], kv_full[kMaxSlots], kv_empty[kMaxSlots], s_full[2], p_full[2], p_empty[2];
-  uint64_t o_full, group[2], drain;
+  uint64_t q_full[2], q_empty[2], k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
+  uint64_t s_full[2], p_full[2], p_empty[2], o_full, group[2], drain[2];
   uint32_t tmem_base;
   volatile int abort;
-  int mma_pending;
+  int pending[2];            // the MMA warps have issued something
   int need[2][2];            // [half][parity]: the last tile at which a warp asked for a new reference
   Range range;
   float warp_max[2][4][R / 2], warp_sum[2][4][R / 2];  // [half][warp]: the rows' maxima of a tile, sums of a unit
@@ -48,11 +48,23 @@ struct Cfg {
   // they hold, and are not read
   static constexpr int kBehind = kQBytes * kQBufs + kPBytes * kPBufs;
   static constexpr int kPad = D == 64 && kBehind < 16384 ? 16384 - kBehind : 0;
+  // rings of K and V tiles; K runs two tiles ahead of V
   static constexpr int kRoom = (232448 - int(sizeof(Shared<R>)) - kBehind - kPad) / kSlotBytes;
-  static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;
-  static constexpr int kSmem = kSlots * kSlotBytes + kBehind + kPad + int(sizeof(Shared<R>));
+  static constexpr int kVSlots = (kRoom + 1) / 2 < kMaxSlots ? (kRoom + 1) / 2 : kMaxSlots;
+  static constexpr int kKSlots = kRoom / 2 < kMaxSlots ? kRoom / 2 : kMaxSlots;
+  static constexpr int kSmem = (kKSlots + kVSlots) * kSlotBytes + kBehind + kPad + int(sizeof(Shared<R>));
   static constexpr int kTmemCols = 4 * R;  // S^T twice, O^T; a power of two
-  static_assert(kSlots >= 3 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "shared memory layout");
+  static_assert(kKSlots >= 2 && kVSlots >= 2 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "shared memory layout");
+};
+
+// A position in a ring of N slots.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == N) slot = 0, phase ^= 1;
+  }
 };
 
 // The tiles of a CTA's range one by one.
@@ -106,11 +118,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D, R>;
   constexpr int RW = R / 2;  // rows per thread
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sKV = smem;
-  uint8_t* sQ = sKV + C::kSlots * C::kSlotBytes;
+  uint8_t* sK = smem;
+  uint8_t* sV = sK + C::kKSlots * C::kSlotBytes;
+  uint8_t* sQ = sV + C::kVSlots * C::kSlotBytes;
   uint8_t* sP = sQ + C::kQBytes * C::kQBufs;
   Shared<R>* sh = reinterpret_cast<Shared<R>*>(sP + C::kPBytes * C::kPBufs + C::kPad);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same for the warp, and known to be
   const int tile_rows = a.tokens * a.g;
   const Waiter wait{&sh->abort, a.timeout_ns};
 
@@ -124,14 +138,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(tc::smem_u32(&sh->group[i]), 4);
       sh->need[i][0] = sh->need[i][1] = 0;
     }
-    for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(tc::smem_u32(&sh->kv_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->kv_empty[i]), 1);
+    for (int i = 0; i < kMaxSlots; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh->k_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->k_empty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->v_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->v_empty[i]), 1);
     }
     tc::mbar_init(tc::smem_u32(&sh->o_full), 1);
-    tc::mbar_init(tc::smem_u32(&sh->drain), 1);
+    tc::mbar_init(tc::smem_u32(&sh->drain[0]), 1);
+    tc::mbar_init(tc::smem_u32(&sh->drain[1]), 1);
     tc::fence_mbar_init();
-    sh->abort = 0, sh->mma_pending = 0, sh->range.bad = 0, sh->range.n_long = 0;
+    sh->abort = 0, sh->pending[0] = sh->pending[1] = 0, sh->range.bad = 0, sh->range.n_long = 0;
     tc::prefetch_tensormap(&map_q);
     tc::prefetch_tensormap(&map_k);
     tc::prefetch_tensormap(&map_v);
@@ -152,10 +169,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 8) {
     // --------------------------------------------------------------------- TMA producer
-    // Ring order: K 0, K 1, then V t, K t + 2, over all tiles of the range; a unit's Q with its first K.
+    // In order: K 0, K 1, then V t, K t + 2, over all tiles of the range; a unit's Q with its first K.
     const uint64_t keep = tc::policy_evict_last(), stream = tc::policy_evict_first();
-    int slot = 0, n_seg = 0, flags = 0;
-    uint32_t phase = 0, issued = 0;
+    Ring<C::kKSlots> kr;
+    Ring<C::kVSlots> vr;
+    int n_seg = 0, flags = 0, n_k = 0, n_v = 0;
     int q_uses[2] = {0, 0};
     int4 info = make_int4(0, 0, 0, 0);
     Cursor cur(sh->range, a.tokens);
@@ -177,16 +195,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return f;
     };
-    auto put = [&](const CUtensorMap* map, const Ahead& f) {
-      if (!wait(&sh->kv_empty[slot], phase ^ 1)) return false;
-      issue_tile<C::kHalves>(a, map, f.t, tc::smem_u32(sKV + slot * C::kSlotBytes), tc::smem_u32(&sh->kv_full[slot]), stream,
-                             lane);
-      issued |= 1u << slot;
-      if (++slot == C::kSlots) slot = 0, phase ^= 1;
+    auto put_v = [&](const Ahead& f) {
+      if (!wait(&sh->v_empty[vr.slot], vr.phase ^ 1)) return false;
+      issue_tile<C::kHalves>(a, &map_v, f.t, tc::smem_u32(sV + vr.slot * C::kSlotBytes), tc::smem_u32(&sh->v_full[vr.slot]),
+                             stream, lane);
+      ++n_v;
+      vr.step();
       return true;
     };
     auto put_k = [&](const Ahead& f) {
-      if (!put(&map_k, f)) return false;
+      if (!wait(&sh->k_empty[kr.slot], kr.phase ^ 1)) return false;
+      issue_tile<C::kHalves>(a, &map_k, f.t, tc::smem_u32(sK + kr.slot * C::kSlotBytes), tc::smem_u32(&sh->k_full[kr.slot]),
+                             stream, lane);
+      ++n_k;
+      kr.step();
       if (f.row0 < 0) return true;
       const int b = n_seg++ % C::kQBufs;
       if (!wait(&sh->q_empty[b], (q_uses[b] & 1) ^ 1)) return false;
@@ -204,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ahead f0 = fetch(), f1 = fetch(), f2 = fetch(), f3 = fetch();
     bool ok = (!f0.there || put_k(f0)) && (!f1.there || put_k(f1));
     while (ok && f0.there) {
-      ok = put(&map_v, f0) && (!f2.there || put_k(f2));
+      ok = put_v(f0) && (!f2.there || put_k(f2));
       f0 = f1, f1 = f2, f2 = f3, f3 = fetch();
     }
     if (!ok) {
@@ -213,9 +235,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // wait (bounded) for every copy in flight before the CTA exits
       const volatile int never = 0;
       const long long dl = tc::deadline_after_ns(200000000ull);
-      for (int i = 0; i < C::kSlots; ++i)  // slots before `slot` were last used in this round, the others in the last one
-        if (issued >> i & 1u)
-          tc::mbar_wait_bounded(tc::smem_u32(&sh->kv_full[i]), i < slot ? phase : phase ^ 1, dl, &never);
+      // slots before the ring's position were last used in this round, the others in the last one
+      for (int i = 0; i < min(n_k, C::kKSlots); ++i)
+        tc::mbar_wait_bounded(tc::smem_u32(&sh->k_full[i]), i < kr.slot ? kr.phase : kr.phase ^ 1, dl, &never);
+      for (int i = 0; i < min(n_v, C::kVSlots); ++i)
+        tc::mbar_wait_bounded(tc::smem_u32(&sh->v_full[i]), i < vr.slot ? vr.phase : vr.phase ^ 1, dl, &never);
       for (int b = 0; b < 2; ++b)
         if (q_uses[b] > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[b]), (q_uses[b] - 1) & 1, dl, &never);
     }
@@ -224,78 +248,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       a.info[blockIdx.x] = info;
     }
   } else if (warp == 9) {
-    // ---------------------------------------------------------------------- MMA issuer
-    constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kTile, R);
-    constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(128, R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
-    int slot = 0, n_seg = 0, n_qk = 0;
-    uint32_t phase = 0;
-    int q_uses[2] = {0, 0};
-    bool any = false;
-    Cursor kc(sh->range, a.tokens), vc(sh->range, a.tokens);
-    auto take = [&](int& which) {  // the next filled slot of the ring
-      which = slot;
-      if (!wait(&sh->kv_full[slot], phase)) return false;
-      if (++slot == C::kSlots) slot = 0, phase ^= 1;
-      return true;
-    };
-    auto qk = [&]() {  // S^T of the tile at kc
+    // ------------------------------------------------------------------ S^T = K Q^T of each tile
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, R);
+    const uint64_t dk = tc::sdesc_kmajor_sw128(tc::smem_u32(sK)), dq = tc::sdesc_kmajor_sw128(tc::smem_u32(sQ));
+    Ring<C::kKSlots> ring;
+    int n_seg = 0, t = 0;
+    bool ok = true;
+    Cursor cur(sh->range, a.tokens);
+    for (; cur.next(a, sh->range); ++t) {
       const int b = n_seg % C::kQBufs;
-      if (kc.first() && !wait(&sh->q_full[b], q_uses[b]++ & 1)) return false;
-      int ks;
-      if (!take(ks)) return false;
+      ok = (!cur.first() || wait(&sh->q_full[b], (n_seg / C::kQBufs) & 1)) && wait(&sh->k_full[ring.slot], ring.phase) &&
+           (t < 2 || wait(&sh->p_full[t & 1], ((t - 2) >> 1) & 1));  // the S before last has been read
+      if (!ok) break;
       tc::tc_fence_after();
-      if (lane == 0) {
-        const uint32_t q = tc::smem_u32(sQ + b * C::kQBytes), k = tc::smem_u32(sKV + ks * C::kSlotBytes);
+      const uint64_t dk_t = dk + uint32_t(ring.slot * (C::kSlotBytes >> 4)), dq_t = dq + uint32_t(b * (C::kQBytes >> 4));
+      const bool last = cur.last();
+      if (tc::elect_one()) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          tc::mma_bf16(tmem + (n_qk & 1) * R, tc::sdesc_kmajor_sw128(k + (i / 4) * (kTile * 128) + (i % 4) * 32),
-                       tc::sdesc_kmajor_sw128(q + (i / 4) * (R * 128) + (i % 4) * 32), idesc_qk, i != 0);
-        tc::mma_commit(tc::smem_u32(&sh->s_full[n_qk & 1]));
-        tc::mma_commit(tc::smem_u32(&sh->kv_empty[ks]));
-        if (kc.last()) tc::mma_commit(tc::smem_u32(&sh->q_empty[b]));
+          tc::mma_bf16(tmem + (t & 1) * R, dk_t + (((i / 4) * (kTile * 128) + (i % 4) * 32) >> 4),
+                       dq_t + (((i / 4) * (R * 128) + (i % 4) * 32) >> 4), idesc, i != 0);
+        tc::mma_commit(tc::smem_u32(&sh->s_full[t & 1]));
+        tc::mma_commit(tc::smem_u32(&sh->k_empty[ring.slot]));
+        if (last) tc::mma_commit(tc::smem_u32(&sh->q_empty[b]));
       }
       __syncwarp();
-      any = true;
-      ++n_qk;
-      if (kc.last()) ++n_seg;
-      return true;
-    };
-    bool more = kc.next(a, sh->range);
-    bool ok = !more || qk();
-    if (ok && more) {
-      more = kc.next(a, sh->range);
-      ok = !more || qk();
-    }
-    int t = 0;
-    for (; ok && vc.next(a, sh->range); ++t) {
-      int vs;
-      ok = take(vs);
-      if (!ok) break;
-      clear_unseen<C::kHalves>(a, vc.s, vc.j, sKV + vs * C::kSlotBytes, lane);
-      ok = wait(&sh->p_full[t & 1], (t >> 1) & 1);
-      if (!ok) break;
-      tc::tc_fence_after();
-      if (lane == 0) {
-        const uint32_t v = tc::smem_u32(sKV + vs * C::kSlotBytes), p = tc::smem_u32(sP + (t % C::kPBufs) * C::kPBytes);
-#pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          tc::mma_bf16(tmem + 2 * R, tc::sdesc_mnmajor<128>(v + i * 2048, kTile * 128),
-                       tc::sdesc_mnmajor<C::kPPitch>(p + i * 16 * C::kPPitch, kTile * 128), idesc_pv, vc.j > 0 || i != 0);
-        tc::mma_commit(tc::smem_u32(&sh->kv_empty[vs]));
-        tc::mma_commit(tc::smem_u32(&sh->p_empty[t % C::kPBufs]));
-        if (vc.last()) tc::mma_commit(tc::smem_u32(&sh->o_full));
-      }
-      __syncwarp();
-      if (more) {
-        more = kc.next(a, sh->range);
-        ok = !more || qk();
-      }
+      ring.step();
+      if (last) ++n_seg;
     }
     if (!ok) {
       sh->abort = 1;
       if (lane == 0) note_timeout(a.status, a.diag, 2u, uint32_t(t));
     }
-    if (lane == 0) sh->mma_pending = any;
+    if (lane == 0) sh->pending[0] = t > 0;
+  } else if (warp == 10) {
+    // -------------------------------------------------------------- O^T += V^T P^T of each tile
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(128, R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
+    const uint64_t dv = tc::sdesc_mnmajor<128>(tc::smem_u32(sV), kTile * 128);
+    const uint64_t dp = tc::sdesc_mnmajor<C::kPPitch>(tc::smem_u32(sP), kTile * 128);
+    Ring<C::kVSlots> ring;
+    int t = 0;
+    bool ok = true;
+    Cursor cur(sh->range, a.tokens);
+    for (; cur.next(a, sh->range); ++t) {
+      ok = wait(&sh->v_full[ring.slot], ring.phase);
+      if (!ok) break;
+      clear_unseen<C::kHalves>(a, cur.s, cur.j, sV + ring.slot * C::kSlotBytes, lane);
+      ok = wait(&sh->p_full[t & 1], (t >> 1) & 1);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint64_t dv_t = dv + uint32_t(ring.slot * (C::kSlotBytes >> 4));
+      const uint64_t dp_t = dp + uint32_t((t % C::kPBufs) * (C::kPBytes >> 4));
+      const bool add = !cur.first(), last = cur.last();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          tc::mma_bf16(tmem + 2 * R, dv_t + ((i * 2048) >> 4), dp_t + ((i * 16 * C::kPPitch) >> 4), idesc, add || i != 0);
+        tc::mma_commit(tc::smem_u32(&sh->p_empty[t % C::kPBufs]));
+        tc::mma_commit(tc::smem_u32(&sh->v_empty[ring.slot]));
+        if (last) tc::mma_commit(tc::smem_u32(&sh->o_full));
+      }
+      __syncwarp();
+      ring.step();
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 4u, uint32_t(t));
+    }
+    if (lane == 0) sh->pending[1] = t > 0;
   } else {
     // ------------------------------------------------------------------------- softmax
     const int half = warp >> 2, w4 = warp & 3;
@@ -321,22 +341,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < RW; ++i) l[i] = 0.f;
       for (int j = 0; j < s.n; ++j, ++t) {
+        const int first = (s.tile0 + j) * (kTile >> a.block_shift);
+        const int begin = block_pos(a, s.u, first);
+        const bool inside = first >= s.u.sb && begin + kTile - 1 <= s.u.p0 && (a.window == 0 || begin > s.u.p1 - a.window);
+        int from = 0, to = R;  // the rows that see this thread's slot
+        if (!inside) {
+          // the token at p0 + tok sees the slot from tok = pos - p0 on, for `window` tokens, a sink always
+          const int pos = block_pos(a, s.u, first + (kv >> a.block_shift)) + (kv & ((1 << a.block_shift) - 1));
+          const int d = pos - s.u.p0;
+          from = d <= 0 ? 0 : d >= a.tokens ? R : d * a.g;
+          if (a.window && pos >= a.n_sink) to = d + a.window <= 0 ? 0 : d + a.window >= a.tokens ? R : (d + a.window) * a.g;
+        }
         ok = wait(&sh->s_full[t & 1], (t >> 1) & 1);
         if (!ok) break;
         tc::tc_fence_after();
         float x[RW];
         tc::tmem_ld<RW>(lane_base + (t & 1) * R + row0, x);
         tc::tmem_ld_wait();
-        const int first = (s.tile0 + j) * (kTile >> a.block_shift);
-        const int begin = block_pos(a, s.u, first);
-        const bool inside = first >= s.u.sb && begin + kTile - 1 <= s.u.p0 && (a.window == 0 || begin > s.u.p1 - a.window);
         if (!inside) {
-          // rows of tokens at p0 + tok see the slot from tok = pos - p0 on, for `window` tokens, sinks always
-          const int pos = block_pos(a, s.u, first + (kv >> a.block_shift)) + (kv & ((1 << a.block_shift) - 1));
-          const int d = pos - s.u.p0;
-          const int from = d <= 0 ? 0 : d >= a.tokens ? R : d * a.g;
-          int to = R;
-          if (a.window && pos >= a.n_sink) to = d + a.window <= 0 ? 0 : d + a.window >= a.tokens ? R : (d + a.window) * a.g;
           const float hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
 #pragma unroll
           for (int i = 0; i < RW; ++i)
@@ -465,17 +487,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_ld_wait();
       tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
       if (kv < D) {           // TMEM lane = lane of the head
-        int tok = row0 / a.g, hh = row0 - tok * a.g;
 #pragma unroll
-        for (int i = 0; i < RW; ++i) {
-          const float v = o[i] * __shfl_sync(~0u, inv[i >> 5], i & 31);
-          if (row0 + i < n_rows) {
-            if (partial)
-              a.partial[(pbase + row0 + i) * D + kv] = v;
-            else
-              a.out[(int64_t(s.row0 + tok) * a.Hq + s.h * a.g + hh) * D + kv] = __float2bfloat16(v);
+        for (int i = 0; i < RW; ++i) o[i] *= __shfl_sync(~0u, inv[i >> 5], i & 31);
+        if (partial) {
+          float* dst = a.partial + (pbase + row0) * D + kv;
+#pragma unroll
+          for (int i = 0; i < RW; ++i)
+            if (row0 + i < n_rows) dst[i * D] = o[i];
+        } else {
+          const int tok = row0 / a.g;
+          int hh = row0 - tok * a.g;
+          __nv_bfloat16* dst = a.out + (int64_t(s.row0 + tok) * a.Hq + s.h * a.g + hh) * D + kv;
+          const int64_t wrap = int64_t(a.Hq - a.g) * D;  // from a token's last head to the next token's first
+#pragma unroll
+          for (int i = 0; i < RW; ++i) {
+            if (row0 + i < n_rows) *dst = __float2bfloat16(o[i]);
+            dst += D;
+            if (++hh == a.g) hh = 0, dst += wrap;
           }
-          if (++hh == a.g) hh = 0, ++tok;
         }
       }
       ++n_seg;
@@ -487,15 +516,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncthreads();
-  if (warp == 9) {
-    if (lane == 0 && sh->mma_pending && sh->abort) {  // MMAs may be in flight: wait (bounded) before TMEM is freed
-      tc::mma_commit(tc::smem_u32(&sh->drain));
+  if (sh->abort) {  // MMAs may be in flight: wait (bounded) before TMEM is freed
+    if ((warp == 9 || warp == 10) && sh->pending[warp - 9]) {
+      if (tc::elect_one()) tc::mma_commit(tc::smem_u32(&sh->drain[warp - 9]));
+      __syncwarp();
       const volatile int never = 0;
-      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain), 0, tc::deadline_after_ns(200000000ull), &never);
+      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain[warp - 9]), 0, tc::deadline_after_ns(200000000ull), &never);
     }
-    __syncwarp();
-    tc::tmem_dealloc(tmem, C::kTmemCols);
+    __syncthreads();
   }
+  if (warp == 9) tc::tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <int D, int R>

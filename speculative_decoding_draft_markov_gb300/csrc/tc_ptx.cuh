@@ -131,6 +131,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// One lane of a converged warp, the same one each time; known to the compiler as a warp-wide choice.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(pred));
+  return pred != 0;
+}
+
 // ---------------------------------------------------------------------------------- tcgen05
 // Allocate / free `ncols` TMEM columns (power of two >= 32); one full warp executes these.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
