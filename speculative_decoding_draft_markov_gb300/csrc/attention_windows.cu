@@ -5,7 +5,7 @@
 //     S^T = K Q^T        [128 slots x R]   (tcgen05, M = 128, N = R; fp32 in TMEM)
 //     P^T = 2^(c S^T - m)                   (bf16, shared memory), partial sums of P per slot in registers
 //     O^T += V^T P^T     [D x R]            (tcgen05, fp32 in TMEM)
-// so that a thread holds one KV slot and half of the rows, and all eight softmax warps have work however few
+// so that a thread holds one KV slot and grp of the rows, and all eight softmax warps have work however few
 // the rows are.  (With the rows on TMEM lanes instead, 32 rows sat in one warp per stream: a
 // unit of 10 tiles of 128 x 128 at 32 rows took 24 us per CTA; so it takes 12.)
 //
@@ -19,20 +19,23 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 352;  // warps 0-3: softmax of rows 0 .. R/2 - 1, 4-7: of the others, 8: TMA, 9: S, 10: O
 constexpr int kMaxSlots = 6;
 constexpr float kUnset = -1e30f, kRescaleAt = 60.f;  // log2 units
 
+// Softmax groups of four warps, a group per run of rows; then one warp each for TMA, S^T and O^T.
+constexpr int groups(int R) { return R >= 32 ? 4 : 2; }
+
 template <int R>
 struct Shared {
+  static constexpr int kGroups = groups(R), kRows = R / kGroups;
   uint64_t q_full[2], q_empty[2], k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
-  uint64_t s_full[2], p_full[2], p_empty[2], o_full, group[2], drain[2];
+  uint64_t s_full[2], p_full[2], p_empty[2], o_full, group[kGroups], drain[2];
   uint32_t tmem_base;
   volatile int abort;
   int pending[2];            // the MMA warps have issued something
-  int need[2][2];            // [half][parity]: the last tile at which a warp asked for a new reference
+  int need[kGroups][2];      // [group][parity]: the last tile at which a warp asked for a new reference
   Range range;
-  float warp_max[2][4][R / 2], warp_sum[2][4][R / 2];  // [half][warp]: the rows' maxima of a tile, sums of a unit
+  float warp_max[kGroups][4][kRows], warp_sum[kGroups][4][kRows];  // the rows' maxima of a tile, sums of a unit
   alignas(16) float ref[R];  // the rows' references, read four at a time
   float scale[R];            // what a new reference scales the old sums by
 };
@@ -82,41 +85,43 @@ struct Cursor {
   __device__ __forceinline__ bool last() const { return j + 1 == s.n; }
 };
 
-// Sums over the 32 lanes of N values each (N = 8, 16 or a multiple of 32), in a fixed order, halving the values with the
-// lanes: afterwards lane l holds the sum of value l * N / 32 (N < 32: of value l / (32 / N)) in v[0], of value
-// 32 + l in v[1], ..
-template <int N>
-__device__ __forceinline__ void warp_sums(float* v, int lane) {
-  constexpr int kFold = N < 32 ? N : 32;
+// Folds N values of each lane over the 32 lanes (kMax: maxima, else sums, in a fixed order), halving the values with the
+// lanes; N = 8, 16 or 32.  Afterwards lane l holds the result of value l / (32 / N) in v[0].
+template <int N, bool kMax>
+__device__ __forceinline__ float fold_lanes(float* v, int lane) {
+  static_assert(N == 8 || N == 16 || N == 32, "values");
+  int cnt = N;
 #pragma unroll
-  for (int b = 0; b < N; b += kFold) {
-    float* x = v + b;
-    int cnt = kFold;
+  for (int o = 16; o > 0; o >>= 1) {
+    if (cnt > 1) {
+      cnt >>= 1;
+      const bool up = lane & o;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      if (cnt > 1) {
-        cnt >>= 1;
-        const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < kFold / 2; ++i)
-          if (i < cnt) {
-            const float send = up ? x[i] : x[i + cnt], keep = up ? x[i + cnt] : x[i];
-            x[i] = keep + __shfl_xor_sync(~0u, send, o);
-          }
-      } else {
-        x[0] += __shfl_xor_sync(~0u, x[0], o);
-      }
+      for (int i = 0; i < N / 2; ++i)
+        if (i < cnt) {
+          const float got = __shfl_xor_sync(~0u, up ? v[i] : v[i + cnt], o), keep = up ? v[i + cnt] : v[i];
+          v[i] = kMax ? fmaxf(keep, got) : keep + got;
+        }
+    } else {
+      const float got = __shfl_xor_sync(~0u, v[0], o);
+      v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
     }
-    v[b / kFold] = x[0];
   }
+  return v[0];
+}
+
+template <int R>
+constexpr int threads() {
+  return (groups(R) + 1) * 128;
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads<R>(), 1)
     window_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnArgs a) {
   using C = Cfg<D, R>;
-  constexpr int RW = R / 2;  // rows per thread
+  constexpr int kGroups = groups(R), RW = R / kGroups;  // rows per thread
+  constexpr int kTma = 4 * kGroups, kSWarp = kTma + 1, kOWarp = kTma + 2;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sK = smem;
   uint8_t* sV = sK + C::kKSlots * C::kSlotBytes;
@@ -133,8 +138,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(tc::smem_u32(&sh->q_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->q_empty[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->s_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->p_full[i]), 8);
+      tc::mbar_init(tc::smem_u32(&sh->p_full[i]), 4 * kGroups);
       tc::mbar_init(tc::smem_u32(&sh->p_empty[i]), 1);
+    }
+    for (int i = 0; i < kGroups; ++i) {
       tc::mbar_init(tc::smem_u32(&sh->group[i]), 4);
       sh->need[i][0] = sh->need[i][1] = 0;
     }
@@ -153,12 +160,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tensormap(&map_k);
     tc::prefetch_tensormap(&map_v);
   }
-  if (warp == 9) {
+  if (warp == kSWarp) {
     tc::tmem_alloc(tc::smem_u32(&sh->tmem_base), C::kTmemCols);
     tc::tmem_relinquish();
   }
   // rows of Q past the unit's last are never loaded: zeros, so that their scores are 0
-  for (int i = tid; i < C::kQBytes * C::kQBufs / 16; i += kThreads)
+  for (int i = tid; i < C::kQBytes * C::kQBufs / 16; i += threads<R>())
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   tc::fence_proxy_async_smem();
   __syncthreads();
@@ -167,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const uint32_t tmem = sh->tmem_base;
 
-  if (warp == 8) {
+  if (warp == kTma) {
     // --------------------------------------------------------------------- TMA producer
     // In order: K 0, K 1, then V t, K t + 2, over all tiles of the range; a unit's Q with its first K.
     const uint64_t keep = tc::policy_evict_last(), stream = tc::policy_evict_first();
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       info.x = ok ? flags : 0;
       a.info[blockIdx.x] = info;
     }
-  } else if (warp == 9) {
+  } else if (warp == kSWarp) {
     // ------------------------------------------------------------------ S^T = K Q^T of each tile
     constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, R);
     const uint64_t dk = tc::sdesc_kmajor_sw128(tc::smem_u32(sK)), dq = tc::sdesc_kmajor_sw128(tc::smem_u32(sQ));
@@ -281,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) note_timeout(a.status, a.diag, 2u, uint32_t(t));
     }
     if (lane == 0) sh->pending[0] = t > 0;
-  } else if (warp == 10) {
+  } else if (warp == kOWarp) {
     // -------------------------------------------------------------- O^T += V^T P^T of each tile
     constexpr uint32_t idesc = tc::idesc_bf16_f32(128, R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
     const uint64_t dv = tc::sdesc_mnmajor<128>(tc::smem_u32(sV), kTile * 128);
@@ -316,38 +323,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) note_timeout(a.status, a.diag, 4u, uint32_t(t));
     }
     if (lane == 0) sh->pending[1] = t > 0;
-  } else {
+  } else if (warp < kTma) {
     // ------------------------------------------------------------------------- softmax
-    const int half = warp >> 2, w4 = warp & 3;
+    const int grp = warp >> 2, w4 = warp & 3;
     const int kv = w4 * 32 + lane;  // this thread's slot of each tile = TMEM lane
-    const int row0 = half * RW;     // and its rows
-    const uint32_t lane_base = tmem + (uint32_t(w4 * 32) << 16);
-    const uint32_t t_o = lane_base + 2 * R + row0;
-    const float c2 = a.c2;
+    const int row0 = grp * RW;      // and its rows
+    const uint32_t lane_base = tmem + (uint32_t(w4 * 32) << 16) + row0;
+    const uint32_t t_o = lane_base + 2 * R;
+    const float c2 = a.c2, hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
+    const unsigned long long cc = pack_f32x2(c2, c2);
     float* ref = sh->ref + row0;
     float* scale = sh->scale + row0;
+    // where this thread's row of P goes: 16-byte pieces, from the first row of the group on
+    uint8_t* p_row = sP + (R == 128 ? (grp >> 1) * (kTile * 128) : 0);
+    const int piece0 = (R == 128 ? row0 % 64 : row0) / 8;
+    // the row that this lane holds after a fold (the lanes of a row hold the same)
+    const int fold_row = lane / (32 / RW);
     int t = 0, sync = 0, n_seg = 0;
     bool ok = true;
     Walk walk(sh->range, a.tokens);
     Segment s = {};
-    // the half's four warps: everything before on all of them is visible after
+    // the group's four warps: everything before on all of them is visible after
     auto meet = [&]() {
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->group[half]));
-      return wait(&sh->group[half], sync++ & 1);
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->group[grp]));
+      return wait(&sh->group[grp], sync++ & 1);
     };
     while (ok && walk.next(a, sh->range, s)) {
+      // tiles first_in .. first_in + n_in - 1 of the segment are seen whole by every row
+      const int per_tile = kTile >> a.block_shift;
+      int in0 = s.u.sb, in1 = (s.u.p0 + 1) >> a.block_shift;  // blocks of the unit: past the sinks; ending by p0
+      if (a.window) in0 = max(in0, ((s.u.p1 - a.window + 1 + (1 << a.block_shift) - 1) >> a.block_shift) - s.u.wb0 + s.u.sb);
+      in1 += s.u.sb - s.u.wb0;
+      const int j_in0 = (in0 + per_tile - 1) / per_tile - s.tile0, j_in1 = in1 / per_tile - s.tile0;
       float l[RW];  // this slot's share of the rows' sums
 #pragma unroll
       for (int i = 0; i < RW; ++i) l[i] = 0.f;
       for (int j = 0; j < s.n; ++j, ++t) {
-        const int first = (s.tile0 + j) * (kTile >> a.block_shift);
-        const int begin = block_pos(a, s.u, first);
-        const bool inside = first >= s.u.sb && begin + kTile - 1 <= s.u.p0 && (a.window == 0 || begin > s.u.p1 - a.window);
+        const bool inside = j >= j_in0 && j < j_in1;
         int from = 0, to = R;  // the rows that see this thread's slot
         if (!inside) {
           // the token at p0 + tok sees the slot from tok = pos - p0 on, for `window` tokens, a sink always
-          const int pos = block_pos(a, s.u, first + (kv >> a.block_shift)) + (kv & ((1 << a.block_shift) - 1));
+          const int v = (s.tile0 + j) * per_tile + (kv >> a.block_shift);
+          const int pos = block_pos(a, s.u, v) + (kv & ((1 << a.block_shift) - 1));
           const int d = pos - s.u.p0;
           from = d <= 0 ? 0 : d >= a.tokens ? R : d * a.g;
           if (a.window && pos >= a.n_sink) to = d + a.window <= 0 ? 0 : d + a.window >= a.tokens ? R : (d + a.window) * a.g;
@@ -356,17 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc::tc_fence_after();
         float x[RW];
-        tc::tmem_ld<RW>(lane_base + (t & 1) * R + row0, x);
+        tc::tmem_ld<RW>(lane_base + (t & 1) * R, x);
         tc::tmem_ld_wait();
         if (!inside) {
-          const float hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
 #pragma unroll
           for (int i = 0; i < RW; ++i)
             if (row0 + i < from || row0 + i >= to) x[i] = hidden;
         }
-        const unsigned long long cc = pack_f32x2(c2, c2);
-        float y[RW];
         bool fresh = j == 0;  // a new reference is needed
+        float y[RW];
         if (!fresh) {
           float top = -INFINITY;
 #pragma unroll
@@ -376,50 +392,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             unpack_f32x2(fma_f32x2(pack_f32x2(x[i + 2], x[i + 3]), cc, pack_f32x2(-m.z, -m.w)), y[i + 2], y[i + 3]);
             top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
           }
-          if (__any_sync(~0u, top > kRescaleAt) && lane == 0) sh->need[half][sync & 1] = t + 1;
           const int at = sync & 1;
+          if (__any_sync(~0u, top > kRescaleAt) && lane == 0) sh->need[grp][at] = t + 1;
           ok = meet();
           if (!ok) break;
-          fresh = sh->need[half][at] == t + 1;
+          fresh = sh->need[grp][at] == t + 1;
+          if (fresh) {  // the scores once more (S is still there: P has not been written)
+            tc::tmem_ld<RW>(lane_base + (t & 1) * R, x);
+            tc::tmem_ld_wait();
+            if (!inside) {
+#pragma unroll
+              for (int i = 0; i < RW; ++i)
+                if (row0 + i < from || row0 + i >= to) x[i] = hidden;
+            }
+          }
         }
         if (fresh) {
-          // each row's maximum over the tile's 128 slots, by warp then over the half's warps
-          float mine[(RW + 31) / 32];
+          // each row's maximum over the tile's 128 slots, by warp then over the group's warps
 #pragma unroll
-          for (int i = 0; i < RW; ++i) {
-            const float m = tc::redux_max(x[i] * c2);
-            if (lane == (i & 31)) mine[i >> 5] = m;
-          }
-          float old[(RW + 31) / 32];
-#pragma unroll
-          for (int b = 0; b < RW; b += 32)
-            if (b + lane < RW) {
-              sh->warp_max[half][w4][b + lane] = mine[b >> 5];
-              old[b >> 5] = j == 0 ? kUnset : ref[b + lane];
-            }
+          for (int i = 0; i < RW; ++i) y[i] = x[i] * c2;
+          const float mine = fold_lanes<RW, true>(y, lane);
+          const float old = j == 0 ? kUnset : ref[fold_row];
+          sh->warp_max[grp][w4][fold_row] = mine;
           ok = meet();
           if (!ok) break;
-#pragma unroll
-          for (int b = 0; b < RW; b += 32)
-            if (b + lane < RW) {  // the four warps write the same values
-              const float (*part)[RW] = sh->warp_max[half];
-              const float m = fmaxf(fmaxf(old[b >> 5], fmaxf(part[0][b + lane], part[1][b + lane])),
-                                    fmaxf(part[2][b + lane], part[3][b + lane]));
-              ref[b + lane] = m;
-              scale[b + lane] = tc::ex2_approx(old[b >> 5] - m);
-            }
+          const float (*part)[RW] = sh->warp_max[grp];
+          const float m = fmaxf(fmaxf(old, fmaxf(part[0][fold_row], part[1][fold_row])),
+                                fmaxf(part[2][fold_row], part[3][fold_row]));
+          ref[fold_row] = m;  // the four warps write the same values
+          scale[fold_row] = tc::ex2_approx(old - m);
           __syncwarp();
           if (j > 0) {
             // the sums so far and this thread's lane of O^T, after the last tile's product
             ok = wait(&sh->p_empty[(t - 1) % C::kPBufs], ((t - 1) / C::kPBufs) & 1);
             if (!ok) break;
             tc::tc_fence_after();
-            float o[RW];
-            tc::tmem_ld<RW>(t_o, o);
+            tc::tmem_ld<RW>(t_o, y);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < RW; ++i) l[i] *= scale[i], o[i] *= scale[i];
-            tc::tmem_st<RW>(t_o, o);
+            for (int i = 0; i < RW; ++i) l[i] *= scale[i], y[i] *= scale[i];
+            tc::tmem_st<RW>(t_o, y);
             tc::tmem_st_wait();
           }
 #pragma unroll
@@ -435,8 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = wait(&sh->p_empty[t % C::kPBufs], ((t / C::kPBufs) & 1) ^ 1);
         if (!ok) break;
-        uint8_t* p = sP + (t % C::kPBufs) * C::kPBytes + (R == 128 ? half * (kTile * 128) : 0);
-        const int piece0 = R == 128 ? 0 : row0 / 8;
+        uint8_t* p = p_row + (t % C::kPBufs) * C::kPBytes;
 #pragma unroll
         for (int i = 0; i < RW / 8; ++i)
           *reinterpret_cast<uint4*>(p + tc::swizzled<C::kPPitch>(kv, piece0 + i)) =
@@ -448,36 +459,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------------------- the unit's rows
-      // rows' sums over the 128 slots: lanes, then the half's warps in order
-      warp_sums<RW>(l, lane);
-      if (RW >= 32 || (lane & (32 / RW - 1)) == 0) {
-#pragma unroll
-        for (int b = 0; b < (RW + 31) / 32; ++b)
-          sh->warp_sum[half][w4][b * 32 + (RW >= 32 ? lane : lane / (32 / RW))] = l[b];
-      }
+      // rows' sums over the 128 slots: lanes, then the group's warps in order
+      const float mine = fold_lanes<RW, false>(l, lane);
+      sh->warp_sum[grp][w4][fold_row] = mine;
       ok = meet();
       if (!ok) break;
       const bool partial = s.n < s.u.ntiles;
-      const int64_t pbase = (int64_t(2) * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * R;
-      const int n_rows = s.ntok * a.g;
-      float inv[(RW + 31) / 32];
-#pragma unroll
-      for (int b = 0; b < RW; b += 32) {
-        const int i = b + lane;
-        inv[b >> 5] = 0.f;
-        if (i < RW) {
-          const float (*part)[RW] = sh->warp_sum[half];
-          const float sum = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
-          inv[b >> 5] = sum > 0.f ? 1.f / sum : 0.f;
-          const int row = row0 + i;
-          if (w4 == 0 && row < n_rows) {
-            const float lse2 = sum > 0.f ? ref[i] + log2f(sum) : -INFINITY;
-            if (partial)
-              a.plse[pbase + row] = lse2;
-            else if (a.lse)
-              a.lse[int64_t(s.row0 + row / a.g) * a.Hq + s.h * a.g + row % a.g] = lse2 * kLn2;
-          }
-        }
+      const int64_t pbase = (int64_t(2) * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * R + row0;
+      const int n_rows = s.ntok * a.g - row0;  // of this group's
+      const float (*part)[RW] = sh->warp_sum[grp];
+      const float sum = (part[0][fold_row] + part[1][fold_row]) + (part[2][fold_row] + part[3][fold_row]);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      if (w4 == 0 && fold_row * (32 / RW) == lane && fold_row < n_rows) {
+        const float lse2 = sum > 0.f ? ref[fold_row] + log2f(sum) : -INFINITY;
+        const int row = row0 + fold_row;
+        if (partial)
+          a.plse[pbase + fold_row] = lse2;
+        else if (a.lse)
+          a.lse[int64_t(s.row0 + row / a.g) * a.Hq + s.h * a.g + row % a.g] = lse2 * kLn2;
       }
       ok = wait(&sh->o_full, n_seg & 1);
       if (!ok) break;
@@ -488,12 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
       if (kv < D) {           // TMEM lane = lane of the head
 #pragma unroll
-        for (int i = 0; i < RW; ++i) o[i] *= __shfl_sync(~0u, inv[i >> 5], i & 31);
+        for (int i = 0; i < RW; ++i) o[i] *= __shfl_sync(~0u, inv, i * (32 / RW));
         if (partial) {
-          float* dst = a.partial + (pbase + row0) * D + kv;
+          float* dst = a.partial + pbase * D + kv;
 #pragma unroll
           for (int i = 0; i < RW; ++i)
-            if (row0 + i < n_rows) dst[i * D] = o[i];
+            if (i < n_rows) dst[i * D] = o[i];
         } else {
           const int tok = row0 / a.g;
           int hh = row0 - tok * a.g;
@@ -501,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t wrap = int64_t(a.Hq - a.g) * D;  // from a token's last head to the next token's first
 #pragma unroll
           for (int i = 0; i < RW; ++i) {
-            if (row0 + i < n_rows) *dst = __float2bfloat16(o[i]);
+            if (i < n_rows) *dst = __float2bfloat16(o[i]);
             dst += D;
             if (++hh == a.g) hh = 0, dst += wrap;
           }
@@ -517,15 +516,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   __syncthreads();
   if (sh->abort) {  // MMAs may be in flight: wait (bounded) before TMEM is freed
-    if ((warp == 9 || warp == 10) && sh->pending[warp - 9]) {
-      if (tc::elect_one()) tc::mma_commit(tc::smem_u32(&sh->drain[warp - 9]));
+    if ((warp == kSWarp || warp == kOWarp) && sh->pending[warp - kSWarp]) {
+      if (tc::elect_one()) tc::mma_commit(tc::smem_u32(&sh->drain[warp - kSWarp]));
       __syncwarp();
       const volatile int never = 0;
-      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain[warp - 9]), 0, tc::deadline_after_ns(200000000ull), &never);
+      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain[warp - kSWarp]), 0, tc::deadline_after_ns(200000000ull), &never);
     }
     __syncthreads();
   }
-  if (warp == 9) tc::tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == kSWarp) tc::tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <int D, int R>
@@ -535,7 +534,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   static std::mutex mu;
   constexpr int kSmem = Cfg<D, R>::kSmem;
   const cudaError_t e = tch::set_smem_once(window_kernel<D, R>, kSmem, done, &mu);
-  return e != cudaSuccess ? e : launch_pdl(window_kernel<D, R>, dim3(n_cta), dim3(kThreads), kSmem, s, q, k, v, a);
+  return e != cudaSuccess ? e : launch_pdl(window_kernel<D, R>, dim3(n_cta), dim3(threads<R>()), kSmem, s, q, k, v, a);
 }
 
 }  // namespace

@@ -303,13 +303,6 @@ __device__ __forceinline__ uint32_t swizzled(int row, int piece) {
 // Instruction descriptor bits: A, B is MN-major.
 constexpr uint32_t kIdescAMajorMN = 1u << 15, kIdescBMajorMN = 1u << 16;
 
-// Maximum over the warp's lanes, in all lanes.
-__device__ __forceinline__ float redux_max(float v) {
-  float m;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-  return m;
-}
-
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, both K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4)                                  // D format: f32

@@ -133,7 +133,7 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   // the kernel hides a score by an infinity before the scale: a scale of 0 becomes one that gives equal weights
   // all the same (2^(1e-30 s) is 1)
   if (a.c2 == 0.f) a.c2 = 1e-30f;
-  a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, 7);
+  a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, prompts ? 7 : 5);
   a.bs = bs, a.rows = rows, a.Hq = Hq, a.Hkv = Hkv, a.g = g, a.tokens = prompts ? fit : std::min(unit_rows / g, std::max(max_rows, 1));
   a.window = window >= a.cache_limit ? 0 : window, a.n_sink = n_sink;
   CUtensorMap mq, mk, mv;
