@@ -5,13 +5,18 @@
 //     S^T = K Q^T        [128 slots x R]   (tcgen05, M = 128, N = R; fp32 in TMEM)
 //     P^T = 2^(c S^T - m)                   (bf16, shared memory), partial sums of P per slot in registers
 //     O^T += V^T P^T     [D x R]            (tcgen05, fp32 in TMEM)
-// so that a thread holds one KV slot and grp of the rows, and all eight softmax warps have work however few
-// the rows are.  (With the rows on TMEM lanes instead, 32 rows sat in one warp per stream: a
-// unit of 10 tiles of 128 x 128 at 32 rows took 24 us per CTA; so it takes 12.)
+// so that a thread holds one KV slot and some of the rows, and all softmax warps have work however few the rows
+// are.  (With the rows on TMEM lanes instead, 32 rows sat in one warp per stream: a unit of 10 tiles at 32
+// rows took 24 us per CTA; it takes 12.)  A tile's way through the softmax is a chain of latencies, so two sets of
+// softmax warps take alternate tiles, each with its own S^T, P^T, O^T and references; a unit's two halves
+// are merged when its rows are written.  At R = 128 one set takes all tiles (its registers allow no more,
+// and it has twice the work per tile).
 //
 // m is a reference that only keeps the exponentials in range, the same for all slots of a row: any value
 // within 2^60 of the maximum gives the same result, since the sum is divided out and neither fp32 nor bf16 loses
-// bits there.  So it is set from a unit's first tile and checked, not recomputed, on the others.
+// bits there.  So it is set from a set's first tile of a unit and checked, not recomputed, on the others.
+#include <type_traits>
+
 #include "attention_common.cuh"
 
 namespace dspark {
@@ -22,31 +27,44 @@ using namespace attn;
 constexpr int kMaxSlots = 6;
 constexpr float kUnset = -1e30f, kRescaleAt = 60.f;  // log2 units
 
-// Softmax groups of four warps, a group per run of rows; then one warp each for TMA, S^T and O^T.
-constexpr int groups(int R) { return R >= 32 ? 4 : 2; }
+// Sixteen softmax warps in groups of four; a group takes R / kRowGroups rows of its set's tiles.  Then one warp
+// each for TMA, S^T and O^T.
+constexpr int kGroups = 4, kThreads = (kGroups + 1) * 128;
+constexpr int kTma = 4 * kGroups, kSWarp = kTma + 1, kOWarp = kTma + 2;
+// Registers: launched with 640 x 96; the softmax warps take what the others give back (512 x 104 + 128 x 56 <= 640 x 96).
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 56;
+
+template <int R>
+struct Split {
+  static constexpr int kSets = R == 128 ? 1 : 2, kRowGroups = kGroups / kSets, kRows = R / kRowGroups;
+};
 
 template <int R>
 struct Shared {
-  static constexpr int kGroups = groups(R), kRows = R / kGroups;
+  static constexpr int kSets = Split<R>::kSets, kRowGroups = Split<R>::kRowGroups, kRows = Split<R>::kRows;
   uint64_t q_full[2], q_empty[2], k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
-  uint64_t s_full[2], p_full[2], p_empty[2], o_full, group[kGroups], drain[2];
+  uint64_t s_full[2], p_full[2], p_empty[2];
+  uint64_t o_full[kSets], o_read[kSets];           // a set's O^T is complete; has been read by all that do
+  uint64_t group[kGroups];                          // the four warps of a group
+  uint64_t pair_put[kRowGroups], pair_got[kRowGroups];  // the two sets' groups of the same rows
+  uint64_t drain[2];
   uint32_t tmem_base;
   volatile int abort;
-  int pending[2];            // the MMA warps have issued something
-  int need[kGroups][2];      // [group][parity]: the last tile at which a warp asked for a new reference
+  int pending[2];                                   // the MMA warps have issued something
+  int need[kGroups][2];                             // [parity]: the last tile at which a warp asked for a new reference
   Range range;
-  float warp_max[kGroups][4][kRows], warp_sum[kGroups][4][kRows];  // the rows' maxima of a tile, sums of a unit
-  alignas(16) float ref[R];  // the rows' references, read four at a time
-  float scale[R];            // what a new reference scales the old sums by
+  float warp_part[kGroups][4][kRows];               // by warp: the rows' maxima of a tile, sums of a unit
+  alignas(16) float ref[kSets][R];                  // the rows' references, read four at a time
+  float scale[kSets][R];                            // what a new reference scales the old sums by
 };
 
 template <int D, int R>
 struct Cfg {
   static constexpr int kHalves = D / 64;                   // 128-byte swizzled column blocks of a tile
   static constexpr int kSlotBytes = kTile * D * 2;
-  static constexpr int kQBytes = R * D * 2, kQBufs = R == 128 ? 1 : 2;
+  static constexpr int kQBytes = R * D * 2, kQBufs = R == 128 || R * D == 64 * 128 ? 1 : 2;
   static constexpr int kPPitch = R < 64 ? R * 2 : 128;      // bytes of a slot's row of P, R > 64: in two chunks
-  static constexpr int kPBytes = kTile * R * 2, kPBufs = R >= 64 ? 1 : 2;
+  static constexpr int kPBytes = kTile * R * 2, kPBufs = Split<R>::kSets;
   // O^T has M = 128 also where D = 64: its lanes 64 .. 127 come from the 16 KB behind the V tile, whatever
   // they hold, and are not read
   static constexpr int kBehind = kQBytes * kQBufs + kPBytes * kPBufs;
@@ -56,7 +74,7 @@ struct Cfg {
   static constexpr int kVSlots = (kRoom + 1) / 2 < kMaxSlots ? (kRoom + 1) / 2 : kMaxSlots;
   static constexpr int kKSlots = kRoom / 2 < kMaxSlots ? kRoom / 2 : kMaxSlots;
   static constexpr int kSmem = (kKSlots + kVSlots) * kSlotBytes + kBehind + kPad + int(sizeof(Shared<R>));
-  static constexpr int kTmemCols = 4 * R;  // S^T twice, O^T; a power of two
+  static constexpr int kTmemCols = 4 * R;  // S^T twice, the sets' O^T; a power of two
   static_assert(kKSlots >= 2 && kVSlots >= 2 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "shared memory layout");
 };
 
@@ -110,18 +128,12 @@ __device__ __forceinline__ float fold_lanes(float* v, int lane) {
   return v[0];
 }
 
-template <int R>
-constexpr int threads() {
-  return (groups(R) + 1) * 128;
-}
-
 template <int D, int R>
-__global__ void __launch_bounds__(threads<R>(), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     window_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnArgs a) {
   using C = Cfg<D, R>;
-  constexpr int kGroups = groups(R), RW = R / kGroups;  // rows per thread
-  constexpr int kTma = 4 * kGroups, kSWarp = kTma + 1, kOWarp = kTma + 2;
+  constexpr int kSets = Split<R>::kSets, kRowGroups = Split<R>::kRowGroups, RW = Split<R>::kRows;  // RW: rows per thread
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sK = smem;
   uint8_t* sV = sK + C::kKSlots * C::kSlotBytes;
@@ -138,7 +150,7 @@ __global__ void __launch_bounds__(threads<R>(), 1)
       tc::mbar_init(tc::smem_u32(&sh->q_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->q_empty[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->s_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->p_full[i]), 4 * kGroups);
+      tc::mbar_init(tc::smem_u32(&sh->p_full[i]), 4 * kRowGroups);
       tc::mbar_init(tc::smem_u32(&sh->p_empty[i]), 1);
     }
     for (int i = 0; i < kGroups; ++i) {
@@ -151,7 +163,14 @@ __global__ void __launch_bounds__(threads<R>(), 1)
       tc::mbar_init(tc::smem_u32(&sh->v_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->v_empty[i]), 1);
     }
-    tc::mbar_init(tc::smem_u32(&sh->o_full), 1);
+    for (int i = 0; i < kSets; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh->o_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->o_read[i]), 4 * kGroups);
+    }
+    for (int i = 0; i < kRowGroups; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh->pair_put[i]), 8);
+      tc::mbar_init(tc::smem_u32(&sh->pair_got[i]), 8);
+    }
     tc::mbar_init(tc::smem_u32(&sh->drain[0]), 1);
     tc::mbar_init(tc::smem_u32(&sh->drain[1]), 1);
     tc::fence_mbar_init();
@@ -165,15 +184,16 @@ __global__ void __launch_bounds__(threads<R>(), 1)
     tc::tmem_relinquish();
   }
   // rows of Q past the unit's last are never loaded: zeros, so that their scores are 0
-  for (int i = tid; i < C::kQBytes * C::kQBufs / 16; i += threads<R>())
+  for (int i = tid; i < C::kQBytes * C::kQBufs / 16; i += kThreads)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   tc::fence_proxy_async_smem();
   __syncthreads();
   pdl_enter();
-  plan_range(a, sh->range, reinterpret_cast<uint8_t*>(sh->warp_max), a.tokens);
+  plan_range(a, sh->range, reinterpret_cast<uint8_t*>(sh->warp_part), a.tokens);
   __syncthreads();
   const uint32_t tmem = sh->tmem_base;
 
+  if (warp >= kTma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kTma) {
     // --------------------------------------------------------------------- TMA producer
     // In order: K 0, K 1, then V t, K t + 2, over all tiles of the range; a unit's Q with its first K.
@@ -294,26 +314,29 @@ __global__ void __launch_bounds__(threads<R>(), 1)
     const uint64_t dv = tc::sdesc_mnmajor<128>(tc::smem_u32(sV), kTile * 128);
     const uint64_t dp = tc::sdesc_mnmajor<C::kPPitch>(tc::smem_u32(sP), kTile * 128);
     Ring<C::kVSlots> ring;
-    int t = 0;
+    int t = 0, o_uses[kSets] = {};
     bool ok = true;
     Cursor cur(sh->range, a.tokens);
     for (; cur.next(a, sh->range); ++t) {
+      const int set = kSets == 2 ? t & 1 : 0;
+      const bool first = cur.j < kSets, last = cur.j + kSets >= cur.s.n;  // of the set's tiles of the unit
       ok = wait(&sh->v_full[ring.slot], ring.phase);
       if (!ok) break;
       clear_unseen<C::kHalves>(a, cur.s, cur.j, sV + ring.slot * C::kSlotBytes, lane);
       ok = wait(&sh->p_full[t & 1], (t >> 1) & 1);
+      // the set's O^T of the unit before has been read
+      if (ok && first) ok = wait(&sh->o_read[set], ((kSets == 2 && set ? o_uses[kSets - 1]++ : o_uses[0]++) & 1) ^ 1);
       if (!ok) break;
       tc::tc_fence_after();
       const uint64_t dv_t = dv + uint32_t(ring.slot * (C::kSlotBytes >> 4));
       const uint64_t dp_t = dp + uint32_t((t % C::kPBufs) * (C::kPBytes >> 4));
-      const bool add = !cur.first(), last = cur.last();
       if (tc::elect_one()) {
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i)
-          tc::mma_bf16(tmem + 2 * R, dv_t + ((i * 2048) >> 4), dp_t + ((i * 16 * C::kPPitch) >> 4), idesc, add || i != 0);
+          tc::mma_bf16(tmem + 2 * R + set * R, dv_t + ((i * 2048) >> 4), dp_t + ((i * 16 * C::kPPitch) >> 4), idesc, !first || i != 0);
         tc::mma_commit(tc::smem_u32(&sh->p_empty[t % C::kPBufs]));
         tc::mma_commit(tc::smem_u32(&sh->v_empty[ring.slot]));
-        if (last) tc::mma_commit(tc::smem_u32(&sh->o_full));
+        if (last) tc::mma_commit(tc::smem_u32(&sh->o_full[set]));
       }
       __syncwarp();
       ring.step();
@@ -325,21 +348,22 @@ __global__ void __launch_bounds__(threads<R>(), 1)
     if (lane == 0) sh->pending[1] = t > 0;
   } else if (warp < kTma) {
     // ------------------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int grp = warp >> 2, w4 = warp & 3;
     const int kv = w4 * 32 + lane;  // this thread's slot of each tile = TMEM lane
-    const int row0 = grp * RW;      // and its rows
+    const int set = kSets == 2 ? grp & 1 : 0, rg = grp / kSets, row0 = rg * RW;  // and its rows
     const uint32_t lane_base = tmem + (uint32_t(w4 * 32) << 16) + row0;
-    const uint32_t t_o = lane_base + 2 * R;
+    const uint32_t t_o = lane_base + 2 * R;  // the first set's O^T
     const float c2 = a.c2, hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
     const unsigned long long cc = pack_f32x2(c2, c2);
-    float* ref = sh->ref + row0;
-    float* scale = sh->scale + row0;
+    float* ref = sh->ref[set] + row0;
+    float* scale = sh->scale[set] + row0;
     // where this thread's row of P goes: 16-byte pieces, from the first row of the group on
-    uint8_t* p_row = sP + (R == 128 ? (grp >> 1) * (kTile * 128) : 0);
+    uint8_t* p_row = sP + (R == 128 ? (row0 / 64) * (kTile * 128) : 0);
     const int piece0 = (R == 128 ? row0 % 64 : row0) / 8;
     // the row that this lane holds after a fold (the lanes of a row hold the same)
     const int fold_row = lane / (32 / RW);
-    int t = 0, sync = 0, n_seg = 0;
+    int t0 = 0, sync = 0, n_pair = 0, n_unit[2] = {0, 0};  // tiles before; meetings; units merged; units of each set
     bool ok = true;
     Walk walk(sh->range, a.tokens);
     Segment s = {};
@@ -350,7 +374,14 @@ __global__ void __launch_bounds__(threads<R>(), 1)
       return wait(&sh->group[grp], sync++ & 1);
     };
     while (ok && walk.next(a, sh->range, s)) {
-      // tiles first_in .. first_in + n_in - 1 of the segment are seen whole by every row
+      const bool both = kSets == 2 && s.n > 1;
+      const int begin = kSets == 2 ? (set ^ t0) & 1 : 0;  // this set's first tile of the unit
+      const int units0 = n_unit[0], units1 = n_unit[1];
+      if (both || kSets == 1 || (t0 & 1) == 0) ++n_unit[0];
+      if (both || (kSets == 2 && (t0 & 1) == 1)) ++n_unit[1];
+      t0 += s.n;
+      if (begin >= s.n) continue;  // a single tile, the other set's
+      // tiles j_in0 .. j_in1 - 1 of the segment are seen whole by every row
       const int per_tile = kTile >> a.block_shift;
       int in0 = s.u.sb, in1 = (s.u.p0 + 1) >> a.block_shift;  // blocks of the unit: past the sinks; ending by p0
       if (a.window) in0 = max(in0, ((s.u.p1 - a.window + 1 + (1 << a.block_shift) - 1) >> a.block_shift) - s.u.wb0 + s.u.sb);
@@ -359,7 +390,9 @@ __global__ void __launch_bounds__(threads<R>(), 1)
       float l[RW];  // this slot's share of the rows' sums
 #pragma unroll
       for (int i = 0; i < RW; ++i) l[i] = 0.f;
-      for (int j = 0; j < s.n; ++j, ++t) {
+      bool fresh = true;  // a new reference is needed
+      for (int j = begin; j < s.n; j += kSets) {
+        const int t = t0 - s.n + j;
         const bool inside = j >= j_in0 && j < j_in1;
         int from = 0, to = R;  // the rows that see this thread's slot
         if (!inside) {
@@ -381,9 +414,10 @@ __global__ void __launch_bounds__(threads<R>(), 1)
           for (int i = 0; i < RW; ++i)
             if (row0 + i < from || row0 + i >= to) x[i] = hidden;
         }
-        bool fresh = j == 0;  // a new reference is needed
+        const bool head = j == begin;
+        fresh = head;
         float y[RW];
-        if (!fresh) {
+        if (!head) {
           float top = -INFINITY;
 #pragma unroll
           for (int i = 0; i < RW; i += 4) {
@@ -412,26 +446,30 @@ __global__ void __launch_bounds__(threads<R>(), 1)
 #pragma unroll
           for (int i = 0; i < RW; ++i) y[i] = x[i] * c2;
           const float mine = fold_lanes<RW, true>(y, lane);
-          const float old = j == 0 ? kUnset : ref[fold_row];
-          sh->warp_max[grp][w4][fold_row] = mine;
+          // the other set's group has read this one's last sums
+          if (head && kSets == 2 && n_pair > 0) ok = wait(&sh->pair_got[rg], (n_pair - 1) & 1);
+          if (!ok) break;
+          const float old = head ? kUnset : ref[fold_row];
+          sh->warp_part[grp][w4][fold_row] = mine;
           ok = meet();
           if (!ok) break;
-          const float (*part)[RW] = sh->warp_max[grp];
+          const float (*part)[RW] = sh->warp_part[grp];
           const float m = fmaxf(fmaxf(old, fmaxf(part[0][fold_row], part[1][fold_row])),
                                 fmaxf(part[2][fold_row], part[3][fold_row]));
           ref[fold_row] = m;  // the four warps write the same values
           scale[fold_row] = tc::ex2_approx(old - m);
           __syncwarp();
-          if (j > 0) {
-            // the sums so far and this thread's lane of O^T, after the last tile's product
-            ok = wait(&sh->p_empty[(t - 1) % C::kPBufs], ((t - 1) / C::kPBufs) & 1);
+          if (!head) {
+            // the sums so far and this thread's lane of O^T, after the set's last product
+            const int last = t - kSets;
+            ok = wait(&sh->p_empty[last % C::kPBufs], (last / C::kPBufs) & 1);
             if (!ok) break;
             tc::tc_fence_after();
-            tc::tmem_ld<RW>(t_o, y);
+            tc::tmem_ld<RW>(t_o + set * R, y);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < RW; ++i) l[i] *= scale[i], y[i] *= scale[i];
-            tc::tmem_st<RW>(t_o, y);
+            tc::tmem_st<RW>(t_o + set * R, y);
             tc::tmem_st_wait();
           }
 #pragma unroll
@@ -460,57 +498,108 @@ __global__ void __launch_bounds__(threads<R>(), 1)
       if (!ok) break;
       // ---------------------------------------------------------------- the unit's rows
       // rows' sums over the 128 slots: lanes, then the group's warps in order
-      const float mine = fold_lanes<RW, false>(l, lane);
-      sh->warp_sum[grp][w4][fold_row] = mine;
-      ok = meet();
+      if (fresh) ok = meet();  // the last tile's maxima, in the same place, have been read
       if (!ok) break;
+      const float mine = fold_lanes<RW, false>(l, lane);
+      sh->warp_part[grp][w4][fold_row] = mine;
+      auto row_sum = [&](int of) {
+        const float (*part)[RW] = sh->warp_part[of];
+        return (part[0][fold_row] + part[1][fold_row]) + (part[2][fold_row] + part[3][fold_row]);
+      };
+      float lse2, f0, f1 = 0.f;  // the row's log2-sum-exp; the factors of its O^T, of the first and second set's
+      if (both) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->pair_put[rg]));
+        ok = wait(&sh->pair_put[rg], n_pair & 1);
+        if (!ok) break;
+        const int g0 = rg * 2;
+        const float r0 = sh->ref[0][row0 + fold_row], r1 = sh->ref[kSets - 1][row0 + fold_row], m = fmaxf(r0, r1);
+        f0 = tc::ex2_approx(r0 - m), f1 = tc::ex2_approx(r1 - m);
+        const float sum = row_sum(g0) * f0 + row_sum(g0 + 1) * f1, inv = sum > 0.f ? 1.f / sum : 0.f;
+        f0 *= inv, f1 *= inv;
+        lse2 = sum > 0.f ? m + log2f(sum) : -INFINITY;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->pair_got[rg]));
+        ++n_pair;
+      } else {
+        ok = meet();
+        if (!ok) break;
+        const float sum = row_sum(grp);
+        f0 = sum > 0.f ? 1.f / sum : 0.f;
+        lse2 = sum > 0.f ? ref[fold_row] + log2f(sum) : -INFINITY;
+        ok = meet();  // read by all four before the next unit writes there
+        if (!ok) break;
+      }
       const bool partial = s.n < s.u.ntiles;
       const int64_t pbase = (int64_t(2) * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * R + row0;
       const int n_rows = s.ntok * a.g - row0;  // of this group's
-      const float (*part)[RW] = sh->warp_sum[grp];
-      const float sum = (part[0][fold_row] + part[1][fold_row]) + (part[2][fold_row] + part[3][fold_row]);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      if (w4 == 0 && fold_row * (32 / RW) == lane && fold_row < n_rows) {
-        const float lse2 = sum > 0.f ? ref[fold_row] + log2f(sum) : -INFINITY;
+      if (w4 == 0 && (set == 0 || !both) && fold_row * (32 / RW) == lane && fold_row < n_rows) {
         const int row = row0 + fold_row;
         if (partial)
           a.plse[pbase + fold_row] = lse2;
         else if (a.lse)
           a.lse[int64_t(s.row0 + row / a.g) * a.Hq + s.h * a.g + row % a.g] = lse2 * kLn2;
       }
-      ok = wait(&sh->o_full, n_seg & 1);
+      ok = (both || set == 0 ? wait(&sh->o_full[0], units0 & 1) : true) &&
+           (both || set == 1 ? wait(&sh->o_full[kSets - 1], units1 & 1) : true);
       if (!ok) break;
       tc::tc_fence_after();
-      float o[RW];
-      tc::tmem_ld<RW>(t_o, o);
-      tc::tmem_ld_wait();
-      tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
-      if (kv < D) {           // TMEM lane = lane of the head
-#pragma unroll
-        for (int i = 0; i < RW; ++i) o[i] *= __shfl_sync(~0u, inv, i * (32 / RW));
+      // N rows from row r of the group's on, already divided, this thread's lane of the head
+      auto put = [&](auto n_of, int r, const float* o) {
+        constexpr int N = decltype(n_of)::value;
         if (partial) {
-          float* dst = a.partial + pbase * D + kv;
+          float* dst = a.partial + (pbase + r) * D + kv;
 #pragma unroll
-          for (int i = 0; i < RW; ++i)
-            if (i < n_rows) dst[i * D] = o[i];
+          for (int i = 0; i < N; ++i)
+            if (r + i < n_rows) dst[i * D] = o[i];
         } else {
-          const int tok = row0 / a.g;
-          int hh = row0 - tok * a.g;
+          const int tok = (row0 + r) / a.g;
+          int hh = row0 + r - tok * a.g;
           __nv_bfloat16* dst = a.out + (int64_t(s.row0 + tok) * a.Hq + s.h * a.g + hh) * D + kv;
           const int64_t wrap = int64_t(a.Hq - a.g) * D;  // from a token's last head to the next token's first
 #pragma unroll
-          for (int i = 0; i < RW; ++i) {
-            if (i < n_rows) *dst = __float2bfloat16(o[i]);
+          for (int i = 0; i < N; ++i) {
+            if (r + i < n_rows) *dst = __float2bfloat16(o[i]);
             dst += D;
             if (++hh == a.g) hh = 0, dst += wrap;
           }
         }
+      };
+      // O^T has been read: the sets' next units may overwrite it
+      auto read = [&](int of, uint32_t count) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_n(tc::smem_u32(&sh->o_read[of]), count);
+      };
+      // TMEM lane = lane of the head; lanes from D on hold nothing
+      if (both) {  // the sets' groups of the same rows write half of them each
+        constexpr int N = RW / 2;
+        const int r = set * N;
+        float o[N], o1[N];
+        tc::tmem_ld<N>(t_o + r, o);
+        tc::tmem_ld<N>(t_o + R + r, o1);
+        tc::tmem_ld_wait();
+        read(0, 1);
+        read(kSets - 1, 1);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float a0 = __shfl_sync(~0u, f0, (r + i) * (32 / RW)), a1 = __shfl_sync(~0u, f1, (r + i) * (32 / RW));
+          o[i] = o[i] * a0 + o1[i] * a1;
+        }
+        if (kv < D) put(std::integral_constant<int, N>(), r, o);
+      } else {
+        float o[RW];
+        tc::tmem_ld<RW>(t_o + set * R, o);
+        tc::tmem_ld_wait();
+        read(set, kSets);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) o[i] *= __shfl_sync(~0u, f0, i * (32 / RW));
+        if (kv < D) put(std::integral_constant<int, RW>(), 0, o);
       }
-      ++n_seg;
     }
     if (!ok) {
       sh->abort = 1;
-      if (lane == 0) note_timeout(a.status, a.diag, 3u, uint32_t(t) | uint32_t(warp) << 24);
+      if (lane == 0) note_timeout(a.status, a.diag, 3u, uint32_t(t0) | uint32_t(warp) << 24);
     }
   }
 
@@ -534,7 +623,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   static std::mutex mu;
   constexpr int kSmem = Cfg<D, R>::kSmem;
   const cudaError_t e = tch::set_smem_once(window_kernel<D, R>, kSmem, done, &mu);
-  return e != cudaSuccess ? e : launch_pdl(window_kernel<D, R>, dim3(n_cta), dim3(threads<R>()), kSmem, s, q, k, v, a);
+  return e != cudaSuccess ? e : launch_pdl(window_kernel<D, R>, dim3(n_cta), dim3(kThreads), kSmem, s, q, k, v, a);
 }
 
 }  // namespace
