@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem;                       // two Q tiles
   uint8_t* sKV = smem + 2 * C::kTileBytes;  // ring
   Shared* sh = reinterpret_cast<Shared*>(sKV + C::kSlots * C::kTileBytes);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same for the warp, and known to be
   const int unit_tokens = 2 * a.tokens, tile_rows = a.tokens * a.g;
   const int active = (tile_rows + 31) / 32;  // softmax warps of a tile that hold rows
   const Waiter wait{&sh->abort, a.timeout_ns};
@@ -161,23 +162,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++slot == C::kSlots) slot = 0, phase ^= 1;
       return true;
     };
+    const uint64_t dq = tc::sdesc_kmajor_sw128(tc::smem_u32(sQ)), dk = tc::sdesc_kmajor_sw128(tc::smem_u32(sKV));
+    const uint64_t dv = tc::sdesc_mnmajor(tc::smem_u32(sKV), C::kHalfBytes);
     // S_st = Q_st K^T for the tile in ring slot `ks`
     auto issue_qk = [&](int st, int ks) {
-      const uint32_t q = tc::smem_u32(sQ + st * C::kTileBytes), k = tc::smem_u32(sKV + ks * C::kTileBytes);
+      const uint64_t q = dq + uint32_t(st * (C::kTileBytes >> 4)), k = dk + uint32_t(ks * (C::kTileBytes >> 4));
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        const uint32_t off = (i / 4) * C::kHalfBytes + (i % 4) * 32;
-        tc::mma_bf16(tmem + st * kTile, tc::sdesc_kmajor_sw128(q + off), tc::sdesc_kmajor_sw128(k + off), idesc_qk, i != 0);
+        constexpr int kHalf = C::kHalfBytes;
+        tc::mma_bf16(tmem + st * kTile, q + (((i / 4) * kHalf + (i % 4) * 32) >> 4),
+                     k + (((i / 4) * kHalf + (i % 4) * 32) >> 4), idesc_qk, i != 0);
       }
       tc::mma_commit(tc::smem_u32(&sh->s_full[st]));
     };
     // O_st (+)= P_st V; P_st lies over the first 64 columns of S_st
     auto issue_pv = [&](int st, int vs, bool add) {
-      const uint32_t v = tc::smem_u32(sKV + vs * C::kTileBytes);
+      const uint64_t v = dv + uint32_t(vs * (C::kTileBytes >> 4));
 #pragma unroll
       for (int i = 0; i < kTile / 16; ++i)
-        tc::mma_bf16_ts(tmem + 2 * kTile + st * D, tmem + st * kTile + 8 * i,
-                        tc::sdesc_mnmajor(v + i * 2048, C::kHalfBytes), idesc_pv, add || i != 0);
+        tc::mma_bf16_ts(tmem + 2 * kTile + st * D, tmem + st * kTile + 8 * i, v + ((i * 2048) >> 4), idesc_pv, add || i != 0);
     };
     while (ok && walk.next(a, sh->range, s)) {
       const int n_st = s.ntok > a.tokens ? 2 : 1;
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = take(ks) && wait(&sh->q_full[0], q_use[0]++ & 1) && (n_st == 1 || wait(&sh->q_full[1], q_use[1]++ & 1));
       if (!ok) break;
       tc::tc_fence_after();
-      if (lane == 0) {
+      if (tc::elect_one()) {
         for (int st = 0; st < n_st; ++st) {
           issue_qk(st, ks);
           if (s.n == 1) tc::mma_commit(tc::smem_u32(&sh->q_empty[st]));
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(&sh->p_full[st], p_use[st]++ & 1) && (st != 0 || !more || take(ks));
           if (!ok) break;
           tc::tc_fence_after();
-          if (lane == 0) {
+          if (tc::elect_one()) {
             issue_pv(st, vs, j > 0);
             if (!more) tc::mma_commit(tc::smem_u32(&sh->o_full[st]));
             if (st == n_st - 1) tc::mma_commit(tc::smem_u32(&sh->kv_empty[vs]));
