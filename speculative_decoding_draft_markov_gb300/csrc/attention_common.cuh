@@ -113,6 +113,16 @@ struct Walk {
   }
 };
 
+// A position in a ring of N slots.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == N) slot = 0, phase ^= 1;
+  }
+};
+
 struct Waiter {
   volatile int* abort;
   uint64_t timeout_ns;

@@ -13,7 +13,8 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 384;  // warps 0-3: softmax of the first tile, 4-7: of the second, 8: TMA, 9: MMA
+constexpr int kThreads = 384;  // warps 0-3: softmax of the first tile, 4-7: of the second, 8: TMA, 9: MMA,
+                               // 10: clears what must not be seen of V
 // Registers: launched with 384 x 168; the softmax warps hold a whole row of S and take what the others
 // give back (256 x 208 + 128 x 80 <= 384 x 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
@@ -24,11 +25,11 @@ struct Cfg {
   static constexpr int kHalves = D / 64;            // 128-byte swizzled column blocks of a tile
   static constexpr int kHalfBytes = kTile * 128;
   static constexpr int kTileBytes = kHalves * kHalfBytes;
-  static constexpr int kSlots = D == 128 ? 5 : 10;  // ring of K and V tiles: 160 KB either way
+  static constexpr int kKSlots = D == 128 ? 2 : 5, kVSlots = D == 128 ? 3 : 5;  // rings: 160 KB either way
 };
 
 struct Shared {
-  uint64_t q_full[2], q_empty[2], kv_full[10], kv_empty[10], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], q_empty[2], k_full[5], k_empty[5], v_full[5], v_empty[5], v_ready[5], s_full[2], p_full[2][2], o_full[2], drain;
   uint32_t tmem_base;
   volatile int abort;
   int mma_pending;
@@ -50,8 +51,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;                       // two Q tiles
-  uint8_t* sKV = smem + 2 * C::kTileBytes;  // ring
-  Shared* sh = reinterpret_cast<Shared*>(sKV + C::kSlots * C::kTileBytes);
+  uint8_t* sK = smem + 2 * C::kTileBytes;
+  uint8_t* sV = sK + C::kKSlots * C::kTileBytes;
+  Shared* sh = reinterpret_cast<Shared*>(sV + C::kVSlots * C::kTileBytes);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same for the warp, and known to be
   const int unit_tokens = 2 * a.tokens, tile_rows = a.tokens * a.g;
@@ -61,14 +63,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::smem_u32(&sh->q_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->q_empty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->q_empty[i]), 1 + active);  // the last S, and the rows written through it
       tc::mbar_init(tc::smem_u32(&sh->s_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->p_full[i]), active);
+      tc::mbar_init(tc::smem_u32(&sh->p_full[i][0]), active);
+      tc::mbar_init(tc::smem_u32(&sh->p_full[i][1]), active);
       tc::mbar_init(tc::smem_u32(&sh->o_full[i]), 1);
     }
-    for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(tc::smem_u32(&sh->kv_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->kv_empty[i]), 1);
+    for (int i = 0; i < 5; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh->k_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->k_empty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->v_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->v_empty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->v_ready[i]), 1);
     }
     tc::mbar_init(tc::smem_u32(&sh->drain), 1);
     tc::fence_mbar_init();
@@ -90,19 +96,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
     // --------------------------------------------------------------------- TMA producer
-    // Ring order in a unit: K 0, then V j, K j + 1.  K and V are read by every unit of the head: kept in L2.
+    // In order: a unit's K 0 and Q, then V j, K j + 1.  K and V are read by every unit of the head: kept in L2.
     const uint64_t keep = tc::policy_evict_last();
-    int slot = 0, seg_i = 0, flags = 0, q_use[2] = {0, 0};
-    uint32_t phase = 0, issued = 0;
+    Ring<C::kKSlots> kr;
+    Ring<C::kVSlots> vr;
+    int seg_i = 0, flags = 0, n_k = 0, n_v = 0, q_use[2] = {0, 0};
     int4 info = make_int4(0, 0, 0, 0);
     bool ok = true;
     Walk walk(sh->range, unit_tokens);
     Segment s = {};
-    auto put = [&](const CUtensorMap* map, const TileLoad& t) {
-      if (!wait(&sh->kv_empty[slot], phase ^ 1)) return false;
-      issue_tile<C::kHalves>(a, map, t, tc::smem_u32(sKV + slot * C::kTileBytes), tc::smem_u32(&sh->kv_full[slot]), keep, lane);
-      issued |= 1u << slot;
-      if (++slot == C::kSlots) slot = 0, phase ^= 1;
+    auto put_k = [&](const TileLoad& t) {
+      if (!wait(&sh->k_empty[kr.slot], kr.phase ^ 1)) return false;
+      issue_tile<C::kHalves>(a, &map_k, t, tc::smem_u32(sK + kr.slot * C::kTileBytes), tc::smem_u32(&sh->k_full[kr.slot]), keep,
+                             lane);
+      ++n_k;
+      kr.step();
+      return true;
+    };
+    auto put_v = [&](const TileLoad& t) {
+      if (!wait(&sh->v_empty[vr.slot], vr.phase ^ 1)) return false;
+      issue_tile<C::kHalves>(a, &map_v, t, tc::smem_u32(sV + vr.slot * C::kTileBytes), tc::smem_u32(&sh->v_full[vr.slot]), keep,
+                             lane);
+      ++n_v;
+      vr.step();
       return true;
     };
     auto put_q = [&](int b, int row) {
@@ -122,11 +138,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s.tile0 == 0 && s.n < s.u.ntiles) flags |= kHeadUsed, info = make_int4(0, s.row0, s.ntok, s.h);
       TileLoad t0 = tile_load(a, s, 0, lane), t1 = t0;
       if (s.n > 1) t1 = tile_load(a, s, 1, lane);
-      ok = put(&map_k, t0) && put_q(0, s.row0) && (s.ntok <= a.tokens || put_q(1, s.row0 + a.tokens));
+      ok = put_k(t0) && put_q(0, s.row0) && (s.ntok <= a.tokens || put_q(1, s.row0 + a.tokens));
       for (int j = 0; ok && j < s.n; ++j) {
         TileLoad t2 = t1;
         if (j + 2 < s.n) t2 = tile_load(a, s, j + 2, lane);
-        ok = put(&map_v, t0) && (j + 1 >= s.n || put(&map_k, t1));
+        ok = put_v(t0) && (j + 1 >= s.n || put_k(t1));
         t0 = t1, t1 = t2;
       }
       ++seg_i;
@@ -137,9 +153,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // wait (bounded) for every copy in flight before the CTA exits
       const volatile int never = 0;
       const long long dl = tc::deadline_after_ns(200000000ull);
-      for (int i = 0; i < C::kSlots; ++i)  // slots before `slot` were last used in this round, the others in the last one
-        if (issued >> i & 1u)
-          tc::mbar_wait_bounded(tc::smem_u32(&sh->kv_full[i]), i < slot ? phase : phase ^ 1, dl, &never);
+      // slots before the ring's position were last used in this round, the others in the last one
+      for (int i = 0; i < min(n_k, C::kKSlots); ++i)
+        tc::mbar_wait_bounded(tc::smem_u32(&sh->k_full[i]), i < kr.slot ? kr.phase : kr.phase ^ 1, dl, &never);
+      for (int i = 0; i < min(n_v, C::kVSlots); ++i)
+        tc::mbar_wait_bounded(tc::smem_u32(&sh->v_full[i]), i < vr.slot ? vr.phase : vr.phase ^ 1, dl, &never);
       for (int b = 0; b < 2; ++b)
         if (q_use[b] > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[b]), (q_use[b] - 1) & 1, dl, &never);
     }
@@ -151,19 +169,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------------- MMA issuer
     constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kTile, kTile);
     constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kTile, D) | tc::kIdescBMajorMN;
-    int slot = 0, seg_i = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
-    uint32_t phase = 0;
+    Ring<C::kKSlots> kr;
+    Ring<C::kVSlots> vr;
+    int seg_i = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
     bool ok = true, any = false;
     Walk walk(sh->range, unit_tokens);
     Segment s = {};
-    auto take = [&](int& which) {  // the next filled slot of the ring
-      which = slot;
-      if (!wait(&sh->kv_full[slot], phase)) return false;
-      if (++slot == C::kSlots) slot = 0, phase ^= 1;
-      return true;
-    };
-    const uint64_t dq = tc::sdesc_kmajor_sw128(tc::smem_u32(sQ)), dk = tc::sdesc_kmajor_sw128(tc::smem_u32(sKV));
-    const uint64_t dv = tc::sdesc_mnmajor(tc::smem_u32(sKV), C::kHalfBytes);
+    const uint64_t dq = tc::sdesc_kmajor_sw128(tc::smem_u32(sQ)), dk = tc::sdesc_kmajor_sw128(tc::smem_u32(sK));
+    const uint64_t dv = tc::sdesc_mnmajor(tc::smem_u32(sV), C::kHalfBytes);
     // S_st = Q_st K^T for the tile in ring slot `ks`
     auto issue_qk = [&](int st, int ks) {
       const uint64_t q = dq + uint32_t(st * (C::kTileBytes >> 4)), k = dk + uint32_t(ks * (C::kTileBytes >> 4));
@@ -176,48 +189,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mma_commit(tc::smem_u32(&sh->s_full[st]));
     };
     // O_st (+)= P_st V; P_st lies over the first 64 columns of S_st
-    auto issue_pv = [&](int st, int vs, bool add) {
+    auto issue_pv = [&](int st, int vs, int hf, bool add) {  // of half of the tile's slots
       const uint64_t v = dv + uint32_t(vs * (C::kTileBytes >> 4));
 #pragma unroll
-      for (int i = 0; i < kTile / 16; ++i)
-        tc::mma_bf16_ts(tmem + 2 * kTile + st * D, tmem + st * kTile + 8 * i, v + ((i * 2048) >> 4), idesc_pv, add || i != 0);
+      for (int i = 0; i < kTile / 32; ++i)
+        tc::mma_bf16_ts(tmem + 2 * kTile + st * D, tmem + st * kTile + 32 * hf + 8 * i,
+                        v + uint32_t(hf * (kTile / 2 * 128 >> 4)) + ((i * 2048) >> 4), idesc_pv, add || i != 0);
     };
     while (ok && walk.next(a, sh->range, s)) {
       const int n_st = s.ntok > a.tokens ? 2 : 1;
-      int ks, vs;
-      ok = take(ks) && wait(&sh->q_full[0], q_use[0]++ & 1) && (n_st == 1 || wait(&sh->q_full[1], q_use[1]++ & 1));
+      ok = wait(&sh->k_full[kr.slot], kr.phase) && wait(&sh->q_full[0], q_use[0]++ & 1) && (n_st == 1 || wait(&sh->q_full[1], q_use[1]++ & 1));
       if (!ok) break;
       tc::tc_fence_after();
       if (tc::elect_one()) {
         for (int st = 0; st < n_st; ++st) {
-          issue_qk(st, ks);
+          issue_qk(st, kr.slot);
           if (s.n == 1) tc::mma_commit(tc::smem_u32(&sh->q_empty[st]));
         }
-        tc::mma_commit(tc::smem_u32(&sh->kv_empty[ks]));
+        tc::mma_commit(tc::smem_u32(&sh->k_empty[kr.slot]));
       }
       __syncwarp();
+      kr.step();
       any = true;
       for (int j = 0; ok && j < s.n; ++j) {
-        ok = take(vs);
-        if (!ok) break;
-        clear_unseen<C::kHalves>(a, s, j, sKV + vs * C::kTileBytes, lane);
         const bool more = j + 1 < s.n;
+        ok = wait(&sh->v_ready[vr.slot], vr.phase) && wait(&sh->v_full[vr.slot], vr.phase) && (!more || wait(&sh->k_full[kr.slot], kr.phase));
+        if (!ok) break;
         for (int st = 0; ok && st < n_st; ++st) {
-          ok = wait(&sh->p_full[st], p_use[st]++ & 1) && (st != 0 || !more || take(ks));
+          const uint32_t p_phase = p_use[st]++ & 1;
+          ok = wait(&sh->p_full[st][0], p_phase);
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (tc::elect_one()) issue_pv(st, vr.slot, 0, j > 0);
+          __syncwarp();
+          ok = wait(&sh->p_full[st][1], p_phase);
           if (!ok) break;
           tc::tc_fence_after();
           if (tc::elect_one()) {
-            issue_pv(st, vs, j > 0);
+            issue_pv(st, vr.slot, 1, true);
             if (!more) tc::mma_commit(tc::smem_u32(&sh->o_full[st]));
-            if (st == n_st - 1) tc::mma_commit(tc::smem_u32(&sh->kv_empty[vs]));
+            if (st == n_st - 1) tc::mma_commit(tc::smem_u32(&sh->v_empty[vr.slot]));
             if (more) {
-              issue_qk(st, ks);
+              issue_qk(st, kr.slot);
               if (j + 2 == s.n) tc::mma_commit(tc::smem_u32(&sh->q_empty[st]));
-              if (st == n_st - 1) tc::mma_commit(tc::smem_u32(&sh->kv_empty[ks]));
+              if (st == n_st - 1) tc::mma_commit(tc::smem_u32(&sh->k_empty[kr.slot]));
             }
           }
           __syncwarp();
         }
+        vr.step();
+        if (more) kr.step();
       }
       ++seg_i;
     }
@@ -226,6 +247,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) note_timeout(a.status, a.diag, 2u, uint32_t(seg_i));
     }
     if (lane == 0) sh->mma_pending = any;
+  } else if (warp == 10) {
+    // ------------------------------------------- V tiles: unseen slots cleared, then ready for the MMA
+    Ring<C::kVSlots> ring;
+    int seg_i = 0;
+    bool ok = true;
+    Walk walk(sh->range, unit_tokens);
+    Segment s = {};
+    while (ok && walk.next(a, sh->range, s)) {
+      for (int j = 0; j < s.n; ++j) {
+        ok = wait(&sh->v_full[ring.slot], ring.phase);
+        if (!ok) break;
+        clear_unseen<C::kHalves>(a, s, j, sV + ring.slot * C::kTileBytes, lane);
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->v_ready[ring.slot]));
+        ring.step();
+      }
+      ++seg_i;
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 4u, uint32_t(seg_i));
+    }
   } else if (warp < 8) {
     // ------------------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -245,6 +287,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p = s.u.p0 + tok0 + tok;  // this row's position; the tile's: q0 .. q1
         const int q0 = s.u.p0 + tok0, q1 = min(q0 + a.tokens - 1, s.u.p1);
         const bool valid = row < tile_rows && tok0 + tok < s.ntok;
+        // tiles j_in0 .. j_in1 - 1 of the segment are seen whole by every row of the tile
+        const int per_tile = kTile >> a.block_shift;
+        int in0 = s.u.sb, in1 = ((q0 + 1) >> a.block_shift) + s.u.sb - s.u.wb0;  // in blocks of the unit
+        if (a.window) in0 = max(in0, ((q1 - a.window + (1 << a.block_shift)) >> a.block_shift) + s.u.sb - s.u.wb0);
+        const int j_in0 = (in0 + per_tile - 1) / per_tile - s.tile0, j_in1 = in1 / per_tile - s.tile0;
         float m = -INFINITY, l = 0.f;  // the reference (log2 units) and the sum
         for (int j = 0; j < s.n; ++j) {
           ok = wait(&sh->s_full[st], s_use++ & 1);
@@ -253,10 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float x[kTile];
           tc::tmem_ld<kTile>(t_s, x);
           tc::tmem_ld_wait();
-          const int first = (s.tile0 + j) * (kTile >> a.block_shift);
-          const int begin = block_pos(a, s.u, first);
-          const bool inside = first >= s.u.sb && begin + kTile - 1 <= q0 && (a.window == 0 || begin > q1 - a.window);
-          if (!inside) {
+          if (j < j_in0 || j >= j_in1) {
+            const int first = (s.tile0 + j) * per_tile;
             const float hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
 #pragma unroll
             for (int gr = 0; gr < kTile / 8; ++gr) {  // 8 slots of one block
@@ -318,14 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               pk[k] = *reinterpret_cast<const uint32_t*>(&h2);
             }
             tc::tmem_st32(t_s + 32 * hf, pk);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->p_full[st][hf]));  // the product with V may begin
           }
           float u0, u1;
           unpack_f32x2(add_f32x2(l2[0], l2[1]), u0, u1);
           l += u0 + u1;
-          tc::tmem_st_wait();
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->p_full[st]));
         }
         if (!ok) break;
         ok = wait(&sh->o_full[st], o_use++ & 1);
@@ -336,18 +381,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t prow = (int64_t(2) * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * (2 * kTile) + st * kTile + row;
         const bool partial = s.n < s.u.ntiles;
         const float inv = l > 0.f ? 1.f / l : 0.f;
+        // whole rows go through the unit's Q tile (its last S is done), so that lanes store 16-byte pieces in
+        // a row; pieces are rotated over the banks
+        constexpr int kPieces = D / 8;
+        uint4* stage = reinterpret_cast<uint4*>(sQ + st * C::kTileBytes);
 #pragma unroll
         for (int i = 0; i < D; i += 32) {
           float v[32];
           tc::tmem_ld<32>(t_o + i, v);
           tc::tmem_ld_wait();
-          if (valid && partial) {
+          if (partial) {
             float4* dst = reinterpret_cast<float4*>(a.partial + prow * D + i);
+            if (valid) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              dst[k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
-          } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + oat * D + i);
+              for (int k = 0; k < 8; ++k)
+                dst[k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+            }
+          } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t w[4];
@@ -356,9 +406,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[8 * k + 2 * z] * inv, v[8 * k + 2 * z + 1] * inv);
                 w[z] = *reinterpret_cast<const uint32_t*>(&h2);
               }
-              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+              stage[row * kPieces + ((i / 8 + k) ^ (row & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
+        }
+        if (!partial) {
+          __syncwarp();  // a warp stores its own 32 rows
+          constexpr int kLanes = kPieces, kAtOnce = 32 / kLanes;  // lanes per row, rows per store
+          const int piece = lane % kLanes;
+#pragma unroll 4
+          for (int i = 0; i < 32; i += kAtOnce) {
+            const int r = (warp & 3) * 32 + i + lane / kLanes, r_tok = r / a.g;
+            if (r < tile_rows && tok0 + r_tok < s.ntok)
+              *reinterpret_cast<uint4*>(a.out + (int64_t(s.row0 + tok0 + r_tok) * a.Hq + s.h * a.g + r - r_tok * a.g) * D +
+                                        piece * 8) = stage[r * kPieces + (piece ^ (r & 7))];
+          }
+          tc::fence_proxy_async_smem();  // before the next TMA into this tile
         }
         if (valid) {
           const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
@@ -368,6 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.lse[oat] = lse2 * kLn2;
         }
         tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->q_empty[st]));
       }
       if (!ok) {
         sh->abort = 1;
@@ -392,7 +457,7 @@ template <int D>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int n_cta,
                    cudaStream_t s) {
   using C = Cfg<D>;
-  constexpr int kSmem = (2 + C::kSlots) * C::kTileBytes + int(sizeof(Shared));
+  constexpr int kSmem = (2 + C::kKSlots + C::kVSlots) * C::kTileBytes + int(sizeof(Shared));
   static_assert(kSmem <= 232448, "dynamic shared memory beyond the 227 KB per-block limit");
   static bool done[tch::kMaxDevices] = {};
   static std::mutex mu;

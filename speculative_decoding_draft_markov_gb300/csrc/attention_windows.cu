@@ -28,9 +28,9 @@ constexpr int kMaxSlots = 6;
 constexpr float kUnset = -1e30f, kRescaleAt = 60.f;  // log2 units
 
 // Sixteen softmax warps in groups of four; a group takes R / kRowGroups rows of its set's tiles.  Then one warp
-// each for TMA, S^T and O^T.
+// each for TMA, S^T, O^T and the clearing of what must not be seen of V.
 constexpr int kGroups = 4, kThreads = (kGroups + 1) * 128;
-constexpr int kTma = 4 * kGroups, kSWarp = kTma + 1, kOWarp = kTma + 2;
+constexpr int kTma = 4 * kGroups, kSWarp = kTma + 1, kOWarp = kTma + 2, kClearWarp = kTma + 3;
 // Registers: launched with 640 x 96; the softmax warps take what the others give back (512 x 104 + 128 x 56 <= 640 x 96).
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 56;
 
@@ -43,6 +43,7 @@ template <int R>
 struct Shared {
   static constexpr int kSets = Split<R>::kSets, kRowGroups = Split<R>::kRowGroups, kRows = Split<R>::kRows;
   uint64_t q_full[2], q_empty[2], k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
+  uint64_t v_ready[kMaxSlots];
   uint64_t s_full[2], p_full[2], p_empty[2];
   uint64_t o_full[kSets], o_read[kSets];           // a set's O^T is complete; has been read by all that do
   uint64_t group[kGroups];                          // the four warps of a group
@@ -76,16 +77,6 @@ struct Cfg {
   static constexpr int kSmem = (kKSlots + kVSlots) * kSlotBytes + kBehind + kPad + int(sizeof(Shared<R>));
   static constexpr int kTmemCols = 4 * R;  // S^T twice, the sets' O^T; a power of two
   static_assert(kKSlots >= 2 && kVSlots >= 2 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "shared memory layout");
-};
-
-// A position in a ring of N slots.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void step() {
-    if (++slot == N) slot = 0, phase ^= 1;
-  }
 };
 
 // The tiles of a CTA's range one by one.
@@ -162,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(tc::smem_u32(&sh->k_empty[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->v_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->v_empty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->v_ready[i]), 1);
     }
     for (int i = 0; i < kSets; ++i) {
       tc::mbar_init(tc::smem_u32(&sh->o_full[i]), 1);
@@ -320,10 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; cur.next(a, sh->range); ++t) {
       const int set = kSets == 2 ? t & 1 : 0;
       const bool first = cur.j < kSets, last = cur.j + kSets >= cur.s.n;  // of the set's tiles of the unit
-      ok = wait(&sh->v_full[ring.slot], ring.phase);
-      if (!ok) break;
-      clear_unseen<C::kHalves>(a, cur.s, cur.j, sV + ring.slot * C::kSlotBytes, lane);
-      ok = wait(&sh->p_full[t & 1], (t >> 1) & 1);
+      ok = wait(&sh->v_ready[ring.slot], ring.phase) && wait(&sh->v_full[ring.slot], ring.phase) &&
+           wait(&sh->p_full[t & 1], (t >> 1) & 1);
       // the set's O^T of the unit before has been read
       if (ok && first) ok = wait(&sh->o_read[set], ((kSets == 2 && set ? o_uses[kSets - 1]++ : o_uses[0]++) & 1) ^ 1);
       if (!ok) break;
@@ -346,6 +336,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) note_timeout(a.status, a.diag, 4u, uint32_t(t));
     }
     if (lane == 0) sh->pending[1] = t > 0;
+  } else if (warp == kClearWarp) {
+    // ------------------------------------------- V tiles: unseen slots cleared, then ready for O^T
+    Ring<C::kVSlots> ring;
+    int t = 0;
+    bool ok = true;
+    Cursor cur(sh->range, a.tokens);
+    for (; cur.next(a, sh->range); ++t) {
+      ok = wait(&sh->v_full[ring.slot], ring.phase);
+      if (!ok) break;
+      clear_unseen<C::kHalves>(a, cur.s, cur.j, sV + ring.slot * C::kSlotBytes, lane);
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->v_ready[ring.slot]));
+      ring.step();
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 5u, uint32_t(t));
+    }
   } else if (warp < kTma) {
     // ------------------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
