@@ -370,24 +370,63 @@ def dspark_sts_fit(z, ceiling, grid, n_bins, T_out, ece_out, ws=None, stream=Non
 
 
 # ----------------------------------------------------------------- the target model's side
+#
+# These calls are made per layer and per token, so their checks are kept cheap: the tensors' types and
+# shapes, which the library cannot see behind bare pointers.
 
-def _same(want, **tensors) -> None:
-    """Every tensor given has the wanted dtype (the library sees bare pointers)."""
-    for name, t in tensors.items():
-        if t is not None and t.dtype != want:
-            raise ValueError(f"{name} must be {want}, not {t.dtype}")
-
-
-def _row_stride(t, name: str) -> int:
-    """Elements from row to row of a [rows, H, D] tensor whose heads and lanes are dense."""
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
-        raise ValueError(f"{name} must be [rows, heads, lanes] with dense heads and lanes")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+_T = None  # torch's types, once torch is in use
 
 
-def _shape(name: str, t, *want) -> None:
-    if tuple(t.shape) != want:
-        raise ValueError(f"{name} must have shape {want}, not {tuple(t.shape)}")
+class _Types:
+    def __init__(self):
+        import torch
+        self.i32, self.f32, self.i16 = torch.int32, torch.float32, torch.int16
+        self.dtypes = {torch.float32: DSPARK_F32, torch.bfloat16: DSPARK_BF16}
+        self.raw_stream, self.device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+
+
+def _types() -> _Types:
+    global _T
+    if _T is None:
+        _T = _Types()
+    return _T
+
+
+def _bad(what: str):
+    raise ValueError(what)
+
+
+def _ptr(t, dtype, shape, name: str) -> Optional[int]:
+    """The pointer of a dense tensor of that type and shape (shape None: any); None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        _bad(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and t.shape != shape:
+        _bad(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_ptr(t, dtype, shape, name: str):
+    """Pointer and elements from row to row of a [rows, H, D] tensor whose heads and lanes are dense."""
+    if t.dtype is not dtype:
+        _bad(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        _bad(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    rows, H, D = shape
+    row, head, lane = t.stride()
+    if lane != 1 or (head != D and H > 1):
+        _bad(f"{name} must be [rows, heads, lanes] with dense heads and lanes")
+    return t.data_ptr(), row if rows > 1 else H * D
+
+
+def _call(name: str, T: _Types, stream, *args) -> None:
+    s = T.raw_stream(T.device()) if stream is None else _stream(stream)
+    rc = getattr(_LIB or lib(), name)(*args, s)
+    if rc != DSPARK_OK:
+        raise DSparkError(rc, name)
 
 
 def dspark_append_kv(q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k_cache, v_cache, ws,
@@ -396,28 +435,23 @@ def dspark_append_kv(q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k
     q, k, v [rows, heads, D] (rows may be strided: parts of one projection); cos_sin [max_pos, rot] fp32;
     page_table [bs, max_pages] int32; k_cache, v_cache [n_pages, Hkv, page_size, D]; q_out [rows, Hq, D]
     (q and q_out may both be None)."""
-    import torch
-    n_pages, Hkv, page, D = k_cache.shape
-    rows, bs = k.shape[0], cu_seqlens.numel() - 1
-    _same(torch.int32, cu_seqlens=cu_seqlens, ctx_len=ctx_len, page_table=page_table)
-    _same(torch.float32, cos_sin=cos_sin)
-    _same(k_cache.dtype, q=q, k=k, v=v, q_out=q_out, v_cache=v_cache)
-    _shape("v_cache", v_cache, n_pages, Hkv, page, D)
-    _shape("k", k, rows, Hkv, D)
-    _shape("v", v, rows, Hkv, D)
-    _shape("page_table", page_table, bs, page_table.shape[-1])
-    _shape("ctx_len", ctx_len, bs)
-    Hq = Hkv
+    T = _T or _types()
+    cache, dt = k_cache.shape, k_cache.dtype
+    n_pages, Hkv, page, D = cache
+    rows, bs, max_pages = k.shape[0], cu_seqlens.shape[0] - 1, page_table.shape[-1]
+    Hq, qp, qs, qo = Hkv, None, 0, None
     if q is not None:
         Hq = q.shape[1]
-        _shape("q", q, rows, Hq, D)
-        _shape("q_out", q_out, rows, Hq, D)
-    _check(lib().dspark_append_kv(
-        None if q is None else q.data_ptr(), 0 if q is None else _row_stride(q, "q"), k.data_ptr(),
-        _row_stride(k, "k"), v.data_ptr(), _row_stride(v, "v"), _dtype(k_cache), _p(cu_seqlens), _p(ctx_len), bs, rows,
-        _p(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(interleaved), _p(page_table), page_table.shape[1],
-        n_pages, page, Hq, Hkv, D, _p(q_out), _p(k_cache), _p(v_cache), _p(ws), ws.numel(), _stream(stream)),
-        "dspark_append_kv")
+        qp, qs = _rows_ptr(q, dt, (rows, Hq, D), "q")
+        qo = _ptr(q_out, dt, (rows, Hq, D), "q_out")
+    kp, ks = _rows_ptr(k, dt, (rows, Hkv, D), "k")
+    vp, vs = _rows_ptr(v, dt, (rows, Hkv, D), "v")
+    max_pos, rot = cos_sin.shape
+    _call("dspark_append_kv", T, stream, qp, qs, kp, ks, vp, vs, T.dtypes.get(dt, -1),
+          _ptr(cu_seqlens, T.i32, None, "cu_seqlens"), _ptr(ctx_len, T.i32, (bs,), "ctx_len"), bs, rows,
+          _ptr(cos_sin, T.f32, None, "cos_sin"), max_pos, rot, interleaved,
+          _ptr(page_table, T.i32, (bs, max_pages), "page_table"), max_pages, n_pages, page, Hq, Hkv, D, qo,
+          _ptr(k_cache, dt, None, "k_cache"), _ptr(v_cache, dt, cache, "v_cache"), ws.data_ptr(), ws.numel())
 
 
 def dspark_window_attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
@@ -438,24 +472,16 @@ def dspark_window_attention(q, k_cache, v_cache, page_table, cu_seqlens, ctx_len
     """Attention of the packed rows q [rows, Hq, D] over the paged cache: a sliding window (0: everything)
     and the first n_sink tokens.  out [rows, Hq, D]; lse [rows, Hq] fp32 or None; max_rows: the longest
     window expected (it only picks the tiling)."""
-    import torch
-    n_pages, Hkv, page, D = k_cache.shape
-    rows, Hq, bs = q.shape[0], q.shape[1], cu_seqlens.numel() - 1
-    _same(torch.int32, cu_seqlens=cu_seqlens, ctx_len=ctx_len, page_table=page_table)
-    _same(k_cache.dtype, q=q, out=out, v_cache=v_cache)
-    _same(torch.float32, lse=lse)
-    _shape("q", q, rows, Hq, D)
-    _shape("out", out, rows, Hq, D)
-    _shape("v_cache", v_cache, n_pages, Hkv, page, D)
-    _shape("page_table", page_table, bs, page_table.shape[-1])
-    _shape("ctx_len", ctx_len, bs)
-    if lse is not None:
-        _shape("lse", lse, rows, Hq)
-    _check(lib().dspark_window_attention(
-        q.data_ptr(), _row_stride(q, "q"), _dtype(k_cache), _p(k_cache), _p(v_cache), _p(page_table),
-        page_table.shape[1], n_pages, page, _p(cu_seqlens), _p(ctx_len), bs, rows, int(max_rows), Hq, Hkv, D,
-        float(scale), int(window), int(n_sink), _p(out), _p(lse), _p(ws), ws.numel(), _stream(stream)),
-        "dspark_window_attention")
+    T = _T or _types()
+    cache, dt, qshape = k_cache.shape, k_cache.dtype, q.shape
+    n_pages, Hkv, page, D = cache
+    rows, Hq, bs, max_pages = qshape[0], qshape[1], cu_seqlens.shape[0] - 1, page_table.shape[-1]
+    qp, qs = _rows_ptr(q, dt, (rows, Hq, D), "q")
+    _call("dspark_window_attention", T, stream, qp, qs, T.dtypes.get(dt, -1), _ptr(k_cache, dt, None, "k_cache"),
+          _ptr(v_cache, dt, cache, "v_cache"), _ptr(page_table, T.i32, (bs, max_pages), "page_table"), max_pages,
+          n_pages, page, _ptr(cu_seqlens, T.i32, None, "cu_seqlens"), _ptr(ctx_len, T.i32, (bs,), "ctx_len"), bs, rows,
+          max_rows, Hq, Hkv, D, scale, window, n_sink, _ptr(out, dt, qshape, "out"),
+          _ptr(lse, T.f32, (rows, Hq), "lse"), ws.data_ptr(), ws.numel())
 
 
 def dspark_process_logits(logits, cu_seqlens, ids, hist, repetition, frequency, presence, bias_start, bias_ids,
@@ -463,45 +489,35 @@ def dspark_process_logits(logits, cu_seqlens, ids, hist, repetition, frequency, 
     """Penalties, biases and grammar masks on the packed target rows logits [rows, V] (out may be logits):
     hist [bs, V] int16 (dspark_history_build) or None; repetition / frequency / presence [bs] fp32 or None;
     bias_start [bs + 1], bias_ids, bias_vals or None; mask [rows, ceil(V / 32)] int32 words or None."""
-    import torch
-    rows, V = logits.shape
-    bs = cu_seqlens.numel() - 1
-    _same(torch.int32, cu_seqlens=cu_seqlens, ids=ids, bias_start=bias_start, bias_ids=bias_ids, mask=mask)
-    _same(torch.float32, repetition=repetition, frequency=frequency, presence=presence, bias_vals=bias_vals)
-    _same(torch.int16, hist=hist)
-    _same(logits.dtype, out=out)
-    _shape("out", out, rows, V)
-    if ids.numel() < rows:
-        raise ValueError("ids must hold one entry per row")
-    if hist is not None:
-        _shape("hist", hist, bs, V)
-    if mask is not None:
-        _shape("mask", mask, rows, (V + 31) // 32)
-    _check(lib().dspark_process_logits(
-        _p(logits), _dtype(logits), rows, V, _p(cu_seqlens), _p(ids), bs, _p(hist), _p(repetition), _p(frequency),
-        _p(presence), _p(bias_start), _p(bias_ids), _p(bias_vals), _p(mask), _p(out), _p(ws), ws.numel(),
-        _stream(stream)), "dspark_process_logits")
+    T = _T or _types()
+    shape, dt = logits.shape, logits.dtype
+    rows, V = shape
+    bs = cu_seqlens.shape[0] - 1
+    if ids.shape[0] < rows:
+        _bad("ids must hold one entry per row")
+    _call("dspark_process_logits", T, stream, _ptr(logits, dt, None, "logits"), T.dtypes.get(dt, -1), rows, V,
+          _ptr(cu_seqlens, T.i32, None, "cu_seqlens"), _ptr(ids, T.i32, None, "ids"), bs,
+          _ptr(hist, T.i16, (bs, V), "hist"), _ptr(repetition, T.f32, (bs,), "repetition"),
+          _ptr(frequency, T.f32, (bs,), "frequency"), _ptr(presence, T.f32, (bs,), "presence"),
+          _ptr(bias_start, T.i32, (bs + 1,), "bias_start"), _ptr(bias_ids, T.i32, None, "bias_ids"),
+          _ptr(bias_vals, T.f32, None, "bias_vals"), _ptr(mask, T.i32, (rows, (V + 31) // 32), "mask"),
+          _ptr(out, dt, shape, "out"), ws.data_ptr(), ws.numel())
 
 
 def dspark_history_build(tokens, start, n_prompt, hist, ws, stream=None):
     """Rewrite hist [bs, V] int16 from token lists: request r's are tokens[start[r] : start[r + 1]], the first
     n_prompt[r] of them its prompt."""
-    import torch
+    T = _T or _types()
     bs, V = hist.shape
-    _same(torch.int32, tokens=tokens, start=start, n_prompt=n_prompt)
-    _same(torch.int16, hist=hist)
-    _shape("start", start, bs + 1)
-    _shape("n_prompt", n_prompt, bs)
-    _check(lib().dspark_history_build(_p(tokens), tokens.numel(), _p(start), _p(n_prompt), bs, V, _p(hist), _p(ws),
-                                      ws.numel(), _stream(stream)), "dspark_history_build")
+    _call("dspark_history_build", T, stream, _ptr(tokens, T.i32, None, "tokens"), tokens.numel(),
+          _ptr(start, T.i32, (bs + 1,), "start"), _ptr(n_prompt, T.i32, (bs,), "n_prompt"), bs, V,
+          _ptr(hist, T.i16, None, "hist"), ws.data_ptr(), ws.numel())
 
 
 def dspark_history_commit(out_tokens, hist, ws, stream=None):
     """Add a step's out_tokens [bs, gamma + 1] (dspark_verify; -1 skipped) to the said counts of hist [bs, V]."""
-    import torch
+    T = _T or _types()
     bs, V = hist.shape
-    _same(torch.int32, out_tokens=out_tokens)
-    _same(torch.int16, hist=hist)
-    _shape("out_tokens", out_tokens, bs, out_tokens.shape[-1])
-    _check(lib().dspark_history_commit(_p(out_tokens), bs, out_tokens.shape[1] - 1, V, _p(hist), _p(ws), ws.numel(),
-                                       _stream(stream)), "dspark_history_commit")
+    width = out_tokens.shape[-1]
+    _call("dspark_history_commit", T, stream, _ptr(out_tokens, T.i32, (bs, width), "out_tokens"), bs, width - 1, V,
+          _ptr(hist, T.i16, None, "hist"), ws.data_ptr(), ws.numel())

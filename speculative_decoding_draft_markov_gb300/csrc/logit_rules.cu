@@ -2,9 +2,12 @@
 // token history that its penalties read.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "pdl.h"
+#include "tc_host.h"
 
 namespace dspark {
 namespace {
@@ -60,29 +63,58 @@ template <> struct Pack8<float> {
 };
 
 // One streaming pass, bound by memory: read the row, write the row.  A block owns 2048 ids of one
-// request and walks the request's rows; each thread keeps what the rules say of its 8 ids (their
-// counts, and the sum of bias and penalties) in registers, so the history and the biases are read
-// once for all rows of a window, and a drafted token changes one thread's registers.
+// request and walks the request's rows (with few requests, blockIdx.z takes a share of them); each
+// thread keeps what the rules say of its 8 ids (seen, said, and the sum of bias and penalties) in
+// registers, so the history and the biases are read once for all rows of a window, and a drafted token
+// changes one thread's registers.  The first
+// rows are asked for before the history and the biases (three dependent trips to memory otherwise
+// stand before a block's stream), and a row's registers take the next row as soon as they are stored.
 template <typename T>
-__global__ void __launch_bounds__(kRuleThreads) rules_kernel(RuleArgs a) {
+__global__ void __launch_bounds__(kRuleThreads, sizeof(T) == 2 ? 5 : 4) rules_kernel(const __grid_constant__ RuleArgs a) {
   __shared__ float sbias[kRuleChunk];
   pdl_enter();
   const int tid = threadIdx.x, r = blockIdx.y;
   const int lo = blockIdx.x * kRuleChunk, base = lo + tid * kRuleIds;
-  const int row0 = a.cu[r], row1 = a.cu[r + 1];
-  if (row0 < 0 || row1 < row0 || row1 > a.rows) {
+  const int row0 = a.cu[r], row1 = a.cu[r + 1], n = row1 - row0;
+  if (row0 < 0 || n < 0 || row1 > a.rows) {
     if (tid == 0 && blockIdx.x == 0) set_status(a.status, DSPARK_EINVAL);
     return;
   }
-  if (row0 == row1) return;
+  // this block's rows of the window
+  const int share = (n + gridDim.z - 1) / gridDim.z, i0 = blockIdx.z * share, i1 = min(n, i0 + share);
+  if (i0 >= i1) return;
+  const bool live = base < a.V;  // V is a multiple of 8
 
-  float bias[kRuleIds];
+  const T* src = static_cast<const T*>(a.logits) + size_t(row0) * a.V + base;
+  T* dst = static_cast<T*>(a.out) + size_t(row0) * a.V + base;
+  const uint8_t* mk = a.mask ? a.mask + size_t(row0) * a.mask_row_bytes + (base >> 3) : nullptr;
+  Pack8<T> x[kRowBatch];
+  uint32_t allowed[kRowBatch];
+  int drafted[kRowBatch];
+  auto ask = [&](int b, int i) {  // row i into buffer b
+    allowed[b] = 0xFFu, drafted[b] = -1;
+    if (i >= i1 || !live) return;
+    if (!a.in_place) x[b].load(src + size_t(i) * a.V);
+    if (mk) allowed[b] = __ldcs(mk + size_t(i) * a.mask_row_bytes);
+    if (a.hist && i > 0) drafted[b] = a.ids[row0 + i];
+  };
 #pragma unroll
-  for (int j = 0; j < kRuleIds; ++j) bias[j] = 0.f;
+  for (int b = 0; b < kRowBatch; ++b) ask(b, i0 + b);
+
+  uint4 words = make_uint4(0u, 0u, 0u, 0u);
+  if (a.hist && live) words = __ldcs(reinterpret_cast<const uint4*>(a.hist + size_t(r) * a.V + base));
+  const float rho = a.repetition ? a.repetition[r] : 1.f;
+  const float inv_rho = 1.f / rho;  // l / rho as a product: within 1.5 ulp of fp32 of the quotient
+  const float freq = a.frequency ? a.frequency[r] : 0.f, pres = a.presence ? a.presence[r] : 0.f;
+
+  float add[kRuleIds];  // bias - frequency * count - presence * [count > 0]
+#pragma unroll
+  for (int j = 0; j < kRuleIds; ++j) add[j] = 0.f;
   if (a.bias_start) {
     const int e0 = a.bias_start[r], e1 = a.bias_start[r + 1];
     if (e1 > e0) {  // the same for the whole block
-      for (int i = tid; i < kRuleChunk; i += kRuleThreads) sbias[i] = 0.f;
+      for (int i = tid; i < kRuleChunk / 4; i += kRuleThreads)
+        reinterpret_cast<float4*>(sbias)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       __syncthreads();
       for (int e = e0 + tid; e < e1; e += kRuleThreads) {
         const int id = a.bias_ids[e];
@@ -92,81 +124,57 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(RuleArgs a) {
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kRuleIds; ++j) bias[j] = sbias[tid * kRuleIds + j];
+      for (int j = 0; j < kRuleIds; j += 4)
+        *reinterpret_cast<float4*>(add + j) = *reinterpret_cast<const float4*>(sbias + tid * kRuleIds + j);
     }
   }
-  if (base >= a.V) return;  // V is a multiple of 8
+  if (!live) return;
 
-  const float rho = a.repetition ? a.repetition[r] : 1.f;
-  const float inv_rho = 1.f / rho;  // l / rho as a product: within 1.5 ulp of fp32 of the quotient
-  const float freq = a.frequency ? a.frequency[r] : 0.f, pres = a.presence ? a.presence[r] : 0.f;
-  int count[kRuleIds];
-  uint32_t seen = 0, acts = 0;  // bit j: id j was seen; a rule but the mask can change id j
-  float add[kRuleIds];
-  auto weigh = [&](int j) {
-    add[j] = bias[j] - freq * float(count[j]) - (count[j] > 0 ? pres : 0.f);
-    if (add[j] != 0.f || ((seen >> j & 1u) && rho != 1.f)) acts |= 1u << j;
+  // bit j: id j was seen; was said; some rule but the mask can change it
+  uint32_t seen = 0, said = 0, acts = 0;
+  const bool scales = rho != 1.f;
+  const uint32_t h[4] = {words.x, words.y, words.z, words.w};
+#pragma unroll
+  for (int j = 0; j < kRuleIds; ++j) {
+    const uint32_t word = (h[j >> 1] >> (16 * (j & 1))) & 0xFFFFu, count = word & 0x7FFFu;
+    add[j] = add[j] - freq * float(count) - (count ? pres : 0.f);
+    if (word) seen |= 1u << j;
+    if (count) said |= 1u << j;
+    if (add[j] != 0.f || (word && scales)) acts |= 1u << j;
+  }
+  auto say = [&](int id) {  // one more of `id`
+    const int d = id - base;
+    if (d >= 0 && d < kRuleIds) {
+#pragma unroll
+      for (int j = 0; j < kRuleIds; ++j)
+        if (j == d) add[j] -= said >> j & 1u ? freq : freq + pres;
+      seen |= 1u << d, said |= 1u << d, acts |= 1u << d;
+    }
+    if (base == 0 && (id < 0 || id >= a.V)) set_status(a.status, DSPARK_EINVAL);
   };
-  {
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (a.hist) w = *reinterpret_cast<const uint4*>(a.hist + size_t(r) * a.V + base);
-    const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < kRuleIds; ++j) {
-      const uint32_t word = (h[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-      count[j] = int(word & 0x7FFFu);
-      if (word) seen |= 1u << j;
-      weigh(j);
-    }
-  }
+  if (a.hist)
+    for (int i = 1; i < i0; ++i) say(a.ids[row0 + i]);  // drafted before this block's rows
 
-  const T* src = static_cast<const T*>(a.logits) + size_t(row0) * a.V + base;
-  T* dst = static_cast<T*>(a.out) + size_t(row0) * a.V + base;
-  const uint8_t* mk = a.mask ? a.mask + size_t(row0) * a.mask_row_bytes + (base >> 3) : nullptr;
-  for (int first = 0; first < row1 - row0; first += kRowBatch) {
-    Pack8<T> x[kRowBatch];
-    uint32_t allowed[kRowBatch];
-    int drafted[kRowBatch];
+  for (int first = i0; first < i1; first += kRowBatch) {
 #pragma unroll
     for (int b = 0; b < kRowBatch; ++b) {
       const int i = first + b;
-      allowed[b] = 0xFFu, drafted[b] = -1;
-      if (i >= row1 - row0) continue;
-      if (!a.in_place) x[b].load(src + size_t(i) * a.V);
-      if (mk) allowed[b] = mk[size_t(i) * a.mask_row_bytes];
-      if (a.hist && i > 0) drafted[b] = a.ids[row0 + i];
-    }
+      if (i >= i1) break;
+      if (a.hist && i > 0) say(drafted[b]);
+      if (!a.in_place || acts != 0 || allowed[b] != 0xFFu) {  // in place, nothing else changes
+        if (a.in_place) x[b].load(src + size_t(i) * a.V);
+        float v[kRuleIds];
+        x[b].get(v);
 #pragma unroll
-    for (int b = 0; b < kRowBatch; ++b) {
-      const int i = first + b;
-      if (i >= row1 - row0) break;
-      if (a.hist && i > 0) {
-        const int d = drafted[b] - base;
-        if (d >= 0 && d < kRuleIds) {
-#pragma unroll
-          for (int j = 0; j < kRuleIds; ++j)
-            if (j == d) {
-              ++count[j];
-              seen |= 1u << j;
-              weigh(j);
-            }
+        for (int j = 0; j < kRuleIds; ++j) {
+          float l = v[j];
+          if (seen >> j & 1u) l *= l > 0.f ? inv_rho : rho;
+          l += add[j];
+          v[j] = allowed[b] >> j & 1u ? l : -INFINITY;
         }
-        if (base == 0 && (drafted[b] < 0 || drafted[b] >= a.V)) set_status(a.status, DSPARK_EINVAL);
+        Pack8<T>::store(dst + size_t(i) * a.V, v);
       }
-      if (a.in_place) {
-        if (acts == 0 && allowed[b] == 0xFFu) continue;  // nothing changes here
-        x[b].load(src + size_t(i) * a.V);
-      }
-      float v[kRuleIds];
-      x[b].get(v);
-#pragma unroll
-      for (int j = 0; j < kRuleIds; ++j) {
-        float l = v[j];
-        if (seen >> j & 1u) l *= l > 0.f ? inv_rho : rho;
-        l += add[j];
-        v[j] = allowed[b] >> j & 1u ? l : -INFINITY;
-      }
-      Pack8<T>::store(dst + size_t(i) * a.V, v);
+      ask(b, i + kRowBatch);
     }
   }
 }
@@ -174,6 +182,7 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(RuleArgs a) {
 // ---------------------------------------------------------------------------- history
 
 constexpr int kHistThreads = 512;
+constexpr int kHistMaxChunk = 18 * 1024;  // ids of a block: 72 KB of cells, three blocks on an SM
 
 // A block counts one request's tokens that fall into its `chunk` ids in shared memory (32-bit:
 // a list can be longer than the 15-bit count) and writes the chunk once.
@@ -181,23 +190,24 @@ __global__ void __launch_bounds__(kHistThreads)
     history_build_kernel(const int32_t* __restrict__ tokens, int n_tokens, const int32_t* __restrict__ start,
                          const int32_t* __restrict__ n_prompt, int V, int chunk, int16_t* __restrict__ hist,
                          uint32_t* status) {
-  extern __shared__ uint32_t cell[];
+  extern __shared__ __align__(16) uint32_t cell[];
   pdl_enter();
   const int tid = threadIdx.x, r = blockIdx.y;
   const int lo = blockIdx.x * chunk, n = min(chunk, V - lo);
-  for (int i = tid; i < n; i += kHistThreads) cell[i] = 0u;
-  __syncthreads();
   int t0 = start[r], t1 = start[r + 1];
+  const int asked = n_prompt[r];
+  for (int i = tid; i < n / 4; i += kHistThreads) reinterpret_cast<uint4*>(cell)[i] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
   if (t0 < 0 || t1 < t0 || t1 > n_tokens) {
     if (tid == 0 && blockIdx.x == 0) set_status(status, DSPARK_EINVAL);
     t0 = t1 = 0;
   }
-  const int said0 = t0 + n_prompt[r];
+#pragma unroll 4
   for (int t = t0 + tid; t < t1; t += kHistThreads) {
     const int id = tokens[t];
     const int d = id - lo;
     if (d >= 0 && d < n) {
-      if (t < said0)
+      if (t - t0 < asked)
         atomicOr(&cell[d], 0x80000000u);
       else
         atomicAdd(&cell[d], 1u);
@@ -205,9 +215,13 @@ __global__ void __launch_bounds__(kHistThreads)
     if (blockIdx.x == 0 && (id < 0 || id >= V)) set_status(status, DSPARK_EINVAL);
   }
   __syncthreads();
-  uint32_t* out = reinterpret_cast<uint32_t*>(hist + size_t(r) * V + lo);
+  uint4* out = reinterpret_cast<uint4*>(hist + size_t(r) * V + lo);  // chunks and V: multiples of 8
   auto word = [](uint32_t c) { return min(c & 0x7FFFFFFFu, 0x7FFFu) | (c >> 16 & 0x8000u); };
-  for (int i = tid; 2 * i < n; i += kHistThreads) out[i] = word(cell[2 * i]) | word(cell[2 * i + 1]) << 16;
+  auto two = [&](uint32_t a, uint32_t b) { return word(a) | word(b) << 16; };
+  for (int i = tid; i < n / 8; i += kHistThreads) {
+    const uint4 a = reinterpret_cast<const uint4*>(cell)[2 * i], b = reinterpret_cast<const uint4*>(cell)[2 * i + 1];
+    out[i] = make_uint4(two(a.x, a.y), two(a.z, a.w), two(b.x, b.y), two(b.z, b.w));
+  }
 }
 
 // One thread per committed token: a saturating add on its half of a 32-bit word.
@@ -247,14 +261,25 @@ cudaError_t launch_process_logits(const void* logits, int dtype, int rows, int V
   a.mask = reinterpret_cast<const uint8_t*>(mask);  // little-endian words: byte i holds ids 8i .. 8i+7
   a.status = status, a.rows = rows, a.V = V, a.mask_row_bytes = (V + 31) / 32 * 4;
   a.in_place = logits == out;
-  const dim3 grid((V + kRuleChunk - 1) / kRuleChunk, bs);
+  // about 8 blocks for each SM: the rows of a window are shared out where requests are few
+  const int chunks = (V + kRuleChunk - 1) / kRuleChunk, want = 8 * tch::sm_count();
+  const int share = std::max(1, std::min({want / (chunks * bs), rows / bs, 8}));
+  const dim3 grid(chunks, bs, share);
   return dtype == DSPARK_F32 ? launch_pdl(rules_kernel<float>, grid, dim3(kRuleThreads), 0, s, a)
                              : launch_pdl(rules_kernel<__nv_bfloat16>, grid, dim3(kRuleThreads), 0, s, a);
 }
 
 cudaError_t launch_history_build(const int32_t* tokens, int n_tokens, const int32_t* start, const int32_t* n_prompt,
                                  int bs, int V, int16_t* hist, uint32_t* status, cudaStream_t s) {
-  const int chunk = 2048;
+  // every block of a request reads the request's whole list, so chunks are as large as still gives each SM
+  // three blocks, and shared memory allows
+  const int per_sm = 3 * tch::sm_count();
+  const int64_t ids = (int64_t(V) * bs + per_sm - 1) / per_sm;
+  const int chunk = int(std::min<int64_t>(kHistMaxChunk, std::max<int64_t>(2048, (ids + 2047) / 2048 * 2048)));
+  static bool done[tch::kMaxDevices] = {};
+  static std::mutex mu;
+  const cudaError_t e = tch::set_smem_once(history_build_kernel, kHistMaxChunk * int(sizeof(uint32_t)), done, &mu);
+  if (e != cudaSuccess) return e;
   return launch_pdl(history_build_kernel, dim3((V + chunk - 1) / chunk, bs), dim3(kHistThreads),
                     chunk * sizeof(uint32_t), s, tokens, n_tokens, start, n_prompt, V, chunk, hist, status);
 }
