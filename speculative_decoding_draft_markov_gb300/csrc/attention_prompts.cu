@@ -3,9 +3,11 @@
 // Bound by the two products and the exponentials.  A unit is two Q tiles of 128 rows that read the same KV tiles:
 //     S = Q K^T  (tcgen05, fp32 in TMEM)  ->  P = 2^(c S - m), l += sum P  (registers, one thread per row)
 //     O += P V   (tcgen05; P in bf16 in TMEM over S, O in fp32 in TMEM)
-// While one tile's softmax runs, the tensor cores work for the other.  m is only a reference that keeps the
-// exponentials in range: it moves (and O and l are rescaled) when a row's maximum has outgrown it by 2^8,
-// which is exact in the end because the sum is divided out.
+// While one tile's softmax runs, the tensor cores work for the other.  The softmax of a tile has to be done within
+// the other tile's two products, so its first half is handed on as soon as it is there, computed by the
+// reference m as it stands while the row's maximum is found: m only keeps the exponentials in range, and
+// any value within 2^60 of the maximum gives the same result, since the sum is divided out and neither fp32 nor
+// bf16 loses bits there.  It moves, and O and l are rescaled, when a maximum has outgrown it by more.
 #include "attention_common.cuh"
 
 namespace dspark {
@@ -18,7 +20,7 @@ constexpr int kThreads = 384;  // warps 0-3: softmax of the first tile, 4-7: of 
 // Registers: launched with 384 x 168; the softmax warps hold a whole row of S and take what the others
 // give back (256 x 208 + 128 x 80 <= 384 x 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
-constexpr float kRescaleAt = 8.f;
+constexpr float kUnset = -1e30f, kRescaleAt = 60.f;  // log2 units
 
 template <int D>
 struct Cfg {
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int in0 = s.u.sb, in1 = ((q0 + 1) >> a.block_shift) + s.u.sb - s.u.wb0;  // in blocks of the unit
         if (a.window) in0 = max(in0, ((q1 - a.window + (1 << a.block_shift)) >> a.block_shift) + s.u.sb - s.u.wb0);
         const int j_in0 = (in0 + per_tile - 1) / per_tile - s.tile0, j_in1 = in1 / per_tile - s.tile0;
-        float m = -INFINITY, l = 0.f;  // the reference (log2 units) and the sum
+        float m = kUnset, l = 0.f;  // the reference (log2 units) and the sum
         for (int j = 0; j < s.n; ++j) {
           ok = wait(&sh->s_full[st], s_use++ & 1);
           if (!ok) break;
@@ -303,16 +305,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j < j_in0 || j >= j_in1) {
             const int first = (s.tile0 + j) * per_tile;
             const float hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
+            if (first >= s.u.sb) {  // one run of positions: slots from .. to are seen
+              const int begin = block_pos(a, s.u, first);
+              const int to = p - begin, from = a.window ? p - a.window + 1 - begin : 0;
+              if (__any_sync(~0u, to < kTile - 1)) {
 #pragma unroll
-            for (int gr = 0; gr < kTile / 8; ++gr) {  // 8 slots of one block
-              const int pos = block_pos(a, s.u, first + ((8 * gr) >> a.block_shift)) + ((8 * gr) & ((1 << a.block_shift) - 1));
-              uint32_t see = bits_between(a.window ? p - a.window + 1 - pos : 0, p - pos);
-              if (a.window) see |= bits_between(0, min(p, a.n_sink - 1) - pos);
+                for (int i = 0; i < kTile; ++i)
+                  if (i > to) x[i] = hidden;
+              }
+              if (__any_sync(~0u, from > 0)) {  // a slot below n_sink stays: none here, unless sinks meet the window
+                const int keep = a.n_sink - begin;
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (!(see >> k & 1u)) x[8 * gr + k] = hidden;
+                for (int i = 0; i < kTile; ++i)
+                  if (i < from && i >= keep) x[i] = hidden;
+              }
+            } else {
+#pragma unroll
+              for (int gr = 0; gr < kTile / 8; ++gr) {  // 8 slots of one block
+                const int pos = block_pos(a, s.u, first + ((8 * gr) >> a.block_shift)) + ((8 * gr) & ((1 << a.block_shift) - 1));
+                const uint32_t see = bits_between(p - a.window + 1 - pos, p - pos) | bits_between(0, min(p, a.n_sink - 1) - pos);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  if (!(see >> k & 1u)) x[8 * gr + k] = hidden;
+              }
             }
           }
+          // The first half's weights by the reference as it stands, and the row's maximum beside them; a new
+          // reference only where that has been outgrown (and at a unit's first tile)
+          const unsigned long long cc = pack_f32x2(c2, c2);
+          unsigned long long l2[2] = {0ull, 0ull};
+          uint32_t pk[32];
+          auto weigh = [&](int hf) {
+            const unsigned long long mm = pack_f32x2(-m, -m);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const int i = 64 * hf + 2 * k;
+              float e0, e1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(x[i], x[i + 1]), cc, mm), e0, e1);
+              e0 = tc::ex2_approx(e0);
+              e1 = tc::ex2_approx(e1);
+              l2[k & 1] = add_f32x2(l2[k & 1], pack_f32x2(e0, e1));
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
+              pk[k] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+          };
+          auto give = [&](int hf) {  // the product with V may begin
+            tc::tmem_st32(t_s + 32 * hf, pk);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->p_full[st][hf]));
+          };
           float t4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) t4[i] = x[i];
@@ -326,12 +369,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             t4[0] = fminf(fminf(t4[0], t4[1]), fminf(t4[2], t4[3]));
           }
           const float top = t4[0] * c2;
-          float alpha = 1.f;
-          if (top > m + kRescaleAt) {
-            alpha = tc::ex2_approx(m - top);
-            m = top;
-          }
-          if (__any_sync(~0u, alpha != 1.f)) {
+          weigh(0);
+          if (__any_sync(~0u, top > m + kRescaleAt)) {
+            const float old = m;
+            if (top > m) m = top;
+            const float alpha = tc::ex2_approx(old - m);
             l *= alpha;
             if (j > 0) {  // the product with the last tile was issued before this tile's S: it is complete
 #pragma unroll
@@ -344,30 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tmem_st<32>(t_o + i, o);
               }
             }
+            l2[0] = l2[1] = 0ull;
+            weigh(0);
           }
-          const float ref = m == -INFINITY ? 0.f : m;
-          const unsigned long long cc = pack_f32x2(c2, c2), mm = pack_f32x2(-ref, -ref);
-          unsigned long long l2[2] = {0ull, 0ull};
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const int i = 64 * hf + 2 * k;
-              float e0, e1;
-              unpack_f32x2(fma_f32x2(pack_f32x2(x[i], x[i + 1]), cc, mm), e0, e1);
-              e0 = tc::ex2_approx(e0);
-              e1 = tc::ex2_approx(e1);
-              l2[k & 1] = add_f32x2(l2[k & 1], pack_f32x2(e0, e1));
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
-              pk[k] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-            tc::tmem_st32(t_s + 32 * hf, pk);
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->p_full[st][hf]));  // the product with V may begin
-          }
+          give(0);
+          weigh(1);
+          give(1);
           float u0, u1;
           unpack_f32x2(add_f32x2(l2[0], l2[1]), u0, u1);
           l += u0 + u1;
@@ -414,12 +438,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();  // a warp stores its own 32 rows
           constexpr int kLanes = kPieces, kAtOnce = 32 / kLanes;  // lanes per row, rows per store
           const int piece = lane % kLanes;
+          int r = (warp & 3) * 32 + lane / kLanes, r_tok = r / a.g, r_head = r - r_tok * a.g;
+          __nv_bfloat16* dst = a.out + (int64_t(s.row0 + tok0 + r_tok) * a.Hq + s.h * a.g + r_head) * D + piece * 8;
+          const int64_t wrap = int64_t(a.Hq - a.g) * D;  // from a token's last head to the next token's first
+          const int r_end = min(tile_rows, (s.ntok - tok0) * a.g);
 #pragma unroll 4
-          for (int i = 0; i < 32; i += kAtOnce) {
-            const int r = (warp & 3) * 32 + i + lane / kLanes, r_tok = r / a.g;
-            if (r < tile_rows && tok0 + r_tok < s.ntok)
-              *reinterpret_cast<uint4*>(a.out + (int64_t(s.row0 + tok0 + r_tok) * a.Hq + s.h * a.g + r - r_tok * a.g) * D +
-                                        piece * 8) = stage[r * kPieces + (piece ^ (r & 7))];
+          for (int i = 0; i < 32; i += kAtOnce, r += kAtOnce) {
+            if (r < r_end) *reinterpret_cast<uint4*>(dst) = stage[r * kPieces + (piece ^ (r & 7))];
+            dst += kAtOnce * D;
+            for (r_head += kAtOnce; r_head >= a.g; r_head -= a.g) dst += wrap;
           }
           tc::fence_proxy_async_smem();  // before the next TMA into this tile
         }

@@ -98,6 +98,15 @@ def test_rules(ns, V, dtype, use_mask):
     assert st == B.DSPARK_OK and torch.equal(got, out)
 
 
+@pytest.mark.parametrize("n_bias", [60, 65, 700, 5000])
+def test_rules_many_biases(n_bias):
+    """Lists that a warp searches in one, two and more steps, as long as the vocabulary at last."""
+    b = Batch([2, 5, 1, 3], 5000, torch.float32, seed=32, n_bias=n_bias)
+    out, st = b.call()
+    assert st == B.DSPARK_OK
+    b.check(out)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_rules_one_by_one(dtype):
     b = Batch([4, 2, 3], 3000, dtype, seed=31)
