@@ -267,13 +267,22 @@ __device__ __forceinline__ void issue_tile(const AttnArgs& a, const CUtensorMap*
     tc::tma_load_4d(dst + lane * block_bytes + hf * (kTile * 128), map, bar, hf * 64, t.slot, t.head, page, policy);
 }
 
+// Tiles j0 .. j1 - 1 of a segment whose every slot is seen by all rows at positions q0 .. q1 of the unit
+// (q0 = p1, q1 = p0: by some row or other).
+__device__ __forceinline__ void whole_tiles(const AttnArgs& a, const Segment& s, int q0, int q1, int& j0, int& j1) {
+  const int per_tile = kTile >> a.block_shift, shift = s.u.sb - s.u.wb0;
+  // in blocks of the unit: past the sinks and not before the window of q1; ending by q0
+  int in0 = s.u.sb;
+  if (a.window) in0 = max(in0, ((q1 - a.window + (1 << a.block_shift)) >> a.block_shift) + shift);
+  const int in1 = ((q0 + 1) >> a.block_shift) + shift;
+  j0 = (in0 + per_tile - 1) / per_tile - s.tile0, j1 = in1 / per_tile - s.tile0;
+}
+
 // Slots that no row of the unit sees hold whatever was there, NaN included, and 0 * NaN is NaN: their rows of
 // the V tile are cleared.  A whole warp, 16-byte stores, rotated so that the lanes spread over the banks.
 template <int kHalves>
 __device__ __forceinline__ void clear_unseen(const AttnArgs& a, const Segment& s, int j, uint8_t* tile, int lane) {
-  const int first = (s.tile0 + j) * (kTile >> a.block_shift), last = first + (kTile >> a.block_shift) - 1;
-  const int begin = block_pos(a, s.u, first), end = block_pos(a, s.u, last) + (1 << a.block_shift) - 1;
-  if (end <= s.u.p1 && (first >= s.u.sb ? begin >= s.u.lo : end < a.n_sink)) return;
+  const int first = (s.tile0 + j) * (kTile >> a.block_shift);
   for (int i = lane; i < kTile; i += 32) {
     const int pos = block_pos(a, s.u, first + (i >> a.block_shift)) + (i & ((1 << a.block_shift) - 1));
     if (pos <= s.u.p1 && (pos >= s.u.lo || pos < a.n_sink)) continue;
@@ -287,6 +296,9 @@ __device__ __forceinline__ void clear_unseen(const AttnArgs& a, const Segment& s
   tc::fence_proxy_async_smem();
   __syncwarp();
 }
+// The clearing warp and the warp that issues the product with V agree on the tiles that need it; their
+// barriers are counted over those tiles alone (more barriers than V slots, so that neither can lap the other).
+constexpr int kReady = 8;
 
 }  // namespace attn
 

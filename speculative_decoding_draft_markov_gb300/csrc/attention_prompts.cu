@@ -31,7 +31,7 @@ struct Cfg {
 };
 
 struct Shared {
-  uint64_t q_full[2], q_empty[2], k_full[5], k_empty[5], v_full[5], v_empty[5], v_ready[5], s_full[2], p_full[2][2], o_full[2], drain;
+  uint64_t q_full[2], q_empty[2], k_full[5], k_empty[5], v_full[5], v_empty[5], v_ready[kReady], s_full[2], p_full[2][2], o_full[2], drain;
   uint32_t tmem_base;
   volatile int abort;
   int mma_pending;
@@ -44,6 +44,12 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
   const uint32_t below = hi >= 7 ? 0xFFu : hi < 0 ? 0u : (2u << hi) - 1u;
   const uint32_t from = lo <= 0 ? 0xFFu : lo > 7 ? 0u : 0xFFu << lo;
   return below & from;
+}
+
+__device__ __forceinline__ void store_32b(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 template <int D>
@@ -65,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::smem_u32(&sh->q_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->q_empty[i]), 1 + active);  // the last S, and the rows written through it
+      tc::mbar_init(tc::smem_u32(&sh->q_empty[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->s_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->p_full[i][0]), active);
       tc::mbar_init(tc::smem_u32(&sh->p_full[i][1]), active);
@@ -75,9 +81,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(tc::smem_u32(&sh->k_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->k_empty[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->v_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->v_empty[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->v_ready[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->v_empty[i]), 2);  // the product, and the clearing warp
     }
+    for (int i = 0; i < kReady; ++i) tc::mbar_init(tc::smem_u32(&sh->v_ready[i]), 1);
     tc::mbar_init(tc::smem_u32(&sh->drain), 1);
     tc::fence_mbar_init();
     sh->abort = 0, sh->mma_pending = 0, sh->range.bad = 0, sh->range.n_long = 0;
@@ -173,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kTile, D) | tc::kIdescBMajorMN;
     Ring<C::kKSlots> kr;
     Ring<C::kVSlots> vr;
+    Ring<kReady> ready;
     int seg_i = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
     bool ok = true, any = false;
     Walk walk(sh->range, unit_tokens);
@@ -213,9 +220,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       kr.step();
       any = true;
+      int j0, j1;  // the tiles that need no clearing
+      whole_tiles(a, s, s.u.p1, s.u.p0, j0, j1);
       for (int j = 0; ok && j < s.n; ++j) {
         const bool more = j + 1 < s.n;
-        ok = wait(&sh->v_ready[vr.slot], vr.phase) && wait(&sh->v_full[vr.slot], vr.phase) && (!more || wait(&sh->k_full[kr.slot], kr.phase));
+        ok = wait(&sh->v_full[vr.slot], vr.phase) && (!more || wait(&sh->k_full[kr.slot], kr.phase));
+        if (ok && (j < j0 || j >= j1)) {
+          ok = wait(&sh->v_ready[ready.slot], ready.phase);
+          ready.step();
+        }
         if (!ok) break;
         for (int st = 0; ok && st < n_st; ++st) {
           const uint32_t p_phase = p_use[st]++ & 1;
@@ -252,17 +265,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 10) {
     // ------------------------------------------- V tiles: unseen slots cleared, then ready for the MMA
     Ring<C::kVSlots> ring;
+    Ring<kReady> ready;
     int seg_i = 0;
     bool ok = true;
     Walk walk(sh->range, unit_tokens);
     Segment s = {};
     while (ok && walk.next(a, sh->range, s)) {
-      for (int j = 0; j < s.n; ++j) {
+      int j0, j1;
+      whole_tiles(a, s, s.u.p1, s.u.p0, j0, j1);
+      for (int j = 0; j < s.n; ++j, ring.step()) {
         ok = wait(&sh->v_full[ring.slot], ring.phase);
         if (!ok) break;
-        clear_unseen<C::kHalves>(a, s, j, sV + ring.slot * C::kTileBytes, lane);
-        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->v_ready[ring.slot]));
-        ring.step();
+        if (j < j0 || j >= j1) {
+          clear_unseen<C::kHalves>(a, s, j, sV + ring.slot * C::kTileBytes, lane);
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->v_ready[ready.slot]));
+          ready.step();
+        }
+        // every tile, so that the ring never turns more than once past this warp (a parity tells no more)
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->v_empty[ring.slot]));
       }
       ++seg_i;
     }
@@ -289,11 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p = s.u.p0 + tok0 + tok;  // this row's position; the tile's: q0 .. q1
         const int q0 = s.u.p0 + tok0, q1 = min(q0 + a.tokens - 1, s.u.p1);
         const bool valid = row < tile_rows && tok0 + tok < s.ntok;
-        // tiles j_in0 .. j_in1 - 1 of the segment are seen whole by every row of the tile
         const int per_tile = kTile >> a.block_shift;
-        int in0 = s.u.sb, in1 = ((q0 + 1) >> a.block_shift) + s.u.sb - s.u.wb0;  // in blocks of the unit
-        if (a.window) in0 = max(in0, ((q1 - a.window + (1 << a.block_shift)) >> a.block_shift) + s.u.sb - s.u.wb0);
-        const int j_in0 = (in0 + per_tile - 1) / per_tile - s.tile0, j_in1 = in1 / per_tile - s.tile0;
+        int j_in0, j_in1;  // the KV tiles that every row of this Q tile sees whole
+        whole_tiles(a, s, q0, q1, j_in0, j_in1);
         float m = kUnset, l = 0.f;  // the reference (log2 units) and the sum
         for (int j = 0; j < s.n; ++j) {
           ok = wait(&sh->s_full[st], s_use++ & 1);
@@ -405,50 +423,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t prow = (int64_t(2) * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * (2 * kTile) + st * kTile + row;
         const bool partial = s.n < s.u.ntiles;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        // whole rows go through the unit's Q tile (its last S is done), so that lanes store 16-byte pieces in
-        // a row; pieces are rotated over the banks
-        constexpr int kPieces = D / 8;
-        uint4* stage = reinterpret_cast<uint4*>(sQ + st * C::kTileBytes);
+        float o[D];
+        tc::tmem_ld<D>(t_o, o);
+        tc::tmem_ld_wait();
+        tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
+        // 32-byte stores: a thread's row is D lanes in a row, other lanes' rows lie elsewhere
+        if (valid && partial) {
 #pragma unroll
-        for (int i = 0; i < D; i += 32) {
-          float v[32];
-          tc::tmem_ld<32>(t_o + i, v);
-          tc::tmem_ld_wait();
-          if (partial) {
-            float4* dst = reinterpret_cast<float4*>(a.partial + prow * D + i);
-            if (valid) {
+          for (int i = 0; i < D; i += 8) {
+            float v[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                dst[k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[8 * k + 2 * z] * inv, v[8 * k + 2 * z + 1] * inv);
-                w[z] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-              stage[row * kPieces + ((i / 8 + k) ^ (row & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int k = 0; k < 8; ++k) v[k] = o[i + k] * inv;
+            store_32b(a.partial + prow * D + i, reinterpret_cast<const uint32_t*>(v));
           }
-        }
-        if (!partial) {
-          __syncwarp();  // a warp stores its own 32 rows
-          constexpr int kLanes = kPieces, kAtOnce = 32 / kLanes;  // lanes per row, rows per store
-          const int piece = lane % kLanes;
-          int r = (warp & 3) * 32 + lane / kLanes, r_tok = r / a.g, r_head = r - r_tok * a.g;
-          __nv_bfloat16* dst = a.out + (int64_t(s.row0 + tok0 + r_tok) * a.Hq + s.h * a.g + r_head) * D + piece * 8;
-          const int64_t wrap = int64_t(a.Hq - a.g) * D;  // from a token's last head to the next token's first
-          const int r_end = min(tile_rows, (s.ntok - tok0) * a.g);
-#pragma unroll 4
-          for (int i = 0; i < 32; i += kAtOnce, r += kAtOnce) {
-            if (r < r_end) *reinterpret_cast<uint4*>(dst) = stage[r * kPieces + (piece ^ (r & 7))];
-            dst += kAtOnce * D;
-            for (r_head += kAtOnce; r_head >= a.g; r_head -= a.g) dst += wrap;
+        } else if (valid) {
+#pragma unroll
+          for (int i = 0; i < D; i += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[i + 2 * k] * inv, o[i + 2 * k + 1] * inv);
+              w[k] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            store_32b(a.out + oat * D + i, w);
           }
-          tc::fence_proxy_async_smem();  // before the next TMA into this tile
         }
         if (valid) {
           const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
@@ -457,9 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           else if (a.lse)
             a.lse[oat] = lse2 * kLn2;
         }
-        tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->q_empty[st]));
       }
       if (!ok) {
         sh->abort = 1;

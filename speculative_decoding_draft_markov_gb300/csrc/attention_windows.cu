@@ -43,7 +43,7 @@ template <int R>
 struct Shared {
   static constexpr int kSets = Split<R>::kSets, kRowGroups = Split<R>::kRowGroups, kRows = Split<R>::kRows;
   uint64_t q_full[2], q_empty[2], k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
-  uint64_t v_ready[kMaxSlots];
+  uint64_t v_ready[kReady];
   uint64_t s_full[2], p_full[2], p_empty[2];
   uint64_t o_full[kSets], o_read[kSets];           // a set's O^T is complete; has been read by all that do
   uint64_t group[kGroups];                          // the four warps of a group
@@ -152,9 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(tc::smem_u32(&sh->k_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->k_empty[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->v_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->v_empty[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh->v_ready[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->v_empty[i]), 2);  // the product, and the clearing warp
     }
+    for (int i = 0; i < kReady; ++i) tc::mbar_init(tc::smem_u32(&sh->v_ready[i]), 1);
     for (int i = 0; i < kSets; ++i) {
       tc::mbar_init(tc::smem_u32(&sh->o_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh->o_read[i]), 4 * kGroups);
@@ -306,14 +306,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dv = tc::sdesc_mnmajor<128>(tc::smem_u32(sV), kTile * 128);
     const uint64_t dp = tc::sdesc_mnmajor<C::kPPitch>(tc::smem_u32(sP), kTile * 128);
     Ring<C::kVSlots> ring;
-    int t = 0, o_uses[kSets] = {};
+    int t = 0, o_uses[kSets] = {}, j0 = 0, j1 = 0;
+    Ring<kReady> ready;
     bool ok = true;
     Cursor cur(sh->range, a.tokens);
     for (; cur.next(a, sh->range); ++t) {
+      if (cur.first()) whole_tiles(a, cur.s, cur.s.u.p1, cur.s.u.p0, j0, j1);
       const int set = kSets == 2 ? t & 1 : 0;
       const bool first = cur.j < kSets, last = cur.j + kSets >= cur.s.n;  // of the set's tiles of the unit
-      ok = wait(&sh->v_ready[ring.slot], ring.phase) && wait(&sh->v_full[ring.slot], ring.phase) &&
-           wait(&sh->p_full[t & 1], (t >> 1) & 1);
+      ok = wait(&sh->v_full[ring.slot], ring.phase);
+      if (ok && (cur.j < j0 || cur.j >= j1)) {
+        ok = wait(&sh->v_ready[ready.slot], ready.phase);
+        ready.step();
+      }
+      ok = ok && wait(&sh->p_full[t & 1], (t >> 1) & 1);
       // the set's O^T of the unit before has been read
       if (ok && first) ok = wait(&sh->o_read[set], ((kSets == 2 && set ? o_uses[kSets - 1]++ : o_uses[0]++) & 1) ^ 1);
       if (!ok) break;
@@ -339,15 +345,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kClearWarp) {
     // ------------------------------------------- V tiles: unseen slots cleared, then ready for O^T
     Ring<C::kVSlots> ring;
-    int t = 0;
+    Ring<kReady> ready;
+    int t = 0, j0 = 0, j1 = 0;
     bool ok = true;
     Cursor cur(sh->range, a.tokens);
-    for (; cur.next(a, sh->range); ++t) {
+    for (; cur.next(a, sh->range); ++t, ring.step()) {
+      if (cur.first()) whole_tiles(a, cur.s, cur.s.u.p1, cur.s.u.p0, j0, j1);
       ok = wait(&sh->v_full[ring.slot], ring.phase);
       if (!ok) break;
-      clear_unseen<C::kHalves>(a, cur.s, cur.j, sV + ring.slot * C::kSlotBytes, lane);
-      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->v_ready[ring.slot]));
-      ring.step();
+      if (cur.j < j0 || cur.j >= j1) {
+        clear_unseen<C::kHalves>(a, cur.s, cur.j, sV + ring.slot * C::kSlotBytes, lane);
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->v_ready[ready.slot]));
+        ready.step();
+      }
+      // every tile, so that the ring never turns more than once past this warp (a parity tells no more)
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->v_empty[ring.slot]));
     }
     if (!ok) {
       sh->abort = 1;
@@ -388,12 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (both || (kSets == 2 && (t0 & 1) == 1)) ++n_unit[1];
       t0 += s.n;
       if (begin >= s.n) continue;  // a single tile, the other set's
-      // tiles j_in0 .. j_in1 - 1 of the segment are seen whole by every row
       const int per_tile = kTile >> a.block_shift;
-      int in0 = s.u.sb, in1 = (s.u.p0 + 1) >> a.block_shift;  // blocks of the unit: past the sinks; ending by p0
-      if (a.window) in0 = max(in0, ((s.u.p1 - a.window + 1 + (1 << a.block_shift) - 1) >> a.block_shift) - s.u.wb0 + s.u.sb);
-      in1 += s.u.sb - s.u.wb0;
-      const int j_in0 = (in0 + per_tile - 1) / per_tile - s.tile0, j_in1 = in1 / per_tile - s.tile0;
+      int j_in0, j_in1;  // the tiles that every row sees whole
+      whole_tiles(a, s, s.u.p0, s.u.p1, j_in0, j_in1);
       float l[RW];  // this slot's share of the rows' sums
 #pragma unroll
       for (int i = 0; i < RW; ++i) l[i] = 0.f;
