@@ -3,9 +3,9 @@
 //
 // A unit of work is one KV head of one request and a run of its rows: the rows' query heads of that KV head
 // are stacked into a tile of (token, head) rows, so that K and V are read once for all of them.  The
-// work of a call, counted in KV tiles of 128 slots, is cut into one equal range per CTA (one CTA per SM),
-// whatever the lengths are; a unit that crosses a cut leaves partial rows in the workspace, which a small
-// kernel joins in a fixed order.
+// work of a call, counted in KV tiles of 128 slots, is cut into equal ranges, one or two per CTA (one CTA per
+// SM), whatever the lengths are; a unit that crosses a cut leaves partial rows in the workspace, which a
+// small kernel joins in a fixed order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,26 +29,18 @@ struct AttnArgs {
   __nv_bfloat16* out;
   float* lse;
   uint32_t *status, *diag;
-  int4* info;       // per CTA: which partials it left (Info)
-  float* partial;   // [2 grid][rows of a unit][D] partial outputs, normalised
-  float* plse;      // [2 grid][rows of a unit] their log2-sum-exp
+  int4* info;       // per range: which partials it left
+  float* partial;   // [2 ranges][rows of a unit][D] partial outputs, normalised
+  float* plse;      // [2 ranges][rows of a unit] their log2-sum-exp
   uint64_t timeout_ns;
   float c2;         // scale * log2(e), never 0
   int max_pages, n_pages, page_shift, block_shift, bs, rows, Hq, Hkv, g, tokens, window, n_sink;
 };
 
-// What a CTA left for the join, as an int4: x = flags, then the unit that it began and did not finish.
+// What a range v left for the join, as an int4: x = flags, then the unit that it began and did not finish.
 enum : int { kTailUsed = 1, kTailEnds = 2, kHeadUsed = 4 };
-// tail: the range began inside a unit (partial slot 2 cta); head: it ends inside one that it began (slot
-// 2 cta + 1).  y = packed row of the unit's first token, z = its tokens, w = its KV head.
-
-// The work of a call and where the range of this CTA begins.
-struct Range {
-  uint32_t pre[DSPARK_MAX_BS + 1];  // work before each request, in KV tiles
-  int bad, n_long;
-  int r, h, t, tile;
-  uint32_t count;
-};
+// tail: the range began inside a unit (partial slot 2 v); head: it ends inside one that it began (slot
+// 2 v + 1).  y = packed row of the unit's first token, z = its tokens, w = its KV head.
 
 // The KV tiles of one unit: its rows sit at positions p0 .. p1 and see, as a whole, the sinks and
 // lo .. p1.  Its blocks (pages, or 128-slot pieces of larger pages) in order: sink blocks 0 .. sb - 1,
@@ -80,21 +72,30 @@ struct Segment {
   int tile0, n;             // KV tiles tile0 .. tile0 + n - 1 of the unit
 };
 
-// Walks a CTA's range; every role walks the same one.
+// Where a range begins: request (its first packed row, rows and tokens cached before), KV head, unit, KV tile.
+struct Start {
+  int r, h, t, tile, row, n, c;
+  uint32_t count;  // KV tiles
+};
+
+// Walks a range; every role of a pipeline walks the same one.
 struct Walk {
   int r, h, t, tile, unit_tokens;
   uint32_t left;
   int loaded, row, n, c;
-  __device__ Walk(const Range& g, int ut)
-      : r(g.r), h(g.h), t(g.t), tile(g.tile), unit_tokens(ut), left(g.count), loaded(-1), row(0), n(0), c(0) {}
-  __device__ __forceinline__ bool next(const AttnArgs& a, const Range& g, Segment& s) {
+  __device__ Walk(const Start& g, int ut)
+      : r(g.r), h(g.h), t(g.t), tile(g.tile), unit_tokens(ut), left(g.count), loaded(g.r), row(g.row), n(g.n), c(g.c) {}
+  __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
     if (left == 0) return false;
-    while (g.pre[r + 1] == g.pre[r]) ++r;  // requests with nothing to do
-    if (loaded != r) {
+    while (loaded != r) {  // the next request with something to do
+      if (r >= a.bs) return false;
       row = a.cu[r];
       n = a.cu[r + 1] - row;
       c = a.ctx[r];
-      loaded = r;
+      if (n > 0 && c >= 0 && int64_t(c) + n <= a.cache_limit)
+        loaded = r;
+      else
+        ++r;
     }
     s.u = unit_geom(a, c, n, t, unit_tokens);
     s.r = r, s.h = h, s.row0 = row + t * unit_tokens, s.ntok = s.u.p1 - s.u.p0 + 1;
@@ -136,98 +137,101 @@ struct Waiter {
 };
 
 
-// The range of this CTA: the call's KV tiles, counted over (request, KV head, unit), are cut into one
-// equal range per CTA.  The whole block calls it (g.bad and g.n_long zeroed before); long_req: scratch
-// of DSPARK_MAX_BS bytes.
-__device__ __forceinline__ void plan_range(const AttnArgs& a, Range& g, uint8_t* long_req, int unit_tokens) {
+// The call's KV tiles, counted over (request, KV head, unit), are cut into kSets * gridDim.x ranges that differ
+// by one tile at most; this CTA has ranges blockIdx.x + set * gridDim.x.
+struct PlanScratch {
+  long long warp_total[DSPARK_MAX_BS / 32];
+  uint32_t long_cost[DSPARK_MAX_BS];
+  uint8_t long_req[DSPARK_MAX_BS];
+  int n_long, bad;
+};
+// The whole block calls it, after one thread has cleared n_long, bad and the starts' counts and a
+// __syncthreads; the starts are there after the next one.
+template <int kSets>
+__device__ __forceinline__ void plan_ranges(const AttnArgs& a, Start* start, PlanScratch& p, int unit_tokens) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int row = 0, n = 0, c = 0;
+  uint32_t cost = 0;  // KV tiles of one KV head
+  bool is_long = false;
   if (tid < a.bs) {
-    const int r0 = a.cu[tid], r1 = a.cu[tid + 1], c = a.ctx[tid];
-    uint32_t cost = 0;
-    if (r0 < 0 || r1 < r0 || r1 > a.rows) {
-      g.bad = 1;
-    } else if (r1 > r0) {
-      const int n = r1 - r0;
+    row = a.cu[tid], n = a.cu[tid + 1] - row, c = a.ctx[tid];
+    if (row < 0 || n < 0 || row + n > a.rows) {
+      p.bad = 1;
+    } else if (n > 0) {
       if (c < 0 || int64_t(c) + n > a.cache_limit) {
         if (blockIdx.x == 0) set_status(a.status, DSPARK_EINVAL);
+      } else if (n > 4 * unit_tokens) {  // many units: summed by the whole block below
+        is_long = true;
+        p.long_cost[tid] = 0;
+        p.long_req[atomicAdd(&p.n_long, 1)] = uint8_t(tid);
       } else {
-        const int nt = (n + unit_tokens - 1) / unit_tokens;
-        if (nt > 4)  // many units: summed by the whole block below
-          long_req[atomicAdd(&g.n_long, 1)] = uint8_t(tid);
-        else
-          for (int t = 0; t < nt; ++t) cost += unit_geom(a, c, n, t, unit_tokens).ntiles;
+        for (int t = 0; t * unit_tokens < n; ++t) cost += unit_geom(a, c, n, t, unit_tokens).ntiles;
       }
     }
-    g.pre[tid + 1] = cost;
-  }
-  if (tid == 0) g.pre[0] = 0;
-  __syncthreads();
-  for (int i = 0; i < g.n_long; ++i) {
-    const int r = long_req[i], n = a.cu[r + 1] - a.cu[r], c = a.ctx[r];
-    uint32_t part = 0;
-    for (int t = tid; t * unit_tokens < n; t += int(blockDim.x)) part += unit_geom(a, c, n, t, unit_tokens).ntiles;
-    part = __reduce_add_sync(~0u, part);
-    if (lane == 0) atomicAdd(&g.pre[r + 1], part);
   }
   __syncthreads();
-  if (warp == 0) {
-    constexpr int kPer = DSPARK_MAX_BS / 32;
-    long long x[kPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = lane * kPer + i;
-      sum += r < a.bs && !g.bad ? static_cast<long long>(g.pre[r + 1]) * a.Hkv : 0;
-      x[i] = sum;
+  if (p.n_long > 0) {
+    for (int i = 0; i < p.n_long; ++i) {
+      const int r = p.long_req[i], rn = a.cu[r + 1] - a.cu[r], rc = a.ctx[r];
+      uint32_t part = 0;
+      for (int t = tid; t * unit_tokens < rn; t += int(blockDim.x)) part += unit_geom(a, rc, rn, t, unit_tokens).ntiles;
+      part = __reduce_add_sync(~0u, part);
+      if (lane == 0) atomicAdd(&p.long_cost[r], part);
     }
-    long long before = sum;
+    __syncthreads();
+    if (is_long) cost = p.long_cost[tid];
+  }
+  const long long mine = p.bad ? 0 : static_cast<long long>(cost) * a.Hkv;
+  long long incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(~0u, before, o);
-      if (lane >= o) before += y;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31 && warp < DSPARK_MAX_BS / 32) p.warp_total[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < DSPARK_MAX_BS / 32; ++i) {
+    if (i < warp) before += p.warp_total[i];
+    total += p.warp_total[i];
+  }
+  const bool too_much = total >> 31 != 0;  // counted in 32 bits
+  if (tid == 0 && blockIdx.x == 0 && (p.bad || too_much)) set_status(a.status, DSPARK_EINVAL);
+  const uint32_t all = too_much ? 0u : uint32_t(total), n_ranges = kSets * gridDim.x;
+  const uint32_t each = all / n_ranges, extra = all - each * n_ranges, first = uint32_t(before + incl - mine);
+#pragma unroll
+  for (int set = 0; set < kSets; ++set) {
+    const uint32_t v = blockIdx.x + set * gridDim.x, w0 = each * v + min(v, extra), count = each + (v < extra ? 1u : 0u);
+    if (count > 0 && w0 >= first && w0 - first < uint32_t(mine)) {  // this thread's request
+      const uint32_t h = (w0 - first) / cost;
+      start[set] = Start{tid, int(h), 0, int(w0 - first - h * cost), row, n, c, count};
     }
-    const bool too_much = __shfl_sync(~0u, before, 31) >> 32 != 0;  // counted in 32 bits below
-    before -= sum;
-    __syncwarp();
+  }
+  __syncthreads();
+  if (warp < kSets && start[warp].count > 0 && start[warp].n > unit_tokens) {  // the unit that holds that tile of the head
+    Start& g = start[warp];
+    int rem = g.tile, t = 0;
+    for (int base = 0;; base += 32) {
+      const int tiles = (base + lane) * unit_tokens < g.n ? unit_geom(a, g.c, g.n, base + lane, unit_tokens).ntiles : 0;
+      int sum = tiles;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane * kPer + i < a.bs) g.pre[lane * kPer + i + 1] = too_much ? 0u : uint32_t(before + x[i]);
-    __syncwarp();
-    const long long total = g.pre[a.bs];
-    const long long w0 = total * blockIdx.x / gridDim.x, w1 = total * (blockIdx.x + 1) / gridDim.x;
-    int r = 0;
-    for (int i = lane; i - lane < a.bs; i += 32) r += __popc(__ballot_sync(~0u, i < a.bs && g.pre[i + 1] <= w0));
-    int h = 0, t = 0, tile = 0;
-    if (w1 > w0) {
-      const long long per_head = (g.pre[r + 1] - g.pre[r]) / a.Hkv;
-      long long rem = w0 - g.pre[r];
-      h = int(rem / per_head);
-      rem -= h * per_head;
-      const int n = a.cu[r + 1] - a.cu[r], c = a.ctx[r], nt = (n + unit_tokens - 1) / unit_tokens;
-      for (int base = 0;; base += 32) {  // the unit that holds tile `rem` of this head
-        const int mine = base + lane < nt ? unit_geom(a, c, n, base + lane, unit_tokens).ntiles : 0;
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(~0u, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const uint32_t past = __ballot_sync(~0u, incl > rem);
-        if (past != 0 || base + 32 >= nt) {
-          const int at = past ? __ffs(past) - 1 : 31;
-          t = base + at;
-          tile = int(rem) - __shfl_sync(~0u, incl - mine, at);
-          break;
-        }
-        rem -= __shfl_sync(~0u, incl, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += y;
       }
+      const uint32_t past = __ballot_sync(~0u, sum > rem);
+      if (past != 0 || (base + 32) * unit_tokens >= g.n) {
+        const int at = past ? __ffs(past) - 1 : 31;
+        t = base + at;
+        rem -= __shfl_sync(~0u, sum - tiles, at);
+        break;
+      }
+      rem -= __shfl_sync(~0u, sum, 31);
     }
-    if (lane == 0) {
-      g.r = r, g.h = h, g.t = t, g.tile = tile;
-      g.count = uint32_t(w1 - w0);
-      if ((g.bad || too_much) && blockIdx.x == 0) set_status(a.status, DSPARK_EINVAL);
-    }
+    __syncwarp();
+    if (lane == 0) g.t = t, g.tile = rem;
   }
-  __syncthreads();
 }
 
 // One tile of a unit as the TMA warp loads it: lane i's block of the tile.
@@ -296,12 +300,10 @@ __device__ __forceinline__ void clear_unseen(const AttnArgs& a, const Segment& s
   tc::fence_proxy_async_smem();
   __syncwarp();
 }
-// The clearing warp and the warp that issues the product with V agree on the tiles that need it; their
-// barriers are counted over those tiles alone (more barriers than V slots, so that neither can lap the other).
-constexpr int kReady = 8;
-
 }  // namespace attn
 
+// Ranges per CTA of the short windows' kernel (partial rows in the workspace are per range).
+int attention_window_sets(int D, int unit_rows);
 cudaError_t launch_attention_prompts(int D, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                      const attn::AttnArgs& a, int n_cta, cudaStream_t s);
 cudaError_t launch_attention_windows(int D, int unit_rows, const CUtensorMap& q, const CUtensorMap& k,

@@ -30,13 +30,16 @@ struct Cfg {
   static constexpr int kKSlots = D == 128 ? 2 : 5, kVSlots = D == 128 ? 3 : 5;  // rings: 160 KB either way
 };
 
+// The clearing warp and the MMA warp agree on the tiles that need clearing; their barriers are counted over those
+// tiles alone (more barriers than V slots, so that neither can lap the other).
+constexpr int kReady = 8;
+
 struct Shared {
   uint64_t q_full[2], q_empty[2], k_full[5], k_empty[5], v_full[5], v_empty[5], v_ready[kReady], s_full[2], p_full[2][2], o_full[2], drain;
   uint32_t tmem_base;
   volatile int abort;
   int mma_pending;
-  Range range;
-  uint8_t long_req[DSPARK_MAX_BS];
+  Start start;
 };
 
 // Bits k = 0 .. 7 with lo <= k <= hi.
@@ -66,6 +69,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same for the warp, and known to be
   const int unit_tokens = 2 * a.tokens, tile_rows = a.tokens * a.g;
   const int active = (tile_rows + 31) / 32;  // softmax warps of a tile that hold rows
+  PlanScratch& plan = *reinterpret_cast<PlanScratch*>(sK);  // before the first load
   const Waiter wait{&sh->abort, a.timeout_ns};
 
   if (tid == 0) {
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kReady; ++i) tc::mbar_init(tc::smem_u32(&sh->v_ready[i]), 1);
     tc::mbar_init(tc::smem_u32(&sh->drain), 1);
     tc::fence_mbar_init();
-    sh->abort = 0, sh->mma_pending = 0, sh->range.bad = 0, sh->range.n_long = 0;
+    sh->abort = 0, sh->mma_pending = 0, sh->start.count = 0, plan.bad = 0, plan.n_long = 0;
     tc::prefetch_tensormap(&map_q);
     tc::prefetch_tensormap(&map_k);
     tc::prefetch_tensormap(&map_v);
@@ -97,7 +101,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   pdl_enter();
-  plan_range(a, sh->range, sh->long_req, unit_tokens);
+  plan_ranges<1>(a, &sh->start, plan, unit_tokens);
+  tc::fence_proxy_async_smem();  // the plan's scratch lies where TMA writes
   __syncthreads();
   const uint32_t tmem = sh->tmem_base;
 
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seg_i = 0, flags = 0, n_k = 0, n_v = 0, q_use[2] = {0, 0};
     int4 info = make_int4(0, 0, 0, 0);
     bool ok = true;
-    Walk walk(sh->range, unit_tokens);
+    Walk walk(sh->start, unit_tokens);
     Segment s = {};
     auto put_k = [&](const TileLoad& t) {
       if (!wait(&sh->k_empty[kr.slot], kr.phase ^ 1)) return false;
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++q_use[b];
       return true;
     };
-    while (ok && walk.next(a, sh->range, s)) {
+    while (ok && walk.next(a, s)) {
       if (s.tile0 > 0) flags |= kTailUsed | (s.tile0 + s.n == s.u.ntiles ? kTailEnds : 0);
       if (s.tile0 == 0 && s.n < s.u.ntiles) flags |= kHeadUsed, info = make_int4(0, s.row0, s.ntok, s.h);
       TileLoad t0 = tile_load(a, s, 0, lane), t1 = t0;
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kReady> ready;
     int seg_i = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
     bool ok = true, any = false;
-    Walk walk(sh->range, unit_tokens);
+    Walk walk(sh->start, unit_tokens);
     Segment s = {};
     const uint64_t dq = tc::sdesc_kmajor_sw128(tc::smem_u32(sQ)), dk = tc::sdesc_kmajor_sw128(tc::smem_u32(sK));
     const uint64_t dv = tc::sdesc_mnmajor(tc::smem_u32(sV), C::kHalfBytes);
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_bf16_ts(tmem + 2 * kTile + st * D, tmem + st * kTile + 32 * hf + 8 * i,
                         v + uint32_t(hf * (kTile / 2 * 128 >> 4)) + ((i * 2048) >> 4), idesc_pv, add || i != 0);
     };
-    while (ok && walk.next(a, sh->range, s)) {
+    while (ok && walk.next(a, s)) {
       const int n_st = s.ntok > a.tokens ? 2 : 1;
       ok = wait(&sh->k_full[kr.slot], kr.phase) && wait(&sh->q_full[0], q_use[0]++ & 1) && (n_st == 1 || wait(&sh->q_full[1], q_use[1]++ & 1));
       if (!ok) break;
@@ -268,9 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kReady> ready;
     int seg_i = 0;
     bool ok = true;
-    Walk walk(sh->range, unit_tokens);
+    Walk walk(sh->start, unit_tokens);
     Segment s = {};
-    while (ok && walk.next(a, sh->range, s)) {
+    while (ok && walk.next(a, s)) {
       int j0, j1;
       whole_tiles(a, s, s.u.p1, s.u.p0, j0, j1);
       for (int j = 0; j < s.n; ++j, ring.step()) {
@@ -301,9 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float c2 = a.c2;
       int seg_i = 0, s_use = 0, o_use = 0;
       bool ok = true;
-      Walk walk(sh->range, unit_tokens);
+      Walk walk(sh->start, unit_tokens);
       Segment s = {};
-      while (ok && walk.next(a, sh->range, s)) {
+      while (ok && walk.next(a, s)) {
         ++seg_i;
         if (tok0 >= s.ntok) continue;  // the unit has no second tile
         const int p = s.u.p0 + tok0 + tok;  // this row's position; the tile's: q0 .. q1

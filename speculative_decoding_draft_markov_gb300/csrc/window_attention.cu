@@ -9,11 +9,11 @@ namespace {
 
 using namespace attn;
 
-// Joins the partial rows of the units that a cut between CTAs runs through: the block of CTA c takes the
-// unit that c began and did not finish, in the order of its KV tiles.  One warp per row:
+// Joins the partial rows of the units that a cut between ranges runs through: block v takes the unit that
+// range v began and did not finish, in the order of its KV tiles.  One warp per row:
 //     out = sum_i 2^(lse_i - M) out_i / sum_i 2^(lse_i - M),   M = max_i lse_i
 template <int D>
-__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int n_cta, int unit_rows) {
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int n_ranges, int unit_rows) {
   constexpr int E = D / 32;
   pdl_enter();
   const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5), c = blockIdx.x;
@@ -21,18 +21,18 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
   if (!(info.x & kHeadUsed)) return;
   const int tok = (row / kTile) * a.tokens + (row % kTile) / a.g, hh = (row % kTile) % a.g;
   if (row % kTile >= a.tokens * a.g || tok >= info.z) return;
-  // the CTAs after c that worked on the unit: up to the first that finished it
+  // the ranges after c that worked on the unit: up to the first that finished it
   int last = c;
-  for (int base = c + 1; base < n_cta; base += 32) {
-    const int fl = base + lane < n_cta ? a.info[base + lane].x : 0;
+  for (int base = c + 1; base < n_ranges; base += 32) {
+    const int fl = base + lane < n_ranges ? a.info[base + lane].x : 0;
     const uint32_t ends = __ballot_sync(~0u, fl & kTailEnds);
     if (ends) {
       last = base + __ffs(ends) - 1;
       break;
     }
-    last = min(base + 31, n_cta - 1);
+    last = min(base + 31, n_ranges - 1);
   }
-  // part i: the head of c, then the tails of c + 1 ..; CTAs without work in between have none
+  // part i: the head of c, then the tails of c + 1 ..
   auto part_row = [&](int i) { return int64_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * unit_rows + row; };
   auto part_lse = [&](int i) {
     if (c + i > last || (i > 0 && !(a.info[c + i].x & kTailUsed))) return -INFINITY;
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
 #pragma unroll 4
     for (int i = 0; i < min(32, n - base); ++i) {
       const float w = __shfl_sync(~0u, w_mine, i);
-      if (w == 0.f) continue;  // nothing seen there (and nothing written by a CTA without work)
+      if (w == 0.f) continue;  // nothing seen there
       sum += w;
       const float* src = a.partial + part_row(base + i) * D + lane * E;
 #pragma unroll
@@ -71,16 +71,16 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
   if (a.lse && lane == 0) a.lse[at] = (ref + log2f(sum)) * kLn2;
 }
 
-// Workspace: status block | Info of each CTA | partial rows | their log-sum-exps.
+// Workspace: status block | what each range left | partial rows | their log-sum-exps.
 struct AttnWs {
   size_t info, partial, plse, total;
 };
-AttnWs attn_ws(int D, int unit_rows, int n_cta) {
+AttnWs attn_ws(int D, int unit_rows, int n_ranges) {
   AttnWs w;
   w.info = 256;
-  w.partial = w.info + align256(n_cta * sizeof(int4));
-  w.plse = w.partial + align256(size_t(2) * n_cta * unit_rows * D * sizeof(float));
-  w.total = w.plse + align256(size_t(2) * n_cta * unit_rows * sizeof(float));
+  w.partial = w.info + align256(n_ranges * sizeof(int4));
+  w.plse = w.partial + align256(size_t(2) * n_ranges * unit_rows * D * sizeof(float));
+  w.total = w.plse + align256(size_t(2) * n_ranges * unit_rows * sizeof(float));
   return w;
 }
 
@@ -106,7 +106,10 @@ bool encode_q(CUtensorMap* map, const void* base, int rows, int Hq, int D, int64
 }  // namespace
 
 size_t window_attention_ws_bytes(int Hq, int Hkv, int D) {
-  return attn_ws(D, 2 * kTile, tch::sm_count()).total;  // either tiling
+  size_t most = attn_ws(D, 2 * kTile, tch::sm_count()).total;  // any tiling
+  for (int rows = 16; rows <= kTile; rows *= 2)
+    most = std::max(most, attn_ws(D, rows, attention_window_sets(D, rows) * tch::sm_count()).total);
+  return most;
 }
 
 cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -124,7 +127,8 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   a.cache_limit = std::min(int64_t(max_pages) << page_shift, int64_t(1) << 30);  // positions: well inside 32 bits
   a.page_table = page_table, a.cu = cu, a.ctx = ctx, a.out = static_cast<__nv_bfloat16*>(out), a.lse = lse;
   char* w = static_cast<char*>(ws);
-  const AttnWs L = attn_ws(D, unit_rows, n_cta);
+  const int n_ranges = n_cta * (prompts ? 1 : attention_window_sets(D, unit_rows));
+  const AttnWs L = attn_ws(D, unit_rows, n_ranges);
   a.status = reinterpret_cast<uint32_t*>(w), a.diag = reinterpret_cast<uint32_t*>(w + 16);
   a.info = reinterpret_cast<int4*>(w + L.info);
   a.partial = reinterpret_cast<float*>(w + L.partial), a.plse = reinterpret_cast<float*>(w + L.plse);
@@ -145,9 +149,9 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   const cudaError_t e = prompts ? launch_attention_prompts(D, mq, mk, mv, a, n_cta, s)
                                 : launch_attention_windows(D, unit_rows, mq, mk, mv, a, n_cta, s);
   if (e != cudaSuccess) return e;
-  const dim3 grid(n_cta, ((prompts ? kTile : 0) + a.tokens * g + 7) / 8);
-  return D == 64 ? launch_pdl(attention_join_kernel<64>, grid, dim3(256), 0, s, a, n_cta, unit_rows)
-                 : launch_pdl(attention_join_kernel<128>, grid, dim3(256), 0, s, a, n_cta, unit_rows);
+  const dim3 grid(n_ranges, ((prompts ? kTile : 0) + a.tokens * g + 7) / 8);
+  return D == 64 ? launch_pdl(attention_join_kernel<64>, grid, dim3(256), 0, s, a, n_ranges, unit_rows)
+                 : launch_pdl(attention_join_kernel<128>, grid, dim3(256), 0, s, a, n_ranges, unit_rows);
 }
 
 }  // namespace dspark
