@@ -367,39 +367,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(&sh->s_full[set][t & 1], (t >> 1) & 1);
         if (!ok) break;
         tc::tc_fence_after();
-        float x[RW];
+        float y[RW];  // the only array beside l: what is needed once more is loaded once more (S is there until P is)
         auto load_scores = [&]() {
-          tc::tmem_ld<RW>(t_s + (t & 1) * R, x);
+          tc::tmem_ld<RW>(t_s + (t & 1) * R, y);
           tc::tmem_ld_wait();
           if (!inside) {
 #pragma unroll
             for (int i = 0; i < RW; ++i)
-              if (row0 + i < from || row0 + i >= to) x[i] = hidden;
+              if (row0 + i < from || row0 + i >= to) y[i] = hidden;
           }
         };
-        load_scores();
-        bool fresh = j == 0;  // a new reference is needed
-        float y[RW];
-        if (j > 0) {
+        auto refer = [&]() {  // scores to exponents; the largest
           float top = -INFINITY;
 #pragma unroll
           for (int i = 0; i < RW; i += 4) {
             const float4 m = *reinterpret_cast<const float4*>(ref + i);
-            unpack_f32x2(fma_f32x2(pack_f32x2(x[i], x[i + 1]), cc, pack_f32x2(-m.x, -m.y)), y[i], y[i + 1]);
-            unpack_f32x2(fma_f32x2(pack_f32x2(x[i + 2], x[i + 3]), cc, pack_f32x2(-m.z, -m.w)), y[i + 2], y[i + 3]);
+            unpack_f32x2(fma_f32x2(pack_f32x2(y[i], y[i + 1]), cc, pack_f32x2(-m.x, -m.y)), y[i], y[i + 1]);
+            unpack_f32x2(fma_f32x2(pack_f32x2(y[i + 2], y[i + 3]), cc, pack_f32x2(-m.z, -m.w)), y[i + 2], y[i + 3]);
             top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
           }
+          return top;
+        };
+        load_scores();
+        bool fresh = j == 0;  // a new reference is needed
+        if (j > 0) {
+          const float top = refer();
           const int at = sync & 1;
           if (__any_sync(~0u, top > kRescaleAt) && lane == 0) sh->need[grp][at] = t + 1;
           ok = meet();
           if (!ok) break;
           fresh = sh->need[grp][at] == t + 1;
-          if (fresh) load_scores();  // once more: S is there until P is
+          if (fresh) load_scores();
         }
         if (fresh) {
           // each row's maximum over the tile's 128 slots, by warp then over the group's warps
 #pragma unroll
-          for (int i = 0; i < RW; ++i) y[i] = x[i] * c2;
+          for (int i = 0; i < RW; ++i) y[i] *= c2;
           const float mine = fold_lanes<RW, true>(y, lane);
           const float old = j == 0 ? kUnset : ref[fold_row];
           sh->warp_max[grp][w4][fold_row] = mine;
@@ -426,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_st<RW>(t_o, y);
             tc::tmem_st_wait();
           }
-#pragma unroll
-          for (int i = 0; i < RW; ++i) y[i] = fmaf(x[i], c2, -ref[i]);
+          load_scores();
+          refer();
         }
         uint32_t pk[RW / 2];
 #pragma unroll
