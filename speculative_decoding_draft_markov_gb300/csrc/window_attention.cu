@@ -12,54 +12,58 @@ using namespace attn;
 // Joins the partial rows of the units that a cut between ranges runs through: block v takes the unit that
 // range v began and did not finish, in the order of its KV tiles.  One warp per row:
 //     out = sum_i 2^(lse_i - M) out_i / sum_i 2^(lse_i - M),   M = max_i lse_i
+// A chain of trips to memory (what the ranges left, the log-sum-exps, the rows), so each step's loads are issued
+// together, eight rows' pieces at a time.
 template <int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int n_ranges, int unit_rows) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kTogether = 8;
   pdl_enter();
   const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5), c = blockIdx.x;
   const int4 info = a.info[c];
+  int flags = c + 1 + lane < n_ranges ? a.info[c + 1 + lane].x : 0;
   if (!(info.x & kHeadUsed)) return;
   const int tok = (row / kTile) * a.tokens + (row % kTile) / a.g, hh = (row % kTile) % a.g;
   if (row % kTile >= a.tokens * a.g || tok >= info.z) return;
-  // the ranges after c that worked on the unit: up to the first that finished it
-  int last = c;
-  for (int base = c + 1; base < n_ranges; base += 32) {
-    const int fl = base + lane < n_ranges ? a.info[base + lane].x : 0;
-    const uint32_t ends = __ballot_sync(~0u, fl & kTailEnds);
-    if (ends) {
-      last = base + __ffs(ends) - 1;
+  // part 0 is the head of c, part i the tail of c + i, up to the first range that finished the unit
+  int n = 0;
+  for (int base = c + 1;; base += 32) {
+    const uint32_t ends = __ballot_sync(~0u, flags & kTailEnds);
+    if (ends || base + 32 >= n_ranges) {
+      n = (ends ? base + __ffs(ends) - 1 : n_ranges - 1) - c + 1;
       break;
     }
-    last = min(base + 31, n_ranges - 1);
+    flags = base + 32 + lane < n_ranges ? a.info[base + 32 + lane].x : 0;
   }
-  // part i: the head of c, then the tails of c + 1 ..
   auto part_row = [&](int i) { return int64_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * unit_rows + row; };
-  auto part_lse = [&](int i) {
-    if (c + i > last || (i > 0 && !(a.info[c + i].x & kTailUsed))) return -INFINITY;
-    return a.plse[part_row(i)];
+  auto part_lse = [&](int i) {  // every range between has worked on the unit and on nothing else
+    return i < n ? a.plse[part_row(i)] : -INFINITY;
   };
-  const int n = last - c + 1;
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, part_lse(i));
-  top = warp_max(top);
-  top = __shfl_sync(~0u, top, 0);
+  const float mine = part_lse(lane);
+  float top = mine;
+  for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, part_lse(i));
+  top = __shfl_sync(~0u, warp_max(top), 0);
   const float ref = top == -INFINITY ? 0.f : top;
   float acc[E], sum = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int base = 0; base < n; base += 32) {
-    const float w_mine = exp2f(part_lse(base + lane) - ref);
-#pragma unroll 4
-    for (int i = 0; i < min(32, n - base); ++i) {
-      const float w = __shfl_sync(~0u, w_mine, i);
-      if (w == 0.f) continue;  // nothing seen there
-      sum += w;
-      const float* src = a.partial + part_row(base + i) * D + lane * E;
+    const float w_mine = exp2f((base == 0 ? mine : part_lse(base + lane)) - ref);  // 0: nothing seen there
+    for (int i0 = 0; i0 < min(32, n - base); i0 += kTogether) {
+      float v[kTogether][E], w[kTogether];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + e);
-        acc[e] += w * v.x;
-        acc[e + 1] += w * v.y;
+      for (int k = 0; k < kTogether; ++k) {
+        w[k] = __shfl_sync(~0u, w_mine, i0 + k);  // beyond the last part: 0, and the last part's row again
+        const float* src = a.partial + part_row(min(base + i0 + k, n - 1)) * D + lane * E;
+        if constexpr (E == 4)
+          *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
+      }
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) {
+        sum += w[k];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = w[k] == 0.f ? acc[e] : fmaf(w[k], v[k][e], acc[e]);
       }
     }
   }
