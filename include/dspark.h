@@ -300,6 +300,8 @@ DSPARK_API int dspark_schedule_pack(const float* surv, int bs, int gamma, const 
  *   acc_len     device [bs] int32 out: accepted draft tokens
  *   ceiling     device [bs] int32 out or NULL: accepted count over the tested positions
  *               (the full-block ceiling in CAP_ACCEPT mode)
+ *   A target logit of -inf (dspark_process_logits) has probability 0: the id is never accepted nor drawn.
+ *   A deciding row of nothing but -inf gives the token -1.
  *   target      device [rows, V] (dtype), rows >= cu_seqlens[bs]
  *   window      device [bs] int32 (ignored in STATIC mode, may be NULL there)
  *   tokens, logit_x, lse, anchor: the draft's outputs / inputs;  U, W1, W2t, r as in S1.

@@ -91,7 +91,9 @@ __device__ __forceinline__ void lse_batch(const uint4 (&cur)[kBatch], int e0, in
   // goes to s4[q & 3] as before, with the scale-and-shift and the adds done two lanes at a time
   // (fma.rn.f32x2 / add.rn.f32x2: each lane rounds exactly as fmaf / + do)
   unsigned long long s01 = pack_f32x2(0.f, 0.f), s23 = pack_f32x2(0.f, 0.f);
-  const unsigned long long cc = pack_f32x2(c2, c2), mm = pack_f32x2(-m2, -m2);
+  // all of the thread's ids masked so far (-inf): terms 2^(-inf - 0) = 0, not 2^(-inf + inf)
+  const float ref = m2 == -INFINITY ? 0.f : m2;
+  const unsigned long long cc = pack_f32x2(c2, c2), mm = pack_f32x2(-ref, -ref);
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
     if (kFull || e0 + u * kRowThreads < ng) {
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) verify_rows_kernel(
     }
     best = block_argmax<kRowThreads>(best, sv, si);
     if (tid == 0) {
-      RowStat o{0.f, 0.f, best.i, 0};
+      RowStat o{0.f, 0.f, best.i == INT_MAX ? -1 : best.i, 0};  // -1: every id is masked
       if (j < n_r - 1 && j < gamma) {
         const int xt = tokens[size_t(r) * gamma + j];
         if (xt < 0 || xt >= V) set_status(status, DSPARK_EINVAL);

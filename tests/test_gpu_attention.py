@@ -298,6 +298,29 @@ def test_attention_device_errors():
     assert call() == B.DSPARK_OK and torch.equal(out, good)
 
 
+@pytest.mark.parametrize("rows,hq", [(1, 4), (8, 4), (16, 8), (60, 4)])
+def test_attention_wait_timeout_is_reported_and_recovers(rows, hq):
+    """With a deadline of 1 ns the kernels' waits run out: they report it, drain their copies and MMAs and
+    return; the next call with the normal deadline is right again, on the same workspace."""
+    c = Cache([rows] * 40, [700] * 40, 2, 64, 32, seed=19)
+    q = torch.randn(40 * rows, 2 * hq, 64, generator=torch.Generator().manual_seed(20)).to(torch.bfloat16).cuda()
+    out, want = torch.zeros_like(q), torch.zeros_like(q)
+    ws = B.alloc_attention_workspace(2 * hq, 2, 64)
+
+    def call(o):
+        B.dspark_window_attention(q, c.k, c.v, c.table, c.cu, c.ctx, rows, 0.125, 300, 4, o, None, ws)
+        return B.dspark_read_device_status(ws)
+
+    assert call(want) == B.DSPARK_OK
+    old = B.dspark_set_wait_timeout_ns(1)
+    try:
+        st = call(out)
+    finally:
+        B.dspark_set_wait_timeout_ns(old)
+    assert st == B.DSPARK_ETIMEOUT, B.dspark_status_string(st)
+    assert call(out) == B.DSPARK_OK and torch.equal(out, want)
+
+
 # ------------------------------------------------------------------------------- append
 
 def _table(max_pos, rot, dtype=np.float32):
