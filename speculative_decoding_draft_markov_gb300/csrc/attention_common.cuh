@@ -127,11 +127,12 @@ struct Ring {
 struct Waiter {
   volatile int* abort;
   uint64_t timeout_ns;
+  bool patient;  // try_wait itself sleeps for a while: with a limit shorter than that, look first
+  __device__ Waiter(volatile int* ab, uint64_t ns) : abort(ab), timeout_ns(ns), patient(ns >= 1000000) {}
   // A whole warp waits; one answer for all lanes (false: given up).
   __device__ __forceinline__ bool operator()(const uint64_t* bar, uint32_t parity) const {
     const uint32_t b = tc::smem_u32(bar);
-    // try_wait itself sleeps for a while: with a limit shorter than that, look first
-    bool ok = timeout_ns >= 1000000 ? tc::mbar_try_wait(b, parity) : tc::mbar_test_wait(b, parity);
+    bool ok = patient ? tc::mbar_try_wait(b, parity) : tc::mbar_test_wait(b, parity);
     if (!ok) {  // the limit holds for each wait by itself: a call over a long cache may take its time
       const long long deadline = tc::deadline_after_ns(timeout_ns);
       while (!ok && !*abort && clock64() <= deadline) ok = tc::mbar_try_wait_suspend(b, parity, 20000u);

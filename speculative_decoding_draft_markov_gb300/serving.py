@@ -1,0 +1,133 @@
+"""The target model's side of a step: the paged cache that takes the packed windows, the rules on the packed
+logits and the token history they read, around step.run_step.
+
+    cache = PagedCache(...); rules = LogitRules(...)
+    run_served_step(inp, buf, sps, forward, cache, rules, ...)
+
+`forward(buf, cache)` is the caller's model: it fills buf.packed from the packed ids, calling cache.attend for
+each layer's attention.  Everything runs on one stream and nothing is read back; pages are handed out on the
+host, from upper bounds of the lengths."""
+from __future__ import annotations
+
+import dataclasses
+from typing import Callable, List, Optional
+
+from . import binding as B
+from . import step as S
+
+
+def rotation_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda"):
+    """cos_sin [max_pos, rot] fp32 of dspark_append_kv: angle of (p, t) = p base^(-2 t / rot)."""
+    import torch
+    half = rot // 2
+    inv = base ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    ang = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
+
+
+class PagedCache:
+    """K and V of every layer in pages [n_pages, Hkv, page_size, D], one page table for all layers.
+
+    ctx_len (device) counts each request's cached tokens; a step's windows are appended behind them and
+    `advance` keeps what the verification accepted.  `bound` (host) is an upper bound of ctx_len."""
+
+    def __init__(self, n_layers: int, n_pages: int, page_size: int, Hq: int, Hkv: int, D: int, bs: int, max_pages: int,
+                 cos_sin, window: int = 0, n_sink: int = 0, interleaved: bool = False, device="cuda"):
+        import torch
+        shape = (n_pages, Hkv, page_size, D)
+        self.k = [torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(n_layers)]
+        self.v = [torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(n_layers)]
+        self.page_size, self.Hq, self.window, self.n_sink = page_size, Hq, window, n_sink
+        self.interleaved, self.cos_sin = interleaved, cos_sin
+        self.page_table = torch.full((bs, max_pages), -1, dtype=torch.int32, device=device)
+        self.ctx_len = torch.zeros(bs, dtype=torch.int32, device=device)
+        self.bound: List[int] = [0] * bs
+        self.pages: List[List[int]] = [[] for _ in range(bs)]
+        self.free = list(range(n_pages - 1, -1, -1))
+        self.ws = B.alloc_attention_workspace(Hq, Hkv, D, device)
+
+    def reserve(self, r: int, tokens: int) -> None:
+        """Pages for `tokens` more of request r (host; raises when none are left)."""
+        import torch
+        first = len(self.pages[r])
+        need = -(-(self.bound[r] + tokens) // self.page_size) - first
+        if need > len(self.free) or first + max(need, 0) > self.page_table.shape[1]:
+            raise RuntimeError("the paged cache is full")
+        new = [self.free.pop() for _ in range(need)]
+        if new:
+            self.pages[r] += new
+            self.page_table[r, first:first + need] = torch.tensor(new, dtype=torch.int32).to(self.page_table.device)
+        self.bound[r] += tokens
+
+    def release(self, r: int) -> None:
+        """Request r is done: its pages go back."""
+        self.free += self.pages[r]
+        self.pages[r], self.bound[r] = [], 0
+        self.page_table[r] = -1
+        self.ctx_len[r] = 0
+
+    def attend(self, layer: int, q, k, v, cu_seqlens, max_rows: int, scale: float, out, stream=None) -> None:
+        """Rotate and append the packed rows' q, k, v, then attend: out [rows, Hq, D].  `out` is the rotated
+        queries' place as well."""
+        B.dspark_append_kv(q, k, v, cu_seqlens, self.ctx_len, self.cos_sin, self.page_table, out, self.k[layer],
+                           self.v[layer], self.ws, self.interleaved, stream)
+        B.dspark_window_attention(out, self.k[layer], self.v[layer], self.page_table, cu_seqlens, self.ctx_len, max_rows,
+                                  scale, self.window, self.n_sink, out, None, self.ws, stream)
+
+    def advance(self, tokens) -> None:
+        """Keep `tokens` [bs] (device int32) more of each request."""
+        self.ctx_len += tokens
+
+
+@dataclasses.dataclass
+class LogitRules:
+    """What dspark_process_logits applies to the packed rows; None: that rule is off."""
+    hist: "object" = None         # [bs, V] int16: build_history
+    repetition: "object" = None   # [bs] fp32
+    frequency: "object" = None
+    presence: "object" = None
+    bias_start: "object" = None   # [bs + 1], bias_ids, bias_vals: sorted ids per request
+    bias_ids: "object" = None
+    bias_vals: "object" = None
+    mask: Optional[Callable] = None  # buf -> [rows, ceil(V / 32)] int32 words for the packed rows, or None
+
+    def apply(self, buf, stream=None) -> None:
+        """The rules on buf.packed, in place."""
+        B.dspark_process_logits(buf.packed, buf.cu, buf.ids, self.hist, self.repetition, self.frequency, self.presence,
+                                self.bias_start, self.bias_ids, self.bias_vals, self.mask(buf) if self.mask else None,
+                                buf.packed, buf.ws, stream)
+
+
+def build_history(rules: LogitRules, prompts, V: int, ws, device="cuda") -> None:
+    """rules.hist from the prompts (host lists of ids); the last id of a prompt, the first step's anchor, is in it."""
+    import torch
+    start = [0]
+    for p in prompts:
+        start.append(start[-1] + len(p))
+    i32 = dict(dtype=torch.int32, device=device)
+    rules.hist = torch.empty((len(prompts), V), dtype=torch.int16, device=device)
+    B.dspark_history_build(torch.tensor([t for p in prompts for t in p], **i32), torch.tensor(start, **i32),
+                           torch.tensor([len(p) for p in prompts], **i32), rules.hist, ws)
+
+
+def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache: PagedCache, rules: LogitRules,
+                    temperature: float, seed: int, step: int, mode: int = B.DSPARK_COMPACT, tiers=None,
+                    stream=None) -> None:
+    """One step: draft, schedule and pack; the target forward over the packed windows, its logits under the
+    rules; the verification; then history, cache lengths and anchors (inp["anchor"]) take its outcome.
+    A request whose deciding row allows nothing keeps its anchor and adds no token."""
+    import torch
+
+    def target(b: S.StepBuffers) -> None:
+        forward(b, cache)
+        rules.apply(b, stream)
+
+    S.run_step(inp, buf, sps, target, temperature, seed, step, mode, tiers=tiers, stream=stream)
+    if rules.hist is not None:
+        B.dspark_history_commit(buf.out_tokens, rules.hist, buf.ws, stream)
+    last = buf.out_tokens.gather(1, buf.acc_len.long()[:, None])[:, 0]
+    dead = last < 0  # the anchor stays the last token: only the accepted ones before it are cached for good
+    before = torch.where(buf.acc_len > 0, buf.out_tokens.gather(1, (buf.acc_len.long() - 1).clamp(min=0)[:, None])[:, 0],
+                         inp["anchor"])
+    inp["anchor"].copy_(torch.where(dead, before, last))
+    cache.advance(buf.acc_len + (~dead).to(torch.int32))
