@@ -124,23 +124,31 @@ struct Ring {
   }
 };
 
+// A whole warp waits; one answer for all lanes (false: given up).  The limit holds for each wait by itself: a
+// call over a long cache may take its time.
 struct Waiter {
   volatile int* abort;
   uint64_t timeout_ns;
-  bool patient;  // try_wait itself sleeps for a while: with a limit shorter than that, look first
-  __device__ Waiter(volatile int* ab, uint64_t ns) : abort(ab), timeout_ns(ns), patient(ns >= 1000000) {}
-  // A whole warp waits; one answer for all lanes (false: given up).
   __device__ __forceinline__ bool operator()(const uint64_t* bar, uint32_t parity) const {
     const uint32_t b = tc::smem_u32(bar);
-    bool ok = patient ? tc::mbar_try_wait(b, parity) : tc::mbar_test_wait(b, parity);
-    if (!ok) {  // the limit holds for each wait by itself: a call over a long cache may take its time
-      const long long deadline = tc::deadline_after_ns(timeout_ns);
-      while (!ok && !*abort && clock64() <= deadline) ok = tc::mbar_try_wait_suspend(b, parity, 20000u);
-    }
+    bool ok = tc::mbar_try_wait(b, parity);
+    if (!ok) ok = tc::mbar_wait_bounded(b, parity, tc::deadline_after_ns(timeout_ns), abort);
     return __all_sync(~0u, ok);
   }
 };
-
+// The same for the TMA warps.  try_wait itself sleeps for a while, so with a limit shorter than that they look
+// instead, and the other warps learn of it by the abort flag.  (In the MMA warps' loops the longer code of this
+// wait cost the prompts' kernel a tenth.)
+struct TmaWaiter {
+  Waiter wait;
+  __device__ __forceinline__ bool operator()(const uint64_t* bar, uint32_t parity) const {
+    if (wait.timeout_ns >= 1000000) return wait(bar, parity);
+    const long long deadline = tc::deadline_after_ns(wait.timeout_ns);
+    bool ok = tc::mbar_test_wait(tc::smem_u32(bar), parity);
+    while (!ok && !*wait.abort && clock64() <= deadline) ok = tc::mbar_test_wait(tc::smem_u32(bar), parity);
+    return __all_sync(~0u, ok);
+  }
+};
 
 // The call's KV tiles, counted over (request, KV head, unit), are cut into kSets * gridDim.x ranges that differ
 // by one tile at most; this CTA has ranges blockIdx.x + set * gridDim.x.

@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int unit_tokens = 2 * a.tokens, tile_rows = a.tokens * a.g;
   const int active = (tile_rows + 31) / 32;  // softmax warps of a tile that hold rows
   PlanScratch& plan = *reinterpret_cast<PlanScratch*>(sK);  // before the first load
-  const Waiter wait{&sh->abort, a.timeout_ns};
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -110,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // --------------------------------------------------------------------- TMA producer
     // In order: a unit's K 0 and Q, then V j, K j + 1.  K and V are read by every unit of the head: kept in L2.
+    const TmaWaiter wait{{&sh->abort, a.timeout_ns}};
     const uint64_t keep = tc::policy_evict_last();
     Ring<C::kKSlots> kr;
     Ring<C::kVSlots> vr;
@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------------- MMA issuer
+    const Waiter wait{&sh->abort, a.timeout_ns};
     constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kTile, kTile);
     constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kTile, D) | tc::kIdescBMajorMN;
     Ring<C::kKSlots> kr;
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) sh->mma_pending = any;
   } else if (warp == 10) {
     // ------------------------------------------- V tiles: unseen slots cleared, then ready for the MMA
+    const Waiter wait{&sh->abort, a.timeout_ns};
     Ring<C::kVSlots> ring;
     Ring<kReady> ready;
     int seg_i = 0;
@@ -299,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     if ((warp & 3) < active) {
+      const Waiter wait{&sh->abort, a.timeout_ns};
       const int st = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
       const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
       const uint32_t t_s = lane_base + st * kTile, t_o = lane_base + 2 * kTile + st * D;

@@ -123,7 +123,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same for the warp, and known to be
   const int tile_rows = a.tokens * a.g;
-  const Waiter wait{&sh->abort, a.timeout_ns};
 
   if (warp == 0) {  // barriers: lane i those of number i
     for (int z = 0; z < kSets; ++z) {
@@ -177,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------------------- TMA producer
     // In order: K 0, K 1, then V t, K t + 2, over all tiles of the range; a unit's Q with its first K.
     const int set = warp - kTmaWarp;
+    const TmaWaiter wait{{&sh->abort, a.timeout_ns}};
     const uint64_t keep = tc::policy_evict_last(), stream = tc::policy_evict_first();
     uint8_t* ring_mem = sRing + set * C::kSlots * C::kSlotBytes;
     Ring<C::kSlots> ring;
@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_s = tc::idesc_bf16_f32(kTile, R);
     constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
     const int set = warp - kMmaWarp;
+    const Waiter wait{&sh->abort, a.timeout_ns};
     uint8_t* ring_mem = sRing + set * C::kSlots * C::kSlotBytes;
     const uint32_t t_s = tmem + set * 3 * R, t_o = t_s + 2 * R;
     const uint64_t dk = tc::sdesc_kmajor_sw128(tc::smem_u32(ring_mem));
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kTmaWarp) {
     // ------------------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const Waiter wait{&sh->abort, a.timeout_ns};
     const int grp = warp >> 2, w4 = warp & 3;
     const int kv = w4 * 32 + lane;  // this thread's slot of each tile = TMEM lane
     const int set = grp % kSets, row0 = grp / kSets * RW;  // and its rows

@@ -302,13 +302,17 @@ def test_attention_device_errors():
 def test_attention_wait_timeout_is_reported_and_recovers(rows, hq):
     """With a deadline of 1 ns the kernels' waits run out: they report it, drain their copies and MMAs and
     return; the next call with the normal deadline is right again, on the same workspace."""
-    c = Cache([rows] * 40, [700] * 40, 2, 64, 32, seed=19)
-    q = torch.randn(40 * rows, 2 * hq, 64, generator=torch.Generator().manual_seed(20)).to(torch.bfloat16).cuda()
+    # enough tiles for each block that its ring of tiles goes round
+    c = Cache([rows] * 20, [1500] * 20, 2, 64, 32, seed=19)
+    many = 12
+    c.table, c.ctx = c.table.repeat(many, 1), c.ctx.repeat(many)
+    c.cu = torch.arange(0, 20 * many * rows + 1, rows, dtype=torch.int32, device="cuda")
+    q = torch.randn(20 * many * rows, 2 * hq, 64, generator=torch.Generator().manual_seed(20)).to(torch.bfloat16).cuda()
     out, want = torch.zeros_like(q), torch.zeros_like(q)
     ws = B.alloc_attention_workspace(2 * hq, 2, 64)
 
     def call(o):
-        B.dspark_window_attention(q, c.k, c.v, c.table, c.cu, c.ctx, rows, 0.125, 300, 4, o, None, ws)
+        B.dspark_window_attention(q, c.k, c.v, c.table, c.cu, c.ctx, rows, 0.125, 1000, 4, o, None, ws)
         return B.dspark_read_device_status(ws)
 
     assert call(want) == B.DSPARK_OK
