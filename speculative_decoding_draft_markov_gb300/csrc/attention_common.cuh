@@ -33,7 +33,8 @@ struct AttnArgs {
   float* partial;   // [2 ranges][rows of a unit][D] partial outputs, normalised
   float* plse;      // [2 ranges][rows of a unit] their log2-sum-exp
   uint64_t timeout_ns;
-  float c2;         // scale * log2(e), never 0
+  float c2;           // |scale| log2(e), never 0
+  uint32_t negate_q;  // instruction descriptor bit: the first operand's sign, for a negative scale
   int max_pages, n_pages, page_shift, block_shift, bs, rows, Hq, Hkv, g, tokens, window, n_sink;
 };
 

@@ -8,6 +8,8 @@
 // reference m as it stands while the row's maximum is found: m only keeps the exponentials in range, and
 // any value within 2^60 of the maximum gives the same result, since the sum is divided out and neither fp32 nor
 // bf16 loses bits there.  It moves, and O and l are rescaled, when a maximum has outgrown it by more.
+#include <type_traits>
+
 #include "attention_common.cuh"
 
 namespace dspark {
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t keep = tc::policy_evict_last();
     Ring<C::kKSlots> kr;
     Ring<C::kVSlots> vr;
-    int seg_i = 0, flags = 0, n_k = 0, n_v = 0, q_use[2] = {0, 0};
+    int seg_i = 0, flags = 0, n_k = 0, n_v = 0, q_use0 = 0, q_use1 = 0;
     int4 info = make_int4(0, 0, 0, 0);
     bool ok = true;
     Walk walk(sh->start, unit_tokens);
@@ -134,8 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       vr.step();
       return true;
     };
-    auto put_q = [&](int b, int row) {
-      if (!wait(&sh->q_empty[b], (q_use[b] & 1) ^ 1)) return false;
+    auto put_q = [&](int b, int& use, int row) {
+      if (!wait(&sh->q_empty[b], (use & 1) ^ 1)) return false;
       if (lane == 0) {
         const uint32_t bar = tc::smem_u32(&sh->q_full[b]);
         tc::mbar_arrive_expect_tx(bar, uint32_t(tile_rows * 128 * C::kHalves));
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int hf = 0; hf < C::kHalves; ++hf)
           tc::tma_load_3d(tc::smem_u32(sQ + b * C::kTileBytes + hf * C::kHalfBytes), &map_q, bar, hf * 64, s.h * a.g, row, keep);
       }
-      ++q_use[b];
+      ++use;
       return true;
     };
     while (ok && walk.next(a, s)) {
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s.tile0 == 0 && s.n < s.u.ntiles) flags |= kHeadUsed, info = make_int4(0, s.row0, s.ntok, s.h);
       TileLoad t0 = tile_load(a, s, 0, lane), t1 = t0;
       if (s.n > 1) t1 = tile_load(a, s, 1, lane);
-      ok = put_k(t0) && put_q(0, s.row0) && (s.ntok <= a.tokens || put_q(1, s.row0 + a.tokens));
+      ok = put_k(t0) && put_q(0, q_use0, s.row0) && (s.ntok <= a.tokens || put_q(1, q_use1, s.row0 + a.tokens));
       for (int j = 0; ok && j < s.n; ++j) {
         TileLoad t2 = t1;
         if (j + 2 < s.n) t2 = tile_load(a, s, j + 2, lane);
@@ -171,8 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_wait_bounded(tc::smem_u32(&sh->k_full[i]), i < kr.slot ? kr.phase : kr.phase ^ 1, dl, &never);
       for (int i = 0; i < min(n_v, C::kVSlots); ++i)
         tc::mbar_wait_bounded(tc::smem_u32(&sh->v_full[i]), i < vr.slot ? vr.phase : vr.phase ^ 1, dl, &never);
-      for (int b = 0; b < 2; ++b)
-        if (q_use[b] > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[b]), (q_use[b] - 1) & 1, dl, &never);
+      if (q_use0 > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[0]), (q_use0 - 1) & 1, dl, &never);
+      if (q_use1 > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[1]), (q_use1 - 1) & 1, dl, &never);
     }
     if (lane == 0) {
       info.x = ok ? flags : 0;
@@ -181,12 +183,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9) {
     // ---------------------------------------------------------------------- MMA issuer
     const Waiter wait{&sh->abort, a.timeout_ns};
-    constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kTile, kTile);
+    const uint32_t idesc_qk = tc::idesc_bf16_f32(kTile, kTile) | a.negate_q;
     constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kTile, D) | tc::kIdescBMajorMN;
     Ring<C::kKSlots> kr;
     Ring<C::kVSlots> vr;
     Ring<kReady> ready;
-    int seg_i = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
+    int seg_i = 0;
+    uint32_t use0 = 0, use1 = 0, p0 = 0, p1 = 0;  // parities: the tiles' Q, their P
     bool ok = true, any = false;
     Walk walk(sh->start, unit_tokens);
     Segment s = {};
@@ -213,13 +216,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     while (ok && walk.next(a, s)) {
       const int n_st = s.ntok > a.tokens ? 2 : 1;
-      ok = wait(&sh->k_full[kr.slot], kr.phase) && wait(&sh->q_full[0], q_use[0]++ & 1) && (n_st == 1 || wait(&sh->q_full[1], q_use[1]++ & 1));
+      const bool two = n_st == 2;
+      ok = wait(&sh->k_full[kr.slot], kr.phase) && wait(&sh->q_full[0], use0) && (!two || wait(&sh->q_full[1], use1));
       if (!ok) break;
+      use0 ^= 1, use1 ^= two;
       tc::tc_fence_after();
       if (tc::elect_one()) {
-        for (int st = 0; st < n_st; ++st) {
-          issue_qk(st, kr.slot);
-          if (s.n == 1) tc::mma_commit(tc::smem_u32(&sh->q_empty[st]));
+        issue_qk(0, kr.slot);
+        if (s.n == 1) tc::mma_commit(tc::smem_u32(&sh->q_empty[0]));
+        if (two) {
+          issue_qk(1, kr.slot);
+          if (s.n == 1) tc::mma_commit(tc::smem_u32(&sh->q_empty[1]));
         }
         tc::mma_commit(tc::smem_u32(&sh->k_empty[kr.slot]));
       }
@@ -228,6 +235,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       any = true;
       int j0, j1;  // the tiles that need no clearing
       whole_tiles(a, s, s.u.p1, s.u.p0, j0, j1);
+      // P_st V of this tile, then S_st of the next; `last` of the unit's Q tiles frees V and K
+      auto step = [&](auto st_of, uint32_t parity, int j, bool more, bool last) {
+        constexpr int st = decltype(st_of)::value;
+        if (!wait(&sh->p_full[st][0], parity)) return false;
+        tc::tc_fence_after();
+        if (tc::elect_one()) issue_pv(st, vr.slot, 0, j > 0);
+        __syncwarp();
+        if (!wait(&sh->p_full[st][1], parity)) return false;
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+          issue_pv(st, vr.slot, 1, true);
+          if (more) issue_qk(st, kr.slot);
+          if (!more) tc::mma_commit(tc::smem_u32(&sh->o_full[st]));
+          if (last) {
+            tc::mma_commit(tc::smem_u32(&sh->v_empty[vr.slot]));
+            if (more) tc::mma_commit(tc::smem_u32(&sh->k_empty[kr.slot]));
+          }
+          if (j + 2 == s.n) tc::mma_commit(tc::smem_u32(&sh->q_empty[st]));
+        }
+        __syncwarp();
+        return true;
+      };
       for (int j = 0; ok && j < s.n; ++j) {
         const bool more = j + 1 < s.n;
         ok = wait(&sh->v_full[vr.slot], vr.phase) && (!more || wait(&sh->k_full[kr.slot], kr.phase));
@@ -235,28 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(&sh->v_ready[ready.slot], ready.phase);
           ready.step();
         }
-        if (!ok) break;
-        for (int st = 0; ok && st < n_st; ++st) {
-          const uint32_t p_phase = p_use[st]++ & 1;
-          ok = wait(&sh->p_full[st][0], p_phase);
-          if (!ok) break;
-          tc::tc_fence_after();
-          if (tc::elect_one()) issue_pv(st, vr.slot, 0, j > 0);
-          __syncwarp();
-          ok = wait(&sh->p_full[st][1], p_phase);
-          if (!ok) break;
-          tc::tc_fence_after();
-          if (tc::elect_one()) {
-            issue_pv(st, vr.slot, 1, true);
-            if (!more) tc::mma_commit(tc::smem_u32(&sh->o_full[st]));
-            if (st == n_st - 1) tc::mma_commit(tc::smem_u32(&sh->v_empty[vr.slot]));
-            if (more) {
-              issue_qk(st, kr.slot);
-              if (j + 2 == s.n) tc::mma_commit(tc::smem_u32(&sh->q_empty[st]));
-              if (st == n_st - 1) tc::mma_commit(tc::smem_u32(&sh->k_empty[kr.slot]));
-            }
-          }
-          __syncwarp();
+        ok = ok && step(std::integral_constant<int, 0>(), p0, j, more, !two);
+        p0 ^= 1;
+        if (two) {
+          ok = ok && step(std::integral_constant<int, 1>(), p1, j, more, true);
+          p1 ^= 1;
         }
         vr.step();
         if (more) kr.step();
@@ -330,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_ld_wait();
           if (j < j_in0 || j >= j_in1) {
             const int first = (s.tile0 + j) * per_tile;
-            const float hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
+            constexpr float hidden = -INFINITY;
             if (first >= s.u.sb) {  // one run of positions: slots from .. to are seen
               const int begin = block_pos(a, s.u, first);
               const int to = p - begin, from = a.window ? p - a.window + 1 - begin : 0;
@@ -385,15 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float t4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) t4[i] = x[i];
-          if (c2 > 0.f) {
 #pragma unroll
-            for (int i = 4; i < kTile; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
-            t4[0] = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-          } else {
-#pragma unroll
-            for (int i = 4; i < kTile; ++i) t4[i & 3] = fminf(t4[i & 3], x[i]);
-            t4[0] = fminf(fminf(t4[0], t4[1]), fminf(t4[2], t4[3]));
-          }
+          for (int i = 4; i < kTile; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
+          t4[0] = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
           const float top = t4[0] * c2;
           weigh(0);
           if (__any_sync(~0u, top > m + kRescaleAt)) {

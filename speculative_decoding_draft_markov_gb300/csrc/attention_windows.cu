@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kMmaWarp && warp < kMmaWarp + kSets) {
     // ------------------------------------------------------------ the two products of each tile
-    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(kTile, R);
+    const uint32_t idesc_s = tc::idesc_bf16_f32(kTile, R) | a.negate_q << 1;  // Q is the second operand here
     constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
     const int set = warp - kMmaWarp;
     const Waiter wait{&sh->abort, a.timeout_ns};
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kv = w4 * 32 + lane;  // this thread's slot of each tile = TMEM lane
     const int set = grp % kSets, row0 = grp / kSets * RW;  // and its rows
     const uint32_t t_s = tmem + (uint32_t(w4 * 32) << 16) + set * 3 * R + row0, t_o = t_s + 2 * R;
-    const float c2 = a.c2, hidden = c2 > 0.f ? -INFINITY : INFINITY;  // 2^-infinity after the scale
+    const float c2 = a.c2;
     const unsigned long long cc = pack_f32x2(c2, c2);
     float* ref = sh->ref[set] + row0;
     // where this thread's row of P goes: 16-byte pieces, from the first row of the group on
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!inside) {
 #pragma unroll
             for (int i = 0; i < RW; ++i)
-              if (row0 + i < from || row0 + i >= to) y[i] = hidden;
+              if (row0 + i < from || row0 + i >= to) y[i] = -INFINITY;
           }
         };
         auto refer = [&]() {  // scores to exponents; the largest

@@ -321,7 +321,8 @@ __device__ __forceinline__ uint32_t swizzled(int row, int piece) {
   return uint32_t(row * kRowBytes + ((piece ^ x) << 4));
 }
 
-// Instruction descriptor bits: A, B is MN-major.
+// Instruction descriptor bits: A is negated (B: the next bit); A, B is MN-major.
+constexpr uint32_t kIdescNegateA = 1u << 13;
 constexpr uint32_t kIdescAMajorMN = 1u << 15, kIdescBMajorMN = 1u << 16;
 
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, both K-major, M x N.

@@ -1,6 +1,7 @@
 // dspark_window_attention, host side and join: which kernel takes a call, and the kernel that joins the
 // partial rows of units that a cut between CTAs runs through.
 #include <algorithm>
+#include <cmath>
 
 #include "attention_common.cuh"
 
@@ -137,9 +138,10 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   a.info = reinterpret_cast<int4*>(w + L.info);
   a.partial = reinterpret_cast<float*>(w + L.partial), a.plse = reinterpret_cast<float*>(w + L.plse);
   a.timeout_ns = g_wait_timeout_ns;
-  a.c2 = scale * kLog2e;
-  // the kernel hides a score by an infinity before the scale: a scale of 0 becomes one that gives equal weights
-  // all the same (2^(1e-30 s) is 1)
+  a.c2 = std::fabs(scale) * kLog2e;
+  a.negate_q = scale < 0.f ? tc::kIdescNegateA : 0u;
+  // a hidden score is -inf before the scale: a scale of 0 becomes one that gives equal weights all the same
+  // (2^(1e-30 s) is 1)
   if (a.c2 == 0.f) a.c2 = 1e-30f;
   a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, prompts ? 7 : 5);
   a.bs = bs, a.rows = rows, a.Hq = Hq, a.Hkv = Hkv, a.g = g, a.tokens = prompts ? fit : std::min(unit_rows / g, std::max(max_rows, 1));
