@@ -77,12 +77,16 @@ template <> struct Pack8<float> {
 // one product and one sum, l * (l > 0 ? up : down) + add, which a thread keeps in registers for its 8 ids: the
 // history and the biases are read once for all rows of a window, a drafted token changes one thread's
 // registers.  The first rows are asked for before the history and the biases.  Each warp finds its own
-// biases in the request's sorted list, so no barrier stands in the way.  (With the factors worked out per
-// row it took 129 instructions per warp and row and 370 before the first row: 65% of the issue
-// slots at half of the bandwidth.)
-template <typename T, bool kInPlace>
-__global__ void __launch_bounds__(kRuleThreads, sizeof(T) == 2 ? 4 : 3) rules_kernel(const __grid_constant__ RuleArgs a) {
-  constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;  // rows in flight
+// biases in the request's sorted list, so no barrier stands in the way.
+// GB300, V 151936, bf16, history, 300 biases and a mask, 256 requests: windows of 8 rows 212 us (95% of the
+// measured copy bandwidth); of 1 .. 8 rows 146 us (82%); of one row 67 us (53%).  A warp executes 360
+// instructions (83 for the biases) before a window's first row and 81 for each row, at 2.0 to 2.1 a
+// cycle and SM: short windows are bound by the instructions before the first row.  Slower, each measured there: the factors worked out per
+// row; rows through shared memory by asynchronous copies (238 us where registers took 212); the biases asked for before the
+// search (153 us for 146); one wave of blocks, each over many windows (197 us for 146).
+// kAhead: rows in flight; kBlocks: blocks on an SM, which sets the registers.
+template <typename T, bool kInPlace, int kAhead, int kBlocks>
+__global__ void __launch_bounds__(kRuleThreads, kBlocks) rules_kernel(const __grid_constant__ RuleArgs a) {
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, r = blockIdx.y;
   const int lo = blockIdx.x * kRuleChunk, base = lo + tid * kRuleIds;  // V is a multiple of 8
@@ -209,50 +213,71 @@ __global__ void __launch_bounds__(kRuleThreads, sizeof(T) == 2 ? 4 : 3) rules_ke
 
 // ---------------------------------------------------------------------------- history
 
-constexpr int kHistThreads = 512;
-constexpr int kHistMaxChunk = 18 * 1024;  // ids of a block: 72 KB of cells, three blocks on an SM
+constexpr int kHistThreads = 512, kHistAhead = 8;  // and tokens that a thread asks for at once
+constexpr int kHistMaxChunk = 36 * 1024;  // ids of a block: 72 KB of words, three blocks on an SM
 
-// A block counts one request's tokens that fall into its `chunk` ids in shared memory (32-bit:
-// a list can be longer than the 15-bit count) and writes the chunk once.
+// One more of the 16-bit word at `sh` of *w: a saturating add on its 15-bit count.
+__device__ __forceinline__ void count_up(uint32_t* w, int sh) {
+  uint32_t old = *w;
+  while (((old >> sh) & 0x7FFFu) != 0x7FFFu) {
+    const uint32_t got = atomicCAS(w, old, old + (1u << sh));
+    if (got == old) break;
+    old = got;
+  }
+}
+
+// A block counts one request's tokens that fall into its `chunk` ids in shared memory, in the words that it
+// then writes once.  A list of up to 2^15 - 1 generated tokens cannot overflow a count: plain adds.
+// Bound by the latency of its steps (launch, list, counts, words): GB300, one list of 2500 tokens, V
+// 151936, 3.7 us with the commit after it; 64 lists of up to 8000 tokens, V 129280, 9.2 us (2.6 by its bytes),
+// of 100 tokens each 6.5.  A word per id (twice the blocks, each reading its list) took 12.4, four loads at a time 11.0,
+// 1024 threads 9.5.
 __global__ void __launch_bounds__(kHistThreads)
     history_build_kernel(const int32_t* __restrict__ tokens, int n_tokens, const int32_t* __restrict__ start,
                          const int32_t* __restrict__ n_prompt, int V, int chunk, int16_t* __restrict__ hist,
                          uint32_t* status) {
-  extern __shared__ __align__(16) uint32_t cell[];
+  extern __shared__ __align__(16) uint32_t cell[];  // two ids each
   pdl_enter();
   const int tid = threadIdx.x, r = blockIdx.y;
-  const int lo = blockIdx.x * chunk, n = min(chunk, V - lo);
+  const int lo = blockIdx.x * chunk, n = min(chunk, V - lo);  // multiples of 8
   int t0 = start[r], t1 = start[r + 1];
   const int asked = n_prompt[r];
-  for (int i = tid; i < n / 4; i += kHistThreads) reinterpret_cast<uint4*>(cell)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = tid; i < n / 8; i += kHistThreads) reinterpret_cast<uint4*>(cell)[i] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
   if (t0 < 0 || t1 < t0 || t1 > n_tokens) {
     if (tid == 0 && blockIdx.x == 0) set_status(status, DSPARK_EINVAL);
     t0 = t1 = 0;
   }
-#pragma unroll 4
-  for (int t = t0 + tid; t < t1; t += kHistThreads) {
-    const int id = tokens[t];
-    const int d = id - lo;
-    if (d >= 0 && d < n) {
-      if (t - t0 < asked)
-        atomicOr(&cell[d], 0x80000000u);
-      else
-        atomicAdd(&cell[d], 1u);
+  const bool fits = int64_t(t1) - t0 - max(asked, 0) <= 0x7FFF;
+  for (int64_t first = int64_t(t0) + tid; first < t1; first += kHistThreads * kHistAhead) {
+    int ids[kHistAhead];
+#pragma unroll
+    for (int k = 0; k < kHistAhead; ++k) {
+      const int64_t t = first + k * kHistThreads;
+      ids[k] = t < t1 ? tokens[t] : 0;
     }
-    if (blockIdx.x == 0 && (id < 0 || id >= V)) set_status(status, DSPARK_EINVAL);
+#pragma unroll
+    for (int k = 0; k < kHistAhead; ++k) {
+      const int64_t t = first + k * kHistThreads;
+      if (t >= t1) break;
+      const int id = ids[k], d = id - lo, sh = (d & 1) * 16;
+      if (d >= 0 && d < n) {
+        if (t - t0 < asked)
+          atomicOr(&cell[d >> 1], 0x8000u << sh);
+        else if (fits)
+          atomicAdd(&cell[d >> 1], 1u << sh);
+        else
+          count_up(&cell[d >> 1], sh);
+      }
+      if (blockIdx.x == 0 && (id < 0 || id >= V)) set_status(status, DSPARK_EINVAL);
+    }
   }
   __syncthreads();
-  uint4* out = reinterpret_cast<uint4*>(hist + size_t(r) * V + lo);  // chunks and V: multiples of 8
-  auto word = [](uint32_t c) { return min(c & 0x7FFFFFFFu, 0x7FFFu) | (c >> 16 & 0x8000u); };
-  auto two = [&](uint32_t a, uint32_t b) { return word(a) | word(b) << 16; };
-  for (int i = tid; i < n / 8; i += kHistThreads) {
-    const uint4 a = reinterpret_cast<const uint4*>(cell)[2 * i], b = reinterpret_cast<const uint4*>(cell)[2 * i + 1];
-    out[i] = make_uint4(two(a.x, a.y), two(a.z, a.w), two(b.x, b.y), two(b.z, b.w));
-  }
+  uint4* out = reinterpret_cast<uint4*>(hist + size_t(r) * V + lo);
+  for (int i = tid; i < n / 8; i += kHistThreads) out[i] = reinterpret_cast<const uint4*>(cell)[i];
 }
 
-// One thread per committed token: a saturating add on its half of a 32-bit word.
+// One thread per committed token.
 __global__ void history_commit_kernel(const int32_t* __restrict__ out_tokens, int n, int per_request, int V,
                                       int16_t* __restrict__ hist, uint32_t* status) {
   pdl_enter();
@@ -265,14 +290,7 @@ __global__ void history_commit_kernel(const int32_t* __restrict__ out_tokens, in
     return;
   }
   const size_t at = size_t(i / per_request) * V + id;
-  uint32_t* w = reinterpret_cast<uint32_t*>(hist) + (at >> 1);
-  const int sh = int(at & 1) * 16;
-  uint32_t old = *w;
-  while (((old >> sh) & 0x7FFFu) != 0x7FFFu) {
-    const uint32_t got = atomicCAS(w, old, old + (1u << sh));
-    if (got == old) break;
-    old = got;
-  }
+  count_up(reinterpret_cast<uint32_t*>(hist) + (at >> 1), int(at & 1) * 16);
 }
 
 }  // namespace
@@ -291,26 +309,30 @@ cudaError_t launch_process_logits(const void* logits, int dtype, int rows, int V
   // the rows of a window are shared out where requests are few: about 8 blocks for each SM
   const int blocks = (V + kRuleChunk - 1) / kRuleChunk, want = 8 * tch::sm_count();
   const dim3 grid(blocks, bs, std::max(1, std::min({want / (blocks * bs), rows / bs, 8}))), block(kRuleThreads);
-  if (logits == out)
-    return dtype == DSPARK_F32 ? launch_pdl(rules_kernel<float, true>, grid, block, 0, s, a)
-                               : launch_pdl(rules_kernel<__nv_bfloat16, true>, grid, block, 0, s, a);
-  return dtype == DSPARK_F32 ? launch_pdl(rules_kernel<float, false>, grid, block, 0, s, a)
-                             : launch_pdl(rules_kernel<__nv_bfloat16, false>, grid, block, 0, s, a);
+  // Windows of one or two rows have nothing to ask for ahead: fewer registers and a fifth block on each SM, once there
+  // are more blocks than an SM holds.  256 windows of one row, bf16: 67 us against 78 (64 in fp32: 19.7
+  // against 24.6); of 1 .. 8 rows 157 against 146; 8 windows of one row 4.3 against 3.9.
+  const bool few = rows < 2 * bs && blocks * bs > 4 * tch::sm_count();
+  auto launch = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, s, a); };
+  using bf16 = __nv_bfloat16;
+  if (dtype == DSPARK_F32)
+    return launch(logits == out ? rules_kernel<float, true, 2, 3> : few ? rules_kernel<float, false, 1, 5> : rules_kernel<float, false, 2, 3>);
+  return launch(logits == out ? rules_kernel<bf16, true, 3, 4> : few ? rules_kernel<bf16, false, 1, 5> : rules_kernel<bf16, false, 3, 4>);
 }
 
 cudaError_t launch_history_build(const int32_t* tokens, int n_tokens, const int32_t* start, const int32_t* n_prompt,
                                  int bs, int V, int16_t* hist, uint32_t* status, cudaStream_t s) {
-  // every block of a request reads the request's whole list, so chunks are as large as still gives each SM
-  // three blocks, and shared memory allows
-  const int per_sm = 3 * tch::sm_count();
-  const int64_t ids = (int64_t(V) * bs + per_sm - 1) / per_sm;
-  const int chunk = int(std::min<int64_t>(kHistMaxChunk, std::max<int64_t>(2048, (ids + 2047) / 2048 * 2048)));
+  // every block of a request reads the request's whole list, so no more blocks than SMs, except as
+  // shared memory asks for (four blocks an SM: 64 lists of up to 8000 tokens, V 129280, 10.6 us against 9.2)
+  const int most = std::max(1, tch::sm_count() / bs), least = (V + kHistMaxChunk - 1) / kHistMaxChunk;
+  const int n = std::max(least, std::min(most, (V + 2047) / 2048));
+  const int chunk = ((V + n - 1) / n + 7) / 8 * 8;
   static bool done[tch::kMaxDevices] = {};
   static std::mutex mu;
-  const cudaError_t e = tch::set_smem_once(history_build_kernel, kHistMaxChunk * int(sizeof(uint32_t)), done, &mu);
+  const cudaError_t e = tch::set_smem_once(history_build_kernel, kHistMaxChunk * 2, done, &mu);
   if (e != cudaSuccess) return e;
   return launch_pdl(history_build_kernel, dim3((V + chunk - 1) / chunk, bs), dim3(kHistThreads),
-                    chunk * sizeof(uint32_t), s, tokens, n_tokens, start, n_prompt, V, chunk, hist, status);
+                    chunk * 2, s, tokens, n_tokens, start, n_prompt, V, chunk, hist, status);
 }
 
 cudaError_t launch_history_commit(const int32_t* out_tokens, int bs, int gamma, int V, int16_t* hist, uint32_t* status,

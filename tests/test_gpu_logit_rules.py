@@ -98,6 +98,20 @@ def test_rules(ns, V, dtype, use_mask):
     assert st == B.DSPARK_OK and torch.equal(got, out)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rules_many_short_windows(dtype):
+    """Windows of one row in the main, a longer one, empty ones."""
+    ns = [1] * 100 + [6, 0, 0, 2] + [1] * 60
+    b = Batch(ns, 8200, dtype, seed=36, n_bias=3)
+    out, st = b.call()
+    assert st == B.DSPARK_OK
+    b.check(out)
+    x = b.logits.cuda()
+    x[sum(ns):] = 7.0
+    got, st = b.call(out=x, logits=x)
+    assert st == B.DSPARK_OK and torch.equal(got, out)
+
+
 @pytest.mark.parametrize("n_bias", [60, 65, 700, 5000])
 def test_rules_many_biases(n_bias):
     """Lists that a warp searches in one, two and more steps, as long as the vocabulary at last."""
