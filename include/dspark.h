@@ -506,16 +506,17 @@ DSPARK_API int dspark_window_attention(const void* q, int64_t q_stride, int dtyp
  *                (dspark_history_build); NULL with repetition, frequency, presence NULL: no penalties
  *   repetition, frequency, presence  device [bs] fp32, or NULL each: 1, 0, 0
  *   bias_start   device [bs + 1] int32, bias_ids / bias_vals device int32 / fp32: request r's biases are
- *                entries bias_start[r] .. bias_start[r+1] - 1, ids strictly increasing; all NULL: none
+ *                entries bias_start[r] .. bias_start[r+1] - 1 of n_bias, ids strictly increasing; all NULL: none
  *   mask         device [rows, ceil(V / 32)] uint32, bit v % 32 of word v / 32 set where v is allowed; or NULL
  * Device errors (status word, EINVAL): cu_seqlens decreasing or beyond rows (the request is skipped),
- * a drafted id outside [0, V) (not counted), bias ids not strictly increasing or outside [0, V).
+ * a drafted id outside [0, V) (not counted), bias ids not strictly increasing or outside [0, V), a
+ * request's bias entries not inside 0 .. n_bias (not read).
  * Limits: 1 <= bs <= 256, V % 8 == 0, 8 <= V < 2^24. */
 DSPARK_API int dspark_process_logits(const void* logits, int dtype, int rows, int V, const int32_t* cu_seqlens,
                                      const int32_t* ids, int bs, const int16_t* hist, const float* repetition,
                                      const float* frequency, const float* presence, const int32_t* bias_start,
-                                     const int32_t* bias_ids, const float* bias_vals, const uint32_t* mask,
-                                     void* out, void* ws, size_t ws_bytes, dspark_stream_t stream);
+                                     const int32_t* bias_ids, const float* bias_vals, int n_bias,
+                                     const uint32_t* mask, void* out, void* ws, size_t ws_bytes, dspark_stream_t stream);
 
 /* Token history of dspark_process_logits.
  * build: rewrites hist[0 .. bs-1] from token lists: request r's tokens are tokens[start[r] ..

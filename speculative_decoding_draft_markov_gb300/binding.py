@@ -61,8 +61,8 @@ _SIGS.update({
     "dspark_window_attention_workspace_bytes": (_sz, [_i, _i, _i]),
     "dspark_window_attention": (_i, [_vp, _i64, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _f,
                                      _i, _i, _vp, _vp, _vp, _sz, _vp]),
-    "dspark_process_logits": (_i, [_vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
-                                   _sz, _vp]),
+    "dspark_process_logits": (_i, [_vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp,
+                                   _vp, _sz, _vp]),
     "dspark_history_build": (_i, [_vp, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp]),
     "dspark_history_commit": (_i, [_vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
 })
@@ -500,7 +500,8 @@ def dspark_process_logits(logits, cu_seqlens, ids, hist, repetition, frequency, 
           _ptr(hist, T.i16, (bs, V), "hist"), _ptr(repetition, T.f32, (bs,), "repetition"),
           _ptr(frequency, T.f32, (bs,), "frequency"), _ptr(presence, T.f32, (bs,), "presence"),
           _ptr(bias_start, T.i32, (bs + 1,), "bias_start"), _ptr(bias_ids, T.i32, None, "bias_ids"),
-          _ptr(bias_vals, T.f32, None, "bias_vals"), _ptr(mask, T.i32, (rows, (V + 31) // 32), "mask"),
+          _ptr(bias_vals, T.f32, None if bias_ids is None else bias_ids.shape, "bias_vals"),
+          0 if bias_ids is None else bias_ids.numel(), _ptr(mask, T.i32, (rows, (V + 31) // 32), "mask"),
           _ptr(out, dt, shape, "out"), ws.data_ptr(), ws.numel())
 
 

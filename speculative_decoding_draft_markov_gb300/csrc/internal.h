@@ -118,8 +118,8 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
 cudaError_t launch_process_logits(const void* logits, int dtype, int rows, int V, const int32_t* cu,
                                   const int32_t* ids, int bs, const int16_t* hist, const float* repetition,
                                   const float* frequency, const float* presence, const int32_t* bias_start,
-                                  const int32_t* bias_ids, const float* bias_vals, const uint32_t* mask, void* out,
-                                  uint32_t* status, cudaStream_t s);
+                                  const int32_t* bias_ids, const float* bias_vals, int n_bias, const uint32_t* mask,
+                                  void* out, uint32_t* status, cudaStream_t s);
 cudaError_t launch_history_build(const int32_t* tokens, int n_tokens, const int32_t* start, const int32_t* n_prompt,
                                  int bs, int V, int16_t* hist, uint32_t* status, cudaStream_t s);
 cudaError_t launch_history_commit(const int32_t* out_tokens, int bs, int gamma, int V, int16_t* hist, uint32_t* status,

@@ -26,7 +26,7 @@ struct RuleArgs {
   const float* bias_vals;
   const uint8_t* mask;
   uint32_t* status;
-  int rows, V, mask_row_bytes;
+  int rows, V, n_bias, mask_row_bytes;
 };
 
 template <typename T> struct Pack8;  // 8 logits of a row
@@ -79,11 +79,11 @@ template <> struct Pack8<float> {
 // registers.  The first rows are asked for before the history and the biases.  Each warp finds its own
 // biases in the request's sorted list, so no barrier stands in the way.
 // GB300, V 151936, bf16, history, 300 biases and a mask, 256 requests: windows of 8 rows 212 us (95% of the
-// measured copy bandwidth); of 1 .. 8 rows 146 us (82%); of one row 67 us (53%).  A warp executes 360
+// measured copy bandwidth); of 1 .. 8 rows 147 us (82%); of one row 69 us (51%).  A warp executes 360
 // instructions (83 for the biases) before a window's first row and 81 for each row, at 2.0 to 2.1 a
 // cycle and SM: short windows are bound by the instructions before the first row.  Slower, each measured there: the factors worked out per
 // row; rows through shared memory by asynchronous copies (238 us where registers took 212); the biases asked for before the
-// search (153 us for 146); one wave of blocks, each over many windows (197 us for 146).
+// search (153 us for 146); one wave of blocks, each over many windows (197 for 146).
 // kAhead: rows in flight; kBlocks: blocks on an SM, which sets the registers.
 template <typename T, bool kInPlace, int kAhead, int kBlocks>
 __global__ void __launch_bounds__(kRuleThreads, kBlocks) rules_kernel(const __grid_constant__ RuleArgs a) {
@@ -139,7 +139,9 @@ __global__ void __launch_bounds__(kRuleThreads, kBlocks) rules_kernel(const __gr
 #pragma unroll
   for (int j = 0; j < kRuleIds; ++j) add[j] = 0.f;
   if (a.bias_start) {
-    const int e0 = a.bias_start[r], e1 = a.bias_start[r + 1];
+    const int e0 = max(a.bias_start[r], 0), e1 = min(a.bias_start[r + 1], a.n_bias);
+    if (checks && tid == 0 && (a.bias_start[r] < 0 || a.bias_start[r + 1] < e0 || a.bias_start[r + 1] > a.n_bias))
+      set_status(a.status, DSPARK_EINVAL);
     if (checks)
       for (int e = e0 + tid; e < e1; e += kRuleThreads) {
         const int id = a.bias_ids[e];
@@ -298,19 +300,19 @@ __global__ void history_commit_kernel(const int32_t* __restrict__ out_tokens, in
 cudaError_t launch_process_logits(const void* logits, int dtype, int rows, int V, const int32_t* cu,
                                   const int32_t* ids, int bs, const int16_t* hist, const float* repetition,
                                   const float* frequency, const float* presence, const int32_t* bias_start,
-                                  const int32_t* bias_ids, const float* bias_vals, const uint32_t* mask, void* out,
-                                  uint32_t* status, cudaStream_t s) {
+                                  const int32_t* bias_ids, const float* bias_vals, int n_bias, const uint32_t* mask,
+                                  void* out, uint32_t* status, cudaStream_t s) {
   RuleArgs a;
   a.logits = logits, a.out = out, a.cu = cu, a.ids = ids, a.hist = hist;
   a.repetition = repetition, a.frequency = frequency, a.presence = presence;
   a.bias_start = bias_start, a.bias_ids = bias_ids, a.bias_vals = bias_vals;
   a.mask = reinterpret_cast<const uint8_t*>(mask);  // little-endian words: byte i holds ids 8i .. 8i+7
-  a.status = status, a.rows = rows, a.V = V, a.mask_row_bytes = (V + 31) / 32 * 4;
+  a.status = status, a.rows = rows, a.V = V, a.n_bias = n_bias, a.mask_row_bytes = (V + 31) / 32 * 4;
   // the rows of a window are shared out where requests are few: about 8 blocks for each SM
   const int blocks = (V + kRuleChunk - 1) / kRuleChunk, want = 8 * tch::sm_count();
   const dim3 grid(blocks, bs, std::max(1, std::min({want / (blocks * bs), rows / bs, 8}))), block(kRuleThreads);
   // Windows of one or two rows have nothing to ask for ahead: fewer registers and a fifth block on each SM, once there
-  // are more blocks than an SM holds.  256 windows of one row, bf16: 67 us against 78 (64 in fp32: 19.7
+  // are more blocks than an SM holds.  256 windows of one row, bf16: 69 us against 79 (64 in fp32: 19.7
   // against 24.6); of 1 .. 8 rows 157 against 146; 8 windows of one row 4.3 against 3.9.
   const bool few = rows < 2 * bs && blocks * bs > 4 * tch::sm_count();
   auto launch = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, s, a); };

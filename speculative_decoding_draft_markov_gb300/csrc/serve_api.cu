@@ -101,8 +101,8 @@ static int check_vocab(int bs, int V) {
 int dspark_process_logits(const void* logits, int dtype, int rows, int V, const int32_t* cu_seqlens,
                           const int32_t* ids, int bs, const int16_t* hist, const float* repetition,
                           const float* frequency, const float* presence, const int32_t* bias_start,
-                          const int32_t* bias_ids, const float* bias_vals, const uint32_t* mask, void* out, void* ws,
-                          size_t ws_bytes, dspark_stream_t stream) {
+                          const int32_t* bias_ids, const float* bias_vals, int n_bias, const uint32_t* mask, void* out,
+                          void* ws, size_t ws_bytes, dspark_stream_t stream) {
   if (!logits || !out || !cu_seqlens || !ids || rows < 1) return DSPARK_EINVAL;
   if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return DSPARK_EINVAL;
   if (int e = check_vocab(bs, V)) return e;
@@ -110,9 +110,10 @@ int dspark_process_logits(const void* logits, int dtype, int rows, int V, const 
   if (!hist && (repetition || frequency || presence)) return DSPARK_EINVAL;  // penalties of what?
   if ((bias_start == nullptr) != (bias_ids == nullptr) || (bias_start == nullptr) != (bias_vals == nullptr))
     return DSPARK_EINVAL;
+  if (n_bias < 0 || !al(bias_start, 4) || !al(bias_ids, 4) || !al(bias_vals, 4)) return DSPARK_EINVAL;
   if (int e = check_status_ws(ws, ws_bytes)) return e;
   return cuda_status(launch_process_logits(logits, dtype, rows, V, cu_seqlens, ids, bs, hist, repetition, frequency,
-                                           presence, bias_start, bias_ids, bias_vals, mask, out,
+                                           presence, bias_start, bias_ids, bias_vals, n_bias, mask, out,
                                            static_cast<uint32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -189,6 +189,23 @@ def test_rules_device_errors():
         b.ids = ids
 
 
+def test_rules_bias_entries_out_of_range():
+    """Entries that are not inside the list: reported; the other requests are served."""
+    b = Batch([3, 2, 4], 512, torch.bfloat16, seed=37, n_bias=9)
+    n = b.bias_ids.size
+    for bad in ([0, n + 1, n, n], [-1, 9, n, n], [0, 9, 4, n]):
+        keep, b.bias_start = b.bias_start, np.array(bad, np.int32)
+        out, st = b.call()
+        assert st == B.DSPARK_EINVAL
+        b.bias_start = keep
+        good, st = b.call()
+        assert st == B.DSPARK_OK
+        for r in range(3):
+            rows = slice(int(b.cu[r]), int(b.cu[r + 1]))
+            if bad[r:r + 2] == keep[r:r + 2].tolist():
+                assert torch.equal(out[rows], good[rows])
+
+
 # ------------------------------------------------------------------------------ history
 
 @pytest.mark.parametrize("V", [8, 2048, 5000, 16392])

@@ -27,7 +27,7 @@ ATTEND = dict(q=PTR, q_stride=1024, dtype=B.DSPARK_BF16, k_cache=PTR, v_cache=PT
               page_size=16, cu=PTR, ctx=PTR, bs=2, rows=5, max_rows=3, Hq=8, Hkv=2, D=128, scale=0.1, window=0, n_sink=0,
               out=PTR, lse=None, ws=PTR, ws_bytes=1 << 40, stream=None)
 RULES = dict(logits=PTR, dtype=B.DSPARK_BF16, rows=5, V=64, cu=PTR, ids=PTR, bs=2, hist=PTR, repetition=PTR, frequency=PTR,
-             presence=PTR, bias_start=PTR, bias_ids=PTR, bias_vals=PTR, mask=PTR, out=OTHER, ws=PTR, ws_bytes=256,
+             presence=PTR, bias_start=PTR, bias_ids=PTR, bias_vals=PTR, n_bias=9, mask=PTR, out=OTHER, ws=PTR, ws_bytes=256,
              stream=None)
 BUILD = dict(tokens=PTR, n_tokens=9, start=PTR, n_prompt=PTR, bs=2, V=64, hist=PTR, ws=PTR, ws_bytes=256, stream=None)
 COMMIT = dict(out_tokens=PTR, bs=2, gamma=7, V=64, hist=PTR, ws=PTR, ws_bytes=256, stream=None)
@@ -76,7 +76,7 @@ def test_attention_workspace_bytes(lib):
     ("logits", None, EINVAL), ("out", None, EINVAL), ("cu", None, EINVAL), ("ids", None, EINVAL), ("rows", 0, EINVAL),
     ("dtype", 5, EINVAL), ("V", 60, EINVAL), ("V", 0, EINVAL), ("V", 1 << 24, EUNSUP), ("bs", 0, EINVAL), ("bs", 257, EUNSUP),
     ("hist", None, EINVAL), ("hist", PTR + 2, EINVAL), ("bias_ids", None, EINVAL), ("bias_start", None, EINVAL),
-    ("bias_vals", None, EINVAL), ("logits", PTR + 2, EINVAL), ("out", PTR + 2, EINVAL), ("mask", PTR + 1, EINVAL),
+    ("bias_vals", None, EINVAL), ("n_bias", -1, EINVAL), ("bias_ids", PTR + 2, EINVAL), ("logits", PTR + 2, EINVAL), ("out", PTR + 2, EINVAL), ("mask", PTR + 1, EINVAL),
     ("ws", None, EWS), ("ws_bytes", 8, EWS)])
 def test_rules_refuse(lib, key, val, want):
     assert _try(lib, "dspark_process_logits", RULES, {key: val}) == want
