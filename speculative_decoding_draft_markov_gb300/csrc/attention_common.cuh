@@ -44,7 +44,7 @@ enum : int { kTailUsed = 1, kTailEnds = 2, kHeadUsed = 4 };
 // 2 v + 1).  y = packed row of the unit's first token, z = its tokens, w = its KV head.
 
 // The KV tiles of one unit: its rows sit at positions p0 .. p1 and see, as a whole, the sinks and
-// lo .. p1.  Its blocks (pages, or 128-slot pieces of larger pages) in order: sink blocks 0 .. sb - 1,
+// lo .. p1.  Its blocks (pages, or 32-slot pieces of larger pages) in order: sink blocks 0 .. sb - 1,
 // then wb0 onwards.
 struct Geom {
   int p0, p1, lo, sb, wb0, nblk, ntiles;
@@ -316,7 +316,9 @@ __device__ __forceinline__ void clear_unseen(const AttnArgs& a, const Segment& s
 }
 }  // namespace attn
 
-// Ranges per CTA of the short windows' kernel (partial rows in the workspace are per range).
+// The most (token, head) rows of a unit of the short windows' kernel, and its ranges per CTA (partial rows in the workspace are
+// per range).
+constexpr int attention_window_rows(int D) { return D == 64 ? 64 : 128; }
 int attention_window_sets(int D, int unit_rows);
 cudaError_t launch_attention_prompts(int D, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                      const attn::AttnArgs& a, int n_cta, cudaStream_t s);

@@ -1,4 +1,4 @@
-// The attention of short windows: all (token, head) rows of a unit fit one tile of R = 16, 32, 64 or 128.
+// The attention of short windows: all (token, head) rows of a unit fit one tile of R = 16, 32, 64 or (D = 128) 128.
 //
 // Bound by reading K and V once, so a KV tile's way through the SM has to be short: the products are taken
 // transposed,
@@ -9,8 +9,8 @@
 // are.  (With the rows on TMEM lanes instead, 32 rows sat in one warp per stream: a unit of 10 tiles at 32
 // rows took 24 us per CTA.)  A tile's way is a chain of latencies, and so are the first and the last tile of
 // a unit.  So an SM runs two pipelines side by side, each with its own range of the work, ring, S^T, P^T and O^T;
-// where a set's registers or shared memory do not allow two (R = 128; R = 64 with D = 128, whose
-// tiles take twice as long to load), one pipeline has all sixteen softmax warps.
+// where tensor memory (R = 128) or shared memory (R = 64 with D = 128) does not allow two, one pipeline has all
+// sixteen softmax warps.
 //
 // m is a reference that only keeps the exponentials in range, the same for all slots of a row: any value
 // within 2^60 of the maximum gives the same result, since the sum is divided out and neither fp32 nor bf16 loses
@@ -31,7 +31,7 @@ constexpr int kSoftmaxRegs = 104, kOtherRegs = 56;
 constexpr float kUnset = -1e30f, kRescaleAt = 60.f;  // log2 units
 constexpr int kMaxSlots = 8;
 
-constexpr int sets_of(int D, int R) { return R == 128 || R * D == 64 * 128 ? 1 : 2; }
+constexpr int sets_of(int D, int R) { return R * D >= 64 * 128 ? 1 : 2; }
 
 template <int D, int R>
 struct Shared {
@@ -544,8 +544,7 @@ cudaError_t launch_attention_windows(int D, int unit_rows, const CUtensorMap& q,
   if (D == 64) switch (unit_rows) {
       case 16: return launch<64, 16>(q, k, v, a, n_cta, s);
       case 32: return launch<64, 32>(q, k, v, a, n_cta, s);
-      case 64: return launch<64, 64>(q, k, v, a, n_cta, s);
-      default: return launch<64, 128>(q, k, v, a, n_cta, s);
+      default: return launch<64, 64>(q, k, v, a, n_cta, s);
     }
   switch (unit_rows) {
     case 16: return launch<128, 16>(q, k, v, a, n_cta, s);

@@ -2,6 +2,8 @@
 // paged cache.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "packed_rows.cuh"
@@ -10,7 +12,7 @@
 namespace dspark {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kMaxAppendThreads = 256;
 
 struct AppendArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -21,7 +23,6 @@ struct AppendArgs {
   __nv_bfloat16 *q_out, *k_cache, *v_cache;
   uint32_t* status;
   int bs, rows, max_pos, rot, max_pages, n_pages, page_shift, Hq, Hkv, D;
-  int rows_per_block;
 };
 
 struct RowPlace {
@@ -41,19 +42,22 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
 
-// A memory-bound copy with two multiplications per element.  An item is 16 lanes of one head, as
+// A memory-bound copy with two multiplications per element.  A block has one row; an item is 16 lanes of one head, as
 // two 16-byte loads and stores: rotated by halves, lanes t .. t+7 and their partners t + rot/2 ..;
 // otherwise 16 lanes in a row (8 interleaved pairs, or lanes that pass).  So each thread holds both
 // lanes of its pairs and q_out may be q.
+// GB300, Hq 32, Hkv 8, D 128: 8191 rows 31.8 us (90% of the measured copy bandwidth); 256 windows of 1 .. 8 rows
+// 7.1 us (4.2 by their bytes); one row 3.0 us, a launch and five dependent trips to memory (window, length, page, row, store).
+// Four rows to a block took 33.9, 7.0 and 3.3 us, eight 41.5, 9.0 and 3.8; a thread's first two items asked for
+// before the row's place is known 36.5, 9.4 and 3.0 (twice the registers); 40 registers in place of 32 34.0 and 8.3.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
-  __shared__ RowPlace place[kAppendThreads / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__global__ void __launch_bounds__(kMaxAppendThreads, 8) append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ RowPlace place;
+  const int tid = threadIdx.x, lane = tid & 31;
   pdl_enter();
-  const int row0 = blockIdx.x * a.rows_per_block;
-  if (warp < a.rows_per_block) {
-    const int row = row0 + warp;
-    const int r = row < a.rows ? warp_request_of(a.cu, a.bs, a.rows, row, lane) : a.bs;
+  const int row = blockIdx.x;
+  if (tid < 32) {
+    const int r = warp_request_of(a.cu, a.bs, a.rows, row, lane);
     if (lane == 0) {
       RowPlace pl{-1, 0};
       if (r < 0) {
@@ -72,30 +76,27 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
           set_status(a.status, DSPARK_EINVAL);
         }
       }
-      place[warp] = pl;
+      place = pl;
     }
   }
   __syncthreads();
 
   const int per_head = a.D / 16, turned = a.rot / 16;
-  const int items = (a.Hq + 2 * a.Hkv) * per_head;
-  for (int it = tid; it < items * a.rows_per_block; it += kAppendThreads) {
-    const int rr = it / items, e = it - rr * items;
-    const RowPlace pl = place[rr];
-    if (pl.pos < 0) continue;
-    const int64_t row = row0 + rr;
-    const int hh = e / per_head, c = e - hh * per_head;
+  const RowPlace pl = place;
+  if (pl.pos < 0) return;
+  for (int it = tid; it < (a.Hq + 2 * a.Hkv) * per_head; it += int(blockDim.x)) {
+    const int hh = it / per_head, c = it - hh * per_head;
     const __nv_bfloat16* src;
     __nv_bfloat16* dst;
     const int64_t head_step = int64_t(a.D) << a.page_shift;
     if (hh < a.Hq) {
-      src = a.q + row * a.q_stride + hh * a.D;
-      dst = a.q_out + (row * a.Hq + hh) * a.D;
+      src = a.q + int64_t(row) * a.q_stride + hh * a.D;
+      dst = a.q_out + (int64_t(row) * a.Hq + hh) * a.D;
     } else if (hh < a.Hq + a.Hkv) {
-      src = a.k + row * a.k_stride + (hh - a.Hq) * a.D;
+      src = a.k + int64_t(row) * a.k_stride + (hh - a.Hq) * a.D;
       dst = a.k_cache + pl.slot + (hh - a.Hq) * head_step;
     } else {
-      src = a.v + row * a.v_stride + (hh - a.Hq - a.Hkv) * a.D;
+      src = a.v + int64_t(row) * a.v_stride + (hh - a.Hq - a.Hkv) * a.D;
       dst = a.v_cache + pl.slot + (hh - a.Hq - a.Hkv) * head_step;
     }
     const bool rotates = hh < a.Hq + a.Hkv && c < turned;
@@ -144,10 +145,9 @@ cudaError_t launch_append_kv(const void* q, int64_t q_stride, const void* k, int
   a.status = status;
   a.bs = bs, a.rows = rows, a.max_pos = max_pos, a.rot = rot, a.max_pages = max_pages, a.n_pages = n_pages;
   a.page_shift = page_shift, a.Hq = q ? Hq : 0, a.Hkv = Hkv, a.D = D;
-  a.rows_per_block = rows >= 4096 ? 4 : 1;
-  const dim3 grid((rows + a.rows_per_block - 1) / a.rows_per_block);
-  return interleaved ? launch_pdl(append_kernel<true>, grid, dim3(kAppendThreads), 0, s, a)
-                     : launch_pdl(append_kernel<false>, grid, dim3(kAppendThreads), 0, s, a);
+  const int items = (a.Hq + 2 * Hkv) * (D / 16);
+  const dim3 block(std::min((items + 31) / 32 * 32, kMaxAppendThreads));
+  return launch_pdl(interleaved ? append_kernel<true> : append_kernel<false>, dim3(rows), block, 0, s, a);
 }
 
 }  // namespace dspark

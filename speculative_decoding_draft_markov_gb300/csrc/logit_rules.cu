@@ -308,9 +308,17 @@ cudaError_t launch_process_logits(const void* logits, int dtype, int rows, int V
   a.bias_start = bias_start, a.bias_ids = bias_ids, a.bias_vals = bias_vals;
   a.mask = reinterpret_cast<const uint8_t*>(mask);  // little-endian words: byte i holds ids 8i .. 8i+7
   a.status = status, a.rows = rows, a.V = V, a.n_bias = n_bias, a.mask_row_bytes = (V + 31) / 32 * 4;
-  // the rows of a window are shared out where requests are few: about 8 blocks for each SM
-  const int blocks = (V + kRuleChunk - 1) / kRuleChunk, want = 8 * tch::sm_count();
-  const dim3 grid(blocks, bs, std::max(1, std::min({want / (blocks * bs), rows / bs, 8}))), block(kRuleThreads);
+  // A window's rows are shared out over z blocks where that fills the SMs better: the z with the least waves x (set-up,
+  // worth about four rows, + rows).  8 windows of 16 rows in fp32, V 129280: z = 2 26.3 us, 1 29.8; in bf16, V
+  // 151936: z = 1 15.6, 2 17.3; one of 8 rows: z = 4 4.2, 8 4.5, 1 4.8.
+  const int blocks = (V + kRuleChunk - 1) / kRuleChunk, slots = (dtype == DSPARK_F32 ? 3 : 4) * tch::sm_count();
+  int z = 1;
+  auto cost = [&](int n) {
+    return int64_t((int64_t(blocks) * bs * n + slots - 1) / slots) * (4 + (rows + bs * n - 1) / (bs * n));
+  };
+  for (int n = 2; n <= 4; n *= 2)
+    if (cost(n) < cost(z)) z = n;
+  const dim3 grid(blocks, bs, z), block(kRuleThreads);
   // Windows of one or two rows have nothing to ask for ahead: fewer registers and a fifth block on each SM, once there
   // are more blocks than an SM holds.  256 windows of one row, bf16: 69 us against 79 (64 in fp32: 19.7
   // against 24.6); of 1 .. 8 rows 157 against 146; 8 windows of one row 4.3 against 3.9.

@@ -76,6 +76,11 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
   if (a.lse && lane == 0) a.lse[at] = (ref + log2f(sum)) * kLn2;
 }
 
+// The cache is read in blocks of 32 slots, or of a smaller page: fewer that nobody sees at a window's ends than with
+// blocks of up to 128 (page 128: 256 windows of 8 rows, window 1024, 187 us against 217; prompts with a window of 500
+// 118 against 152, without 318 against 326).
+constexpr int kMaxBlockShift = 5;
+
 // Workspace: status block | what each range left | partial rows | their log-sum-exps.
 struct AttnWs {
   size_t info, partial, plse, total;
@@ -112,7 +117,7 @@ bool encode_q(CUtensorMap* map, const void* base, int rows, int Hq, int D, int64
 
 size_t window_attention_ws_bytes(int Hq, int Hkv, int D) {
   size_t most = attn_ws(D, 2 * kTile, tch::sm_count()).total;  // any tiling
-  for (int rows = 16; rows <= kTile; rows *= 2)
+  for (int rows = 16; rows <= attention_window_rows(D); rows *= 2)
     most = std::max(most, attn_ws(D, rows, attention_window_sets(D, rows) * tch::sm_count()).total);
   return most;
 }
@@ -124,8 +129,12 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
                                     void* ws, cudaStream_t s) {
   AttnArgs a;
   const int n_cta = tch::sm_count(), g = Hq / Hkv, fit = kTile / g;
-  const bool prompts = max_rows > fit;  // more (token, head) rows than one tile of 128 holds
-  // short windows: the narrowest tile that holds the expected rows
+  // GB300, 64 requests over 3000 .. 5000 positions, 8 KV heads, D 128: 132 rows to a KV head, the prompts' kernel 192 us, the
+  // windows' 319; 128 rows 182 and 181; 80 rows 175 and 172 (256 requests, window 256: 152 and 128).  D 64: 80 rows
+  // 131 and 153 (window 256: 140 and 128); 64 rows 131 and 95.
+  const bool prompts = max_rows > attention_window_rows(D) / g;
+  // short windows: the narrowest tile that holds the expected rows.  256 requests, window 256, D 128, a row to a
+  // request (4 to a KV head): R = 16 58 us, 32 59, 64 88, 128 123
   int unit_rows = 16;
   while (!prompts && unit_rows < max_rows * g) unit_rows *= 2;
   if (prompts) unit_rows = 2 * kTile;
@@ -143,7 +152,7 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   // a hidden score is -inf before the scale: a scale of 0 becomes one that gives equal weights all the same
   // (2^(1e-30 s) is 1)
   if (a.c2 == 0.f) a.c2 = 1e-30f;
-  a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, prompts ? 7 : 5);
+  a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, kMaxBlockShift);
   a.bs = bs, a.rows = rows, a.Hq = Hq, a.Hkv = Hkv, a.g = g, a.tokens = prompts ? fit : std::min(unit_rows / g, std::max(max_rows, 1));
   a.window = window >= a.cache_limit ? 0 : window, a.n_sink = n_sink;
   CUtensorMap mq, mk, mv;
