@@ -29,7 +29,7 @@ struct AttnArgs {
   __nv_bfloat16* out;
   float* lse;
   uint32_t *status, *diag;
-  int4* info;       // per range: which partials it left
+  int4* info;       // per range: the unit that it began and did not finish
   float* partial;   // [2 ranges][rows of a unit][D] partial outputs, normalised
   float* plse;      // [2 ranges][rows of a unit] their log2-sum-exp
   uint64_t timeout_ns;
@@ -38,10 +38,10 @@ struct AttnArgs {
   int max_pages, n_pages, page_shift, block_shift, bs, rows, Hq, Hkv, g, tokens, window, n_sink;
 };
 
-// What a range v left for the join, as an int4: x = flags, then the unit that it began and did not finish.
-enum : int { kTailUsed = 1, kTailEnds = 2, kHeadUsed = 4 };
-// tail: the range began inside a unit (partial slot 2 v); head: it ends inside one that it began (slot
-// 2 v + 1).  y = packed row of the unit's first token, z = its tokens, w = its KV head.
+// What a range v leaves for the join.  Its rows of a unit that it began and did not finish are partial slot 2 v + 1,
+// those of a unit that an earlier range began slot 2 v.  info[v] is the unit that it began and did not finish: x =
+// how many ranges from v on have a part of it (0: there is no such unit), y = packed row of its first token,
+// z = its tokens, w = its KV head.
 
 // The KV tiles of one unit: its rows sit at positions p0 .. p1 and see, as a whole, the sinks and
 // lo .. p1.  Its blocks (pages, or 32-slot pieces of larger pages) in order: sink blocks 0 .. sb - 1,
@@ -161,8 +161,17 @@ struct PlanScratch {
 };
 // The whole block calls it, after one thread has cleared n_long, bad and the starts' counts and a
 // __syncthreads; the starts are there after the next one.
+struct Cut {
+  uint32_t each, extra;  // tiles of a range, and how many ranges (the first) have one more
+  // how many ranges from v on `tiles` tiles take
+  __device__ __forceinline__ int ranges(uint32_t v, uint32_t tiles) const {
+    const uint32_t big = v < extra ? extra - v : 0u;
+    if (tiles <= big * (each + 1)) return int((tiles + each) / (each + 1));
+    return int(big + (tiles - big * (each + 1) + each - 1) / each);
+  }
+};
 template <int kSets>
-__device__ __forceinline__ void plan_ranges(const AttnArgs& a, Start* start, PlanScratch& p, int unit_tokens) {
+__device__ __forceinline__ Cut plan_ranges(const AttnArgs& a, Start* start, PlanScratch& p, int unit_tokens) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int row = 0, n = 0, c = 0;
   uint32_t cost = 0;  // KV tiles of one KV head
@@ -246,6 +255,7 @@ __device__ __forceinline__ void plan_ranges(const AttnArgs& a, Start* start, Pla
     __syncwarp();
     if (lane == 0) g.t = t, g.tile = rem;
   }
+  return Cut{each, extra};
 }
 
 // One tile of a unit as the TMA warp loads it: lane i's block of the tile.

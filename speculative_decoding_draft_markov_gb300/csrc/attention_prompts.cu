@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   pdl_enter();
-  plan_ranges<1>(a, &sh->start, plan, unit_tokens);
+  const Cut cut = plan_ranges<1>(a, &sh->start, plan, unit_tokens);
   tc::fence_proxy_async_smem();  // the plan's scratch lies where TMA writes
   __syncthreads();
   const uint32_t tmem = sh->tmem_base;
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t keep = tc::policy_evict_last();
     Ring<C::kKSlots> kr;
     Ring<C::kVSlots> vr;
-    int seg_i = 0, flags = 0, n_k = 0, n_v = 0, q_use0 = 0, q_use1 = 0;
+    int seg_i = 0, n_k = 0, n_v = 0, q_use0 = 0, q_use1 = 0;
     int4 info = make_int4(0, 0, 0, 0);
     bool ok = true;
     Walk walk(sh->start, unit_tokens);
@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     while (ok && walk.next(a, s)) {
-      if (s.tile0 > 0) flags |= kTailUsed | (s.tile0 + s.n == s.u.ntiles ? kTailEnds : 0);
-      if (s.tile0 == 0 && s.n < s.u.ntiles) flags |= kHeadUsed, info = make_int4(0, s.row0, s.ntok, s.h);
+      if (s.tile0 == 0 && s.n < s.u.ntiles)
+        info = make_int4(1 + cut.ranges(blockIdx.x + 1, uint32_t(s.u.ntiles - s.n)), s.row0, s.ntok, s.h);
       TileLoad t0 = tile_load(a, s, 0, lane), t1 = t0;
       if (s.n > 1) t1 = tile_load(a, s, 1, lane);
       ok = put_k(t0) && put_q(0, q_use0, s.row0) && (s.ntok <= a.tokens || put_q(1, q_use1, s.row0 + a.tokens));
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (q_use1 > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[1]), (q_use1 - 1) & 1, dl, &never);
     }
     if (lane == 0) {
-      info.x = ok ? flags : 0;
+      if (!ok) info.x = 0;
       a.info[blockIdx.x] = info;
     }
   } else if (warp == 9) {

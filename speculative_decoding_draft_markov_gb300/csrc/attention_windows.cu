@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
   pdl_enter();
-  plan_ranges<kSets>(a, sh->start, plan, a.tokens);
+  const Cut cut = plan_ranges<kSets>(a, sh->start, plan, a.tokens);
   tc::fence_proxy_async_smem();  // the zeros, and the plan's scratch, which lies where TMA writes
   __syncthreads();
   const uint32_t tmem = sh->tmem_base;
@@ -176,11 +176,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------------------- TMA producer
     // In order: K 0, K 1, then V t, K t + 2, over all tiles of the range; a unit's Q with its first K.
     const int set = warp - kTmaWarp;
+    const uint32_t range = blockIdx.x + set * gridDim.x;
     const TmaWaiter wait{{&sh->abort, a.timeout_ns}};
     const uint64_t keep = tc::policy_evict_last(), stream = tc::policy_evict_first();
     uint8_t* ring_mem = sRing + set * C::kSlots * C::kSlotBytes;
     Ring<C::kSlots> ring;
-    int n_seg = 0, flags = 0, n_put = 0;
+    int n_seg = 0, n_put = 0;
     int4 info = make_int4(0, 0, 0, 0);
     Cursor cur(sh->start[set], a.tokens);
     struct Ahead {
@@ -195,10 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Segment& s = cur.s;
       f.t = tile_load(a, s, cur.j, lane);
       f.row0 = cur.first() ? s.row0 : -1;
-      if (cur.first()) {
-        if (s.tile0 > 0) flags |= kTailUsed | (s.tile0 + s.n == s.u.ntiles ? kTailEnds : 0);
-        if (s.tile0 == 0 && s.n < s.u.ntiles) flags |= kHeadUsed, info = make_int4(0, s.row0, s.ntok, s.h);
-      }
+      if (cur.first() && s.tile0 == 0 && s.n < s.u.ntiles)
+        info = make_int4(1 + cut.ranges(range + 1, uint32_t(s.u.ntiles - s.n)), s.row0, s.ntok, s.h);
       return f;
     };
     auto put = [&](const CUtensorMap* map, const Ahead& f) {
@@ -244,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[set][b]), ((n_seg - 1 - b) / C::kQBufs) & 1, dl, &never);
     }
     if (lane == 0) {
-      info.x = ok ? flags : 0;
-      a.info[blockIdx.x + set * gridDim.x] = info;
+      if (!ok) info.x = 0;
+      a.info[range] = info;
     }
   } else if (warp >= kMmaWarp && warp < kMmaWarp + kSets) {
     // ------------------------------------------------------------ the two products of each tile

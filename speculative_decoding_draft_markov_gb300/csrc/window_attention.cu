@@ -13,59 +13,52 @@ using namespace attn;
 // Joins the partial rows of the units that a cut between ranges runs through: block v takes the unit that
 // range v began and did not finish, in the order of its KV tiles.  One warp per row:
 //     out = sum_i 2^(lse_i - M) out_i / sum_i 2^(lse_i - M),   M = max_i lse_i
-// A chain of trips to memory (what the ranges left, the log-sum-exps, the rows), so each step's loads are issued
-// together, eight rows' pieces at a time.
-template <int D>
-__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int n_ranges, int unit_rows) {
-  constexpr int E = D / 32, kTogether = 8;
+// A chain of trips to memory (the unit, its parts, the row), so the parts' loads are issued kTogether at a time with
+// their log-sum-exps, under a running maximum: two with few registers, so that more rows are under way, or eight.
+// GB300, prompts of 4000 rows each: 13 us of the call's 306 (40 MB of partial rows), and 6 for the launch; 64 windows 3 and 5
+// of 83; one token 1 and 2 of 10.  Slower: blocks of 1024 threads that take a range's rows in turn (64 windows 88 us), and the warps of
+// a block sharing a row's parts (20.2 us where one token has 40 of them, against 15.9).
+template <int D, int kTogether>
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int unit_rows) {
+  constexpr int E = D / 32;
   pdl_enter();
   const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5), c = blockIdx.x;
   const int4 info = a.info[c];
-  int flags = c + 1 + lane < n_ranges ? a.info[c + 1 + lane].x : 0;
-  if (!(info.x & kHeadUsed)) return;
+  const int n = info.x;  // part 0 is the unit's rows in range c, part i those in range c + i
   const int tok = (row / kTile) * a.tokens + (row % kTile) / a.g, hh = (row % kTile) % a.g;
-  if (row % kTile >= a.tokens * a.g || tok >= info.z) return;
-  // part 0 is the head of c, part i the tail of c + i, up to the first range that finished the unit
-  int n = 0;
-  for (int base = c + 1;; base += 32) {
-    const uint32_t ends = __ballot_sync(~0u, flags & kTailEnds);
-    if (ends || base + 32 >= n_ranges) {
-      n = (ends ? base + __ffs(ends) - 1 : n_ranges - 1) - c + 1;
-      break;
-    }
-    flags = base + 32 + lane < n_ranges ? a.info[base + 32 + lane].x : 0;
-  }
-  auto part_row = [&](int i) { return int64_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * unit_rows + row; };
-  auto part_lse = [&](int i) {  // every range between has worked on the unit and on nothing else
-    return i < n ? a.plse[part_row(i)] : -INFINITY;
-  };
-  const float mine = part_lse(lane);
-  float top = mine;
-  for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, part_lse(i));
-  top = __shfl_sync(~0u, warp_max(top), 0);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float acc[E], sum = 0.f;
+  if (n == 0 || row % kTile >= a.tokens * a.g || tok >= info.z) return;
+  float ref = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int base = 0; base < n; base += 32) {
-    const float w_mine = exp2f((base == 0 ? mine : part_lse(base + lane)) - ref);  // 0: nothing seen there
-    for (int i0 = 0; i0 < min(32, n - base); i0 += kTogether) {
-      float v[kTogether][E], w[kTogether];
+  for (int i0 = 0; i0 < n; i0 += kTogether) {
+    float v[kTogether][E], lse[kTogether];
 #pragma unroll
-      for (int k = 0; k < kTogether; ++k) {
-        w[k] = __shfl_sync(~0u, w_mine, i0 + k);  // beyond the last part: 0, and the last part's row again
-        const float* src = a.partial + part_row(min(base + i0 + k, n - 1)) * D + lane * E;
-        if constexpr (E == 4)
-          *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(src);
-        else
-          *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
-      }
+    for (int k = 0; k < kTogether; ++k) {
+      lse[k] = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kTogether; ++k) {
-        sum += w[k];
+      for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+      if (i0 + k >= n) continue;
+      const int64_t at = int64_t(i0 + k == 0 ? 2 * c + 1 : 2 * (c + i0 + k)) * unit_rows + row;
+      lse[k] = a.plse[at];
+      if constexpr (E == 4)
+        *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(a.partial + at * D + lane * E);
+      else
+        *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(a.partial + at * D + lane * E);
+    }
+    float top = ref;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = w[k] == 0.f ? acc[e] : fmaf(w[k], v[k][e], acc[e]);
-      }
+    for (int k = 0; k < kTogether; ++k) top = fmaxf(top, lse[k]);
+    const float base = top == -INFINITY ? 0.f : top, keep = exp2f(ref - base);
+    ref = top;
+    sum *= keep;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= keep;
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k) {
+      const float w = exp2f(lse[k] - base);  // 0: nothing seen there
+      sum += w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = w == 0.f ? acc[e] : fmaf(w, v[k][e], acc[e]);
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -164,9 +157,13 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   const cudaError_t e = prompts ? launch_attention_prompts(D, mq, mk, mv, a, n_cta, s)
                                 : launch_attention_windows(D, unit_rows, mq, mk, mv, a, n_cta, s);
   if (e != cudaSuccess) return e;
+  // A unit is cut about once where units outnumber the ranges (64 windows over up to 32000 positions: two parts at a time 83.2
+  // us, eight 85.1; prompts 306 and 316), and often where there are few (one token over 5000 positions: 20.4 and 16.9).
+  const bool many_parts = n_ranges > 4 * Hkv * std::max(bs, rows / (prompts ? 2 * a.tokens : a.tokens));
   const dim3 grid(n_ranges, ((prompts ? kTile : 0) + a.tokens * g + 7) / 8);
-  return D == 64 ? launch_pdl(attention_join_kernel<64>, grid, dim3(256), 0, s, a, n_ranges, unit_rows)
-                 : launch_pdl(attention_join_kernel<128>, grid, dim3(256), 0, s, a, n_ranges, unit_rows);
+  auto join = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, a, unit_rows); };
+  if (many_parts) return D == 64 ? join(attention_join_kernel<64, 8>) : join(attention_join_kernel<128, 8>);
+  return D == 64 ? join(attention_join_kernel<64, 2>) : join(attention_join_kernel<128, 2>);
 }
 
 }  // namespace dspark
