@@ -342,9 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk walk(sh->start[set], a.tokens);
     Segment s = {};
     // the group's four warps: everything before on all of them is visible after
-    auto meet = [&]() {
+    auto arrive = [&]() {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->group[grp]));
+    };
+    auto meet = [&]() {
+      arrive();
       return wait(&sh->group[grp], sync++ & 1);
     };
     while (ok && walk.next(a, s)) {
@@ -389,13 +392,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return top;
         };
+        auto weigh = [&]() {
+#pragma unroll
+          for (int i = 0; i < RW; ++i) y[i] = tc::ex2_approx(y[i]);
+        };
         load_scores();
         bool fresh = j == 0;  // a new reference is needed
         if (j > 0) {
           const float top = refer();
           const int at = sync & 1;
           if (__any_sync(~0u, top > kRescaleAt) && lane == 0) sh->need[grp][at] = t + 1;
-          ok = meet();
+          arrive();
+          weigh();  // while the others arrive; done again where the reference moves
+          ok = wait(&sh->group[grp], sync++ & 1);
           if (!ok) break;
           fresh = sh->need[grp][at] == t + 1;
           if (fresh) load_scores();
@@ -432,13 +441,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           load_scores();
           refer();
+          weigh();
         }
         uint32_t pk[RW / 2];
 #pragma unroll
         for (int i = 0; i < RW; i += 2) {
-          const float e0 = tc::ex2_approx(y[i]), e1 = tc::ex2_approx(y[i + 1]);
-          l[i] += e0, l[i + 1] += e1;
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
+          l[i] += y[i], l[i + 1] += y[i + 1];
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(y[i], y[i + 1]);
           pk[i / 2] = *reinterpret_cast<const uint32_t*>(&h2);
         }
         ok = wait(&sh->p_empty[set], (t & 1) ^ 1);
