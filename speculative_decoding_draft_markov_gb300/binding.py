@@ -371,62 +371,29 @@ def dspark_sts_fit(z, ceiling, grid, n_bins, T_out, ece_out, ws=None, stream=Non
 
 # ----------------------------------------------------------------- the target model's side
 #
-# These calls are made per layer and per token, so their checks are kept cheap: the tensors' types and
-# shapes, which the library cannot see behind bare pointers.
+# These calls are made per layer and per token, so their checks (the tensors' types and shapes, which the library
+# cannot see behind bare pointers) and the calls themselves are compiled (csrc/calls.cpp).
 
-_T = None  # torch's types, once torch is in use
+_CALLS = None
 
 
-class _Types:
-    def __init__(self):
+def _calls():
+    """The compiled calls, loaded on first use."""
+    global _CALLS
+    if _CALLS is None:
+        import importlib.util
         import torch
-        self.i32, self.f32, self.i16 = torch.int32, torch.float32, torch.int16
-        self.dtypes = {torch.float32: DSPARK_F32, torch.bfloat16: DSPARK_BF16}
-        self.raw_stream, self.device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
-
-
-def _types() -> _Types:
-    global _T
-    if _T is None:
-        _T = _Types()
-    return _T
-
-
-def _bad(what: str):
-    raise ValueError(what)
-
-
-def _ptr(t, dtype, shape, name: str) -> Optional[int]:
-    """The pointer of a dense tensor of that type and shape (shape None: any); None stays None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        _bad(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and t.shape != shape:
-        _bad(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        _bad(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows_ptr(t, dtype, shape, name: str):
-    """Pointer and elements from row to row of a [rows, H, D] tensor whose heads and lanes are dense."""
-    if t.dtype is not dtype:
-        _bad(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        _bad(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    rows, H, D = shape
-    row, head, lane = t.stride()
-    if lane != 1 or (head != D and H > 1):
-        _bad(f"{name} must be [rows, heads, lanes] with dense heads and lanes")
-    return t.data_ptr(), row if rows > 1 else H * D
-
-
-def _call(name: str, T: _Types, stream, *args) -> None:
-    s = T.raw_stream(T.device()) if stream is None else _stream(stream)
-    rc = getattr(_LIB or lib(), name)(*args, s)
-    if rc != DSPARK_OK:
-        raise DSparkError(rc, name)
+        path = os.path.join(os.path.dirname(library_path()), "_calls.so")
+        lib()
+        if not os.path.exists(path):
+            raise RuntimeError(f"_calls.so is not built ({path}); run __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("_calls", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.init(torch.float32, torch.bfloat16, torch.int32, torch.int16, torch._C._cuda_getCurrentRawStream,
+                 torch.cuda.current_device, DSparkError)
+        _CALLS = mod
+    return _CALLS
 
 
 def dspark_append_kv(q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k_cache, v_cache, ws,
@@ -435,23 +402,8 @@ def dspark_append_kv(q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k
     q, k, v [rows, heads, D] (rows may be strided: parts of one projection); cos_sin [max_pos, rot] fp32;
     page_table [bs, max_pages] int32; k_cache, v_cache [n_pages, Hkv, page_size, D]; q_out [rows, Hq, D]
     (q and q_out may both be None)."""
-    T = _T or _types()
-    cache, dt = k_cache.shape, k_cache.dtype
-    n_pages, Hkv, page, D = cache
-    rows, bs, max_pages = k.shape[0], cu_seqlens.shape[0] - 1, page_table.shape[-1]
-    Hq, qp, qs, qo = Hkv, None, 0, None
-    if q is not None:
-        Hq = q.shape[1]
-        qp, qs = _rows_ptr(q, dt, (rows, Hq, D), "q")
-        qo = _ptr(q_out, dt, (rows, Hq, D), "q_out")
-    kp, ks = _rows_ptr(k, dt, (rows, Hkv, D), "k")
-    vp, vs = _rows_ptr(v, dt, (rows, Hkv, D), "v")
-    max_pos, rot = cos_sin.shape
-    _call("dspark_append_kv", T, stream, qp, qs, kp, ks, vp, vs, T.dtypes.get(dt, -1),
-          _ptr(cu_seqlens, T.i32, None, "cu_seqlens"), _ptr(ctx_len, T.i32, (bs,), "ctx_len"), bs, rows,
-          _ptr(cos_sin, T.f32, None, "cos_sin"), max_pos, rot, interleaved,
-          _ptr(page_table, T.i32, (bs, max_pages), "page_table"), max_pages, n_pages, page, Hq, Hkv, D, qo,
-          _ptr(k_cache, dt, None, "k_cache"), _ptr(v_cache, dt, cache, "v_cache"), ws.data_ptr(), ws.numel())
+    (_CALLS or _calls()).append_kv(q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k_cache, v_cache, ws,
+                                   interleaved, stream)
 
 
 def dspark_window_attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
@@ -472,16 +424,8 @@ def dspark_window_attention(q, k_cache, v_cache, page_table, cu_seqlens, ctx_len
     """Attention of the packed rows q [rows, Hq, D] over the paged cache: a sliding window (0: everything)
     and the first n_sink tokens.  out [rows, Hq, D]; lse [rows, Hq] fp32 or None; max_rows: the longest
     window expected (it only picks the tiling)."""
-    T = _T or _types()
-    cache, dt, qshape = k_cache.shape, k_cache.dtype, q.shape
-    n_pages, Hkv, page, D = cache
-    rows, Hq, bs, max_pages = qshape[0], qshape[1], cu_seqlens.shape[0] - 1, page_table.shape[-1]
-    qp, qs = _rows_ptr(q, dt, (rows, Hq, D), "q")
-    _call("dspark_window_attention", T, stream, qp, qs, T.dtypes.get(dt, -1), _ptr(k_cache, dt, None, "k_cache"),
-          _ptr(v_cache, dt, cache, "v_cache"), _ptr(page_table, T.i32, (bs, max_pages), "page_table"), max_pages,
-          n_pages, page, _ptr(cu_seqlens, T.i32, None, "cu_seqlens"), _ptr(ctx_len, T.i32, (bs,), "ctx_len"), bs, rows,
-          max_rows, Hq, Hkv, D, scale, window, n_sink, _ptr(out, dt, qshape, "out"),
-          _ptr(lse, T.f32, (rows, Hq), "lse"), ws.data_ptr(), ws.numel())
+    (_CALLS or _calls()).window_attention(q, k_cache, v_cache, page_table, cu_seqlens, ctx_len, max_rows, scale, window,
+                                          n_sink, out, lse, ws, stream)
 
 
 def dspark_process_logits(logits, cu_seqlens, ids, hist, repetition, frequency, presence, bias_start, bias_ids,
@@ -489,36 +433,16 @@ def dspark_process_logits(logits, cu_seqlens, ids, hist, repetition, frequency, 
     """Penalties, biases and grammar masks on the packed target rows logits [rows, V] (out may be logits):
     hist [bs, V] int16 (dspark_history_build) or None; repetition / frequency / presence [bs] fp32 or None;
     bias_start [bs + 1], bias_ids, bias_vals or None; mask [rows, ceil(V / 32)] int32 words or None."""
-    T = _T or _types()
-    shape, dt = logits.shape, logits.dtype
-    rows, V = shape
-    bs = cu_seqlens.shape[0] - 1
-    if ids.shape[0] < rows:
-        _bad("ids must hold one entry per row")
-    _call("dspark_process_logits", T, stream, _ptr(logits, dt, None, "logits"), T.dtypes.get(dt, -1), rows, V,
-          _ptr(cu_seqlens, T.i32, None, "cu_seqlens"), _ptr(ids, T.i32, None, "ids"), bs,
-          _ptr(hist, T.i16, (bs, V), "hist"), _ptr(repetition, T.f32, (bs,), "repetition"),
-          _ptr(frequency, T.f32, (bs,), "frequency"), _ptr(presence, T.f32, (bs,), "presence"),
-          _ptr(bias_start, T.i32, (bs + 1,), "bias_start"), _ptr(bias_ids, T.i32, None, "bias_ids"),
-          _ptr(bias_vals, T.f32, None if bias_ids is None else bias_ids.shape, "bias_vals"),
-          0 if bias_ids is None else bias_ids.numel(), _ptr(mask, T.i32, (rows, (V + 31) // 32), "mask"),
-          _ptr(out, dt, shape, "out"), ws.data_ptr(), ws.numel())
+    (_CALLS or _calls()).process_logits(logits, cu_seqlens, ids, hist, repetition, frequency, presence, bias_start,
+                                        bias_ids, bias_vals, mask, out, ws, stream)
 
 
 def dspark_history_build(tokens, start, n_prompt, hist, ws, stream=None):
     """Rewrite hist [bs, V] int16 from token lists: request r's are tokens[start[r] : start[r + 1]], the first
     n_prompt[r] of them its prompt."""
-    T = _T or _types()
-    bs, V = hist.shape
-    _call("dspark_history_build", T, stream, _ptr(tokens, T.i32, None, "tokens"), tokens.numel(),
-          _ptr(start, T.i32, (bs + 1,), "start"), _ptr(n_prompt, T.i32, (bs,), "n_prompt"), bs, V,
-          _ptr(hist, T.i16, None, "hist"), ws.data_ptr(), ws.numel())
+    (_CALLS or _calls()).history_build(tokens, start, n_prompt, hist, ws, stream)
 
 
 def dspark_history_commit(out_tokens, hist, ws, stream=None):
     """Add a step's out_tokens [bs, gamma + 1] (dspark_verify; -1 skipped) to the said counts of hist [bs, V]."""
-    T = _T or _types()
-    bs, V = hist.shape
-    width = out_tokens.shape[-1]
-    _call("dspark_history_commit", T, stream, _ptr(out_tokens, T.i32, (bs, width), "out_tokens"), bs, width - 1, V,
-          _ptr(hist, T.i16, None, "hist"), ws.data_ptr(), ws.numel())
+    (_CALLS or _calls()).history_commit(out_tokens, hist, ws, stream)

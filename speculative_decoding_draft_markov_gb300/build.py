@@ -2,7 +2,8 @@
 
 Each .cu file compiles in its own nvcc process (in parallel), then one link step makes
 speculative_decoding_draft_markov_gb300/lib/libdspark.so.  No cmake, no torch extension:
-the library exports a plain C ABI (include/dspark.h)."""
+the library exports a plain C ABI (include/dspark.h).  Beside it lib/_calls.so (csrc/calls.cpp, the
+CPython C API): the Python calls that are made per layer and per token."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libdspark.so")
+CALLS = os.path.join(LIBDIR, "_calls.so")
 SOURCES = ["api.cu", "draft.cu", "draft_tc.cu", "decide_tc.cu", "sched_pack.cu", "verify.cu", "draft_noalloc.cu", "rnn.cu",
            "observe.cu", "serve_api.cu", "kv_append.cu", "window_attention.cu", "attention_windows.cu", "attention_prompts.cu",
            "logit_rules.cu"]
@@ -63,6 +66,14 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if res.returncode != 0:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError("link of libdspark.so failed")
+    src = os.path.join(CSRC, "calls.cpp")
+    if force or not _newer(CALLS, [src, os.path.join(ROOT, "include", "dspark.h")]):
+        cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I" + os.path.join(ROOT, "include"),
+               "-I" + sysconfig.get_paths()["include"], src, "-o", CALLS, "-L" + LIBDIR, "-ldspark", "-Wl,-rpath,$ORIGIN"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            sys.stderr.write(res.stdout + res.stderr)
+            raise RuntimeError("build of _calls.so failed")
     return LIB
 
 
