@@ -7,7 +7,16 @@
 // the other tile's two products, so its first half is handed on as soon as it is there, computed by the
 // reference m as it stands while the row's maximum is found: m only keeps the exponentials in range, and
 // any value within 2^60 of the maximum gives the same result, since the sum is divided out and neither fp32 nor
-// bf16 loses bits there.  It moves, and O and l are rescaled, when a maximum has outgrown it by more.
+// bf16 loses bits there.  It moves, and O and l are rescaled, when a maximum has outgrown it by more.  P is rounded to
+// bf16 for the second product, its sum is taken before that, in fp32.
+//
+// GB300, 2 prompts of about 4000 rows over 1000 .. 5000 cached positions, window 4096, Hq 32, Hkv 8: D 128 303 us of 238 at the
+// measured matrix rate (79%), 19 us of it the join and its launch; D 64 292 us (132 by its products, 206 by its exponentials at
+// 16 a cycle and SM).  What holds it is the chain of one tile, S into registers, maximum, exponentials, P, product,
+// next S, which two tiles in turn do not quite hide (tensor pipes 62% busy, 4.4 instructions an exponential).  Slower or the
+// same, each measured on D 128: P handed on in 4 or 8 parts (338, 389 us); all eight warps on each tile together
+// (356); a polynomial for an eighth to a half of the exponentials (319 .. 365; D 64 with an eighth 280, not kept for one
+// head size); the first half's store waited for later, and the MMA loop in one thread (no change).
 #include <type_traits>
 
 #include "attention_common.cuh"

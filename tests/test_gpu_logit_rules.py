@@ -112,6 +112,16 @@ def test_rules_many_short_windows(dtype):
     assert st == B.DSPARK_OK and torch.equal(got, out)
 
 
+@pytest.mark.parametrize("bs,n,V,dtype", [(130, 4, 10248, torch.bfloat16), (128, 16, 8192, torch.float32)])
+def test_rules_large_batches(bs, n, V, dtype):
+    """More blocks than the SMs hold: a window's rows in one block, or shared by two."""
+    rng = np.random.default_rng(bs)
+    b = Batch([int(x) for x in rng.integers(n // 2, n + n // 2 + 1, bs)], V, dtype, seed=38, n_bias=2)
+    out, st = b.call()
+    assert st == B.DSPARK_OK
+    b.check(out)
+
+
 @pytest.mark.parametrize("n_bias", [60, 65, 700, 5000])
 def test_rules_many_biases(n_bias):
     """Lists that a warp searches in one, two and more steps, as long as the vocabulary at last."""
