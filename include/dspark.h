@@ -507,6 +507,7 @@ DSPARK_API int dspark_window_attention(const void* q, int64_t q_stride, int dtyp
  *   repetition, frequency, presence  device [bs] fp32, or NULL each: 1, 0, 0
  *   bias_start   device [bs + 1] int32, bias_ids / bias_vals device int32 / fp32: request r's biases are
  *                entries bias_start[r] .. bias_start[r+1] - 1 of n_bias, ids strictly increasing; all NULL: none
+ *                (n_bias = 0: bias_ids and bias_vals may be NULL)
  *   mask         device [rows, ceil(V / 32)] uint32, bit v % 32 of word v / 32 set where v is allowed; or NULL
  * Device errors (status word, EINVAL): cu_seqlens decreasing or beyond rows (the request is skipped),
  * a drafted id outside [0, V) (not counted), bias ids not strictly increasing or outside [0, V), a

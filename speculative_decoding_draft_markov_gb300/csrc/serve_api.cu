@@ -108,8 +108,8 @@ int dspark_process_logits(const void* logits, int dtype, int rows, int V, const 
   if (int e = check_vocab(bs, V)) return e;
   if (!al(logits, 16) || !al(out, 16) || !al(hist, 16) || !al(mask, 4)) return DSPARK_EINVAL;
   if (!hist && (repetition || frequency || presence)) return DSPARK_EINVAL;  // penalties of what?
-  if ((bias_start == nullptr) != (bias_ids == nullptr) || (bias_start == nullptr) != (bias_vals == nullptr))
-    return DSPARK_EINVAL;
+  if (!bias_start && (bias_ids || bias_vals)) return DSPARK_EINVAL;
+  if (bias_start && n_bias != 0 && (!bias_ids || !bias_vals)) return DSPARK_EINVAL;
   if (n_bias < 0 || !al(bias_start, 4) || !al(bias_ids, 4) || !al(bias_vals, 4)) return DSPARK_EINVAL;
   if (int e = check_status_ws(ws, ws_bytes)) return e;
   return cuda_status(launch_process_logits(logits, dtype, rows, V, cu_seqlens, ids, bs, hist, repetition, frequency,

@@ -159,7 +159,7 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   if (e != cudaSuccess) return e;
   // A unit is cut about once where units outnumber the ranges (64 windows over up to 32000 positions: two parts at a time 83.2
   // us, eight 85.1; prompts 306 and 316), and often where there are few (one token over 5000 positions: 20.4 and 16.9).
-  const bool many_parts = n_ranges > 4 * Hkv * std::max(bs, rows / (prompts ? 2 * a.tokens : a.tokens));
+  const bool many_parts = n_ranges > int64_t(4) * Hkv * std::max(bs, rows / (prompts ? 2 * a.tokens : a.tokens));
   const dim3 grid(n_ranges, ((prompts ? kTile : 0) + a.tokens * g + 7) / 8);
   auto join = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, a, unit_rows); };
   if (many_parts) return D == 64 ? join(attention_join_kernel<64, 8>) : join(attention_join_kernel<128, 8>);

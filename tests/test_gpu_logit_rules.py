@@ -216,6 +216,16 @@ def test_rules_bias_entries_out_of_range():
                 assert torch.equal(out[rows], good[rows])
 
 
+def test_rules_empty_bias_lists():
+    """A batch whose requests have no biases right now: lists that are there and empty."""
+    b = Batch([3, 2, 4], 512, torch.bfloat16, seed=39, n_bias=9)
+    none, st = b.call(bias_start=None, bias_ids=None, bias_vals=None)
+    assert st == B.DSPARK_OK
+    out, st = b.call(bias_start=_dev([0, 0, 0, 0], torch.int32), bias_ids=torch.empty(0, dtype=torch.int32, device="cuda"),
+                     bias_vals=torch.empty(0, device="cuda"))
+    assert st == B.DSPARK_OK and torch.equal(out, none)
+
+
 # ------------------------------------------------------------------------------ history
 
 @pytest.mark.parametrize("V", [8, 2048, 5000, 16392])
