@@ -21,6 +21,7 @@ namespace dspark {
 namespace attn {
 
 constexpr int kTile = 128;  // KV slots per tile
+constexpr int kJoinTogether = 16;  // parts of a row that the join reads at a time, where they are many
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnArgs {
@@ -221,11 +222,18 @@ __device__ __forceinline__ Cut plan_ranges(const AttnArgs& a, Start* start, Plan
   }
   const bool too_much = total >> 31 != 0;  // counted in 32 bits
   if (tid == 0 && blockIdx.x == 0 && (p.bad || too_much)) set_status(a.status, DSPARK_EINVAL);
-  const uint32_t all = too_much ? 0u : uint32_t(total), n_ranges = kSets * gridDim.x;
-  const uint32_t each = all / n_ranges, extra = all - each * n_ranges, first = uint32_t(before + incl - mine);
+  const uint32_t all = too_much ? 0u : uint32_t(total);
+  // A unit of T tiles in ranges of m has T / m parts, which the join reads kJoinTogether at a time, one trip to memory each, and
+  // a trip takes about as long as a tile: m >= sqrt(T / kJoinTogether), T the mean over requests and KV heads.  GB300, one
+  // token over 50000 positions, 1 KV head: 18.0 us, cut as finely as there are CTAs 30.3; 8 KV heads over 5000 14.2 and 16.4,
+  // over 1500 the same.
+  const uint32_t least = max(1u, uint32_t(ceilf(sqrtf(float(all) / (float(a.Hkv) * float(a.bs * kJoinTogether))))));
+  const uint32_t n_ranges = min(kSets * gridDim.x, (all + least - 1) / least), some = max(n_ranges, 1u);
+  const uint32_t each = all / some, extra = all - each * some, first = uint32_t(before + incl - mine);
 #pragma unroll
   for (int set = 0; set < kSets; ++set) {
-    const uint32_t v = blockIdx.x + set * gridDim.x, w0 = each * v + min(v, extra), count = each + (v < extra ? 1u : 0u);
+    const uint32_t v = blockIdx.x + set * gridDim.x, w0 = each * v + min(v, extra);
+    const uint32_t count = v < n_ranges ? each + (v < extra ? 1u : 0u) : 0u;
     if (count > 0 && w0 >= first && w0 - first < uint32_t(mine)) {  // this thread's request
       const uint32_t h = (w0 - first) / cost;
       start[set] = Start{tid, int(h), 0, int(w0 - first - h * cost), row, n, c, count};

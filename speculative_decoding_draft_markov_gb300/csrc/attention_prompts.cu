@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // wait (bounded) for every copy in flight before the CTA exits
       const volatile int never = 0;
       const long long dl = tc::deadline_after_ns(200000000ull);
-      // slots before the ring's position were last used in this round, the others in the last one
+      // slots before the ring's position were last used in this turn of the ring, the others in the last one
       for (int i = 0; i < min(n_k, C::kKSlots); ++i)
         tc::mbar_wait_bounded(tc::smem_u32(&sh->k_full[i]), i < kr.slot ? kr.phase : kr.phase ^ 1, dl, &never);
       for (int i = 0; i < min(n_v, C::kVSlots); ++i)

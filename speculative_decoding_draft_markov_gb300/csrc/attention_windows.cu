@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // wait (bounded) for every copy in flight before the CTA exits
       const volatile int never = 0;
       const long long dl = tc::deadline_after_ns(200000000ull);
-      // slots before the ring's position were last used in this round, the others in the last one
+      // slots before the ring's position were last used in this turn of the ring, the others in the last one
       for (int i = 0; i < min(n_put, C::kSlots); ++i)
         tc::mbar_wait_bounded(tc::smem_u32(&sh->full[set][i]), i < ring.slot ? ring.phase : ring.phase ^ 1, dl, &never);
       for (int b = 0; b < min(n_seg, C::kQBufs); ++b)  // the last unit whose Q went to b

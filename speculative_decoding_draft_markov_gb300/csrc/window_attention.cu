@@ -14,7 +14,7 @@ using namespace attn;
 // range v began and did not finish, in the order of its KV tiles.  One warp per row:
 //     out = sum_i 2^(lse_i - M) out_i / sum_i 2^(lse_i - M),   M = max_i lse_i
 // A chain of trips to memory (the unit, its parts, the row), so the parts' loads are issued kTogether at a time with
-// their log-sum-exps, under a running maximum: two with few registers, so that more rows are under way, or eight.
+// their log-sum-exps, under a running maximum: two with few registers, so that more rows are under way, or sixteen.
 // GB300, prompts of 4000 rows each: 13 us of the call's 306 (40 MB of partial rows), and 6 for the launch; 64 windows 3 and 5
 // of 83; one token 1 and 2 of 10.  Slower: blocks of 1024 threads that take a range's rows in turn (64 windows 88 us), and the warps of
 // a block sharing a row's parts (20.2 us where one token has 40 of them, against 15.9).
@@ -158,11 +158,12 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
                                 : launch_attention_windows(D, unit_rows, mq, mk, mv, a, n_cta, s);
   if (e != cudaSuccess) return e;
   // A unit is cut about once where units outnumber the ranges (64 windows over up to 32000 positions: two parts at a time 83.2
-  // us, eight 85.1; prompts 306 and 316), and often where there are few (one token over 5000 positions: 20.4 and 16.9).
+  // us, eight 85.1; prompts 306 and 316), and often where there are few (one token over 5000 positions: two 20.4, four 19.1,
+  // eight 16.9).
   const bool many_parts = n_ranges > int64_t(4) * Hkv * std::max(bs, rows / (prompts ? 2 * a.tokens : a.tokens));
   const dim3 grid(n_ranges, ((prompts ? kTile : 0) + a.tokens * g + 7) / 8);
   auto join = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, a, unit_rows); };
-  if (many_parts) return D == 64 ? join(attention_join_kernel<64, 8>) : join(attention_join_kernel<128, 8>);
+  if (many_parts) return D == 64 ? join(attention_join_kernel<64, kJoinTogether>) : join(attention_join_kernel<128, kJoinTogether>);
   return D == 64 ? join(attention_join_kernel<64, 2>) : join(attention_join_kernel<128, 2>);
 }
 
