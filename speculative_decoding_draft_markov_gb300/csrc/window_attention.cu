@@ -159,8 +159,9 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   if (e != cudaSuccess) return e;
   // A unit is cut about once where units outnumber the ranges (64 windows over up to 32000 positions: two parts at a time 83.2
   // us, eight 85.1; prompts 306 and 316), and often where there are few (one token over 5000 positions: two 20.4, four 19.1,
-  // eight 16.9).
-  const bool many_parts = n_ranges > int64_t(4) * Hkv * std::max(bs, rows / (prompts ? 2 * a.tokens : a.tokens));
+  // eight 16.9).  A prompt has so many rows that their number counts for more than their parts (500 rows: two 22.8, sixteen
+  // 28.0; 100 over 50000 positions: 42.7 and 40.3).
+  const bool many_parts = !prompts && n_ranges > int64_t(4) * Hkv * std::max(bs, rows / a.tokens);
   const dim3 grid(n_ranges, ((prompts ? kTile : 0) + a.tokens * g + 7) / 8);
   auto join = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, a, unit_rows); };
   if (many_parts) return D == 64 ? join(attention_join_kernel<64, kJoinTogether>) : join(attention_join_kernel<128, kJoinTogether>);
