@@ -21,10 +21,11 @@
 //
 // GB300, D 128, 8 KV heads: 2 requests of 16 rows over 125000 positions 152 us (1.02 GB of K and V, 6.7 TB/s: 99% of the
 // measured copy bandwidth); 256 of 8 rows, window 4096, 636 us; window 1024, 184 us (90%), where the ~20 us of
-// launches, the cut of the work, first loads and join are a tenth; one token over 1500 positions 10 us, nearly all of
+// launches, the cut of the work, first loads and join are a tenth; one token over 1500 positions 9 us, nearly all of
 // it those.  D 64, 64 rows to a KV head: 135 us of 85 (61%): softmax-bound, a warp's chain through a tile (its
 // stalls: tensor memory and barriers 3.5 cycles an instruction, fixed latencies 1.8).  Slower there, each measured: sums in packed pairs and
-// three-way maxima (140 us); one pipeline in place of two (window 4096: 417 us, 344).  With rows on lanes, window 1024: 304 us,
+// three-way maxima (140 us); a unit's rows read after the next one's first tile (139); each step of a tile once, in a loop of rounds
+// (154); sums after P is handed on (144); one pipeline in place of two (window 4096: 417 us, 344).  With rows on lanes, window 1024: 304 us,
 // transposed 206, all before the second pipeline.
 #include "attention_common.cuh"
 

@@ -1,6 +1,6 @@
 // The Python calls of the target model's side, which are made per layer and per token: arguments are checked
 // (tensors' types, shapes and strides, which the C ABI cannot see behind bare pointers), handed to the C ABI, and a
-// status other than DSPARK_OK is raised.  GB300's host: 5.9 us for an append, 7.5 for an attention (its two launches and
+// status other than DSPARK_OK is raised.  GB300's host: 5.6 us for an append, 7.6 for an attention (its two launches and
 // three tensor maps), 5.9 for the logit rules; through ctypes, with the checks in Python, 10.0, 11.7 and 9.2, more
 // than the GPU spends on one token.
 #define PY_SSIZE_T_CLEAN

@@ -16,7 +16,7 @@ using namespace attn;
 // A chain of trips to memory (the unit, its parts, the row), so the parts' loads are issued kTogether at a time with
 // their log-sum-exps, under a running maximum: two with few registers, so that more rows are under way, or sixteen.
 // GB300, prompts of 4000 rows each: 13 us of the call's 306 (40 MB of partial rows), and 6 for the launch; 64 windows 3 and 5
-// of 83; one token 1 and 2 of 10.  Slower: blocks of 1024 threads that take a range's rows in turn (64 windows 88 us), and the warps of
+// of 83; one token 1 and 2 of 9.  Slower: blocks of 1024 threads that take a range's rows in turn (64 windows 88 us), and the warps of
 // a block sharing a row's parts (20.2 us where one token has 40 of them, against 15.9).
 template <int D, int kTogether>
 __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int unit_rows) {
