@@ -51,7 +51,7 @@ struct Geom {
   int p0, p1, lo, sb, wb0, nblk, ntiles;
 };
 
-__device__ __forceinline__ Geom unit_geom(const AttnArgs& a, int c, int n, int t, int unit_tokens) {
+__host__ __device__ __forceinline__ Geom unit_geom(const AttnArgs& a, int c, int n, int t, int unit_tokens) {
   Geom u;
   u.p0 = c + t * unit_tokens;
   u.p1 = c + min((t + 1) * unit_tokens, n) - 1;
@@ -64,7 +64,7 @@ __device__ __forceinline__ Geom unit_geom(const AttnArgs& a, int c, int n, int t
   return u;
 }
 // Position of the first slot of block v of a unit.
-__device__ __forceinline__ int block_pos(const AttnArgs& a, const Geom& u, int v) {
+__host__ __device__ __forceinline__ int block_pos(const AttnArgs& a, const Geom& u, int v) {
   return (v < u.sb ? v : v - u.sb + u.wb0) << a.block_shift;
 }
 
@@ -80,14 +80,14 @@ struct Start {
   uint32_t count;  // KV tiles
 };
 
-// Walks a range; every role of a pipeline walks the same one.
+// Walks a range; every role of a pipeline walks the same one.  After its end it stays at its end.
 struct Walk {
   int r, h, t, tile, unit_tokens;
   uint32_t left;
   int loaded, row, n, c;
-  __device__ Walk(const Start& g, int ut)
+  __host__ __device__ Walk(const Start& g, int ut)
       : r(g.r), h(g.h), t(g.t), tile(g.tile), unit_tokens(ut), left(g.count), loaded(g.r), row(g.row), n(g.n), c(g.c) {}
-  __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
+  __host__ __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
     if (left == 0) return false;
     while (loaded != r) {  // the next request with something to do
       if (r >= a.bs) return false;
@@ -115,6 +115,40 @@ struct Walk {
     return true;
   }
 };
+
+// The tiles of a range one by one.  After the last tile `next` is false however often it is called.
+struct Cursor {
+  Walk walk;
+  Segment s = {};
+  int j = 0;
+  __host__ __device__ Cursor(const Start& g, int unit_tokens) : walk(g, unit_tokens) {}
+  __host__ __device__ __forceinline__ bool next(const AttnArgs& a) {
+    if (j + 1 < s.n) {
+      ++j;
+      return true;
+    }
+    if (!walk.next(a, s)) return false;
+    j = 0;
+    return true;
+  }
+  __host__ __device__ __forceinline__ bool first() const { return j == 0; }
+  __host__ __device__ __forceinline__ bool last() const { return j + 1 == s.n; }
+};
+
+// The order in which the tiles of a range are loaded: K 0, K 1, then V t, K t + 2.  fetch() describes the next tile
+// (`there` false after the last, as often as it is asked), three tiles before its V is put; put_k and put_v say
+// whether to go on.  Every load is waited for by the products, which take the same tiles in the same order.
+#pragma nv_exec_check_disable
+template <typename Fetch, typename PutK, typename PutV>
+__host__ __device__ __forceinline__ bool load_in_order(Fetch fetch, PutK put_k, PutV put_v) {
+  auto f0 = fetch(), f1 = fetch(), f2 = fetch(), f3 = fetch();
+  bool ok = (!f0.there || put_k(f0)) && (!f1.there || put_k(f1));
+  while (ok && f0.there) {
+    ok = put_v(f0) && (!f2.there || put_k(f2));
+    f0 = f1, f1 = f2, f2 = f3, f3 = fetch();
+  }
+  return ok;
+}
 
 // A position in a ring of N slots.
 template <int N>

@@ -80,21 +80,6 @@ struct Cfg {
   static_assert(kSlots >= 3 && kUsedCols <= 512 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "layout");
 };
 
-// The tiles of a range one by one.
-struct Cursor {
-  Walk walk;
-  Segment s = {};
-  int j = 0;
-  __device__ Cursor(const Start& g, int unit_tokens) : walk(g, unit_tokens) {}
-  __device__ __forceinline__ bool next(const AttnArgs& a) {
-    if (++j < s.n) return true;
-    j = 0;
-    return walk.next(a, s);
-  }
-  __device__ __forceinline__ bool first() const { return j == 0; }
-  __device__ __forceinline__ bool last() const { return j + 1 == s.n; }
-};
-
 // Folds N values of each lane over the 32 lanes (kMax: maxima, else sums, in a fixed order), halving the values with the
 // lanes; N = 8, 16 or 32.  Afterwards lane l holds the result of value l / (32 / N) in v[0].
 template <int N, bool kMax>
@@ -186,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kTmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp >= kTmaWarp && warp < kTmaWarp + kSets) {
     // --------------------------------------------------------------------- TMA producer
-    // In order: K 0, K 1, then V t, K t + 2, over all tiles of the range; a unit's Q with its first K.
+    // In the order of load_in_order over all tiles of the range; a unit's Q with its first K.
     const int set = warp - kTmaWarp;
     const uint32_t range = blockIdx.x + set * gridDim.x;
     const TmaWaiter wait{{&sh->abort, a.timeout_ns}};
@@ -201,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int row0;  // >= 0: the unit's first tile here
       bool there;
     };
-    auto fetch = [&]() {  // the next tile's pages; used three tiles later
+    auto fetch = [&]() {  // the next tile's pages
       Ahead f = {};
       f.there = cur.next(a);
       if (!f.there) return f;
@@ -236,12 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n_seg;
       return true;
     };
-    Ahead f0 = fetch(), f1 = fetch(), f2 = fetch(), f3 = fetch();
-    bool ok = (!f0.there || put_k(f0)) && (!f1.there || put_k(f1));
-    while (ok && f0.there) {
-      ok = put(&map_v, f0) && (!f2.there || put_k(f2));
-      f0 = f1, f1 = f2, f2 = f3, f3 = fetch();
-    }
+    const bool ok = load_in_order(fetch, put_k, [&](const Ahead& f) { return put(&map_v, f); });
     if (!ok) {
       sh->abort = 1;
       if (lane == 0) note_timeout(a.status, a.diag, 1u, uint32_t(n_seg));
