@@ -160,6 +160,19 @@ struct Ring {
   }
 };
 
+// The parity of the phase in which a ring's slot was used last, after n > slot uses of the ring in order.
+__host__ __device__ __forceinline__ uint32_t last_phase(int n, int slots, int slot) {
+  return uint32_t((n - 1 - slot) / slots) & 1;
+}
+// A block whose roles gave up, whichever of them did, may not end with copies into its shared memory under way: wait
+// (bounded) for the last one into each slot of a ring that n copies went to.
+__device__ __forceinline__ void drain_copies(const uint64_t* full, int slots, int n, long long deadline) {
+  const volatile int never = 0;
+  for (int i = 0; i < min(n, slots); ++i)
+    tc::mbar_wait_bounded(tc::smem_u32(&full[i]), last_phase(n, slots, i), deadline, &never);
+}
+constexpr uint64_t kDrainNs = 200000000ull;
+
 // A whole warp waits; one answer for all lanes (false: given up).  The limit holds for each wait by itself: a
 // call over a long cache may take its time.
 struct Waiter {

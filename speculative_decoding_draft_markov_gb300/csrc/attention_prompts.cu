@@ -50,6 +50,7 @@ struct Shared {
   uint32_t tmem_base;
   volatile int abort;
   int mma_pending;
+  int n_k, n_v, n_q[2];  // copies issued
   Start start;
 };
 
@@ -174,20 +175,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {
       sh->abort = 1;
       if (lane == 0) note_timeout(a.status, a.diag, 1u, uint32_t(seg_i));
-      // wait (bounded) for every copy in flight before the CTA exits
-      const volatile int never = 0;
-      const long long dl = tc::deadline_after_ns(200000000ull);
-      // slots before the ring's position were last used in this turn of the ring, the others in the last one
-      for (int i = 0; i < min(n_k, C::kKSlots); ++i)
-        tc::mbar_wait_bounded(tc::smem_u32(&sh->k_full[i]), i < kr.slot ? kr.phase : kr.phase ^ 1, dl, &never);
-      for (int i = 0; i < min(n_v, C::kVSlots); ++i)
-        tc::mbar_wait_bounded(tc::smem_u32(&sh->v_full[i]), i < vr.slot ? vr.phase : vr.phase ^ 1, dl, &never);
-      if (q_use0 > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[0]), (q_use0 - 1) & 1, dl, &never);
-      if (q_use1 > 0) tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[1]), (q_use1 - 1) & 1, dl, &never);
     }
     if (lane == 0) {
       if (!ok) info.x = 0;
       a.info[blockIdx.x] = info;
+      sh->n_k = n_k, sh->n_v = n_v, sh->n_q[0] = q_use0, sh->n_q[1] = q_use1;
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------------- MMA issuer
@@ -487,15 +479,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncthreads();
-  if (warp == 9) {
-    if (lane == 0 && sh->mma_pending && sh->abort) {  // MMAs may be in flight: wait (bounded) before TMEM is freed
-      tc::mma_commit(tc::smem_u32(&sh->drain));
+  if (sh->abort) {  // MMAs and copies may be in flight: wait (bounded) before TMEM is freed and the block ends
+    const long long deadline = tc::deadline_after_ns(kDrainNs);
+    if (warp == 9 && sh->mma_pending) {
+      if (tc::elect_one()) tc::mma_commit(tc::smem_u32(&sh->drain));  // by the thread that issued them
+      __syncwarp();
       const volatile int never = 0;
-      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain), 0, tc::deadline_after_ns(200000000ull), &never);
+      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain), 0, deadline, &never);
+    } else if (warp == 8) {
+      drain_copies(sh->k_full, C::kKSlots, sh->n_k, deadline);
+      drain_copies(sh->v_full, C::kVSlots, sh->n_v, deadline);
+      drain_copies(&sh->q_full[0], 1, sh->n_q[0], deadline);
+      drain_copies(&sh->q_full[1], 1, sh->n_q[1], deadline);
     }
-    __syncwarp();
-    tc::tmem_dealloc(tmem, 512);
+    __syncthreads();
   }
+  if (warp == 9) tc::tmem_dealloc(tmem, 512);
 }
 
 template <int D>

@@ -54,6 +54,7 @@ struct Shared {
   uint32_t tmem_base;
   volatile int abort;
   int pending[kSets];        // the MMA warp has issued something
+  int n_put[kSets], n_q[kSets];  // copies issued: tiles, units' Q
   int need[kGroups][2];      // [parity]: the last tile at which a warp asked for a new reference
   Start start[kSets];
   float warp_max[kGroups][4][kRows], warp_sum[kGroups][4][kRows];  // by warp: the rows' maxima of a tile, sums of a unit
@@ -225,18 +226,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {
       sh->abort = 1;
       if (lane == 0) note_timeout(a.status, a.diag, 1u, uint32_t(n_seg));
-      // wait (bounded) for every copy in flight before the CTA exits
-      const volatile int never = 0;
-      const long long dl = tc::deadline_after_ns(200000000ull);
-      // slots before the ring's position were last used in this turn of the ring, the others in the last one
-      for (int i = 0; i < min(n_put, C::kSlots); ++i)
-        tc::mbar_wait_bounded(tc::smem_u32(&sh->full[set][i]), i < ring.slot ? ring.phase : ring.phase ^ 1, dl, &never);
-      for (int b = 0; b < min(n_seg, C::kQBufs); ++b)  // the last unit whose Q went to b
-        tc::mbar_wait_bounded(tc::smem_u32(&sh->q_full[set][b]), ((n_seg - 1 - b) / C::kQBufs) & 1, dl, &never);
     }
     if (lane == 0) {
       if (!ok) info.x = 0;
       a.info[range] = info;
+      sh->n_put[set] = n_put, sh->n_q[set] = n_seg;
     }
   } else if (warp >= kMmaWarp && warp < kMmaWarp + kSets) {
     // ------------------------------------------------------------ the two products of each tile
@@ -512,13 +506,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncthreads();
-  if (sh->abort) {  // MMAs may be in flight: wait (bounded) before TMEM is freed
-    const int set = warp - kMmaWarp;
-    if (set >= 0 && set < kSets && sh->pending[set]) {
+  if (sh->abort) {  // MMAs and copies may be in flight: wait (bounded) before TMEM is freed and the block ends
+    const long long deadline = tc::deadline_after_ns(kDrainNs);
+    const int set = (warp - kTmaWarp) % 2;
+    if (warp >= kMmaWarp && set < kSets && sh->pending[set]) {
       if (tc::elect_one()) tc::mma_commit(tc::smem_u32(&sh->drain[set]));
       __syncwarp();
       const volatile int never = 0;
-      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain[set]), 0, tc::deadline_after_ns(200000000ull), &never);
+      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain[set]), 0, deadline, &never);
+    } else if (warp >= kTmaWarp && warp < kMmaWarp && set < kSets) {
+      drain_copies(sh->full[set], C::kSlots, sh->n_put[set], deadline);
+      drain_copies(sh->q_full[set], C::kQBufs, sh->n_q[set], deadline);
     }
     __syncthreads();
   }

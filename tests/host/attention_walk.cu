@@ -61,4 +61,7 @@ __attribute__((visibility("default"))) int tiles_of_unit(int c, int n, int t, in
   return unit_geom(a, c, n, t, unit_tokens).ntiles;
 }
 
+// Parity of the last use of a ring's slot after n uses.
+__attribute__((visibility("default"))) int last_use(int n, int slots, int slot) { return int(last_phase(n, slots, slot)); }
+
 }  // extern "C"

@@ -73,3 +73,14 @@ def test_a_range_that_the_call_does_not_fill(host):
 
 def test_an_empty_range_loads_nothing(host):
     assert _loads(host, *CALLS[1], (0, 0, 0, 0), 0) == []
+
+
+@pytest.mark.parametrize("slots", [1, 2, 3, 5, 8])
+def test_the_phase_that_a_drain_waits_for(host, slots):
+    """The parity of a slot's last use, however far the ring has turned: not all slots used, whole turns, a part of one."""
+    used = {}
+    for n in range(1, 4 * slots + 3):
+        slot = (n - 1) % slots
+        used[slot] = used.get(slot, 0) + 1
+        for s, times in used.items():
+            assert host.last_use(n, slots, s) == (times - 1) % 2
