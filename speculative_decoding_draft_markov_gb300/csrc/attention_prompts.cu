@@ -66,6 +66,10 @@ __device__ __forceinline__ void store_32b(void* p, const uint32_t* v) {
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+__device__ __forceinline__ void store_2x16b(void* p, const uint32_t* v) {
+  uint4* to = static_cast<uint4*>(p);
+  to[0] = make_uint4(v[0], v[1], v[2], v[3]), to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -442,7 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld<D>(t_o, o);
         tc::tmem_ld_wait();
         tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
-        // 32-byte stores: a thread's row is D lanes in a row, other lanes' rows lie elsewhere
+        // 32-byte stores: a thread's row is D lanes in a row, other lanes' rows lie elsewhere.  The caller's tensor may
+        // begin at any multiple of 16 bytes, and then takes two stores.
+        const bool out_32b = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         if (valid && partial) {
 #pragma unroll
           for (int i = 0; i < D; i += 8) {
@@ -460,7 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[i + 2 * k] * inv, o[i + 2 * k + 1] * inv);
               w[k] = *reinterpret_cast<const uint32_t*>(&h2);
             }
-            store_32b(a.out + oat * D + i, w);
+            if (out_32b)
+              store_32b(a.out + oat * D + i, w);
+            else
+              store_2x16b(a.out + oat * D + i, w);
           }
         }
         if (valid) {

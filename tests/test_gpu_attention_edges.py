@@ -1,5 +1,5 @@
-"""The windows' attention where its memory, its masks and its waits can go wrong: work that fits its rings when a wait
-runs out."""
+"""The target-side calls where memory, masks and waits can go wrong: work that fits the attention's rings when a wait
+runs out, tensors at the least alignment that is allowed."""
 import numpy as np
 import pytest
 
@@ -34,3 +34,69 @@ def test_waits_that_run_out_over_little_work(rows, hq, ctx):
             B.dspark_set_wait_timeout_ns(old)
         assert st == B.DSPARK_ETIMEOUT or (st == B.DSPARK_OK and torch.equal(out, want))
         assert call(out) == B.DSPARK_OK and torch.equal(out, want)
+
+
+def _at_16(t):
+    """A copy of t that begins 16 bytes after a multiple of 32."""
+    room = torch.empty(t.numel() + 32 // t.element_size(), dtype=t.dtype, device="cuda")
+    skip = (16 - room.data_ptr() % 32) % 32 // t.element_size()
+    out = room[skip:skip + t.numel()].view(t.shape)
+    out.copy_(t)
+    assert out.data_ptr() % 32 == 16 and out.is_contiguous()
+    return out
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [1, 8, 40, 150])
+def test_tensors_that_begin_at_16_bytes(rows, d):
+    """Every tensor begins at an odd multiple of 16 bytes, at each tiling, whole units and cut ones."""
+    ns, ctxs = [rows, max(1, rows - 3)] * 3, [300, 20, 1000, 0, 64, 5]
+    c = Cache(ns, ctxs, 2, d, 16, seed=42)
+    q = torch.randn(sum(ns), 8, d, generator=torch.Generator().manual_seed(43)).to(torch.bfloat16).cuda()
+    ws = B.alloc_attention_workspace(8, 2, d)
+    got = []
+    for at in (lambda t: t, _at_16):
+        out = at(torch.full_like(q, 7.0))
+        lse = at(torch.zeros(sum(ns), 8, device="cuda"))
+        B.dspark_window_attention(at(q), at(c.k), at(c.v), at(c.table), at(c.cu), at(c.ctx), rows, d ** -0.5, 100, 2, out, lse, ws)
+        assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+        got.append((out.clone(), lse.clone()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_append_and_rules_on_tensors_that_begin_at_16_bytes():
+    ns, ctxs = [3, 1, 20], [40, 0, 7]
+    c = Cache(ns, ctxs, 2, 64, 16, seed=44, fill=0.0)
+    g = torch.Generator().manual_seed(45)
+    q, k, v = (torch.randn(sum(ns), h, 64, generator=g).to(torch.bfloat16).cuda() for h in (4, 2, 2))
+    ang = torch.arange(64)[:, None] * 10000.0 ** (-torch.arange(32) / 32)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).cuda()
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = []
+    for at in (lambda t: t, _at_16):
+        qo, kc, vc = at(torch.zeros_like(q)), at(c.k), at(c.v)
+        B.dspark_append_kv(at(q), at(k), at(v), at(c.cu), at(c.ctx), at(cs), at(c.table), qo, kc, vc, ws)
+        got.append((qo, kc.clone(), vc.clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    V, bs = 4104, 3
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.randn(sum(ns), V, generator=g).to(dtype).cuda()
+        hist = torch.zeros(bs, V, dtype=torch.int16, device="cuda")
+        ids = torch.arange(sum(ns), dtype=torch.int32, device="cuda")
+        toks = torch.arange(0, 900, 7, dtype=torch.int32, device="cuda")
+        start = torch.tensor([0, 50, 60, len(toks)], dtype=torch.int32, device="cuda")
+        asked = torch.tensor([10, 0, 30], dtype=torch.int32, device="cuda")
+        mask = torch.randint(-2 ** 31, 2 ** 31 - 1, (sum(ns), (V + 31) // 32), generator=g).int().cuda()
+        some = torch.tensor([1.3, 0.7, 1.1], device="cuda")
+        bias = (torch.tensor([0, 2, 2, 3], dtype=torch.int32, device="cuda"), torch.tensor([5, 900, 11], dtype=torch.int32, device="cuda"),
+                torch.tensor([1.0, -2.0, 3.0], device="cuda"))
+        got = []
+        for at in (lambda t: t, _at_16):
+            h, out = at(hist), at(torch.zeros_like(x))
+            B.dspark_history_build(at(toks), at(start), at(asked), h, ws)
+            B.dspark_process_logits(at(x), at(c.cu), at(ids), h, at(some), at(some), at(some), *(at(t) for t in bias), at(mask), out, ws)
+            out_tokens = at(torch.tensor([[1, 2], [3, -1], [-1, -1]], dtype=torch.int32, device="cuda"))
+            B.dspark_history_commit(out_tokens, h, ws)
+            got.append((h.clone(), out.clone()))
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert B.dspark_read_device_status(ws) == B.DSPARK_OK
