@@ -445,7 +445,7 @@ DSPARK_API int dspark_sts_fit(const float* z, const int32_t* ceiling, int N, int
  * with (a, b) = lanes (t, t + rot/2), or lanes (2t, 2t + 1) when `interleaved`.
  *   q, k, v     device, row strides q_stride, k_stride, v_stride (parts of one fused projection)
  *   cu_seqlens  device [bs + 1] int32;  ctx_len device [bs] int32
- *   rows        rows of q, k, v and q_out; rows from cu_seqlens[bs] on are left alone
+ *   rows        rows of q, k, v and q_out; rows before cu_seqlens[0] or from cu_seqlens[bs] on are left alone
  *   cos_sin     device [max_pos, rot] fp32: rot/2 cosines, then rot/2 sines, of each position
  *   page_table  device [bs, max_pages] int32
  *   q_out       device [rows, Hq, D]; may be q itself when q is dense.  q and q_out may both be NULL
@@ -475,7 +475,7 @@ DSPARK_API int dspark_append_kv(const void* q, int64_t q_stride, const void* k, 
  *   out       device [rows, Hq, D];  lse device [rows, Hq] fp32 or NULL (natural logarithm)
  *   ws        dspark_window_attention_workspace_bytes bytes, zeroed once; calls that can overlap on
  *             the device must not share it
- * Rows from cu_seqlens[bs] on are left alone.  Pages that no row of a request sees are not read, and
+ * Rows before cu_seqlens[0] or from cu_seqlens[bs] on are left alone.  Pages that no row of a request sees are not read, and
  * slots that no row sees (past the last row, before the window) may hold anything, NaN included; a NaN
  * or infinity in a slot that one row of a window sees can reach that window's other rows.
  * Device errors (status word, EINVAL): ctx_len below 0, or a window beyond max_pages pages (its rows are
@@ -498,7 +498,7 @@ DSPARK_API int dspark_window_attention(const void* q, int64_t q_stride, int dtyp
  *     l' = seen ? (l > 0 ? l / repetition[r] : l * repetition[r]) : l
  *     l' = l' - frequency[r] * c[v] - presence[r] * [c[v] > 0] + bias[r, v]
  *     out = mask bit v of the row is 0 ? -inf : l'          (fp32, rounded once)
- * A row whose mask leaves nothing is all -inf.
+ * A row whose mask leaves nothing is all -inf.  Rows before cu_seqlens[0] or from cu_seqlens[bs] on are left alone.
  *   logits, out  device [rows, V] (dtype, fp32 or bf16); out may be logits itself: then only the
  *                elements that a rule can change are read and written
  *   ids          device [rows] int32 (dspark_pack)

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kMaxAppendThreads, 8) append_kernel(const __gr
         const int64_t p = int64_t(c) + row - a.cu[r];
         const int64_t pi = p >> a.page_shift;
         int page = -1;
-        if (c >= 0 && p < a.max_pos && pi < a.max_pages)
+        if (c >= 0 && p >= 0 && p < a.max_pos && pi < a.max_pages)
           page = a.page_table[int64_t(r) * a.max_pages + pi];
         if (page >= 0 && page < a.n_pages) {
           pl.pos = int(p);

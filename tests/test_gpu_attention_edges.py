@@ -100,3 +100,51 @@ def test_append_and_rules_on_tensors_that_begin_at_16_bytes():
             got.append((h.clone(), out.clone()))
         assert all(torch.equal(a, b) for a, b in zip(*got))
     assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+
+
+@pytest.mark.parametrize("ctx0", [40, 2, 0])
+def test_lists_that_start_behind_row_0(ctx0):
+    """The last requests of a batch, with the whole batch's rows: what lies before their windows belongs to nobody (and no
+    length makes it a cached position)."""
+    ns, ctxs, skip = [5, 2, 3, 1], [9, 30, ctx0, 17], 2
+    whole = Cache(ns, ctxs, 2, 64, 16, seed=46, fill=0.0)
+    rows, first = sum(ns) + 2, sum(ns[:skip])
+    g = torch.Generator().manual_seed(47)
+    q, k, v = (torch.randn(rows, h, 64, generator=g).to(torch.bfloat16).cuda() for h in (4, 2, 2))
+    ang = torch.arange(64)[:, None] * 10000.0 ** (-torch.arange(32) / 32)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).cuda()
+    ws = B.alloc_attention_workspace(4, 2, 64)
+    kc, vc, qo = whole.k.clone(), whole.v.clone(), torch.full_like(q, 7.0)
+    B.dspark_append_kv(q, k, v, whole.cu, whole.ctx, cs, whole.table, qo, kc, vc, ws)
+    out = torch.full_like(q, 7.0)
+    B.dspark_window_attention(qo, kc, vc, whole.table, whole.cu, whole.ctx, 5, 0.125, 20, 2, out, None, ws)
+    cu, ctx, table = whole.cu[skip:], whole.ctx[skip:], whole.table[skip:]
+    k2, v2, q2 = whole.k.clone(), whole.v.clone(), torch.full_like(q, 7.0)
+    B.dspark_append_kv(q, k, v, cu, ctx, cs, table, q2, k2, v2, ws)
+    assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+    assert (q2[:first] == 7.0).all() and torch.equal(q2[first:], qo[first:])
+    for r, (n, x) in enumerate(zip(ns, ctxs)):  # the other requests' slots are as they were
+        pos = torch.arange(x, x + n, device="cuda")
+        pages = whole.table[r][pos // 16].long()
+        for got, full, before in ((k2, kc, whole.k), (v2, vc, whole.v)):
+            want = full if r >= skip else before
+            assert torch.equal(got[pages, :, pos % 16], want[pages, :, pos % 16])
+            got[pages, :, pos % 16] = full[pages, :, pos % 16]
+    assert torch.equal(k2, kc) and torch.equal(v2, vc)
+    for max_rows in (5, 100):
+        o2 = torch.full_like(q, 7.0)
+        B.dspark_window_attention(qo, kc, vc, table, cu, ctx, max_rows, 0.125, 20, 2, o2, None, ws)
+        assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+        assert (o2[:first] == 7.0).all() and (o2[sum(ns):] == 7.0).all()
+        if max_rows == 5:
+            assert torch.equal(o2[first:], out[first:])
+    V = 2056
+    x = torch.randn(rows, V, generator=g).to(torch.bfloat16).cuda()
+    ids = torch.randint(0, 40, (rows,), generator=g).int().cuda()
+    hist = torch.zeros(len(ns), V, dtype=torch.int16, device="cuda")
+    some = torch.full((len(ns),), 1.5, device="cuda")
+    a, b = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+    B.dspark_process_logits(x, whole.cu, ids, hist, some, some, some, None, None, None, None, a, ws)
+    B.dspark_process_logits(x, cu, ids, hist[skip:], some[skip:], some[skip:], some[skip:], None, None, None, None, b, ws)
+    assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+    assert (b[:first] == 7.0).all() and torch.equal(b[first:], a[first:])
