@@ -480,8 +480,10 @@ DSPARK_API int dspark_append_kv(const void* q, int64_t q_stride, const void* k, 
  * or infinity in a slot that one row of a window sees can reach that window's other rows.
  * Device errors (status word, EINVAL): ctx_len below 0, or a window beyond max_pages pages (its rows are
  * then left alone); a page number outside [0, n_pages) on a page that is read (read as zeros); cu_seqlens
- * decreasing or beyond rows (no row is written).
- * Limits: the common ones; scale finite. */
+ * decreasing or beyond rows, or 2^31 and more tiles of 128 positions to read, counted for each KV head and
+ * each pass of a request's rows over the cache, of max_rows rows or 256 (row, query head) pairs (no row is
+ * written).
+ * Limits: the common ones; scale finite; positions below 2^30. */
 DSPARK_API size_t dspark_window_attention_workspace_bytes(int Hq, int Hkv, int D);
 DSPARK_API int dspark_window_attention(const void* q, int64_t q_stride, int dtype, const void* k_cache,
                                        const void* v_cache, const int32_t* page_table, int max_pages, int n_pages,

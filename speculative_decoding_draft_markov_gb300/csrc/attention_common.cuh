@@ -203,7 +203,7 @@ struct TmaWaiter {
 // by one tile at most; this CTA has ranges blockIdx.x + set * gridDim.x.
 struct PlanScratch {
   long long warp_total[DSPARK_MAX_BS / 32];
-  uint32_t long_cost[DSPARK_MAX_BS];
+  unsigned long long long_cost[DSPARK_MAX_BS];
   uint8_t long_req[DSPARK_MAX_BS];
   int n_long, bad;
 };
@@ -222,7 +222,8 @@ template <int kSets>
 __device__ __forceinline__ Cut plan_ranges(const AttnArgs& a, Start* start, PlanScratch& p, int unit_tokens) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int row = 0, n = 0, c = 0;
-  uint32_t cost = 0;  // KV tiles of one KV head
+  uint32_t cost = 0;  // KV tiles of one KV head; from kTooMany on the call is refused
+  constexpr uint32_t kTooMany = 1u << 31;
   bool is_long = false;
   if (tid < a.bs) {
     row = a.cu[tid], n = a.cu[tid + 1] - row, c = a.ctx[tid];
@@ -244,13 +245,14 @@ __device__ __forceinline__ Cut plan_ranges(const AttnArgs& a, Start* start, Plan
   if (p.n_long > 0) {
     for (int i = 0; i < p.n_long; ++i) {
       const int r = p.long_req[i], rn = a.cu[r + 1] - a.cu[r], rc = a.ctx[r];
-      uint32_t part = 0;
+      unsigned long long part = 0;  // 2^20 rows over 2^29 positions pass 32 bits
       for (int t = tid; t * unit_tokens < rn; t += int(blockDim.x)) part += unit_geom(a, rc, rn, t, unit_tokens).ntiles;
-      part = __reduce_add_sync(~0u, part);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
       if (lane == 0) atomicAdd(&p.long_cost[r], part);
     }
     __syncthreads();
-    if (is_long) cost = p.long_cost[tid];
+    if (is_long) cost = uint32_t(min(p.long_cost[tid], static_cast<unsigned long long>(kTooMany)));
   }
   const long long mine = p.bad ? 0 : static_cast<long long>(cost) * a.Hkv;
   long long incl = mine;
@@ -267,7 +269,7 @@ __device__ __forceinline__ Cut plan_ranges(const AttnArgs& a, Start* start, Plan
     if (i < warp) before += p.warp_total[i];
     total += p.warp_total[i];
   }
-  const bool too_much = total >> 31 != 0;  // counted in 32 bits
+  const bool too_much = total >= kTooMany;  // counted in 32 bits from here on
   if (tid == 0 && blockIdx.x == 0 && (p.bad || too_much)) set_status(a.status, DSPARK_EINVAL);
   const uint32_t all = too_much ? 0u : uint32_t(total);
   // A unit of T tiles in ranges of m has T / m parts, which the join reads kJoinTogether at a time, one trip to memory each, and

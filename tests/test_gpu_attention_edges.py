@@ -148,3 +148,19 @@ def test_lists_that_start_behind_row_0(ctx0):
     B.dspark_process_logits(x, cu, ids, hist[skip:], some[skip:], some[skip:], some[skip:], None, None, None, None, b, ws)
     assert B.dspark_read_device_status(ws) == B.DSPARK_OK
     assert (b[:first] == 7.0).all() and torch.equal(b[first:], a[first:])
+
+
+@pytest.mark.parametrize("max_rows", [1, 5, 1 << 20])
+def test_more_tiles_than_are_counted(max_rows):
+    """A window of 2^20 rows over 2^29 positions is more work than a call takes, at every tiling: it is refused as a
+    whole, also where the count passes 2^32."""
+    n, ctx, page = 1 << 20, 1 << 29, 4096
+    k = torch.zeros(1, 1, page, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(1, (ctx + n) // page + 1, dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros(n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    ws = B.alloc_attention_workspace(1, 1, 64)
+    B.dspark_window_attention(q, k, k, table, torch.tensor([0, n], **i32), torch.tensor([ctx], **i32), max_rows, 0.125, 0, 0,
+                              out, None, ws)
+    assert B.dspark_read_device_status(ws) == B.DSPARK_EINVAL and (out == 7.0).all()
