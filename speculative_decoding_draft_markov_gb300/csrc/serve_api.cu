@@ -111,6 +111,7 @@ int dspark_process_logits(const void* logits, int dtype, int rows, int V, const 
   if (!bias_start && (bias_ids || bias_vals)) return DSPARK_EINVAL;
   if (bias_start && n_bias != 0 && (!bias_ids || !bias_vals)) return DSPARK_EINVAL;
   if (n_bias < 0 || !al(bias_start, 4) || !al(bias_ids, 4) || !al(bias_vals, 4)) return DSPARK_EINVAL;
+  if (!al(cu_seqlens, 4) || !al(ids, 4) || !al(repetition, 4) || !al(frequency, 4) || !al(presence, 4)) return DSPARK_EINVAL;
   if (int e = check_status_ws(ws, ws_bytes)) return e;
   return cuda_status(launch_process_logits(logits, dtype, rows, V, cu_seqlens, ids, bs, hist, repetition, frequency,
                                            presence, bias_start, bias_ids, bias_vals, n_bias, mask, out,
@@ -120,6 +121,7 @@ int dspark_process_logits(const void* logits, int dtype, int rows, int V, const 
 int dspark_history_build(const int32_t* tokens, int n_tokens, const int32_t* start, const int32_t* n_prompt, int bs,
                          int V, int16_t* hist, void* ws, size_t ws_bytes, dspark_stream_t stream) {
   if ((!tokens && n_tokens > 0) || n_tokens < 0 || !start || !n_prompt || !hist || !al(hist, 16)) return DSPARK_EINVAL;
+  if (!al(tokens, 4) || !al(start, 4) || !al(n_prompt, 4)) return DSPARK_EINVAL;
   if (int e = check_vocab(bs, V)) return e;
   if (int e = check_status_ws(ws, ws_bytes)) return e;
   return cuda_status(launch_history_build(tokens, n_tokens, start, n_prompt, bs, V, hist, static_cast<uint32_t*>(ws),
@@ -128,7 +130,7 @@ int dspark_history_build(const int32_t* tokens, int n_tokens, const int32_t* sta
 
 int dspark_history_commit(const int32_t* out_tokens, int bs, int gamma, int V, int16_t* hist, void* ws,
                           size_t ws_bytes, dspark_stream_t stream) {
-  if (!out_tokens || !hist || !al(hist, 16) || gamma < 1) return DSPARK_EINVAL;
+  if (!out_tokens || !al(out_tokens, 4) || !hist || !al(hist, 16) || gamma < 1) return DSPARK_EINVAL;
   if (int e = check_vocab(bs, V)) return e;
   if (gamma > DSPARK_MAX_GAMMA) return DSPARK_EUNSUPPORTED;
   if (int e = check_status_ws(ws, ws_bytes)) return e;
