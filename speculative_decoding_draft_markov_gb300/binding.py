@@ -76,6 +76,14 @@ class DSparkError(RuntimeError):
         super().__init__(f"{where}: {dspark_status_string(status) if _LIB else status}")
 
 
+class DSparkDeviceError(DSparkError, ValueError):
+    """A tensor of a target-side call that is not in the current device's memory: found by the binding, since the library
+    sees bare pointers.  Nothing was launched."""
+
+    def __init__(self, where: str, name: str):
+        super().__init__(DSPARK_EINVAL, f"{where}: {name} must be on the current CUDA device")
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -391,7 +399,7 @@ def _calls():
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         mod.init(torch.float32, torch.bfloat16, torch.int32, torch.int16, torch._C._cuda_getCurrentRawStream,
-                 torch.cuda.current_device, DSparkError)
+                 torch.cuda.current_device, DSparkError, DSparkDeviceError)
         _CALLS = mod
     return _CALLS
 

@@ -1,5 +1,5 @@
 // The Python calls of the target model's side, which are made per layer and per token: arguments are checked
-// (tensors' types, shapes and strides, which the C ABI cannot see behind bare pointers), handed to the C ABI, and a
+// (tensors' types, shapes, strides and devices, which the C ABI cannot see behind bare pointers), handed to the C ABI, and a
 // status other than DSPARK_OK is raised.  GB300's host: 5.6 us for an append, 7.6 for an attention (its two launches and
 // three tensor maps), 5.9 for the logit rules; through ctypes, with the checks in Python, 10.0, 11.7 and 9.2, more
 // than the GPU spends on one token.
@@ -15,8 +15,8 @@ namespace {
 
 // set by init
 PyObject *t_f32, *t_bf16, *t_i32, *t_i16;          // torch's types
-PyObject *current_stream, *current_device, *error;  // raw stream of a device; DSparkError
-PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_cuda_stream, *s_numel;
+PyObject *current_stream, *current_device, *error, *device_error;  // raw stream of a device; DSparkError, DSparkDeviceError
+PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_cuda_stream, *s_numel, *s_get_device;
 
 bool bad(const char* name, const char* what) {
   PyErr_Format(PyExc_ValueError, "%s %s", name, what);
@@ -60,12 +60,26 @@ bool has_type(PyObject* t, PyObject* dtype, const char* name) {
   return ok;
 }
 
-bool pointer(PyObject* t, void** p) {
+// Where a call's tensors lie: the first one's device, and the name of one that lies elsewhere or in host memory.
+struct Place {
+  long device = -1;
+  const char* other = nullptr;
+};
+
+bool pointer(PyObject* t, const char* name, void** p, Place& at) {
   PyObject* o = PyObject_CallMethodNoArgs(t, s_data_ptr);
   if (!o) return false;
   *p = PyLong_AsVoidPtr(o);
   Py_DECREF(o);
-  return *p || !PyErr_Occurred();
+  if (!*p) return !PyErr_Occurred();  // an empty tensor lies nowhere
+  o = PyObject_CallMethodNoArgs(t, s_get_device);
+  if (!o) return false;
+  const long d = PyLong_AsLong(o);  // -1: host memory
+  Py_DECREF(o);
+  if (d == -1 && PyErr_Occurred()) return false;
+  if (at.device < 0) at.device = d;
+  if ((d < 0 || d != at.device) && !at.other) at.other = name;
+  return true;
 }
 
 bool contiguous(PyObject* t, const char* name) {
@@ -76,7 +90,7 @@ bool contiguous(PyObject* t, const char* name) {
 }
 
 // The pointer of a dense tensor of that type and shape (nd = 0: any shape); None: NULL.
-bool dense(PyObject* t, PyObject* dtype, int nd, const int64_t* want, const char* name, void** p) {
+bool dense(PyObject* t, PyObject* dtype, int nd, const int64_t* want, const char* name, void** p, Place& at) {
   *p = nullptr;
   if (t == Py_None) return true;
   if (!has_type(t, dtype, name)) return false;
@@ -90,22 +104,24 @@ bool dense(PyObject* t, PyObject* dtype, int nd, const int64_t* want, const char
         return false;
       }
   }
-  return contiguous(t, name) && pointer(t, p);
+  return contiguous(t, name) && pointer(t, name, p, at);
 }
-bool dense1(PyObject* t, PyObject* dtype, int64_t n, const char* name, void** p) { return dense(t, dtype, 1, &n, name, p); }
-bool dense2(PyObject* t, PyObject* dtype, int64_t n, int64_t m, const char* name, void** p) {
+bool dense1(PyObject* t, PyObject* dtype, int64_t n, const char* name, void** p, Place& at) {
+  return dense(t, dtype, 1, &n, name, p, at);
+}
+bool dense2(PyObject* t, PyObject* dtype, int64_t n, int64_t m, const char* name, void** p, Place& at) {
   const int64_t d[2] = {n, m};
-  return dense(t, dtype, 2, d, name, p);
+  return dense(t, dtype, 2, d, name, p, at);
 }
 
-bool table_of(PyObject* t, const int64_t* d, int64_t bs, void** p) {  // a page table of shape d
+bool table_of(PyObject* t, const int64_t* d, int64_t bs, void** p, Place& at) {  // a page table of shape d
   if (d[0] != bs) return bad("page_table", "must have one row per request");
-  return dense(t, t_i32, 0, nullptr, "page_table", p);
+  return dense(t, t_i32, 0, nullptr, "page_table", p, at);
 }
 
 // Pointer and elements from row to row of a [rows, H, D] tensor of shape d whose heads and lanes are dense.
 bool rows_of(PyObject* t, PyObject* dtype, const int64_t* d, int64_t rows, int64_t H, int64_t D, const char* name, void** p,
-             int64_t* stride) {
+             int64_t* stride, Place& at) {
   int64_t st[3];
   if (!has_type(t, dtype, name)) return false;
   if (d[0] != rows || d[1] != H || d[2] != D) {
@@ -116,7 +132,7 @@ bool rows_of(PyObject* t, PyObject* dtype, const int64_t* d, int64_t rows, int64
   if (!ints_of(t, s_stride, true, 3, st, name)) return false;
   if (st[2] != 1 || (st[1] != D && H > 1)) return bad(name, "must be [rows, heads, lanes] with dense heads and lanes");
   *stride = rows > 1 ? st[0] : H * D;
-  return pointer(t, p);
+  return pointer(t, name, p, at);
 }
 
 // Entries of a 1-D tensor, of any tensor.
@@ -129,26 +145,34 @@ bool numel(PyObject* t, int64_t* n) {
   return !PyErr_Occurred();
 }
 
-bool workspace(PyObject* t, void** p, size_t* bytes) {
+bool workspace(PyObject* t, void** p, size_t* bytes, Place& at) {
   int64_t n;
-  if (!numel(t, &n) || !pointer(t, p)) return false;
+  if (!numel(t, &n) || !pointer(t, "ws", p, at)) return false;
   *bytes = size_t(n);
   return true;
 }
 
-// A torch stream, an integer, or None: torch's current one.
-bool stream_of(PyObject* s, dspark_stream_t* out) {
-  PyObject* o;
-  if (s == Py_None) {
-    PyObject* dev = PyObject_CallNoArgs(current_device);
-    if (!dev) return false;
-    o = PyObject_CallOneArg(current_stream, dev);
-    Py_DECREF(dev);
-  } else if (PyLong_Check(s)) {
-    o = Py_NewRef(s);
-  } else {
-    o = PyObject_GetAttr(s, s_cuda_stream);
+// A torch stream, an integer, or None: torch's current one.  The kernels run on the current device, so that is where the
+// tensors have to lie.
+bool stream_of(PyObject* s, const char* call, const Place& at, dspark_stream_t* out) {
+  long device = -1;
+  PyObject *o, *dev = nullptr;
+  if (!at.other) {
+    if (!(dev = PyObject_CallNoArgs(current_device))) return false;
+    device = PyLong_AsLong(dev);
   }
+  if (at.other || device != at.device) {
+    Py_XDECREF(dev);
+    if (PyErr_Occurred()) return false;
+    PyObject* e = PyObject_CallFunction(device_error, "ss", call, at.other ? at.other : "every tensor");
+    if (e) PyErr_SetObject(device_error, e), Py_DECREF(e);
+    return false;
+  }
+  if (s == Py_None)
+    o = PyObject_CallOneArg(current_stream, dev);
+  else
+    o = PyLong_Check(s) ? Py_NewRef(s) : PyObject_GetAttr(s, s_cuda_stream);
+  Py_DECREF(dev);
   if (!o) return false;
   *out = reinterpret_cast<dspark_stream_t>(PyLong_AsVoidPtr(o));
   Py_DECREF(o);
@@ -183,6 +207,7 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t c[4], k3[3], v3[3], cu_n, table[2], cs[2], q3[3], qs = 0, ks, vs;
   void *q = nullptr, *k, *v, *cu, *ctx, *cos, *pt, *qo = nullptr, *kc, *vc, *ws;
   size_t ws_bytes;
+  Place at;
   dspark_stream_t s;
   const int code = dtype_code(a[8], &dt), turn = PyObject_IsTrue(a[11]);
   if (!dt || turn < 0 || !shape_of(a[8], 4, c, "k_cache") || !shape_of(a[1], 3, k3, "k") || !shape_of(a[2], 3, v3, "v") ||
@@ -195,13 +220,13 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!shape_of(a[0], 3, q3, "q")) return nullptr;
     Hq = q3[1];
     const int64_t o[3] = {rows, Hq, D};
-    if (!rows_of(a[0], dt, q3, rows, Hq, D, "q", &q, &qs) || !dense(a[7], dt, 3, o, "q_out", &qo)) return nullptr;
+    if (!rows_of(a[0], dt, q3, rows, Hq, D, "q", &q, &qs, at) || !dense(a[7], dt, 3, o, "q_out", &qo, at)) return nullptr;
   }
-  if (!rows_of(a[1], dt, k3, rows, Hkv, D, "k", &k, &ks) || !rows_of(a[2], dt, v3, rows, Hkv, D, "v", &v, &vs) ||
-      !dense(a[3], t_i32, 0, nullptr, "cu_seqlens", &cu) || !dense1(a[4], t_i32, bs, "ctx_len", &ctx) ||
-      !dense(a[5], t_f32, 0, nullptr, "cos_sin", &cos) || !table_of(a[6], table, bs, &pt) ||
-      !dense(a[8], dt, 0, nullptr, "k_cache", &kc) || !dense(a[9], dt, 4, c, "v_cache", &vc) ||
-      !workspace(a[10], &ws, &ws_bytes) || !stream_of(a[12], &s))
+  if (!rows_of(a[1], dt, k3, rows, Hkv, D, "k", &k, &ks, at) || !rows_of(a[2], dt, v3, rows, Hkv, D, "v", &v, &vs, at) ||
+      !dense(a[3], t_i32, 0, nullptr, "cu_seqlens", &cu, at) || !dense1(a[4], t_i32, bs, "ctx_len", &ctx, at) ||
+      !dense(a[5], t_f32, 0, nullptr, "cos_sin", &cos, at) || !table_of(a[6], table, bs, &pt, at) ||
+      !dense(a[8], dt, 0, nullptr, "k_cache", &kc, at) || !dense(a[9], dt, 4, c, "v_cache", &vc, at) ||
+      !workspace(a[10], &ws, &ws_bytes, at) || !stream_of(a[12], "dspark_append_kv", at, &s))
     return nullptr;
   int rc;
   Py_BEGIN_ALLOW_THREADS
@@ -219,6 +244,7 @@ PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t c[4], q3[3], cu_n, table[2], qs;
   void *q, *kc, *vc, *pt, *cu, *ctx, *out, *lse, *ws;
   size_t ws_bytes;
+  Place at;
   dspark_stream_t s;
   int max_rows, window, n_sink;
   const int code = dtype_code(a[1], &dt);
@@ -229,11 +255,11 @@ PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   const int64_t rows = q3[0], Hq = q3[1], bs = cu_n - 1, Hkv = c[1], D = c[3];
   const int64_t o[3] = {rows, Hq, D};
-  if (!rows_of(a[0], dt, q3, rows, Hq, D, "q", &q, &qs) || !dense(a[1], dt, 0, nullptr, "k_cache", &kc) ||
-      !dense(a[2], dt, 4, c, "v_cache", &vc) || !table_of(a[3], table, bs, &pt) ||
-      !dense(a[4], t_i32, 0, nullptr, "cu_seqlens", &cu) || !dense1(a[5], t_i32, bs, "ctx_len", &ctx) ||
-      !dense(a[10], dt, 3, o, "out", &out) || !dense2(a[11], t_f32, rows, Hq, "lse", &lse) ||
-      !workspace(a[12], &ws, &ws_bytes) || !stream_of(a[13], &s))
+  if (!rows_of(a[0], dt, q3, rows, Hq, D, "q", &q, &qs, at) || !dense(a[1], dt, 0, nullptr, "k_cache", &kc, at) ||
+      !dense(a[2], dt, 4, c, "v_cache", &vc, at) || !table_of(a[3], table, bs, &pt, at) ||
+      !dense(a[4], t_i32, 0, nullptr, "cu_seqlens", &cu, at) || !dense1(a[5], t_i32, bs, "ctx_len", &ctx, at) ||
+      !dense(a[10], dt, 3, o, "out", &out, at) || !dense2(a[11], t_f32, rows, Hq, "lse", &lse, at) ||
+      !workspace(a[12], &ws, &ws_bytes, at) || !stream_of(a[13], "dspark_window_attention", at, &s))
     return nullptr;
   int rc;
   Py_BEGIN_ALLOW_THREADS
@@ -251,6 +277,7 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t x[2], cu_n, ids_n, n_bias = 0;
   void *in, *cu, *ids, *hist, *rep, *freq, *pres, *bst, *bid, *bval, *mask, *out, *ws;
   size_t ws_bytes;
+  Place at;
   dspark_stream_t s;
   const int code = dtype_code(a[0], &dt);
   if (!dt || !shape_of(a[0], 2, x, "logits") || !length(a[1], &cu_n, "cu_seqlens") || !length(a[2], &ids_n, "ids") ||
@@ -258,13 +285,13 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   const int64_t rows = x[0], V = x[1], bs = cu_n - 1;
   if (ids_n < rows) return bad("ids", "must hold one entry per row"), nullptr;
-  if (!dense(a[0], dt, 0, nullptr, "logits", &in) || !dense(a[1], t_i32, 0, nullptr, "cu_seqlens", &cu) ||
-      !dense(a[2], t_i32, 0, nullptr, "ids", &ids) || !dense2(a[3], t_i16, bs, V, "hist", &hist) ||
-      !dense1(a[4], t_f32, bs, "repetition", &rep) || !dense1(a[5], t_f32, bs, "frequency", &freq) ||
-      !dense1(a[6], t_f32, bs, "presence", &pres) || !dense1(a[7], t_i32, bs + 1, "bias_start", &bst) ||
-      !dense(a[8], t_i32, 0, nullptr, "bias_ids", &bid) || !dense1(a[9], t_f32, n_bias, "bias_vals", &bval) ||
-      !dense2(a[10], t_i32, rows, (V + 31) / 32, "mask", &mask) || !dense(a[11], dt, 2, x, "out", &out) ||
-      !workspace(a[12], &ws, &ws_bytes) || !stream_of(a[13], &s))
+  if (!dense(a[0], dt, 0, nullptr, "logits", &in, at) || !dense(a[1], t_i32, 0, nullptr, "cu_seqlens", &cu, at) ||
+      !dense(a[2], t_i32, 0, nullptr, "ids", &ids, at) || !dense2(a[3], t_i16, bs, V, "hist", &hist, at) ||
+      !dense1(a[4], t_f32, bs, "repetition", &rep, at) || !dense1(a[5], t_f32, bs, "frequency", &freq, at) ||
+      !dense1(a[6], t_f32, bs, "presence", &pres, at) || !dense1(a[7], t_i32, bs + 1, "bias_start", &bst, at) ||
+      !dense(a[8], t_i32, 0, nullptr, "bias_ids", &bid, at) || !dense1(a[9], t_f32, n_bias, "bias_vals", &bval, at) ||
+      !dense2(a[10], t_i32, rows, (V + 31) / 32, "mask", &mask, at) || !dense(a[11], dt, 2, x, "out", &out, at) ||
+      !workspace(a[12], &ws, &ws_bytes, at) || !stream_of(a[13], "dspark_process_logits", at, &s))
     return nullptr;
   int rc;
   Py_BEGIN_ALLOW_THREADS
@@ -281,10 +308,13 @@ PyObject* history_build(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t h[2], n_tokens;
   void *tokens, *start, *asked, *hist, *ws;
   size_t ws_bytes;
+  Place at;
   dspark_stream_t s;
-  if (!shape_of(a[3], 2, h, "hist") || !length(a[0], &n_tokens, "tokens") || !dense(a[0], t_i32, 0, nullptr, "tokens", &tokens) ||
-      !dense1(a[1], t_i32, h[0] + 1, "start", &start) || !dense1(a[2], t_i32, h[0], "n_prompt", &asked) ||
-      !dense(a[3], t_i16, 0, nullptr, "hist", &hist) || !workspace(a[4], &ws, &ws_bytes) || !stream_of(a[5], &s))
+  if (!shape_of(a[3], 2, h, "hist") || !length(a[0], &n_tokens, "tokens") ||
+      !dense(a[0], t_i32, 0, nullptr, "tokens", &tokens, at) ||
+      !dense1(a[1], t_i32, h[0] + 1, "start", &start, at) || !dense1(a[2], t_i32, h[0], "n_prompt", &asked, at) ||
+      !dense(a[3], t_i16, 0, nullptr, "hist", &hist, at) || !workspace(a[4], &ws, &ws_bytes, at) ||
+      !stream_of(a[5], "dspark_history_build", at, &s))
     return nullptr;
   int rc;
   Py_BEGIN_ALLOW_THREADS
@@ -300,11 +330,12 @@ PyObject* history_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t h[2], o[2];
   void *tokens, *hist, *ws;
   size_t ws_bytes;
+  Place at;
   dspark_stream_t s;
   if (!shape_of(a[1], 2, h, "hist") || !shape_of(a[0], 2, o, "out_tokens")) return nullptr;
   if (o[0] != h[0]) return bad("out_tokens", "must have one row per request"), nullptr;
-  if (!dense(a[0], t_i32, 0, nullptr, "out_tokens", &tokens) || !dense(a[1], t_i16, 0, nullptr, "hist", &hist) ||
-      !workspace(a[2], &ws, &ws_bytes) || !stream_of(a[3], &s))
+  if (!dense(a[0], t_i32, 0, nullptr, "out_tokens", &tokens, at) || !dense(a[1], t_i16, 0, nullptr, "hist", &hist, at) ||
+      !workspace(a[2], &ws, &ws_bytes, at) || !stream_of(a[3], "dspark_history_commit", at, &s))
     return nullptr;
   int rc;
   Py_BEGIN_ALLOW_THREADS
@@ -313,11 +344,11 @@ PyObject* history_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return result(rc, "dspark_history_commit");
 }
 
-// float32, bfloat16, int32, int16, current raw stream of a device, current device, DSparkError
+// float32, bfloat16, int32, int16, current raw stream of a device, current device, DSparkError, DSparkDeviceError
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!expect(n, 7)) return nullptr;
-  PyObject** const to[7] = {&t_f32, &t_bf16, &t_i32, &t_i16, &current_stream, &current_device, &error};
-  for (int i = 0; i < 7; ++i) *to[i] = Py_NewRef(a[i]);
+  if (!expect(n, 8)) return nullptr;
+  PyObject** const to[8] = {&t_f32, &t_bf16, &t_i32, &t_i16, &current_stream, &current_device, &error, &device_error};
+  for (int i = 0; i < 8; ++i) *to[i] = Py_NewRef(a[i]);
   Py_RETURN_NONE;
 }
 
@@ -332,7 +363,9 @@ PyMODINIT_FUNC PyInit__calls() {
   s_dtype = PyUnicode_InternFromString("dtype"), s_shape = PyUnicode_InternFromString("shape");
   s_stride = PyUnicode_InternFromString("stride"), s_data_ptr = PyUnicode_InternFromString("data_ptr");
   s_is_contiguous = PyUnicode_InternFromString("is_contiguous"), s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-  s_numel = PyUnicode_InternFromString("numel");
-  if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_is_contiguous || !s_cuda_stream || !s_numel) return nullptr;
+  s_numel = PyUnicode_InternFromString("numel"), s_get_device = PyUnicode_InternFromString("get_device");
+  if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_is_contiguous || !s_cuda_stream || !s_numel ||
+      !s_get_device)
+    return nullptr;
   return PyModule_Create(&module);
 }
