@@ -147,7 +147,7 @@ bool numel(PyObject* t, int64_t* n) {
 
 bool workspace(PyObject* t, void** p, size_t* bytes, Place& at) {
   int64_t n;
-  if (!numel(t, &n) || !pointer(t, "ws", p, at)) return false;
+  if (!numel(t, &n) || !contiguous(t, "ws") || !pointer(t, "ws", p, at)) return false;
   *bytes = size_t(n);
   return true;
 }

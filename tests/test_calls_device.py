@@ -49,3 +49,12 @@ def test_shapes_are_looked_at_first():
     with pytest.raises(ValueError, match="q must have shape") as e:
         B.dspark_append_kv(q[:2], *rest, stream=0)
     assert not isinstance(e.value, B.DSparkDeviceError)
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_a_workspace_that_is_no_block_of_bytes(name):
+    """An expanded byte has as many entries as one likes, and no memory behind them."""
+    args = _calls()[name][:-1]
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 26), _ws(1 << 10)[::2]):
+        with pytest.raises(ValueError, match="ws must be contiguous"):
+            getattr(B, name)(*args, ws, stream=0)
