@@ -5,15 +5,28 @@ logits and the token history they read, around step.run_step.
     run_served_step(inp, buf, sps, forward, cache, rules, ...)
 
 `forward(buf, cache)` is the caller's model: it fills buf.packed from the packed ids, calling cache.attend for
-each layer's attention.  Everything runs on one stream and nothing is read back; pages are handed out on the
-host, from upper bounds of the lengths."""
+each layer's attention.  Everything runs on one stream, torch's current one or the `stream` that is given (a torch
+stream or a raw handle); forward and the rules' mask are called with it as the current one.  A cache's `reserve`,
+`release` and `advance` are enqueued like the rest: they take the stream of the steps around them.  Nothing is
+read back; pages are handed out on the host, from upper bounds of the lengths."""
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Callable, List, Optional
 
 from . import binding as B
 from . import step as S
+
+
+def _on(stream):
+    """What torch does in this context it does on `stream`."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def rotation_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda"):
@@ -46,7 +59,7 @@ class PagedCache:
         self.free = list(range(n_pages - 1, -1, -1))
         self.ws = B.alloc_attention_workspace(Hq, Hkv, D, device)
 
-    def reserve(self, r: int, tokens: int) -> None:
+    def reserve(self, r: int, tokens: int, stream=None) -> None:
         """Pages for `tokens` more of request r (host; raises when none are left)."""
         import torch
         first = len(self.pages[r])
@@ -56,15 +69,17 @@ class PagedCache:
         new = [self.free.pop() for _ in range(need)]
         if new:
             self.pages[r] += new
-            self.page_table[r, first:first + need] = torch.tensor(new, dtype=torch.int32).to(self.page_table.device)
+            with _on(stream):
+                self.page_table[r, first:first + need] = torch.tensor(new, dtype=torch.int32).to(self.page_table.device)
         self.bound[r] += tokens
 
-    def release(self, r: int) -> None:
+    def release(self, r: int, stream=None) -> None:
         """Request r is done: its pages go back."""
         self.free += self.pages[r]
         self.pages[r], self.bound[r] = [], 0
-        self.page_table[r] = -1
-        self.ctx_len[r] = 0
+        with _on(stream):
+            self.page_table[r] = -1
+            self.ctx_len[r] = 0
 
     def attend(self, layer: int, q, k, v, cu_seqlens, max_rows: int, scale: float, out, stream=None) -> None:
         """Rotate and append the packed rows' q, k, v, then attend: out [rows, Hq, D].  `out` is the rotated
@@ -74,9 +89,10 @@ class PagedCache:
         B.dspark_window_attention(out, self.k[layer], self.v[layer], self.page_table, cu_seqlens, self.ctx_len, max_rows,
                                   scale, self.window, self.n_sink, out, None, self.ws, stream)
 
-    def advance(self, tokens) -> None:
+    def advance(self, tokens, stream=None) -> None:
         """Keep `tokens` [bs] (device int32) more of each request."""
-        self.ctx_len += tokens
+        with _on(stream):
+            self.ctx_len += tokens
 
 
 @dataclasses.dataclass
@@ -93,21 +109,23 @@ class LogitRules:
 
     def apply(self, buf, stream=None) -> None:
         """The rules on buf.packed, in place."""
-        B.dspark_process_logits(buf.packed, buf.cu, buf.ids, self.hist, self.repetition, self.frequency, self.presence,
-                                self.bias_start, self.bias_ids, self.bias_vals, self.mask(buf) if self.mask else None,
-                                buf.packed, buf.ws, stream)
+        with _on(stream):
+            B.dspark_process_logits(buf.packed, buf.cu, buf.ids, self.hist, self.repetition, self.frequency, self.presence,
+                                    self.bias_start, self.bias_ids, self.bias_vals, self.mask(buf) if self.mask else None,
+                                    buf.packed, buf.ws)
 
 
-def build_history(rules: LogitRules, prompts, V: int, ws, device="cuda") -> None:
+def build_history(rules: LogitRules, prompts, V: int, ws, device="cuda", stream=None) -> None:
     """rules.hist from the prompts (host lists of ids); the last id of a prompt, the first step's anchor, is in it."""
     import torch
     start = [0]
     for p in prompts:
         start.append(start[-1] + len(p))
     i32 = dict(dtype=torch.int32, device=device)
-    rules.hist = torch.empty((len(prompts), V), dtype=torch.int16, device=device)
-    B.dspark_history_build(torch.tensor([t for p in prompts for t in p], **i32), torch.tensor(start, **i32),
-                           torch.tensor([len(p) for p in prompts], **i32), rules.hist, ws)
+    with _on(stream):
+        rules.hist = torch.empty((len(prompts), V), dtype=torch.int16, device=device)
+        B.dspark_history_build(torch.tensor([t for p in prompts for t in p], **i32), torch.tensor(start, **i32),
+                               torch.tensor([len(p) for p in prompts], **i32), rules.hist, ws)
 
 
 def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache: PagedCache, rules: LogitRules,
@@ -120,14 +138,15 @@ def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache
 
     def target(b: S.StepBuffers) -> None:
         forward(b, cache)
-        rules.apply(b, stream)
+        rules.apply(b)
 
-    S.run_step(inp, buf, sps, target, temperature, seed, step, mode, tiers=tiers, stream=stream)
-    if rules.hist is not None:
-        B.dspark_history_commit(buf.out_tokens, rules.hist, buf.ws, stream)
-    last = buf.out_tokens.gather(1, buf.acc_len.long()[:, None])[:, 0]
-    dead = last < 0  # the anchor stays the last token: only the accepted ones before it are cached for good
-    before = torch.where(buf.acc_len > 0, buf.out_tokens.gather(1, (buf.acc_len.long() - 1).clamp(min=0)[:, None])[:, 0],
-                         inp["anchor"])
-    inp["anchor"].copy_(torch.where(dead, before, last))
-    cache.advance(buf.acc_len + (~dead).to(torch.int32))
+    with _on(stream):
+        S.run_step(inp, buf, sps, target, temperature, seed, step, mode, tiers=tiers)
+        if rules.hist is not None:
+            B.dspark_history_commit(buf.out_tokens, rules.hist, buf.ws)
+        last = buf.out_tokens.gather(1, buf.acc_len.long()[:, None])[:, 0]
+        dead = last < 0  # the anchor stays the last token: only the accepted ones before it are cached for good
+        before = torch.where(buf.acc_len > 0, buf.out_tokens.gather(1, (buf.acc_len.long() - 1).clamp(min=0)[:, None])[:, 0],
+                             inp["anchor"])
+        inp["anchor"].copy_(torch.where(dead, before, last))
+        cache.advance(buf.acc_len + (~dead).to(torch.int32))
