@@ -477,7 +477,9 @@ DSPARK_API int dspark_append_kv(const void* q, int64_t q_stride, const void* k, 
  *             the device must not share it
  * Rows before cu_seqlens[0] or from cu_seqlens[bs] on are left alone.  Pages that no row of a request sees are not read, and
  * slots that no row sees (past the last row, before the window) may hold anything, NaN included; a NaN
- * or infinity in a slot that one row of a window sees can reach that window's other rows.
+ * or infinity in a slot that one row of a window sees can reach that window's other rows.  A row that sees a
+ * score of NaN or +infinity is NaN, lse included; a score of -infinity has the weight 0, a row of nothing
+ * else is 0 with lse -infinity.
  * Device errors (status word, EINVAL): ctx_len below 0, or a window beyond max_pages pages (its rows are
  * then left alone); a page number outside [0, n_pages) on a page that is read (read as zeros); cu_seqlens
  * decreasing or beyond rows, or 2^31 and more tiles of 128 positions to read, counted for each KV head and

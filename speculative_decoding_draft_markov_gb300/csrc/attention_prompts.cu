@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t oat = int64_t(s.row0 + tok0 + tok) * a.Hq + s.h * a.g + hh;
         const int64_t prow = (int64_t(2) * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * (2 * kTile) + st * kTile + row;
         const bool partial = s.n < s.u.ntiles;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN, in the log-sum-exp too
         float o[D];
         tc::tmem_ld<D>(t_o, o);
         tc::tmem_ld_wait();
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (valid) {
-          const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+          const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
           if (partial)
             a.plse[prow] = lse2;
           else if (a.lse)

@@ -456,12 +456,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const float (*part)[RW] = sh->warp_sum[grp];
       const float sum = (part[0][fold_row] + part[1][fold_row]) + (part[2][fold_row] + part[3][fold_row]);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN, in the log-sum-exp too
       const bool partial = s.n < s.u.ntiles;
       const int64_t pbase = (int64_t(2) * (blockIdx.x + set * gridDim.x) + (s.tile0 > 0 ? 0 : 1)) * R + row0;
       const int n_rows = s.ntok * a.g - row0;  // of this group's
       if (w4 == 0 && fold_row * (32 / RW) == lane && fold_row < n_rows) {
-        const float lse2 = sum > 0.f ? ref[fold_row] + log2f(sum) : -INFINITY;
+        const float lse2 = sum == 0.f ? -INFINITY : ref[fold_row] + log2f(sum);
         const int row = row0 + fold_row;
         if (partial)
           a.plse[pbase + fold_row] = lse2;

@@ -55,13 +55,13 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     for (int e = 0; e < E; ++e) acc[e] *= keep;
 #pragma unroll
     for (int k = 0; k < kTogether; ++k) {
-      const float w = exp2f(lse[k] - base);  // 0: nothing seen there
+      const float w = exp2f(lse[k] - base);  // 0: nothing seen there; NaN: no number seen there
       sum += w;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = w == 0.f ? acc[e] : fmaf(w, v[k][e], acc[e]);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t at = int64_t(info.y + tok) * a.Hq + info.w * a.g + hh;
 #pragma unroll
   for (int e = 0; e < E; e += 2)

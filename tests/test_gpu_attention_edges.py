@@ -164,3 +164,53 @@ def test_more_tiles_than_are_counted(max_rows):
     B.dspark_window_attention(q, k, k, table, torch.tensor([0, n], **i32), torch.tensor([ctx], **i32), max_rows, 0.125, 0, 0,
                               out, None, ws)
     assert B.dspark_read_device_status(ws) == B.DSPARK_EINVAL and (out == 7.0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,hq,ctx", [(1, 2, 40), (1, 2, 9000), (8, 4, 9000), (16, 16, 6000), (150, 4, 5000)])
+def test_scores_that_are_no_numbers(n, hq, ctx, d):
+    """A key that holds NaN makes the rows that see it NaN, output and log-sum-exp, also where the tile that it lies in is
+    one part of a unit that is cut; a score of -inf is a weight of 0, one of +inf no number (inf - inf).  The other KV
+    head is untouched."""
+    page = 32
+    c = Cache([n], [ctx], 2, d, page, seed=48)
+    table = c.table.cpu().numpy()
+    q = torch.randn(n, hq, d, generator=torch.Generator().manual_seed(49)).to(torch.bfloat16)
+    q[..., 0] = torch.where(torch.arange(hq) % 2 == 0, 1.0, -1.0).to(torch.bfloat16)  # the sign of an infinite lane's score
+    ws = B.alloc_attention_workspace(hq, 2, d)
+    g = hq // 2
+    for value in (float("nan"), float("inf")):
+        for at in (3, ctx // 2, ctx):
+            keys = [c.keys[0].copy()]
+            keys[0][at, 0, 0] = value
+            k = c.k.clone()
+            k[table[0, at // page], 0, at % page, 0] = value
+            out = torch.zeros(n, hq, d, dtype=torch.bfloat16, device="cuda")
+            lse = torch.zeros(n, hq, device="cuda")
+            B.dspark_window_attention(q.cuda(), k, c.v, c.table, c.cu, c.ctx, n, d ** -0.5, 0, 0, out, lse, ws)
+            assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+            with np.errstate(invalid="ignore"):
+                ref, rl, mag = R.attention(_f64(q), keys[0], c.vals[0], ctx, d ** -0.5, 0, 0)
+            got, got_lse = _f64(out), _f64(lse)
+            no_number = np.isnan(ref)
+            assert no_number[:, :g].any() and not no_number[:, g:].any()
+            assert np.array_equal(np.isnan(got), no_number) and np.array_equal(np.isnan(got_lse), no_number.any(2))
+            assert (np.abs(got - ref)[~no_number] <= R.attention_bound(mag)[~no_number]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,hq,ctx", [(1, 2, 40), (1, 2, 9000), (16, 4, 3000), (150, 2, 3000)])
+def test_rows_whose_scores_are_all_minus_infinity(n, hq, ctx, d):
+    """Every key of a KV head has an infinite lane: heads whose query has the other sign there are 0 with lse -inf."""
+    c = Cache([n], [ctx], 2, d, 32, seed=50)
+    k = torch.nan_to_num(c.k, nan=0.0)
+    k[:, 0, :, 0] = float("inf")
+    q = torch.randn(n, hq, d, generator=torch.Generator().manual_seed(51)).to(torch.bfloat16).cuda()
+    q[..., 0] = -1.0
+    out, lse = torch.full_like(q, 7.0), torch.zeros(n, hq, device="cuda")
+    ws = B.alloc_attention_workspace(hq, 2, d)
+    B.dspark_window_attention(q, k, c.v, c.table, c.cu, c.ctx, n, d ** -0.5, 0, 0, out, lse, ws)
+    assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+    g = hq // 2
+    assert (out[:, :g] == 0).all() and torch.isneginf(lse[:, :g]).all()
+    assert torch.isfinite(out[:, g:]).all() and torch.isfinite(lse[:, g:]).all()
