@@ -129,7 +129,7 @@ def generate(steps=20, temperature=0.0, seed=5, **kw):
         out, lens = buf.out_tokens.tolist(), cache.ctx_len.tolist()
         for r, row in enumerate(out):
             said[r] += [x for x in row if x >= 0]
-            cache.bound[r] = lens[r]  # the exact length is known here: fewer pages are needed next
+            cache.settle(r, lens[r])  # the exact length is known here: fewer pages are needed next
     status = B.dspark_read_device_status(buf.ws) or B.dspark_read_device_status(cache.ws)
     if status != B.DSPARK_OK:
         raise B.DSparkError(status, "served step")

@@ -42,7 +42,9 @@ class PagedCache:
     """K and V of every layer in pages [n_pages, Hkv, page_size, D], one page table for all layers.
 
     ctx_len (device) counts each request's cached tokens; a step's windows are appended behind them and
-    `advance` keeps what the verification accepted.  `bound` (host) is an upper bound of ctx_len."""
+    `advance` keeps what the verification accepted.  `bound` (host) is an upper bound of ctx_len: `reserve` raises it by a
+    whole window each step, and only `settle` lowers it, by a length that has been read back.  Without it every
+    rejected draft keeps its place and the cache fills too early; how late the length comes does not matter."""
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, Hq: int, Hkv: int, D: int, bs: int, max_pages: int,
                  cos_sin, window: int = 0, n_sink: int = 0, interleaved: bool = False, device="cuda"):
@@ -72,6 +74,13 @@ class PagedCache:
             with _on(stream):
                 self.page_table[r, first:first + need] = torch.tensor(new, dtype=torch.int32).to(self.page_table.device)
         self.bound[r] += tokens
+
+    def settle(self, r: int, length: int, since: int = 0) -> None:
+        """Request r had `length` tokens in the cache after some step (ctx_len, read back at any later time); `since`
+        tokens were reserved for its steps after that one.  Lowers the bound to what that allows."""
+        if length < 0 or since < 0:
+            raise ValueError("length and since must not be negative")
+        self.bound[r] = min(self.bound[r], length + since)
 
     def release(self, r: int, stream=None) -> None:
         """Request r is done: its pages go back."""

@@ -1,0 +1,53 @@
+"""The paged cache's bookkeeping on the host (no GPU: the tensors lie in host memory and no call is made on them)."""
+import random
+
+import pytest
+
+torch = pytest.importorskip("torch")
+from speculative_decoding_draft_markov_gb300 import build as _build  # noqa: E402
+from speculative_decoding_draft_markov_gb300 import serving as V  # noqa: E402
+
+PAGE = 16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    _build.build()
+
+
+def _cache(n_pages, bs, max_pages, window=0, n_sink=0):
+    return V.PagedCache(1, n_pages, PAGE, 2, 1, 64, bs, max_pages, V.rotation_table(8, 64, device="cpu"), window, n_sink,
+                        device="cpu")
+
+
+@pytest.mark.parametrize("lag", [0, 1, 3])
+def test_rejected_drafts_give_their_place_back(lag):
+    """Windows of 8 rows of which 1 to 3 are kept, lengths known `lag` steps late: the pages are those of the tokens that
+    are there and of the steps under way."""
+    rng, rows, steps = random.Random(lag), 8, 200
+    c = _cache(1 + (3 * steps + rows * (lag + 2)) // PAGE, 1, 200)
+    length, known = 0, []
+    for t in range(steps):
+        c.reserve(0, rows)
+        assert c.bound[0] >= length + rows  # room for this step whatever the ones before kept
+        assert len(c.pages[0]) * PAGE >= c.bound[0]
+        length += rng.randint(1, 3)
+        known.append(length)
+        if t >= lag:
+            c.settle(0, known[t - lag], since=rows * lag)
+        assert c.bound[0] <= length + rows * (lag + 1)
+    assert len(c.pages[0]) <= 1 + (length + rows * (lag + 2)) // PAGE
+
+
+def test_a_length_never_raises_the_bound():
+    c = _cache(10, 1, 10)
+    c.reserve(0, 20)
+    c.settle(0, 100)
+    assert c.bound[0] == 20
+    c.settle(0, 7, since=5)
+    assert c.bound[0] == 12 and len(c.pages[0]) == 2
+    c.reserve(0, 20)  # 32 tokens: the two pages it has
+    assert len(c.pages[0]) == 2
+    for bad in ((-1, 0), (3, -1)):
+        with pytest.raises(ValueError):
+            c.settle(0, *bad)
