@@ -44,7 +44,8 @@ class PagedCache:
     ctx_len (device) counts each request's cached tokens; a step's windows are appended behind them and
     `advance` keeps what the verification accepted.  `bound` (host) is an upper bound of ctx_len: `reserve` raises it by a
     whole window each step, and only `settle` lowers it, by a length that has been read back.  Without it every
-    rejected draft keeps its place and the cache fills too early; how late the length comes does not matter."""
+    rejected draft keeps its place and the cache fills too early; how late the length comes does not matter.  With a
+    window, `settle` also gives back the pages that the window has left behind."""
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, Hq: int, Hkv: int, D: int, bs: int, max_pages: int,
                  cos_sin, window: int = 0, n_sink: int = 0, interleaved: bool = False, device="cuda"):
@@ -57,7 +58,7 @@ class PagedCache:
         self.page_table = torch.full((bs, max_pages), -1, dtype=torch.int32, device=device)
         self.ctx_len = torch.zeros(bs, dtype=torch.int32, device=device)
         self.bound: List[int] = [0] * bs
-        self.pages: List[List[int]] = [[] for _ in range(bs)]
+        self.pages: List[List[Optional[int]]] = [[] for _ in range(bs)]  # None: given back from behind the window
         self.free = list(range(n_pages - 1, -1, -1))
         self.ws = B.alloc_attention_workspace(Hq, Hkv, D, device)
 
@@ -75,16 +76,29 @@ class PagedCache:
                 self.page_table[r, first:first + need] = torch.tensor(new, dtype=torch.int32).to(self.page_table.device)
         self.bound[r] += tokens
 
-    def settle(self, r: int, length: int, since: int = 0) -> None:
+    def settle(self, r: int, length: int, since: int = 0, stream=None) -> None:
         """Request r had `length` tokens in the cache after some step (ctx_len, read back at any later time); `since`
-        tokens were reserved for its steps after that one.  Lowers the bound to what that allows."""
+        tokens were reserved for its steps after that one.  Lowers the bound to what that allows, and gives back the
+        pages that lie between the sinks and the window of the next position, which no later row sees."""
         if length < 0 or since < 0:
             raise ValueError("length and since must not be negative")
         self.bound[r] = min(self.bound[r], length + since)
+        if not self.window:
+            return
+        # rows from position `length` on see j > length - window and j < n_sink
+        pages, first = self.pages[r], -(-self.n_sink // self.page_size)
+        gone = [i for i in range(first, min(max(0, length - self.window + 1) // self.page_size, len(pages)))
+                if pages[i] is not None]
+        if gone:
+            self.free += [pages[i] for i in gone]
+            for i in gone:
+                pages[i] = None
+            with _on(stream):
+                self.page_table[r, gone[0]:gone[-1] + 1] = -1
 
     def release(self, r: int, stream=None) -> None:
         """Request r is done: its pages go back."""
-        self.free += self.pages[r]
+        self.free += [p for p in self.pages[r] if p is not None]
         self.pages[r], self.bound[r] = [], 0
         with _on(stream):
             self.page_table[r] = -1

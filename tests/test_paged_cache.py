@@ -51,3 +51,34 @@ def test_a_length_never_raises_the_bound():
     for bad in ((-1, 0), (3, -1)):
         with pytest.raises(ValueError):
             c.settle(0, *bad)
+
+
+@pytest.mark.parametrize("window,n_sink,lag", [(40, 0, 0), (33, 4, 2), (1, 17, 0), (64, 100, 1)])
+def test_pages_behind_the_window_come_back(window, n_sink, lag):
+    """Two long requests in a cache that holds their windows and sinks: every position that a row can see has a page of
+    its request's own, and nothing else is kept."""
+    rng, rows, steps = random.Random(window), 8, 400
+    one = -(-n_sink // PAGE) + -(-(window + rows * (lag + 2)) // PAGE) + 2
+    c = _cache(2 * one, 2, 300, window, n_sink)
+    length, known, owner = [0, 0], [[0, 0]], {}
+    for t in range(steps):
+        for r in range(2):
+            c.reserve(r, rows)
+        table = c.page_table.tolist()
+        held = [p for q in c.pages for p in q if p is not None] + c.free
+        assert sorted(held) == list(range(2 * one))
+        for r in range(2):
+            last = length[r] + rows - 1  # the step's rows: length .. last
+            for j in range(last + 1):
+                page = table[r][j // PAGE]
+                if j > length[r] - window or j < n_sink:
+                    assert page >= 0 and c.pages[r][j // PAGE] == page
+            length[r] += rng.randint(1, 4)
+        known.append(list(length))
+        if t >= lag:
+            for r in range(2):
+                c.settle(r, known[t + 1 - lag][r], since=rows * lag)
+    assert min(length) > 2 * one * PAGE  # more than the whole cache holds
+    for r in range(2):
+        c.release(r)
+    assert sorted(c.free) == list(range(2 * one)) and (c.page_table == -1).all()
