@@ -472,7 +472,8 @@ DSPARK_API int dspark_append_kv(const void* q, int64_t q_stride, const void* k, 
  *   max_rows  the longest window that the caller expects (>= 1).  It only picks how rows are tiled:
  *             any n_r is computed correctly.
  *   window    >= 0;  n_sink >= 0 (ignored when window = 0)
- *   out       device [rows, Hq, D];  lse device [rows, Hq] fp32 or NULL (natural logarithm)
+ *   out       device [rows, Hq, D]; may be q itself when q is dense (a unit's queries are read before its
+ *             rows are written).  lse device [rows, Hq] fp32 or NULL (natural logarithm)
  *   ws        dspark_window_attention_workspace_bytes bytes, zeroed once; calls that can overlap on
  *             the device must not share it
  * Rows before cu_seqlens[0] or from cu_seqlens[bs] on are left alone.  Pages that no row of a request sees are not read, and

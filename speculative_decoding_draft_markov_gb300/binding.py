@@ -430,7 +430,7 @@ def alloc_attention_workspace(Hq: int, Hkv: int, D: int, device="cuda"):
 def dspark_window_attention(q, k_cache, v_cache, page_table, cu_seqlens, ctx_len, max_rows, scale, window, n_sink, out,
                             lse, ws, stream=None):
     """Attention of the packed rows q [rows, Hq, D] over the paged cache: a sliding window (0: everything)
-    and the first n_sink tokens.  out [rows, Hq, D]; lse [rows, Hq] fp32 or None; max_rows: the longest
+    and the first n_sink tokens.  out [rows, Hq, D], or q itself; lse [rows, Hq] fp32 or None; max_rows: the longest
     window expected (it only picks the tiling)."""
     (_CALLS or _calls()).window_attention(q, k_cache, v_cache, page_table, cu_seqlens, ctx_len, max_rows, scale, window,
                                           n_sink, out, lse, ws, stream)

@@ -85,6 +85,7 @@ int dspark_window_attention(const void* q, int64_t q_stride, int dtype, const vo
     return e;
   if (int e = check_heads(Hq, Hkv, D)) return e;
   if (bad_rows(q, q_stride, Hq * D) || !out || !al(out, 16) || !al(lse, 4)) return DSPARK_EINVAL;
+  if (q == out && q_stride != int64_t(Hq) * D) return DSPARK_EINVAL;  // other rows' queries would be overwritten
   if (!std::isfinite(scale) || window < 0 || n_sink < 0 || max_rows < 1) return DSPARK_EINVAL;
   if (int e = check_status_ws(ws, ws_bytes, window_attention_ws_bytes(Hq, Hkv, D))) return e;
   return cuda_status(launch_window_attention(q, q_stride, k_cache, v_cache, page_table, max_pages, n_pages,

@@ -214,3 +214,23 @@ def test_rows_whose_scores_are_all_minus_infinity(n, hq, ctx, d):
     g = hq // 2
     assert (out[:, :g] == 0).all() and torch.isneginf(lse[:, :g]).all()
     assert torch.isfinite(out[:, g:]).all() and torch.isfinite(lse[:, g:]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("name,ns,ctxs,hq,max_rows", [
+    ("one", [1], [2500], 4, 1), ("windows", [1, 8, 3, 0, 5] * 30, [300, 17, 900, 90, 128] * 30, 8, 8),
+    ("wide windows", [16, 9] * 20, [3000, 130] * 20, 8, 16), ("longer than expected", [20, 3, 40], [700, 9, 2000], 8, 2),
+    ("prompts", [150, 33, 260], [700, 0, 2000], 8, 260), ("one prompt", [70], [9000], 4, 70)])
+def test_output_in_place_of_the_queries(name, ns, ctxs, hq, max_rows, d):
+    """`out` may be `q`: the same bits as with an output of its own, whole units and cut ones, at each tiling."""
+    c = Cache(ns, ctxs, 2, d, 32, seed=52)
+    q = torch.randn(sum(ns) + 2, hq, d, generator=torch.Generator().manual_seed(53)).to(torch.bfloat16).cuda()
+    ws = B.alloc_attention_workspace(hq, 2, d)
+    for window, sinks in ((0, 0), (200, 4)):
+        out, both = torch.empty_like(q), q.clone()
+        out[sum(ns):] = q[sum(ns):]
+        lse = [torch.zeros(sum(ns) + 2, hq, device="cuda") for _ in range(2)]
+        for x, o, l in ((q, out, lse[0]), (both, both, lse[1])):
+            B.dspark_window_attention(x, c.k, c.v, c.table, c.cu, c.ctx, max_rows, d ** -0.5, window, sinks, o, l, ws)
+        assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+        assert torch.equal(both, out) and torch.equal(lse[0], lse[1])

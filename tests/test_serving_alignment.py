@@ -1,5 +1,5 @@
-"""Pointers that no 4-byte load may use are refused on the host by every target-side call, before anything is launched
-(no GPU; pointers are host buffers that no call may touch)."""
+"""Pointers that no 4-byte load may use, and an output that lies over strided queries, are refused on the host before
+anything is launched (no GPU; pointers are host buffers that no call may touch)."""
 import pytest
 
 pytest.importorskip("torch")
@@ -19,3 +19,7 @@ def test_misaligned_words_are_refused(lib, name, args, keys, off):  # noqa: F811
         args = dict(args, q_stride=1024)
     for key in keys:
         assert _try(lib, name, args, {key: PTR + off}) == EINVAL, key
+
+
+def test_attention_refuses_strided_in_place(lib):  # noqa: F811
+    assert _try(lib, "dspark_window_attention", ATTEND, {"q": PTR, "out": PTR, "q_stride": 1536}) == EINVAL
