@@ -394,7 +394,7 @@ def _calls():
         path = os.path.join(os.path.dirname(library_path()), "_calls.so")
         lib()
         if not os.path.exists(path):
-            raise RuntimeError(f"_calls.so is not built ({path}); run __graft_entry__.build()")
+            raise RuntimeError(f"_calls.so is not built ({path}); run __graft_entry__.build() (it needs Python's headers)")
         spec = importlib.util.spec_from_file_location("_calls", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)

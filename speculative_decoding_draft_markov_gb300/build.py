@@ -66,15 +66,27 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if res.returncode != 0:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError("link of libdspark.so failed")
-    src = os.path.join(CSRC, "calls.cpp")
-    if force or not _newer(CALLS, [src, os.path.join(ROOT, "include", "dspark.h")]):
-        cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I" + os.path.join(ROOT, "include"),
-               "-I" + sysconfig.get_paths()["include"], src, "-o", CALLS, "-L" + LIBDIR, "-ldspark", "-Wl,-rpath,$ORIGIN"]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            sys.stderr.write(res.stdout + res.stderr)
-            raise RuntimeError("build of _calls.so failed")
+    _build_calls(force)
     return LIB
+
+
+def _build_calls(force: bool) -> None:
+    """lib/_calls.so.  Without Python's headers the library alone is built: its other calls need no extension module, and
+    the calls that do need one say that it is missing."""
+    src, include = os.path.join(CSRC, "calls.cpp"), sysconfig.get_paths()["include"]
+    if not force and _newer(CALLS, [src, os.path.join(ROOT, "include", "dspark.h")]):
+        return
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        if os.path.exists(CALLS):
+            os.remove(CALLS)  # of older sources
+        sys.stderr.write(f"_calls.so is not built: no Python.h in {include}\n")
+        return
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I" + os.path.join(ROOT, "include"),
+           "-I" + include, src, "-o", CALLS, "-L" + LIBDIR, "-ldspark", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("build of _calls.so failed")
 
 
 if __name__ == "__main__":
