@@ -151,20 +151,11 @@ def build_history(rules: LogitRules, prompts, V: int, ws, device="cuda", stream=
                                torch.tensor([len(p) for p in prompts], **i32), rules.hist, ws)
 
 
-def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache: PagedCache, rules: LogitRules,
-                    temperature: float, seed: int, step: int, mode: int = B.DSPARK_COMPACT, tiers=None,
-                    stream=None) -> None:
-    """One step: draft, schedule and pack; the target forward over the packed windows, its logits under the
-    rules; the verification; then history, cache lengths and anchors (inp["anchor"]) take its outcome.
+def take_outcome(inp: dict, buf: S.StepBuffers, cache: PagedCache, rules: LogitRules, stream=None) -> None:
+    """After a verification: history, cache lengths and anchors (inp["anchor"]) take its outcome.
     A request whose deciding row allows nothing keeps its anchor and adds no token."""
     import torch
-
-    def target(b: S.StepBuffers) -> None:
-        forward(b, cache)
-        rules.apply(b)
-
     with _on(stream):
-        S.run_step(inp, buf, sps, target, temperature, seed, step, mode, tiers=tiers)
         if rules.hist is not None:
             B.dspark_history_commit(buf.out_tokens, rules.hist, buf.ws)
         last = buf.out_tokens.gather(1, buf.acc_len.long()[:, None])[:, 0]
@@ -173,3 +164,20 @@ def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache
                              inp["anchor"])
         inp["anchor"].copy_(torch.where(dead, before, last))
         cache.advance(buf.acc_len + (~dead).to(torch.int32))
+
+
+def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache: PagedCache, rules: LogitRules,
+                    temperature: float, seed: int, step: int, mode: int = B.DSPARK_COMPACT, tiers=None,
+                    stream=None, sched_mode: int = B.DSPARK_SCHED_EARLY_STOP, ring=None, side_stream=None) -> None:
+    """One step: draft, schedule and pack; the target forward over the packed windows, its logits under the
+    rules; the verification; then take_outcome.  mode, tiers, sched_mode, ring and side_stream as in step.run_step.
+    A drafter that step.run_step does not run (the RNN head) takes the same way by hand: its draft and the pack,
+    forward, rules.apply, step.verify with its states, take_outcome."""
+
+    def target(b: S.StepBuffers) -> None:
+        forward(b, cache)
+        rules.apply(b)
+
+    with _on(stream):
+        S.run_step(inp, buf, sps, target, temperature, seed, step, mode, sched_mode, tiers, ring=ring, side_stream=side_stream)
+        take_outcome(inp, buf, cache, rules)
