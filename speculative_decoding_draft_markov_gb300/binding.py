@@ -399,7 +399,8 @@ def _calls():
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         mod.init(torch.float32, torch.bfloat16, torch.int32, torch.int16, torch._C._cuda_getCurrentRawStream,
-                 torch.cuda.current_device, DSparkError, DSparkDeviceError)
+                 torch._C._cuda_getDevice, DSparkError, DSparkDeviceError, torch.Tensor.data_ptr, torch.Tensor.get_device,
+                 torch.Tensor.is_contiguous)
         _CALLS = mod
     return _CALLS
 

@@ -1,7 +1,7 @@
 // The Python calls of the target model's side, which are made per layer and per token: arguments are checked
 // (tensors' types, shapes, strides and devices, which the C ABI cannot see behind bare pointers), handed to the C ABI, and a
-// status other than DSPARK_OK is raised.  GB300's host: 5.6 us for an append, 7.6 for an attention (its two launches and
-// three tensor maps), 5.9 for the logit rules; through ctypes, with the checks in Python, 10.0, 11.7 and 9.2, more
+// status other than DSPARK_OK is raised.  GB300's host: 5.8 us for an append, 7.6 for an attention (its two launches and
+// three tensor maps), 6.1 for the logit rules; through ctypes, with the checks in Python, 10.0, 11.7 and 9.2, more
 // than the GPU spends on one token.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -16,7 +16,8 @@ namespace {
 // set by init
 PyObject *t_f32, *t_bf16, *t_i32, *t_i16;          // torch's types
 PyObject *current_stream, *current_device, *error, *device_error;  // raw stream of a device; DSparkError, DSparkDeviceError
-PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_cuda_stream, *s_numel, *s_get_device;
+PyObject *m_data_ptr, *m_get_device, *m_is_contiguous;             // a tensor's methods, found once
+PyObject *s_dtype, *s_shape, *s_stride, *s_cuda_stream, *s_numel;
 
 bool bad(const char* name, const char* what) {
   PyErr_Format(PyExc_ValueError, "%s %s", name, what);
@@ -67,12 +68,12 @@ struct Place {
 };
 
 bool pointer(PyObject* t, const char* name, void** p, Place& at) {
-  PyObject* o = PyObject_CallMethodNoArgs(t, s_data_ptr);
+  PyObject* o = PyObject_CallOneArg(m_data_ptr, t);
   if (!o) return false;
   *p = PyLong_AsVoidPtr(o);
   Py_DECREF(o);
   if (!*p) return !PyErr_Occurred();  // an empty tensor lies nowhere
-  o = PyObject_CallMethodNoArgs(t, s_get_device);
+  o = PyObject_CallOneArg(m_get_device, t);
   if (!o) return false;
   const long d = PyLong_AsLong(o);  // -1: host memory
   Py_DECREF(o);
@@ -83,7 +84,7 @@ bool pointer(PyObject* t, const char* name, void** p, Place& at) {
 }
 
 bool contiguous(PyObject* t, const char* name) {
-  PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+  PyObject* c = PyObject_CallOneArg(m_is_contiguous, t);
   if (!c) return false;
   Py_DECREF(c);  // a singleton
   return c == Py_True || bad(name, "must be contiguous");
@@ -155,19 +156,15 @@ bool workspace(PyObject* t, void** p, size_t* bytes, Place& at) {
 // A torch stream, an integer, or None: torch's current one.  The kernels run on the current device, so that is where the
 // tensors have to lie.
 bool stream_of(PyObject* s, const char* call, const Place& at, dspark_stream_t* out) {
-  long device = -1;
-  PyObject *o, *dev = nullptr;
-  if (!at.other) {
-    if (!(dev = PyObject_CallNoArgs(current_device))) return false;
-    device = PyLong_AsLong(dev);
-  }
-  if (at.other || device != at.device) {
+  PyObject* dev = nullptr;
+  if (!at.other && at.device >= 0 && !(dev = PyObject_CallNoArgs(current_device))) return false;
+  if (!dev || PyLong_AsLong(dev) != at.device) {
     Py_XDECREF(dev);
-    if (PyErr_Occurred()) return false;
     PyObject* e = PyObject_CallFunction(device_error, "ss", call, at.other ? at.other : "every tensor");
     if (e) PyErr_SetObject(device_error, e), Py_DECREF(e);
     return false;
   }
+  PyObject* o;
   if (s == Py_None)
     o = PyObject_CallOneArg(current_stream, dev);
   else
@@ -344,11 +341,13 @@ PyObject* history_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return result(rc, "dspark_history_commit");
 }
 
-// float32, bfloat16, int32, int16, current raw stream of a device, current device, DSparkError, DSparkDeviceError
+// float32, bfloat16, int32, int16, current raw stream of a device, current device, DSparkError, DSparkDeviceError, and the
+// tensors' data_ptr, get_device and is_contiguous
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!expect(n, 8)) return nullptr;
-  PyObject** const to[8] = {&t_f32, &t_bf16, &t_i32, &t_i16, &current_stream, &current_device, &error, &device_error};
-  for (int i = 0; i < 8; ++i) *to[i] = Py_NewRef(a[i]);
+  if (!expect(n, 11)) return nullptr;
+  PyObject** const to[11] = {&t_f32, &t_bf16, &t_i32, &t_i16, &current_stream, &current_device, &error, &device_error,
+                             &m_data_ptr, &m_get_device, &m_is_contiguous};
+  for (int i = 0; i < 11; ++i) *to[i] = Py_NewRef(a[i]);
   Py_RETURN_NONE;
 }
 
@@ -361,11 +360,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 PyMODINIT_FUNC PyInit__calls() {
   s_dtype = PyUnicode_InternFromString("dtype"), s_shape = PyUnicode_InternFromString("shape");
-  s_stride = PyUnicode_InternFromString("stride"), s_data_ptr = PyUnicode_InternFromString("data_ptr");
-  s_is_contiguous = PyUnicode_InternFromString("is_contiguous"), s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-  s_numel = PyUnicode_InternFromString("numel"), s_get_device = PyUnicode_InternFromString("get_device");
-  if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_is_contiguous || !s_cuda_stream || !s_numel ||
-      !s_get_device)
-    return nullptr;
+  s_stride = PyUnicode_InternFromString("stride"), s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
+  s_numel = PyUnicode_InternFromString("numel");
+  if (!s_dtype || !s_shape || !s_stride || !s_cuda_stream || !s_numel) return nullptr;
   return PyModule_Create(&module);
 }
