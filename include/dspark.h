@@ -466,7 +466,8 @@ DSPARK_API int dspark_append_kv(const void* q, int64_t q_stride, const void* k, 
  * i.e. a sliding window and the sequence's first tokens, which stay visible:
  *     s_j = scale * q . k_j,   lse = log sum_j exp(s_j),   out = sum_j exp(s_j - lse) v_j
  * Query head h reads KV head h / (Hq / Hkv).  Scores, maxima and sums are fp32; the weights
- * exp(s_j - m) enter the second product in bf16 and their sum in fp32.
+ * exp(s_j - m) enter the second product in bf16 and their sum in fp32.  m may lie 16 binary orders below a row's
+ * largest score: with n visible positions, values of V beyond 2^111 / n may overflow fp32 and give infinities.
  *   q         device, row stride q_stride (rotated: dspark_append_kv's q_out)
  *   k_cache, v_cache, page_table, cu_seqlens, ctx_len, rows as dspark_append_kv
  *   max_rows  the longest window that the caller expects (>= 1).  It only picks how rows are tiled:

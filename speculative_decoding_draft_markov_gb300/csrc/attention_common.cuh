@@ -23,6 +23,10 @@ namespace attn {
 constexpr int kTile = 128;  // KV slots per tile
 constexpr int kJoinTogether = 16;  // parts of a row that the join reads at a time, where they are many
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// The exponentials' reference m (log2 units) before a row has one, and by how much a score may outgrow it before it moves
+// and O and l are rescaled.  It costs range in O, which holds up to 2^16 n |v| for n positions: |v| of
+// 2^90 is safe with 2^21 of them; scores hardly ever outgrow the first tile's by more.
+constexpr float kUnset = -1e30f, kRescaleAt = 16.f;
 
 struct AttnArgs {
   int64_t cache_limit;  // positions that the page table can hold

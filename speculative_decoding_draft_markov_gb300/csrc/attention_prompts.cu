@@ -6,8 +6,8 @@
 // While one tile's softmax runs, the tensor cores work for the other.  The softmax of a tile has to be done within
 // the other tile's two products, so its first half is handed on as soon as it is there, computed by the
 // reference m as it stands while the row's maximum is found: m only keeps the exponentials in range, and
-// any value within 2^60 of the maximum gives the same result, since the sum is divided out and neither fp32 nor
-// bf16 loses bits there.  It moves, and O and l are rescaled, when a maximum has outgrown it by more.  P is rounded to
+// weights of up to 2^16 give the same result, since the sum is divided out and neither fp32 nor bf16 loses bits
+// there.  It moves, and O and l are rescaled, when a maximum has outgrown it by more (kRescaleAt).  P is rounded to
 // bf16 for the second product, its sum is taken before that, in fp32.
 //
 // GB300, 2 prompts of about 4000 rows over 1000 .. 5000 cached positions, window 4096, Hq 32, Hkv 8: D 128 303 us of 238 at the
@@ -31,7 +31,6 @@ constexpr int kThreads = 384;  // warps 0-3: softmax of the first tile, 4-7: of 
 // Registers: launched with 384 x 168; the softmax warps hold a whole row of S and take what the others
 // give back (256 x 208 + 128 x 80 <= 384 x 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
-constexpr float kUnset = -1e30f, kRescaleAt = 60.f;  // log2 units
 
 template <int D>
 struct Cfg {

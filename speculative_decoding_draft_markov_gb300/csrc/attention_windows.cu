@@ -12,9 +12,9 @@
 // where tensor memory (R = 128) or shared memory (R = 64 with D = 128) does not allow two, one pipeline has all
 // sixteen softmax warps.
 //
-// m is a reference that only keeps the exponentials in range, the same for all slots of a row: any value
-// within 2^60 of the maximum gives the same result, since the sum is divided out and neither fp32 nor bf16 loses
-// bits there.  So it is set from a unit's first tile and checked, not recomputed, on the others.
+// m is a reference that only keeps the exponentials in range, the same for all slots of a row: weights of up to
+// 2^16 give the same result, since the sum is divided out and neither fp32 nor bf16 loses bits there.  So it is
+// set from a unit's first tile and checked against kRescaleAt, not recomputed, on the others.
 // P is rounded to bf16 for the second product (relative 2^-9 a weight), its sum is taken before that, in fp32: the
 // outputs' error against 64 bits is 0.0023 of their size, that of a product with fp32 weights and one rounding
 // 0.0017.
@@ -40,7 +40,6 @@ constexpr int kGroups = 4, kThreads = (kGroups + 1) * 128;
 constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 2;
 // Registers: launched with 640 x 96; the softmax warps take what the others give back (512 x 104 + 128 x 56 <= 640 x 96).
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 56;
-constexpr float kUnset = -1e30f, kRescaleAt = 60.f;  // log2 units
 constexpr int kMaxSlots = 8;
 
 constexpr int sets_of(int D, int R) { return R * D >= 64 * 128 ? 1 : 2; }

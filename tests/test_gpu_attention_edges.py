@@ -234,3 +234,32 @@ def test_output_in_place_of_the_queries(name, ns, ctxs, hq, max_rows, d):
             B.dspark_window_attention(x, c.k, c.v, c.table, c.cu, c.ctx, max_rows, d ** -0.5, window, sinks, o, l, ws)
         assert B.dspark_read_device_status(ws) == B.DSPARK_OK
         assert torch.equal(both, out) and torch.equal(lse[0], lse[1])
+
+
+@pytest.mark.parametrize("n,hq", [(1, 2), (8, 4), (16, 8), (90, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values_under_scores_that_grow(n, hq, d):
+    """Values of 2^75 and weights that outgrow those of the first tile by 2^57: finite outputs stay finite.  q = 1, key j =
+    c_j in every lane, scale 1 / D: the scores are c_j."""
+    page, ctx = 32, 700
+    c = Cache([n], [ctx], 1, d, page, seed=55)
+    level = np.where(np.arange(ctx + n) < 200, 0.0, 40.0) + (np.arange(ctx + n) % 4) * 0.25
+    level[-1] = 0.0
+    c.keys[0] = np.repeat(level[:, None, None], d, 2)
+    c.vals[0] = c.vals[0] * 2.0 ** 75
+    table = c.table.cpu().numpy()
+    for j in range(ctx + n):
+        c.k[table[0, j // page], :, j % page] = float(level[j])
+    c.v = c.v * 2.0 ** 75
+    bs = 160  # enough work that a block takes whole units, too
+    q = torch.ones(bs * n, hq, d, dtype=torch.bfloat16, device="cuda")
+    ws = B.alloc_attention_workspace(hq, 1, d)
+    ref, rl, mag = R.attention(_f64(q)[:n], c.keys[0], c.vals[0], ctx, 1.0 / d, 0, 0)
+    for many in (1, bs):
+        out, lse = torch.zeros_like(q[:many * n]), torch.zeros(many * n, hq, device="cuda")
+        cu = torch.arange(0, many * n + 1, n, dtype=torch.int32, device="cuda")
+        B.dspark_window_attention(q[:many * n], c.k, c.v, c.table.repeat(many, 1), cu, c.ctx.repeat(many), n, 1.0 / d, 0, 0, out,
+                                  lse, ws)
+        assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+        assert (np.abs(_f64(out).reshape(many, n, hq, d) - ref) <= R.attention_bound(mag)).all()
+        assert np.abs(_f64(lse).reshape(many, n, hq) - rl).max() <= 1e-4 * (1 + np.abs(rl).max())
