@@ -263,3 +263,14 @@ def test_large_values_under_scores_that_grow(n, hq, d):
         assert B.dspark_read_device_status(ws) == B.DSPARK_OK
         assert (np.abs(_f64(out).reshape(many, n, hq, d) - ref) <= R.attention_bound(mag)).all()
         assert np.abs(_f64(lse).reshape(many, n, hq) - rl).max() <= 1e-4 * (1 + np.abs(rl).max())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [49, 64, 65, 100, 127, 128])
+@pytest.mark.parametrize("ns,ctxs", [([1, 2], [130, 3000]), ([5, 0, 40], [64, 9, 300])])
+def test_many_query_heads_to_a_kv_head(g, d, ns, ctxs):
+    """Groups of up to 128 query heads, the most that is allowed, at each tiling that takes them."""
+    for window, sinks in ((0, 0), (100, 3)):
+        c = Cache(ns, ctxs, 1, d, 16, seed=g, evict=(window, sinks) if window else None)
+        for max_rows in (1, max(ns)):
+            _check_attention(c, g, window, sinks, seed=56, max_rows=max_rows)
