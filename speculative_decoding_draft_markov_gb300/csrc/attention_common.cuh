@@ -279,7 +279,7 @@ __device__ __forceinline__ Cut plan_ranges(const AttnArgs& a, Start* start, Plan
   // A unit of T tiles in ranges of m has T / m parts, which the join reads kJoinTogether at a time, one trip to memory each, and
   // a trip takes about as long as a tile: m >= sqrt(T / kJoinTogether), T the mean over requests and KV heads.  GB300, one
   // token over 50000 positions, 1 KV head: 18.0 us, cut as finely as there are CTAs 30.3; 8 KV heads over 5000 14.2 and 16.4,
-  // over 1500 the same.
+  // over 1500 the same.  Those batches are uniform: a long context among short ones is cut by the mean as well.
   const uint32_t least = max(1u, uint32_t(ceilf(sqrtf(float(all) / (float(a.Hkv) * float(a.bs * kJoinTogether))))));
   const uint32_t n_ranges = min(kSets * gridDim.x, (all + least - 1) / least), some = max(n_ranges, 1u);
   const uint32_t each = all / some, extra = all - each * some, first = uint32_t(before + incl - mine);

@@ -10,13 +10,13 @@
 // there.  It moves, and O and l are rescaled, when a maximum has outgrown it by more (kRescaleAt).  P is rounded to
 // bf16 for the second product, its sum is taken before that, in fp32.
 //
-// GB300, 2 prompts of about 4000 rows over 1000 .. 5000 cached positions, window 4096, Hq 32, Hkv 8: D 128 303 us of 238 at the
-// measured matrix rate (79%), 19 us of it the join and its launch; D 64 292 us (132 by its products, 206 by its exponentials at
+// GB300, 2 prompts of about 4000 rows over 1000 .. 5000 cached positions, window 4096, Hq 32, Hkv 8: D 128 304 us of 238 at the
+// measured matrix rate (78%), 19 us of it the join and its launch; D 64 296 us (132 by its products, 206 by its exponentials at
 // 16 a cycle and SM).  What holds it is the chain of one tile, S into registers, maximum, exponentials, P, product,
 // next S, which two tiles in turn do not quite hide (tensor pipes 62% busy, 4.4 instructions an exponential).  Slower or the
 // same, each measured on D 128: P handed on in 4 or 8 parts (338, 389 us); all eight warps on each tile together
-// (356); a polynomial for an eighth to a half of the exponentials (319 .. 365; D 64 with an eighth 280, not kept for one
-// head size); the first half's store waited for later, and the MMA loop in one thread (no change).
+// (356); a polynomial for an eighth to a half of the exponentials (319 .. 365; D 64, then 292 us, 280 with an eighth and 279
+// with a quarter); the first half's store waited for later, and the MMA loop in one thread (no change).
 #include <type_traits>
 
 #include "attention_common.cuh"
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld_wait();
         tc::tc_fence_before();  // O has been read: the next unit's first product may follow its first P
         // 32-byte stores: a thread's row is D lanes in a row, other lanes' rows lie elsewhere.  The caller's tensor may
-        // begin at any multiple of 16 bytes, and then takes two stores.
+        // begin at any multiple of 16 bytes, and then takes two stores (the branch: 2 us of 296 with D 64, none with D 128; each kind in a loop of its own 315 and 313).
         const bool out_32b = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         if (valid && partial) {
 #pragma unroll

@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(tc::smem_u32(&sh->tmem_base), C::kTmemCols);
     tc::tmem_relinquish();
   }
-  // rows of Q past the unit's last are never loaded: zeros, so that their scores are 0
+  // A unit's Q is always `tokens` rows, beyond its last the next request's (or zeros past the last packed row), whose
+  // results nobody stores.  Rows of the tile beyond those are never loaded: zeros, so that their scores are 0.
   for (int i = tid; i < kSets * C::kQBufs * C::kQBytes / 16; i += kThreads)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();

@@ -84,6 +84,10 @@ template <> struct Pack8<float> {
 // cycle and SM: short windows are bound by the instructions before the first row.  Slower, each measured there: the factors worked out per
 // row; rows through shared memory by asynchronous copies (238 us where registers took 212); the biases asked for before the
 // search (153 us for 146); one wave of blocks, each over many windows (197 for 146).
+// In place a row's logits are asked for when its rules are known, for the groups of 8 ids that a rule changes (under a
+// mask nearly all of them): 256 windows of 1 .. 8 rows 200 us with the mask, 180 without (out of place 147 and 139), of 8
+// rows 303 (218), of one row 91 (69); 8 windows of 16 rows in fp32 without a mask 16.0 (26.1), with one 27.4 (27.1); one
+// row 3.3 (3.1).  The sectors that the rules touch are worth 120, 42, 201, 35, 1.3, 19 and 0.1 us.
 // kAhead: rows in flight; kBlocks: blocks on an SM, which sets the registers.
 template <typename T, bool kInPlace, int kAhead, int kBlocks>
 __global__ void __launch_bounds__(kRuleThreads, kBlocks) rules_kernel(const __grid_constant__ RuleArgs a) {

@@ -160,7 +160,9 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   // A unit is cut about once where units outnumber the ranges (64 windows over up to 32000 positions: two parts at a time 83.2
   // us, eight 85.1; prompts 306 and 316), and often where there are few (one token over 5000 positions: two 20.4, four 19.1,
   // eight 16.9).  A prompt has so many rows that their number counts for more than their parts (500 rows: two 22.8, sixteen
-  // 28.0; 100 over 50000 positions: 42.7 and 40.3).
+  // 28.0; 100 over 50000 positions: 42.7 and 40.3).  The number of units says nothing of a long context among short ones: 1 of
+  // 30000 positions among 15 of 300, 8 KV heads, D 128, takes two parts (36.2) though sixteen were better (29.4), 1 of 100000
+  // among 63 of 500 as well (91.7 and 85.9); with one KV head both take sixteen (18.0, two 41.1; 28.6, two 66.2).
   const bool many_parts = !prompts && n_ranges > int64_t(4) * Hkv * std::max(bs, rows / a.tokens);
   const dim3 grid(n_ranges, ((prompts ? kTile : 0) + a.tokens * g + 7) / 8);
   auto join = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, a, unit_rows); };
