@@ -79,9 +79,13 @@ class PagedCache:
     def settle(self, r: int, length: int, since: int = 0, stream=None) -> None:
         """Request r had `length` tokens in the cache after some step (ctx_len, read back at any later time); `since`
         tokens were reserved for its steps after that one.  Lowers the bound to what that allows, and gives back the
-        pages that lie between the sinks and the window of the next position, which no later row sees."""
+        pages that lie between the sinks and the window of the next position, which no later row sees.  A length of a
+        request that has been released since must not be passed; one beyond the bound is seen to be such and changes
+        nothing."""
         if length < 0 or since < 0:
             raise ValueError("length and since must not be negative")
+        if length > self.bound[r]:
+            return
         self.bound[r] = min(self.bound[r], length + since)
         if not self.window:
             return

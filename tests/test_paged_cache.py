@@ -82,3 +82,16 @@ def test_pages_behind_the_window_come_back(window, n_sink, lag):
     for r in range(2):
         c.release(r)
     assert sorted(c.free) == list(range(2 * one)) and (c.page_table == -1).all()
+
+
+def test_a_length_of_an_earlier_request_takes_no_pages():
+    """A length that came late, after its request was released and the place taken by a shorter one."""
+    c = _cache(40, 1, 40, window=32)
+    c.reserve(0, 500)
+    c.release(0)
+    c.reserve(0, 60)
+    before = list(c.pages[0])
+    c.settle(0, 490)
+    assert c.pages[0] == before and c.bound[0] == 60 and (c.page_table[0, :4] >= 0).all()
+    c.settle(0, 60)
+    assert c.pages[0] == [None] + before[1:] and c.page_table[0, 0] == -1
