@@ -539,6 +539,79 @@ DSPARK_API int dspark_history_build(const int32_t* tokens, int n_tokens, const i
 DSPARK_API int dspark_history_commit(const int32_t* out_tokens, int bs, int gamma, int V, int16_t* hist, void* ws,
                                      size_t ws_bytes, dspark_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The paged cache in 8 bits.  Pages as above, but of e4m3: k_cache and v_cache are [n_pages, Hkv, page_size, D] bytes,
+ * and kv_scale [n_pages, Hkv, page_size, 2] holds an exponent byte for each position's K and V of each KV head:
+ *     K = code * 2^(kv_scale[.., 0] - 127),   V = code * 2^(kv_scale[.., 1] - 127);   byte 255: the vector is NaN
+ * i.e. the power of two under which the vector's largest magnitude is at most 448 (all codes that an append writes are
+ * numbers, the largest of a vector above 224 unless the vector is tiny or 0).  A value x is off by at most 2^-4 |x| where its
+ * code is normal, by 2^-10 of the power of two below.  Page table, lengths and limits are those of the bf16 cache, and
+ * dtype is the queries', keys' and values' (bf16).
+ *
+ * append_kv8: dspark_append_kv with that cache.  The rotated K is rounded once, from fp32.  A vector with a NaN or an
+ * infinity is written as NaN (byte 255, codes 0).  Device errors, limits and aliases as dspark_append_kv. */
+DSPARK_API int dspark_append_kv8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, int dtype, const int32_t* cu_seqlens, const int32_t* ctx_len, int bs,
+                                 int rows, const float* cos_sin, int max_pos, int rot, int interleaved,
+                                 const int32_t* page_table, int max_pages, int n_pages, int page_size, int Hq, int Hkv,
+                                 int D, void* q_out, void* k_cache, void* v_cache, uint8_t* kv_scale, void* ws,
+                                 size_t ws_bytes, dspark_stream_t stream);
+
+/* Read back: every position that some packed row of a request sees (dspark_window_attention's j, for any of its rows)
+ * goes to a bf16 cache of the same page_size, Hkv and D, rounded once (exact but for values below bf16's normal range):
+ * slot p % page_size of page out_table[r, p / page_size].  Nothing else is written.
+ *   out_table    device [bs, max_pages] int32; may be page_table itself.  Pages that two requests share have to hold the
+ *                same values in both.
+ *   k_out, v_out device [n_out_pages, Hkv, page_size, D] bf16, no part of the 8-bit cache
+ * With window = 0, ctx_len = length - 1 and one row to a request the whole of a sequence is read.
+ * Device errors (status word, EINVAL): as dspark_window_attention; a page number outside [0, n_pages), or outside
+ * [0, n_out_pages) in out_table, on a page that is read (left out). */
+DSPARK_API int dspark_read_kv8(const void* k_cache, const void* v_cache, const uint8_t* kv_scale, int dtype,
+                               const int32_t* page_table, int max_pages, int n_pages, int page_size,
+                               const int32_t* cu_seqlens, const int32_t* ctx_len, int bs, int rows, int Hkv, int D,
+                               int window, int n_sink, const int32_t* out_table, int n_out_pages, void* k_out,
+                               void* v_out, void* ws, size_t ws_bytes, dspark_stream_t stream);
+
+/* dspark_window_attention over the 8-bit cache (the same formulas, arguments, workspace, errors and limits).
+ *   k_scratch, v_scratch  device [n_pages, Hkv, page_size, D] bf16 each, or both NULL: pages of the same numbers that the
+ *                         call may overwrite.  Windows of more than 128 (row, query head) pairs to a KV head (64 where
+ *                         D = 64), by max_rows, are then read back into them first, once for all rows (dspark_read_kv8), and
+ *                         attended to there; without them the windows' kernel takes such calls too, more slowly.  One pair
+ *                         serves all layers of a model.  Calls that can overlap on the device must not share it. */
+DSPARK_API int dspark_window_attention_kv8(const void* q, int64_t q_stride, int dtype, const void* k_cache,
+                                           const void* v_cache, const uint8_t* kv_scale, const int32_t* page_table,
+                                           int max_pages, int n_pages, int page_size, const int32_t* cu_seqlens,
+                                           const int32_t* ctx_len, int bs, int rows, int max_rows, int Hq, int Hkv, int D,
+                                           float scale, int window, int n_sink, void* out, float* lse, void* k_scratch,
+                                           void* v_scratch, void* ws, size_t ws_bytes, dspark_stream_t stream);
+
+/* Log probabilities of given tokens.  With x = logits of a packed row / temperature, for its token t:
+ *     logprob = x_t - log sum_v exp(x_v),   entropy = - sum_v p_v log p_v,   p = softmax(x)
+ *     rank    = 1 + the ids before t, by logit, then by the lower id
+ *     top_ids, top_logprobs = the first top_n ids in that order, with their log probabilities
+ * in fp32 (sums over the row in a fixed order).
+ *   logits      device [rows, V] (dtype, fp32 or bf16)
+ *   tokens      device [n, per] int32.  Given cu_seqlens [n + 1], token (r, j) belongs to row cu_seqlens[r] + j: a
+ *               verification's out_tokens [bs, gamma + 1] with the packed windows, or the next tokens of prompts.  With
+ *               NULL it belongs to row r * per + j (n * per <= rows).  -1: nothing is asked.
+ *   logprob     device [n, per] fp32;  entropy [n, per] fp32, rank [n, per] int32: or NULL
+ *   top_ids     device [n, per, top_n] int32, top_logprobs [n, per, top_n] fp32; both NULL with top_n = 0
+ *   ws          dspark_token_logprobs_workspace_bytes(n * per, V, top_n) bytes, zeroed once; calls that can overlap on the
+ *               device must not share it
+ * Where nothing is asked: logprob 0, entropy 0, rank 0, ids -1 with -infinity.  A logit of -infinity has probability 0 and is
+ * no alternative; where fewer than top_n are left the rest is -1 with -infinity.  A row that holds a NaN or +infinity, or
+ * nothing but -infinity, has NaN for its logprob, entropy and alternatives' log probabilities; a NaN is no alternative and
+ * stands before nothing.
+ * Device errors (status word, EINVAL; nothing is asked there): a token outside [-1, V), a token beyond its window,
+ * a window that begins below 0 or ends beyond rows.
+ * Limits: V % 8 == 0, 8 <= V < 2^24, n * per <= 2^20, top_n <= DSPARK_MAX_TOP; temperature > 0, it and its reciprocal finite. */
+#define DSPARK_MAX_TOP 32
+DSPARK_API size_t dspark_token_logprobs_workspace_bytes(int items, int V, int top_n);
+DSPARK_API int dspark_token_logprobs(const void* logits, int dtype, int rows, int V, const int32_t* cu_seqlens, int n,
+                                     int per, const int32_t* tokens, float temperature, float* logprob, float* entropy,
+                                     int32_t* rank, int32_t* top_ids, float* top_logprobs, int top_n, void* ws,
+                                     size_t ws_bytes, dspark_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

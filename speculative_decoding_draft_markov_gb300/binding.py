@@ -65,6 +65,14 @@ _SIGS.update({
                                    _vp, _sz, _vp]),
     "dspark_history_build": (_i, [_vp, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp]),
     "dspark_history_commit": (_i, [_vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "dspark_append_kv8": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _vp, _vp, _i, _i, _vp, _i, _i, _i, _vp, _i, _i, _i,
+                               _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dspark_read_kv8": (_i, [_vp, _vp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp,
+                             _sz, _vp]),
+    "dspark_window_attention_kv8": (_i, [_vp, _i64, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                         _f, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dspark_token_logprobs_workspace_bytes": (_sz, [_i, _i, _i]),
+    "dspark_token_logprobs": (_i, [_vp, _i, _i, _i, _vp, _i, _i, _vp, _f, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
 })
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -398,7 +406,7 @@ def _calls():
         spec = importlib.util.spec_from_file_location("_calls", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
-        mod.init(torch.float32, torch.bfloat16, torch.int32, torch.int16, torch._C._cuda_getCurrentRawStream,
+        mod.init(torch.float32, torch.bfloat16, torch.int32, torch.int16, torch.float8_e4m3fn, torch.uint8, torch._C._cuda_getCurrentRawStream,
                  torch._C._cuda_getDevice, DSparkError, DSparkDeviceError, torch.Tensor.data_ptr, torch.Tensor.get_device,
                  torch.Tensor.is_contiguous)
         _CALLS = mod
@@ -455,3 +463,54 @@ def dspark_history_build(tokens, start, n_prompt, hist, ws, stream=None):
 def dspark_history_commit(out_tokens, hist, ws, stream=None):
     """Add a step's out_tokens [bs, gamma + 1] (dspark_verify; -1 skipped) to the said counts of hist [bs, V]."""
     (_CALLS or _calls()).history_commit(out_tokens, hist, ws, stream)
+
+
+# the 8-bit cache: k_cache, v_cache [n_pages, Hkv, page_size, D] float8_e4m3fn, kv_scale [n_pages, Hkv, page_size, 2]
+# uint8 (exponent bytes of K and V)
+
+def dspark_append_kv8(q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k_cache, v_cache, kv_scale, ws,
+                      interleaved=False, stream=None):
+    """dspark_append_kv into an 8-bit cache: rotate q and k, quantise k and v, append."""
+    (_CALLS or _calls()).append_kv8(q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k_cache, v_cache, kv_scale,
+                                    ws, interleaved, stream)
+
+
+def dspark_read_kv8(k_cache, v_cache, kv_scale, page_table, cu_seqlens, ctx_len, rows, window, n_sink, out_table, k_out,
+                    v_out, ws, stream=None):
+    """Read what the packed rows (of `rows` in all) see of an 8-bit cache back to pages k_out, v_out [n_out_pages, Hkv,
+    page_size, D] bf16 under out_table [bs, max_pages] (may be page_table)."""
+    (_CALLS or _calls()).read_kv8(k_cache, v_cache, kv_scale, page_table, cu_seqlens, ctx_len, rows, window, n_sink,
+                                  out_table, k_out, v_out, ws, stream)
+
+
+def dspark_window_attention_kv8(q, k_cache, v_cache, kv_scale, page_table, cu_seqlens, ctx_len, max_rows, scale, window,
+                                n_sink, out, lse, k_scratch, v_scratch, ws, stream=None):
+    """dspark_window_attention over an 8-bit cache.  k_scratch, v_scratch: bf16 pages of the cache's shape that long
+    windows (prompts) are read back to first, or None both."""
+    (_CALLS or _calls()).window_attention_kv8(q, k_cache, v_cache, kv_scale, page_table, cu_seqlens, ctx_len, max_rows,
+                                              scale, window, n_sink, out, lse, k_scratch, v_scratch, ws, stream)
+
+
+DSPARK_MAX_TOP = 32
+
+
+def dspark_token_logprobs_workspace_bytes(items: int, V: int, top_n: int) -> int:
+    return int(lib().dspark_token_logprobs_workspace_bytes(items, V, top_n))
+
+
+def alloc_logprobs_workspace(items: int, V: int, top_n: int, device="cuda"):
+    """A zero-initialised workspace tensor of dspark_token_logprobs for up to `items` tokens."""
+    import torch
+    n = dspark_token_logprobs_workspace_bytes(items, V, top_n)
+    if n == 0:
+        raise ValueError("invalid sizes for a workspace of log probabilities")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def dspark_token_logprobs(logits, cu_seqlens, tokens, temperature, logprob, entropy, rank, top_ids, top_logprobs, ws,
+                          stream=None):
+    """Log probabilities of tokens [n, per] under the packed rows logits [rows, V]: token (r, j) belongs to row
+    cu_seqlens[r] + j, or with None to row r * per + j; -1 asks nothing.  logprob, entropy [n, per] fp32, rank [n, per]
+    int32 (entropy and rank may be None); top_ids [n, per, top_n] int32 with top_logprobs fp32, or None both."""
+    (_CALLS or _calls()).token_logprobs(logits, cu_seqlens, tokens, temperature, logprob, entropy, rank, top_ids,
+                                        top_logprobs, ws, stream)

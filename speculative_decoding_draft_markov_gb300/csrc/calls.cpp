@@ -14,7 +14,7 @@
 namespace {
 
 // set by init
-PyObject *t_f32, *t_bf16, *t_i32, *t_i16;          // torch's types
+PyObject *t_f32, *t_bf16, *t_i32, *t_i16, *t_f8, *t_u8;  // torch's types
 PyObject *current_stream, *current_device, *error, *device_error;  // raw stream of a device; DSparkError, DSparkDeviceError
 PyObject *m_data_ptr, *m_get_device, *m_is_contiguous;             // a tensor's methods, found once
 PyObject *s_dtype, *s_shape, *s_stride, *s_cuda_stream, *s_numel;
@@ -195,6 +195,13 @@ bool expect(Py_ssize_t n, Py_ssize_t want) {
   return n == want;
 }
 
+// k_cache, v_cache and kv_scale of an 8-bit cache of shape c.
+bool cache8(PyObject* const* t, const int64_t* c, void** k, void** v, void** scale, Place& at) {
+  const int64_t d[4] = {c[0], c[1], c[2], 2};
+  return dense(t[0], t_f8, 0, nullptr, "k_cache", k, at) && dense(t[1], t_f8, 4, c, "v_cache", v, at) &&
+         dense(t[2], t_u8, 4, d, "kv_scale", scale, at);
+}
+
 template <typename T> T* as(void* p) { return static_cast<T*>(p); }
 
 // q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k_cache, v_cache, ws, interleaved, stream
@@ -341,19 +348,157 @@ PyObject* history_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return result(rc, "dspark_history_commit");
 }
 
-// float32, bfloat16, int32, int16, current raw stream of a device, current device, DSparkError, DSparkDeviceError, and the
-// tensors' data_ptr, get_device and is_contiguous
-PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// q, k, v, cu_seqlens, ctx_len, cos_sin, page_table, q_out, k_cache, v_cache, kv_scale, ws, interleaved, stream
+PyObject* append_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!expect(n, 14)) return nullptr;
+  PyObject* dt;
+  int64_t c[4], k3[3], v3[3], cu_n, table[2], cs[2], q3[3], qs = 0, ks, vs;
+  void *q = nullptr, *k, *v, *cu, *ctx, *cos, *pt, *qo = nullptr, *kc, *vc, *sc, *ws;
+  size_t ws_bytes;
+  Place at;
+  dspark_stream_t s;
+  const int code = dtype_code(a[1], &dt), turn = PyObject_IsTrue(a[12]);
+  if (!dt || turn < 0 || !shape_of(a[8], 4, c, "k_cache") || !shape_of(a[1], 3, k3, "k") || !shape_of(a[2], 3, v3, "v") ||
+      !length(a[3], &cu_n, "cu_seqlens") ||
+      !shape_of(a[6], 2, table, "page_table") || !shape_of(a[5], 2, cs, "cos_sin"))
+    return nullptr;
+  const int64_t rows = k3[0], bs = cu_n - 1, Hkv = c[1], D = c[3];
+  int64_t Hq = Hkv;
+  if (a[0] != Py_None) {
+    if (!shape_of(a[0], 3, q3, "q")) return nullptr;
+    Hq = q3[1];
+    const int64_t o[3] = {rows, Hq, D};
+    if (!rows_of(a[0], dt, q3, rows, Hq, D, "q", &q, &qs, at) || !dense(a[7], dt, 3, o, "q_out", &qo, at)) return nullptr;
+  }
+  if (!rows_of(a[1], dt, k3, rows, Hkv, D, "k", &k, &ks, at) || !rows_of(a[2], dt, v3, rows, Hkv, D, "v", &v, &vs, at) ||
+      !dense(a[3], t_i32, 0, nullptr, "cu_seqlens", &cu, at) || !dense1(a[4], t_i32, bs, "ctx_len", &ctx, at) ||
+      !dense(a[5], t_f32, 0, nullptr, "cos_sin", &cos, at) || !table_of(a[6], table, bs, &pt, at) ||
+      !cache8(a + 8, c, &kc, &vc, &sc, at) || !workspace(a[11], &ws, &ws_bytes, at) ||
+      !stream_of(a[13], "dspark_append_kv8", at, &s))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = dspark_append_kv8(q, qs, k, ks, v, vs, code, as<int32_t>(cu), as<int32_t>(ctx), int(bs), int(rows), as<float>(cos),
+                         int(cs[0]), int(cs[1]), turn, as<int32_t>(pt), int(table[1]), int(c[0]), int(c[2]), int(Hq), int(Hkv),
+                         int(D), qo, kc, vc, as<uint8_t>(sc), ws, ws_bytes, s);
+  Py_END_ALLOW_THREADS
+  return result(rc, "dspark_append_kv8");
+}
+
+// k_cache, v_cache, kv_scale, page_table, cu_seqlens, ctx_len, rows, window, n_sink, out_table, k_out, v_out, ws, stream
+PyObject* read_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!expect(n, 14)) return nullptr;
+  PyObject* dt;
+  int64_t c[4], o[4], cu_n, table[2], to[2];
+  void *kc, *vc, *sc, *pt, *cu, *ctx, *ot, *ko, *vo, *ws;
+  size_t ws_bytes;
+  Place at;
+  dspark_stream_t s;
+  int rows, window, n_sink;
+  const int code = dtype_code(a[10], &dt);
+  if (!dt || !to_int(a[6], &rows, "rows") || !to_int(a[7], &window, "window") || !to_int(a[8], &n_sink, "n_sink") ||
+      !shape_of(a[0], 4, c, "k_cache") || !shape_of(a[10], 4, o, "k_out") || !length(a[4], &cu_n, "cu_seqlens") ||
+      !shape_of(a[3], 2, table, "page_table") || !shape_of(a[9], 2, to, "out_table"))
+    return nullptr;
+  const int64_t bs = cu_n - 1;
+  if (to[0] != table[0] || to[1] != table[1]) return bad("out_table", "must have page_table's shape"), nullptr;
+  if (o[1] != c[1] || o[2] != c[2] || o[3] != c[3]) return bad("k_out", "must have the cache's heads, page size and lanes"), nullptr;
+  if (!cache8(a, c, &kc, &vc, &sc, at) || !table_of(a[3], table, bs, &pt, at) ||
+      !dense(a[4], t_i32, 0, nullptr, "cu_seqlens", &cu, at) || !dense1(a[5], t_i32, bs, "ctx_len", &ctx, at) ||
+      !dense(a[9], t_i32, 0, nullptr, "out_table", &ot, at) || !dense(a[10], dt, 0, nullptr, "k_out", &ko, at) ||
+      !dense(a[11], dt, 4, o, "v_out", &vo, at) || !workspace(a[12], &ws, &ws_bytes, at) ||
+      !stream_of(a[13], "dspark_read_kv8", at, &s))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = dspark_read_kv8(kc, vc, as<uint8_t>(sc), code, as<int32_t>(pt), int(table[1]), int(c[0]), int(c[2]), as<int32_t>(cu),
+                       as<int32_t>(ctx), int(bs), rows, int(c[1]), int(c[3]), window, n_sink, as<int32_t>(ot), int(o[0]), ko, vo,
+                       ws, ws_bytes, s);
+  Py_END_ALLOW_THREADS
+  return result(rc, "dspark_read_kv8");
+}
+
+// q, k_cache, v_cache, kv_scale, page_table, cu_seqlens, ctx_len, max_rows, scale, window, n_sink, out, lse, k_scratch,
+// v_scratch, ws, stream
+PyObject* window_attention_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!expect(n, 17)) return nullptr;
+  PyObject* dt;
+  int64_t c[4], q3[3], cu_n, table[2], qs;
+  void *q, *kc, *vc, *sc, *pt, *cu, *ctx, *out, *lse, *kt, *vt, *ws;
+  size_t ws_bytes;
+  Place at;
+  dspark_stream_t s;
+  int max_rows, window, n_sink;
+  const int code = dtype_code(a[0], &dt);
+  const double scale = PyFloat_AsDouble(a[8]);
+  if (!dt || (scale == -1. && PyErr_Occurred()) || !to_int(a[7], &max_rows, "max_rows") || !to_int(a[9], &window, "window") ||
+      !to_int(a[10], &n_sink, "n_sink") || !shape_of(a[1], 4, c, "k_cache") || !shape_of(a[0], 3, q3, "q") ||
+      !length(a[5], &cu_n, "cu_seqlens") || !shape_of(a[4], 2, table, "page_table"))
+    return nullptr;
+  const int64_t rows = q3[0], Hq = q3[1], bs = cu_n - 1, Hkv = c[1], D = c[3];
+  const int64_t o[3] = {rows, Hq, D};
+  if (!rows_of(a[0], dt, q3, rows, Hq, D, "q", &q, &qs, at) || !cache8(a + 1, c, &kc, &vc, &sc, at) ||
+      !table_of(a[4], table, bs, &pt, at) ||
+      !dense(a[5], t_i32, 0, nullptr, "cu_seqlens", &cu, at) || !dense1(a[6], t_i32, bs, "ctx_len", &ctx, at) ||
+      !dense(a[11], dt, 3, o, "out", &out, at) || !dense2(a[12], t_f32, rows, Hq, "lse", &lse, at) ||
+      !dense(a[13], dt, 4, c, "k_scratch", &kt, at) || !dense(a[14], dt, 4, c, "v_scratch", &vt, at) ||
+      !workspace(a[15], &ws, &ws_bytes, at) || !stream_of(a[16], "dspark_window_attention_kv8", at, &s))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = dspark_window_attention_kv8(q, qs, code, kc, vc, as<uint8_t>(sc), as<int32_t>(pt), int(table[1]), int(c[0]), int(c[2]),
+                                   as<int32_t>(cu), as<int32_t>(ctx), int(bs), int(rows), max_rows, int(Hq), int(Hkv), int(D),
+                                   float(scale), window, n_sink, out, as<float>(lse), kt, vt, ws, ws_bytes, s);
+  Py_END_ALLOW_THREADS
+  return result(rc, "dspark_window_attention_kv8");
+}
+
+// logits, cu_seqlens, tokens, temperature, logprob, entropy, rank, top_ids, top_logprobs, ws, stream
+PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!expect(n, 11)) return nullptr;
-  PyObject** const to[11] = {&t_f32, &t_bf16, &t_i32, &t_i16, &current_stream, &current_device, &error, &device_error,
-                             &m_data_ptr, &m_get_device, &m_is_contiguous};
-  for (int i = 0; i < 11; ++i) *to[i] = Py_NewRef(a[i]);
+  PyObject* dt;
+  int64_t x[2], t[2], top[3] = {0, 0, 0};
+  void *in, *cu, *tokens, *lp, *ent, *rank, *ids, *best, *ws;
+  size_t ws_bytes;
+  Place at;
+  dspark_stream_t s;
+  const int code = dtype_code(a[0], &dt);
+  const double temperature = PyFloat_AsDouble(a[3]);
+  if (!dt || (temperature == -1. && PyErr_Occurred()) || !shape_of(a[0], 2, x, "logits") || !shape_of(a[2], 2, t, "tokens") ||
+      (a[7] != Py_None && !shape_of(a[7], 3, top, "top_ids")))
+    return nullptr;
+  if (a[4] == Py_None) return bad("logprob", "must be given"), nullptr;
+  if (a[7] != Py_None && (top[0] != t[0] || top[1] != t[1])) return bad("top_ids", "must have one row per token"), nullptr;
+  if (top[2] > INT_MAX || t[0] * t[1] > INT_MAX) return bad("tokens", "is beyond 32 bits"), nullptr;
+  if (!dense(a[0], dt, 0, nullptr, "logits", &in, at) || !dense1(a[1], t_i32, t[0] + 1, "cu_seqlens", &cu, at) ||
+      !dense(a[2], t_i32, 0, nullptr, "tokens", &tokens, at) || !dense2(a[4], t_f32, t[0], t[1], "logprob", &lp, at) ||
+      !dense2(a[5], t_f32, t[0], t[1], "entropy", &ent, at) || !dense2(a[6], t_i32, t[0], t[1], "rank", &rank, at) ||
+      !dense(a[7], t_i32, 0, nullptr, "top_ids", &ids, at) || !dense(a[8], t_f32, 3, top, "top_logprobs", &best, at) ||
+      !workspace(a[9], &ws, &ws_bytes, at) || !stream_of(a[10], "dspark_token_logprobs", at, &s))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = dspark_token_logprobs(in, code, int(x[0]), int(x[1]), as<int32_t>(cu), int(t[0]), int(t[1]), as<int32_t>(tokens),
+                             float(temperature), as<float>(lp), as<float>(ent), as<int32_t>(rank), as<int32_t>(ids),
+                             as<float>(best), int(top[2]), ws, ws_bytes, s);
+  Py_END_ALLOW_THREADS
+  return result(rc, "dspark_token_logprobs");
+}
+
+// float32, bfloat16, int32, int16, float8_e4m3fn, uint8, current raw stream of a device, current device, DSparkError,
+// DSparkDeviceError, and the tensors' data_ptr, get_device and is_contiguous
+PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!expect(n, 13)) return nullptr;
+  PyObject** const to[13] = {&t_f32, &t_bf16, &t_i32, &t_i16, &t_f8, &t_u8, &current_stream, &current_device, &error,
+                             &device_error, &m_data_ptr, &m_get_device, &m_is_contiguous};
+  for (int i = 0; i < 13; ++i) *to[i] = Py_NewRef(a[i]);
   Py_RETURN_NONE;
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(init), FAST(append_kv), FAST(window_attention), FAST(process_logits), FAST(history_build),
-                         FAST(history_commit), {nullptr, nullptr, 0, nullptr}};
+                         FAST(history_commit), FAST(append_kv8), FAST(read_kv8), FAST(window_attention_kv8),
+                         FAST(token_logprobs), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -125,4 +125,26 @@ cudaError_t launch_history_build(const int32_t* tokens, int n_tokens, const int3
 cudaError_t launch_history_commit(const int32_t* out_tokens, int bs, int gamma, int V, int16_t* hist, uint32_t* status,
                                   cudaStream_t s);
 
+// ---- the 8-bit paged cache and the tokens' log probabilities ---------------------------------
+cudaError_t launch_append_kv8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const int32_t* cu, const int32_t* ctx, int bs, int rows,
+                              const float* cos_sin, int max_pos, int rot, int interleaved, const int32_t* page_table,
+                              int max_pages, int n_pages, int page_shift, int Hq, int Hkv, int D, void* q_out,
+                              void* k_cache, void* v_cache, uint8_t* kv_scale, uint32_t* status, cudaStream_t s);
+cudaError_t launch_read_kv8(const void* k_cache, const void* v_cache, const uint8_t* kv_scale, const int32_t* page_table,
+                            int max_pages, int n_pages, int page_shift, const int32_t* cu, const int32_t* ctx, int bs,
+                            int rows, int Hkv, int D, int window, int n_sink, const int32_t* out_table, int n_out_pages,
+                            void* k_out, void* v_out, uint32_t* status, cudaStream_t s);
+cudaError_t launch_window_attention_kv8(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                        const uint8_t* kv_scale, const int32_t* page_table, int max_pages, int n_pages,
+                                        int page_shift, const int32_t* cu, const int32_t* ctx, int bs, int rows,
+                                        int max_rows, int Hq, int Hkv, int D, float scale, int window, int n_sink,
+                                        void* out, float* lse, void* k_scratch, void* v_scratch, void* ws,
+                                        cudaStream_t s);
+size_t token_logprobs_ws_bytes(int items, int V, int top_n);
+cudaError_t launch_token_logprobs(const void* logits, int dtype, int rows, int V, const int32_t* cu, int bs,
+                                  const int32_t* tokens, int per, float temperature, float* logprob, float* entropy,
+                                  int32_t* rank, int32_t* top_ids, float* top_logprobs, int top_n, void* ws,
+                                  cudaStream_t s);
+
 }  // namespace dspark

@@ -1,0 +1,299 @@
+// dspark_append_kv8 and dspark_read_kv8: rotate, quantise and append the packed rows to an 8-bit paged cache, and read what
+// they see of it back to pages of bf16.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv8.cuh"
+#include "packed_rows.cuh"
+#include "pdl.h"
+#include "tc_host.h"
+
+namespace dspark {
+namespace {
+
+constexpr int kMaxAppendThreads = 256;
+
+struct AppendArgs {
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *cu, *ctx;
+  const float* cos_sin;
+  const int32_t* page_table;
+  __nv_bfloat16* q_out;
+  uint8_t *k_cache, *v_cache, *kv_scale;
+  uint32_t* status;
+  int bs, rows, max_pos, rot, max_pages, n_pages, page_shift, Hq, Hkv, D;
+};
+
+struct RowPlace {
+  int pos;       // position in its sequence; < 0: the row is skipped
+  int64_t slot;  // slots of the cache before (page, KV head 0, slot)
+};
+
+__device__ __forceinline__ void unpack8(uint4 w, float* x) {
+  x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
+  x[4] = bf16lo(w.z), x[5] = bf16hi(w.z), x[6] = bf16lo(w.w), x[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+// 8 values times `by` (a power of two) as codes
+__device__ __forceinline__ uint2 codes8(const float* x, float by) {
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = kv8::code2(x[2 * i] * by, x[2 * i + 1] * by);
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+// A memory-bound copy: two multiplications per element, and for K and V the largest magnitude of a head.  A block has one
+// row; an item is 16 lanes of one head: rotated by halves, lanes t .. t+7 and their partners t + rot/2 ..; otherwise 16
+// lanes in a row (8 interleaved pairs, or lanes that pass).  So each thread holds both lanes of its pairs and q_out may be q,
+// and a head's D / 16 items lie in neighbouring lanes of one warp, which agree on the head's power of two.
+// The rotated K goes into 8 bits from fp32, with one rounding.  Products and sums of a pair are rounded one by one (no fused
+// multiply-add), so that the powers of two are those of any plain fp32 evaluation.
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kMaxAppendThreads) append8_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ RowPlace place;
+  const int tid = threadIdx.x, lane = tid & 31;
+  pdl_enter();
+  const int row = blockIdx.x;
+  if (tid < 32) {
+    const int r = warp_request_of(a.cu, a.bs, a.rows, row, lane);
+    if (lane == 0) {
+      RowPlace pl{-1, 0};
+      if (r < 0) {
+        set_status(a.status, DSPARK_EINVAL);
+      } else if (r < a.bs) {
+        const int c = a.ctx[r];
+        const int64_t p = int64_t(c) + row - a.cu[r];
+        const int64_t pi = p >> a.page_shift;
+        int page = -1;
+        if (c >= 0 && p >= 0 && p < a.max_pos && pi < a.max_pages)
+          page = a.page_table[int64_t(r) * a.max_pages + pi];
+        if (page >= 0 && page < a.n_pages) {
+          pl.pos = int(p);
+          pl.slot = (int64_t(page) * a.Hkv << a.page_shift) + (p & ((1 << a.page_shift) - 1));
+        } else {
+          set_status(a.status, DSPARK_EINVAL);
+        }
+      }
+      place = pl;
+    }
+  }
+  __syncthreads();
+
+  const int per_head = a.D / 16, turned = a.rot / 16;
+  const RowPlace pl = place;
+  if (pl.pos < 0) return;
+  const int items = (a.Hq + 2 * a.Hkv) * per_head;
+  for (int first = tid - lane; first < items; first += int(blockDim.x)) {  // the warp's: all its lanes agree below
+    const int it = first + lane;
+    const bool live = it < items;
+    const int hh = live ? it / per_head : 0, c = live ? it - hh * per_head : 0;
+    const bool is_q = hh < a.Hq, is_k = !is_q && hh < a.Hq + a.Hkv;
+    const int kv = is_q ? 0 : hh - a.Hq - (is_k ? 0 : a.Hkv);
+    const __nv_bfloat16* src = is_q   ? a.q + int64_t(row) * a.q_stride + hh * a.D
+                               : is_k ? a.k + int64_t(row) * a.k_stride + kv * a.D
+                                      : a.v + int64_t(row) * a.v_stride + kv * a.D;
+    const bool rotates = (is_q || is_k) && c < turned;
+    const int lo = !kInterleaved && rotates ? c * 8 : c * 16;
+    const int hi = !kInterleaved && rotates ? lo + a.rot / 2 : lo + 8;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+    if (live) x = *reinterpret_cast<const uint4*>(src + lo), y = *reinterpret_cast<const uint4*>(src + hi);
+    float u[8], w[8];
+    unpack8(x, u);
+    unpack8(y, w);
+    if (live && rotates) {
+      // pairs t0 .. t0+7 of this position: cosines and sines
+      const float* cs = a.cos_sin + int64_t(pl.pos) * a.rot + c * 8;
+      float co[8], si[8];
+      *reinterpret_cast<float4*>(co) = *reinterpret_cast<const float4*>(cs);
+      *reinterpret_cast<float4*>(co + 4) = *reinterpret_cast<const float4*>(cs + 4);
+      *reinterpret_cast<float4*>(si) = *reinterpret_cast<const float4*>(cs + a.rot / 2);
+      *reinterpret_cast<float4*>(si + 4) = *reinterpret_cast<const float4*>(cs + a.rot / 2 + 4);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        float& p0 = kInterleaved ? (t < 4 ? u[2 * t] : w[2 * t - 8]) : u[t];
+        float& p1 = kInterleaved ? (t < 4 ? u[2 * t + 1] : w[2 * t - 7]) : w[t];
+        const float n0 = __fsub_rn(__fmul_rn(p0, co[t]), __fmul_rn(p1, si[t]));
+        const float n1 = __fadd_rn(__fmul_rn(p1, co[t]), __fmul_rn(p0, si[t]));
+        p0 = n0, p1 = n1;
+      }
+      x = pack8(u);
+      y = pack8(w);
+    }
+    // the head's largest magnitude: as bits, so that a NaN is larger than everything
+    uint32_t top = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) top = max(top, max(__float_as_uint(u[t]) & 0x7FFFFFFFu, __float_as_uint(w[t]) & 0x7FFFFFFFu));
+    for (int o = 1; o < per_head; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+    if (!live) continue;
+    if (is_q) {
+      __nv_bfloat16* dst = a.q_out + (int64_t(row) * a.Hq + hh) * a.D;
+      *reinterpret_cast<uint4*>(dst + lo) = x;
+      *reinterpret_cast<uint4*>(dst + hi) = y;
+      continue;
+    }
+    const uint32_t byte = kv8::exponent_byte(top);
+    const float by = byte == kv8::kNan ? 0.f : kv8::power(127 - int(byte));
+    if (byte == kv8::kNan) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) u[t] = w[t] = 0.f;
+    }
+    const int64_t slot = pl.slot + (int64_t(kv) << a.page_shift);
+    uint8_t* dst = (is_k ? a.k_cache : a.v_cache) + slot * a.D;
+    *reinterpret_cast<uint2*>(dst + lo) = codes8(u, by);
+    *reinterpret_cast<uint2*>(dst + hi) = codes8(w, by);
+    if (c == 0) a.kv_scale[slot * 2 + (is_k ? 0 : 1)] = uint8_t(byte);
+  }
+}
+
+// ------------------------------------------------------------------------------- reading back
+
+struct ReadArgs {
+  const uint8_t *k_cache, *v_cache, *kv_scale;
+  const int32_t *page_table, *cu, *ctx, *out_table;
+  __nv_bfloat16 *k_out, *v_out;
+  uint32_t* status;
+  int64_t cache_limit;
+  int max_pages, n_pages, page_shift, block_shift, bs, rows, Hkv, D, window, n_sink, n_out_pages;
+};
+
+constexpr int kReadThreads = 256;
+
+// 16 codes to 16 values of bf16: exact, but for values below bf16's normal range.
+__device__ __forceinline__ void widen16(uint4 w, float by, uint4* out) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = kv8::values(in[i] & 0xFFFFu), b = kv8::values(in[i] >> 16);
+    r[2 * i] = pack2(a.x * by, a.y * by), r[2 * i + 1] = pack2(b.x * by, b.y * by);
+  }
+  out[0] = make_uint4(r[0], r[1], r[2], r[3]), out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// What a request's packed rows see, in blocks of the cache (pages, or 32-slot pieces of larger pages): those that hold
+// sinks, then those of the window.  Blocks are counted over the requests; a unit is a block of one KV head, and the units are
+// dealt out to the blocks of the grid in turn.
+__global__ void __launch_bounds__(kReadThreads) read8_kernel(const __grid_constant__ ReadArgs a) {
+  __shared__ long long before[DSPARK_MAX_BS + 1];  // blocks of the requests before
+  __shared__ long long warp_total[DSPARK_MAX_BS / 32];
+  __shared__ int bad;
+  pdl_enter();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bsh = a.block_shift;
+  if (tid == 0) bad = 0;
+  __syncthreads();
+  int mine = 0;
+  if (tid < a.bs) {
+    const int row = a.cu[tid], n = a.cu[tid + 1] - row, c = a.ctx[tid];
+    if (row < 0 || n < 0 || row + n > a.rows) {
+      bad = 1;
+    } else if (n > 0) {
+      if (c < 0 || int64_t(c) + n > a.cache_limit) {
+        if (blockIdx.x == 0) set_status(a.status, DSPARK_EINVAL);
+      } else {
+        const int lo = a.window ? max(0, c - a.window + 1) : 0;
+        const int sinks = a.window ? min(a.n_sink, lo) : 0;
+        mine = ((c + n - 1) >> bsh) - (lo >> bsh) + 1;
+        // sink blocks that the window's do not reach
+        mine += min((sinks + (1 << bsh) - 1) >> bsh, lo >> bsh);
+      }
+    }
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_total[warp] = incl;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) incl += warp_total[i];
+  if (tid == 0) before[0] = 0;
+  before[tid + 1] = incl;
+  __syncthreads();
+  if (bad) {
+    if (tid == 0 && blockIdx.x == 0) set_status(a.status, DSPARK_EINVAL);
+    return;
+  }
+  const int64_t units = before[a.bs] * a.Hkv;
+  const int per_slot = a.D / 16, pieces = per_slot << bsh;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const long long block = u / a.Hkv;
+    const int h = int(u - block * a.Hkv);
+    int r = 0;
+    for (int step = DSPARK_MAX_BS / 2; step > 0; step >>= 1)
+      if (r + step < a.bs && before[r + step] <= block) r += step;
+    const int c = a.ctx[r], end = c + a.cu[r + 1] - a.cu[r];
+    const int lo = a.window ? max(0, c - a.window + 1) : 0, sinks = a.window ? min(a.n_sink, lo) : 0;
+    const int sb = min((sinks + (1 << bsh) - 1) >> bsh, lo >> bsh), v = int(block - before[r]);
+    const int pos0 = (v < sb ? v : v - sb + (lo >> bsh)) << bsh;
+    const int64_t at = int64_t(r) * a.max_pages + (pos0 >> a.page_shift);
+    const int page = a.page_table[at], to = a.out_table[at];
+    if (page < 0 || page >= a.n_pages || to < 0 || to >= a.n_out_pages) {
+      if (tid == 0) set_status(a.status, DSPARK_EINVAL);
+      continue;
+    }
+    const int slot0 = pos0 & ((1 << a.page_shift) - 1);
+    const int64_t src = ((int64_t(page) * a.Hkv + h) << a.page_shift) + slot0;
+    const int64_t dst = ((int64_t(to) * a.Hkv + h) << a.page_shift) + slot0;
+    for (int i = tid; i < pieces; i += kReadThreads) {
+      const int s = i / per_slot, pos = pos0 + s;
+      if (pos >= end || (pos < lo && pos >= sinks)) continue;
+      const uint16_t sc = reinterpret_cast<const uint16_t*>(a.kv_scale)[src + s];
+      const uint4 k = reinterpret_cast<const uint4*>(a.k_cache)[src * per_slot + i];
+      const uint4 x = reinterpret_cast<const uint4*>(a.v_cache)[src * per_slot + i];
+      uint4* ko = reinterpret_cast<uint4*>(a.k_out) + (dst * per_slot + i) * 2;
+      uint4* vo = reinterpret_cast<uint4*>(a.v_out) + (dst * per_slot + i) * 2;
+      widen16(k, kv8::factor(sc & 0xFFu), ko);
+      widen16(x, kv8::factor(sc >> 8), vo);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append_kv8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const int32_t* cu, const int32_t* ctx, int bs, int rows,
+                              const float* cos_sin, int max_pos, int rot, int interleaved, const int32_t* page_table,
+                              int max_pages, int n_pages, int page_shift, int Hq, int Hkv, int D, void* q_out,
+                              void* k_cache, void* v_cache, uint8_t* kv_scale, uint32_t* status, cudaStream_t s) {
+  AppendArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q), a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.cu = cu, a.ctx = ctx, a.cos_sin = cos_sin, a.page_table = page_table;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out), a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache), a.kv_scale = kv_scale;
+  a.status = status;
+  a.bs = bs, a.rows = rows, a.max_pos = max_pos, a.rot = rot, a.max_pages = max_pages, a.n_pages = n_pages;
+  a.page_shift = page_shift, a.Hq = q ? Hq : 0, a.Hkv = Hkv, a.D = D;
+  const int items = (a.Hq + 2 * Hkv) * (D / 16);
+  const dim3 block(std::min((items + 31) / 32 * 32, kMaxAppendThreads));
+  return launch_pdl(interleaved ? append8_kernel<true> : append8_kernel<false>, dim3(rows), block, 0, s, a);
+}
+
+cudaError_t launch_read_kv8(const void* k_cache, const void* v_cache, const uint8_t* kv_scale, const int32_t* page_table,
+                            int max_pages, int n_pages, int page_shift, const int32_t* cu, const int32_t* ctx, int bs,
+                            int rows, int Hkv, int D, int window, int n_sink, const int32_t* out_table, int n_out_pages,
+                            void* k_out, void* v_out, uint32_t* status, cudaStream_t s) {
+  ReadArgs a;
+  a.k_cache = static_cast<const uint8_t*>(k_cache), a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.kv_scale = kv_scale, a.page_table = page_table, a.cu = cu, a.ctx = ctx, a.out_table = out_table;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out), a.v_out = static_cast<__nv_bfloat16*>(v_out), a.status = status;
+  a.cache_limit = std::min(int64_t(max_pages) << page_shift, int64_t(1) << 30);  // positions: well inside 32 bits
+  a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, 5);
+  a.bs = bs, a.rows = rows, a.Hkv = Hkv, a.D = D, a.window = window >= a.cache_limit ? 0 : window, a.n_sink = n_sink;
+  a.n_out_pages = n_out_pages;
+  return launch_pdl(read8_kernel, dim3(tch::sm_count() * 8), dim3(kReadThreads), 0, s, a);
+}
+
+}  // namespace dspark
