@@ -545,7 +545,7 @@ DSPARK_API int dspark_history_commit(const int32_t* out_tokens, int bs, int gamm
  *     K = code * 2^(kv_scale[.., 0] - 127),   V = code * 2^(kv_scale[.., 1] - 127);   byte 255: the vector is NaN
  * i.e. the power of two under which the vector's largest magnitude is at most 448 (all codes that an append writes are
  * numbers, the largest of a vector above 224 unless the vector is tiny or 0).  A value x is off by at most 2^-4 |x| where its
- * code is normal, by 2^-10 of the power of two below.  Page table, lengths and limits are those of the bf16 cache, and
+ * code is normal, by 2^-10 of the power of two below.  All three tensors begin at a multiple of 16 bytes.  Page table, lengths and limits are those of the bf16 cache, and
  * dtype is the queries', keys' and values' (bf16).
  *
  * append_kv8: dspark_append_kv with that cache.  The rotated K is rounded once, from fp32.  A vector with a NaN or an

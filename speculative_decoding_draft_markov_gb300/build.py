@@ -22,7 +22,7 @@ LIB = os.path.join(LIBDIR, "libdspark.so")
 CALLS = os.path.join(LIBDIR, "_calls.so")
 SOURCES = ["api.cu", "draft.cu", "draft_tc.cu", "decide_tc.cu", "sched_pack.cu", "verify.cu", "draft_noalloc.cu", "rnn.cu",
            "observe.cu", "serve_api.cu", "kv_append.cu", "window_attention.cu", "attention_windows.cu", "attention_prompts.cu",
-           "logit_rules.cu", "kv8_cache.cu", "kv8_attention.cu", "token_logprobs.cu"]
+           "logit_rules.cu", "kv8_cache.cu", "attention_windows8.cu", "token_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

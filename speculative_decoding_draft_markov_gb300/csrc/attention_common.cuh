@@ -385,6 +385,30 @@ __device__ __forceinline__ void clear_unseen(const AttnArgs& a, const Segment& s
   tc::fence_proxy_async_smem();
   __syncwarp();
 }
+// Folds N values of each lane over the 32 lanes (kMax: maxima, else sums, in a fixed order), halving the values with the
+// lanes; N = 8, 16 or 32.  Afterwards lane l holds the result of value l / (32 / N) in v[0].
+template <int N, bool kMax>
+__device__ __forceinline__ float fold_lanes(float* v, int lane) {
+  static_assert(N == 8 || N == 16 || N == 32, "values");
+  int cnt = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (cnt > 1) {
+      cnt >>= 1;
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        if (i < cnt) {
+          const float got = __shfl_xor_sync(~0u, up ? v[i] : v[i + cnt], o), keep = up ? v[i + cnt] : v[i];
+          v[i] = kMax ? fmaxf(keep, got) : keep + got;
+        }
+    } else {
+      const float got = __shfl_xor_sync(~0u, v[0], o);
+      v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+    }
+  }
+  return v[0];
+}
 }  // namespace attn
 
 // The most (token, head) rows of a unit of the short windows' kernel, and its ranges per CTA (partial rows in the workspace are
@@ -395,5 +419,20 @@ cudaError_t launch_attention_prompts(int D, const CUtensorMap& q, const CUtensor
                                      const attn::AttnArgs& a, int n_cta, cudaStream_t s);
 cudaError_t launch_attention_windows(int D, int unit_rows, const CUtensorMap& q, const CUtensorMap& k,
                                      const CUtensorMap& v, const attn::AttnArgs& a, int n_cta, cudaStream_t s);
+
+// The same over an 8-bit cache: its exponent bytes, and the queries, which are read with plain loads.
+namespace attn {
+struct Attn8Args {
+  AttnArgs a;
+  const uint8_t* kv_scale;
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  int negate;
+};
+}  // namespace attn
+constexpr int kWindow8Rows = 128;  // the most (token, head) rows of a unit
+int attention_window8_sets(int D, int unit_rows);
+cudaError_t launch_attention_windows8(int D, int unit_rows, const CUtensorMap& k, const CUtensorMap& v,
+                                      const attn::Attn8Args& a, int n_cta, cudaStream_t s);
 
 }  // namespace dspark

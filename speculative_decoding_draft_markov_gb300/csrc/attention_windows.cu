@@ -80,31 +80,6 @@ struct Cfg {
   static_assert(kSlots >= 3 && kUsedCols <= 512 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "layout");
 };
 
-// Folds N values of each lane over the 32 lanes (kMax: maxima, else sums, in a fixed order), halving the values with the
-// lanes; N = 8, 16 or 32.  Afterwards lane l holds the result of value l / (32 / N) in v[0].
-template <int N, bool kMax>
-__device__ __forceinline__ float fold_lanes(float* v, int lane) {
-  static_assert(N == 8 || N == 16 || N == 32, "values");
-  int cnt = N;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    if (cnt > 1) {
-      cnt >>= 1;
-      const bool up = lane & o;
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i)
-        if (i < cnt) {
-          const float got = __shfl_xor_sync(~0u, up ? v[i] : v[i + cnt], o), keep = up ? v[i + cnt] : v[i];
-          v[i] = kMax ? fmaxf(keep, got) : keep + got;
-        }
-    } else {
-      const float got = __shfl_xor_sync(~0u, v[0], o);
-      v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
-    }
-  }
-  return v[0];
-}
-
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 1)
     window_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,

@@ -1,0 +1,687 @@
+// The attention of short windows over the 8-bit cache: attention_windows.cu's pipelines with half the bytes to read.
+//
+//     S^T = K8 (Qh + Ql)^T      [128 slots x R]   (tcgen05 kind::f8f6f4, fp32 in TMEM)
+//     x = S^T 2^(ek + eq) c,  P^T = 2^(x - m) 2^(ev - f)   (fp16, shared memory), partial sums of 2^(x - m) in registers
+//     O^T += V^T P^T            [D x R]           (tcgen05 kind::f16, V as fp16; fp32 in TMEM), out = O^T 2^f / l
+//
+// K goes into its product as it lies in the cache.  The other operand is Q as a sum of two e4m3 parts under a power of two of
+// its row, 2^eq: the first takes the upper four of bf16's eight bits, the second what is left, which is exact for lanes down
+// to 2^-10 of the row's largest; smaller ones are off by at most 2^-19 of that.  (One part alone would be off by 2^-4.)  The
+// slots' powers of two, ek, are one factor per thread, the rows', eq, one per score.
+// V is the operand whose contraction runs over slots, so its factors 2^ev have to go into P.  P has to have more bits and more
+// range than e4m3 has; fp16 has eleven bits from 2^-14 on.  So four warps turn V's tiles into fp16 (exact: one conversion for two
+// values), clearing the slots that nobody sees on the way.  P is kept inside fp16's range by two references, a row's m, which
+// lies 2^6 below its maximum of a unit's first tile, and f, the largest ev of the tile's slots; both are checked on each tile
+// against 2^15, and set anew where they are outgrown, O^T and the sums with them.  A weight keeps its eleven bits down to 2^-20 of
+// the largest, and its place down to 2^-31.
+#include "attention_common.cuh"
+#include "kv8.cuh"
+
+namespace dspark {
+namespace {
+
+using namespace attn;
+
+// Sixteen softmax warps in groups of four; a group takes a share of the rows of its pipeline's tiles.  Then a
+// TMA warp for each pipeline, an MMA warp for each, and four warps that convert (all four for a lone pipeline).
+constexpr int kGroups = 4, kThreads = (kGroups + 2) * 128;
+constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 2, kConvWarp = kMmaWarp + 2;
+// Registers: launched with 768 x 80; the softmax warps take what the others give back (512 x 96 + 256 x 48 <= 768 x 80).
+constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
+constexpr int kMaxSlots = 8;
+constexpr int kQRing = 4;  // units whose rows' factors are kept
+// m lies kTop below a maximum; a score or a value's power may outgrow the references up to kMost (fp16 holds 2^16 - 2^5)
+constexpr float kTop = 6.f, kMost = 15.f;
+
+constexpr int sets_of(int D, int R) { return R * D >= 64 * 128 ? 1 : 2; }
+
+template <int D, int R>
+struct Shared {
+  static constexpr int kSets = sets_of(D, R), kRowGroups = kGroups / kSets, kRows = R / kRowGroups;
+  // tiles whose exponent bytes are kept: a slot of the ring ahead of the products, which are two tiles ahead of the softmax
+  static constexpr int kScales = 16;
+  static_assert(kScales >= kMaxSlots + 3, "a tile's bytes are written anew when its softmax is over");
+  uint64_t q_ready[kSets][kQRing], q_empty[kSets][2], full[kSets][kMaxSlots], empty[kSets][kMaxSlots];
+  uint64_t sc_full[kSets][kScales], v_full[kSets], v_empty[kSets];
+  uint64_t s_full[kSets][2], p_full[kSets], p_empty[kSets], o_full[kSets], o_read[kSets];
+  uint64_t group[kGroups], drain[kSets];
+  uint32_t tmem_base;
+  volatile int abort;
+  int pending[kSets];          // the MMA warp has issued something
+  int n_put[kSets], n_k[kSets];  // copies issued: tiles, exponent bytes
+  int need[kGroups][2];        // [parity]: the last tile at which a warp asked for new references
+  Start start[kSets];
+  int warp_byte[kGroups][4];   // by warp: the largest exponent byte of V in a tile
+  float warp_max[kGroups][4][kRows], warp_sum[kGroups][4][kRows];  // by warp: the rows' maxima of a tile, sums of a unit
+  alignas(16) float ref[kSets][R];             // the rows' references, read four at a time
+  alignas(16) float row_factor[kSets][kQRing][R];  // 2^eq c
+  alignas(16) uint16_t scales[kSets][kScales][kTile];
+};
+
+template <int D, int R>
+struct Cfg {
+  static constexpr int kSets = sets_of(D, R), kRowGroups = kGroups / kSets;
+  static constexpr int kConvWarps = 4 / kSets;               // of a pipeline
+  static constexpr int kSlotBytes = kTile * D;               // a tile of codes
+  static constexpr int kVBytes = kTile * D * 2;              // a tile of V in fp16: 128-byte swizzled blocks of 64 columns
+  static constexpr int kQPart = R * D, kQBytes = 2 * kQPart;
+  static constexpr int kQBufs = R * D <= 64 * 128 ? 2 : 1;   // where they fit
+  static constexpr int kPPitch = R < 64 ? R * 2 : 128;       // bytes of a slot's row of P, R > 64: in two chunks
+  static constexpr int kPBytes = kTile * R * 2;
+  // O^T has M = 128 also where D = 64: its lanes 64 .. 127 come from the 16 KB behind the V tile, whatever
+  // they hold, and are not read
+  static constexpr int kBehind = kSets * (kQBytes * kQBufs + kPBytes);
+  static constexpr int kPad = D == 64 && kBehind < 16384 ? 16384 - kBehind : 0;
+  static constexpr int kRoom = (232448 - int(sizeof(Shared<D, R>)) - kBehind - kPad - kSets * kVBytes) / kSlotBytes / kSets;
+  static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;  // ring of a pipeline
+  static constexpr int kSmem = kSets * (kSlots * kSlotBytes + kVBytes) + kBehind + kPad + int(sizeof(Shared<D, R>));
+  static constexpr int kUsedCols = kSets * 3 * R;            // per pipeline: S^T twice, O^T
+  static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
+  static_assert(kSlots >= 3 && kUsedCols <= 512 && kQPart % 1024 == 0 && kPBytes % 1024 == 0, "layout");
+};
+
+// Issue a tile's loads: the codes, and for K (`scales` given) the exponent bytes of K and V with them.
+template <int D>
+__device__ __forceinline__ void issue_codes(const AttnArgs& a, const CUtensorMap* map, const TileLoad& t, uint32_t dst,
+                                            uint32_t bar, uint64_t policy, int lane) {
+  const int block_bytes = D << a.block_shift;
+  if (lane == 0) tc::mbar_arrive_expect_tx(bar, uint32_t(t.n_blocks * block_bytes));
+  __syncwarp();
+  if (lane >= t.n_blocks) return;
+  int page = t.page;
+  if (page < 0 || page >= a.n_pages) {
+    set_status(a.status, DSPARK_EINVAL);
+    page = a.n_pages;  // outside the tensor: reads as zeros
+  }
+  tc::tma_load_4d(dst + lane * block_bytes, map, bar, 0, t.slot, t.head, page, policy);
+}
+__device__ __forceinline__ void issue_scales(const Attn8Args& p, const TileLoad& t, uint16_t* dst, uint32_t bar, int lane) {
+  const AttnArgs& a = p.a;
+  const bool mine = lane < t.n_blocks, good = mine && t.page >= 0 && t.page < a.n_pages;
+  const uint32_t n_good = __popc(__ballot_sync(~0u, good)), bytes = 2u << a.block_shift;
+  uint16_t* to = dst + (lane << a.block_shift);
+  if (mine && !good)  // zeros of any power of two
+    for (int i = 0; i < 1 << a.block_shift; ++i) to[i] = 0x7F7F;
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive_expect_tx(bar, n_good * bytes);
+  __syncwarp();
+  if (good) {
+    const int64_t slot = ((int64_t(t.page) * a.Hkv + t.head) << a.page_shift) + t.slot;
+    tc::bulk_load(tc::smem_u32(to), p.kv_scale + 2 * slot, bytes, bar);
+  }
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    window8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ Attn8Args args) {
+  using C = Cfg<D, R>;
+  using Sh = Shared<D, R>;
+  constexpr int kSets = C::kSets, kRowGroups = C::kRowGroups, RW = R / kRowGroups;  // RW: rows per thread
+  const AttnArgs& a = args.a;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sRing = smem;
+  uint8_t* sV = sRing + kSets * C::kSlots * C::kSlotBytes;
+  uint8_t* sQ = sV + kSets * C::kVBytes;
+  uint8_t* sP = sQ + kSets * C::kQBufs * C::kQBytes;
+  Sh* sh = reinterpret_cast<Sh*>(sP + kSets * C::kPBytes + C::kPad);
+  PlanScratch& plan = *reinterpret_cast<PlanScratch*>(sRing);  // before the first load
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same for the warp, and known to be
+
+  if (warp == 0) {  // barriers: lane i those of number i
+    for (int z = 0; z < kSets; ++z) {
+      if (lane < kQRing) tc::mbar_init(tc::smem_u32(&sh->q_ready[z][lane]), C::kConvWarps);
+      if (lane < 2) {
+        tc::mbar_init(tc::smem_u32(&sh->q_empty[z][lane]), 1);
+        tc::mbar_init(tc::smem_u32(&sh->s_full[z][lane]), 1);
+      }
+      if (lane < C::kSlots) {
+        tc::mbar_init(tc::smem_u32(&sh->full[z][lane]), 1);
+        tc::mbar_init(tc::smem_u32(&sh->empty[z][lane]), C::kConvWarps);  // a K tile's product arrives as often
+      }
+      if (lane < Sh::kScales) tc::mbar_init(tc::smem_u32(&sh->sc_full[z][lane]), 1);
+    }
+    if (lane < kSets) {
+      tc::mbar_init(tc::smem_u32(&sh->v_full[lane]), C::kConvWarps);
+      tc::mbar_init(tc::smem_u32(&sh->v_empty[lane]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->p_full[lane]), 4 * kRowGroups);
+      tc::mbar_init(tc::smem_u32(&sh->p_empty[lane]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->o_full[lane]), 1);
+      tc::mbar_init(tc::smem_u32(&sh->o_read[lane]), 4 * kRowGroups);
+      tc::mbar_init(tc::smem_u32(&sh->drain[lane]), 1);
+      sh->pending[lane] = 0;
+      sh->start[lane].count = 0;
+    }
+    if (lane < kGroups) {
+      tc::mbar_init(tc::smem_u32(&sh->group[lane]), 4);
+      sh->need[lane][0] = sh->need[lane][1] = 0;
+    }
+    if (lane == 0) sh->abort = 0, plan.bad = 0, plan.n_long = 0;
+    tc::fence_mbar_init();
+  }
+  if (tid == 32) {
+    tc::prefetch_tensormap(&map_k);
+    tc::prefetch_tensormap(&map_v);
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tc::smem_u32(&sh->tmem_base), C::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  __syncthreads();
+  pdl_enter();
+  const Cut cut = plan_ranges<kSets>(a, sh->start, plan, a.tokens);
+  tc::fence_proxy_async_smem();  // the plan's scratch lies where TMA writes
+  __syncthreads();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (warp >= kTmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp >= kTmaWarp && warp < kTmaWarp + kSets) {
+    // --------------------------------------------------------------------- TMA producer
+    // In the order of load_in_order over all tiles of the range.
+    const int set = warp - kTmaWarp;
+    const uint32_t range = blockIdx.x + set * gridDim.x;
+    const TmaWaiter wait{{&sh->abort, a.timeout_ns}};
+    const uint64_t stream = tc::policy_evict_first();
+    uint8_t* ring_mem = sRing + set * C::kSlots * C::kSlotBytes;
+    Ring<C::kSlots> ring;
+    int n_put = 0, n_k = 0;
+    int4 info = make_int4(0, 0, 0, 0);
+    Cursor cur(sh->start[set], a.tokens);
+    struct Ahead {
+      TileLoad t;
+      bool there;
+    };
+    auto fetch = [&]() {  // the next tile's pages
+      Ahead f = {};
+      f.there = cur.next(a);
+      if (!f.there) return f;
+      const Segment& s = cur.s;
+      f.t = tile_load(a, s, cur.j, lane);
+      if (cur.first() && s.tile0 == 0 && s.n < s.u.ntiles)
+        info = make_int4(1 + cut.ranges(range + 1, uint32_t(s.u.ntiles - s.n)), s.row0, s.ntok, s.h);
+      return f;
+    };
+    auto put = [&](const CUtensorMap* map, const Ahead& f) {
+      if (!wait(&sh->empty[set][ring.slot], ring.phase ^ 1)) return false;
+      issue_codes<D>(a, map, f.t, tc::smem_u32(ring_mem + ring.slot * C::kSlotBytes),
+                     tc::smem_u32(&sh->full[set][ring.slot]), stream, lane);
+      ++n_put;
+      ring.step();
+      return true;
+    };
+    auto put_k = [&](const Ahead& f) {
+      if (!put(&map_k, f)) return false;
+      const int b = n_k++ % Sh::kScales;
+      issue_scales(args, f.t, sh->scales[set][b], tc::smem_u32(&sh->sc_full[set][b]), lane);
+      return true;
+    };
+    const bool ok = load_in_order(fetch, put_k, [&](const Ahead& f) { return put(&map_v, f); });
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 1u, uint32_t(n_put));
+    }
+    if (lane == 0) {
+      if (!ok) info.x = 0;
+      a.info[range] = info;
+      sh->n_put[set] = n_put, sh->n_k[set] = n_k;
+    }
+  } else if (warp >= kMmaWarp && warp < kMmaWarp + kSets) {
+    // ------------------------------------------------------------ the two products of each tile
+    constexpr uint32_t idesc_s = tc::idesc_e4m3_f32(kTile, R);
+    constexpr uint32_t idesc_o = tc::idesc_f16_f32(128, R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
+    const int set = warp - kMmaWarp;
+    const Waiter wait{&sh->abort, a.timeout_ns};
+    const uint32_t t_s = tmem + set * 3 * R, t_o = t_s + 2 * R;
+    const uint64_t dk = tc::sdesc_kmajor<D>(tc::smem_u32(sRing + set * C::kSlots * C::kSlotBytes));
+    const uint64_t dq = tc::sdesc_kmajor<D>(tc::smem_u32(sQ + set * C::kQBufs * C::kQBytes));
+    const uint64_t dv = tc::sdesc_mnmajor<128>(tc::smem_u32(sV + set * C::kVBytes), kTile * 128);
+    const uint64_t dp = tc::sdesc_mnmajor<C::kPPitch>(tc::smem_u32(sP + set * C::kPBytes), kTile * 128);
+    Ring<C::kSlots> ring;
+    int n_seg = 0, n_s = 0, t = 0, units = 0;
+    Cursor kc(sh->start[set], a.tokens), vc(sh->start[set], a.tokens);
+    auto s_product = [&]() {  // S^T of the tile at kc; the S before last has been read (its P is there)
+      const int b = n_seg % C::kQBufs;
+      if (kc.first() && !wait(&sh->q_ready[set][n_seg % kQRing], (n_seg / kQRing) & 1)) return false;
+      if (!wait(&sh->full[set][ring.slot], ring.phase)) return false;
+      tc::tc_fence_after();
+      const uint64_t dk_t = dk + uint32_t(ring.slot * (C::kSlotBytes >> 4)), dq_t = dq + uint32_t(b * (C::kQBytes >> 4));
+      const bool last = kc.last();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            tc::mma_f8(t_s + (n_s & 1) * R, dk_t + ((i * 32) >> 4), dq_t + ((part * C::kQPart + i * 32) >> 4), idesc_s,
+                       part != 0 || i != 0);
+        tc::mma_commit(tc::smem_u32(&sh->s_full[set][n_s & 1]));
+#pragma unroll
+        for (int i = 0; i < C::kConvWarps; ++i) tc::mma_commit(tc::smem_u32(&sh->empty[set][ring.slot]));
+        if (last) tc::mma_commit(tc::smem_u32(&sh->q_empty[set][b]));
+      }
+      __syncwarp();
+      ring.step();
+      ++n_s;
+      if (last) ++n_seg;
+      return true;
+    };
+    bool more = kc.next(a);
+    bool ok = !more || s_product();
+    if (ok && more) {
+      more = kc.next(a);
+      ok = !more || s_product();
+    }
+    for (; ok && vc.next(a); ++t) {
+      const bool first = vc.first(), last = vc.last();
+      ok = wait(&sh->v_full[set], t & 1) && wait(&sh->p_full[set], t & 1);
+      if (ok && first) ok = wait(&sh->o_read[set], (units++ & 1) ^ 1);  // the unit before has been read
+      if (!ok) break;
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          tc::mma_bf16(t_o, dv + ((i * 2048) >> 4), dp + ((i * 16 * C::kPPitch) >> 4), idesc_o, !first || i != 0);
+        tc::mma_commit(tc::smem_u32(&sh->p_empty[set]));
+        tc::mma_commit(tc::smem_u32(&sh->v_empty[set]));
+        if (last) tc::mma_commit(tc::smem_u32(&sh->o_full[set]));
+      }
+      __syncwarp();
+      ring.step();  // the V tile's slot
+      if (more) {
+        more = kc.next(a);
+        ok = !more || s_product();
+      }
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 2u, uint32_t(t));
+    }
+    if (lane == 0) sh->pending[set] = n_s > 0;
+  } else if (warp >= kConvWarp) {
+    // ---------------------------------------------- Q into two parts of e4m3, V tiles into fp16
+    const int set = (warp - kConvWarp) / C::kConvWarps, w = (warp - kConvWarp) % C::kConvWarps;
+    const Waiter wait{&sh->abort, a.timeout_ns};
+    const uint8_t* ring_mem = sRing + set * C::kSlots * C::kSlotBytes;
+    uint8_t* v_mem = sV + set * C::kVBytes;
+    Ring<C::kSlots> ring;
+    bool ok = true;
+    int n_seg = 0, q_tile = 0, t = 0;  // units whose Q is done; the range's tile at which the next one begins
+    Walk qw(sh->start[set], a.tokens);
+    Cursor vc(sh->start[set], a.tokens);
+    Segment sq = {};
+    bool q_more = qw.next(a, sq);
+    auto convert_q = [&]() {
+      const int b = n_seg % C::kQBufs;
+      if (!wait(&sh->q_empty[set][b], ((n_seg / C::kQBufs) & 1) ^ 1)) return false;
+      constexpr int kLanes = D / 16, kPass = 32 / kLanes * C::kConvWarps;  // threads to a row, rows at a time
+      uint8_t* q_mem = sQ + (set * C::kQBufs + b) * C::kQBytes;
+      const int piece = lane % kLanes;
+#pragma unroll 1
+      for (int row = w * (32 / kLanes) + lane / kLanes; row < R; row += kPass) {
+        const int tok = row / a.g, hh = row - tok * a.g;
+        uint4 x[2] = {};
+        if (tok < sq.ntok) {
+          const uint4* src = reinterpret_cast<const uint4*>(args.q + int64_t(sq.row0 + tok) * args.q_stride +
+                                                            int64_t(sq.h * a.g + hh) * D) + 2 * piece;
+          x[0] = src[0], x[1] = src[1];
+        }
+        const uint32_t word[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+        uint32_t top = 0;  // the row's largest magnitude, as bits of fp32
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, max(word[i] & 0x7FFF0000u, (word[i] << 16) & 0x7FFF0000u));
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+        const uint32_t byte = kv8::exponent_byte(top);
+        const float by = byte == kv8::kNan ? 0.f : kv8::power(127 - int(byte)) * (args.negate ? -1.f : 1.f);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h[2], l[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t y = word[2 * i + k];
+            const float y0 = bf16lo(y) * by, y1 = bf16hi(y) * by;
+            h[k] = kv8::code2(y0, y1);
+            const float2 got = kv8::values(h[k]);
+            l[k] = kv8::code2(y0 - got.x, y1 - got.y);
+          }
+          hi[i] = h[0] | h[1] << 16, lo[i] = l[0] | l[1] << 16;
+        }
+        uint8_t* dst = q_mem + tc::swizzled<D>(row, piece);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + C::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (piece == 0) sh->row_factor[set][n_seg % kQRing][row] = kv8::factor(byte) * a.c2;
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->q_ready[set][n_seg % kQRing]));
+      ++n_seg;
+      return true;
+    };
+    // The ring's slots in the order of the loads: K 0, K 1, then V t, K t + 2 (as far as there are such tiles)
+    uint32_t left = sh->start[set].count;
+    left = left < 2 ? left : 2;
+    for (uint32_t i = 0; i < left; ++i) ring.step();
+    const uint32_t n_tiles = sh->start[set].count;
+    for (; ok && vc.next(a); ++t) {
+      while (ok && q_more && q_tile <= t + 2) {
+        ok = convert_q();
+        q_tile += sq.n;
+        q_more = qw.next(a, sq);
+      }
+      ok = ok && wait(&sh->full[set][ring.slot], ring.phase) && wait(&sh->v_empty[set], (t & 1) ^ 1);
+      if (!ok) break;
+      const uint8_t* src = ring_mem + ring.slot * C::kSlotBytes;
+      const Segment& s = vc.s;
+      int j0, j1;  // the tiles of which every slot is seen by some row
+      whole_tiles(a, s, s.u.p1, s.u.p0, j0, j1);
+      const int first = (s.tile0 + vc.j) * (kTile >> a.block_shift);
+#pragma unroll 1
+      for (int slot = w * 32 + lane; slot < kTile; slot += C::kConvWarps * 32) {
+        bool seen = vc.j >= j0 && vc.j < j1;
+        if (!seen) {
+          const int pos = block_pos(a, s.u, first + (slot >> a.block_shift)) + (slot & ((1 << a.block_shift) - 1));
+          seen = pos <= s.u.p1 && (pos >= s.u.lo || pos < a.n_sink);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint4 c = *reinterpret_cast<const uint4*>(src + tc::swizzled<D>(slot, i));
+          if (!seen) c = make_uint4(0u, 0u, 0u, 0u);  // it holds whatever was there, NaN included, and 0 * NaN is NaN
+          uint8_t* dst = v_mem + (i / 4) * (kTile * 128);
+          *reinterpret_cast<uint4*>(dst + tc::swizzled<128>(slot, (2 * i) % 8)) =
+              make_uint4(kv8::halves(c.x & 0xFFFFu), kv8::halves(c.x >> 16), kv8::halves(c.y & 0xFFFFu), kv8::halves(c.y >> 16));
+          *reinterpret_cast<uint4*>(dst + tc::swizzled<128>(slot, (2 * i) % 8 + 1)) =
+              make_uint4(kv8::halves(c.z & 0xFFFFu), kv8::halves(c.z >> 16), kv8::halves(c.w & 0xFFFFu), kv8::halves(c.w >> 16));
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(tc::smem_u32(&sh->v_full[set]));
+        tc::mbar_arrive(tc::smem_u32(&sh->empty[set][ring.slot]));
+      }
+      ring.step();
+      if (uint32_t(t) + 2 < n_tiles) ring.step();  // K t + 2
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 4u, uint32_t(t));
+    }
+  } else if (warp < kTmaWarp) {
+    // ------------------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const Waiter wait{&sh->abort, a.timeout_ns};
+    const int grp = warp >> 2, w4 = warp & 3;
+    const int kv = w4 * 32 + lane;  // this thread's slot of each tile = TMEM lane
+    const int set = grp % kSets, row0 = grp / kSets * RW;  // and its rows
+    const uint32_t t_s = tmem + (uint32_t(w4 * 32) << 16) + set * 3 * R + row0, t_o = t_s + 2 * R;
+    float* ref = sh->ref[set] + row0;
+    // where this thread's row of P goes: 16-byte pieces, from the first row of the group on
+    uint8_t* p_row = sP + set * C::kPBytes + (R == 128 ? (row0 / 64) * (kTile * 128) : 0);
+    const int piece0 = (R == 128 ? row0 % 64 : row0) / 8;
+    // the row that this lane holds after a fold (the lanes of a row hold the same)
+    const int fold_row = lane / (32 / RW);
+    int t = 0, sync = 0, units = 0;
+    bool ok = true;
+    Walk walk(sh->start[set], a.tokens);
+    Segment s = {};
+    // the group's four warps: everything before on all of them is visible after
+    auto arrive = [&]() {
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->group[grp]));
+    };
+    auto meet = [&]() {
+      arrive();
+      return wait(&sh->group[grp], sync++ & 1);
+    };
+    while (ok && walk.next(a, s)) {
+      const int per_tile = kTile >> a.block_shift;
+      int j_in0, j_in1;  // the tiles that every row sees whole
+      whole_tiles(a, s, s.u.p0, s.u.p1, j_in0, j_in1);
+      const float* factor = sh->row_factor[set][units % kQRing] + row0;
+      ok = wait(&sh->q_ready[set][units % kQRing], (units / kQRing) & 1);
+      if (!ok) break;
+      int f = 0;  // the reference of V's powers of two, as an exponent byte
+      float l[RW];  // this slot's share of the rows' sums
+#pragma unroll
+      for (int i = 0; i < RW; ++i) l[i] = 0.f;
+      for (int j = 0; j < s.n; ++j, ++t) {
+        const bool inside = j >= j_in0 && j < j_in1;
+        int from = 0, to = R;  // the rows that see this thread's slot
+        if (!inside) {
+          // the token at p0 + tok sees the slot from tok = pos - p0 on, for `window` tokens, a sink always.  Rows behind the
+          // unit's see nothing here: a slot for them alone holds whatever was there, and may not set V's reference
+          const int v = (s.tile0 + j) * per_tile + (kv >> a.block_shift);
+          const int pos = block_pos(a, s.u, v) + (kv & ((1 << a.block_shift) - 1));
+          const int d = pos - s.u.p0;
+          from = d <= 0 ? 0 : d >= a.tokens ? R : d * a.g;
+          to = s.ntok * a.g;
+          if (a.window && pos >= a.n_sink) to = d + a.window <= 0 ? 0 : d + a.window >= s.ntok ? to : (d + a.window) * a.g;
+        }
+        ok = wait(&sh->sc_full[set][t % Sh::kScales], (t / Sh::kScales) & 1);
+        if (!ok) break;
+        const uint32_t bytes = sh->scales[set][t % Sh::kScales][kv];
+        const float kf = kv8::factor(bytes & 0xFFu);
+        const unsigned long long kk = pack_f32x2(kf, kf);
+        // V's: a slot that no row sees counts for nothing, a NaN has no power
+        const int v_byte = from >= to || bytes >> 8 == kv8::kNan ? 0 : max(1, int(bytes >> 8));
+        ok = wait(&sh->s_full[set][t & 1], (t >> 1) & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        float y[RW];  // the only array beside l: what is needed once more is loaded once more (S is there until P is)
+        auto load_scores = [&]() {
+          tc::tmem_ld<RW>(t_s + (t & 1) * R, y);
+          tc::tmem_ld_wait();
+        };
+        auto hide = [&](float with) {
+          if (!inside) {
+#pragma unroll
+            for (int i = 0; i < RW; ++i)
+              if (row0 + i < from || row0 + i >= to) y[i] = with;
+          }
+        };
+        auto refer = [&]() {  // scores to exponents; the largest
+#pragma unroll
+          for (int i = 0; i < RW; i += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(ref + i), c = *reinterpret_cast<const float4*>(factor + i);
+            unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(y[i], y[i + 1]), kk), pack_f32x2(c.x, c.y), pack_f32x2(-m.x, -m.y)), y[i], y[i + 1]);
+            unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(y[i + 2], y[i + 3]), kk), pack_f32x2(c.z, c.w), pack_f32x2(-m.z, -m.w)), y[i + 2], y[i + 3]);
+          }
+          hide(-INFINITY);
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < RW; i += 4) top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
+          return top;
+        };
+        auto weigh = [&]() {
+#pragma unroll
+          for (int i = 0; i < RW; ++i) y[i] = tc::ex2_approx(y[i]);
+        };
+        load_scores();
+        bool fresh = j == 0;  // new references are needed
+        if (j > 0) {
+          const float top = refer() + float(max(0, v_byte - f));
+          const int at = sync & 1;
+          if (__any_sync(~0u, top > kMost) && lane == 0) sh->need[grp][at] = t + 1;
+          arrive();
+          weigh();  // while the others arrive; done again where a reference moves
+          ok = wait(&sh->group[grp], sync++ & 1);
+          if (!ok) break;
+          fresh = sh->need[grp][at] == t + 1;
+          if (fresh) load_scores();
+        }
+        if (fresh) {
+          // each row's maximum over the tile's 128 slots, by warp then over the group's warps
+#pragma unroll
+          for (int i = 0; i < RW; i += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(factor + i);
+            y[i] *= kf * c.x, y[i + 1] *= kf * c.y, y[i + 2] *= kf * c.z, y[i + 3] *= kf * c.w;
+          }
+          hide(-INFINITY);
+          const float mine = fold_lanes<RW, true>(y, lane);
+          const float old = j == 0 ? kUnset : ref[fold_row];
+          const int my_byte = __reduce_max_sync(~0u, v_byte);
+          sh->warp_max[grp][w4][fold_row] = mine;
+          if (lane == 0) sh->warp_byte[grp][w4] = my_byte;
+          ok = meet();
+          if (!ok) break;
+          const float (*part)[RW] = sh->warp_max[grp];
+          const float m = fmaxf(old, fmaxf(fmaxf(part[0][fold_row], part[1][fold_row]),
+                                           fmaxf(part[2][fold_row], part[3][fold_row])) - kTop);
+          const int* byte = sh->warp_byte[grp];
+          const int f_old = f;
+          f = max(max(f, 1), max(max(byte[0], byte[1]), max(byte[2], byte[3])));
+          ref[fold_row] = m;  // the four warps write the same values
+          __syncwarp();
+          if (j > 0) {
+            // the sums so far and this thread's lane of O^T, after the last product
+            ok = wait(&sh->p_empty[set], (t - 1) & 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const float alpha = tc::ex2_approx(old - m), fewer = tc::ex2_approx(float(f_old - f));
+            tc::tmem_ld<RW>(t_o, y);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+              const float al = __shfl_sync(~0u, alpha, i * (32 / RW));
+              l[i] *= al, y[i] *= al * fewer;
+            }
+            tc::tmem_st<RW>(t_o, y);
+            tc::tmem_st_wait();
+          }
+          load_scores();
+          refer();
+          weigh();
+        }
+        // 2^(ev - f); NaN where V is NaN to the rows that see it
+        const float vf = from < to && bytes >> 8 == kv8::kNan ? kv8::factor(kv8::kNan) : kv8::power(max(v_byte - f, -126));
+        const unsigned long long vv = pack_f32x2(vf, vf);
+        uint32_t pk[RW / 2];
+#pragma unroll
+        for (int i = 0; i < RW; i += 2) l[i] += y[i], l[i + 1] += y[i + 1];
+#pragma unroll
+        for (int i = 0; i < RW; i += 2) unpack_f32x2(mul_f32x2(pack_f32x2(y[i], y[i + 1]), vv), y[i], y[i + 1]);
+        if (vf != vf) hide(0.f);
+#pragma unroll
+        for (int i = 0; i < RW; i += 2) {
+          const __half2 h2 = __floats2half2_rn(y[i], y[i + 1]);
+          pk[i / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        ok = wait(&sh->p_empty[set], (t & 1) ^ 1);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < RW / 8; ++i)
+          *reinterpret_cast<uint4*>(p_row + tc::swizzled<C::kPPitch>(kv, piece0 + i)) =
+              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        tc::fence_proxy_async_smem();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->p_full[set]));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------------- the unit's rows
+      // rows' sums over the 128 slots: lanes, then the group's warps in order
+      const float mine = fold_lanes<RW, false>(l, lane);
+      sh->warp_sum[grp][w4][fold_row] = mine;
+      ok = meet();
+      if (!ok) break;
+      const float (*part)[RW] = sh->warp_sum[grp];
+      const float sum = (part[0][fold_row] + part[1][fold_row]) + (part[2][fold_row] + part[3][fold_row]);
+      // NaN stays NaN, in the log-sum-exp too
+      const float inv = sum == 0.f ? 0.f : 1.f / sum, of = kv8::power(f - 127);
+      const bool partial = s.n < s.u.ntiles;
+      const int64_t pbase = (int64_t(2) * (blockIdx.x + set * gridDim.x) + (s.tile0 > 0 ? 0 : 1)) * R + row0;
+      const int n_rows = s.ntok * a.g - row0;  // of this group's
+      if (w4 == 0 && fold_row * (32 / RW) == lane && fold_row < n_rows) {
+        const float lse2 = sum == 0.f ? -INFINITY : ref[fold_row] + log2f(sum);
+        const int row = row0 + fold_row;
+        if (partial)
+          a.plse[pbase + fold_row] = lse2;
+        else if (a.lse)
+          a.lse[int64_t(s.row0 + row / a.g) * a.Hq + s.h * a.g + row % a.g] = lse2 * kLn2;
+      }
+      ok = wait(&sh->o_full[set], units++ & 1);
+      if (!ok) break;
+      tc::tc_fence_after();
+      float o[RW];
+      tc::tmem_ld<RW>(t_o, o);
+      tc::tmem_ld_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->o_read[set]));  // the next unit may overwrite it
+      if (kv < D) {  // TMEM lane = lane of the head; lanes from D on hold nothing
+#pragma unroll
+        for (int i = 0; i < RW; ++i) o[i] = o[i] * __shfl_sync(~0u, inv, i * (32 / RW)) * of;
+        if (partial) {
+          float* dst = a.partial + pbase * D + kv;
+#pragma unroll
+          for (int i = 0; i < RW; ++i)
+            if (i < n_rows) dst[i * D] = o[i];
+        } else {
+          const int tok = row0 / a.g;
+          int hh = row0 - tok * a.g;
+          __nv_bfloat16* dst = a.out + (int64_t(s.row0 + tok) * a.Hq + s.h * a.g + hh) * D + kv;
+          const int64_t wrap = int64_t(a.Hq - a.g) * D;  // from a token's last head to the next token's first
+#pragma unroll
+          for (int i = 0; i < RW; ++i) {
+            if (i < n_rows) *dst = __float2bfloat16(o[i]);
+            dst += D;
+            if (++hh == a.g) hh = 0, dst += wrap;
+          }
+        }
+      }
+    }
+    if (!ok) {
+      sh->abort = 1;
+      if (lane == 0) note_timeout(a.status, a.diag, 3u, uint32_t(t) | uint32_t(warp) << 24);
+    }
+  }
+
+  __syncthreads();
+  if (sh->abort) {  // MMAs and copies may be in flight: wait (bounded) before TMEM is freed and the block ends
+    const long long deadline = tc::deadline_after_ns(kDrainNs);
+    const int set = (warp - kTmaWarp) % 2;
+    if (warp >= kMmaWarp && warp < kConvWarp && set < kSets && sh->pending[set]) {
+      if (tc::elect_one()) tc::mma_commit(tc::smem_u32(&sh->drain[set]));
+      __syncwarp();
+      const volatile int never = 0;
+      tc::mbar_wait_bounded(tc::smem_u32(&sh->drain[set]), 0, deadline, &never);
+    } else if (warp >= kTmaWarp && warp < kMmaWarp && set < kSets) {
+      drain_copies(sh->full[set], C::kSlots, sh->n_put[set], deadline);
+      drain_copies(sh->sc_full[set], Sh::kScales, sh->n_k[set], deadline);
+    }
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <int D, int R>
+cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Attn8Args& a, int n_cta, cudaStream_t s) {
+  static bool done[tch::kMaxDevices] = {};
+  static std::mutex mu;
+  constexpr int kSmem = Cfg<D, R>::kSmem;
+  const cudaError_t e = tch::set_smem_once(window8_kernel<D, R>, kSmem, done, &mu);
+  return e != cudaSuccess ? e : launch_pdl(window8_kernel<D, R>, dim3(n_cta), dim3(kThreads), kSmem, s, k, v, a);
+}
+
+}  // namespace
+
+int attention_window8_sets(int D, int unit_rows) { return sets_of(D, unit_rows); }
+
+cudaError_t launch_attention_windows8(int D, int unit_rows, const CUtensorMap& k, const CUtensorMap& v,
+                                      const attn::Attn8Args& a, int n_cta, cudaStream_t s) {
+  if (D == 64) switch (unit_rows) {
+      case 16: return launch<64, 16>(k, v, a, n_cta, s);
+      case 32: return launch<64, 32>(k, v, a, n_cta, s);
+      case 64: return launch<64, 64>(k, v, a, n_cta, s);
+      default: return launch<64, 128>(k, v, a, n_cta, s);
+    }
+  switch (unit_rows) {
+    case 16: return launch<128, 16>(k, v, a, n_cta, s);
+    case 32: return launch<128, 32>(k, v, a, n_cta, s);
+    case 64: return launch<128, 64>(k, v, a, n_cta, s);
+    default: return launch<128, 128>(k, v, a, n_cta, s);
+  }
+}
+
+}  // namespace dspark

@@ -1,4 +1,4 @@
-// Two fp32 values in one 64-bit register and the paired fp32 FMA / add on them (sm_100 and
+// Two fp32 values in one 64-bit register and the paired fp32 FMA / add / mul on them (sm_100 and
 // later): each lane is an IEEE fma / add rounded to nearest, so a loop that pairs its lanes
 // gives the same bits as the scalar loop in the same order, with half the instructions.
 #pragma once
@@ -24,6 +24,12 @@ __device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, un
 __device__ __forceinline__ unsigned long long add_f32x2(unsigned long long a, unsigned long long b) {
   unsigned long long d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// a * b, lane by lane
+__device__ __forceinline__ unsigned long long mul_f32x2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 

@@ -150,7 +150,7 @@ int dspark_append_kv8(const void* q, int64_t q_stride, const void* k, int64_t k_
                           v_cache))
     return e;
   if (int e = check_heads(Hq, Hkv, D)) return e;
-  if (!kv_scale || !al(kv_scale, 2)) return DSPARK_EINVAL;
+  if (!kv_scale || !al(kv_scale, 16)) return DSPARK_EINVAL;
   if ((q == nullptr) != (q_out == nullptr)) return DSPARK_EINVAL;
   if (q && (bad_rows(q, q_stride, Hq * D) || !al(q_out, 16) || (q == q_out && q_stride != int64_t(Hq) * D)))
     return DSPARK_EINVAL;
@@ -172,7 +172,7 @@ int dspark_read_kv8(const void* k_cache, const void* v_cache, const uint8_t* kv_
                           v_cache))
     return e;
   if (int e = check_heads(Hkv, Hkv, D)) return e;
-  if (!kv_scale || !al(kv_scale, 2) || !out_table || !al(out_table, 4) || n_out_pages < 1) return DSPARK_EINVAL;
+  if (!kv_scale || !al(kv_scale, 16) || !out_table || !al(out_table, 4) || n_out_pages < 1) return DSPARK_EINVAL;
   if (!k_out || !v_out || !al(k_out, 16) || !al(v_out, 16) || k_out == v_out) return DSPARK_EINVAL;
   if (window < 0 || n_sink < 0) return DSPARK_EINVAL;
   if (int e = check_status_ws(ws, ws_bytes)) return e;
@@ -191,7 +191,7 @@ int dspark_window_attention_kv8(const void* q, int64_t q_stride, int dtype, cons
                           v_cache))
     return e;
   if (int e = check_heads(Hq, Hkv, D)) return e;
-  if (!kv_scale || !al(kv_scale, 2)) return DSPARK_EINVAL;
+  if (!kv_scale || !al(kv_scale, 16)) return DSPARK_EINVAL;
   if (bad_rows(q, q_stride, Hq * D) || !out || !al(out, 16) || !al(lse, 4)) return DSPARK_EINVAL;
   if (q == out && q_stride != int64_t(Hq) * D) return DSPARK_EINVAL;  // other rows' queries would be overwritten
   if ((k_scratch == nullptr) != (v_scratch == nullptr) || !al(k_scratch, 16) || !al(v_scratch, 16)) return DSPARK_EINVAL;

@@ -1,5 +1,5 @@
-// dspark_window_attention, host side and join: which kernel takes a call, and the kernel that joins the
-// partial rows of units that a cut between CTAs runs through.
+// dspark_window_attention and dspark_window_attention_kv8, host side and join: which kernel takes a call, and the kernel that
+// joins the partial rows of units that a cut between CTAs runs through.
 #include <algorithm>
 #include <cmath>
 
@@ -96,6 +96,15 @@ bool encode_cache(CUtensorMap* map, const void* base, int n_pages, int Hkv, int 
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// The 8-bit cache likewise; a box is one block's D bytes, the swizzle span.
+bool encode_cache8(CUtensorMap* map, const void* base, int n_pages, int Hkv, int page, int D, int block) {
+  const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(page), cuuint64_t(Hkv), cuuint64_t(n_pages)};
+  const cuuint64_t strides[3] = {cuuint64_t(D), cuuint64_t(page) * D, cuuint64_t(Hkv) * page * D};
+  const cuuint32_t box[4] = {cuuint32_t(D), cuuint32_t(block), 1u, 1u}, es[4] = {1, 1, 1, 1};
+  return tch::encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // Q as [row, head, lane]; a box is 64 columns of the g heads of `tokens` rows: the tile's rows in order.
 bool encode_q(CUtensorMap* map, const void* base, int rows, int Hq, int D, int64_t stride, int g, int tokens) {
   const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(Hq), cuuint64_t(rows)};
@@ -106,36 +115,29 @@ bool encode_q(CUtensorMap* map, const void* base, int rows, int Hq, int D, int64
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-size_t window_attention_ws_bytes(int Hq, int Hkv, int D) {
-  size_t most = attn_ws(D, 2 * kTile, tch::sm_count()).total;  // any tiling
-  for (int rows = 16; rows <= attention_window_rows(D); rows *= 2)
-    most = std::max(most, attn_ws(D, rows, attention_window_sets(D, rows) * tch::sm_count()).total);
-  return most;
-}
-
-cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
-                                    const int32_t* page_table, int max_pages, int n_pages, int page_shift,
-                                    const int32_t* cu, const int32_t* ctx, int bs, int rows, int max_rows, int Hq,
-                                    int Hkv, int D, float scale, int window, int n_sink, void* out, float* lse,
-                                    void* ws, cudaStream_t s) {
+// How a call is tiled, and its arguments but for the tensors that the kernels read through maps.
+struct Tiling {
   AttnArgs a;
-  const int n_cta = tch::sm_count(), g = Hq / Hkv, fit = kTile / g;
-  // GB300, 64 requests over 3000 .. 5000 positions, 8 KV heads, D 128: 132 rows to a KV head, the prompts' kernel 192 us, the
-  // windows' 319; 128 rows 182 and 181; 80 rows 175 and 172 (256 requests, window 256: 152 and 128).  D 64: 80 rows
-  // 131 and 153 (window 256: 140 and 128); 64 rows 131 and 95.
-  const bool prompts = max_rows > attention_window_rows(D) / g;
+  int unit_rows, n_ranges, n_cta;
+  bool prompts;
+};
+Tiling tile_call(const int32_t* page_table, int max_pages, int n_pages, int page_shift, const int32_t* cu,
+                 const int32_t* ctx, int bs, int rows, int max_rows, int Hq, int Hkv, int D, float scale, int window,
+                 int n_sink, void* out, float* lse, void* ws, bool prompts, int most_rows, int (*sets)(int, int)) {
+  Tiling t;
+  AttnArgs& a = t.a;
+  const int g = Hq / Hkv, fit = kTile / g;
+  t.n_cta = tch::sm_count(), t.prompts = prompts;
   // short windows: the narrowest tile that holds the expected rows.  256 requests, window 256, D 128, a row to a
   // request (4 to a KV head): R = 16 58 us, 32 59, 64 88, 128 123
-  int unit_rows = 16;
-  while (!prompts && unit_rows < max_rows * g) unit_rows *= 2;
-  if (prompts) unit_rows = 2 * kTile;
+  t.unit_rows = 16;
+  while (!prompts && t.unit_rows < max_rows * int64_t(g) && t.unit_rows < most_rows) t.unit_rows *= 2;
+  if (prompts) t.unit_rows = 2 * kTile;
   a.cache_limit = std::min(int64_t(max_pages) << page_shift, int64_t(1) << 30);  // positions: well inside 32 bits
   a.page_table = page_table, a.cu = cu, a.ctx = ctx, a.out = static_cast<__nv_bfloat16*>(out), a.lse = lse;
   char* w = static_cast<char*>(ws);
-  const int n_ranges = n_cta * (prompts ? 1 : attention_window_sets(D, unit_rows));
-  const AttnWs L = attn_ws(D, unit_rows, n_ranges);
+  t.n_ranges = t.n_cta * (prompts ? 1 : sets(D, t.unit_rows));
+  const AttnWs L = attn_ws(D, t.unit_rows, t.n_ranges);
   a.status = reinterpret_cast<uint32_t*>(w), a.diag = reinterpret_cast<uint32_t*>(w + 16);
   a.info = reinterpret_cast<int4*>(w + L.info);
   a.partial = reinterpret_cast<float*>(w + L.partial), a.plse = reinterpret_cast<float*>(w + L.plse);
@@ -146,28 +148,87 @@ cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void*
   // (2^(1e-30 s) is 1)
   if (a.c2 == 0.f) a.c2 = 1e-30f;
   a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, kMaxBlockShift);
-  a.bs = bs, a.rows = rows, a.Hq = Hq, a.Hkv = Hkv, a.g = g, a.tokens = prompts ? fit : std::min(unit_rows / g, std::max(max_rows, 1));
+  a.bs = bs, a.rows = rows, a.Hq = Hq, a.Hkv = Hkv, a.g = g;
+  a.tokens = prompts ? fit : std::min(t.unit_rows / g, std::max(max_rows, 1));
   a.window = window >= a.cache_limit ? 0 : window, a.n_sink = n_sink;
-  CUtensorMap mq, mk, mv;
-  const int page = 1 << page_shift, block = 1 << a.block_shift;
-  if (!tch::encode_fn() || !encode_q(&mq, q, rows, Hq, D, q_stride, a.g, a.tokens) ||
-      !encode_cache(&mk, k_cache, n_pages, Hkv, page, D, block) ||
-      !encode_cache(&mv, v_cache, n_pages, Hkv, page, D, block))
-    return cudaErrorInvalidValue;
-  const cudaError_t e = prompts ? launch_attention_prompts(D, mq, mk, mv, a, n_cta, s)
-                                : launch_attention_windows(D, unit_rows, mq, mk, mv, a, n_cta, s);
-  if (e != cudaSuccess) return e;
+  return t;
+}
+
+cudaError_t launch_join(const Tiling& t, int D, cudaStream_t s) {
+  const AttnArgs& a = t.a;
   // A unit is cut about once where units outnumber the ranges (64 windows over up to 32000 positions: two parts at a time 83.2
   // us, eight 85.1; prompts 306 and 316), and often where there are few (one token over 5000 positions: two 20.4, four 19.1,
   // eight 16.9).  A prompt has so many rows that their number counts for more than their parts (500 rows: two 22.8, sixteen
   // 28.0; 100 over 50000 positions: 42.7 and 40.3).  The number of units says nothing of a long context among short ones: 1 of
   // 30000 positions among 15 of 300, 8 KV heads, D 128, takes two parts (36.2) though sixteen were better (29.4), 1 of 100000
   // among 63 of 500 as well (91.7 and 85.9); with one KV head both take sixteen (18.0, two 41.1; 28.6, two 66.2).
-  const bool many_parts = !prompts && n_ranges > int64_t(4) * Hkv * std::max(bs, rows / a.tokens);
-  const dim3 grid(n_ranges, ((prompts ? kTile : 0) + a.tokens * g + 7) / 8);
-  auto join = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, a, unit_rows); };
+  const bool many_parts = !t.prompts && t.n_ranges > int64_t(4) * a.Hkv * std::max(a.bs, a.rows / a.tokens);
+  const dim3 grid(t.n_ranges, ((t.prompts ? kTile : 0) + a.tokens * a.g + 7) / 8);
+  auto join = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, a, t.unit_rows); };
   if (many_parts) return D == 64 ? join(attention_join_kernel<64, kJoinTogether>) : join(attention_join_kernel<128, kJoinTogether>);
   return D == 64 ? join(attention_join_kernel<64, 2>) : join(attention_join_kernel<128, 2>);
+}
+
+}  // namespace
+
+size_t window_attention_ws_bytes(int Hq, int Hkv, int D) {
+  size_t most = attn_ws(D, 2 * kTile, tch::sm_count()).total;  // any tiling, either cache
+  for (int rows = 16; rows <= attention_window_rows(D); rows *= 2)
+    most = std::max(most, attn_ws(D, rows, attention_window_sets(D, rows) * tch::sm_count()).total);
+  for (int rows = 16; rows <= kWindow8Rows; rows *= 2)
+    most = std::max(most, attn_ws(D, rows, attention_window8_sets(D, rows) * tch::sm_count()).total);
+  return most;
+}
+
+cudaError_t launch_window_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                    const int32_t* page_table, int max_pages, int n_pages, int page_shift,
+                                    const int32_t* cu, const int32_t* ctx, int bs, int rows, int max_rows, int Hq,
+                                    int Hkv, int D, float scale, int window, int n_sink, void* out, float* lse,
+                                    void* ws, cudaStream_t s) {
+  // GB300, 64 requests over 3000 .. 5000 positions, 8 KV heads, D 128: 132 rows to a KV head, the prompts' kernel 192 us, the
+  // windows' 319; 128 rows 182 and 181; 80 rows 175 and 172 (256 requests, window 256: 152 and 128).  D 64: 80 rows
+  // 131 and 153 (window 256: 140 and 128); 64 rows 131 and 95.
+  const bool prompts = max_rows > attention_window_rows(D) / (Hq / Hkv);
+  const Tiling t = tile_call(page_table, max_pages, n_pages, page_shift, cu, ctx, bs, rows, max_rows, Hq, Hkv, D, scale,
+                             window, n_sink, out, lse, ws, prompts, attention_window_rows(D), attention_window_sets);
+  CUtensorMap mq, mk, mv;
+  const int page = 1 << page_shift, block = 1 << t.a.block_shift;
+  if (!tch::encode_fn() || !encode_q(&mq, q, rows, Hq, D, q_stride, t.a.g, t.a.tokens) ||
+      !encode_cache(&mk, k_cache, n_pages, Hkv, page, D, block) ||
+      !encode_cache(&mv, v_cache, n_pages, Hkv, page, D, block))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = prompts ? launch_attention_prompts(D, mq, mk, mv, t.a, t.n_cta, s)
+                                : launch_attention_windows(D, t.unit_rows, mq, mk, mv, t.a, t.n_cta, s);
+  return e != cudaSuccess ? e : launch_join(t, D, s);
+}
+
+cudaError_t launch_window_attention_kv8(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                        const uint8_t* kv_scale, const int32_t* page_table, int max_pages, int n_pages,
+                                        int page_shift, const int32_t* cu, const int32_t* ctx, int bs, int rows,
+                                        int max_rows, int Hq, int Hkv, int D, float scale, int window, int n_sink,
+                                        void* out, float* lse, void* k_scratch, void* v_scratch, void* ws,
+                                        cudaStream_t s) {
+  if (k_scratch && max_rows > kWindow8Rows / (Hq / Hkv)) {
+    // every unit of 256 rows would convert K and V for itself: converted once, for all of a request's units
+    const cudaError_t e = launch_read_kv8(k_cache, v_cache, kv_scale, page_table, max_pages, n_pages, page_shift, cu, ctx, bs,
+                                          rows, Hkv, D, window, n_sink, page_table, n_pages, k_scratch, v_scratch,
+                                          static_cast<uint32_t*>(ws), s);
+    return e != cudaSuccess ? e
+                            : launch_window_attention(q, q_stride, k_scratch, v_scratch, page_table, max_pages, n_pages,
+                                                      page_shift, cu, ctx, bs, rows, max_rows, Hq, Hkv, D, scale, window,
+                                                      n_sink, out, lse, ws, s);
+  }
+  const Tiling t = tile_call(page_table, max_pages, n_pages, page_shift, cu, ctx, bs, rows, max_rows, Hq, Hkv, D, scale,
+                             window, n_sink, out, lse, ws, false, kWindow8Rows, attention_window8_sets);
+  Attn8Args a;
+  a.a = t.a, a.kv_scale = kv_scale, a.q = static_cast<const __nv_bfloat16*>(q), a.q_stride = q_stride, a.negate = scale < 0.f;
+  CUtensorMap mk, mv;
+  const int page = 1 << page_shift, block = 1 << t.a.block_shift;
+  if (!tch::encode_fn() || !encode_cache8(&mk, k_cache, n_pages, Hkv, page, D, block) ||
+      !encode_cache8(&mv, v_cache, n_pages, Hkv, page, D, block))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = launch_attention_windows8(D, t.unit_rows, mk, mv, a, t.n_cta, s);
+  return e != cudaSuccess ? e : launch_join(t, D, s);
 }
 
 }  // namespace dspark
