@@ -1,19 +1,19 @@
 // The attention of short windows over the 8-bit cache: attention_windows.cu's pipelines with half the bytes to read.
 //
 //     S^T = K8 (Qh + Ql)^T      [128 slots x R]   (tcgen05 kind::f8f6f4, fp32 in TMEM)
-//     x = S^T 2^(ek + eq) c,  P^T = 2^(x - m) 2^(ev - f)   (fp16, shared memory), partial sums of 2^(x - m) in registers
-//     O^T += V^T P^T            [D x R]           (tcgen05 kind::f16, V as fp16; fp32 in TMEM), out = O^T 2^f / l
+//     x = S^T 2^(ek + eq) c,  P^T = 2^(x - m) 2^(ev - f) = Ph + Pl / 16   (e4m3, shared memory), sums of 2^(x - m) in registers
+//     Oh^T | Ol^T += V8^T (Ph | Pl)^T  [D x 2R]   (tcgen05, fp32 in TMEM),   out = (Oh + Ol / 16) 2^f / l
 //
-// K goes into its product as it lies in the cache.  The other operand is Q as a sum of two e4m3 parts under a power of two of
-// its row, 2^eq: the first takes the upper four of bf16's eight bits, the second what is left, which is exact for lanes down
-// to 2^-10 of the row's largest; smaller ones are off by at most 2^-19 of that.  (One part alone would be off by 2^-4.)  The
-// slots' powers of two, ek, are one factor per thread, the rows', eq, one per score.
-// V is the operand whose contraction runs over slots, so its factors 2^ev have to go into P.  P has to have more bits and more
-// range than e4m3 has; fp16 has eleven bits from 2^-14 on.  So four warps turn V's tiles into fp16 (exact: one conversion for two
-// values), clearing the slots that nobody sees on the way.  P is kept inside fp16's range by two references, a row's m, which
-// lies 2^6 below its maximum of a unit's first tile, and f, the largest ev of the tile's slots; both are checked on each tile
-// against 2^15, and set anew where they are outgrown, O^T and the sums with them.  A weight keeps its eleven bits down to 2^-20 of
-// the largest, and its place down to 2^-31.
+// K and V go into the products as they lie in the cache; nothing is converted but the other operands, which one code of e4m3
+// (relative error 2^-4) would be too little for, so each is a sum of two.
+// Q's row is taken under a power of two of its own, 2^eq: the first part has the upper four of bf16's eight bits, the second
+// what is left, exact for lanes down to 2^-10 of the row's largest; smaller ones are off by at most 2^-19 of that.  The slots'
+// powers, ek, are one factor per thread, the rows' one per score.
+// A weight has eight bits, as bf16 has (relative 2^-8), down to 2^-16 of the largest and an error of 2^-20 of it
+// below; the second part is kept times 16 and in accumulators of its own for that.  V's contraction runs over slots, so its
+// powers 2^ev have to go into P.  P is kept inside e4m3's range by two references, a row's m, which lies kTop below its
+// maximum of a unit's first tile, and f, the largest ev of the tile's slots; both are checked on each tile against kMost, and
+// set anew where they are outgrown, O^T and the sums with them.
 #include "attention_common.cuh"
 #include "kv8.cuh"
 
@@ -23,17 +23,18 @@ namespace {
 using namespace attn;
 
 // Sixteen softmax warps in groups of four; a group takes a share of the rows of its pipeline's tiles.  Then a
-// TMA warp for each pipeline, an MMA warp for each, and four warps that convert (all four for a lone pipeline).
+// TMA warp for each pipeline, an MMA warp for each, and four warps that split Q (all four for a lone pipeline).
 constexpr int kGroups = 4, kThreads = (kGroups + 2) * 128;
-constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 2, kConvWarp = kMmaWarp + 2;
+constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 2, kSplitWarp = kMmaWarp + 2;
 // Registers: launched with 768 x 80; the softmax warps take what the others give back (512 x 96 + 256 x 48 <= 768 x 80).
 constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
 constexpr int kMaxSlots = 8;
-constexpr int kQRing = 4;  // units whose rows' factors are kept
-// m lies kTop below a maximum; a score or a value's power may outgrow the references up to kMost (fp16 holds 2^16 - 2^5)
-constexpr float kTop = 6.f, kMost = 15.f;
+constexpr int kQBufs = 2, kQRing = 4;  // units whose Q, whose rows' factors are kept
+// m lies kTop below a maximum; a score and a value's power together may outgrow the references up to kMost (e4m3 ends at
+// 448 = 2^8.8)
+constexpr float kTop = 6.f, kMost = 8.75f;
 
-constexpr int sets_of(int D, int R) { return R * D >= 64 * 128 ? 1 : 2; }
+constexpr int sets_of(int D, int R) { return R == 128 ? 1 : 2; }
 
 template <int D, int R>
 struct Shared {
@@ -41,8 +42,8 @@ struct Shared {
   // tiles whose exponent bytes are kept: a slot of the ring ahead of the products, which are two tiles ahead of the softmax
   static constexpr int kScales = 16;
   static_assert(kScales >= kMaxSlots + 3, "a tile's bytes are written anew when its softmax is over");
-  uint64_t q_ready[kSets][kQRing], q_empty[kSets][2], full[kSets][kMaxSlots], empty[kSets][kMaxSlots];
-  uint64_t sc_full[kSets][kScales], v_full[kSets], v_empty[kSets];
+  uint64_t q_ready[kSets][kQRing], q_empty[kSets][kQBufs], full[kSets][kMaxSlots], empty[kSets][kMaxSlots];
+  uint64_t sc_full[kSets][kScales];
   uint64_t s_full[kSets][2], p_full[kSets], p_empty[kSets], o_full[kSets], o_read[kSets];
   uint64_t group[kGroups], drain[kSets];
   uint32_t tmem_base;
@@ -61,24 +62,34 @@ struct Shared {
 template <int D, int R>
 struct Cfg {
   static constexpr int kSets = sets_of(D, R), kRowGroups = kGroups / kSets;
-  static constexpr int kConvWarps = 4 / kSets;               // of a pipeline
-  static constexpr int kSlotBytes = kTile * D;               // a tile of codes
-  static constexpr int kVBytes = kTile * D * 2;              // a tile of V in fp16: 128-byte swizzled blocks of 64 columns
+  static constexpr int kSplitWarps = 4 / kSets;              // of a pipeline
+  static constexpr int kSlotBytes = kTile * D;               // a tile of codes: rows of D bytes, D-byte swizzled
   static constexpr int kQPart = R * D, kQBytes = 2 * kQPart;
-  static constexpr int kQBufs = R * D <= 64 * 128 ? 2 : 1;   // where they fit
   static constexpr int kPPitch = R < 64 ? R * 2 : 128;       // bytes of a slot's row of P, R > 64: in two chunks
   static constexpr int kPBytes = kTile * R * 2;
-  // O^T has M = 128 also where D = 64: its lanes 64 .. 127 come from the 16 KB behind the V tile, whatever
-  // they hold, and are not read
-  static constexpr int kBehind = kSets * (kQBytes * kQBufs + kPBytes);
-  static constexpr int kPad = D == 64 && kBehind < 16384 ? 16384 - kBehind : 0;
-  static constexpr int kRoom = (232448 - int(sizeof(Shared<D, R>)) - kBehind - kPad - kSets * kVBytes) / kSlotBytes / kSets;
+  static constexpr int kRoom = (232448 - int(sizeof(Shared<D, R>)) - kSets * (kQBytes * kQBufs + kPBytes)) / kSlotBytes / kSets;
   static constexpr int kSlots = kRoom < kMaxSlots ? kRoom : kMaxSlots;  // ring of a pipeline
-  static constexpr int kSmem = kSets * (kSlots * kSlotBytes + kVBytes) + kBehind + kPad + int(sizeof(Shared<D, R>));
-  static constexpr int kUsedCols = kSets * 3 * R;            // per pipeline: S^T twice, O^T
+  static constexpr int kSmem = kSets * (kSlots * kSlotBytes + kQBytes * kQBufs + kPBytes) + int(sizeof(Shared<D, R>));
+  static constexpr int kUsedCols = kSets * 4 * R;            // per pipeline: S^T twice, Oh^T, Ol^T
   static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static_assert(kSlots >= 3 && kUsedCols <= 512 && kQPart % 1024 == 0 && kPBytes % 1024 == 0, "layout");
 };
+
+// V's slots that no row of the unit sees hold whatever was there, NaN included, and 0 * NaN is NaN: their codes are
+// cleared.  A whole warp, 16-byte stores, rotated so that the lanes spread over the banks.
+template <int D>
+__device__ __forceinline__ void clear_unseen_codes(const AttnArgs& a, const Segment& s, int j, uint8_t* tile, int lane) {
+  const int first = (s.tile0 + j) * (kTile >> a.block_shift);
+  for (int i = lane; i < kTile; i += 32) {
+    const int pos = block_pos(a, s.u, first + (i >> a.block_shift)) + (i & ((1 << a.block_shift) - 1));
+    if (pos <= s.u.p1 && (pos >= s.u.lo || pos < a.n_sink)) continue;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+      *reinterpret_cast<uint4*>(tile + i * D + (((k + lane) & (D / 16 - 1)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  tc::fence_proxy_async_smem();
+  __syncwarp();
+}
 
 // Issue a tile's loads: the codes, and for K (`scales` given) the exponent bytes of K and V with them.
 template <int D>
@@ -121,30 +132,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   const AttnArgs& a = args.a;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sRing = smem;
-  uint8_t* sV = sRing + kSets * C::kSlots * C::kSlotBytes;
-  uint8_t* sQ = sV + kSets * C::kVBytes;
-  uint8_t* sP = sQ + kSets * C::kQBufs * C::kQBytes;
-  Sh* sh = reinterpret_cast<Sh*>(sP + kSets * C::kPBytes + C::kPad);
+  uint8_t* sQ = sRing + kSets * C::kSlots * C::kSlotBytes;
+  uint8_t* sP = sQ + kSets * kQBufs * C::kQBytes;
+  Sh* sh = reinterpret_cast<Sh*>(sP + kSets * C::kPBytes);
   PlanScratch& plan = *reinterpret_cast<PlanScratch*>(sRing);  // before the first load
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same for the warp, and known to be
 
   if (warp == 0) {  // barriers: lane i those of number i
     for (int z = 0; z < kSets; ++z) {
-      if (lane < kQRing) tc::mbar_init(tc::smem_u32(&sh->q_ready[z][lane]), C::kConvWarps);
+      if (lane < kQRing) tc::mbar_init(tc::smem_u32(&sh->q_ready[z][lane]), C::kSplitWarps);
       if (lane < 2) {
-        tc::mbar_init(tc::smem_u32(&sh->q_empty[z][lane]), 1);
+        if (lane < kQBufs) tc::mbar_init(tc::smem_u32(&sh->q_empty[z][lane]), 1);
         tc::mbar_init(tc::smem_u32(&sh->s_full[z][lane]), 1);
       }
       if (lane < C::kSlots) {
         tc::mbar_init(tc::smem_u32(&sh->full[z][lane]), 1);
-        tc::mbar_init(tc::smem_u32(&sh->empty[z][lane]), C::kConvWarps);  // a K tile's product arrives as often
+        tc::mbar_init(tc::smem_u32(&sh->empty[z][lane]), 1);
       }
       if (lane < Sh::kScales) tc::mbar_init(tc::smem_u32(&sh->sc_full[z][lane]), 1);
     }
     if (lane < kSets) {
-      tc::mbar_init(tc::smem_u32(&sh->v_full[lane]), C::kConvWarps);
-      tc::mbar_init(tc::smem_u32(&sh->v_empty[lane]), 1);
       tc::mbar_init(tc::smem_u32(&sh->p_full[lane]), 4 * kRowGroups);
       tc::mbar_init(tc::smem_u32(&sh->p_empty[lane]), 1);
       tc::mbar_init(tc::smem_u32(&sh->o_full[lane]), 1);
@@ -229,19 +237,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kMmaWarp && warp < kMmaWarp + kSets) {
     // ------------------------------------------------------------ the two products of each tile
     constexpr uint32_t idesc_s = tc::idesc_e4m3_f32(kTile, R);
-    constexpr uint32_t idesc_o = tc::idesc_f16_f32(128, R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
+    constexpr uint32_t idesc_o = tc::idesc_e4m3_f32(128, 2 * R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
     const int set = warp - kMmaWarp;
     const Waiter wait{&sh->abort, a.timeout_ns};
-    const uint32_t t_s = tmem + set * 3 * R, t_o = t_s + 2 * R;
-    const uint64_t dk = tc::sdesc_kmajor<D>(tc::smem_u32(sRing + set * C::kSlots * C::kSlotBytes));
-    const uint64_t dq = tc::sdesc_kmajor<D>(tc::smem_u32(sQ + set * C::kQBufs * C::kQBytes));
-    const uint64_t dv = tc::sdesc_mnmajor<128>(tc::smem_u32(sV + set * C::kVBytes), kTile * 128);
+    uint8_t* ring_mem = sRing + set * C::kSlots * C::kSlotBytes;
+    const uint32_t t_s = tmem + set * 4 * R, t_o = t_s + 2 * R;
+    const uint64_t dk = tc::sdesc_kmajor<D>(tc::smem_u32(ring_mem));
+    const uint64_t dq = tc::sdesc_kmajor<D>(tc::smem_u32(sQ + set * kQBufs * C::kQBytes));
+    // O^T has M = 128 also where D = 64: its lanes 64 .. 127 come from the tile behind, whatever it holds, and are not read
+    const uint64_t dv = tc::sdesc_mnmajor<D>(tc::smem_u32(ring_mem), C::kSlotBytes);
     const uint64_t dp = tc::sdesc_mnmajor<C::kPPitch>(tc::smem_u32(sP + set * C::kPBytes), kTile * 128);
     Ring<C::kSlots> ring;
-    int n_seg = 0, n_s = 0, t = 0, units = 0;
+    int n_seg = 0, n_s = 0, t = 0, units = 0, j0 = 0, j1 = 0;
     Cursor kc(sh->start[set], a.tokens), vc(sh->start[set], a.tokens);
     auto s_product = [&]() {  // S^T of the tile at kc; the S before last has been read (its P is there)
-      const int b = n_seg % C::kQBufs;
+      const int b = n_seg % kQBufs;
       if (kc.first() && !wait(&sh->q_ready[set][n_seg % kQRing], (n_seg / kQRing) & 1)) return false;
       if (!wait(&sh->full[set][ring.slot], ring.phase)) return false;
       tc::tc_fence_after();
@@ -255,8 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mma_f8(t_s + (n_s & 1) * R, dk_t + ((i * 32) >> 4), dq_t + ((part * C::kQPart + i * 32) >> 4), idesc_s,
                        part != 0 || i != 0);
         tc::mma_commit(tc::smem_u32(&sh->s_full[set][n_s & 1]));
-#pragma unroll
-        for (int i = 0; i < C::kConvWarps; ++i) tc::mma_commit(tc::smem_u32(&sh->empty[set][ring.slot]));
+        tc::mma_commit(tc::smem_u32(&sh->empty[set][ring.slot]));
         if (last) tc::mma_commit(tc::smem_u32(&sh->q_empty[set][b]));
       }
       __syncwarp();
@@ -273,20 +282,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (; ok && vc.next(a); ++t) {
       const bool first = vc.first(), last = vc.last();
-      ok = wait(&sh->v_full[set], t & 1) && wait(&sh->p_full[set], t & 1);
+      ok = wait(&sh->full[set][ring.slot], ring.phase);
+      if (!ok) break;
+      if (first) whole_tiles(a, vc.s, vc.s.u.p1, vc.s.u.p0, j0, j1);
+      // while the softmax works on this tile
+      if (vc.j < j0 || vc.j >= j1) clear_unseen_codes<D>(a, vc.s, vc.j, ring_mem + ring.slot * C::kSlotBytes, lane);
+      ok = wait(&sh->p_full[set], t & 1);
       if (ok && first) ok = wait(&sh->o_read[set], (units++ & 1) ^ 1);  // the unit before has been read
       if (!ok) break;
       tc::tc_fence_after();
+      const uint64_t dv_t = dv + uint32_t(ring.slot * (C::kSlotBytes >> 4));
       if (tc::elect_one()) {
 #pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          tc::mma_bf16(t_o, dv + ((i * 2048) >> 4), dp + ((i * 16 * C::kPPitch) >> 4), idesc_o, !first || i != 0);
+        for (int i = 0; i < kTile / 32; ++i)
+          tc::mma_f8(t_o, dv_t + ((i * 32 * D) >> 4), dp + ((i * 32 * C::kPPitch) >> 4), idesc_o, !first || i != 0);
         tc::mma_commit(tc::smem_u32(&sh->p_empty[set]));
-        tc::mma_commit(tc::smem_u32(&sh->v_empty[set]));
+        tc::mma_commit(tc::smem_u32(&sh->empty[set][ring.slot]));
         if (last) tc::mma_commit(tc::smem_u32(&sh->o_full[set]));
       }
       __syncwarp();
-      ring.step();  // the V tile's slot
+      ring.step();
       if (more) {
         more = kc.next(a);
         ok = !more || s_product();
@@ -297,32 +312,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) note_timeout(a.status, a.diag, 2u, uint32_t(t));
     }
     if (lane == 0) sh->pending[set] = n_s > 0;
-  } else if (warp >= kConvWarp) {
-    // ---------------------------------------------- Q into two parts of e4m3, V tiles into fp16
-    const int set = (warp - kConvWarp) / C::kConvWarps, w = (warp - kConvWarp) % C::kConvWarps;
+  } else if (warp >= kSplitWarp) {
+    // ---------------------------------------------------------------- Q into two parts of e4m3
+    const int set = (warp - kSplitWarp) / C::kSplitWarps, w = (warp - kSplitWarp) % C::kSplitWarps;
     const Waiter wait{&sh->abort, a.timeout_ns};
-    const uint8_t* ring_mem = sRing + set * C::kSlots * C::kSlotBytes;
-    uint8_t* v_mem = sV + set * C::kVBytes;
-    Ring<C::kSlots> ring;
+    constexpr int kLanes = D / 16, kPass = 32 / kLanes * C::kSplitWarps;  // threads to a row, rows at a time
+    const int piece = lane % kLanes;
+    int n_seg = 0;
     bool ok = true;
-    int n_seg = 0, q_tile = 0, t = 0;  // units whose Q is done; the range's tile at which the next one begins
-    Walk qw(sh->start[set], a.tokens);
-    Cursor vc(sh->start[set], a.tokens);
-    Segment sq = {};
-    bool q_more = qw.next(a, sq);
-    auto convert_q = [&]() {
-      const int b = n_seg % C::kQBufs;
-      if (!wait(&sh->q_empty[set][b], ((n_seg / C::kQBufs) & 1) ^ 1)) return false;
-      constexpr int kLanes = D / 16, kPass = 32 / kLanes * C::kConvWarps;  // threads to a row, rows at a time
-      uint8_t* q_mem = sQ + (set * C::kQBufs + b) * C::kQBytes;
-      const int piece = lane % kLanes;
-#pragma unroll 1
+    Walk walk(sh->start[set], a.tokens);
+    Segment s = {};
+    for (; walk.next(a, s); ++n_seg) {
+      const int b = n_seg % kQBufs;
+      ok = wait(&sh->q_empty[set][b], ((n_seg / kQBufs) & 1) ^ 1);
+      if (!ok) break;
+      uint8_t* q_mem = sQ + (set * kQBufs + b) * C::kQBytes;
+#pragma unroll 2
       for (int row = w * (32 / kLanes) + lane / kLanes; row < R; row += kPass) {
         const int tok = row / a.g, hh = row - tok * a.g;
-        uint4 x[2] = {};
-        if (tok < sq.ntok) {
-          const uint4* src = reinterpret_cast<const uint4*>(args.q + int64_t(sq.row0 + tok) * args.q_stride +
-                                                            int64_t(sq.h * a.g + hh) * D) + 2 * piece;
+        uint4 x[2] = {};  // rows behind the unit's are 0
+        if (tok < s.ntok) {
+          const uint4* src = reinterpret_cast<const uint4*>(args.q + int64_t(s.row0 + tok) * args.q_stride +
+                                                            int64_t(s.h * a.g + hh) * D) + 2 * piece;
           x[0] = src[0], x[1] = src[1];
         }
         const uint32_t word[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
@@ -355,57 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->q_ready[set][n_seg % kQRing]));
-      ++n_seg;
-      return true;
-    };
-    // The ring's slots in the order of the loads: K 0, K 1, then V t, K t + 2 (as far as there are such tiles)
-    uint32_t left = sh->start[set].count;
-    left = left < 2 ? left : 2;
-    for (uint32_t i = 0; i < left; ++i) ring.step();
-    const uint32_t n_tiles = sh->start[set].count;
-    for (; ok && vc.next(a); ++t) {
-      while (ok && q_more && q_tile <= t + 2) {
-        ok = convert_q();
-        q_tile += sq.n;
-        q_more = qw.next(a, sq);
-      }
-      ok = ok && wait(&sh->full[set][ring.slot], ring.phase) && wait(&sh->v_empty[set], (t & 1) ^ 1);
-      if (!ok) break;
-      const uint8_t* src = ring_mem + ring.slot * C::kSlotBytes;
-      const Segment& s = vc.s;
-      int j0, j1;  // the tiles of which every slot is seen by some row
-      whole_tiles(a, s, s.u.p1, s.u.p0, j0, j1);
-      const int first = (s.tile0 + vc.j) * (kTile >> a.block_shift);
-#pragma unroll 1
-      for (int slot = w * 32 + lane; slot < kTile; slot += C::kConvWarps * 32) {
-        bool seen = vc.j >= j0 && vc.j < j1;
-        if (!seen) {
-          const int pos = block_pos(a, s.u, first + (slot >> a.block_shift)) + (slot & ((1 << a.block_shift) - 1));
-          seen = pos <= s.u.p1 && (pos >= s.u.lo || pos < a.n_sink);
-        }
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint4 c = *reinterpret_cast<const uint4*>(src + tc::swizzled<D>(slot, i));
-          if (!seen) c = make_uint4(0u, 0u, 0u, 0u);  // it holds whatever was there, NaN included, and 0 * NaN is NaN
-          uint8_t* dst = v_mem + (i / 4) * (kTile * 128);
-          *reinterpret_cast<uint4*>(dst + tc::swizzled<128>(slot, (2 * i) % 8)) =
-              make_uint4(kv8::halves(c.x & 0xFFFFu), kv8::halves(c.x >> 16), kv8::halves(c.y & 0xFFFFu), kv8::halves(c.y >> 16));
-          *reinterpret_cast<uint4*>(dst + tc::swizzled<128>(slot, (2 * i) % 8 + 1)) =
-              make_uint4(kv8::halves(c.z & 0xFFFFu), kv8::halves(c.z >> 16), kv8::halves(c.w & 0xFFFFu), kv8::halves(c.w >> 16));
-        }
-      }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(tc::smem_u32(&sh->v_full[set]));
-        tc::mbar_arrive(tc::smem_u32(&sh->empty[set][ring.slot]));
-      }
-      ring.step();
-      if (uint32_t(t) + 2 < n_tiles) ring.step();  // K t + 2
     }
     if (!ok) {
       sh->abort = 1;
-      if (lane == 0) note_timeout(a.status, a.diag, 4u, uint32_t(t));
+      if (lane == 0) note_timeout(a.status, a.diag, 4u, uint32_t(n_seg));
     }
   } else if (warp < kTmaWarp) {
     // ------------------------------------------------------------------------- softmax
@@ -414,11 +378,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int grp = warp >> 2, w4 = warp & 3;
     const int kv = w4 * 32 + lane;  // this thread's slot of each tile = TMEM lane
     const int set = grp % kSets, row0 = grp / kSets * RW;  // and its rows
-    const uint32_t t_s = tmem + (uint32_t(w4 * 32) << 16) + set * 3 * R + row0, t_o = t_s + 2 * R;
+    const uint32_t t_s = tmem + (uint32_t(w4 * 32) << 16) + set * 4 * R + row0, t_o = t_s + 2 * R;
     float* ref = sh->ref[set] + row0;
-    // where this thread's row of P goes: 16-byte pieces, from the first row of the group on
-    uint8_t* p_row = sP + set * C::kPBytes + (R == 128 ? (row0 / 64) * (kTile * 128) : 0);
-    const int piece0 = (R == 128 ? row0 % 64 : row0) / 8;
+    // a slot's row of P: its R first parts, then its second parts (R = 128: in a chunk of their own)
+    uint8_t* p_mem = sP + set * C::kPBytes;
     // the row that this lane holds after a fold (the lanes of a row hold the same)
     const int fold_row = lane / (32 / RW);
     int t = 0, sync = 0, units = 0;
@@ -530,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            fmaxf(part[2][fold_row], part[3][fold_row])) - kTop);
           const int* byte = sh->warp_byte[grp];
           const int f_old = f;
-          f = max(max(f, 1), max(max(byte[0], byte[1]), max(byte[2], byte[3])));
+          // f may fall, too: O^T keeps its place in fp32, and this tile's weights theirs in e4m3
+          f = max(max(max(byte[0], byte[1]), max(byte[2], byte[3])), max(f - 40, 1));
           ref[fold_row] = m;  // the four warps write the same values
           __syncwarp();
           if (j > 0) {
@@ -539,14 +503,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc::tc_fence_after();
             const float alpha = tc::ex2_approx(old - m), fewer = tc::ex2_approx(float(f_old - f));
-            tc::tmem_ld<RW>(t_o, y);
-            tc::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < RW; ++i) {
-              const float al = __shfl_sync(~0u, alpha, i * (32 / RW));
-              l[i] *= al, y[i] *= al * fewer;
+            for (int part = 0; part < 2; ++part) {
+              tc::tmem_ld<RW>(t_o + part * R, y);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < RW; ++i) {
+                const float al = __shfl_sync(~0u, alpha, i * (32 / RW));
+                if (part == 0) l[i] *= al;
+                y[i] *= al * fewer;
+              }
+              tc::tmem_st<RW>(t_o + part * R, y);
             }
-            tc::tmem_st<RW>(t_o, y);
             tc::tmem_st_wait();
           }
           load_scores();
@@ -556,23 +524,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 2^(ev - f); NaN where V is NaN to the rows that see it
         const float vf = from < to && bytes >> 8 == kv8::kNan ? kv8::factor(kv8::kNan) : kv8::power(max(v_byte - f, -126));
         const unsigned long long vv = pack_f32x2(vf, vf);
-        uint32_t pk[RW / 2];
 #pragma unroll
         for (int i = 0; i < RW; i += 2) l[i] += y[i], l[i + 1] += y[i + 1];
 #pragma unroll
         for (int i = 0; i < RW; i += 2) unpack_f32x2(mul_f32x2(pack_f32x2(y[i], y[i + 1]), vv), y[i], y[i + 1]);
         if (vf != vf) hide(0.f);
+        uint32_t hi[RW / 4], lo[RW / 4];
 #pragma unroll
-        for (int i = 0; i < RW; i += 2) {
-          const __half2 h2 = __floats2half2_rn(y[i], y[i + 1]);
-          pk[i / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+        for (int i = 0; i < RW / 4; ++i) {
+          uint32_t h[2], r[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) kv8::split2(__floats2half2_rn(y[4 * i + 2 * k], y[4 * i + 2 * k + 1]), h[k], r[k]);
+          hi[i] = h[0] | h[1] << 16, lo[i] = r[0] | r[1] << 16;
         }
         ok = wait(&sh->p_empty[set], (t & 1) ^ 1);
         if (!ok) break;
+        auto put_p = [&](const uint32_t* w, int at) {  // at byte `at` of the slot's row
+          uint8_t* dst = p_mem + (at / C::kPPitch) * (kTile * C::kPPitch);
+          const int in = at % C::kPPitch;
+          if constexpr (RW == 8) {
+            *reinterpret_cast<uint2*>(dst + tc::swizzled<C::kPPitch>(kv, in / 16) + in % 16) = make_uint2(w[0], w[1]);
+          } else {
 #pragma unroll
-        for (int i = 0; i < RW / 8; ++i)
-          *reinterpret_cast<uint4*>(p_row + tc::swizzled<C::kPPitch>(kv, piece0 + i)) =
-              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            for (int i = 0; i < RW / 16; ++i)
+              *reinterpret_cast<uint4*>(dst + tc::swizzled<C::kPPitch>(kv, in / 16 + i)) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        };
+        put_p(hi, row0);
+        put_p(lo, R + row0);
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
         __syncwarp();
@@ -604,8 +584,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc::tc_fence_after();
       float o[RW];
+      tc::tmem_ld<RW>(t_o + R, o);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < RW; ++i) l[i] = o[i];
       tc::tmem_ld<RW>(t_o, o);
       tc::tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < RW; ++i) o[i] = fmaf(l[i], 1.f / 16, o[i]);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->o_read[set]));  // the next unit may overwrite it
@@ -641,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (sh->abort) {  // MMAs and copies may be in flight: wait (bounded) before TMEM is freed and the block ends
     const long long deadline = tc::deadline_after_ns(kDrainNs);
     const int set = (warp - kTmaWarp) % 2;
-    if (warp >= kMmaWarp && warp < kConvWarp && set < kSets && sh->pending[set]) {
+    if (warp >= kMmaWarp && warp < kSplitWarp && set < kSets && sh->pending[set]) {
       if (tc::elect_one()) tc::mma_commit(tc::smem_u32(&sh->drain[set]));
       __syncwarp();
       const volatile int never = 0;
