@@ -22,14 +22,20 @@ namespace {
 
 using namespace attn;
 
-// Sixteen softmax warps in groups of four; a group takes a share of the rows of its pipeline's tiles.  Then a
+// Eight softmax warps in two groups of four, one for each pipeline (R = 128: half the rows of the lone one each).  Then a
 // TMA warp for each pipeline, an MMA warp for each, and four warps that split Q (all four for a lone pipeline).
-constexpr int kGroups = 4, kThreads = (kGroups + 2) * 128;
+constexpr int kGroups = 2, kThreads = (kGroups + 2) * 128;
 constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 2, kSplitWarp = kMmaWarp + 2;
-// Registers: launched with 768 x 80; the softmax warps take what the others give back (512 x 96 + 256 x 48 <= 768 x 80).
-constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
-constexpr int kMaxSlots = 8;
-constexpr int kQBufs = 2, kQRing = 4;  // units whose Q, whose rows' factors are kept
+// Registers: launched with 512 x 128; the softmax warps take what the others give back (256 x 184 + 256 x 72 = 512 x 128).
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+#ifndef KV8_SLOTS
+#define KV8_SLOTS 8
+#endif
+#ifndef KV8_QBUFS
+#define KV8_QBUFS 2
+#endif
+constexpr int kMaxSlots = KV8_SLOTS;
+constexpr int kQBufs = KV8_QBUFS, kQRing = 4;  // units whose Q, whose rows' factors are kept
 // m lies kTop below a maximum; a score and a value's power together may outgrow the references up to kMost (e4m3 ends at
 // 448 = 2^8.8)
 constexpr float kTop = 6.f, kMost = 8.75f;
@@ -54,7 +60,10 @@ struct Shared {
   Start start[kSets];
   int warp_byte[kGroups][4];   // by warp: the largest exponent byte of V in a tile
   float warp_max[kGroups][4][kRows], warp_sum[kGroups][4][kRows];  // by warp: the rows' maxima of a tile, sums of a unit
-  alignas(16) float ref[kSets][R];             // the rows' references, read four at a time
+  alignas(16) float neg_ref[kSets][R];         // the rows' references, negated; read four at a time
+  alignas(16) float row_by[kSets][R];          // what a row's sums, and its output, are to be multiplied by
+  alignas(16) float zeros[kRows];
+  float next_ref[kGroups][4][kRows];
   alignas(16) float row_factor[kSets][kQRing][R];  // 2^eq c
   alignas(16) uint16_t scales[kSets][kScales][kTile];
 };
@@ -90,6 +99,39 @@ __device__ __forceinline__ void clear_unseen_codes(const AttnArgs& a, const Segm
   tc::fence_proxy_async_smem();
   __syncwarp();
 }
+
+// Bits i = 0 .. 31 with from <= i < to.
+__device__ __forceinline__ uint32_t bits32(int from, int to) {
+  const uint32_t below = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
+  return from >= 32 ? 0u : from <= 0 ? below : below & (~0u << from);
+}
+// The largest of the lanes' values (NaN where all are).
+__device__ __forceinline__ float warp_max_f32(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A whole warp waits, as Waiter does, in fewer instructions: the limit begins with the first look that fails.
+struct ShortWaiter {
+  volatile int* abort;
+  long long cycles;
+  __device__ __forceinline__ bool operator()(const uint64_t* bar, uint32_t parity) const {
+    const uint32_t b = tc::smem_u32(bar);
+    bool ok = true;
+    long long deadline = 0;
+    while (!tc::mbar_try_wait_suspend(b, parity, 20000u)) {
+      const long long now = clock64();
+      if (deadline == 0) deadline = now + cycles;
+      if (*abort || now > deadline) {
+        ok = false;
+        break;
+      }
+    }
+    return __all_sync(~0u, ok);
+  }
+};
+__device__ __forceinline__ long long cycles_of(uint64_t ns) { return tc::deadline_after_ns(ns) - clock64(); }
 
 // Issue a tile's loads: the codes, and for K (`scales` given) the exponent bytes of K and V with them.
 template <int D>
@@ -165,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(tc::smem_u32(&sh->group[lane]), 4);
       sh->need[lane][0] = sh->need[lane][1] = 0;
     }
+    for (int i = lane; i < Sh::kRows; i += 32) sh->zeros[i] = 0.f;
     if (lane == 0) sh->abort = 0, plan.bad = 0, plan.n_long = 0;
     tc::fence_mbar_init();
   }
@@ -196,35 +239,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n_put = 0, n_k = 0;
     int4 info = make_int4(0, 0, 0, 0);
     Cursor cur(sh->start[set], a.tokens);
-    struct Ahead {
-      TileLoad t;
-      bool there;
-    };
-    auto fetch = [&]() {  // the next tile's pages
-      Ahead f = {};
-      f.there = cur.next(a);
-      if (!f.there) return f;
-      const Segment& s = cur.s;
-      f.t = tile_load(a, s, cur.j, lane);
-      if (cur.first() && s.tile0 == 0 && s.n < s.u.ntiles)
-        info = make_int4(1 + cut.ranges(range + 1, uint32_t(s.u.ntiles - s.n)), s.row0, s.ntok, s.h);
-      return f;
-    };
-    auto put = [&](const CUtensorMap* map, const Ahead& f) {
+    auto put = [&](const CUtensorMap* map, const TileLoad& t) {
       if (!wait(&sh->empty[set][ring.slot], ring.phase ^ 1)) return false;
-      issue_codes<D>(a, map, f.t, tc::smem_u32(ring_mem + ring.slot * C::kSlotBytes),
-                     tc::smem_u32(&sh->full[set][ring.slot]), stream, lane);
+      issue_codes<D>(a, map, t, tc::smem_u32(ring_mem + ring.slot * C::kSlotBytes), tc::smem_u32(&sh->full[set][ring.slot]),
+                     stream, lane);
       ++n_put;
       ring.step();
       return true;
     };
-    auto put_k = [&](const Ahead& f) {
-      if (!put(&map_k, f)) return false;
-      const int b = n_k++ % Sh::kScales;
-      issue_scales(args, f.t, sh->scales[set][b], tc::smem_u32(&sh->sc_full[set][b]), lane);
-      return true;
+    // The order of the loads: K 0, K 1, V 0, K 2, V 1 and so on.  The tiles' pages are looked up three tiles before they are
+    // wanted.  Each step stands here once: the role's code has to stay in the instruction cache beside the others'.
+    struct Ahead {
+      TileLoad t;
+      bool there;
     };
-    const bool ok = load_in_order(fetch, put_k, [&](const Ahead& f) { return put(&map_v, f); });
+    Ahead before = {}, now = {}, next = {}, last = {};  // V, K, and two tiles ahead
+    bool ok = true;
+    for (int i = -3; ok; ++i) {
+      if (i >= 0) {
+        const int n = (now.there ? 1 : 0) | (before.there ? 2 : 0);
+        if (n == 0) break;
+#pragma unroll 1
+        for (int what = 0; ok && what < 2; ++what)
+          if (n >> what & 1) ok = put(what ? &map_v : &map_k, what ? before.t : now.t);
+        if (ok && now.there) {
+          const int b = n_k++ % Sh::kScales;
+          issue_scales(args, now.t, sh->scales[set][b], tc::smem_u32(&sh->sc_full[set][b]), lane);
+        }
+      }
+      before = now, now = next, next = last;
+      last.there = cur.next(a);
+      if (last.there) {
+        const Segment& s = cur.s;
+        last.t = tile_load(a, s, cur.j, lane);
+        if (cur.first() && s.tile0 == 0 && s.n < s.u.ntiles)
+          info = make_int4(1 + cut.ranges(range + 1, uint32_t(s.u.ntiles - s.n)), s.row0, s.ntok, s.h);
+      }
+    }
     if (!ok) {
       sh->abort = 1;
       if (lane == 0) note_timeout(a.status, a.diag, 1u, uint32_t(n_put));
@@ -239,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_s = tc::idesc_e4m3_f32(kTile, R);
     constexpr uint32_t idesc_o = tc::idesc_e4m3_f32(128, 2 * R) | tc::kIdescAMajorMN | tc::kIdescBMajorMN;
     const int set = warp - kMmaWarp;
-    const Waiter wait{&sh->abort, a.timeout_ns};
+    const ShortWaiter wait{&sh->abort, cycles_of(a.timeout_ns)};
     uint8_t* ring_mem = sRing + set * C::kSlots * C::kSlotBytes;
     const uint32_t t_s = tmem + set * 4 * R, t_o = t_s + 2 * R;
     const uint64_t dk = tc::sdesc_kmajor<D>(tc::smem_u32(ring_mem));
@@ -274,38 +325,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (last) ++n_seg;
       return true;
     };
-    bool more = kc.next(a);
-    bool ok = !more || s_product();
-    if (ok && more) {
-      more = kc.next(a);
-      ok = !more || s_product();
-    }
-    for (; ok && vc.next(a); ++t) {
-      const bool first = vc.first(), last = vc.last();
-      ok = wait(&sh->full[set][ring.slot], ring.phase);
-      if (!ok) break;
-      if (first) whole_tiles(a, vc.s, vc.s.u.p1, vc.s.u.p0, j0, j1);
-      // while the softmax works on this tile
-      if (vc.j < j0 || vc.j >= j1) clear_unseen_codes<D>(a, vc.s, vc.j, ring_mem + ring.slot * C::kSlotBytes, lane);
-      ok = wait(&sh->p_full[set], t & 1);
-      if (ok && first) ok = wait(&sh->o_read[set], (units++ & 1) ^ 1);  // the unit before has been read
-      if (!ok) break;
-      tc::tc_fence_after();
-      const uint64_t dv_t = dv + uint32_t(ring.slot * (C::kSlotBytes >> 4));
-      if (tc::elect_one()) {
+    bool ok = true, more = true;
+    for (t = -2; ok; ++t) {  // O^T of tile t, then S^T of tile t + 2
+      if (t >= 0) {
+        if (!vc.next(a)) break;
+        const bool first = vc.first(), last = vc.last();
+        ok = wait(&sh->full[set][ring.slot], ring.phase);
+        if (!ok) break;
+        if (first) whole_tiles(a, vc.s, vc.s.u.p1, vc.s.u.p0, j0, j1);
+        // while the softmax works on this tile
+        if (vc.j < j0 || vc.j >= j1) clear_unseen_codes<D>(a, vc.s, vc.j, ring_mem + ring.slot * C::kSlotBytes, lane);
+        ok = wait(&sh->p_full[set], t & 1);
+        if (ok && first) ok = wait(&sh->o_read[set], (units++ & 1) ^ 1);  // the unit before has been read
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t dv_t = dv + uint32_t(ring.slot * (C::kSlotBytes >> 4));
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int i = 0; i < kTile / 32; ++i)
-          tc::mma_f8(t_o, dv_t + ((i * 32 * D) >> 4), dp + ((i * 32 * C::kPPitch) >> 4), idesc_o, !first || i != 0);
-        tc::mma_commit(tc::smem_u32(&sh->p_empty[set]));
-        tc::mma_commit(tc::smem_u32(&sh->empty[set][ring.slot]));
-        if (last) tc::mma_commit(tc::smem_u32(&sh->o_full[set]));
+          for (int i = 0; i < kTile / 32; ++i)
+            tc::mma_f8(t_o, dv_t + ((i * 32 * D) >> 4), dp + ((i * 32 * C::kPPitch) >> 4), idesc_o, !first || i != 0);
+          tc::mma_commit(tc::smem_u32(&sh->p_empty[set]));
+          tc::mma_commit(tc::smem_u32(&sh->empty[set][ring.slot]));
+          if (last) tc::mma_commit(tc::smem_u32(&sh->o_full[set]));
+        }
+        __syncwarp();
+        ring.step();
       }
-      __syncwarp();
-      ring.step();
-      if (more) {
-        more = kc.next(a);
-        ok = !more || s_product();
-      }
+      more = more && kc.next(a);
+      if (more) ok = s_product();
     }
     if (!ok) {
       sh->abort = 1;
@@ -315,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kSplitWarp) {
     // ---------------------------------------------------------------- Q into two parts of e4m3
     const int set = (warp - kSplitWarp) / C::kSplitWarps, w = (warp - kSplitWarp) % C::kSplitWarps;
-    const Waiter wait{&sh->abort, a.timeout_ns};
+    const ShortWaiter wait{&sh->abort, cycles_of(a.timeout_ns)};
     constexpr int kLanes = D / 16, kPass = 32 / kLanes * C::kSplitWarps;  // threads to a row, rows at a time
     const int piece = lane % kLanes;
     int n_seg = 0;
@@ -374,16 +421,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kTmaWarp) {
     // ------------------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const Waiter wait{&sh->abort, a.timeout_ns};
+    const ShortWaiter wait{&sh->abort, cycles_of(a.timeout_ns)};
     const int grp = warp >> 2, w4 = warp & 3;
     const int kv = w4 * 32 + lane;  // this thread's slot of each tile = TMEM lane
     const int set = grp % kSets, row0 = grp / kSets * RW;  // and its rows
     const uint32_t t_s = tmem + (uint32_t(w4 * 32) << 16) + set * 4 * R + row0, t_o = t_s + 2 * R;
-    float* ref = sh->ref[set] + row0;
+    float* neg_ref = sh->neg_ref[set] + row0;
     // a slot's row of P: its R first parts, then its second parts (R = 128: in a chunk of their own)
     uint8_t* p_mem = sP + set * C::kPBytes;
-    // the row that this lane holds after a fold (the lanes of a row hold the same)
-    const int fold_row = lane / (32 / RW);
+    // the rows that this lane holds after a fold, of 32 rows or all of them at a time (the lanes of a row hold the same)
+    constexpr int kFolds = RW > 32 ? RW / 32 : 1, kFold = RW / kFolds;
+    const int fold_row = lane / (32 / kFold);
+    float* row_by = sh->row_by[set] + row0;
     int t = 0, sync = 0, units = 0;
     bool ok = true;
     Walk walk(sh->start[set], a.tokens);
@@ -404,132 +453,141 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* factor = sh->row_factor[set][units % kQRing] + row0;
       ok = wait(&sh->q_ready[set][units % kQRing], (units / kQRing) & 1);
       if (!ok) break;
-      int f = 0;  // the reference of V's powers of two, as an exponent byte
+      int f = 1;  // the reference of V's powers of two, as an exponent byte
       float l[RW];  // this slot's share of the rows' sums
 #pragma unroll
       for (int i = 0; i < RW; ++i) l[i] = 0.f;
       for (int j = 0; j < s.n; ++j, ++t) {
         const bool inside = j >= j_in0 && j < j_in1;
-        int from = 0, to = R;  // the rows that see this thread's slot
+        int from = 0, to = RW;  // the rows of this thread's that see its slot
         if (!inside) {
           // the token at p0 + tok sees the slot from tok = pos - p0 on, for `window` tokens, a sink always.  Rows behind the
           // unit's see nothing here: a slot for them alone holds whatever was there, and may not set V's reference
           const int v = (s.tile0 + j) * per_tile + (kv >> a.block_shift);
           const int pos = block_pos(a, s.u, v) + (kv & ((1 << a.block_shift) - 1));
           const int d = pos - s.u.p0;
-          from = d <= 0 ? 0 : d >= a.tokens ? R : d * a.g;
+          from = d <= 0 ? 0 : min(d, a.tokens) * a.g;
           to = s.ntok * a.g;
-          if (a.window && pos >= a.n_sink) to = d + a.window <= 0 ? 0 : d + a.window >= s.ntok ? to : (d + a.window) * a.g;
+          if (a.window && pos >= a.n_sink) to = min(max(d + a.window, 0), s.ntok) * a.g;
+          from = max(from - row0, 0), to = min(to - row0, RW);
         }
+        const bool seen = from < to;
         ok = wait(&sh->sc_full[set][t % Sh::kScales], (t / Sh::kScales) & 1);
         if (!ok) break;
         const uint32_t bytes = sh->scales[set][t % Sh::kScales][kv];
-        const float kf = kv8::factor(bytes & 0xFFu);
+        // a V of NaN makes the rows that see it NaN by way of their scores: a weight of 0 would not do
+        const bool v_nan = bytes >> 8 == kv8::kNan;
+        const float kf = kv8::factor(v_nan ? kv8::kNan : bytes & 0xFFu);
         const unsigned long long kk = pack_f32x2(kf, kf);
-        // V's: a slot that no row sees counts for nothing, a NaN has no power
-        const int v_byte = from >= to || bytes >> 8 == kv8::kNan ? 0 : max(1, int(bytes >> 8));
+        const int v_byte = seen && !v_nan ? max(1, int(bytes >> 8)) : 0;  // a slot that no row sees counts for nothing
         ok = wait(&sh->s_full[set][t & 1], (t >> 1) & 1);
         if (!ok) break;
         tc::tc_fence_after();
         float y[RW];  // the only array beside l: what is needed once more is loaded once more (S is there until P is)
-        auto load_scores = [&]() {
+        // Steps: 0 a tile under the references as they stand; 1 new references are set; 2 the tile under those.  They are
+        // rounds of one loop because the code of a tile has to stay in the instruction cache.
+        for (int step = j == 0 ? 1 : 0;; ) {
+          const float* minus = step == 1 ? sh->zeros : neg_ref;
           tc::tmem_ld<RW>(t_s + (t & 1) * R, y);
           tc::tmem_ld_wait();
-        };
-        auto hide = [&](float with) {
-          if (!inside) {
-#pragma unroll
-            for (int i = 0; i < RW; ++i)
-              if (row0 + i < from || row0 + i >= to) y[i] = with;
-          }
-        };
-        auto refer = [&]() {  // scores to exponents; the largest
 #pragma unroll
           for (int i = 0; i < RW; i += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(ref + i), c = *reinterpret_cast<const float4*>(factor + i);
-            unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(y[i], y[i + 1]), kk), pack_f32x2(c.x, c.y), pack_f32x2(-m.x, -m.y)), y[i], y[i + 1]);
-            unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(y[i + 2], y[i + 3]), kk), pack_f32x2(c.z, c.w), pack_f32x2(-m.z, -m.w)), y[i + 2], y[i + 3]);
+            const float4 m = *reinterpret_cast<const float4*>(minus + i), c = *reinterpret_cast<const float4*>(factor + i);
+            unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(y[i], y[i + 1]), kk), pack_f32x2(c.x, c.y), pack_f32x2(m.x, m.y)), y[i], y[i + 1]);
+            unpack_f32x2(fma_f32x2(mul_f32x2(pack_f32x2(y[i + 2], y[i + 3]), kk), pack_f32x2(c.z, c.w), pack_f32x2(m.z, m.w)), y[i + 2], y[i + 3]);
           }
-          hide(-INFINITY);
-          float top = -INFINITY;
+          if (__builtin_expect(!inside, 0)) {
 #pragma unroll
-          for (int i = 0; i < RW; i += 4) top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
-          return top;
-        };
-        auto weigh = [&]() {
+            for (int k = 0; k < RW; k += 32) {
+              const uint32_t see = bits32(from - k, to - k);
 #pragma unroll
-          for (int i = 0; i < RW; ++i) y[i] = tc::ex2_approx(y[i]);
-        };
-        load_scores();
-        bool fresh = j == 0;  // new references are needed
-        if (j > 0) {
-          const float top = refer() + float(max(0, v_byte - f));
-          const int at = sync & 1;
-          if (__any_sync(~0u, top > kMost) && lane == 0) sh->need[grp][at] = t + 1;
-          arrive();
-          weigh();  // while the others arrive; done again where a reference moves
-          ok = wait(&sh->group[grp], sync++ & 1);
-          if (!ok) break;
-          fresh = sh->need[grp][at] == t + 1;
-          if (fresh) load_scores();
-        }
-        if (fresh) {
-          // each row's maximum over the tile's 128 slots, by warp then over the group's warps
-#pragma unroll
-          for (int i = 0; i < RW; i += 4) {
-            const float4 c = *reinterpret_cast<const float4*>(factor + i);
-            y[i] *= kf * c.x, y[i + 1] *= kf * c.y, y[i + 2] *= kf * c.z, y[i + 3] *= kf * c.w;
-          }
-          hide(-INFINITY);
-          const float mine = fold_lanes<RW, true>(y, lane);
-          const float old = j == 0 ? kUnset : ref[fold_row];
-          const int my_byte = __reduce_max_sync(~0u, v_byte);
-          sh->warp_max[grp][w4][fold_row] = mine;
-          if (lane == 0) sh->warp_byte[grp][w4] = my_byte;
-          ok = meet();
-          if (!ok) break;
-          const float (*part)[RW] = sh->warp_max[grp];
-          const float m = fmaxf(old, fmaxf(fmaxf(part[0][fold_row], part[1][fold_row]),
-                                           fmaxf(part[2][fold_row], part[3][fold_row])) - kTop);
-          const int* byte = sh->warp_byte[grp];
-          const int f_old = f;
-          // f may fall, too: O^T keeps its place in fp32, and this tile's weights theirs in e4m3
-          f = max(max(max(byte[0], byte[1]), max(byte[2], byte[3])), max(f - 40, 1));
-          ref[fold_row] = m;  // the four warps write the same values
-          __syncwarp();
-          if (j > 0) {
-            // the sums so far and this thread's lane of O^T, after the last product
-            ok = wait(&sh->p_empty[set], (t - 1) & 1);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const float alpha = tc::ex2_approx(old - m), fewer = tc::ex2_approx(float(f_old - f));
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              tc::tmem_ld<RW>(t_o + part * R, y);
-              tc::tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < RW; ++i) {
-                const float al = __shfl_sync(~0u, alpha, i * (32 / RW));
-                if (part == 0) l[i] *= al;
-                y[i] *= al * fewer;
-              }
-              tc::tmem_st<RW>(t_o + part * R, y);
+              for (int i = k; i < k + 32 && i < RW; ++i)
+                if (!(see >> (i - k) & 1u)) y[i] = -INFINITY;
             }
-            tc::tmem_st_wait();
           }
-          load_scores();
-          refer();
-          weigh();
+          if (__builtin_expect(step == 1, 0)) {
+            // each row's maximum over the tile's 128 slots, by warp then over the group's warps; lane i has row i, and 32 + i
+#pragma unroll
+            for (int k = 0; k < kFolds; ++k) {
+              float mine = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < kFold; ++i) {
+                const float top = warp_max_f32(y[k * 32 + i]);
+                if (lane == i) mine = top;
+              }
+              if (lane < kFold) sh->warp_max[grp][w4][k * 32 + lane] = mine;
+            }
+            const int my_byte = __reduce_max_sync(~0u, v_byte);
+            if (lane == 0) sh->warp_byte[grp][w4] = my_byte;
+            ok = meet();
+            if (!ok) break;
+            const float (*part)[RW] = sh->warp_max[grp];
+            const int* byte = sh->warp_byte[grp];
+            const int f_old = f;
+            // f may fall, too: O^T keeps its place in fp32, and this tile's weights theirs in e4m3
+            f = max(max(max(byte[0], byte[1]), max(byte[2], byte[3])), max(f - 40, 1));
+            for (int row = lane; row < RW; row += 32) {  // the four warps write the same values
+              const float old = j == 0 ? kUnset : -neg_ref[row];
+              const float m = fmaxf(old, fmaxf(fmaxf(part[0][row], part[1][row]), fmaxf(part[2][row], part[3][row])) - kTop);
+              row_by[row] = tc::ex2_approx(old - m);
+              sh->next_ref[grp][w4][row] = -m;
+            }
+            ok = meet();  // every warp has read the old references
+            if (!ok) break;
+            for (int row = lane; row < RW; row += 32) neg_ref[row] = sh->next_ref[grp][w4][row];
+            __syncwarp();
+            if (j > 0) {
+              // the sums so far and this thread's lane of O^T, after the last product
+              ok = wait(&sh->p_empty[set], (t - 1) & 1);
+              if (!ok) break;
+              tc::tc_fence_after();
+              const float fewer = tc::ex2_approx(float(f_old - f));
+#pragma unroll
+              for (int i = 0; i < RW; i += 4) {
+                const float4 by = *reinterpret_cast<const float4*>(row_by + i);
+                l[i] *= by.x, l[i + 1] *= by.y, l[i + 2] *= by.z, l[i + 3] *= by.w;
+              }
+#pragma unroll 1
+              for (int i = 0; i < 2 * RW; i += 8) {
+                const int col = i < RW ? i : R + i - RW;
+                const float* by = row_by + (i < RW ? i : i - RW);
+                float o[8];
+                tc::tmem_ld<8>(t_o + col, o);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] *= by[k] * fewer;
+                tc::tmem_st<8>(t_o + col, o);
+              }
+              tc::tmem_st_wait();
+            }
+            step = 2;
+            continue;
+          }
+          const int at = sync & 1;
+          if (step == 0) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < RW; i += 4) top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
+            if (__any_sync(~0u, top + float(max(0, v_byte - f)) > kMost) && lane == 0) sh->need[grp][at] = t + 1;
+            arrive();
+          }
+#pragma unroll
+          for (int i = 0; i < RW; ++i) y[i] = tc::ex2_approx(y[i]);  // while the others arrive; done again where a reference moves
+          if (step == 2) break;
+          ok = wait(&sh->group[grp], sync++ & 1);
+          if (!ok || sh->need[grp][at] != t + 1) break;
+          step = 1;
         }
-        // 2^(ev - f); NaN where V is NaN to the rows that see it
-        const float vf = from < to && bytes >> 8 == kv8::kNan ? kv8::factor(kv8::kNan) : kv8::power(max(v_byte - f, -126));
+        if (!ok) break;
+        const float vf = kv8::power(max(v_byte - f, -126));  // 2^(ev - f)
         const unsigned long long vv = pack_f32x2(vf, vf);
-#pragma unroll
-        for (int i = 0; i < RW; i += 2) l[i] += y[i], l[i + 1] += y[i + 1];
-#pragma unroll
-        for (int i = 0; i < RW; i += 2) unpack_f32x2(mul_f32x2(pack_f32x2(y[i], y[i + 1]), vv), y[i], y[i + 1]);
-        if (vf != vf) hide(0.f);
         uint32_t hi[RW / 4], lo[RW / 4];
+#pragma unroll
+        for (int i = 0; i < RW; i += 2) {
+          const unsigned long long p2 = pack_f32x2(y[i], y[i + 1]);
+          unpack_f32x2(add_f32x2(pack_f32x2(l[i], l[i + 1]), p2), l[i], l[i + 1]);
+          unpack_f32x2(mul_f32x2(p2, vv), y[i], y[i + 1]);
+        }
 #pragma unroll
         for (int i = 0; i < RW / 4; ++i) {
           uint32_t h[2], r[2];
@@ -542,14 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto put_p = [&](const uint32_t* w, int at) {  // at byte `at` of the slot's row
           uint8_t* dst = p_mem + (at / C::kPPitch) * (kTile * C::kPPitch);
           const int in = at % C::kPPitch;
-          if constexpr (RW == 8) {
-            *reinterpret_cast<uint2*>(dst + tc::swizzled<C::kPPitch>(kv, in / 16) + in % 16) = make_uint2(w[0], w[1]);
-          } else {
 #pragma unroll
-            for (int i = 0; i < RW / 16; ++i)
-              *reinterpret_cast<uint4*>(dst + tc::swizzled<C::kPPitch>(kv, in / 16 + i)) =
-                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-          }
+          for (int i = 0; i < RW / 16; ++i)
+            *reinterpret_cast<uint4*>(dst + tc::swizzled<C::kPPitch>(kv, in / 16 + i)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         };
         put_p(hi, row0);
         put_p(lo, R + row0);
@@ -561,61 +615,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // ---------------------------------------------------------------- the unit's rows
       // rows' sums over the 128 slots: lanes, then the group's warps in order
-      const float mine = fold_lanes<RW, false>(l, lane);
-      sh->warp_sum[grp][w4][fold_row] = mine;
+#pragma unroll
+      for (int k = 0; k < kFolds; ++k) sh->warp_sum[grp][w4][k * 32 + fold_row] = fold_lanes<kFold, false>(l + k * 32, lane);
       ok = meet();
       if (!ok) break;
       const float (*part)[RW] = sh->warp_sum[grp];
-      const float sum = (part[0][fold_row] + part[1][fold_row]) + (part[2][fold_row] + part[3][fold_row]);
-      // NaN stays NaN, in the log-sum-exp too
-      const float inv = sum == 0.f ? 0.f : 1.f / sum, of = kv8::power(f - 127);
+      const float of = kv8::power(f - 127);
       const bool partial = s.n < s.u.ntiles;
       const int64_t pbase = (int64_t(2) * (blockIdx.x + set * gridDim.x) + (s.tile0 > 0 ? 0 : 1)) * R + row0;
       const int n_rows = s.ntok * a.g - row0;  // of this group's
-      if (w4 == 0 && fold_row * (32 / RW) == lane && fold_row < n_rows) {
-        const float lse2 = sum == 0.f ? -INFINITY : ref[fold_row] + log2f(sum);
-        const int row = row0 + fold_row;
-        if (partial)
-          a.plse[pbase + fold_row] = lse2;
-        else if (a.lse)
-          a.lse[int64_t(s.row0 + row / a.g) * a.Hq + s.h * a.g + row % a.g] = lse2 * kLn2;
+      for (int mine = lane; mine < RW; mine += 32) {  // the four warps write the same values
+        const int row = row0 + mine;
+        const float sum = (part[0][mine] + part[1][mine]) + (part[2][mine] + part[3][mine]);
+        row_by[mine] = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN, in the log-sum-exp too
+        if (w4 == 0 && mine < n_rows) {
+          const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - neg_ref[mine];
+          if (partial)
+            a.plse[pbase + mine] = lse2;
+          else if (a.lse)
+            a.lse[int64_t(s.row0 + row / a.g) * a.Hq + s.h * a.g + row % a.g] = lse2 * kLn2;
+        }
       }
+      __syncwarp();
       ok = wait(&sh->o_full[set], units++ & 1);
       if (!ok) break;
       tc::tc_fence_after();
-      float o[RW];
-      tc::tmem_ld<RW>(t_o + R, o);
-      tc::tmem_ld_wait();
+      const int tok = row0 / a.g;
+      int hh = row0 - tok * a.g;
+      __nv_bfloat16* dst = a.out + (int64_t(s.row0 + tok) * a.Hq + s.h * a.g + hh) * D + kv;
+      const int64_t wrap = int64_t(a.Hq - a.g) * D;  // from a token's last head to the next token's first
+      float* pdst = a.partial + pbase * D + kv;
+#pragma unroll 1
+      for (int i = 0; i < RW; i += 8) {
+        float o[8], o2[8];
+        tc::tmem_ld<8>(t_o + i, o);
+        tc::tmem_ld<8>(t_o + R + i, o2);
+        tc::tmem_ld_wait();
+        if (kv >= D) continue;  // TMEM lane = lane of the head; lanes from D on hold nothing
 #pragma unroll
-      for (int i = 0; i < RW; ++i) l[i] = o[i];
-      tc::tmem_ld<RW>(t_o, o);
-      tc::tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < RW; ++i) o[i] = fmaf(l[i], 1.f / 16, o[i]);
+        for (int k = 0; k < 8; ++k) {
+          const float x = fmaf(o2[k], 1.f / 16, o[k]) * row_by[i + k] * of;
+          if (i + k >= n_rows) continue;
+          if (partial)
+            pdst[(i + k) * D] = x;
+          else
+            *dst = __float2bfloat16(x);
+          dst += D;
+          if (++hh == a.g) hh = 0, dst += wrap;
+        }
+      }
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh->o_read[set]));  // the next unit may overwrite it
-      if (kv < D) {  // TMEM lane = lane of the head; lanes from D on hold nothing
-#pragma unroll
-        for (int i = 0; i < RW; ++i) o[i] = o[i] * __shfl_sync(~0u, inv, i * (32 / RW)) * of;
-        if (partial) {
-          float* dst = a.partial + pbase * D + kv;
-#pragma unroll
-          for (int i = 0; i < RW; ++i)
-            if (i < n_rows) dst[i * D] = o[i];
-        } else {
-          const int tok = row0 / a.g;
-          int hh = row0 - tok * a.g;
-          __nv_bfloat16* dst = a.out + (int64_t(s.row0 + tok) * a.Hq + s.h * a.g + hh) * D + kv;
-          const int64_t wrap = int64_t(a.Hq - a.g) * D;  // from a token's last head to the next token's first
-#pragma unroll
-          for (int i = 0; i < RW; ++i) {
-            if (i < n_rows) *dst = __float2bfloat16(o[i]);
-            dst += D;
-            if (++hh == a.g) hh = 0, dst += wrap;
-          }
-        }
-      }
     }
     if (!ok) {
       sh->abort = 1;
