@@ -24,10 +24,10 @@ using namespace attn;
 
 // Eight softmax warps in two groups of four, one for each pipeline (R = 128: half the rows of the lone one each).  Then a
 // TMA warp for each pipeline, an MMA warp for each, and four warps that split Q (all four for a lone pipeline).
-constexpr int kGroups = 2, kThreads = (kGroups + 2) * 128;
+constexpr int kGroups = 4, kThreads = (kGroups + 2) * 128;
 constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 2, kSplitWarp = kMmaWarp + 2;
 // Registers: launched with 512 x 128; the softmax warps take what the others give back (256 x 184 + 256 x 72 = 512 x 128).
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
 #ifndef KV8_SLOTS
 #define KV8_SLOTS 8
 #endif
@@ -600,10 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto put_p = [&](const uint32_t* w, int at) {  // at byte `at` of the slot's row
           uint8_t* dst = p_mem + (at / C::kPPitch) * (kTile * C::kPPitch);
           const int in = at % C::kPPitch;
+          if constexpr (RW == 8) {
+            *reinterpret_cast<uint2*>(dst + tc::swizzled<C::kPPitch>(kv, in / 16) + in % 16) = make_uint2(w[0], w[1]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < RW / 16; ++i)
-            *reinterpret_cast<uint4*>(dst + tc::swizzled<C::kPPitch>(kv, in / 16 + i)) =
-                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            for (int i = 0; i < RW / 16; ++i)
+              *reinterpret_cast<uint4*>(dst + tc::swizzled<C::kPPitch>(kv, in / 16 + i)) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
         };
         put_p(hi, row0);
         put_p(lo, R + row0);
