@@ -22,10 +22,10 @@ namespace {
 
 using namespace attn;
 
-// Eight softmax warps in two groups of four, one for each pipeline (R = 128: half the rows of the lone one each).  Then a
-// TMA warp for each pipeline, an MMA warp for each, and four warps that split Q (all four for a lone pipeline).
+// Sixteen softmax warps in groups of four; a group takes a share of the rows of its pipeline's tiles.  Then for each pipeline a
+// warp that loads K, one that issues the products and one that loads V, and two warps that split Q (both for a lone pipeline).
 constexpr int kGroups = 4, kThreads = (kGroups + 2) * 128;
-constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 2, kSplitWarp = kMmaWarp + 2;
+constexpr int kKWarp = 4 * kGroups, kMmaWarp = kKWarp + 2, kVWarp = kMmaWarp + 2, kSplitWarp = kVWarp + 2;
 // Registers: launched with 512 x 128; the softmax warps take what the others give back (256 x 184 + 256 x 72 = 512 x 128).
 constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
 #ifndef KV8_SLOTS
@@ -55,15 +55,14 @@ struct Shared {
   uint32_t tmem_base;
   volatile int abort;
   int pending[kSets];          // the MMA warp has issued something
-  int n_put[kSets], n_k[kSets];  // copies issued: tiles, exponent bytes
   int need[kGroups][2];        // [parity]: the last tile at which a warp asked for new references
   Start start[kSets];
   int warp_byte[kGroups][4];   // by warp: the largest exponent byte of V in a tile
   float warp_max[kGroups][4][kRows], warp_sum[kGroups][4][kRows];  // by warp: the rows' maxima of a tile, sums of a unit
   alignas(16) float neg_ref[kSets][R];         // the rows' references, negated; read four at a time
   alignas(16) float row_by[kSets][R];          // what a row's sums, and its output, are to be multiplied by
+  alignas(16) int row_at[kSets][R];            // where a row's output lies behind the unit's first; -1: nowhere
   alignas(16) float zeros[kRows];
-  float next_ref[kGroups][4][kRows];
   alignas(16) float row_factor[kSets][kQRing][R];  // 2^eq c
   alignas(16) uint16_t scales[kSets][kScales][kTile];
 };
@@ -71,7 +70,7 @@ struct Shared {
 template <int D, int R>
 struct Cfg {
   static constexpr int kSets = sets_of(D, R), kRowGroups = kGroups / kSets;
-  static constexpr int kSplitWarps = 4 / kSets;              // of a pipeline
+  static constexpr int kSplitWarps = 2 / kSets;              // of a pipeline
   static constexpr int kSlotBytes = kTile * D;               // a tile of codes: rows of D bytes, D-byte swizzled
   static constexpr int kQPart = R * D, kQBytes = 2 * kQPart;
   static constexpr int kPPitch = R < 64 ? R * 2 : 128;       // bytes of a slot's row of P, R > 64: in two chunks
@@ -130,38 +129,60 @@ struct ShortWaiter {
     }
     return __all_sync(~0u, ok);
   }
+  // Two barriers at once: a wait that finds its phase complete takes some 200 cycles all the same.
+  __device__ __forceinline__ bool both(const uint64_t* bar, uint32_t parity, const uint64_t* bar2, uint32_t parity2) const {
+    const uint32_t b = tc::smem_u32(bar), b2 = tc::smem_u32(bar2);
+    bool ok = true;
+    long long deadline = 0;
+    while (!(tc::mbar_try_wait_suspend(b, parity, 20000u) & tc::mbar_try_wait_suspend(b2, parity2, 20000u))) {
+      const long long now = clock64();
+      if (deadline == 0) deadline = now + cycles;
+      if (*abort || now > deadline) {
+        ok = false;
+        break;
+      }
+    }
+    return __all_sync(~0u, ok);
+  }
 };
 __device__ __forceinline__ long long cycles_of(uint64_t ns) { return tc::deadline_after_ns(ns) - clock64(); }
 
-// Issue a tile's loads: the codes, and for K (`scales` given) the exponent bytes of K and V with them.
+// The place of tile i's load in the ring's order, which is that of the products: K 0, K 1, V 0, K 2, V 1 and so on.
+__device__ __forceinline__ uint32_t ring_place(bool v, uint32_t i, uint32_t n_tiles) {
+  return v ? min(2 * i + 2, n_tiles + i) : i < 2 ? i : 2 * i - 1;
+}
+
+// Issue a tile's loads of codes.  One lane issues them all: issued by the blocks' own lanes, a load takes some 180 cycles.
 template <int D>
 __device__ __forceinline__ void issue_codes(const AttnArgs& a, const CUtensorMap* map, const TileLoad& t, uint32_t dst,
                                             uint32_t bar, uint64_t policy, int lane) {
   const int block_bytes = D << a.block_shift;
-  if (lane == 0) tc::mbar_arrive_expect_tx(bar, uint32_t(t.n_blocks * block_bytes));
-  __syncwarp();
-  if (lane >= t.n_blocks) return;
   int page = t.page;
-  if (page < 0 || page >= a.n_pages) {
+  if (lane < t.n_blocks && (page < 0 || page >= a.n_pages)) {
     set_status(a.status, DSPARK_EINVAL);
     page = a.n_pages;  // outside the tensor: reads as zeros
   }
-  tc::tma_load_4d(dst + lane * block_bytes, map, bar, 0, t.slot, t.head, page, policy);
+  const int head = __shfl_sync(~0u, t.head, 0), n = __shfl_sync(~0u, t.n_blocks, 0);
+  if (lane == 0) tc::mbar_arrive_expect_tx(bar, uint32_t(n * block_bytes));
+  __syncwarp();
+  for (int i = 0; i < n; ++i) {
+    const int to = __shfl_sync(~0u, page, i), slot = __shfl_sync(~0u, t.slot, i);
+    if (tc::elect_one()) tc::tma_load_4d(dst + i * block_bytes, map, bar, 0, slot, head, to, policy);
+    __syncwarp();
+  }
 }
+// The exponent bytes of a tile's slots, four slots to a lane; zeros of any power of two where there is no page.  Every lane
+// arrives at `bar` when its own are there.
 __device__ __forceinline__ void issue_scales(const Attn8Args& p, const TileLoad& t, uint16_t* dst, uint32_t bar, int lane) {
   const AttnArgs& a = p.a;
-  const bool mine = lane < t.n_blocks, good = mine && t.page >= 0 && t.page < a.n_pages;
-  const uint32_t n_good = __popc(__ballot_sync(~0u, good)), bytes = 2u << a.block_shift;
-  uint16_t* to = dst + (lane << a.block_shift);
-  if (mine && !good)  // zeros of any power of two
-    for (int i = 0; i < 1 << a.block_shift; ++i) to[i] = 0x7F7F;
-  __syncwarp();
-  if (lane == 0) tc::mbar_arrive_expect_tx(bar, n_good * bytes);
-  __syncwarp();
-  if (good) {
-    const int64_t slot = ((int64_t(t.page) * a.Hkv + t.head) << a.page_shift) + t.slot;
-    tc::bulk_load(tc::smem_u32(to), p.kv_scale + 2 * slot, bytes, bar);
-  }
+  const int block = (lane * 4) >> a.block_shift, in = (lane * 4) & ((1 << a.block_shift) - 1);
+  const int page = __shfl_sync(~0u, t.page, block), slot = __shfl_sync(~0u, t.slot, block) + in;
+  uint16_t* to = dst + lane * 4;
+  if (block < t.n_blocks && page >= 0 && page < a.n_pages)
+    tc::async_copy_8(tc::smem_u32(to), p.kv_scale + 2 * (((int64_t(page) * a.Hkv + t.head) << a.page_shift) + slot));
+  else
+    *reinterpret_cast<uint2*>(to) = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  tc::async_copies_arrive(bar);
 }
 
 template <int D, int R>
@@ -192,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_init(tc::smem_u32(&sh->full[z][lane]), 1);
         tc::mbar_init(tc::smem_u32(&sh->empty[z][lane]), 1);
       }
-      if (lane < Sh::kScales) tc::mbar_init(tc::smem_u32(&sh->sc_full[z][lane]), 1);
+      if (lane < Sh::kScales) tc::mbar_init(tc::smem_u32(&sh->sc_full[z][lane]), 32);
     }
     if (lane < kSets) {
       tc::mbar_init(tc::smem_u32(&sh->p_full[lane]), 4 * kRowGroups);
@@ -226,48 +247,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const uint32_t tmem = sh->tmem_base;
 
-  if (warp >= kTmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp >= kTmaWarp && warp < kTmaWarp + kSets) {
-    // --------------------------------------------------------------------- TMA producer
-    // In the order of load_in_order over all tiles of the range.
-    const int set = warp - kTmaWarp;
+  int n_put = 0;  // loads that this warp has issued
+  if (warp >= kKWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if ((warp >= kKWarp && warp < kKWarp + kSets) || (warp >= kVWarp && warp < kVWarp + kSets)) {
+    // ------------------------------------------------------------------ K, and V, into the ring
+    // Two warps, since a load costs the warp that issues it some 180 cycles.
+    const bool loads_v = warp >= kVWarp;
+    const int set = warp - (loads_v ? kVWarp : kKWarp);
     const uint32_t range = blockIdx.x + set * gridDim.x;
     const TmaWaiter wait{{&sh->abort, a.timeout_ns}};
     const uint64_t stream = tc::policy_evict_first();
     uint8_t* ring_mem = sRing + set * C::kSlots * C::kSlotBytes;
-    Ring<C::kSlots> ring;
-    int n_put = 0, n_k = 0;
+    const CUtensorMap* map = loads_v ? &map_v : &map_k;
+    const uint32_t n_tiles = sh->start[set].count;
     int4 info = make_int4(0, 0, 0, 0);
     Cursor cur(sh->start[set], a.tokens);
-    auto put = [&](const CUtensorMap* map, const TileLoad& t) {
-      if (!wait(&sh->empty[set][ring.slot], ring.phase ^ 1)) return false;
-      issue_codes<D>(a, map, t, tc::smem_u32(ring_mem + ring.slot * C::kSlotBytes), tc::smem_u32(&sh->full[set][ring.slot]),
-                     stream, lane);
-      ++n_put;
-      ring.step();
-      return true;
-    };
-    // The order of the loads: K 0, K 1, V 0, K 2, V 1 and so on.  The tiles' pages are looked up three tiles before they are
-    // wanted.  Each step stands here once: the role's code has to stay in the instruction cache beside the others'.
+    // The tiles' pages are looked up two tiles before they are wanted
     struct Ahead {
       TileLoad t;
       bool there;
     };
-    Ahead before = {}, now = {}, next = {}, last = {};  // V, K, and two tiles ahead
+    Ahead now = {}, next = {}, last = {};
     bool ok = true;
-    for (int i = -3; ok; ++i) {
+    int i = -3;
+    for (;; ++i) {
       if (i >= 0) {
-        const int n = (now.there ? 1 : 0) | (before.there ? 2 : 0);
-        if (n == 0) break;
-#pragma unroll 1
-        for (int what = 0; ok && what < 2; ++what)
-          if (n >> what & 1) ok = put(what ? &map_v : &map_k, what ? before.t : now.t);
-        if (ok && now.there) {
-          const int b = n_k++ % Sh::kScales;
+        if (!now.there) break;
+        const uint32_t at = ring_place(loads_v, uint32_t(i), n_tiles), slot = at % C::kSlots;
+        ok = wait(&sh->empty[set][slot], (at / C::kSlots & 1) ^ 1);
+        if (!ok) break;
+        issue_codes<D>(a, map, now.t, tc::smem_u32(ring_mem + slot * C::kSlotBytes), tc::smem_u32(&sh->full[set][slot]), stream,
+                       lane);
+        if (!loads_v) {
+          const int b = i % Sh::kScales;
           issue_scales(args, now.t, sh->scales[set][b], tc::smem_u32(&sh->sc_full[set][b]), lane);
         }
       }
-      before = now, now = next, next = last;
+      now = next, next = last;
       last.there = cur.next(a);
       if (last.there) {
         const Segment& s = cur.s;
@@ -278,13 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) {
       sh->abort = 1;
-      if (lane == 0) note_timeout(a.status, a.diag, 1u, uint32_t(n_put));
+      info.x = 0;
+      if (lane == 0) note_timeout(a.status, a.diag, loads_v ? 5u : 1u, uint32_t(i));
     }
-    if (lane == 0) {
-      if (!ok) info.x = 0;
-      a.info[range] = info;
-      sh->n_put[set] = n_put, sh->n_k[set] = n_k;
-    }
+    if (lane == 0 && !loads_v) a.info[range] = info;
+    n_put = max(i, 0);
   } else if (warp >= kMmaWarp && warp < kMmaWarp + kSets) {
     // ------------------------------------------------------------ the two products of each tile
     constexpr uint32_t idesc_s = tc::idesc_e4m3_f32(kTile, R);
@@ -306,7 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kc.first() && !wait(&sh->q_ready[set][n_seg % kQRing], (n_seg / kQRing) & 1)) return false;
       if (!wait(&sh->full[set][ring.slot], ring.phase)) return false;
       tc::tc_fence_after();
-      const uint64_t dk_t = dk + uint32_t(ring.slot * (C::kSlotBytes >> 4)), dq_t = dq + uint32_t(b * (C::kQBytes >> 4));
+      // shuffled, so that the compiler knows them to be the same for the warp
+      const uint64_t dk_t = dk + uint32_t(__shfl_sync(~0u, ring.slot, 0) * (C::kSlotBytes >> 4));
+      const uint64_t dq_t = dq + uint32_t(__shfl_sync(~0u, b, 0) * (C::kQBytes >> 4));
       const bool last = kc.last();
       if (tc::elect_one()) {
 #pragma unroll
@@ -330,16 +346,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t >= 0) {
         if (!vc.next(a)) break;
         const bool first = vc.first(), last = vc.last();
-        ok = wait(&sh->full[set][ring.slot], ring.phase);
-        if (!ok) break;
         if (first) whole_tiles(a, vc.s, vc.s.u.p1, vc.s.u.p0, j0, j1);
-        // while the softmax works on this tile
-        if (vc.j < j0 || vc.j >= j1) clear_unseen_codes<D>(a, vc.s, vc.j, ring_mem + ring.slot * C::kSlotBytes, lane);
-        ok = wait(&sh->p_full[set], t & 1);
+        if (vc.j < j0 || vc.j >= j1) {  // while the softmax works on this tile
+          ok = wait(&sh->full[set][ring.slot], ring.phase);
+          if (!ok) break;
+          clear_unseen_codes<D>(a, vc.s, vc.j, ring_mem + ring.slot * C::kSlotBytes, lane);
+        }
+        ok = wait.both(&sh->full[set][ring.slot], ring.phase, &sh->p_full[set], t & 1);
         if (ok && first) ok = wait(&sh->o_read[set], (units++ & 1) ^ 1);  // the unit before has been read
         if (!ok) break;
         tc::tc_fence_after();
-        const uint64_t dv_t = dv + uint32_t(ring.slot * (C::kSlotBytes >> 4));
+        const uint64_t dv_t = dv + uint32_t(__shfl_sync(~0u, ring.slot, 0) * (C::kSlotBytes >> 4));
         if (tc::elect_one()) {
 #pragma unroll
           for (int i = 0; i < kTile / 32; ++i)
@@ -418,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh->abort = 1;
       if (lane == 0) note_timeout(a.status, a.diag, 4u, uint32_t(n_seg));
     }
-  } else if (warp < kTmaWarp) {
+  } else if (warp < kKWarp) {
     // ------------------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const ShortWaiter wait{&sh->abort, cycles_of(a.timeout_ns)};
@@ -472,22 +489,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           from = max(from - row0, 0), to = min(to - row0, RW);
         }
         const bool seen = from < to;
-        ok = wait(&sh->sc_full[set][t % Sh::kScales], (t / Sh::kScales) & 1);
+        ok = wait.both(&sh->s_full[set][t & 1], (t >> 1) & 1, &sh->sc_full[set][t % Sh::kScales], (t / Sh::kScales) & 1);
         if (!ok) break;
+        tc::tc_fence_after();
         const uint32_t bytes = sh->scales[set][t % Sh::kScales][kv];
         // a V of NaN makes the rows that see it NaN by way of their scores: a weight of 0 would not do
         const bool v_nan = bytes >> 8 == kv8::kNan;
         const float kf = kv8::factor(v_nan ? kv8::kNan : bytes & 0xFFu);
         const unsigned long long kk = pack_f32x2(kf, kf);
         const int v_byte = seen && !v_nan ? max(1, int(bytes >> 8)) : 0;  // a slot that no row sees counts for nothing
-        ok = wait(&sh->s_full[set][t & 1], (t >> 1) & 1);
-        if (!ok) break;
-        tc::tc_fence_after();
         float y[RW];  // the only array beside l: what is needed once more is loaded once more (S is there until P is)
-        // Steps: 0 a tile under the references as they stand; 1 new references are set; 2 the tile under those.  They are
-        // rounds of one loop because the code of a tile has to stay in the instruction cache.
-        for (int step = j == 0 ? 1 : 0;; ) {
-          const float* minus = step == 1 ? sh->zeros : neg_ref;
+        // First by the references as they stand; where they are outgrown, and on a unit's first tile, once more without, and by
+        // new ones.  (Rounds of one loop: a tile's code has to stay in the instruction cache.)
+        for (bool fresh = j == 0;; fresh = true) {
+          const float* minus = fresh ? sh->zeros : neg_ref;
           tc::tmem_ld<RW>(t_s + (t & 1) * R, y);
           tc::tmem_ld_wait();
 #pragma unroll
@@ -505,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(see >> (i - k) & 1u)) y[i] = -INFINITY;
             }
           }
-          if (__builtin_expect(step == 1, 0)) {
+          if (__builtin_expect(fresh, 0)) {
             // each row's maximum over the tile's 128 slots, by warp then over the group's warps; lane i has row i, and 32 + i
 #pragma unroll
             for (int k = 0; k < kFolds; ++k) {
@@ -517,6 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (lane < kFold) sh->warp_max[grp][w4][k * 32 + lane] = mine;
             }
+            float old[kFolds];  // before any warp writes the new ones
+#pragma unroll
+            for (int k = 0; k < kFolds; ++k) old[k] = j == 0 || lane >= kFold ? kUnset : -neg_ref[k * 32 + lane];
             const int my_byte = __reduce_max_sync(~0u, v_byte);
             if (lane == 0) sh->warp_byte[grp][w4] = my_byte;
             ok = meet();
@@ -526,20 +544,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int f_old = f;
             // f may fall, too: O^T keeps its place in fp32, and this tile's weights theirs in e4m3
             f = max(max(max(byte[0], byte[1]), max(byte[2], byte[3])), max(f - 40, 1));
-            for (int row = lane; row < RW; row += 32) {  // the four warps write the same values
-              const float old = j == 0 ? kUnset : -neg_ref[row];
-              const float m = fmaxf(old, fmaxf(fmaxf(part[0][row], part[1][row]), fmaxf(part[2][row], part[3][row])) - kTop);
-              row_by[row] = tc::ex2_approx(old - m);
-              sh->next_ref[grp][w4][row] = -m;
+#pragma unroll
+            for (int k = 0; k < kFolds; ++k) {
+              const int row = k * 32 + lane;
+              if (lane >= kFold) break;
+              const float m = fmaxf(old[k], fmaxf(fmaxf(part[0][row], part[1][row]), fmaxf(part[2][row], part[3][row])) - kTop);
+              row_by[row] = tc::ex2_approx(old[k] - m);  // the four warps write the same values
+              neg_ref[row] = row0 + row < s.ntok * a.g ? -m : -INFINITY;  // rows behind the unit's weigh nothing
             }
-            ok = meet();  // every warp has read the old references
-            if (!ok) break;
-            for (int row = lane; row < RW; row += 32) neg_ref[row] = sh->next_ref[grp][w4][row];
             __syncwarp();
-            if (j > 0) {
-              // the sums so far and this thread's lane of O^T, after the last product
-              ok = wait(&sh->p_empty[set], (t - 1) & 1);
-              if (!ok) break;
+            ok = wait(&sh->p_empty[set], (t & 1) ^ 1);  // the last product is over
+            if (!ok) break;
+            if (j > 0) {  // the sums so far and this thread's lane of O^T
               tc::tc_fence_after();
               const float fewer = tc::ex2_approx(float(f_old - f));
 #pragma unroll
@@ -560,11 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tc::tmem_st_wait();
             }
-            step = 2;
-            continue;
+#pragma unroll
+            for (int i = 0; i < RW; i += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(neg_ref + i);
+              y[i] += m.x, y[i + 1] += m.y, y[i + 2] += m.z, y[i + 3] += m.w;
+            }
           }
           const int at = sync & 1;
-          if (step == 0) {
+          if (!fresh) {
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < RW; i += 4) top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
@@ -573,10 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < RW; ++i) y[i] = tc::ex2_approx(y[i]);  // while the others arrive; done again where a reference moves
-          if (step == 2) break;
-          ok = wait(&sh->group[grp], sync++ & 1);
+          if (fresh) break;
+          // and the last product, which reads P, is over
+          ok = wait.both(&sh->group[grp], sync++ & 1, &sh->p_empty[set], (t & 1) ^ 1);
           if (!ok || sh->need[grp][at] != t + 1) break;
-          step = 1;
         }
         if (!ok) break;
         const float vf = kv8::power(max(v_byte - f, -126));  // 2^(ev - f)
@@ -595,8 +614,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 2; ++k) kv8::split2(__floats2half2_rn(y[4 * i + 2 * k], y[4 * i + 2 * k + 1]), h[k], r[k]);
           hi[i] = h[0] | h[1] << 16, lo[i] = r[0] | r[1] << 16;
         }
-        ok = wait(&sh->p_empty[set], (t & 1) ^ 1);
-        if (!ok) break;
         auto put_p = [&](const uint32_t* w, int at) {  // at byte `at` of the slot's row
           uint8_t* dst = p_mem + (at / C::kPPitch) * (kTile * C::kPPitch);
           const int in = at % C::kPPitch;
@@ -628,44 +645,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool partial = s.n < s.u.ntiles;
       const int64_t pbase = (int64_t(2) * (blockIdx.x + set * gridDim.x) + (s.tile0 > 0 ? 0 : 1)) * R + row0;
       const int n_rows = s.ntok * a.g - row0;  // of this group's
+      int* row_at = sh->row_at[set] + row0;
       for (int mine = lane; mine < RW; mine += 32) {  // the four warps write the same values
-        const int row = row0 + mine;
+        const int tok = (row0 + mine) / a.g, at = tok * (a.Hq - a.g) + row0 + mine;  // heads from the unit's first
         const float sum = (part[0][mine] + part[1][mine]) + (part[2][mine] + part[3][mine]);
-        row_by[mine] = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN, in the log-sum-exp too
+        row_by[mine] = (sum == 0.f ? 0.f : 1.f / sum) * of;  // NaN stays NaN, in the log-sum-exp too
+        row_at[mine] = mine < n_rows ? at * D : -1;
         if (w4 == 0 && mine < n_rows) {
           const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - neg_ref[mine];
           if (partial)
             a.plse[pbase + mine] = lse2;
           else if (a.lse)
-            a.lse[int64_t(s.row0 + row / a.g) * a.Hq + s.h * a.g + row % a.g] = lse2 * kLn2;
+            a.lse[int64_t(s.row0) * a.Hq + s.h * a.g + at] = lse2 * kLn2;
         }
       }
       __syncwarp();
       ok = wait(&sh->o_full[set], units++ & 1);
       if (!ok) break;
       tc::tc_fence_after();
-      const int tok = row0 / a.g;
-      int hh = row0 - tok * a.g;
-      __nv_bfloat16* dst = a.out + (int64_t(s.row0 + tok) * a.Hq + s.h * a.g + hh) * D + kv;
-      const int64_t wrap = int64_t(a.Hq - a.g) * D;  // from a token's last head to the next token's first
-      float* pdst = a.partial + pbase * D + kv;
+      if (w4 * 32 < D) {  // TMEM lane = lane of the head; lanes from D on hold nothing
+        __nv_bfloat16* dst = a.out + (int64_t(s.row0) * a.Hq + s.h * a.g) * D + kv;
+        float* pdst = a.partial + pbase * D + kv;
 #pragma unroll 1
-      for (int i = 0; i < RW; i += 8) {
-        float o[8], o2[8];
-        tc::tmem_ld<8>(t_o + i, o);
-        tc::tmem_ld<8>(t_o + R + i, o2);
-        tc::tmem_ld_wait();
-        if (kv >= D) continue;  // TMEM lane = lane of the head; lanes from D on hold nothing
+        for (int i = 0; i < RW; i += 8) {
+          float o[8], o2[8], by[8];
+          int to[8];
+          tc::tmem_ld<8>(t_o + i, o);
+          tc::tmem_ld<8>(t_o + R + i, o2);
+          *reinterpret_cast<float4*>(by) = *reinterpret_cast<const float4*>(row_by + i);
+          *reinterpret_cast<float4*>(by + 4) = *reinterpret_cast<const float4*>(row_by + i + 4);
+          *reinterpret_cast<int4*>(to) = *reinterpret_cast<const int4*>(row_at + i);
+          *reinterpret_cast<int4*>(to + 4) = *reinterpret_cast<const int4*>(row_at + i + 4);
+          tc::tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float x = fmaf(o2[k], 1.f / 16, o[k]) * row_by[i + k] * of;
-          if (i + k >= n_rows) continue;
-          if (partial)
-            pdst[(i + k) * D] = x;
-          else
-            *dst = __float2bfloat16(x);
-          dst += D;
-          if (++hh == a.g) hh = 0, dst += wrap;
+          for (int k = 0; k < 8; ++k) o[k] = fmaf(o2[k], 1.f / 16, o[k]) * by[k];
+          if (partial) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (to[k] >= 0) pdst[(i + k) * D] = o[k];
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (to[k] >= 0) dst[to[k]] = __float2bfloat16(o[k]);
+          }
         }
       }
       tc::tc_fence_before();
@@ -681,16 +703,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (sh->abort) {  // MMAs and copies may be in flight: wait (bounded) before TMEM is freed and the block ends
     const long long deadline = tc::deadline_after_ns(kDrainNs);
-    const int set = (warp - kTmaWarp) % 2;
-    if (warp >= kMmaWarp && warp < kSplitWarp && set < kSets && sh->pending[set]) {
+    const int set = warp - kMmaWarp;
+    if (set >= 0 && set < kSets && sh->pending[set]) {
       if (tc::elect_one()) tc::mma_commit(tc::smem_u32(&sh->drain[set]));
       __syncwarp();
       const volatile int never = 0;
       tc::mbar_wait_bounded(tc::smem_u32(&sh->drain[set]), 0, deadline, &never);
-    } else if (warp >= kTmaWarp && warp < kMmaWarp && set < kSets) {
-      drain_copies(sh->full[set], C::kSlots, sh->n_put[set], deadline);
-      drain_copies(sh->sc_full[set], Sh::kScales, sh->n_k[set], deadline);
     }
+    // a loading warp's last copies, the newest first; of one whose slot has been filled anew since the barrier may tell or not
+    const bool loads_v = warp >= kVWarp;
+    const int from = loads_v ? kVWarp : kKWarp;
+    if (n_put > 0) {
+      const volatile int never = 0;
+      for (int i = n_put - 1; i >= 0 && i >= n_put - C::kSlots; --i) {
+        const uint32_t at = ring_place(loads_v, uint32_t(i), sh->start[warp - from].count);
+        tc::mbar_wait_bounded(tc::smem_u32(&sh->full[warp - from][at % C::kSlots]), at / C::kSlots & 1, deadline, &never);
+      }
+    }
+    tc::async_copies_wait();
     __syncthreads();
   }
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, C::kTmemCols);
