@@ -391,16 +391,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(&sh->q_empty[set][b], ((n_seg / kQBufs) & 1) ^ 1);
       if (!ok) break;
       uint8_t* q_mem = sQ + (set * kQBufs + b) * C::kQBytes;
-#pragma unroll 2
+      // A thread's 16 lanes of a row are copied to where their two parts will lie, all rows at once, and then split in place.
+      const __nv_bfloat16* src = args.q + int64_t(s.row0) * args.q_stride + int64_t(s.h) * a.g * D + piece * 16;
+#pragma unroll 1
       for (int row = w * (32 / kLanes) + lane / kLanes; row < R; row += kPass) {
         const int tok = row / a.g, hh = row - tok * a.g;
-        uint4 x[2] = {};  // rows behind the unit's are 0
+        uint8_t* to = q_mem + tc::swizzled<D>(row, piece);
         if (tok < s.ntok) {
-          const uint4* src = reinterpret_cast<const uint4*>(args.q + int64_t(s.row0 + tok) * args.q_stride +
-                                                            int64_t(s.h * a.g + hh) * D) + 2 * piece;
-          x[0] = src[0], x[1] = src[1];
+          const __nv_bfloat16* from = src + tok * args.q_stride + hh * D;
+          tc::async_copy_16(tc::smem_u32(to), from);
+          tc::async_copy_16(tc::smem_u32(to + C::kQPart), from + 8);
+        } else {  // rows behind the unit's are 0
+          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<uint4*>(to + C::kQPart) = make_uint4(0u, 0u, 0u, 0u);
         }
-        const uint32_t word[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+      }
+      tc::async_copies_wait();
+#pragma unroll 1
+      for (int row = w * (32 / kLanes) + lane / kLanes; row < R; row += kPass) {
+        uint8_t* at = q_mem + tc::swizzled<D>(row, piece);
+        uint32_t word[8];
+        *reinterpret_cast<uint4*>(word) = *reinterpret_cast<const uint4*>(at);
+        *reinterpret_cast<uint4*>(word + 4) = *reinterpret_cast<const uint4*>(at + C::kQPart);
         uint32_t top = 0;  // the row's largest magnitude, as bits of fp32
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = max(top, max(word[i] & 0x7FFF0000u, (word[i] << 16) & 0x7FFF0000u));
@@ -408,23 +419,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
         const uint32_t byte = kv8::exponent_byte(top);
         const float by = byte == kv8::kNan ? 0.f : kv8::power(127 - int(byte)) * (args.negate ? -1.f : 1.f);
+        const unsigned long long by2 = pack_f32x2(by, by);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t h[2], l[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t y = word[2 * i + k];
-            const float y0 = bf16lo(y) * by, y1 = bf16hi(y) * by;
-            h[k] = kv8::code2(y0, y1);
-            const float2 got = kv8::values(h[k]);
-            l[k] = kv8::code2(y0 - got.x, y1 - got.y);
+            float y0, y1;  // at most 448: exact in fp16, but for what lies 2^-25 below
+            unpack_f32x2(mul_f32x2(pack_f32x2(bf16lo(word[2 * i + k]), bf16hi(word[2 * i + k])), by2), y0, y1);
+            kv8::split2<false>(__floats2half2_rn(y0, y1), h[k], l[k]);
           }
           hi[i] = h[0] | h[1] << 16, lo[i] = l[0] | l[1] << 16;
         }
-        uint8_t* dst = q_mem + tc::swizzled<D>(row, piece);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + C::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + C::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (piece == 0) sh->row_factor[set][n_seg % kQRing][row] = kv8::factor(byte) * a.c2;
       }
       tc::fence_proxy_async_smem();
@@ -611,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < RW / 4; ++i) {
           uint32_t h[2], r[2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) kv8::split2(__floats2half2_rn(y[4 * i + 2 * k], y[4 * i + 2 * k + 1]), h[k], r[k]);
+          for (int k = 0; k < 2; ++k) kv8::split2<true>(__floats2half2_rn(y[4 * i + 2 * k], y[4 * i + 2 * k + 1]), h[k], r[k]);
           hi[i] = h[0] | h[1] << 16, lo[i] = r[0] | r[1] << 16;
         }
         auto put_p = [&](const uint32_t* w, int at) {  // at byte `at` of the slot's row

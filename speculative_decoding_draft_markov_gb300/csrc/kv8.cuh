@@ -54,13 +54,14 @@ __device__ __forceinline__ float2 values(uint32_t codes) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Two halves as codes of their first parts and of 16 times what those leave (exact in fp16: a part has four bits).
+// Two halves as codes of their first parts and of what those leave (exact in fp16: a part has four bits), times 16 if asked.
+template <bool kTimes16>
 __device__ __forceinline__ void split2(__half2 x, uint32_t& first, uint32_t& rest) {
   uint16_t f, r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(f) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
   const uint32_t got = halves(f);
-  const __half2 by = __float2half2_rn(16.f);
-  const __half2 left = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&got)), by);
+  __half2 left = __hsub2(x, *reinterpret_cast<const __half2*>(&got));
+  if (kTimes16) left = __hmul2(left, __float2half2_rn(16.f));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&left)));
   first = f, rest = r;
 }
