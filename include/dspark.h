@@ -604,7 +604,7 @@ DSPARK_API int dspark_window_attention_kv8(const void* q, int64_t q_stride, int 
  * stands before nothing.
  * Device errors (status word, EINVAL; nothing is asked there): a token outside [-1, V), a token beyond its window,
  * a window that begins below 0 or ends beyond rows.
- * Limits: V % 8 == 0, 8 <= V < 2^24, n * per <= 2^20, top_n <= DSPARK_MAX_TOP; temperature > 0, it and its reciprocal finite. */
+ * Limits: V % 8 == 0, 8 <= V < 2^24, n * per <= 2^20, top_n <= DSPARK_MAX_TOP; temperature > 0, it and twice its reciprocal finite. */
 #define DSPARK_MAX_TOP 32
 DSPARK_API size_t dspark_token_logprobs_workspace_bytes(int items, int V, int top_n);
 DSPARK_API int dspark_token_logprobs(const void* logits, int dtype, int rows, int V, const int32_t* cu_seqlens, int n,

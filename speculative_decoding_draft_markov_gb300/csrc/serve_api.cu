@@ -226,7 +226,7 @@ int dspark_token_logprobs(const void* logits, int dtype, int rows, int V, const 
       !al(top_ids, 4) || !al(top_logprobs, 4))
     return DSPARK_EINVAL;
   if (top_n > 0 ? !top_ids || !top_logprobs : top_ids || top_logprobs) return DSPARK_EINVAL;
-  if (!std::isfinite(temperature) || !(temperature > 0.f) || !std::isfinite(1.f / temperature)) return DSPARK_EINVAL;
+  if (!std::isfinite(temperature) || !(temperature > 0.f) || !std::isfinite(2.f / temperature)) return DSPARK_EINVAL;
   if (int e = check_status_ws(ws, ws_bytes, token_logprobs_ws_bytes(n * per, V, top_n))) return e;
   return cuda_status(launch_token_logprobs(logits, dtype, rows, V, cu_seqlens, n, tokens, per, temperature, logprob,
                                            entropy, rank, top_ids, top_logprobs, top_n, ws,

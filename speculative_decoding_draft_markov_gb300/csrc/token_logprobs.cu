@@ -1,15 +1,32 @@
 // dspark_token_logprobs: log probabilities of given tokens, with the rows' entropies, the tokens' ranks and the
 // likeliest alternatives.
+//
+// One pass over the row: with d = (l - m) log2(e) / T and a reference m of the thread's own,
+//     S = sum 2^d,  W = sum 2^d d      logprob of t = d_t - log2 S,  entropy = log2 S - W / S      (times ln 2)
+// The alternatives come from a threshold that n ids at least reach: each warp's share of n among its lanes' maxima, the
+// least over the warps.  Each thread keeps the maxima of four parts of its ids, so that only parts that reach the threshold,
+// some dozen of 1024, are looked at again; what reaches it there (some dozen ids) is ranked by counting.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 #include "pdl.h"
+#include "tc_host.h"
+#include "tc_ptx.cuh"
 
 namespace dspark {
 namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kParts = 4;    // of a thread's ids, each with a maximum of its own
+constexpr int kRoom = 512;   // ids that may reach the threshold; with more, the alternatives are found one by one
+constexpr int kMaxSegments = 128;
+constexpr float kSlack = 8.f;  // what d may grow to: W / S and log2 S cancel to 2^-21
+constexpr float kLowest = -3.402823466e38f;  // m before there is a logit
 
 struct LogprobArgs {
   const void* logits;
@@ -18,8 +35,10 @@ struct LogprobArgs {
   int32_t *rank, *top_ids;
   float* top_logprobs;
   uint32_t* status;
-  float by;  // 1 / temperature
-  int rows, V, per, top_n;
+  float4* part;              // [items][segments]: m, S, W, and the ids before the token (as an int)
+  unsigned long long* best;  // [items][segments][top_n] keys, 0: none
+  float c2, slack;           // log2(e) / temperature; kSlack of it
+  int rows, V, per, top_n, segments, segment;  // ids of a segment
 };
 
 // The packed row of item i and its token; row < 0: the item reports nothing.
@@ -43,8 +62,6 @@ __device__ __forceinline__ Item item_of(const LogprobArgs& a, int i, bool report
   return t;
 }
 
-constexpr int kThreads = 512;
-
 // A value and its id as one number that orders by value, then by the lower id; 0: nothing (NaN and -inf among it).
 __device__ __forceinline__ unsigned long long key_of(float x, int id) {
   if (!(x > -INFINITY)) return 0ull;
@@ -56,96 +73,354 @@ __device__ __forceinline__ float value_of(unsigned long long key) {
   const uint32_t o = uint32_t(key >> 32);
   return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
-__device__ __forceinline__ unsigned long long warp_top(unsigned long long k) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long y = __shfl_xor_sync(~0u, k, o);
-    k = y > k ? y : k;
+
+template <typename T> struct Eight;  // 8 logits of a row
+template <> struct Eight<__nv_bfloat16> {
+  uint4 w;
+  __device__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ void get(float* x) const {
+    x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
+    x[4] = bf16lo(w.z), x[5] = bf16hi(w.z), x[6] = bf16lo(w.w), x[7] = bf16hi(w.w);
   }
-  return k;
+};
+template <> struct Eight<float> {
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ void get(float* x) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
+// Sums of a row or of a part of it, under a reference of their own.
+struct Sums {
+  float m, s, w;
+  int before;
+};
+__device__ __forceinline__ Sums joined(const Sums& a, const Sums& b, float c2) {
+  const float m = a.m > b.m ? a.m : b.m;  // references are numbers or +inf
+  const float da = (a.m - m) * c2, db = (b.m - m) * c2, fa = tc::ex2_approx(da), fb = tc::ex2_approx(db);
+  // W under another reference is f (W + S d), where f is not 0
+  const float wa = fa == 0.f ? 0.f : fa * fmaf(a.s, da, a.w), wb = fb == 0.f ? 0.f : fb * fmaf(b.s, db, b.w);
+  return Sums{m, fmaf(a.s, fa, b.s * fb), wa + wb, a.before + b.before};
+}
+__device__ __forceinline__ Sums warp_joined(Sums v, float c2) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Sums y{__shfl_xor_sync(~0u, v.m, o), __shfl_xor_sync(~0u, v.s, o), __shfl_xor_sync(~0u, v.w, o),
+                 __shfl_xor_sync(~0u, v.before, o)};
+    v = (threadIdx.x & o) ? joined(y, v, c2) : joined(v, y, c2);  // the same sum in both lanes
+  }
+  return v;
+}
+
+__device__ __forceinline__ void report_sums(const LogprobArgs& a, int64_t i, const Sums& t, float chosen) {
+  const float log_sum = log2f(t.s);
+  a.logprob[i] = ((chosen - t.m) * a.c2 - log_sum) * kLn2;
+  if (a.entropy) a.entropy[i] = (log_sum - t.w / t.s) * kLn2;
+  if (a.rank) a.rank[i] = 1 + t.before;
+}
+__device__ __forceinline__ void report_top(const LogprobArgs& a, int64_t at, unsigned long long key, const Sums& t) {
+  a.top_ids[at] = key ? int(~uint32_t(key)) : -1;
+  a.top_logprobs[at] = key ? ((value_of(key) - t.m) * a.c2 - log2f(t.s)) * kLn2 : -INFINITY;
+}
+__device__ __forceinline__ void report_nothing(const LogprobArgs& a, int64_t i, int tid, int threads) {
+  if (tid == 0) {
+    a.logprob[i] = 0.f;
+    if (a.entropy) a.entropy[i] = 0.f;
+    if (a.rank) a.rank[i] = 0;
+  }
+  for (int k = tid; k < a.top_n; k += threads) a.top_ids[i * a.top_n + k] = -1, a.top_logprobs[i * a.top_n + k] = -INFINITY;
+}
+
+struct Scan {
+  Sums warp_sums[kWarps];
+  float warp_least[kWarps];
+  float most[kParts][kThreads];  // maxima
+  unsigned long long key[kRoom], warp_key[kWarps];
+  uint16_t reach[kParts * kThreads];  // the parts that reach the threshold
+  int n_reach, n_key;
+};
+
+// A block takes one item's segment of the vocabulary.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-  __shared__ float scratch[kThreads / 32];
-  __shared__ unsigned long long keys[kThreads / 32];
+  __shared__ Scan sh;
   pdl_enter();
-  const int tid = threadIdx.x, i = blockIdx.x;
-  const Item it = item_of(a, i, tid == 0);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t i = blockIdx.x / uint32_t(a.segments);
+  const int seg = int(blockIdx.x - i * a.segments);
+  const Item it = item_of(a, int(i), tid == 0 && seg == 0);
   if (it.row < 0) {
-    if (tid == 0) {
-      a.logprob[i] = 0.f;
-      if (a.entropy) a.entropy[i] = 0.f;
-      if (a.rank) a.rank[i] = 0;
-    }
-    for (int k = tid; k < a.top_n; k += kThreads)
-      a.top_ids[int64_t(i) * a.top_n + k] = -1, a.top_logprobs[int64_t(i) * a.top_n + k] = -INFINITY;
+    if (a.segments == 1) report_nothing(a, i, tid, kThreads);
     return;
   }
-  const T* x = static_cast<const T*>(a.logits) + size_t(it.row) * a.V;
-  const float chosen = ld_f32(x, it.token);
-  float top = -INFINITY;
-  bool nan = false;
-  for (int v = tid; v < a.V; v += kThreads) {
-    const float l = ld_f32(x, v);
-    top = fmaxf(top, l), nan |= l != l;
+  if (tid == 0) sh.n_reach = sh.n_key = 0;
+  const int lo = seg * a.segment, hi = min(a.V, lo + a.segment);  // multiples of 8
+  const T* row = static_cast<const T*>(a.logits) + size_t(it.row) * a.V;
+  const float chosen = ld_f32(row, it.token);
+  const int packs = (hi - lo) / 8, mine = (packs + kThreads - 1) / kThreads;  // of the segment, of a thread
+  const int part = (mine + kParts - 1) / kParts;
+  const float c2 = a.c2;
+  const unsigned long long cc = pack_f32x2(c2, c2);
+  float m = kLowest;
+  unsigned long long s2 = 0ull, w2 = 0ull;
+  int before = 0;
+  constexpr int kAhead = 4;
+#pragma unroll 1
+  for (int q = 0; q < kParts; ++q) {
+    float most = -INFINITY;
+    const int k1 = min(mine, (q + 1) * part);
+#pragma unroll 1
+    for (int k0 = q * part; k0 < k1; k0 += kAhead) {
+      Eight<T> x[kAhead];
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) {
+        const int p = (k0 + b) * kThreads + tid;
+        if (k0 + b < k1 && p < packs) x[b].load(row + lo + p * 8);
+      }
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) {
+        const int p = (k0 + b) * kThreads + tid;
+        if (k0 + b >= k1 || p >= packs) break;
+        float l[8];
+        x[b].get(l);
+        const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
+        most = fmaxf(most, top);
+        if (top > m + a.slack) {  // a new reference
+          const float d = (m - top) * c2, f = tc::ex2_approx(d);
+          float s0, s1, w0, w1;
+          unpack_f32x2(s2, s0, s1);
+          unpack_f32x2(w2, w0, w1);
+          w0 = f == 0.f ? 0.f : f * fmaf(s0, d, w0), w1 = f == 0.f ? 0.f : f * fmaf(s1, d, w1);
+          s2 = pack_f32x2(s0 * f, s1 * f), w2 = pack_f32x2(w0, w1), m = top;
+        }
+        const unsigned long long mm = pack_f32x2(-m, -m);
+        // ids before the token stand before it with its own logit too
+        const int id0 = lo + p * 8;
+        if (id0 + 8 <= it.token) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) before += l[j] >= chosen;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) before += l[j] > chosen || (l[j] == chosen && id0 + j < it.token);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          float d0, d1;
+          unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(l[j], l[j + 1]), mm), cc), d0, d1);
+          d0 = max_or_nan(d0, -200.f), d1 = max_or_nan(d1, -200.f);  // 2^-200 is 0, and 0 * -inf is not
+          const unsigned long long e = pack_f32x2(tc::ex2_approx(d0), tc::ex2_approx(d1));
+          s2 = add_f32x2(s2, e);
+          w2 = fma_f32x2(e, pack_f32x2(d0, d1), w2);
+        }
+      }
+    }
+    if (a.top_n > 0) sh.most[q][tid] = most;
   }
-  top = block_max<kThreads>(top, scratch);
-  if (__syncthreads_or(nan)) top = __uint_as_float(0x7FFFFFFFu);
-  float sum = 0.f, dot = 0.f, ahead = 0.f;
-  for (int v = tid; v < a.V; v += kThreads) {
-    const float l = ld_f32(x, v), d = (l - top) * a.by, w = expf(d);
-    sum += w;
-    dot += w == 0.f ? 0.f : w * d;
-    ahead += l > chosen || (l == chosen && v < it.token) ? 1.f : 0.f;
+  float s0, s1, w0, w1;
+  unpack_f32x2(s2, s0, s1);
+  unpack_f32x2(w2, w0, w1);
+  Sums t = warp_joined(Sums{m, s0 + s1, w0 + w1, before}, c2);
+  if (lane == 0) sh.warp_sums[warp] = t;
+  const int n = a.top_n;
+  if (n > 0) {
+    // a value that the warp's share of n lanes reach
+    float best = fmaxf(fmaxf(sh.most[0][tid], sh.most[1][tid]), fmaxf(sh.most[2][tid], sh.most[3][tid])), least = -INFINITY;
+    static_assert(kParts == 4, "parts");
+    for (int k = 0; k < (n + kWarps - 1) / kWarps; ++k) {
+      asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(least) : "f"(best));
+      const uint32_t who = __ballot_sync(~0u, best == least);
+      if (who == 0 || least == -INFINITY) break;
+      if (lane == __ffs(who) - 1) best = -INFINITY;
+    }
+    if (lane == 0) sh.warp_least[warp] = least;
   }
-  sum = block_sum<kThreads>(sum, scratch);
   __syncthreads();
-  dot = block_sum<kThreads>(dot, scratch);
-  __syncthreads();
-  ahead = block_sum<kThreads>(ahead, scratch);
-  const float log_sum = logf(sum);
+  t = sh.warp_sums[0];
+#pragma unroll
+  for (int k = 1; k < kWarps; ++k) t = joined(t, sh.warp_sums[k], c2);
+  const bool whole = a.segments == 1;
   if (tid == 0) {
-    a.logprob[i] = (chosen - top) * a.by - log_sum;
-    if (a.entropy) a.entropy[i] = log_sum - dot / sum;
-    if (a.rank) a.rank[i] = 1 + int(ahead);
+    if (whole)
+      report_sums(a, i, t, chosen);
+    else
+      a.part[i * a.segments + seg] = make_float4(t.m, t.s, t.w, __int_as_float(t.before));
   }
+  if (n == 0) return;
+  float least = sh.warp_least[0];
+#pragma unroll
+  for (int k = 1; k < kWarps; ++k) least = fminf(least, sh.warp_least[k]);
+#pragma unroll
+  for (int q = 0; q < kParts; ++q) {
+    const bool in = sh.most[q][tid] >= least && sh.most[q][tid] > -INFINITY;
+    const uint32_t all = __ballot_sync(~0u, in);
+    int at = 0;
+    if (lane == 0 && all) at = atomicAdd(&sh.n_reach, __popc(all));
+    at = __shfl_sync(~0u, at, 0) + __popc(all & ((1u << lane) - 1u));
+    if (in) sh.reach[at] = uint16_t(q * kThreads + tid);
+  }
+  __syncthreads();
+  const int looks = sh.n_reach * part;
+  for (int k = tid; k < looks; k += kThreads) {
+    const int what = sh.reach[k / part], q = what / kThreads;
+    const int kk = q * part + k % part, p = kk * kThreads + what % kThreads;
+    if (kk >= mine || p >= packs) continue;
+    Eight<T> x;
+    x.load(row + lo + p * 8);
+    float l[8];
+    x.get(l);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (l[j] >= least && l[j] > -INFINITY) {
+        const int at = atomicAdd(&sh.n_key, 1);
+        if (at < kRoom) sh.key[at] = key_of(l[j], lo + p * 8 + j);
+      }
+  }
+  __syncthreads();
+  const int found = sh.n_key;
+  auto give = [&](int place, unsigned long long key) {
+    if (whole)
+      report_top(a, i * n + place, key, t);
+    else
+      a.best[(i * a.segments + seg) * n + place] = key;
+  };
+  if (found <= kRoom) {
+    for (int k = tid; k < found; k += kThreads) {
+      const unsigned long long key = sh.key[k];
+      int place = 0;
+      for (int j = 0; j < found; ++j) place += sh.key[j] > key;
+      if (place < n) give(place, key);
+    }
+    for (int k = found + tid; k < n; k += kThreads) give(k, 0ull);
+    return;
+  }
+  // many ids of one value, or all of the likeliest in a few threads' parts: one after the other, over the whole segment
   unsigned long long last = ~0ull;
-  for (int k = 0; k < a.top_n; ++k) {
+  for (int k = 0; k < n; ++k) {
     unsigned long long best = 0;
-    for (int v = tid; v < a.V; v += kThreads) {
-      const unsigned long long key = key_of(ld_f32(x, v), v);
-      if (key < last && key > best) best = key;
+    for (int p = tid; p < packs; p += kThreads) {
+      Eight<T> x;
+      x.load(row + lo + p * 8);
+      float l[8];
+      x.get(l);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const unsigned long long key = key_of(l[j], lo + p * 8 + j);
+        if (key < last && key > best) best = key;
+      }
     }
-    best = warp_top(best);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(~0u, best, o));
     __syncthreads();
-    if ((tid & 31) == 0) keys[tid >> 5] = best;
+    if (lane == 0) sh.warp_key[warp] = best;
     __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) best = max(best, keys[w]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) best = max(best, sh.warp_key[w]);
     last = best;
-    if (tid == 0) {
-      const int64_t at = int64_t(i) * a.top_n + k;
-      a.top_ids[at] = best ? int(~uint32_t(best)) : -1;
-      a.top_logprobs[at] = best ? (value_of(best) - top) * a.by - log_sum : -INFINITY;
-    }
+    if (tid == 0) give(k, best);
   }
+}
+
+// Joins an item's segments: their sums in order, and n times the largest of their lists' heads.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(const __grid_constant__ LogprobArgs a, int dtype) {
+  extern __shared__ __align__(16) unsigned long long list[];  // [segments][top_n]
+  __shared__ float4 part[kMaxSegments];
+  pdl_enter();
+  const int tid = threadIdx.x, lane = tid & 31, n = a.top_n, S = a.segments;
+  const int64_t i = blockIdx.x;
+  const Item it = item_of(a, int(i), false);
+  if (it.row < 0) {
+    report_nothing(a, i, tid, kJoinThreads);
+    return;
+  }
+  for (int k = tid; k < S; k += kJoinThreads) part[k] = a.part[i * S + k];
+  for (int k = tid; k < S * n; k += kJoinThreads) list[k] = a.best[i * S * n + k];
+  const size_t at = size_t(it.row) * a.V + it.token;
+  const float chosen = dtype == DSPARK_F32 ? static_cast<const float*>(a.logits)[at]
+                                           : ld_f32(static_cast<const __nv_bfloat16*>(a.logits), at);
+  __syncthreads();
+  if (tid >= 32) return;
+  Sums t{kLowest, 0.f, 0.f, 0};
+  for (int k = lane; k < S; k += 32) t = joined(t, Sums{part[k].x, part[k].y, part[k].z, __float_as_int(part[k].w)}, a.c2);
+  t = warp_joined(t, a.c2);
+  if (lane == 0) report_sums(a, i, t, chosen);
+  constexpr int kHeads = kMaxSegments / 32;
+  int head[kHeads];
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) head[h] = 0;
+  unsigned long long mine = 0;  // the key of rank `lane`
+  for (int k = 0; k < n; ++k) {
+    unsigned long long best = 0;
+    int from = -1;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      const int seg = h * 32 + lane;
+      const unsigned long long key = seg < S && head[h] < n ? list[seg * n + head[h]] : 0ull;
+      if (key > best) best = key, from = h;
+    }
+    const uint32_t high = __reduce_max_sync(~0u, uint32_t(best >> 32));
+    const uint32_t low = __reduce_max_sync(~0u, uint32_t(best >> 32) == high ? uint32_t(best) : 0u);
+    const unsigned long long top = (static_cast<unsigned long long>(high) << 32) | low;
+    if (top != 0 && top == best) {
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h)
+        if (h == from) ++head[h];
+    }
+    if (lane == k) mine = top;
+  }
+  if (lane < n) report_top(a, i * n + lane, mine, t);
+}
+static_assert(DSPARK_MAX_TOP <= 32, "a lane has one alternative");
+
+// How many segments a row is cut into: as many as it takes to fill the SMs, of 2048 ids at least.
+int segments_of(int items, int V) {
+  const int most = std::min(kMaxSegments, std::max(1, V / (8 * kThreads)));
+  return std::max(1, std::min(most, 4 * tch::sm_count() / items));
 }
 
 }  // namespace
 
-size_t token_logprobs_ws_bytes(int items, int V, int top_n) { return 256; }
+size_t token_logprobs_ws_bytes(int items, int V, int top_n) {
+  size_t most = 256;
+  // any number of items up to that: fewer are cut into more segments
+  const int S = std::min(kMaxSegments, std::max(1, V / (8 * kThreads)));
+  const size_t parts = std::min(size_t(items) * S, std::max(size_t(items), size_t(4) * tch::sm_count()));
+  most += align256(parts * sizeof(float4)) + align256(parts * top_n * sizeof(unsigned long long));
+  return most;
+}
 
 cudaError_t launch_token_logprobs(const void* logits, int dtype, int rows, int V, const int32_t* cu, int bs,
                                   const int32_t* tokens, int per, float temperature, float* logprob, float* entropy,
                                   int32_t* rank, int32_t* top_ids, float* top_logprobs, int top_n, void* ws,
                                   cudaStream_t s) {
   LogprobArgs a;
+  const int items = bs * per;
   a.logits = logits, a.cu = cu, a.tokens = tokens, a.logprob = logprob, a.entropy = entropy, a.rank = rank;
   a.top_ids = top_ids, a.top_logprobs = top_logprobs, a.status = static_cast<uint32_t*>(ws);
-  a.by = 1.f / temperature, a.rows = rows, a.V = V, a.per = per, a.top_n = top_n;
-  const dim3 grid(bs * per);
-  return dtype == DSPARK_F32 ? launch_pdl(logprobs_kernel<float>, grid, dim3(kThreads), 0, s, a)
-                             : launch_pdl(logprobs_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, a);
+  a.c2 = kLog2e / temperature, a.slack = std::min(kSlack / a.c2, 1e37f), a.rows = rows, a.V = V, a.per = per, a.top_n = top_n;
+  a.segments = segments_of(items, V);
+  a.segment = ((V + a.segments - 1) / a.segments + 7) / 8 * 8;
+  a.segments = (V + a.segment - 1) / a.segment;
+  char* w = static_cast<char*>(ws) + 256;
+  a.part = reinterpret_cast<float4*>(w);
+  a.best = reinterpret_cast<unsigned long long*>(w + align256(size_t(items) * a.segments * sizeof(float4)));
+  const dim3 grid(a.segments * items);
+  const cudaError_t e = dtype == DSPARK_F32
+                            ? launch_pdl(logprobs_kernel<float>, grid, dim3(kThreads), 0, s, a)
+                            : launch_pdl(logprobs_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, a);
+  if (e != cudaSuccess || a.segments == 1) return e;
+  return launch_pdl(logprobs_join_kernel, dim3(items), dim3(kJoinThreads),
+                    size_t(a.segments) * std::max(top_n, 1) * sizeof(unsigned long long), s, a, dtype);
 }
 
 }  // namespace dspark

@@ -120,6 +120,26 @@ def test_masked_rows(dtype):
     _check(x[1:4].contiguous(), None, [[int((x[r] == float("-inf")).nonzero()[0])] for r in (1, 2, 3)], 1.0, top)
 
 
+def test_masks_of_the_lowest_value():
+    """Ids masked by the type's lowest value weigh nothing, unless there is nothing else: then all are equal."""
+    for dtype in (torch.float32, torch.bfloat16):
+        x = _logits(3, 9000, dtype, 12)
+        x[0, 100:8000] = torch.finfo(dtype).min
+        x[1] = torch.finfo(dtype).min
+        x[2, 1:] = torch.finfo(dtype).min
+        outs = _outputs(3, 1, 3)
+        ws = B.alloc_logprobs_workspace(3, 9000, 3)
+        B.dspark_token_logprobs(x, None, torch.tensor([[50], [77], [0]], dtype=torch.int32, device="cuda"), 1.0, *outs, ws)
+        assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+        lp, ent, rank, ids, best = (o.cpu().numpy() for o in outs)
+        want = K.token_logprobs(_f64(x)[0], 50, 1.0, 3)
+        np.testing.assert_allclose([lp[0, 0], ent[0, 0]], want[:2], atol=3e-5)
+        assert rank[0, 0] == want[2] and np.array_equal(ids[0, 0], want[3])
+        np.testing.assert_allclose([lp[1, 0], ent[1, 0]], [-np.log(9000), np.log(9000)], atol=3e-5)
+        assert rank[1, 0] == 78 and ids[1, 0].tolist() == [0, 1, 2] and ids[2, 0].tolist() == [0, 1, 2]
+        assert lp[2, 0] == 0 and abs(ent[2, 0]) < 1e-6 and rank[2, 0] == 1
+
+
 def test_rows_with_nan_and_infinity():
     """NaN wherever it stands in the row, and +inf: NaN results; alternatives and ranks are those of the numbers."""
     V = 20000
