@@ -59,7 +59,7 @@ __device__ __forceinline__ uint2 codes8(const float* x, float by) {
 // The rotated K goes into 8 bits from fp32, with one rounding.  Products and sums of a pair are rounded one by one (no fused
 // multiply-add), so that the powers of two are those of any plain fp32 evaluation.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kMaxAppendThreads) append8_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kMaxAppendThreads, 6) append8_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ RowPlace place;
   const int tid = threadIdx.x, lane = tid & 31;
   pdl_enter();
@@ -129,18 +129,18 @@ __global__ void __launch_bounds__(kMaxAppendThreads) append8_kernel(const __grid
       x = pack8(u);
       y = pack8(w);
     }
+    if (live && is_q) {
+      __nv_bfloat16* dst = a.q_out + (int64_t(row) * a.Hq + hh) * a.D;
+      *reinterpret_cast<uint4*>(dst + lo) = x;
+      *reinterpret_cast<uint4*>(dst + hi) = y;
+    }
+    if (__all_sync(~0u, is_q || !live)) continue;
     // the head's largest magnitude: as bits, so that a NaN is larger than everything
     uint32_t top = 0;
 #pragma unroll
     for (int t = 0; t < 8; ++t) top = max(top, max(__float_as_uint(u[t]) & 0x7FFFFFFFu, __float_as_uint(w[t]) & 0x7FFFFFFFu));
     for (int o = 1; o < per_head; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-    if (!live) continue;
-    if (is_q) {
-      __nv_bfloat16* dst = a.q_out + (int64_t(row) * a.Hq + hh) * a.D;
-      *reinterpret_cast<uint4*>(dst + lo) = x;
-      *reinterpret_cast<uint4*>(dst + hi) = y;
-      continue;
-    }
+    if (!live || is_q) continue;
     const uint32_t byte = kv8::exponent_byte(top);
     const float by = byte == kv8::kNan ? 0.f : kv8::power(127 - int(byte));
     if (byte == kv8::kNan) {
@@ -182,10 +182,12 @@ __device__ __forceinline__ void widen16(uint4 w, float by, uint4* out) {
 
 // What a request's packed rows see, in blocks of the cache (pages, or 32-slot pieces of larger pages): those that hold
 // sinks, then those of the window.  Blocks are counted over the requests; a unit is a block of one KV head, and the units are
-// dealt out to the blocks of the grid in turn.
-__global__ void __launch_bounds__(kReadThreads) read8_kernel(const __grid_constant__ ReadArgs a) {
+// dealt out to the grid's warps in turn.
+template <int D>
+__global__ void __launch_bounds__(kReadThreads, 4) read8_kernel(const __grid_constant__ ReadArgs a) {
   __shared__ long long before[DSPARK_MAX_BS + 1];  // blocks of the requests before
   __shared__ long long warp_total[DSPARK_MAX_BS / 32];
+  __shared__ int2 first[DSPARK_MAX_BS];  // the first position of a request's window, and behind its last
   __shared__ int bad;
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bsh = a.block_shift;
@@ -202,6 +204,7 @@ __global__ void __launch_bounds__(kReadThreads) read8_kernel(const __grid_consta
       } else {
         const int lo = a.window ? max(0, c - a.window + 1) : 0;
         const int sinks = a.window ? min(a.n_sink, lo) : 0;
+        first[tid] = make_int2(lo, c + n);
         mine = ((c + n - 1) >> bsh) - (lo >> bsh) + 1;
         // sink blocks that the window's do not reach
         mine += min((sinks + (1 << bsh) - 1) >> bsh, lo >> bsh);
@@ -225,36 +228,51 @@ __global__ void __launch_bounds__(kReadThreads) read8_kernel(const __grid_consta
     return;
   }
   const int64_t units = before[a.bs] * a.Hkv;
-  const int per_slot = a.D / 16, pieces = per_slot << bsh;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+  constexpr int kPerSlot = D / 16, kRounds = 32 * kPerSlot / 32;  // 16-byte pieces; rounds of a warp over a whole block
+  for (int64_t u = int64_t(blockIdx.x) * (kReadThreads / 32) + warp; u < units; u += int64_t(gridDim.x) * (kReadThreads / 32)) {
     const long long block = u / a.Hkv;
     const int h = int(u - block * a.Hkv);
     int r = 0;
     for (int step = DSPARK_MAX_BS / 2; step > 0; step >>= 1)
       if (r + step < a.bs && before[r + step] <= block) r += step;
-    const int c = a.ctx[r], end = c + a.cu[r + 1] - a.cu[r];
-    const int lo = a.window ? max(0, c - a.window + 1) : 0, sinks = a.window ? min(a.n_sink, lo) : 0;
+    const int lo = first[r].x, end = first[r].y, sinks = a.window ? min(a.n_sink, lo) : 0;
     const int sb = min((sinks + (1 << bsh) - 1) >> bsh, lo >> bsh), v = int(block - before[r]);
     const int pos0 = (v < sb ? v : v - sb + (lo >> bsh)) << bsh;
     const int64_t at = int64_t(r) * a.max_pages + (pos0 >> a.page_shift);
     const int page = a.page_table[at], to = a.out_table[at];
     if (page < 0 || page >= a.n_pages || to < 0 || to >= a.n_out_pages) {
-      if (tid == 0) set_status(a.status, DSPARK_EINVAL);
+      if (lane == 0) set_status(a.status, DSPARK_EINVAL);
       continue;
     }
     const int slot0 = pos0 & ((1 << a.page_shift) - 1);
     const int64_t src = ((int64_t(page) * a.Hkv + h) << a.page_shift) + slot0;
     const int64_t dst = ((int64_t(to) * a.Hkv + h) << a.page_shift) + slot0;
-    for (int i = tid; i < pieces; i += kReadThreads) {
-      const int s = i / per_slot, pos = pos0 + s;
-      if (pos >= end || (pos < lo && pos >= sinks)) continue;
-      const uint16_t sc = reinterpret_cast<const uint16_t*>(a.kv_scale)[src + s];
-      const uint4 k = reinterpret_cast<const uint4*>(a.k_cache)[src * per_slot + i];
-      const uint4 x = reinterpret_cast<const uint4*>(a.v_cache)[src * per_slot + i];
-      uint4* ko = reinterpret_cast<uint4*>(a.k_out) + (dst * per_slot + i) * 2;
-      uint4* vo = reinterpret_cast<uint4*>(a.v_out) + (dst * per_slot + i) * 2;
-      widen16(k, kv8::factor(sc & 0xFFu), ko);
-      widen16(x, kv8::factor(sc >> 8), vo);
+    // lane i has slot i's exponents, and whether some row sees it
+    const int pos = pos0 + lane;
+    const bool mine = lane < 1 << bsh && pos < end && (pos >= lo || pos < sinks);
+    const uint32_t seen = __ballot_sync(~0u, mine);
+    const uint32_t bytes = mine ? reinterpret_cast<const uint16_t*>(a.kv_scale)[src + lane] : 0u;
+    const uint4* ks = reinterpret_cast<const uint4*>(a.k_cache) + src * kPerSlot + lane;
+    const uint4* vs = reinterpret_cast<const uint4*>(a.v_cache) + src * kPerSlot + lane;
+    uint4* ko = reinterpret_cast<uint4*>(a.k_out) + (dst * kPerSlot + lane) * 2;
+    uint4* vo = reinterpret_cast<uint4*>(a.v_out) + (dst * kPerSlot + lane) * 2;
+#pragma unroll
+    for (int k0 = 0; k0 < kRounds; k0 += 4) {  // eight loads under way
+      uint4 k[4], x[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int s = ((k0 + b) * 32 + lane) / kPerSlot;
+        if (seen >> s & 1u) k[b] = __ldcs(ks + (k0 + b) * 32), x[b] = __ldcs(vs + (k0 + b) * 32);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int s = ((k0 + b) * 32 + lane) / kPerSlot;
+        const uint32_t e = __shfl_sync(~0u, bytes, s);
+        if (seen >> s & 1u) {
+          widen16(k[b], kv8::factor(e & 0xFFu), ko + (k0 + b) * 64);
+          widen16(x[b], kv8::factor(e >> 8), vo + (k0 + b) * 64);
+        }
+      }
     }
   }
 }
@@ -277,7 +295,9 @@ cudaError_t launch_append_kv8(const void* q, int64_t q_stride, const void* k, in
   a.bs = bs, a.rows = rows, a.max_pos = max_pos, a.rot = rot, a.max_pages = max_pages, a.n_pages = n_pages;
   a.page_shift = page_shift, a.Hq = q ? Hq : 0, a.Hkv = Hkv, a.D = D;
   const int items = (a.Hq + 2 * Hkv) * (D / 16);
-  const dim3 block(std::min((items + 31) / 32 * 32, kMaxAppendThreads));
+  // as many threads as share the items evenly: 384 items, 8191 rows, 192 threads 40.8 us, 256 45.6
+  const int rounds = (items + kMaxAppendThreads - 1) / kMaxAppendThreads;
+  const dim3 block(((items + rounds - 1) / rounds + 31) / 32 * 32);
   return launch_pdl(interleaved ? append8_kernel<true> : append8_kernel<false>, dim3(rows), block, 0, s, a);
 }
 
@@ -293,7 +313,9 @@ cudaError_t launch_read_kv8(const void* k_cache, const void* v_cache, const uint
   a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, 5);
   a.bs = bs, a.rows = rows, a.Hkv = Hkv, a.D = D, a.window = window >= a.cache_limit ? 0 : window, a.n_sink = n_sink;
   a.n_out_pages = n_out_pages;
-  return launch_pdl(read8_kernel, dim3(tch::sm_count() * 8), dim3(kReadThreads), 0, s, a);
+  const dim3 grid(tch::sm_count() * 4);
+  return D == 64 ? launch_pdl(read8_kernel<64>, grid, dim3(kReadThreads), 0, s, a)
+                 : launch_pdl(read8_kernel<128>, grid, dim3(kReadThreads), 0, s, a);
 }
 
 }  // namespace dspark

@@ -26,6 +26,9 @@ constexpr int kParts = 4;    // of a thread's ids, each with a maximum of its ow
 constexpr int kRoom = 512;   // ids that may reach the threshold; with more, the alternatives are found one by one
 constexpr int kMaxSegments = 128;
 constexpr float kSlack = 8.f;  // what d may grow to: W / S and log2 S cancel to 2^-21
+// Logits below -kPlain count as that, so that no mask's value (-inf times the weight 0 is NaN) needs care; a segment without
+// any above it, or a temperature under which it would weigh something, is summed with care.
+constexpr float kPlain = 0x1.9200000000000p+99f;  // 9.95e29, exact in bf16
 constexpr float kLowest = -3.402823466e38f;  // m before there is a logit
 
 struct LogprobArgs {
@@ -74,10 +77,23 @@ __device__ __forceinline__ float value_of(unsigned long long key) {
   return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
 
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <typename T> struct Eight;  // 8 logits of a row
 template <> struct Eight<__nv_bfloat16> {
   uint4 w;
   __device__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ void raise() {  // to -kPlain at least; a NaN stays
+    const uint32_t to = 0xF149F149u;
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.x) : "r"(to));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.y) : "r"(to));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.z) : "r"(to));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.w) : "r"(to));
+  }
   __device__ void get(float* x) const {
     x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
     x[4] = bf16lo(w.z), x[5] = bf16hi(w.z), x[6] = bf16lo(w.w), x[7] = bf16hi(w.w);
@@ -89,16 +105,14 @@ template <> struct Eight<float> {
     a = *reinterpret_cast<const float4*>(p);
     b = *(reinterpret_cast<const float4*>(p) + 1);
   }
+  __device__ void raise() {
+    a.x = max_or_nan(a.x, -kPlain), a.y = max_or_nan(a.y, -kPlain), a.z = max_or_nan(a.z, -kPlain), a.w = max_or_nan(a.w, -kPlain);
+    b.x = max_or_nan(b.x, -kPlain), b.y = max_or_nan(b.y, -kPlain), b.z = max_or_nan(b.z, -kPlain), b.w = max_or_nan(b.w, -kPlain);
+  }
   __device__ void get(float* x) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
 };
-
-__device__ __forceinline__ float max_or_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 // Sums of a row or of a part of it, under a reference of their own.
 struct Sums {
@@ -152,7 +166,7 @@ struct Scan {
 
 // A block takes one item's segment of the vocabulary.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
   __shared__ Scan sh;
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -166,65 +180,88 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   if (tid == 0) sh.n_reach = sh.n_key = 0;
   const int lo = seg * a.segment, hi = min(a.V, lo + a.segment);  // multiples of 8
   const T* row = static_cast<const T*>(a.logits) + size_t(it.row) * a.V;
-  const float chosen = ld_f32(row, it.token);
+  const float chosen = ld_f32(row, it.token), chosen_raised = max_or_nan(chosen, -kPlain);
   const int packs = (hi - lo) / 8, mine = (packs + kThreads - 1) / kThreads;  // of the segment, of a thread
-  const int part = (mine + kParts - 1) / kParts;
+  constexpr int kAhead = 4;
+  const int part = ((mine + kParts - 1) / kParts + kAhead - 1) / kAhead * kAhead;
   const float c2 = a.c2;
   const unsigned long long cc = pack_f32x2(c2, c2);
-  float m = kLowest;
+  float m = kLowest, most = -INFINITY, all = -INFINITY;  // the largest of a part, of all
+  int q = 0;
   unsigned long long s2 = 0ull, w2 = 0ull;
   int before = 0;
-  constexpr int kAhead = 4;
-#pragma unroll 1
-  for (int q = 0; q < kParts; ++q) {
-    float most = -INFINITY;
-    const int k1 = min(mine, (q + 1) * part);
-#pragma unroll 1
-    for (int k0 = q * part; k0 < k1; k0 += kAhead) {
-      Eight<T> x[kAhead];
+  auto refer = [&](float top) {  // a new reference
+    const float d = (m - top) * c2, f = tc::ex2_approx(d);
+    float s0, s1, w0, w1;
+    unpack_f32x2(s2, s0, s1);
+    unpack_f32x2(w2, w0, w1);
+    w0 = f == 0.f ? 0.f : f * fmaf(s0, d, w0), w1 = f == 0.f ? 0.f : f * fmaf(s1, d, w1);
+    s2 = pack_f32x2(s0 * f, s1 * f), w2 = pack_f32x2(w0, w1), m = top;
+  };
+  if (a.top_n > 0)
+    for (int k = 0; k < kParts; ++k) sh.most[k][tid] = -INFINITY;
+  Eight<T> x[kAhead];
 #pragma unroll
-      for (int b = 0; b < kAhead; ++b) {
-        const int p = (k0 + b) * kThreads + tid;
-        if (k0 + b < k1 && p < packs) x[b].load(row + lo + p * 8);
-      }
+  for (int b = 0; b < kAhead; ++b)
+    if (b * kThreads + tid < packs) x[b].load(row + lo + (b * kThreads + tid) * 8);
+#pragma unroll 1
+  for (int k0 = 0; k0 < mine; k0 += kAhead) {
 #pragma unroll
-      for (int b = 0; b < kAhead; ++b) {
-        const int p = (k0 + b) * kThreads + tid;
-        if (k0 + b >= k1 || p >= packs) break;
-        float l[8];
-        x[b].get(l);
-        const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
-        most = fmaxf(most, top);
-        if (top > m + a.slack) {  // a new reference
-          const float d = (m - top) * c2, f = tc::ex2_approx(d);
-          float s0, s1, w0, w1;
-          unpack_f32x2(s2, s0, s1);
-          unpack_f32x2(w2, w0, w1);
-          w0 = f == 0.f ? 0.f : f * fmaf(s0, d, w0), w1 = f == 0.f ? 0.f : f * fmaf(s1, d, w1);
-          s2 = pack_f32x2(s0 * f, s1 * f), w2 = pack_f32x2(w0, w1), m = top;
-        }
-        const unsigned long long mm = pack_f32x2(-m, -m);
+    for (int b = 0; b < kAhead; ++b) {
+      const int p = (k0 + b) * kThreads + tid, next = p + kAhead * kThreads;
+      if (p >= packs) break;
+      float l[8];
+      x[b].raise();
+      x[b].get(l);
+      if (next < packs) x[b].load(row + lo + next * 8);
+      const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
+      most = fmaxf(most, top);
+      if (top > m + a.slack && top > -kPlain) refer(top);  // (m * c2 is rounded: of a raised logit that would be far off)
+      if (top >= chosen_raised) {
+        Eight<T> raw = {};
+        float r[8];
+        raw.load(row + lo + p * 8);
+        raw.get(r);
         // ids before the token stand before it with its own logit too
         const int id0 = lo + p * 8;
-        if (id0 + 8 <= it.token) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) before += l[j] >= chosen;
-        } else {
+        for (int j = 0; j < 8; ++j) before += r[j] > chosen || (r[j] == chosen && id0 + j < it.token);
+      }
+      const float mc = m == kLowest ? 0.f : m * c2;  // nothing but raised ones so far: they weigh nothing
+      const unsigned long long mm = pack_f32x2(-mc, -mc);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) before += l[j] > chosen || (l[j] == chosen && id0 + j < it.token);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          float d0, d1;
-          unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(l[j], l[j + 1]), mm), cc), d0, d1);
-          d0 = max_or_nan(d0, -200.f), d1 = max_or_nan(d1, -200.f);  // 2^-200 is 0, and 0 * -inf is not
-          const unsigned long long e = pack_f32x2(tc::ex2_approx(d0), tc::ex2_approx(d1));
-          s2 = add_f32x2(s2, e);
-          w2 = fma_f32x2(e, pack_f32x2(d0, d1), w2);
-        }
+      for (int j = 0; j < 8; j += 2) {
+        float d0, d1;
+        const unsigned long long d = fma_f32x2(pack_f32x2(l[j], l[j + 1]), cc, mm);
+        unpack_f32x2(d, d0, d1);
+        const unsigned long long e = pack_f32x2(tc::ex2_approx(d0), tc::ex2_approx(d1));
+        s2 = add_f32x2(s2, e);
+        w2 = fma_f32x2(e, d, w2);
       }
     }
-    if (a.top_n > 0) sh.most[q][tid] = most;
+    if (k0 + kAhead == (q + 1) * part || k0 + kAhead >= mine) {
+      if (a.top_n > 0) sh.most[q][tid] = most;
+      all = fmaxf(all, most), most = -INFINITY;
+      ++q;
+    }
+  }
+  const bool some = __syncthreads_or(all > -kPlain), huge = __syncthreads_or(all >= kPlain);
+  if (!some || huge || c2 * kPlain < 400.f || c2 > 1e7f) {  // (c2 beyond: d would overflow, and 0 * -inf is NaN)
+    m = kLowest, s2 = w2 = 0ull;
+    for (int p = tid; p < packs; p += kThreads) {
+      float l[8];
+      x[0].load(row + lo + p * 8);
+      x[0].get(l);
+      const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
+      if (top > m + a.slack) refer(top);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float d0 = max_or_nan((l[j] - m) * c2, -200.f), d1 = max_or_nan((l[j + 1] - m) * c2, -200.f);  // 2^-200 is 0
+        const unsigned long long e = pack_f32x2(tc::ex2_approx(d0), tc::ex2_approx(d1));
+        s2 = add_f32x2(s2, e);
+        w2 = fma_f32x2(e, pack_f32x2(d0, d1), w2);
+      }
+    }
   }
   float s0, s1, w0, w1;
   unpack_f32x2(s2, s0, s1);
@@ -259,6 +296,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   float least = sh.warp_least[0];
 #pragma unroll
   for (int k = 1; k < kWarps; ++k) least = fminf(least, sh.warp_least[k]);
+  if (least <= -kPlain) least = -INFINITY;  // raised: what it was is to be seen
 #pragma unroll
   for (int q = 0; q < kParts; ++q) {
     const bool in = sh.most[q][tid] >= least && sh.most[q][tid] > -INFINITY;
