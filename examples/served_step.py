@@ -1,9 +1,10 @@
 """Speculative decoding over a paged cache: a small target model with random weights, its attention on the
 paged cache with a sliding window and sinks, penalties, a bias and a mask on its logits, and the verification.
 
-    python examples/served_step.py [--steps N] [--temperature T]
+    python examples/served_step.py [--steps N] [--temperature T] [--eight-bit] [--top N]
 
-The target is a stack of attention layers (no feed-forward parts: the cache and the attention are what is
+With --eight-bit the cache's pages are of 8 bits; with --top the log probability, rank and N likeliest alternatives
+of each token are reported.  The target is a stack of attention layers (no feed-forward parts: the cache and the attention are what is
 shown).  The drafter sees no context: its base logits U are 0 and its Markov term is the target's head on the
 previous token's embedding, in low rank; some drafts are accepted, some are not."""
 import argparse
@@ -79,7 +80,7 @@ class SmallTarget:
         cache.advance(torch.tensor(n, **i32))
 
 
-def set_up(bs=4, gamma=3, seed=3, window=48, n_sink=4, max_tokens=400, device="cuda"):
+def set_up(bs=4, gamma=3, seed=3, window=48, n_sink=4, max_tokens=400, device="cuda", eight_bit=False):
     """A target, a cache with the prompts in it, rules, and the step's inputs and buffers."""
     rng = np.random.default_rng(seed)
     model = SmallTarget(device=device)
@@ -87,7 +88,8 @@ def set_up(bs=4, gamma=3, seed=3, window=48, n_sink=4, max_tokens=400, device="c
     page = 16
     max_pages = -(-(max_tokens + 2 * gamma) // page)
     cache = V.PagedCache(model.layers, bs * max_pages, page, model.Hq, model.Hkv, model.D, bs, max_pages,
-                         V.rotation_table(max_tokens + 2 * gamma, model.D, device=device), window, n_sink, device=device)
+                         V.rotation_table(max_tokens + 2 * gamma, model.D, device=device), window, n_sink, device=device,
+                         eight_bit=eight_bit)
     buf = S.StepBuffers.allocate(bs, gamma, model.vocab, bs * (gamma + 1), torch.bfloat16, device)
     f32 = dict(dtype=torch.float32, device=device)
     i32 = dict(dtype=torch.int32, device=device)
@@ -117,20 +119,27 @@ def set_up(bs=4, gamma=3, seed=3, window=48, n_sink=4, max_tokens=400, device="c
     return model, prompts, cache, rules, inp, buf, S.sps_table(T_raw, np.zeros(0, np.int32), device)
 
 
-def generate(steps=20, temperature=0.0, seed=5, **kw):
-    """`steps` served steps; returns the prompts, what was generated for each and the set-up."""
+def generate(steps=20, temperature=0.0, seed=5, logprobs=None, on_step=None, **kw):
+    """`steps` served steps; returns the prompts, what was generated for each and the set-up.  on_step(buf, logprobs) is
+    called after each step; logprobs: how many alternatives to report, or None."""
     made = set_up(**kw)
     model, prompts, cache, rules, inp, buf, sps = made
+    report = None if logprobs is None else V.Logprobs.allocate(len(prompts), buf.gamma, model.vocab, logprobs,
+                                                               device=buf.packed.device)
     said = [[] for _ in prompts]
     for t in range(steps):
         for r in range(len(prompts)):
             cache.reserve(r, buf.gamma + 1)
-        V.run_served_step(inp, buf, sps, model.forward, cache, rules, temperature, seed, t)
+        V.run_served_step(inp, buf, sps, model.forward, cache, rules, temperature, seed, t, logprobs=report)
+        if on_step:
+            on_step(buf, report)
         out, lens = buf.out_tokens.tolist(), cache.ctx_len.tolist()
         for r, row in enumerate(out):
             said[r] += [x for x in row if x >= 0]
             cache.settle(r, lens[r])  # the exact length is known here: fewer pages are needed next
     status = B.dspark_read_device_status(buf.ws) or B.dspark_read_device_status(cache.ws)
+    if report is not None:
+        status = status or B.dspark_read_device_status(report.ws)
     if status != B.DSPARK_OK:
         raise B.DSparkError(status, "served step")
     return prompts, said, made
@@ -140,8 +149,21 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--temperature", type=float, default=0.0)
+    ap.add_argument("--eight-bit", action="store_true")
+    ap.add_argument("--top", type=int, default=None)
     a = ap.parse_args()
-    prompts, said, made = generate(a.steps, a.temperature)
+    reported = []
+
+    def note(buf, report):
+        if report is not None:
+            reported.append([x.tolist() for x in (buf.out_tokens, report.logprob, report.rank)])
+
+    prompts, said, made = generate(a.steps, a.temperature, logprobs=a.top, on_step=note, eight_bit=a.eight_bit)
     for r, s in enumerate(said):
         print(f"request {r}: prompt of {len(prompts[r])} tokens, {len(s)} tokens in {a.steps} steps "
               f"({len(s) / a.steps:.2f} a step): {s[:12]} ...")
+        if reported:
+            tokens, lp, rank = ([x for step in reported for x in step[k][r]] for k in range(3))
+            kept = [i for i, t in enumerate(tokens) if t >= 0]
+            print(f"  mean log probability {sum(lp[i] for i in kept) / len(kept):.3f}, "
+                  f"{sum(rank[i] == 1 for i in kept)} of {len(kept)} the likeliest")

@@ -154,6 +154,13 @@ __host__ __device__ __forceinline__ bool load_in_order(Fetch fetch, PutK put_k, 
   return ok;
 }
 
+// The place in a shared ring of the load of tile i's K, or V, where two warps load them in the same order: K 0, K 1, V 0, K 2,
+// V 1 and so on.
+__host__ __device__ __forceinline__ uint32_t ring_place(bool v, uint32_t i, uint32_t n_tiles) {
+  if (!v) return i < 2 ? i : 2 * i - 1;
+  return 2 * i + 2 < n_tiles + i ? 2 * i + 2 : n_tiles + i;
+}
+
 // A position in a ring of N slots.
 template <int N>
 struct Ring {

@@ -147,11 +147,6 @@ struct ShortWaiter {
 };
 __device__ __forceinline__ long long cycles_of(uint64_t ns) { return tc::deadline_after_ns(ns) - clock64(); }
 
-// The place of tile i's load in the ring's order, which is that of the products: K 0, K 1, V 0, K 2, V 1 and so on.
-__device__ __forceinline__ uint32_t ring_place(bool v, uint32_t i, uint32_t n_tiles) {
-  return v ? min(2 * i + 2, n_tiles + i) : i < 2 ? i : 2 * i - 1;
-}
-
 // Issue a tile's loads of codes.  One lane issues them all: issued by the blocks' own lanes, a load takes some 180 cycles.
 template <int D>
 __device__ __forceinline__ void issue_codes(const AttnArgs& a, const CUtensorMap* map, const TileLoad& t, uint32_t dst,

@@ -14,7 +14,7 @@
 namespace dspark {
 namespace {
 
-constexpr int kMaxAppendThreads = 256;
+constexpr int kMaxAppendThreads = 128;
 
 struct AppendArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -59,7 +59,7 @@ __device__ __forceinline__ uint2 codes8(const float* x, float by) {
 // The rotated K goes into 8 bits from fp32, with one rounding.  Products and sums of a pair are rounded one by one (no fused
 // multiply-add), so that the powers of two are those of any plain fp32 evaluation.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kMaxAppendThreads, 6) append8_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kMaxAppendThreads, 12) append8_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ RowPlace place;
   const int tid = threadIdx.x, lane = tid & 31;
   pdl_enter();
@@ -295,7 +295,7 @@ cudaError_t launch_append_kv8(const void* q, int64_t q_stride, const void* k, in
   a.bs = bs, a.rows = rows, a.max_pos = max_pos, a.rot = rot, a.max_pages = max_pages, a.n_pages = n_pages;
   a.page_shift = page_shift, a.Hq = q ? Hq : 0, a.Hkv = Hkv, a.D = D;
   const int items = (a.Hq + 2 * Hkv) * (D / 16);
-  // as many threads as share the items evenly: 384 items, 8191 rows, 192 threads 40.8 us, 256 45.6
+  // as many threads as share the items evenly: 384 items, 8191 rows, 128 threads 37.7 us, 192 38.7, 256 45.6
   const int rounds = (items + kMaxAppendThreads - 1) / kMaxAppendThreads;
   const dim3 block(((items + rounds - 1) / rounds + 31) / 32 * 32);
   return launch_pdl(interleaved ? append8_kernel<true> : append8_kernel<false>, dim3(rows), block, 0, s, a);

@@ -1,5 +1,5 @@
 """The target model's side of a step: the paged cache that takes the packed windows, the rules on the packed
-logits and the token history they read, around step.run_step.
+logits, the token history they read and the log probabilities that are reported, around step.run_step.
 
     cache = PagedCache(...); rules = LogitRules(...)
     run_served_step(inp, buf, sps, forward, cache, rules, ...)
@@ -45,14 +45,26 @@ class PagedCache:
     `advance` keeps what the verification accepted.  `bound` (host) is an upper bound of ctx_len: `reserve` raises it by a
     whole window each step, and only `settle` lowers it, by a length that has been read back.  Without it every
     rejected draft keeps its place and the cache fills too early; how late the length comes does not matter.  With a
-    window, `settle` also gives back the pages that the window has left behind."""
+    window, `settle` also gives back the pages that the window has left behind.
+
+    eight_bit: pages of e4m3 with an exponent byte for each position's K and V of each KV head (half the memory and half the
+    reads of a step).  One pair of bf16 pages, `wide`, serves all layers: prompts are read back into it, and read_back
+    leaves there what the packed rows see."""
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, Hq: int, Hkv: int, D: int, bs: int, max_pages: int,
-                 cos_sin, window: int = 0, n_sink: int = 0, interleaved: bool = False, device="cuda"):
+                 cos_sin, window: int = 0, n_sink: int = 0, interleaved: bool = False, device="cuda", eight_bit: bool = False):
         import torch
         shape = (n_pages, Hkv, page_size, D)
-        self.k = [torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(n_layers)]
-        self.v = [torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(n_layers)]
+
+        def pages(dtype, n, last=D):
+            bits = {torch.float8_e4m3fn: torch.uint8}.get(dtype, dtype)  # zeros of eight bits are zeros of e4m3
+            return [torch.zeros(shape[:3] + (last,), dtype=bits, device=device).view(dtype) for _ in range(n)]
+
+        dtype = torch.float8_e4m3fn if eight_bit else torch.bfloat16
+        self.k, self.v = pages(dtype, n_layers), pages(dtype, n_layers)
+        self.eight_bit = eight_bit
+        if eight_bit:
+            self.scale, self.wide = pages(torch.uint8, n_layers, 2), pages(torch.bfloat16, 2)
         self.page_size, self.Hq, self.window, self.n_sink = page_size, Hq, window, n_sink
         self.interleaved, self.cos_sin = interleaved, cos_sin
         self.page_table = torch.full((bs, max_pages), -1, dtype=torch.int32, device=device)
@@ -111,10 +123,26 @@ class PagedCache:
     def attend(self, layer: int, q, k, v, cu_seqlens, max_rows: int, scale: float, out, stream=None) -> None:
         """Rotate and append the packed rows' q, k, v, then attend: out [rows, Hq, D].  `out` is the rotated
         queries' place as well."""
+        if self.eight_bit:
+            pages = self.k[layer], self.v[layer], self.scale[layer]
+            B.dspark_append_kv8(q, k, v, cu_seqlens, self.ctx_len, self.cos_sin, self.page_table, out, *pages, self.ws,
+                                self.interleaved, stream)
+            B.dspark_window_attention_kv8(out, *pages, self.page_table, cu_seqlens, self.ctx_len, max_rows, scale,
+                                          self.window, self.n_sink, out, None, *self.wide, self.ws, stream)
+            return
         B.dspark_append_kv(q, k, v, cu_seqlens, self.ctx_len, self.cos_sin, self.page_table, out, self.k[layer],
                            self.v[layer], self.ws, self.interleaved, stream)
         B.dspark_window_attention(out, self.k[layer], self.v[layer], self.page_table, cu_seqlens, self.ctx_len, max_rows,
                                   scale, self.window, self.n_sink, out, None, self.ws, stream)
+
+    def read_back(self, layer: int, cu_seqlens, rows: int, stream=None):
+        """bf16 pages k, v, numbered as the cache's, that hold what the packed rows (of `rows` in all) see of a layer: an
+        8-bit cache's are `wide`, until the next layer that is read back or attends to a prompt."""
+        if not self.eight_bit:
+            return self.k[layer], self.v[layer]
+        B.dspark_read_kv8(self.k[layer], self.v[layer], self.scale[layer], self.page_table, cu_seqlens, self.ctx_len, rows,
+                          self.window, self.n_sink, self.page_table, *self.wide, self.ws, stream)
+        return tuple(self.wide)
 
     def advance(self, tokens, stream=None) -> None:
         """Keep `tokens` [bs] (device int32) more of each request."""
@@ -140,6 +168,36 @@ class LogitRules:
             B.dspark_process_logits(buf.packed, buf.cu, buf.ids, self.hist, self.repetition, self.frequency, self.presence,
                                     self.bias_start, self.bias_ids, self.bias_vals, self.mask(buf) if self.mask else None,
                                     buf.packed, buf.ws)
+
+
+@dataclasses.dataclass
+class Logprobs:
+    """What a step reports of the tokens that it commits, by the target's logits under the rules at `temperature`: for
+    out_tokens[r, j] its log probability, the entropy of its row, its rank, and the top_n likeliest ids.  Where
+    out_tokens is -1: 0, 0, 0, and ids -1 with -infinity."""
+    logprob: "object"        # [bs, gamma + 1] fp32
+    entropy: "object"        # [bs, gamma + 1] fp32
+    rank: "object"           # [bs, gamma + 1] int32, from 1
+    top_ids: "object"        # [bs, gamma + 1, top_n] int32, or None
+    top_logprobs: "object"   # [bs, gamma + 1, top_n] fp32, or None
+    ws: "object"
+    temperature: float = 1.0
+
+    @staticmethod
+    def allocate(bs: int, gamma: int, V: int, top_n: int = 0, temperature: float = 1.0, device="cuda") -> "Logprobs":
+        import torch
+        f32, i32 = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
+        n = gamma + 1
+        return Logprobs(torch.zeros((bs, n), **f32), torch.zeros((bs, n), **f32), torch.zeros((bs, n), **i32),
+                        torch.full((bs, n, top_n), -1, **i32) if top_n else None,
+                        torch.full((bs, n, top_n), float("-inf"), **f32) if top_n else None,
+                        B.alloc_logprobs_workspace(bs * n, V, top_n, device), temperature)
+
+    def take(self, buf, stream=None) -> None:
+        """Of buf.out_tokens, after a verification and before buf.packed is written anew."""
+        with _on(stream):
+            B.dspark_token_logprobs(buf.packed, buf.cu, buf.out_tokens, self.temperature, self.logprob, self.entropy,
+                                    self.rank, self.top_ids, self.top_logprobs, self.ws)
 
 
 def build_history(rules: LogitRules, prompts, V: int, ws, device="cuda", stream=None) -> None:
@@ -172,9 +230,10 @@ def take_outcome(inp: dict, buf: S.StepBuffers, cache: PagedCache, rules: LogitR
 
 def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache: PagedCache, rules: LogitRules,
                     temperature: float, seed: int, step: int, mode: int = B.DSPARK_COMPACT, tiers=None,
-                    stream=None, sched_mode: int = B.DSPARK_SCHED_EARLY_STOP, ring=None, side_stream=None) -> None:
+                    stream=None, sched_mode: int = B.DSPARK_SCHED_EARLY_STOP, ring=None, side_stream=None,
+                    logprobs: Optional[Logprobs] = None) -> None:
     """One step: draft, schedule and pack; the target forward over the packed windows, its logits under the
-    rules; the verification; then take_outcome.  mode, tiers, sched_mode, ring and side_stream as in step.run_step.
+    rules; the verification; with `logprobs` its report; then take_outcome.  mode, tiers, sched_mode, ring and side_stream as in step.run_step.
     A drafter that step.run_step does not run (the RNN head) takes the same way by hand: its draft and the pack,
     forward, rules.apply, step.verify with its states, take_outcome."""
 
@@ -184,4 +243,6 @@ def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache
 
     with _on(stream):
         S.run_step(inp, buf, sps, target, temperature, seed, step, mode, sched_mode, tiers, ring=ring, side_stream=side_stream)
+        if logprobs is not None:
+            logprobs.take(buf)
         take_outcome(inp, buf, cache, rules)
