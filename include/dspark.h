@@ -545,8 +545,8 @@ DSPARK_API int dspark_history_commit(const int32_t* out_tokens, int bs, int gamm
  *     K = code * 2^(kv_scale[.., 0] - 127),   V = code * 2^(kv_scale[.., 1] - 127);   byte 255: the vector is NaN
  * i.e. the power of two under which the vector's largest magnitude is at most 448 (all codes that an append writes are
  * numbers, the largest of a vector above 224 unless the vector is tiny or 0).  A value x is off by at most 2^-4 |x| where its
- * code is normal, by 2^-10 of the power of two below.  All three tensors begin at a multiple of 16 bytes.  Page table, lengths and limits are those of the bf16 cache, and
- * dtype is the queries', keys' and values' (bf16).
+ * code is normal, by 2^-10 of the power of two below.  All three tensors begin at a multiple of 16 bytes.  Page table,
+ * lengths and limits are those of the bf16 cache, and dtype is the queries', keys' and values' (bf16).
  *
  * append_kv8: dspark_append_kv with that cache.  The rotated K is rounded once, from fp32.  A vector with a NaN or an
  * infinity is written as NaN (byte 255, codes 0).  Device errors, limits and aliases as dspark_append_kv. */
@@ -574,10 +574,15 @@ DSPARK_API int dspark_read_kv8(const void* k_cache, const void* v_cache, const u
 
 /* dspark_window_attention over the 8-bit cache (the same formulas, arguments, workspace, errors and limits).
  *   k_scratch, v_scratch  device [n_pages, Hkv, page_size, D] bf16 each, or both NULL: pages of the same numbers that the
- *                         call may overwrite.  Windows of more than 128 (row, query head) pairs to a KV head (64 where
+ *                         call may overwrite.  Windows of more than 512 (row, query head) pairs to a KV head (128 where
  *                         D = 64), by max_rows, are then read back into them first, once for all rows (dspark_read_kv8), and
  *                         attended to there; without them the windows' kernel takes such calls too, more slowly.  One pair
- *                         serves all layers of a model.  Calls that can overlap on the device must not share it. */
+ *                         serves all layers of a model.  Calls that can overlap on the device must not share it.
+ * The products take the codes as they are, and each query and each weight as a sum of two e4m3 parts.  A query's lanes keep
+ * bf16's eight bits down to 2^-10 of the row's largest and are off by at most 2^-19 of that below; a weight is off by at most 2^-8 of
+ * itself, or by about 2^-20 of the row's largest weight where V's powers of two are alike (where a V's power lies 2^k below
+ * the largest of its tile, by 2^(k - 20) of what that V is worth).  A row that sees a vector of NaN (byte 255), in K or in V, is NaN,
+ * lse included, and no other row is.  Magnitudes of K beyond 2^100 may overflow fp32 on the way to a score. */
 DSPARK_API int dspark_window_attention_kv8(const void* q, int64_t q_stride, int dtype, const void* k_cache,
                                            const void* v_cache, const uint8_t* kv_scale, const int32_t* page_table,
                                            int max_pages, int n_pages, int page_size, const int32_t* cu_seqlens,

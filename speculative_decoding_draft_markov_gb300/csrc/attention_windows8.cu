@@ -28,14 +28,8 @@ constexpr int kGroups = 4, kThreads = (kGroups + 2) * 128;
 constexpr int kKWarp = 4 * kGroups, kMmaWarp = kKWarp + 2, kVWarp = kMmaWarp + 2, kSplitWarp = kVWarp + 2;
 // Registers: launched with 512 x 128; the softmax warps take what the others give back (256 x 184 + 256 x 72 = 512 x 128).
 constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
-#ifndef KV8_SLOTS
-#define KV8_SLOTS 8
-#endif
-#ifndef KV8_QBUFS
-#define KV8_QBUFS 2
-#endif
-constexpr int kMaxSlots = KV8_SLOTS;
-constexpr int kQBufs = KV8_QBUFS, kQRing = 4;  // units whose Q, whose rows' factors are kept
+constexpr int kMaxSlots = 8;
+constexpr int kQBufs = 2, kQRing = 4;  // units whose Q, whose rows' factors are kept
 // m lies kTop below a maximum; a score and a value's power together may outgrow the references up to kMost (e4m3 ends at
 // 448 = 2^8.8)
 constexpr float kTop = 6.f, kMost = 8.75f;
@@ -119,7 +113,7 @@ struct ShortWaiter {
     const uint32_t b = tc::smem_u32(bar);
     bool ok = true;
     long long deadline = 0;
-    while (!tc::mbar_try_wait_suspend(b, parity, 20000u)) {
+    while (!tc::mbar_try_wait(b, parity)) {
       const long long now = clock64();
       if (deadline == 0) deadline = now + cycles;
       if (*abort || now > deadline) {
@@ -134,7 +128,7 @@ struct ShortWaiter {
     const uint32_t b = tc::smem_u32(bar), b2 = tc::smem_u32(bar2);
     bool ok = true;
     long long deadline = 0;
-    while (!(tc::mbar_try_wait_suspend(b, parity, 20000u) & tc::mbar_try_wait_suspend(b2, parity2, 20000u))) {
+    while (!(tc::mbar_try_wait(b, parity) & tc::mbar_try_wait(b2, parity2))) {
       const long long now = clock64();
       if (deadline == 0) deadline = now + cycles;
       if (*abort || now > deadline) {
@@ -591,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < RW; i += 4) top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
-            if (__any_sync(~0u, top + float(max(0, v_byte - f)) > kMost) && lane == 0) sh->need[grp][at] = t + 1;
+            // (a V far beyond f is looked at however little it weighs: its weight would leave fp32)
+            if (__any_sync(~0u, top + float(max(0, v_byte - f)) > kMost || v_byte - f > 60) && lane == 0) sh->need[grp][at] = t + 1;
             arrive();
           }
 #pragma unroll

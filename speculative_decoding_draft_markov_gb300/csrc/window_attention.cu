@@ -208,8 +208,10 @@ cudaError_t launch_window_attention_kv8(const void* q, int64_t q_stride, const v
                                         int max_rows, int Hq, int Hkv, int D, float scale, int window, int n_sink,
                                         void* out, float* lse, void* k_scratch, void* v_scratch, void* ws,
                                         cudaStream_t s) {
-  if (k_scratch && max_rows > kWindow8Rows / (Hq / Hkv)) {
-    // every unit of 256 rows would convert K and V for itself: converted once, for all of a request's units
+  // Read back once for all of a request's units, or read in 8 bits by each unit of 128 rows?  GB300, 8 KV heads, 4000 positions, 64
+  // requests: D 64, 128 rows to a KV head 188 us by the windows' kernel and 284 read back, 136 rows 341 and 302; D 128, 256 rows 362 and
+  // 525, 512 rows (32 requests) 365 and 369.  256 requests, window 256: D 128, 128 rows 161 and 215, 256 rows 289 and 249.
+  if (k_scratch && int64_t(max_rows) * (Hq / Hkv) > (D == 64 ? 128 : 512)) {
     const cudaError_t e = launch_read_kv8(k_cache, v_cache, kv_scale, page_table, max_pages, n_pages, page_shift, cu, ctx, bs,
                                           rows, Hkv, D, window, n_sink, page_table, n_pages, k_scratch, v_scratch,
                                           static_cast<uint32_t*>(ws), s);
