@@ -14,6 +14,18 @@
 // powers 2^ev have to go into P.  P is kept inside e4m3's range by two references, a row's m, which lies kTop below its
 // maximum of a unit's first tile, and f, the largest ev of the tile's slots; both are checked on each tile against kMost, and
 // set anew where they are outgrown, O^T and the sums with them.
+//
+// GB300, 8 KV heads: D 128, 256 windows of 8 rows, window 1024, 118 us (81.5 by its bytes; over a bf16 cache 175); 2 requests of
+// 16 rows over 125000 positions 102 us (77; 154); one token over 1500 positions 10.4 (9.7); D 64, 64 windows of 64 rows to a KV
+// head, window 4096, 94 us (33; 83).  What bounds it is the chain of a tile's steps, some 3200 cycles for a pipeline with 64
+// rows, and the softmax warps' instructions (0.6 of the issue slots): a satisfied wait costs about 200 cycles, a TMA load its
+// warp 180, so K and V have a warp each (one for both took 3000 cycles a tile) and the exponent bytes come by 8-byte
+// asynchronous copies (1000 cycles of bulk copies before).  The code has to stay small: with every step inlined where it is used
+// (172 KB of instructions) the first three took 201 us, with each step there once 147.
+// Slower, in us for 256 windows / 125000 positions / 64 rows: V converted to fp16 by four warps and P in fp16 237 / 178 / 178;
+// eight softmax warps of 184 registers 129 / 116 / 109 where sixteen took 123 / 105 / 98; blocks of 64 slots 126 / 104 / 98
+// beside the same; waits that may sleep 123 / 105 / 98 beside 118 / 102 / 94.  Q split by plain loads took 33000 cycles for 64
+// rows, copied to where it is split 20000.
 #include "attention_common.cuh"
 #include "kv8.cuh"
 
@@ -26,7 +38,7 @@ using namespace attn;
 // warp that loads K, one that issues the products and one that loads V, and two warps that split Q (both for a lone pipeline).
 constexpr int kGroups = 4, kThreads = (kGroups + 2) * 128;
 constexpr int kKWarp = 4 * kGroups, kMmaWarp = kKWarp + 2, kVWarp = kMmaWarp + 2, kSplitWarp = kVWarp + 2;
-// Registers: launched with 512 x 128; the softmax warps take what the others give back (256 x 184 + 256 x 72 = 512 x 128).
+// Registers: launched with 768 x 80; the softmax warps take what the others give back (512 x 96 + 256 x 48 = 768 x 80).
 constexpr int kSoftmaxRegs = 96, kOtherRegs = 48;
 constexpr int kMaxSlots = 8;
 constexpr int kQBufs = 2, kQRing = 4;  // units whose Q, whose rows' factors are kept

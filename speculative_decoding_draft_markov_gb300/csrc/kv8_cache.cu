@@ -56,6 +56,9 @@ __device__ __forceinline__ uint2 codes8(const float* x, float by) {
 // row; an item is 16 lanes of one head: rotated by halves, lanes t .. t+7 and their partners t + rot/2 ..; otherwise 16
 // lanes in a row (8 interleaved pairs, or lanes that pass).  So each thread holds both lanes of its pairs and q_out may be q,
 // and a head's D / 16 items lie in neighbouring lanes of one warp, which agree on the head's power of two.
+// GB300, Hq 32, Hkv 8, D 128: 8191 rows 37.7 us (26.8 by their bytes), one row 6.2, of which most is the call.  Bound by the
+// instructions between a row's loads (half of the issue slots) and by registers, 40 to hold an item: with 32 it took 54.8; 256
+// threads, which leave half of them idle in a row's second turn, 45.6, 192 threads 38.7, two items at a time 45.1.
 // The rotated K goes into 8 bits from fp32, with one rounding.  Products and sums of a pair are rounded one by one (no fused
 // multiply-add), so that the powers of two are those of any plain fp32 evaluation.
 template <bool kInterleaved>
@@ -183,6 +186,8 @@ __device__ __forceinline__ void widen16(uint4 w, float by, uint4* out) {
 // What a request's packed rows see, in blocks of the cache (pages, or 32-slot pieces of larger pages): those that hold
 // sinks, then those of the window.  Blocks are counted over the requests; a unit is a block of one KV head, and the units are
 // dealt out to the grid's warps in turn.
+// A copy that doubles in size: bound by memory.  GB300, what 64 windows of 4096 see, D 64: 118 us (92 by
+// its bytes); a block for each unit 142, five blocks on an SM 138, three 134.
 template <int D>
 __global__ void __launch_bounds__(kReadThreads, 4) read8_kernel(const __grid_constant__ ReadArgs a) {
   __shared__ long long before[DSPARK_MAX_BS + 1];  // blocks of the requests before

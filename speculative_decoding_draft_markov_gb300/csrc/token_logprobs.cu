@@ -6,6 +6,12 @@
 // The alternatives come from a threshold that n ids at least reach: each warp's share of n among its lanes' maxima, the
 // least over the warps.  Each thread keeps the maxima of four parts of its ids, so that only parts that reach the threshold,
 // some dozen of 1024, are looked at again; what reaches it there (some dozen ids) is ranked by counting.
+//
+// GB300, V 151936, bf16, 761 tokens (256 windows of 1 to 8 rows) with rank and 20 alternatives: 69 us (34.6 by their bytes), 59
+// without alternatives, with or without the rank.  Bound by instructions (0.66 of the issue slots; 11 for a logit) and, at
+// one block for a token, by the last wave.  One token with 5 alternatives 9.2, without 5.2: a launch, then the second look, the
+// segments' meeting.  Slower, with 20 alternatives, where this form took 73: half rows 78, quarters 90; equal ranges over persistent
+// blocks 113; a second look for the rank too 94; 5 to 8 blocks an SM 76 to 150; 512 threads 74 to 82.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -25,7 +31,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kParts = 4;    // of a thread's ids, each with a maximum of its own
 constexpr int kRoom = 512;   // ids that may reach the threshold; with more, the alternatives are found one by one
 constexpr int kMaxSegments = 128;
-constexpr float kSlack = 8.f;  // what d may grow to: W / S and log2 S cancel to 2^-21
+constexpr float kSlack = 20.f;  // what d may grow to before m moves; at the end m is a thread's maximum
 // Logits below -kPlain count as that, so that no mask's value (-inf times the weight 0 is NaN) needs care; a segment without
 // any above it, or a temperature under which it would weigh something, is summed with care.
 constexpr float kPlain = 0x1.9200000000000p+99f;  // 9.95e29, exact in bf16
@@ -218,10 +224,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprobs_ker
       most = fmaxf(most, top);
       if (top > m + a.slack && top > -kPlain) refer(top);  // (m * c2 is rounded: of a raised logit that would be far off)
       if (top >= chosen_raised) {
-        Eight<T> raw = {};
         float r[8];
-        raw.load(row + lo + p * 8);
-        raw.get(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = l[j];
+        if (chosen_raised == -kPlain) {  // as they are, not raised
+          Eight<T> raw = {};
+          raw.load(row + lo + p * 8);
+          raw.get(r);
+        }
         // ids before the token stand before it with its own logit too
         const int id0 = lo + p * 8;
 #pragma unroll
@@ -245,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprobs_ker
       ++q;
     }
   }
+  if (all > m && all > -kPlain) refer(all);
   const bool some = __syncthreads_or(all > -kPlain), huge = __syncthreads_or(all >= kPlain);
   if (!some || huge || c2 * kPlain < 400.f || c2 > 1e7f) {  // (c2 beyond: d would overflow, and 0 * -inf is NaN)
     m = kLowest, s2 = w2 = 0ull;
