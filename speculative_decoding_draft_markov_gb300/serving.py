@@ -236,6 +236,8 @@ def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache
     rules; the verification; with `logprobs` its report; then take_outcome.  mode, tiers, sched_mode, ring and side_stream as in step.run_step.
     A drafter that step.run_step does not run (the RNN head) takes the same way by hand: its draft and the pack,
     forward, rules.apply, step.verify with its states, take_outcome."""
+    if logprobs is not None and logprobs.logprob.shape != buf.out_tokens.shape:
+        raise ValueError("logprobs must be of the step's requests and gamma")
 
     def target(b: S.StepBuffers) -> None:
         forward(b, cache)

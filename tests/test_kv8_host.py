@@ -66,3 +66,14 @@ def test_exponent_bytes(host):
             got = host.exponent_byte(int(x.view(np.uint32)))
             assert got == int(K.exponent_byte(np.array([[float(x)]]))[0]), (e, m)
     assert host.exponent_byte(0) == 1 and host.exponent_byte(0x7F800000) == 255 and host.exponent_byte(0x7FC00000) == 255
+
+
+def test_a_step_refuses_a_report_of_other_sizes(host):
+    """Before anything of the step has run."""
+    class Buf:
+        out_tokens = torch.zeros(2, 4, dtype=torch.int32)
+
+    for bs, gamma in ((3, 3), (2, 2)):
+        with pytest.raises(ValueError, match="logprobs"):
+            V.run_served_step({}, Buf, None, None, None, None, 1.0, 0, 0,
+                              logprobs=V.Logprobs.allocate(bs, gamma, 64, 0, device="cpu"))
