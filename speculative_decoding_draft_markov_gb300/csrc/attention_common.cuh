@@ -237,10 +237,12 @@ __device__ __forceinline__ Cut plan_ranges(const AttnArgs& a, Start* start, Plan
   constexpr uint32_t kTooMany = 1u << 31;
   bool is_long = false;
   if (tid < a.bs) {
-    row = a.cu[tid], n = a.cu[tid + 1] - row, c = a.ctx[tid];
-    if (row < 0 || n < 0 || row + n > a.rows) {
+    const int end = a.cu[tid + 1];
+    row = a.cu[tid], c = a.ctx[tid];
+    if (row < 0 || end < row || end > a.rows) {
       p.bad = 1;
-    } else if (n > 0) {
+    } else if (end > row) {
+      n = end - row;
       if (c < 0 || int64_t(c) + n > a.cache_limit) {
         if (blockIdx.x == 0) set_status(a.status, DSPARK_EINVAL);
       } else if (n > 4 * unit_tokens) {  // many units: summed by the whole block below

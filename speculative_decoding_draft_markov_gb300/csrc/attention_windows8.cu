@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* factor = sh->row_factor[set][units % kQRing] + row0;
       ok = wait(&sh->q_ready[set][units % kQRing], (units / kQRing) & 1);
       if (!ok) break;
-      int f = 1;  // the reference of V's powers of two, as an exponent byte
+      int f = 1, f_top = 1;  // the reference of V's powers of two, as an exponent byte, and the largest one so far
       float l[RW];  // this slot's share of the rows' sums
 #pragma unroll
       for (int i = 0; i < RW; ++i) l[i] = 0.f;
@@ -552,8 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float (*part)[RW] = sh->warp_max[grp];
             const int* byte = sh->warp_byte[grp];
             const int f_old = f;
-            // f may fall, too: O^T keeps its place in fp32, and this tile's weights theirs in e4m3
-            f = max(max(max(byte[0], byte[1]), max(byte[2], byte[3])), max(f - 40, 1));
+            // f may fall, too, so that this tile's weights keep their place in e4m3, but not so far that O^T leaves fp32: its terms
+            // are below 2^18 2^70
+            f = max(max(max(byte[0], byte[1]), max(byte[2], byte[3])), max(f_top - 70, 1));
+            f_top = max(f_top, f);
 #pragma unroll
             for (int k = 0; k < kFolds; ++k) {
               const int row = k * 32 + lane;

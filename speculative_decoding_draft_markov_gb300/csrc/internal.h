@@ -134,7 +134,7 @@ cudaError_t launch_append_kv8(const void* q, int64_t q_stride, const void* k, in
 cudaError_t launch_read_kv8(const void* k_cache, const void* v_cache, const uint8_t* kv_scale, const int32_t* page_table,
                             int max_pages, int n_pages, int page_shift, const int32_t* cu, const int32_t* ctx, int bs,
                             int rows, int Hkv, int D, int window, int n_sink, const int32_t* out_table, int n_out_pages,
-                            void* k_out, void* v_out, uint32_t* status, cudaStream_t s);
+                            void* k_out, void* v_out, bool attended, uint32_t* status, cudaStream_t s);
 cudaError_t launch_window_attention_kv8(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
                                         const uint8_t* kv_scale, const int32_t* page_table, int max_pages, int n_pages,
                                         int page_shift, const int32_t* cu, const int32_t* ctx, int bs, int rows,

@@ -167,6 +167,7 @@ struct ReadArgs {
   uint32_t* status;
   int64_t cache_limit;
   int max_pages, n_pages, page_shift, block_shift, bs, rows, Hkv, D, window, n_sink, n_out_pages;
+  bool attended;  // by products over whole tiles, next
 };
 
 constexpr int kReadThreads = 256;
@@ -200,10 +201,11 @@ __global__ void __launch_bounds__(kReadThreads, 4) read8_kernel(const __grid_con
   __syncthreads();
   int mine = 0;
   if (tid < a.bs) {
-    const int row = a.cu[tid], n = a.cu[tid + 1] - row, c = a.ctx[tid];
-    if (row < 0 || n < 0 || row + n > a.rows) {
+    const int row = a.cu[tid], next = a.cu[tid + 1], c = a.ctx[tid];
+    if (row < 0 || next < row || next > a.rows) {
       bad = 1;
-    } else if (n > 0) {
+    } else if (next > row) {
+      const int n = next - row;
       if (c < 0 || int64_t(c) + n > a.cache_limit) {
         if (blockIdx.x == 0) set_status(a.status, DSPARK_EINVAL);
       } else {
@@ -256,7 +258,9 @@ __global__ void __launch_bounds__(kReadThreads, 4) read8_kernel(const __grid_con
     const int pos = pos0 + lane;
     const bool mine = lane < 1 << bsh && pos < end && (pos >= lo || pos < sinks);
     const uint32_t seen = __ballot_sync(~0u, mine);
-    const uint32_t bytes = mine ? reinterpret_cast<const uint16_t*>(a.kv_scale)[src + lane] : 0u;
+    uint32_t bytes = mine ? reinterpret_cast<const uint16_t*>(a.kv_scale)[src + lane] : 0u;
+    // A V of NaN would reach rows that do not see it, as 0 * NaN, and leave the log-sum-exp: its K is NaN instead
+    if (a.attended && ((bytes & 0xFFu) == kv8::kNan || bytes >> 8 == kv8::kNan)) bytes = 127u << 8 | kv8::kNan;
     const uint4* ks = reinterpret_cast<const uint4*>(a.k_cache) + src * kPerSlot + lane;
     const uint4* vs = reinterpret_cast<const uint4*>(a.v_cache) + src * kPerSlot + lane;
     uint4* ko = reinterpret_cast<uint4*>(a.k_out) + (dst * kPerSlot + lane) * 2;
@@ -309,7 +313,7 @@ cudaError_t launch_append_kv8(const void* q, int64_t q_stride, const void* k, in
 cudaError_t launch_read_kv8(const void* k_cache, const void* v_cache, const uint8_t* kv_scale, const int32_t* page_table,
                             int max_pages, int n_pages, int page_shift, const int32_t* cu, const int32_t* ctx, int bs,
                             int rows, int Hkv, int D, int window, int n_sink, const int32_t* out_table, int n_out_pages,
-                            void* k_out, void* v_out, uint32_t* status, cudaStream_t s) {
+                            void* k_out, void* v_out, bool attended, uint32_t* status, cudaStream_t s) {
   ReadArgs a;
   a.k_cache = static_cast<const uint8_t*>(k_cache), a.v_cache = static_cast<const uint8_t*>(v_cache);
   a.kv_scale = kv_scale, a.page_table = page_table, a.cu = cu, a.ctx = ctx, a.out_table = out_table;
@@ -317,7 +321,7 @@ cudaError_t launch_read_kv8(const void* k_cache, const void* v_cache, const uint
   a.cache_limit = std::min(int64_t(max_pages) << page_shift, int64_t(1) << 30);  // positions: well inside 32 bits
   a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, 5);
   a.bs = bs, a.rows = rows, a.Hkv = Hkv, a.D = D, a.window = window >= a.cache_limit ? 0 : window, a.n_sink = n_sink;
-  a.n_out_pages = n_out_pages;
+  a.n_out_pages = n_out_pages, a.attended = attended;
   const dim3 grid(tch::sm_count() * 4);
   return D == 64 ? launch_pdl(read8_kernel<64>, grid, dim3(kReadThreads), 0, s, a)
                  : launch_pdl(read8_kernel<128>, grid, dim3(kReadThreads), 0, s, a);

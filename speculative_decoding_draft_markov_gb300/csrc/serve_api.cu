@@ -178,7 +178,7 @@ int dspark_read_kv8(const void* k_cache, const void* v_cache, const uint8_t* kv_
   if (int e = check_status_ws(ws, ws_bytes)) return e;
   return cuda_status(launch_read_kv8(k_cache, v_cache, kv_scale, page_table, max_pages, n_pages, log2_of(page_size),
                                      cu_seqlens, ctx_len, bs, rows, Hkv, D, window, n_sink, out_table, n_out_pages, k_out,
-                                     v_out, static_cast<uint32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+                                     v_out, false, static_cast<uint32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dspark_window_attention_kv8(const void* q, int64_t q_stride, int dtype, const void* k_cache, const void* v_cache,

@@ -60,9 +60,9 @@ __device__ __forceinline__ Item item_of(const LogprobArgs& a, int i, bool report
   int row = i;
   bool ok = t.token >= 0 && t.token < a.V;
   if (a.cu) {
-    const int r = i / a.per, first = a.cu[r], end = a.cu[r + 1];
-    row = first + (i - r * a.per);
-    ok = ok && first >= 0 && end <= a.rows && row < end;
+    const int r = i / a.per, j = i - r * a.per, first = a.cu[r], end = a.cu[r + 1];
+    ok = ok && first >= 0 && first <= end && end <= a.rows && j < end - first;
+    row = ok ? first + j : 0;
   }
   if (ok)
     t.row = row;

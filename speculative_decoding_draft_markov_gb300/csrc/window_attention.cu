@@ -213,7 +213,7 @@ cudaError_t launch_window_attention_kv8(const void* q, int64_t q_stride, const v
   // 525, 512 rows (32 requests) 365 and 369.  256 requests, window 256: D 128, 128 rows 161 and 215, 256 rows 289 and 249.
   if (k_scratch && int64_t(max_rows) * (Hq / Hkv) > (D == 64 ? 128 : 512)) {
     const cudaError_t e = launch_read_kv8(k_cache, v_cache, kv_scale, page_table, max_pages, n_pages, page_shift, cu, ctx, bs,
-                                          rows, Hkv, D, window, n_sink, page_table, n_pages, k_scratch, v_scratch,
+                                          rows, Hkv, D, window, n_sink, page_table, n_pages, k_scratch, v_scratch, true,
                                           static_cast<uint32_t*>(ws), s);
     return e != cudaSuccess ? e
                             : launch_window_attention(q, q_stride, k_scratch, v_scratch, page_table, max_pages, n_pages,

@@ -189,3 +189,73 @@ def test_two_streams_at_once():
                 call(ws, scratch, out, max_rows, s)
         torch.cuda.synchronize()
         assert all(torch.equal(out, want) for _, _, _, out in made)
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_vectors_of_nan_among_pages_read_back(which):
+    """By way of bf16 pages, too, a vector of NaN reaches the rows that see it and no other row, log-sum-exps included."""
+    c = Cache8([4, 4], [150, 150], 1, 64, 16, seed=30)
+    c.scale[c.table[0, 151 // 16], 0, 151 % 16, which] = 255  # row 1's own position
+    ws, q = B.alloc_attention_workspace(2, 1, 64), torch.randn(11, 2, 64, generator=torch.Generator().manual_seed(32))
+    for max_rows, scratch in ((4, (None, None)), (200, c.scratch())):
+        out = torch.zeros(11, 2, 64, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(11, 2, device="cuda")
+        B.dspark_window_attention_kv8(q.to(torch.bfloat16).cuda(), c.k, c.v, c.scale, c.table, c.cu, c.ctx, max_rows, 0.125, 0,
+                                      0, out, lse, *scratch, ws)
+        assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+        for got in (out, lse):
+            assert torch.isnan(got[1:4]).all() and not torch.isnan(got[0]).any() and not torch.isnan(got[4:]).any()
+
+
+def test_values_that_fall_by_powers_of_two():
+    """V's powers of two fall by 40 from tile to tile while one head's scores grow, so that the tiles' references are set anew
+    each time: another head, whose scores do not change, keeps its output of the first tile's size."""
+    d, page, n, ctx, bs = 64, 32, 1, 1023, 250
+    c = Cache8([n], [ctx], 1, d, page, seed=60, spread=0)
+    pos = np.arange(ctx + n)
+    tile = pos // 128
+    up = np.array([0, -40, -80, -110, -110, -110, -110, -110])[tile]
+    c.keys[0] = np.repeat((8.0 * tile)[:, None, None], d, 2)
+    c.vals[0] = c.vals[0] * 2.0 ** up[:, None, None]
+    byte = K.exponent_byte(c.keys[0])
+    table = c.table.cpu().numpy()[0]
+    k, s = _codes(c.k).copy(), c.scale.cpu().numpy().copy()
+    k[table[pos // page], :, pos % page] = K.codes(c.keys[0], byte)
+    s[table[pos // page], :, pos % page, 0] = byte
+    s[table[pos // page], :, pos % page, 1] += up[:, None].astype(np.uint8)
+    c.k, c.scale = torch.from_numpy(k).cuda().view(F8), torch.from_numpy(s).cuda()
+    q = torch.ones(bs * n, 2, d, dtype=torch.bfloat16, device="cuda")
+    q[:, 1] = 0.0
+    cu = torch.arange(0, bs * n + 1, n, dtype=torch.int32, device="cuda")
+    ws, out = B.alloc_attention_workspace(2, 1, d), torch.zeros_like(q)
+    B.dspark_window_attention_kv8(q, c.k, c.v, c.scale, c.table.repeat(bs, 1), cu, c.ctx.repeat(bs), n, 1.0 / d, 0, 0, out,
+                                  None, None, None, ws)
+    assert B.dspark_read_device_status(ws) == B.DSPARK_OK
+    ref, _, mag = R.attention(_f64(q)[:n], c.keys[0], c.vals[0], ctx, 1.0 / d, 0, 0)
+    assert (np.abs(_f64(out).reshape(bs, n, 2, d) - ref) <= R.attention_bound(mag)).all()
+
+
+@pytest.mark.parametrize("list_", [[2 ** 31 - 1, -2 ** 31], [2 ** 31 - 1, 4], [5, -2 ** 31 + 8], [2, 2 ** 31 - 1], [-2 ** 31, 1]])
+def test_lists_at_the_ends_of_32_bits(list_):
+    """A list of windows whose differences pass 32 bits is refused by each call, and nothing is written."""
+    c = Cache8([4], [20], 1, 64, 16, seed=61)
+    cu = torch.tensor(list_, dtype=torch.int32, device="cuda")
+    q = torch.ones(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    wide = c.scratch()
+    ws = B.alloc_attention_workspace(2, 1, 64)
+
+    def refused(call):
+        out = torch.full_like(q, 7.0)
+        call(out)
+        assert B.dspark_read_device_status(ws) == B.DSPARK_EINVAL and (out == 7.0).all()
+
+    refused(lambda out: B.dspark_window_attention_kv8(q, c.k, c.v, c.scale, c.table, cu, c.ctx, 4, 0.125, 0, 0, out, None, None,
+                                                      None, ws))
+    refused(lambda out: B.dspark_window_attention_kv8(q, c.k, c.v, c.scale, c.table, cu, c.ctx, 400, 0.125, 0, 0, out, None,
+                                                      *wide, ws))
+    refused(lambda out: B.dspark_window_attention(q, *wide, c.table, cu, c.ctx, 4, 0.125, 0, 0, out, None, ws))
+    refused(lambda out: B.dspark_window_attention(q, *wide, c.table, cu, c.ctx, 400, 0.125, 0, 0, out, None, ws))
+    refused(lambda out: B.dspark_read_kv8(c.k, c.v, c.scale, c.table, cu, c.ctx, 4, 0, 0, c.table, *wide, ws))
+    assert all(torch.isnan(w).all() for w in wide)
+    refused(lambda out: B.dspark_append_kv8(q, q[:, :1], q[:, 1:], cu, c.ctx, torch.from_numpy(_table(100, 64)).cuda(), c.table,
+                                            out, c.k, c.v, c.scale, ws))

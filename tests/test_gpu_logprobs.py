@@ -226,3 +226,15 @@ def test_same_bits_on_another_stream_and_in_a_graph(n, per, top):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("cu", [[2 ** 31 - 1, 4], [2 ** 31 - 1, -2 ** 31], [2 ** 31 - 2, 2], [5, 3], [-2 ** 31, 1]])
+def test_lists_at_the_ends_of_32_bits(cu):
+    """A window whose rows' numbers pass 32 bits asks nothing, on whole rows and on segments."""
+    x = _logits(4, 20000, torch.float32, 11)
+    ws = B.alloc_logprobs_workspace(4, 20000, 2)
+    outs = _outputs(1, 4, 2)
+    B.dspark_token_logprobs(x, torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                            torch.tensor([[5, 6, 7, 8]], dtype=torch.int32, device="cuda"), 1.0, *outs, ws)
+    assert B.dspark_read_device_status(ws) == B.DSPARK_EINVAL
+    assert (outs[0] == 0).all() and (outs[2] == 0).all() and (outs[3] == -1).all()
