@@ -322,7 +322,9 @@ cudaError_t launch_read_kv8(const void* k_cache, const void* v_cache, const uint
   a.max_pages = max_pages, a.n_pages = n_pages, a.page_shift = page_shift, a.block_shift = std::min(page_shift, 5);
   a.bs = bs, a.rows = rows, a.Hkv = Hkv, a.D = D, a.window = window >= a.cache_limit ? 0 : window, a.n_sink = n_sink;
   a.n_out_pages = n_out_pages, a.attended = attended;
-  const dim3 grid(tch::sm_count() * 4);
+  // a warp for each block that the page table can hold, where that is fewer
+  const int64_t most = (int64_t(bs) * (a.cache_limit >> a.block_shift) * Hkv + kReadThreads / 32 - 1) / (kReadThreads / 32);
+  const dim3 grid(unsigned(std::min(int64_t(tch::sm_count()) * 4, std::max(most, int64_t(1)))));
   return D == 64 ? launch_pdl(read8_kernel<64>, grid, dim3(kReadThreads), 0, s, a)
                  : launch_pdl(read8_kernel<128>, grid, dim3(kReadThreads), 0, s, a);
 }
