@@ -56,17 +56,34 @@ __device__ __forceinline__ uint2 codes8(const float* x, float by) {
 // row; an item is 16 lanes of one head: rotated by halves, lanes t .. t+7 and their partners t + rot/2 ..; otherwise 16
 // lanes in a row (8 interleaved pairs, or lanes that pass).  So each thread holds both lanes of its pairs and q_out may be q,
 // and a head's D / 16 items lie in neighbouring lanes of one warp, which agree on the head's power of two.
-// GB300, Hq 32, Hkv 8, D 128: 8191 rows 37.7 us (26.8 by their bytes), one row 6.2, of which most is the call.  Bound by the
-// instructions between a row's loads (half of the issue slots) and by registers, 40 to hold an item: with 32 it took 54.8; 256
-// threads, which leave half of them idle in a row's second turn, 45.6, 192 threads 38.7, two items at a time 45.1.
+// GB300, Hq 32, Hkv 8, D 128: 8191 rows 36.3 us (26.8 by their bytes), one row 6.2, of which most is the call.  Bound by a
+// block's chain (its row's place, an item's lanes, the head's maximum) and by the instructions between (half of the issue
+// slots).  A thread's next item is asked for before this one is turned; without that 37.4, with the first one alone asked for
+// early 38.3 (10 blocks an SM) and 39.7 (12).  256 threads, which leave half of them idle in a row's second turn, took 45.6
+// where 128 took 37.7, 192 threads 38.7, two items at a time 45.1, registers for 16 blocks 54.8, for 8 36.9.
 // The rotated K goes into 8 bits from fp32, with one rounding.  Products and sums of a pair are rounded one by one (no fused
 // multiply-add), so that the powers of two are those of any plain fp32 evaluation.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kMaxAppendThreads, 12) append8_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kMaxAppendThreads, 10) append8_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ RowPlace place;
   const int tid = threadIdx.x, lane = tid & 31;
   pdl_enter();
   const int row = blockIdx.x;
+  const int per_head = a.D / 16, turned = a.rot / 16, items = (a.Hq + 2 * a.Hkv) * per_head;
+  uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+  auto fetch = [&](int it) {  // an item's lanes: in time for a thread's next turn, the first while the row's place is looked up
+    if (it >= items) return;
+    const int hh = it / per_head, c = it - hh * per_head;
+    const bool is_q = hh < a.Hq, is_k = !is_q && hh < a.Hq + a.Hkv;
+    const int kv = is_q ? 0 : hh - a.Hq - (is_k ? 0 : a.Hkv);
+    const __nv_bfloat16* src = is_q   ? a.q + int64_t(row) * a.q_stride + hh * a.D
+                               : is_k ? a.k + int64_t(row) * a.k_stride + kv * a.D
+                                      : a.v + int64_t(row) * a.v_stride + kv * a.D;
+    const bool halves = !kInterleaved && !(hh >= a.Hq + a.Hkv) && c < turned;
+    const int lo = halves ? c * 8 : c * 16, hi = halves ? lo + a.rot / 2 : lo + 8;
+    x = *reinterpret_cast<const uint4*>(src + lo), y = *reinterpret_cast<const uint4*>(src + hi);
+  };
+  fetch(tid);
   if (tid < 32) {
     const int r = warp_request_of(a.cu, a.bs, a.rows, row, lane);
     if (lane == 0) {
@@ -92,27 +109,21 @@ __global__ void __launch_bounds__(kMaxAppendThreads, 12) append8_kernel(const __
   }
   __syncthreads();
 
-  const int per_head = a.D / 16, turned = a.rot / 16;
   const RowPlace pl = place;
   if (pl.pos < 0) return;
-  const int items = (a.Hq + 2 * a.Hkv) * per_head;
   for (int first = tid - lane; first < items; first += int(blockDim.x)) {  // the warp's: all its lanes agree below
     const int it = first + lane;
     const bool live = it < items;
     const int hh = live ? it / per_head : 0, c = live ? it - hh * per_head : 0;
     const bool is_q = hh < a.Hq, is_k = !is_q && hh < a.Hq + a.Hkv;
     const int kv = is_q ? 0 : hh - a.Hq - (is_k ? 0 : a.Hkv);
-    const __nv_bfloat16* src = is_q   ? a.q + int64_t(row) * a.q_stride + hh * a.D
-                               : is_k ? a.k + int64_t(row) * a.k_stride + kv * a.D
-                                      : a.v + int64_t(row) * a.v_stride + kv * a.D;
     const bool rotates = (is_q || is_k) && c < turned;
     const int lo = !kInterleaved && rotates ? c * 8 : c * 16;
     const int hi = !kInterleaved && rotates ? lo + a.rot / 2 : lo + 8;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-    if (live) x = *reinterpret_cast<const uint4*>(src + lo), y = *reinterpret_cast<const uint4*>(src + hi);
     float u[8], w[8];
     unpack8(x, u);
     unpack8(y, w);
+    fetch(it + int(blockDim.x));
     if (live && rotates) {
       // pairs t0 .. t0+7 of this position: cosines and sines
       const float* cs = a.cos_sin + int64_t(pl.pos) * a.rot + c * 8;
@@ -129,13 +140,11 @@ __global__ void __launch_bounds__(kMaxAppendThreads, 12) append8_kernel(const __
         const float n1 = __fadd_rn(__fmul_rn(p1, co[t]), __fmul_rn(p0, si[t]));
         p0 = n0, p1 = n1;
       }
-      x = pack8(u);
-      y = pack8(w);
     }
     if (live && is_q) {
       __nv_bfloat16* dst = a.q_out + (int64_t(row) * a.Hq + hh) * a.D;
-      *reinterpret_cast<uint4*>(dst + lo) = x;
-      *reinterpret_cast<uint4*>(dst + hi) = y;
+      *reinterpret_cast<uint4*>(dst + lo) = pack8(u);
+      *reinterpret_cast<uint4*>(dst + hi) = pack8(w);
     }
     if (__all_sync(~0u, is_q || !live)) continue;
     // the head's largest magnitude: as bits, so that a NaN is larger than everything

@@ -7,11 +7,12 @@
 // least over the warps.  Each thread keeps the maxima of four parts of its ids, so that only parts that reach the threshold,
 // some dozen of 1024, are looked at again; what reaches it there (some dozen ids) is ranked by counting.
 //
-// GB300, V 151936, bf16, 761 tokens (256 windows of 1 to 8 rows) with rank and 20 alternatives: 69 us (34.6 by their bytes), 59
-// without alternatives, with or without the rank.  Bound by instructions (0.66 of the issue slots; 11 for a logit) and, at
-// one block for a token, by the last wave.  One token with 5 alternatives 9.2, without 5.2: a launch, then the second look, the
-// segments' meeting.  Slower, with 20 alternatives, where this form took 73: half rows 78, quarters 90; equal ranges over persistent
-// blocks 113; a second look for the rank too 94; 5 to 8 blocks an SM 76 to 150; 512 threads 74 to 82.
+// GB300, V 151936, bf16, 761 tokens (256 windows of 1 to 8 rows) with rank and 20 alternatives: 67 us (34.6 by their bytes); of
+// tokens drawn evenly from the allowed ids, which many ids stand before, 77 (96 by comparing each of them twice).  Bound by
+// instructions (12 or 13 a logit) that the SMs have unevenly: five blocks each on average, the busiest a third more.
+// Slower, where this form took 70 to 73: half rows 78, quarters 90; equal ranges over persistent blocks 113; a second look for
+// the rank too 94; 2 or 3 blocks an SM with eight loads ahead 79 and 71, 5 to 8 blocks 76 to 150; 512 threads 74 to 82; a maximum
+// over two loads before the next are asked for 85.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -87,6 +88,12 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// The next number below a finite x, in fp32.
+__device__ __forceinline__ float number_below(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);  // one zero
+  return __uint_as_float(b == 0u ? 0x80000001u : b & 0x80000000u ? b + 1u : b - 1u);
 }
 
 template <typename T> struct Eight;  // 8 logits of a row
@@ -186,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprobs_ker
   if (tid == 0) sh.n_reach = sh.n_key = 0;
   const int lo = seg * a.segment, hi = min(a.V, lo + a.segment);  // multiples of 8
   const T* row = static_cast<const T*>(a.logits) + size_t(it.row) * a.V;
-  const float chosen = ld_f32(row, it.token), chosen_raised = max_or_nan(chosen, -kPlain);
+  const float chosen = ld_f32(row, it.token), chosen_raised = a.rank ? max_or_nan(chosen, -kPlain) : INFINITY;
+  const float below = number_below(chosen);
   const int packs = (hi - lo) / 8, mine = (packs + kThreads - 1) / kThreads;  // of the segment, of a thread
   constexpr int kAhead = 4;
   const int part = ((mine + kParts - 1) / kParts + kAhead - 1) / kAhead * kAhead;
@@ -224,18 +232,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprobs_ker
       most = fmaxf(most, top);
       if (top > m + a.slack && top > -kPlain) refer(top);  // (m * c2 is rounded: of a raised logit that would be far off)
       if (top >= chosen_raised) {
-        float r[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = l[j];
-        if (chosen_raised == -kPlain) {  // as they are, not raised
-          Eight<T> raw = {};
-          raw.load(row + lo + p * 8);
-          raw.get(r);
-        }
-        // ids before the token stand before it with its own logit too
         const int id0 = lo + p * 8;
+        if (chosen_raised > -kPlain && (id0 > it.token || id0 + 8 <= it.token)) {
+          // how many lie above the logit, or the number below it (ids before the token stand before it with its own logit
+          // too): by the differences' signs; a NaN's is positive
+          const float over = id0 > it.token ? chosen + 0.f : below;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) before += r[j] > chosen || (r[j] == chosen && id0 + j < it.token);
+          for (int j = 0; j < 8; j += 2) {
+            float d0, d1;
+            unpack_f32x2(fma_f32x2(pack_f32x2(l[j], l[j + 1]), pack_f32x2(-1.f, -1.f), pack_f32x2(over, over)), d0, d1);
+            before += int(__float_as_uint(d0) >> 31), before += int(__float_as_uint(d1) >> 31);
+          }
+        } else {
+          Eight<T> raw = {};  // as they are, not raised
+          raw.load(row + id0);
+          float r[8];
+          raw.get(r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) before += r[j] > chosen || (r[j] == chosen && id0 + j < it.token);
+        }
       }
       const float mc = m == kLowest ? 0.f : m * c2;  // nothing but raised ones so far: they weigh nothing
       const unsigned long long mm = pack_f32x2(-mc, -mc);

@@ -238,3 +238,25 @@ def test_lists_at_the_ends_of_32_bits(cu):
                             torch.tensor([[5, 6, 7, 8]], dtype=torch.int32, device="cuda"), 1.0, *outs, ws)
     assert B.dspark_read_device_status(ws) == B.DSPARK_EINVAL
     assert (outs[0] == 0).all() and (outs[2] == 0).all() and (outs[3] == -1).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,n", [(2000, 40), (30000, 3), (30000, 400)])
+def test_ranks_among_ties_and_zeros_of_both_signs(dtype, V, n):
+    """Tokens of any likelihood among few values, half of them zeros of either sign, some masked, some NaN and the least
+    numbers around 0: the rank counts what is larger, and of what is equal the lower ids."""
+    rng = np.random.default_rng(V + n)
+    tiny = float(torch.finfo(dtype).tiny) * torch.finfo(dtype).eps  # the least number above 0
+    values = np.array([0.0, -0.0, 0.0, -0.0, tiny, -tiny, 1.0, -2.5, 3.0, -np.inf, -1e30, np.nan])
+    x = torch.from_numpy(values[rng.integers(0, values.size - (np.arange(n) % 3 != 0)[:, None], (n, V))]).to(dtype).cuda()
+    tokens = rng.integers(0, V, (n, 1)).astype(np.int32)
+    tokens[:2, 0] = 0, V - 1
+    outs = _outputs(n, 1, 3)
+    B.dspark_token_logprobs(x, None, torch.from_numpy(tokens).cuda(), 1.0, *outs, B.alloc_logprobs_workspace(n, V, 3))
+    host, rank = x.double().cpu().numpy(), outs[2].cpu().numpy()[:, 0]
+    assert (host[:, :] == tiny).any() and (np.signbit(host) & (host == 0)).any()
+    for r in range(n):
+        t = int(tokens[r, 0])
+        with np.errstate(invalid="ignore"):
+            want = 1 + int((host[r] > host[r, t]).sum() + (host[r, :t] == host[r, t]).sum())
+        assert rank[r] == want, (r, t, host[r, t])
