@@ -186,6 +186,8 @@ class Logprobs:
     @staticmethod
     def allocate(bs: int, gamma: int, V: int, top_n: int = 0, temperature: float = 1.0, device="cuda") -> "Logprobs":
         import torch
+        if not 0 < temperature < float("inf"):
+            raise ValueError("temperature of the report must be positive (1 for the logits as they are)")
         f32, i32 = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
         n = gamma + 1
         return Logprobs(torch.zeros((bs, n), **f32), torch.zeros((bs, n), **f32), torch.zeros((bs, n), **i32),

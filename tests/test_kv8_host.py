@@ -77,3 +77,9 @@ def test_a_step_refuses_a_report_of_other_sizes(host):
         with pytest.raises(ValueError, match="logprobs"):
             V.run_served_step({}, Buf, None, None, None, None, 1.0, 0, 0,
                               logprobs=V.Logprobs.allocate(bs, gamma, 64, 0, device="cpu"))
+
+
+@pytest.mark.parametrize("temperature", [0.0, -1.0, float("inf"), float("nan")])
+def test_a_report_at_no_temperature_is_refused(host, temperature):
+    with pytest.raises(ValueError, match="temperature"):
+        V.Logprobs.allocate(2, 3, 64, 4, temperature, device="cpu")
