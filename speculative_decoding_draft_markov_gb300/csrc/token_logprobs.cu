@@ -7,8 +7,9 @@
 // least over the warps.  Each thread keeps the maxima of four parts of its ids, so that only parts that reach the threshold,
 // some dozen of 1024, are looked at again; what reaches it there (some dozen ids) is ranked by counting.
 //
-// GB300, V 151936, bf16, 761 tokens (256 windows of 1 to 8 rows) with rank and 20 alternatives: 67 us (34.6 by their bytes); of
-// tokens drawn evenly from the allowed ids, which many ids stand before, 77 (96 by comparing each of them twice).  Bound by
+// GB300, V 151936, bf16, 761 tokens (256 windows of 1 to 8 rows) with rank and 20 alternatives: 69 us (34.6 by their bytes; 67.7 with
+// d as one fma under a rounded m log2(e) / T, an error that grows with the logits); of tokens drawn evenly from the allowed ids,
+// which many ids stand before, 77 (96 by comparing each of them twice).  Bound by
 // instructions (12 or 13 a logit) that the SMs have unevenly: five blocks each on average, the busiest a third more.
 // Slower, where this form took 70 to 73: half rows 78, quarters 90; equal ranges over persistent blocks 113; a second look for
 // the rank too 94; 2 or 3 blocks an SM with eight loads ahead 79 and 71, 5 to 8 blocks 76 to 150; 512 threads 74 to 82; a maximum
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprobs_ker
       if (next < packs) x[b].load(row + lo + next * 8);
       const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
       most = fmaxf(most, top);
-      if (top > m + a.slack && top > -kPlain) refer(top);  // (m * c2 is rounded: of a raised logit that would be far off)
+      if (top > m + a.slack && top > -kPlain) refer(top);
       if (top >= chosen_raised) {
         const int id0 = lo + p * 8;
         if (chosen_raised > -kPlain && (id0 > it.token || id0 + 8 <= it.token)) {
@@ -252,12 +253,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprobs_ker
           for (int j = 0; j < 8; ++j) before += r[j] > chosen || (r[j] == chosen && id0 + j < it.token);
         }
       }
-      const float mc = m == kLowest ? 0.f : m * c2;  // nothing but raised ones so far: they weigh nothing
-      const unsigned long long mm = pack_f32x2(-mc, -mc);
+      const float neg = m == kLowest ? 0.f : -m;  // nothing but raised ones so far: they weigh nothing
+      const unsigned long long mm = pack_f32x2(neg, neg);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         float d0, d1;
-        const unsigned long long d = fma_f32x2(pack_f32x2(l[j], l[j + 1]), cc, mm);
+        // the difference first: under a rounded m c2, d would be off by up to 2^-24 |m| / T
+        const unsigned long long d = mul_f32x2(add_f32x2(pack_f32x2(l[j], l[j + 1]), mm), cc);
         unpack_f32x2(d, d0, d1);
         const unsigned long long e = pack_f32x2(tc::ex2_approx(d0), tc::ex2_approx(d1));
         s2 = add_f32x2(s2, e);
@@ -274,11 +276,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprobs_ker
   const bool some = __syncthreads_or(all > -kPlain), huge = __syncthreads_or(all >= kPlain);
   if (!some || huge || c2 * kPlain < 400.f || c2 > 1e7f) {  // (c2 beyond: d would overflow, and 0 * -inf is NaN)
     m = kLowest, s2 = w2 = 0ull;
+    float high = -INFINITY;
     for (int p = tid; p < packs; p += kThreads) {
       float l[8];
       x[0].load(row + lo + p * 8);
       x[0].get(l);
       const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
+      high = fmaxf(high, top);
       if (top > m + a.slack) refer(top);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -288,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) logprobs_ker
         w2 = fma_f32x2(e, pack_f32x2(d0, d1), w2);
       }
     }
+    if (high > m) refer(high);
   }
   float s0, s1, w0, w1;
   unpack_f32x2(s2, s0, s1);
