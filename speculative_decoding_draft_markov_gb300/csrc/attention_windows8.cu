@@ -9,22 +9,24 @@
 // Q's row is taken under a power of two of its own, 2^eq: the first part has the upper four of bf16's eight bits, the second
 // what is left, exact for lanes down to 2^-10 of the row's largest; smaller ones are off by at most 2^-19 of that.  The slots'
 // powers, ek, are one factor per thread, the rows' one per score.
-// A weight has eight bits, as bf16 has (relative 2^-8), down to 2^-16 of the largest and an error of 2^-20 of it
+// A weight has eight bits, as bf16 has (relative 2^-8), down to 2^-12 of the largest and an error of 2^-20 of it
 // below; the second part is kept times 16 and in accumulators of its own for that.  V's contraction runs over slots, so its
-// powers 2^ev have to go into P.  P is kept inside e4m3's range by two references, a row's m, which lies kTop below its
-// maximum of a unit's first tile, and f, the largest ev of the tile's slots; both are checked on each tile against kMost, and
-// set anew where they are outgrown, O^T and the sums with them.
+// powers 2^ev have to go into P, and a V that lies 2^k below their reference has k bits fewer of its weight.
+// P is kept inside e4m3's range by two references, a row's m, which lies kTop below its maximum of a unit's first tile, and f,
+// the largest ev of a tile's slots.  Both are checked on each tile against kMost, f also for lying above all of the tile's ev by
+// more than kFall (else a large V would take the weights' bits from all tiles behind it); they are set anew where they have to
+// be, O^T and the sums with them.  The last check takes 2% (256 windows 117.6 us without it).
 //
-// GB300, 8 KV heads: D 128, 256 windows of 8 rows, window 1024, 118 us (81.5 by its bytes; over a bf16 cache 175); 2 requests of
-// 16 rows over 125000 positions 102 us (77; 154); one token over 1500 positions 10.4 (9.7); D 64, 64 windows of 64 rows to a KV
-// head, window 4096, 94 us (33; 83).  What bounds it is the chain of a tile's steps, some 3200 cycles for a pipeline with 64
+// GB300, 8 KV heads: D 128, 256 windows of 8 rows, window 1024, 120 us (81.5 by its bytes; over a bf16 cache 175); 2 requests of
+// 16 rows over 125000 positions 104 us (77; 154); one token over 1500 positions 10.4 (9.7); D 64, 64 windows of 64 rows to a KV
+// head, window 4096, 97 us (33; 83).  What bounds it is the chain of a tile's steps, some 3200 cycles for a pipeline with 64
 // rows, and the softmax warps' instructions (0.6 of the issue slots): a satisfied wait costs about 200 cycles, a TMA load its
 // warp 180, so K and V have a warp each (one for both took 3000 cycles a tile) and the exponent bytes come by 8-byte
 // asynchronous copies (1000 cycles of bulk copies before).  The code has to stay small: with every step inlined where it is used
 // (172 KB of instructions) the first three took 201 us, with each step there once 147.
 // Slower, in us for 256 windows / 125000 positions / 64 rows: V converted to fp16 by four warps and P in fp16 237 / 178 / 178;
 // eight softmax warps of 184 registers 129 / 116 / 109 where sixteen took 123 / 105 / 98; blocks of 64 slots 126 / 104 / 98
-// beside the same; waits that may sleep 123 / 105 / 98 beside 118 / 102 / 94.  Q split by plain loads took 33000 cycles for 64
+// beside the same; waits that may sleep 123 / 105 / 98 beside 118 / 102 / 94 (all of these without the last check).  Q split by plain loads took 33000 cycles for 64
 // rows, copied to where it is split 20000.
 #include "attention_common.cuh"
 #include "kv8.cuh"
@@ -45,6 +47,8 @@ constexpr int kQBufs = 2, kQRing = 4;  // units whose Q, whose rows' factors are
 // m lies kTop below a maximum; a score and a value's power together may outgrow the references up to kMost (e4m3 ends at
 // 448 = 2^8.8)
 constexpr float kTop = 6.f, kMost = 8.75f;
+// V's reference may lie above a tile's largest power of two by this much.
+constexpr int kFall = 4;
 
 constexpr int sets_of(int D, int R) { return R == 128 ? 1 : 2; }
 
@@ -62,6 +66,7 @@ struct Shared {
   volatile int abort;
   int pending[kSets];          // the MMA warp has issued something
   int need[kGroups][2];        // [parity]: the last tile at which a warp asked for new references
+  alignas(16) int low[kGroups][2][4];  // [parity], by warp: the last tile whose V it found to lie far below the reference
   Start start[kSets];
   int warp_byte[kGroups][4];   // by warp: the largest exponent byte of V in a tile
   float warp_max[kGroups][4][kRows], warp_sum[kGroups][4][kRows];  // by warp: the rows' maxima of a tile, sums of a unit
@@ -228,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane < kGroups) {
       tc::mbar_init(tc::smem_u32(&sh->group[lane]), 4);
       sh->need[lane][0] = sh->need[lane][1] = 0;
+      for (int i = 0; i < 8; ++i) sh->low[lane][i / 4][i % 4] = 0;
     }
     for (int i = lane; i < Sh::kRows; i += 32) sh->zeros[i] = 0.f;
     if (lane == 0) sh->abort = 0, plan.bad = 0, plan.n_long = 0;
@@ -601,6 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < RW; i += 4) top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
             // (a V far beyond f is looked at however little it weighs: its weight would leave fp32)
             if (__any_sync(~0u, top + float(max(0, v_byte - f)) > kMost || v_byte - f > 60) && lane == 0) sh->need[grp][at] = t + 1;
+            // V's powers far below f: this warp's slots; the tile's where the others say so too
+            if (!__any_sync(~0u, v_byte >= f - kFall)) {
+              const int seen_by = __any_sync(~0u, v_byte > 0);
+              if (lane == 0) sh->low[grp][at][w4] = 2 * (t + 1) + seen_by;
+            }
             arrive();
           }
 #pragma unroll
@@ -608,7 +619,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (fresh) break;
           // and the last product, which reads P, is over
           ok = wait.both(&sh->group[grp], sync++ & 1, &sh->p_empty[set], (t & 1) ^ 1);
-          if (!ok || sh->need[grp][at] != t + 1) break;
+          if (!ok) break;
+          bool again = sh->need[grp][at] == t + 1;
+          if (__builtin_expect(!__any_sync(~0u, v_byte >= f - kFall), 0)) {
+            const int4 low = *reinterpret_cast<const int4*>(sh->low[grp][at]);
+            again |= low.x / 2 == t + 1 && low.y / 2 == t + 1 && low.z / 2 == t + 1 && low.w / 2 == t + 1 &&
+                     ((low.x | low.y | low.z | low.w) & 1) && f > f_top - 70;
+          }
+          if (!again) break;
         }
         if (!ok) break;
         const float vf = kv8::power(max(v_byte - f, -126));  // 2^(ev - f)
