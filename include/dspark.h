@@ -579,7 +579,7 @@ DSPARK_API int dspark_read_kv8(const void* k_cache, const void* v_cache, const u
  *                         attended to there; without them the windows' kernel takes such calls too, more slowly.  One pair
  *                         serves all layers of a model.  Calls that can overlap on the device must not share it.
  * The products take the codes as they are, and each query and each weight as a sum of two e4m3 parts.  A query's lanes keep
- * bf16's eight bits down to 2^-10 of the row's largest and are off by at most 2^-19 of that below; a weight is off by at most 2^-8 of
+ * bf16's eight bits down to 2^-9.8 of the row's largest and are off by at most 2^-17.8 of that below; a weight is off by at most 2^-8 of
  * itself, or by 2^(k - 20) of the row's largest weight where its V's power of two lies 2^k below a reference: at most 2^4 times
  * the largest power of a tile of 128 positions that are read together (whatever those weigh), and at least 2^-70 of the largest
  * of the tiles before.  A row that sees a vector of NaN (byte 255), in K or in V, is NaN,

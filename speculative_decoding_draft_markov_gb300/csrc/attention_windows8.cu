@@ -7,7 +7,8 @@
 // K and V go into the products as they lie in the cache; nothing is converted but the other operands, which one code of e4m3
 // (relative error 2^-4) would be too little for, so each is a sum of two.
 // Q's row is taken under a power of two of its own, 2^eq: the first part has the upper four of bf16's eight bits, the second
-// what is left, exact for lanes down to 2^-10 of the row's largest; smaller ones are off by at most 2^-19 of that.  The slots'
+// what is left, exact for lanes down to 2^-9.8 of the row's largest, which lies above 224 = 2^7.8 of that power; smaller ones are
+// off by at most half of the second part's least step, 2^-10 of the power, i.e. 2^-17.8 of the row's largest.  The slots'
 // powers, ek, are one factor per thread, the rows' one per score.
 // A weight has eight bits, as bf16 has (relative 2^-8), down to 2^-12 of the largest and an error of 2^-20 of it
 // below; the second part is kept times 16 and in accumulators of its own for that.  V's contraction runs over slots, so its
