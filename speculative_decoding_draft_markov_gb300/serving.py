@@ -12,6 +12,7 @@ read back; pages are handed out on the host, from upper bounds of the lengths.""
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import dataclasses
 from typing import Callable, List, Optional
 
@@ -170,6 +171,12 @@ class LogitRules:
                                     buf.packed, buf.ws)
 
 
+def _check_temperature(temperature: float) -> None:
+    t = ctypes.c_float(temperature).value  # as dspark_token_logprobs takes it
+    if not 0 < t < float("inf") or ctypes.c_float(2 / t).value == float("inf"):
+        raise ValueError("temperature of the report must be positive (1 for the logits as they are)")
+
+
 @dataclasses.dataclass
 class Logprobs:
     """What a step reports of the tokens that it commits, by the target's logits under the rules at `temperature`: for
@@ -186,14 +193,23 @@ class Logprobs:
     @staticmethod
     def allocate(bs: int, gamma: int, V: int, top_n: int = 0, temperature: float = 1.0, device="cuda") -> "Logprobs":
         import torch
-        if not 0 < temperature < float("inf"):
-            raise ValueError("temperature of the report must be positive (1 for the logits as they are)")
+        _check_temperature(temperature)
         f32, i32 = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
         n = gamma + 1
         return Logprobs(torch.zeros((bs, n), **f32), torch.zeros((bs, n), **f32), torch.zeros((bs, n), **i32),
                         torch.full((bs, n, top_n), -1, **i32) if top_n else None,
                         torch.full((bs, n, top_n), float("-inf"), **f32) if top_n else None,
                         B.alloc_logprobs_workspace(bs * n, V, top_n, device), temperature)
+
+    def check(self, buf) -> None:
+        """Raises where `take` could not report of buf's steps."""
+        if self.logprob.shape != buf.out_tokens.shape:
+            raise ValueError("logprobs must be of the step's requests and gamma")
+        _check_temperature(self.temperature)
+        top_n = 0 if self.top_ids is None else self.top_ids.shape[2]
+        n = B.dspark_token_logprobs_workspace_bytes(self.logprob.numel(), buf.packed.shape[1], top_n)
+        if n == 0 or self.ws.numel() < n:
+            raise ValueError("logprobs must be of the step's vocabulary")
 
     def take(self, buf, stream=None) -> None:
         """Of buf.out_tokens, after a verification and before buf.packed is written anew."""
@@ -238,8 +254,8 @@ def run_served_step(inp: dict, buf: S.StepBuffers, sps, forward: Callable, cache
     rules; the verification; with `logprobs` its report; then take_outcome.  mode, tiers, sched_mode, ring and side_stream as in step.run_step.
     A drafter that step.run_step does not run (the RNN head) takes the same way by hand: its draft and the pack,
     forward, rules.apply, step.verify with its states, take_outcome."""
-    if logprobs is not None and logprobs.logprob.shape != buf.out_tokens.shape:
-        raise ValueError("logprobs must be of the step's requests and gamma")
+    if logprobs is not None:
+        logprobs.check(buf)
 
     def target(b: S.StepBuffers) -> None:
         forward(b, cache)
