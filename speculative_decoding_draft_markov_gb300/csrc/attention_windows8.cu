@@ -179,17 +179,19 @@ __device__ __forceinline__ void issue_codes(const AttnArgs& a, const CUtensorMap
   }
 }
 // The exponent bytes of a tile's slots, four slots to a lane; zeros of any power of two where there is no page.  Every lane
-// arrives at `bar` when its own are there.
+// arrives at `bar` when its own are there: by its copy's end, or itself behind its store, which an arrival by copies does not order.
 __device__ __forceinline__ void issue_scales(const Attn8Args& p, const TileLoad& t, uint16_t* dst, uint32_t bar, int lane) {
   const AttnArgs& a = p.a;
   const int block = (lane * 4) >> a.block_shift, in = (lane * 4) & ((1 << a.block_shift) - 1);
   const int page = __shfl_sync(~0u, t.page, block), slot = __shfl_sync(~0u, t.slot, block) + in;
   uint16_t* to = dst + lane * 4;
-  if (block < t.n_blocks && page >= 0 && page < a.n_pages)
+  if (block < t.n_blocks && page >= 0 && page < a.n_pages) {
     tc::async_copy_8(tc::smem_u32(to), p.kv_scale + 2 * (((int64_t(page) * a.Hkv + t.head) << a.page_shift) + slot));
-  else
+    tc::async_copies_arrive(bar);
+  } else {
     *reinterpret_cast<uint2*>(to) = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  tc::async_copies_arrive(bar);
+    tc::mbar_arrive(bar);
+  }
 }
 
 template <int D, int R>
