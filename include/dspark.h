@@ -575,9 +575,11 @@ DSPARK_API int dspark_read_kv8(const void* k_cache, const void* v_cache, const u
 /* dspark_window_attention over the 8-bit cache (the same formulas, arguments, workspace, errors and limits).
  *   k_scratch, v_scratch  device [n_pages, Hkv, page_size, D] bf16 each, or both NULL: pages of the same numbers that the
  *                         call may overwrite.  Windows of more than 512 (row, query head) pairs to a KV head (128 where
- *                         D = 64), by max_rows, are then read back into them first, once for all rows (dspark_read_kv8), and
- *                         attended to there; without them the windows' kernel takes such calls too, more slowly.  One pair
- *                         serves all layers of a model.  Calls that can overlap on the device must not share it.
+ *                         D = 64) are then read back into them first, once for all rows (dspark_read_kv8), and attended to
+ *                         there.  max_rows decides for the whole batch: short windows beside a long one are read back too,
+ *                         their whole caches, which can take 2.5 times as long as the call with NULL.  With NULL the windows'
+ *                         kernel takes every call, a batch of prompts at half the speed.  One pair serves all layers of a
+ *                         model.  Calls that can overlap on the device must not share it.
  * The products take the codes as they are, and each query and each weight as a sum of two e4m3 parts.  A query's lanes keep
  * bf16's eight bits down to 2^-9.8 of the row's largest and are off by at most 2^-17.8 of that below; a weight is off by at most 2^-8 of
  * itself, or by 2^(k - 20) of the row's largest weight where its V's power of two lies 2^k below a reference: at most 2^4 times

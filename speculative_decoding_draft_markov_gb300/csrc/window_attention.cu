@@ -210,7 +210,11 @@ cudaError_t launch_window_attention_kv8(const void* q, int64_t q_stride, const v
                                         cudaStream_t s) {
   // Read back once for all of a request's units, or read in 8 bits by each unit of 128 rows?  GB300, 8 KV heads, 4000 positions, 64
   // requests: D 64, 128 rows to a KV head 188 us by the windows' kernel and 284 read back, 136 rows 341 and 302; D 128, 256 rows 362 and
-  // 525, 512 rows (32 requests) 365 and 369.  256 requests, window 256: D 128, 128 rows 161 and 215, 256 rows 289 and 249.
+  // 525, 512 rows (32 requests) 365 and 369.  256 requests, window 256: D 128, 128 rows 161 and 215, 256 rows 289 and 249.  Two
+  // prompts of 4000, window 4096: 494 and 235, D 64 438 and 209.
+  // These are batches of equal windows.  The longest window decides for all, and which are long is known on the device only; a
+  // caller that mixes them gives no pages.  A chunk of 2000 rows over 1000 positions, Hq 32, beside 100 windows of 8 over 4000: 408 and 886,
+  // D 64 394 and 519; beside 30 windows over 30000: 734 and 1879, D 64 721 and 1037; alone 123 and 83, D 64 114 and 69.
   if (k_scratch && int64_t(max_rows) * (Hq / Hkv) > (D == 64 ? 128 : 512)) {
     const cudaError_t e = launch_read_kv8(k_cache, v_cache, kv_scale, page_table, max_pages, n_pages, page_shift, cu, ctx, bs,
                                           rows, Hkv, D, window, n_sink, page_table, n_pages, k_scratch, v_scratch, true,

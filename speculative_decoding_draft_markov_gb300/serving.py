@@ -48,9 +48,11 @@ class PagedCache:
     rejected draft keeps its place and the cache fills too early; how late the length comes does not matter.  With a
     window, `settle` also gives back the pages that the window has left behind.
 
-    eight_bit: pages of e4m3 with an exponent byte for each position's K and V of each KV head (half the memory and half the
-    reads of a step).  One pair of bf16 pages, `wide`, serves all layers: prompts are read back into it, and read_back
-    leaves there what the packed rows see."""
+    eight_bit: pages of e4m3 with an exponent byte for each position's K and V of each KV head: half of the pages' memory.
+    One pair of bf16 pages, `wide`, of one layer's size serves all layers: prompts are read back into it, and read_back
+    leaves there what the packed rows see.  So L layers take 1/2 + 1/L of a 16-bit cache (and 1/D for the exponents).  A step
+    reads half as much, which windows over 128-lane heads gain by (GB300: a third less time); over 64-lane heads, where the reads
+    are not what bounds it, a step's attention can take longer than over 16 bits (64 windows of 64 rows to a KV head: 97 us, 84)."""
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, Hq: int, Hkv: int, D: int, bs: int, max_pages: int,
                  cos_sin, window: int = 0, n_sink: int = 0, interleaved: bool = False, device="cuda", eight_bit: bool = False):
@@ -121,15 +123,17 @@ class PagedCache:
             self.page_table[r] = -1
             self.ctx_len[r] = 0
 
-    def attend(self, layer: int, q, k, v, cu_seqlens, max_rows: int, scale: float, out, stream=None) -> None:
+    def attend(self, layer: int, q, k, v, cu_seqlens, max_rows: int, scale: float, out, stream=None,
+               widen: bool = True) -> None:
         """Rotate and append the packed rows' q, k, v, then attend: out [rows, Hq, D].  `out` is the rotated
-        queries' place as well."""
+        queries' place as well.  widen (8 bits): whether what the rows see may be read back to `wide` first where max_rows is a
+        prompt's; False for a prompt's chunk among many short windows, whose whole caches would be read back with it."""
         if self.eight_bit:
             pages = self.k[layer], self.v[layer], self.scale[layer]
             B.dspark_append_kv8(q, k, v, cu_seqlens, self.ctx_len, self.cos_sin, self.page_table, out, *pages, self.ws,
                                 self.interleaved, stream)
             B.dspark_window_attention_kv8(out, *pages, self.page_table, cu_seqlens, self.ctx_len, max_rows, scale,
-                                          self.window, self.n_sink, out, None, *self.wide, self.ws, stream)
+                                          self.window, self.n_sink, out, None, *(self.wide if widen else (None, None)), self.ws, stream)
             return
         B.dspark_append_kv(q, k, v, cu_seqlens, self.ctx_len, self.cos_sin, self.page_table, out, self.k[layer],
                            self.v[layer], self.ws, self.interleaved, stream)
