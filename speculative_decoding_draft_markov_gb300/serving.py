@@ -50,7 +50,7 @@ class PagedCache:
 
     eight_bit: pages of e4m3 with an exponent byte for each position's K and V of each KV head: half of the pages' memory.
     One pair of bf16 pages, `wide`, of one layer's size serves all layers: prompts are read back into it, and read_back
-    leaves there what the packed rows see.  So L layers take 1/2 + 1/L of a 16-bit cache (and 1/D for the exponents).  A step
+    leaves there what the packed rows see.  So L layers take 1/2 + 1/L of a 16-bit cache (and 1/(2 D) for the exponents).  A step
     reads half as much, which windows over 128-lane heads gain by (GB300: a third less time); over 64-lane heads, where the reads
     are not what bounds it, a step's attention can take longer than over 16 bits (64 windows of 64 rows to a KV head: 97 us, 84)."""
 
